@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import Optional
 
@@ -25,13 +26,16 @@ HEAD_DIM = 128
 EXPORTED = ("kda_workspace_size", "kda_fwd", "kda_status_string", "kda_last_error",
             "kda_read_device_status", "kda_fwd_no_alloc", "kda_fwd_host_device_bytes", "kda_fwd_host",
             "kda_fwd_host_workspace_offset", "kda_decode", "kda_fwd_ex", "kda_decode_ex", "kda_fwd_schedule",
-            "kda_fwd_set_trace")
+            "kda_fwd_set_trace", "kda_qk_norm_rope", "kda_attn_workspace_size", "kda_attn_fwd", "kda_lin_workspace_size",
+            "kda_lin_fwd", "kda_lin_decode")
 KDA_FLAG_BETA_LOGIT, KDA_FLAG_GATE_SOFTPLUS = 0x1, 0x2
 KDA_FLAG_KERNEL_MASK = 0xF00
 KDA_KERNEL_DEFAULT, KDA_KERNEL_CHUNK16, KDA_KERNEL_REGISTER_STATE, KDA_KERNEL_BF16_STATE = 0x000, 0x100, 0x200, 0x300
 KDA_KERNEL_SMEM_STATE = 0x400
 KDA_SCHEDULE_TWO_PER_SM, KDA_SCHEDULE_ONE_PER_SM, KDA_SCHEDULE_CLUSTER, KDA_SCHEDULE_CLUSTER2 = 0, 1, 2, 3
 KDA_TRACE_POINTS = 8
+KDA_DEVERR_POSITION = 0x8
+KDA_FLAG_ROPE_INTERLEAVED = 0x1
 
 _DTYPE = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32, torch.int64: KDA_I64}
 
@@ -104,6 +108,19 @@ def load(path: Optional[str] = None):
         lib.kda_fwd_host.restype = ctypes.c_int
         lib.kda_fwd_host.argtypes = [T, T, T, T, T, ctypes.c_float, T, T, T, ctypes.c_float, T, T, T,
                                      ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_void_p]
+        D, V, F = ctypes.c_char_p, ctypes.c_void_p, ctypes.c_float   # D: a packed kda_view or kda_tensor (_view, _dense)
+        lib.kda_qk_norm_rope.restype = ctypes.c_int
+        lib.kda_qk_norm_rope.argtypes = [D, D, D, D, F, D, D, D, D, V, ctypes.c_uint32, V]
+        lib.kda_attn_workspace_size.restype = ctypes.c_size_t
+        lib.kda_attn_workspace_size.argtypes = [ctypes.c_int64, ctypes.c_int, ctypes.c_int]
+        lib.kda_attn_fwd.restype = ctypes.c_int
+        lib.kda_attn_fwd.argtypes = [D, D, D, F, D, D, D, D, D, V, ctypes.c_size_t, V]
+        lib.kda_lin_workspace_size.restype = ctypes.c_size_t
+        lib.kda_lin_workspace_size.argtypes = [ctypes.c_int64, ctypes.c_int, ctypes.c_int]
+        lib.kda_lin_fwd.restype = ctypes.c_int
+        lib.kda_lin_fwd.argtypes = [D, D, D, D, F, D, D, D, D, V, ctypes.c_size_t, V]
+        lib.kda_lin_decode.restype = ctypes.c_int
+        lib.kda_lin_decode.argtypes = [D, D, D, D, F, D, D, D, V]
         if path is None:
             _lib = lib
         return lib
@@ -334,3 +351,160 @@ def fwd(q, k, v, g, beta, scale, out, A_log, dt_bias, lower_bound, initial_state
     kda_fwd(q, k, v, g, beta, scale, out, A_log, dt_bias, lower_bound, initial_state=initial_state,
             final_state=final_state, cu_seqlens=cu_seqlens)
     return out
+
+
+# ---------------------------------------------------------------------------
+# The token mixers beside KDA.  Their small calls last a few microseconds on the GPU, so the
+# descriptors are packed straight into bytes (the layout of kda_view, whose first 48 bytes are
+# a kda_tensor) instead of filling ctypes structures field by field.
+# ---------------------------------------------------------------------------
+_PACK_VIEW = struct.Struct("=Qii4q4q").pack
+_PACK_DENSE = struct.Struct("=Qii4q").pack
+_PAD = ((0, 0, 0, 0), (0, 0, 0), (0, 0), (0,), ())
+
+
+def _bad_tensor(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor (there is no CPU fallback)")
+    if t.dim() > 4:
+        raise ValueError(f"{name}: at most 4 dims")
+    if t.dtype not in _DTYPE:
+        raise ValueError(f"{name}: unsupported dtype {t.dtype}")
+    raise ValueError(f"{name}: on another device than the first tensor")
+
+
+def _view(t, name, device):
+    """The packed kda_view of a CUDA tensor of any strides."""
+    if t is None:
+        return None
+    dtype = _DTYPE.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if dtype is None or t.get_device() != device or device < 0 or t.dim() > 4:
+        _bad_tensor(t, name)
+    shape = t.shape
+    pad = _PAD[len(shape)]
+    return _PACK_VIEW(t.data_ptr() or 16, dtype, len(shape), *shape, *pad, *t.stride(), *pad)
+
+
+def _dense(t, name, device):
+    """The packed kda_tensor of a contiguous CUDA tensor."""
+    if t is None:
+        return None
+    dtype = _DTYPE.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if dtype is None or t.get_device() != device or device < 0 or t.dim() > 4:
+        _bad_tensor(t, name)
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    shape = t.shape
+    return _PACK_DENSE(t.data_ptr() or 16, dtype, len(shape), *shape, *_PAD[len(shape)])
+
+
+def _device(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    return t.get_device()
+
+
+def _stream(stream, device):
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _workspace(workspace, nbytes, device, stream):
+    """The caller's workspace, or one from torch that lives until the work on ``stream`` is done."""
+    if workspace is None:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
+        if stream is not None:
+            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
+                                    else torch.cuda.ExternalStream(_stream(stream, device), device=device))
+    elif not (isinstance(workspace, torch.Tensor) and workspace.is_cuda and workspace.dtype == torch.uint8
+              and workspace.is_contiguous()):
+        raise ValueError("workspace: must be a contiguous uint8 CUDA tensor")
+    return workspace
+
+
+def kda_qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, q_out, k_out, eps=1e-6, status=None, flags=0,
+                     stream=None):
+    """RMS norm of every head of q [T, Hq, 128] and k [T, Hk, 128] and the rotary rotation, in
+    one pass; q_out / k_out may be q / k themselves.  Tensors as in ``include/kda.h``; q and k
+    may be strided views of one projection buffer.  ``status``: a CUDA uint8 tensor of at least 4
+    bytes whose first word collects KDA_DEVERR_POSITION (see kda_read_device_status)."""
+    lib = _lib or load()
+    dev = _device(q, "q")
+    if status is not None and not (status.is_cuda and status.dtype == torch.uint8 and status.numel() >= 4):
+        raise ValueError("status: must be a uint8 CUDA tensor of at least 4 bytes")
+    st = lib.kda_qk_norm_rope(_view(q, "q", dev), _view(k, "k", dev), _dense(q_weight, "q_weight", dev),
+                              _dense(k_weight, "k_weight", dev), eps, _dense(cos_sin, "cos_sin", dev),
+                              _dense(positions, "positions", dev), _view(q_out, "q_out", dev), _view(k_out, "k_out", dev),
+                              None if status is None else status.data_ptr(), flags, _stream(stream, dev))
+    if st:
+        _check(lib, st)
+
+
+def kda_attn_workspace_size(Tq: int, Hq: int, Hk: int) -> int:
+    return int(load().kda_attn_workspace_size(int(Tq), int(Hq), int(Hk)))
+
+
+def kda_attn_fwd(q, k, v, scale, out, lse=None, cu_seqlens_q=None, cu_seqlens_k=None, seqlens_k=None, workspace=None,
+                 stream=None):
+    """Causal softmax attention with grouped heads: q, out [Tq, Hq, 128]; k, v [Tk, Hk, 128]
+    (packed prompts) or [N, S, Hk, 128] with ``seqlens_k`` (caches; one or more new tokens per
+    sequence).  Tensors and modes as in ``include/kda.h``.  ``workspace`` (uint8 CUDA tensor) is
+    allocated with torch when omitted.  Returns the workspace (its first word is the device status)."""
+    lib = _lib or load()
+    dev = _device(q, "q")
+    dq, dk = _view(q, "q", dev), _view(k, "k", dev)
+    if workspace is None and q.dim() == 3 and k.dim() in (3, 4):
+        nbytes = lib.kda_attn_workspace_size(q.shape[0], q.shape[1], k.shape[-2]) or 256   # 0: refused below
+        workspace = _workspace(None, nbytes, dev, stream)
+    else:
+        workspace = _workspace(workspace, 256, dev, stream)
+    st = lib.kda_attn_fwd(dq, dk, _view(v, "v", dev), scale, _view(out, "out", dev), _dense(lse, "lse", dev),
+                          _dense(cu_seqlens_q, "cu_seqlens_q", dev), _dense(cu_seqlens_k, "cu_seqlens_k", dev),
+                          _dense(seqlens_k, "seqlens_k", dev), workspace.data_ptr(), workspace.numel(),
+                          _stream(stream, dev))
+    if st:
+        _check(lib, st)
+    return workspace
+
+
+def kda_lin_workspace_size(T_total: int, H: int, N: int) -> int:
+    return int(load().kda_lin_workspace_size(int(T_total), int(H), int(N)))
+
+
+def kda_lin_fwd(q, k, v, log_decay, scale, out, initial_state=None, final_state=None, cu_seqlens=None, workspace=None,
+                stream=None):
+    """Linear attention with a decay for each head over prompts: q, k, v, out [B, T, H, 128],
+    log_decay [H], states [Nseq, H, 128, 128]; packed with ``cu_seqlens`` as kda_fwd.  Tensors as in
+    ``include/kda.h``.  Returns the workspace (its first word is the device status)."""
+    lib = _lib or load()
+    dev = _device(q, "q")
+    dq = _view(q, "q", dev)
+    if workspace is None and q.dim() == 4:
+        B, T, H, _ = q.shape
+        nseq = B if cu_seqlens is None else max(cu_seqlens.numel() - 1, 0)
+        workspace = _workspace(None, lib.kda_lin_workspace_size(B * T, H, nseq), dev, stream)
+    else:
+        workspace = _workspace(workspace, 256, dev, stream)
+    st = lib.kda_lin_fwd(dq, _view(k, "k", dev), _view(v, "v", dev), _dense(log_decay, "log_decay", dev), scale,
+                         _view(out, "out", dev), _dense(initial_state, "initial_state", dev),
+                         _dense(final_state, "final_state", dev), _dense(cu_seqlens, "cu_seqlens", dev),
+                         workspace.data_ptr(), workspace.numel(), _stream(stream, dev))
+    if st:
+        _check(lib, st)
+    return workspace
+
+
+def kda_lin_decode(q, k, v, log_decay, scale, out, initial_state=None, final_state=None, stream=None):
+    """One token of kda_lin_fwd's recurrence for every sequence: q, k, v, out [B, H, 128],
+    states [B, H, 128, 128]; final_state may be initial_state itself."""
+    lib = _lib or load()
+    dev = _device(q, "q")
+    st = lib.kda_lin_decode(_view(q, "q", dev), _view(k, "k", dev), _view(v, "v", dev),
+                            _dense(log_decay, "log_decay", dev), scale, _view(out, "out", dev),
+                            _dense(initial_state, "initial_state", dev), _dense(final_state, "final_state", dev),
+                            _stream(stream, dev))
+    if st:
+        _check(lib, st)

@@ -330,6 +330,127 @@ kda_status kda_fwd_host(const kda_tensor* q, const kda_tensor* k, const kda_tens
  * device_buffer of a kda_fwd_host call with these arguments; 0 for invalid ones. */
 size_t kda_fwd_host_workspace_offset(int64_t B, int64_t T, int H, int64_t N, int init_dtype, int final_dtype);
 
+/* ------------------------------------------------------------------------------------
+ * The token mixers that stand beside KDA in a hybrid stack: the norm and rotation of q and
+ * k, causal softmax attention with grouped heads, and linear attention with a decay for
+ * each head.  They share this library's manner: bf16 tokens, head dim 128, packed sequences
+ * given by int64 cu_seqlens, fp32 or bf16 states, caller-owned buffers, every host-side check
+ * made before anything is enqueued, nothing allocated and no stream synchronised.  The pages
+ * describe no counterpart of these calls; they are additions of this library.
+ * ------------------------------------------------------------------------------------ */
+
+/* A strided device tensor: strides in elements, the innermost one 1.  q, k and v may be
+ * columns of one projection buffer, or a cache in any order of its outer dimensions.  Data
+ * is 16-byte aligned and every outer stride a multiple of 8 elements (a dimension of size 1
+ * may carry any stride). */
+typedef struct {
+    void* data;
+    int32_t dtype;     /* kda_dtype */
+    int32_t ndim;
+    int64_t shape[4];
+    int64_t stride[4];
+} kda_view;
+
+/* Device-side status bit of kda_qk_norm_rope: a position outside the table. */
+#define KDA_DEVERR_POSITION 0x8u
+
+/* kda_qk_norm_rope: the rotation pairs elements (2 i, 2 i + 1) instead of (i, i + R/2). */
+#define KDA_FLAG_ROPE_INTERLEAVED 0x1u
+
+/*
+ * RMS norm of every query and key head, then the rotary position rotation, in one pass:
+ *   y = x / sqrt(mean(x^2) + eps) * weight;  for each pair (a, b) of the first R elements
+ *   a' = a cos - b sin,  b' = b cos + a sin   with cos, sin of the token's position.
+ *
+ *   q, q_out   bf16 [T, Hq, 128]    k, k_out  bf16 [T, Hk, 128]   (views; k and k_out may be absent)
+ *   q_weight, k_weight  fp32 [128], or NULL/absent (= 1)
+ *   eps        finite, >= 0
+ *   cos_sin    fp32 [P, R]: row p holds R/2 cosines, then R/2 sines, of position p; R a
+ *              multiple of 16, 16 <= R <= 128.  NULL/absent: no rotation (positions absent too)
+ *   positions  int64 [T].  A token whose position is outside [0, P) gets NaN in every
+ *              element, and KDA_DEVERR_POSITION is set in *status
+ *   status     device word (4-byte aligned) that error bits are added to, or NULL
+ *   flags      KDA_FLAG_ROPE_INTERLEAVED or 0
+ * q_out may be exactly q, and k_out exactly k (same data and strides): in place.  Any other
+ * overlap of an output with an input or the other output is KDA_ERR_ALIAS; columns of one
+ * buffer that do not meet are no overlap.  Arithmetic is fp32, rounded once at the end.
+ */
+kda_status kda_qk_norm_rope(const kda_view* q, const kda_view* k, const kda_tensor* q_weight,
+                            const kda_tensor* k_weight, float eps, const kda_tensor* cos_sin,
+                            const kda_tensor* positions, const kda_view* q_out, const kda_view* k_out,
+                            uint32_t* status, uint32_t flags, kda_stream_t stream);
+
+/*
+ * Bytes of workspace kda_attn_fwd needs for Tq query tokens, Hq query heads and Hk key/value
+ * heads.  Its contents need no initialisation.  Returns 0 for invalid arguments.
+ */
+size_t kda_attn_workspace_size(int64_t Tq, int Hq, int Hk);
+
+/*
+ * Causal softmax attention with grouped heads.  Query head h reads key/value head
+ * h / (Hq / Hk).  Sequence n has Lq queries and Lk keys; query i sees keys j <= i + Lk - Lq
+ * (the last query sees every key):
+ *   out_i = sum_j softmax_j(scale q_i . k_j) v_j,   lse_i = log sum_j exp(scale q_i . k_j)
+ * A query that sees no key (Lq > Lk, or no keys) gets out = 0 and lse = -inf.
+ *
+ *   q, out         bf16 [Tq, Hq, 128] (views)
+ *   lse            fp32 [Tq, Hq], or NULL/absent
+ *   k, v           packed: bf16 [Tk, Hk, 128];  cache: bf16 [N, S, Hk, 128] (views; Hk divides Hq,
+ *                  Hq / Hk <= 128)
+ *   cu_seqlens_q   int64 [N + 1]; NULL/absent: N sequences of Tq / N queries each (N from the cache
+ *                  or cu_seqlens_k, else 1)
+ *   cu_seqlens_k   packed keys: int64 [N + 1]; NULL/absent: the same as cu_seqlens_q (Tk == Tq there)
+ *                  or, without that either, N = 1.  Must be absent with a cache
+ *   seqlens_k      cache: int64 [N], sequence n's keys are k[n, 0 .. seqlens_k[n]); required with a
+ *                  cache, absent otherwise
+ *   workspace      >= kda_attn_workspace_size(Tq, Hq, Hk) bytes, 256-byte aligned
+ * Rows past a sequence's keys are never used, whatever they hold (NaN included); the keys and
+ * values inside a sequence are taken to be finite.  Query rows that belong to no sequence are not
+ * written.  out must overlap no other tensor (KDA_ERR_ALIAS).  Lengths that contradict the
+ * tensors set KDA_DEVERR_CU_SEQLENS in the workspace's status word, and nothing is written.
+ * Scores, softmax sums and the output's accumulation are fp32; the weights are rounded to
+ * bf16 for the product with v.  The same inputs give the same bits.
+ */
+kda_status kda_attn_fwd(const kda_view* q, const kda_view* k, const kda_view* v, float scale,
+                        const kda_view* out, const kda_tensor* lse, const kda_tensor* cu_seqlens_q,
+                        const kda_tensor* cu_seqlens_k, const kda_tensor* seqlens_k, void* workspace,
+                        size_t workspace_bytes, kda_stream_t stream);
+
+/*
+ * Bytes of workspace kda_lin_fwd needs for T_total = B*T tokens, H heads and N sequences
+ * (as for kda_workspace_size).  Its contents need no initialisation.  Returns 0 for negative
+ * arguments.
+ */
+size_t kda_lin_workspace_size(int64_t T_total, int H, int N);
+
+/*
+ * Linear attention with a decay for each head, over whole prompts: per (sequence, head) and
+ * per token,   S <- exp(log_decay[h]) S + v k^T,   out = scale S q   (S is V x K, as in kda_fwd).
+ *
+ *   q, k, v        bf16 [B, T, H, 128] (views);  out  bf16 [B, T, H, 128] (view)
+ *   log_decay      fp32 [H], the natural log of the decay (<= 0 in use; -inf forgets everything)
+ *   initial_state, final_state, cu_seqlens, workspace   as for kda_fwd, the workspace of
+ *                  kda_lin_workspace_size(B*T, H, Nseq) bytes
+ * Rows of tokens that belong to no sequence are not written; bad cu_seqlens contents set
+ * KDA_DEVERR_CU_SEQLENS, and then nothing is written.  out must overlap no other tensor
+ * (KDA_ERR_ALIAS).  Values past a sequence's end are never used, whatever they hold.  The
+ * state is kept and updated to fp32 accuracy across the whole sequence.
+ */
+kda_status kda_lin_fwd(const kda_view* q, const kda_view* k, const kda_view* v, const kda_tensor* log_decay,
+                       float scale, const kda_view* out, const kda_tensor* initial_state,
+                       const kda_tensor* final_state, const kda_tensor* cu_seqlens, void* workspace,
+                       size_t workspace_bytes, kda_stream_t stream);
+
+/*
+ * One token of the recurrence of kda_lin_fwd for every sequence.
+ *   q, k, v, out   bf16 [B, H, 128] (views);  log_decay  fp32 [H]
+ *   initial_state, final_state   as for kda_decode ([B, H, 128, 128]; in place allowed)
+ * No workspace and no device-side error.
+ */
+kda_status kda_lin_decode(const kda_view* q, const kda_view* k, const kda_view* v, const kda_tensor* log_decay,
+                          float scale, const kda_view* out, const kda_tensor* initial_state,
+                          const kda_tensor* final_state, kda_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
