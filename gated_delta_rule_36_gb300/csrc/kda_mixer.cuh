@@ -1,0 +1,102 @@
+// Building blocks shared by the tensor-core mixers (kda_attn.cu, kda_lin_fwd.cu): bounded waits
+// that wind a CTA down, bulk-tensor copies, tensor maps and the packed-sequence checks.
+#pragma once
+
+#include <cuda.h>
+
+#include "kda_device.cuh"
+#include "kda_ops.h"
+#include "kda_sm100.cuh"
+
+namespace kda {
+
+#ifdef KDA_WAIT_TEST
+constexpr long long MX_WAIT_LIMIT = 4000000LL;
+#else
+constexpr long long MX_WAIT_LIMIT = 2000000000LL;   // SM cycles (~1 s) before a wait gives up
+#endif
+
+// Wait for the phase with `parity`.  Returns false when the limit expires, or when another
+// warp of the CTA has given up (*abort): the caller then leaves its loop.  Every wait of these
+// kernels is one of these and no named barrier is used, so a CTA always reaches its end.
+__device__ __forceinline__ bool mx_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort, uint32_t* status) {
+    bool ok = mbar_test_wait(bar, parity);
+    if (!ok) {
+        const long long t0 = clock64();
+        while (!(ok = mbar_try_wait(bar, parity))) {
+            if (*abort) break;
+            if (clock64() - t0 > MX_WAIT_LIMIT) {
+                atomicOr(status, KDA_DEVERR_TIMEOUT);
+                *abort = 1u;
+                break;
+            }
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
+// One arrival for a converged warp whose lanes' earlier work the arrival publishes.
+__device__ __forceinline__ void mx_arrive_warp(uint32_t bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+    __syncwarp();
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int c0, int c1, int c2, int c3, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];\n" ::"r"(dst),
+        "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ float mx_u2f(uint32_t x) { return __uint_as_float(x); }
+
+// cuTensorMapEncodeTiled through the runtime's driver entry point (no libcuda link).
+typedef CUresult (*MxEncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+inline MxEncodeFn mx_encode_fn() {
+    static MxEncodeFn fn = []() -> MxEncodeFn {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return nullptr;
+        return reinterpret_cast<MxEncodeFn>(f);
+    }();
+    return fn;
+}
+
+// A bf16 tensor (128 channels, heads, rows, sequences) with strides in elements, read or
+// written in boxes of 64 channels x box_heads x box_rows in the 128-byte swizzle.
+inline bool mx_encode(CUtensorMap* m, const void* ptr, int64_t heads, int64_t rows, int64_t seqs, int64_t head_stride,
+                      int64_t row_stride, int64_t seq_stride, int box_heads, int box_rows) {
+    MxEncodeFn fn = mx_encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)HD, (cuuint64_t)heads, (cuuint64_t)(rows > 0 ? rows : 1), (cuuint64_t)(seqs > 0 ? seqs : 1)};
+    const cuuint64_t strides[3] = {(cuuint64_t)head_stride * 2, (cuuint64_t)row_stride * 2,
+                                   (cuuint64_t)(seq_stride > 0 ? seq_stride : row_stride) * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The same tensor without the sequence dimension, for stores of 64 channels x 1 head x box_rows.
+inline bool mx_encode_3d(CUtensorMap* m, const void* ptr, int64_t heads, int64_t rows, int64_t head_stride, int64_t row_stride,
+                         int box_rows) {
+    MxEncodeFn fn = mx_encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)HD, (cuuint64_t)heads, (cuuint64_t)(rows > 0 ? rows : 1)};
+    const cuuint64_t strides[2] = {(cuuint64_t)head_stride * 2, (cuuint64_t)row_stride * 2};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace kda
