@@ -17,9 +17,12 @@
 // (kStateOnly) sums v k^T over the share ends that a later share continues, and the second
 // starts from their decayed sum.
 //
-// Warp roles (three warpgroups): warps 0-3 turn W into P, scale O and write the output (thread =
-// token row); warps 4-7 make K' and carry the state (thread = key channel); warp 8 loads q, k,
-// v by TMA through a ring of two chunks; warp 9 issues the MMAs.  Every wait is bounded.
+// Warp roles: warps 0-3 turn W into P and scale O (thread = token row); warps 4-7 write the
+// output out; warps 8-11 carry the state (thread = key channel); warps 12-15 and 16-19 make K',
+// alternate parts of 32 tokens; warp 20 loads q, k, v by TMA through a ring of two chunks; warp
+// 21 issues the products W, O and P V, warp 22 those of KV.  Each scheduler of the SM then runs
+// one warp of every role, and the chunk lasts as long as the busiest role's chain of dependent
+// instructions; that is why K' is spread over two groups.  Every wait is bounded.
 //
 // Bound by HBM: 1,024 bytes a token-head against 4 x 128 x 128 x 2 (+ 2 x the state's extra
 // terms) flop; a chunk at HBM speed lasts about 5,700 SM cycles, its MMAs 3,072.
@@ -29,19 +32,21 @@ namespace kda {
 namespace {
 
 constexpr int LF_C = 128;            // tokens a chunk
-constexpr int LF_THREADS = 384;      // three warpgroups, the third with two idle warps
+constexpr int LF_THREADS = 768;      // six warpgroups, the last with an idle warp
 constexpr int LF_MAX_CTAS = 160;     // shares (and partial states) at most
 constexpr uint32_t TILE = 128 * 256; // one 128 x 128 bf16 tile: two 64-channel halves of 16 KB
 constexpr uint32_t HALF = TILE / 2;
 constexpr uint32_t STAGE = 3 * TILE; // q, k, v
 constexpr uint32_t OFF_S = 2 * STAGE;
-constexpr uint32_t OFF_POW = OFF_S + TILE;       // per warp: a^(31 - j), j < 32; and a short chunk's weights
-constexpr uint32_t OFF_BAR = OFF_POW + 12 * 128;
-enum { FQ = 0, FK = 2, FV = 4, EQ = 6, EK = 8, EV = 10, KPF = 12, KPE = 14, WF = 16, PF, QSF, OS, OF, OE, KVF, SB, DRAIN, NBAR };
-constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;   // tmem address, abort flag, scan scratch
-constexpr uint32_t LF_SMEM = OFF_MISC + 128 + 1024;
+// powers a^(31 - j), j < 32: for each of warps 0-3 followed by 32 zeros, for each of warps 12-19
+// alone (a short chunk puts its own weights there)
+constexpr uint32_t OFF_POW = OFF_S + TILE, OFF_KPOW = OFF_POW + 4 * 256;
+constexpr uint32_t OFF_BAR = OFF_KPOW + 8 * 128;
+enum { FQ = 0, FK = 2, FV = 4, EQ = 6, EK = 8, EV = 10, KPF = 12, KPE = 14, VR = 16, WF = 18, PF, QSF, OS, OF, OE, KVF, KVE, SB, DRAIN, DRAIN2, NBAR };
+constexpr uint32_t OFF_TMEM = OFF_BAR + NBAR * 8, OFF_ABORT = OFF_TMEM + 4;
+constexpr uint32_t LF_SMEM = OFF_ABORT + 4;   // no room to align the base: it has to be (and is checked to be) 1 KB aligned
 static_assert(LF_SMEM <= 232448, "one CTA's shared memory");
-// Tensor Memory columns: W then P; KV; O; two slots of K' (three terms of 16 columns: 32 tokens)
+// Tensor Memory columns: W then P; KV; O; two slots of K' (32 tokens: three terms of 16 columns)
 constexpr uint32_t TM_W = 0, TM_KV = 128, TM_O = 256, TM_KP = 384, KP_SLOT = 48;
 
 struct LinMaps {
@@ -100,7 +105,7 @@ __device__ __forceinline__ int64_t share_start(int64_t total, int b, int ctas) {
 // The whole CTA: checks cu_seqlens, counts the chunks and finds the chunk `x0` (of the share's
 // start, or with kEnd of its end) among the units in the order (n, h, c).
 template <bool kEnd>
-__device__ Share find_share(const LinParams& p, int64_t* scratch /* 16 */) {
+__device__ Share find_share(const LinParams& p, int64_t* scratch /* 32 */) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (p.nseq + LF_THREADS - 1) / LF_THREADS;
     const int n0 = min(tid * per, p.nseq), n1 = min(n0 + per, p.nseq);
@@ -159,16 +164,14 @@ __device__ Share find_share(const LinParams& p, int64_t* scratch /* 16 */) {
 }
 
 struct Ctx {
-    uint32_t base, tmem;
-    unsigned char* g;
-    volatile uint32_t* abort;
+    uint32_t base, tmem, abort;   // shared-window addresses, but tmem
     uint32_t* status;
     int64_t count;   // chunks to do
     __device__ uint32_t bar(int b) const { return base + OFF_BAR + 8u * b; }
     __device__ bool wait(int b, int64_t use) const { return mx_wait(bar(b), (uint32_t)(use & 1), abort, status); }
 };
 
-// ---------------------------------------------------------------- warp 8: loads
+// ---------------------------------------------------------------- warp 20: loads
 template <bool kStateOnly>
 __device__ void load_warp(const LinParams& p, const LinMaps& maps, const Ctx& x, Cursor u) {
     if ((threadIdx.x & 31) == 0) {
@@ -177,18 +180,7 @@ __device__ void load_warp(const LinParams& p, const LinMaps& maps, const Ctx& x,
             const int s = (int)(i & 1);
             const int t0 = (int)(u.bos + (int64_t)u.c * LF_C);
             auto one = [&](int full, int empty, const CUtensorMap* m, uint32_t off) {
-                if (i >= 2) {
-                    const uint32_t par = (uint32_t)(((i >> 1) - 1) & 1);
-                    const long long c0 = clock64();
-                    while (!mbar_try_wait(x.bar(empty + s), par)) {
-                        if (*x.abort) return false;
-                        if (clock64() - c0 > MX_WAIT_LIMIT) {
-                            atomicOr(x.status, KDA_DEVERR_TIMEOUT);
-                            *x.abort = 1u;
-                            return false;
-                        }
-                    }
-                }
+                if (i >= 2 && !mx_wait_lane(x.bar(empty + s), (uint32_t)(((i >> 1) - 1) & 1), x.abort, x.status)) return false;
                 const uint32_t dst = x.base + s * STAGE + off;
                 mbar_arrive_expect_tx(x.bar(full + s), TILE);
                 tma_load_4d(dst, m, 0, u.h, t0, 0, x.bar(full + s));
@@ -201,7 +193,7 @@ __device__ void load_warp(const LinParams& p, const LinMaps& maps, const Ctx& x,
         }
         // after a wait gave up: the copies in flight land before the CTA leaves (their phases
         // complete by themselves; a phase not armed is not waited for long)
-        if (*x.abort) {
+        if (lds_u32(x.abort)) {
             const long long c0 = clock64();
             while (clock64() - c0 < 2000000LL) __nanosleep(1000);
         }
@@ -209,187 +201,233 @@ __device__ void load_warp(const LinParams& p, const LinMaps& maps, const Ctx& x,
     __syncwarp();
 }
 
-// ---------------------------------------------------------------- warp 9: MMAs
-template <bool kStateOnly>
-__device__ void mma_warp(const LinParams& p, const Ctx& x) {
-    constexpr uint32_t id_kk = make_idesc_bf16_f32(128, 128);          // both operands K-major
-    constexpr uint32_t id_mn = make_idesc_bf16_f32(128, 128, true);    // B MN-major
-    const uint32_t tm = x.tmem, sS = x.base + OFF_S;
-    int64_t i = 0;
-    for (; i < x.count; ++i) {
+// ---------------------------------------------------------------- warps 21 and 22: MMAs
+// Descriptors: a slice of 16 along K is 32 bytes further in a K-major tile (64 of K to a half
+// tile), 2 KB further in an MN-major one.
+constexpr uint64_t K_STEP = 32 >> 4, K_HALF = HALF >> 4, MN_STEP = 2048 >> 4, D_STAGE = STAGE >> 4;
+constexpr uint32_t ID_KK = make_idesc_bf16_f32(128, 128);          // both operands K-major
+constexpr uint32_t ID_MN = make_idesc_bf16_f32(128, 128, true);    // B MN-major
+
+// the MMAs in flight finish before the CTA frees Tensor Memory
+__device__ __forceinline__ void drain_mma(const Ctx& x, int bar) {
+    __syncwarp();
+    tc_commit_warp(x.bar(bar));
+    if (!mbar_wait_bounded(x.bar(bar), 0, x.status, KDA_DEVERR_TIMEOUT, MX_WAIT_LIMIT)) sts_u32(x.abort, 1u);
+    __syncwarp();
+}
+
+__device__ void mma_out_warp(const Ctx& x) {
+    const uint32_t tm = x.tmem;
+    const uint64_t dQ = make_sdesc_kmajor_sw128(x.base), dS = make_sdesc_mnmajor_sw128(x.base + OFF_S, HALF, 1024);
+    for (int64_t i = 0; i < x.count; ++i) {
         const int s = (int)(i & 1);
         const int64_t use = i >> 1;
-        const uint32_t sQ = x.base + s * STAGE, sK = sQ + TILE, sV = sK + TILE;
-        if (!kStateOnly) {
-            // W = Q K^T, over the P that the previous chunk's product has read
-            if (i > 0 && !x.wait(OF, i - 1)) break;
-            if (!x.wait(FK + s, use) || !x.wait(FQ + s, use)) break;
-            tc_fence_after();
+        const uint64_t q = dQ + s * D_STAGE, k = q + (TILE >> 4);
+        // W = Q K^T, over the P that the previous chunk's product has read
+        if (i > 0 && !x.wait(OF, i - 1)) break;
+        if (!x.wait(FK + s, use) || !x.wait(FQ + s, use)) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half)
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-                tc_mma_ss_warp(tm + TM_W, make_sdesc_kmajor_sw128(sQ + (kk >> 2) * HALF + (kk & 3) * 32),
-                               make_sdesc_kmajor_sw128(sK + (kk >> 2) * HALF + (kk & 3) * 32), id_kk, kk > 0);
-            tc_commit_warp(x.bar(WF));
-            tc_commit_warp(x.bar(EK + s));
-            // O = Q S, once the state is in shared memory and the previous O has been read
-            if (!x.wait(SB, i) || (i > 0 && !x.wait(OE, i - 1))) break;
-            tc_fence_after();
+            for (int kk = 0; kk < 4; ++kk)
+                tc_mma_ss_warp(tm + TM_W, q + half * K_HALF + kk * K_STEP, k + half * K_HALF + kk * K_STEP, ID_KK, half + kk > 0);
+        tc_commit_warp(x.bar(WF));
+        tc_commit_warp(x.bar(EK + s));
+        // O = Q S, once the state is in shared memory and the previous O has been read
+        if (!x.wait(SB, i) || (i > 0 && !x.wait(OE, i - 1))) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half)
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-                tc_mma_ss_warp(tm + TM_O, make_sdesc_kmajor_sw128(sQ + (kk >> 2) * HALF + (kk & 3) * 32),
-                               make_sdesc_mnmajor_sw128(sS + kk * 2048, HALF, 1024), id_mn, kk > 0);
-            tc_commit_warp(x.bar(QSF));
-        }
-        // KV = K'^T V, 32 tokens at a time as warps 4-7 hand them over
-        if (!x.wait(FV + s, use)) break;
+            for (int kk = 0; kk < 4; ++kk)
+                tc_mma_ss_warp(tm + TM_O, q + half * K_HALF + kk * K_STEP, dS + (4 * half + kk) * MN_STEP, ID_MN, half + kk > 0);
+        tc_commit_warp(x.bar(QSF));
+        // O += P V
+        if (!x.wait(VR + s, use) || !x.wait(PF, i) || !x.wait(OS, i)) break;
+        tc_fence_after();
+        const uint64_t v = make_sdesc_mnmajor_sw128(x.base + s * STAGE + 2 * TILE, HALF, 1024);
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+                tc_mma_ts_warp(tm + TM_O, tm + TM_W + (4 * half + kk) * 8, v + (4 * half + kk) * MN_STEP, ID_MN, 1u);
+        tc_commit_warp(x.bar(OF));
+        tc_commit_warp(x.bar(EV + s));
+    }
+    drain_mma(x, DRAIN);
+}
+
+// KV = K'^T V, 32 tokens at a time as the key warps hand them over
+__device__ void mma_state_warp(const Ctx& x) {
+    const uint32_t tm = x.tmem;
+    for (int64_t i = 0; i < x.count; ++i) {
+        const int s = (int)(i & 1);
+        const uint64_t v = make_sdesc_mnmajor_sw128(x.base + s * STAGE + 2 * TILE, HALF, 1024);
+        if (!x.wait(VR + s, i >> 1) || (i > 0 && !x.wait(KVE, i - 1))) break;
         bool ok = true;
 #pragma unroll 1
-        for (int b = 0; b < 4 && ok; ++b) {
+        for (int b = 0; b < 4; ++b) {
             const int slot = b & 1;
             ok = x.wait(KPF + slot, 2 * i + (b >> 1));
             if (!ok) break;
             tc_fence_after();
+            const uint32_t a = tm + TM_KP + slot * KP_SLOT;
+            const uint64_t vb = v + 2 * b * MN_STEP;
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-                for (int term = 0; term < 3; ++term)
-                    tc_mma_ts_warp(tm + TM_KV, tm + TM_KP + slot * KP_SLOT + term * 16 + kk * 8,
-                                   make_sdesc_mnmajor_sw128(sV + (2 * b + kk) * 2048, HALF, 1024), id_mn, b + kk + term > 0);
+            for (int kk = 0; kk < 2; ++kk) {
+                tc_mma_ts_warp(tm + TM_KV, a + 8 * kk, vb + kk * MN_STEP, ID_MN, b + kk > 0);
+                tc_mma_ts_warp(tm + TM_KV, a + 16 + 8 * kk, vb + kk * MN_STEP, ID_MN, 1u);
+                tc_mma_ts_warp(tm + TM_KV, a + 32 + 8 * kk, vb + kk * MN_STEP, ID_MN, 1u);
+            }
             tc_commit_warp(x.bar(KPE + slot));
         }
         if (!ok) break;
         tc_commit_warp(x.bar(KVF));
-        if (kStateOnly) {
-            tc_commit_warp(x.bar(EV + s));
-            continue;
-        }
-        // O += P V
-        if (!x.wait(PF, i) || !x.wait(OS, i)) break;
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-            tc_mma_ts_warp(tm + TM_O, tm + TM_W + kk * 8, make_sdesc_mnmajor_sw128(sV + kk * 2048, HALF, 1024), id_mn, 1u);
-        tc_commit_warp(x.bar(OF));
         tc_commit_warp(x.bar(EV + s));
     }
-    // the MMAs in flight finish before the CTA frees Tensor Memory
-    tc_commit_warp(x.bar(DRAIN));
-    if (!mbar_wait_bounded(x.bar(DRAIN), 0, x.status, KDA_DEVERR_TIMEOUT, MX_WAIT_LIMIT)) *x.abort = 1u;
-    __syncwarp();
+    drain_mma(x, DRAIN2);
 }
 
-// ---------------------------------------------------------------- warps 0-3: P, O, output
-__device__ void out_warps(const LinParams& p, const LinMaps& maps, const Ctx& x, Cursor u) {
+// ---------------------------------------------------------------- warps 0-3: P and the scale of O
+__device__ void score_warps(const LinParams& p, const Ctx& x, Cursor u) {
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(32 * warp) << 16;
-    float* pow = reinterpret_cast<float*>(x.g + OFF_POW + warp * 128);
-    float l2 = 0.f, since = 0.f;
+    const uint32_t pow = x.base + OFF_POW + warp * 256;
+    sts_f32(pow + 128 + 4 * lane, 0.f);
+    float since = 0.f, left = 0.f, hop = 0.f;
     int h = -1;
-    int64_t i = 0;
-    for (; i < x.count; ++i, next_chunk(p, u)) {
-        const int s = (int)(i & 1);
-        const int valid = chunk_tokens(u);
+    for (int64_t i = 0; i < x.count; ++i, next_chunk(p, u)) {
         if (u.h != h) {
             h = u.h;
-            l2 = log2_decay(p, h);
+            const float l2 = log2_decay(p, h);
             __syncwarp();
-            pow[lane] = exp2f(l2 * (float)(31 - lane));
+            sts_f32(pow + 4 * lane, exp2f(l2 * (float)(31 - lane)));
+            __syncwarp();
             since = p.scale * exp2f(l2 * (float)(row + 1));
-            __syncwarp();
+            // the row's factor for the block just left of the diagonal one, and from block to block
+            left = p.scale * exp2f(l2 * (float)(lane + 1));
+            hop = exp2f(l2 * 32.f);
         }
-        // P: column blocks of 32; the blocks left of this warp's rows factor into a power for the
-        // row and one for the column (all exponents >= 0), the diagonal one takes a^(i-j) each
+        // P, in blocks of 32 columns (its 16 registers a block go over columns of W that have been
+        // read): left of the diagonal block a^(i-j) is a power for the row times one for the column, all
+        // exponents >= 0; in the diagonal block it is looked up; right of it P is zero
         if (!x.wait(WF, i)) break;
         tc_fence_after();
+        uint32_t w[32], y[16];
 #pragma unroll 1
-        for (int b = 0; b < 4; ++b) {
-            uint32_t w[32], o[16];
-            if (b < warp) {
-                tmem_ld32(x.tmem + lanes + TM_W + 32 * b, w);
-                const float f = p.scale * exp2f(l2 * (float)(row - 32 * b - 31));
-                tmem_wait_ld();
+        for (int b = 0; b < warp; ++b) {
+            tmem_ld32(x.tmem + lanes + TM_W + 32 * b, w);
+            const int e = warp - 1 - b;
+            const float f = e == 0 ? left : e == 1 ? left * hop : left * hop * hop;
+            const float2 f2 = make_float2(f, f);
+            tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                    const float4 c = *reinterpret_cast<const float4*>(pow + j);
-                    o[j / 2] = pack_bf16x2(mx_u2f(w[j]) * (f * c.x), mx_u2f(w[j + 1]) * (f * c.y));
-                    o[j / 2 + 1] = pack_bf16x2(mx_u2f(w[j + 2]) * (f * c.z), mx_u2f(w[j + 3]) * (f * c.w));
-                }
-            } else if (b == warp) {
-                tmem_ld32(x.tmem + lanes + TM_W + 32 * b, w);
-                tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 32; j += 2) {
-                    const float a0 = j <= lane ? mx_u2f(w[j]) * (p.scale * pow[31 - (lane - j)]) : 0.f;
-                    const float a1 = j + 1 <= lane ? mx_u2f(w[j + 1]) * (p.scale * pow[31 - (lane - j - 1)]) : 0.f;
-                    o[j / 2] = pack_bf16x2(a0, a1);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) o[j] = 0u;
+            for (int j = 0; j < 32; j += 4) {
+                const float4 c = lds_f32x4(pow + 4 * j);
+                const float2 y0 = __fmul2_rn(make_float2(mx_u2f(w[j]), mx_u2f(w[j + 1])), __fmul2_rn(f2, make_float2(c.x, c.y)));
+                const float2 y1 = __fmul2_rn(make_float2(mx_u2f(w[j + 2]), mx_u2f(w[j + 3])), __fmul2_rn(f2, make_float2(c.z, c.w)));
+                y[j / 2] = pack_bf16x2(y0.x, y0.y);
+                y[j / 2 + 1] = pack_bf16x2(y1.x, y1.y);
             }
-            tmem_st16(x.tmem + lanes + TM_W + 16 * b, o);
+            tmem_st16(x.tmem + lanes + TM_W + 16 * b, y);
         }
+        tmem_ld32(x.tmem + lanes + TM_W + 32 * warp, w);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {   // a^(lane - j) is power 31 - lane + j of the table, zeros follow
+            const float a0 = mx_u2f(w[j]) * (p.scale * lds_f32(pow + 4 * (31 + j) - 4 * lane));
+            const float a1 = mx_u2f(w[j + 1]) * (p.scale * lds_f32(pow + 4 * (32 + j) - 4 * lane));
+            y[j / 2] = pack_bf16x2(j <= lane ? a0 : 0.f, j < lane ? a1 : 0.f);   // whatever W holds there
+        }
+        tmem_st16(x.tmem + lanes + TM_W + 16 * warp, y);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) y[j] = 0u;
+#pragma unroll 1
+        for (int b = warp + 1; b < 4; ++b) tmem_st16(x.tmem + lanes + TM_W + 16 * b, y);
         tmem_wait_st();
         tc_fence_before();
         mx_arrive_warp(x.bar(PF));
         // O = Q S, each row scaled by scale a^(i+1)
         if (!x.wait(QSF, i)) break;
         tc_fence_after();
+        const float2 s2 = make_float2(since, since);
 #pragma unroll 1
         for (int b = 0; b < 4; ++b) {
             uint32_t w[32];
             tmem_ld32(x.tmem + lanes + TM_O + 32 * b, w);
             tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(mx_u2f(w[j]) * since);
+            for (int j = 0; j < 32; j += 2) {
+                const float2 y = __fmul2_rn(make_float2(mx_u2f(w[j]), mx_u2f(w[j + 1])), s2);
+                w[j] = __float_as_uint(y.x);
+                w[j + 1] = __float_as_uint(y.y);
+            }
             tmem_st32(x.tmem + lanes + TM_O + 32 * b, w);
         }
         tmem_wait_st();
         tc_fence_before();
         mx_arrive_warp(x.bar(OS));
-        // the previous chunk's output tile has left its q buffer
-        if (i > 0 && lane == 0) {
-            bulk_wait_read_all();
-            mbar_arrive(x.bar(EQ + (s ^ 1)));
-        }
-        __syncwarp();
-        // the output, through this chunk's q buffer (both products have read it)
+    }
+}
+
+// ---------------------------------------------------------------- warps 4-7: the output
+__device__ void out_warps(const LinParams& p, const LinMaps& maps, const Ctx& x, Cursor u) {
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, row = threadIdx.x & 127;
+    const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+    for (int64_t i = 0; i < x.count; ++i, next_chunk(p, u)) {
+        const int s = (int)(i & 1);
+        const int valid = chunk_tokens(u);
         if (!x.wait(OF, i)) break;
         tc_fence_after();
+        // through this chunk's q buffer (both products have read it); a short chunk's rows go
+        // straight to memory
         const int64_t t0 = u.bos + (int64_t)u.c * LF_C;
-        unsigned char* tile = x.g + s * STAGE;
+        const bool full = valid == LF_C;
+        const uint32_t tile = x.base + s * STAGE + row * 128;
+        __nv_bfloat16* direct = p.out.data + (t0 + row) * p.out.row + u.h * p.out.head;
+        const bool mine = row < valid;
 #pragma unroll 1
         for (int b = 0; b < 4; ++b) {
             uint32_t w[32];
             tmem_ld32(x.tmem + lanes + TM_O + 32 * b, w);
             tmem_wait_ld();
+            uint32_t o[16];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint4 o = make_uint4(pack_bf16x2(mx_u2f(w[8 * j]), mx_u2f(w[8 * j + 1])), pack_bf16x2(mx_u2f(w[8 * j + 2]), mx_u2f(w[8 * j + 3])),
-                                           pack_bf16x2(mx_u2f(w[8 * j + 4]), mx_u2f(w[8 * j + 5])), pack_bf16x2(mx_u2f(w[8 * j + 6]), mx_u2f(w[8 * j + 7])));
-                if (valid == LF_C) *reinterpret_cast<uint4*>(tile + sw128_offset(row, 32 * b + 8 * j, 128)) = o;
-                else if (row < valid) *reinterpret_cast<uint4*>(p.out.data + (t0 + row) * p.out.row + u.h * p.out.head + 32 * b + 8 * j) = o;
+            for (int j = 0; j < 16; ++j) o[j] = pack_bf16x2(mx_u2f(w[2 * j]), mx_u2f(w[2 * j + 1]));
+            if (full) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    sts_u128(tile + (b >> 1) * HALF + (((4 * (b & 1) + j) ^ (row & 7)) << 4), o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            } else if (mine) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    *reinterpret_cast<uint4*>(direct + 32 * b + 8 * j) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
             }
         }
         tc_fence_before();
         mx_arrive_warp(x.bar(OE));
-        if (valid == LF_C) {
+        if (full) {
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) {
+        }
+        if (lane == 0) {
+            if (full) {
                 const uint32_t src = x.base + s * STAGE + 32 * warp * 128;
                 tma_store_3d(&maps.out, src, 0, u.h, (int)t0 + 32 * warp);
                 tma_store_3d(&maps.out, src + HALF, 64, u.h, (int)t0 + 32 * warp);
                 bulk_commit();
+                bulk_wait_read_all();
             }
-            __syncwarp();
+            mbar_arrive(x.bar(EQ + s));
         }
+        __syncwarp();
     }
     if (lane == 0) bulk_wait_all();
     __syncwarp();
 }
 
-// ---------------------------------------------------------------- warps 4-7: K' and the state
+// ---------------------------------------------------------------- warps 8-11: the state
 // Thread k holds S[k][0 .. 127] (column v).  Global states are [V][K]: the 32 lanes of a warp
 // read and write 32 neighbouring k of one v.
 __device__ __forceinline__ float state_at(const void* s, int f32, size_t off) {
@@ -398,158 +436,201 @@ __device__ __forceinline__ float state_at(const void* s, int f32, size_t off) {
 
 template <bool kStateOnly>
 __device__ void state_warps(const LinParams& p, const Ctx& x, Cursor u, const Share& share) {
-    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, k = threadIdx.x & 127;
+    const int warp = (threadIdx.x >> 5) & 3, k = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(32 * warp) << 16;
-    float* pow = reinterpret_cast<float*>(x.g + OFF_POW + (4 + warp) * 128);
-    float* tail = reinterpret_cast<float*>(x.g + OFF_POW + (8 + warp) * 128);
-    float S[LF_C];
+    float2 S[LF_C / 2];
     float l2 = 0.f, all = 0.f;
     bool fresh = true;   // a unit (or this share) starts
-    int64_t i = 0;
-    for (; i < x.count; ++i, next_chunk(p, u)) {
-        const int s = (int)(i & 1);
+    for (int64_t i = 0; i < x.count; ++i, next_chunk(p, u)) {
         const int valid = chunk_tokens(u);
         const size_t unit = (size_t)u.n * p.H + u.h;
         if (fresh) {
             fresh = false;
             l2 = log2_decay(p, u.h);
-            __syncwarp();
-            pow[lane] = exp2f(l2 * (float)(31 - lane));
             all = exp2f(l2 * (float)LF_C);
-            __syncwarp();
-            if (kStateOnly || (u.c == 0 && p.init_state == nullptr)) {
+            if (kStateOnly || p.init_state == nullptr) {
 #pragma unroll
-                for (int v = 0; v < LF_C; ++v) S[v] = 0.f;
+                for (int v = 0; v < LF_C / 2; ++v) S[v] = make_float2(0.f, 0.f);
             } else {
                 const float f = exp2f(l2 * (float)u.c * (float)LF_C);
-                if (p.init_state) {
+                const size_t off = unit * HD * HD + k;
 #pragma unroll
-                    for (int v = 0; v < LF_C; ++v) S[v] = f * state_at(p.init_state, p.init_f32, (unit * HD + v) * HD + k);
-                } else {
-#pragma unroll
-                    for (int v = 0; v < LF_C; ++v) S[v] = 0.f;
-                }
+                for (int v = 0; v < LF_C / 2; ++v)
+                    S[v] = make_float2(f * state_at(p.init_state, p.init_f32, off + (size_t)(2 * v) * HD),
+                                       f * state_at(p.init_state, p.init_f32, off + (size_t)(2 * v + 1) * HD));
+            }
+            if (!kStateOnly && u.c > 0) {
                 // the shares before this one that hold earlier chunks of the unit
                 const int64_t first = share.x0 - u.c;
-                for (int b = (int)blockIdx.x - 1; u.c > 0 && b >= 0; --b) {
+                for (int b = (int)blockIdx.x - 1; b >= 0; --b) {
                     const int64_t end = share_start(share.total, b + 1, gridDim.x);
                     if (end <= first) break;
                     if (share_start(share.total, b, gridDim.x) == end) continue;
                     const float g = exp2f(l2 * (float)(share.x0 - end) * (float)LF_C);
                     const float* part = static_cast<const float*>(p.workspace) + (size_t)b * HD * HD + k;
 #pragma unroll
-                    for (int v = 0; v < LF_C; ++v) S[v] = fmaf(g, __ldg(part + v * HD), S[v]);
+                    for (int v = 0; v < LF_C / 2; ++v) {
+                        S[v].x = fmaf(g, __ldg(part + (2 * v) * HD), S[v].x);
+                        S[v].y = fmaf(g, __ldg(part + (2 * v + 1) * HD), S[v].y);
+                    }
                 }
             }
         }
         if (!kStateOnly) {
             // the bf16 copy of the state, once the previous product with it is done
             if (i > 0 && !x.wait(QSF, i - 1)) break;
-            unsigned char* tile = x.g + OFF_S;
+            const uint32_t tile = x.base + OFF_S + k * 128;
 #pragma unroll
-            for (int v = 0; v < LF_C; v += 8)
-                *reinterpret_cast<uint4*>(tile + sw128_offset(k, v, 128)) =
-                    make_uint4(pack_bf16x2(S[v], S[v + 1]), pack_bf16x2(S[v + 2], S[v + 3]), pack_bf16x2(S[v + 4], S[v + 5]), pack_bf16x2(S[v + 6], S[v + 7]));
+            for (int c = 0; c < 16; ++c)
+                sts_u128(tile + (c >> 3) * HALF + (((c & 7) ^ (k & 7)) << 4), pack_bf16x2(S[4 * c].x, S[4 * c].y),
+                         pack_bf16x2(S[4 * c + 1].x, S[4 * c + 1].y), pack_bf16x2(S[4 * c + 2].x, S[4 * c + 2].y),
+                         pack_bf16x2(S[4 * c + 3].x, S[4 * c + 3].y));
             fence_proxy_async_smem();
             mx_arrive_warp(x.bar(SB));
         }
-        // K': 32 tokens at a time, transposed into lane k, each value as a sum of three bf16
-        if (!x.wait(FK + s, i >> 1)) break;
-        if (valid < LF_C) {   // rows past the end count for nothing, whatever they hold
-            if (!x.wait(FV + s, i >> 1)) break;
-            unsigned char* v = x.g + s * STAGE + 2 * TILE;
-            for (int r = valid + warp; r < LF_C; r += 4)
-                *reinterpret_cast<uint2*>(v + (lane >> 4) * HALF + r * 128 + (lane & 15) * 8) = make_uint2(0u, 0u);
-            fence_proxy_async_smem();
-        }
-        const unsigned char* kt = x.g + s * STAGE + TILE + (k >> 6) * HALF + (k & 7) * 2;
-        const int kc = (k >> 3) & 7;
-        bool ok = true;
-#pragma unroll 1
-        for (int b = 0; b < 4; ++b) {
-            const int slot = b & 1;
-            const int64_t use = 2 * i + (b >> 1);
-            if (use > 0) ok = x.wait(KPE + slot, use - 1);
-            if (!ok) break;
-            tc_fence_after();
-            uint32_t raw[16];   // two tokens each
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-                const unsigned char* at = kt + (32 * b + j) * 128;
-                raw[j / 2] = *reinterpret_cast<const uint16_t*>(at + ((kc ^ (j & 7)) << 4)) |
-                             (uint32_t)*reinterpret_cast<const uint16_t*>(at + 128 + ((kc ^ ((j + 1) & 7)) << 4)) << 16;
-            }
-            if (valid < LF_C) {
-                // weights of a shorter chunk; tokens past the end count for nothing
-                __syncwarp();
-                tail[lane] = 32 * b + lane < valid ? exp2f(l2 * (float)(valid - 1 - 32 * b - lane)) : 0.f;
-                __syncwarp();
-#pragma unroll
-                for (int j = 0; j < 32; j += 2) {
-                    if (32 * b + j >= valid) raw[j / 2] = 0u;
-                    else if (32 * b + j + 1 >= valid) raw[j / 2] &= 0xffffu;
-                }
-            }
-            const float f = valid < LF_C ? 1.f : exp2f(l2 * (float)(96 - 32 * b));
-            const float* weight = valid < LF_C ? tail : pow;
-            uint32_t hi[16], mid[16], lo[16];
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-                const float4 w = *reinterpret_cast<const float4*>(weight + j);
-                const float y[4] = {bf16_lo(raw[j / 2]) * (f * w.x), bf16_hi(raw[j / 2]) * (f * w.y),
-                                    bf16_lo(raw[j / 2 + 1]) * (f * w.z), bf16_hi(raw[j / 2 + 1]) * (f * w.w)};
-#pragma unroll
-                for (int e = 0; e < 4; e += 2) {
-                    const uint32_t a = pack_bf16x2(y[e], y[e + 1]);
-                    const float r0 = y[e] - bf16_lo(a), r1 = y[e + 1] - bf16_hi(a);
-                    const uint32_t m = pack_bf16x2(r0, r1);
-                    hi[(j + e) / 2] = a;
-                    mid[(j + e) / 2] = m;
-                    lo[(j + e) / 2] = pack_bf16x2(r0 - bf16_lo(m), r1 - bf16_hi(m));
-                }
-            }
-            const uint32_t kp = x.tmem + lanes + TM_KP + slot * KP_SLOT;
-            tmem_st16(kp, hi);
-            tmem_st16(kp + 16, mid);
-            tmem_st16(kp + 32, lo);
-            tmem_wait_st();
-            tc_fence_before();
-            mx_arrive_warp(x.bar(KPF + slot));
-        }
-        if (!ok) break;
-        mx_arrive_warp(x.bar(EK + s));
         // S <- a^C S + KV
         if (!x.wait(KVF, i)) break;
         tc_fence_after();
         const float ac = valid == LF_C ? all : exp2f(l2 * (float)valid);
+        const float2 ac2 = make_float2(ac, ac);
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            uint32_t w[32];
-            tmem_ld32(x.tmem + lanes + TM_KV + 32 * b, w);
+        for (int b = 0; b < 8; ++b) {
+            uint32_t w[16];
+            tmem_ld16(x.tmem + lanes + TM_KV + 16 * b, w);
             tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) S[32 * b + j] = fmaf(ac, S[32 * b + j], mx_u2f(w[j]));
+            for (int j = 0; j < 8; ++j)
+                S[8 * b + j] = __ffma2_rn(ac2, S[8 * b + j], make_float2(mx_u2f(w[2 * j]), mx_u2f(w[2 * j + 1])));
         }
         tc_fence_before();
+        mx_arrive_warp(x.bar(KVE));
         if (kStateOnly) {
             if (i + 1 == x.count) {
                 float* part = static_cast<float*>(p.workspace) + (size_t)blockIdx.x * HD * HD + k;
 #pragma unroll
-                for (int v = 0; v < LF_C; ++v) part[v * HD] = S[v];
+                for (int v = 0; v < LF_C / 2; ++v) {
+                    part[(2 * v) * HD] = S[v].x;
+                    part[(2 * v + 1) * HD] = S[v].y;
+                }
             }
         } else if (u.c + 1 == u.nc) {
             fresh = true;
             if (p.final_state) {
                 const size_t off = unit * HD * HD + k;
                 if (p.final_f32) {
+                    float* f = static_cast<float*>(p.final_state) + off;
 #pragma unroll
-                    for (int v = 0; v < LF_C; ++v) static_cast<float*>(p.final_state)[off + (size_t)v * HD] = S[v];
+                    for (int v = 0; v < LF_C / 2; ++v) {
+                        f[(2 * v) * HD] = S[v].x;
+                        f[(2 * v + 1) * HD] = S[v].y;
+                    }
                 } else {
+                    __nv_bfloat16* f = static_cast<__nv_bfloat16*>(p.final_state) + off;
 #pragma unroll
-                    for (int v = 0; v < LF_C; ++v) static_cast<__nv_bfloat16*>(p.final_state)[off + (size_t)v * HD] = __float2bfloat16_rn(S[v]);
+                    for (int v = 0; v < LF_C / 2; ++v) {
+                        f[(2 * v) * HD] = __float2bfloat16_rn(S[v].x);
+                        f[(2 * v + 1) * HD] = __float2bfloat16_rn(S[v].y);
+                    }
                 }
             }
         }
+    }
+}
+
+// ---------------------------------------------------------------- warps 12-19: K'
+// Thread k reads column k of the key tile, weighs it by a^(C-1-j) and leaves each value as a
+// sum of three bf16 in lane k of Tensor Memory, 32 tokens at a time; group g takes the parts
+// g and g + 2 of each chunk and owns slot g.
+__device__ __forceinline__ float2 unpack2(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
+
+__device__ void key_warps(const LinParams& p, const Ctx& x, Cursor u, int g) {
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, k = threadIdx.x & 127;
+    const uint32_t kp = x.tmem + ((uint32_t)(32 * warp) << 16) + TM_KP + g * KP_SLOT;
+    const uint32_t pow = x.base + OFF_KPOW + (4 * g + warp) * 128;
+    const int kc = (k >> 3) & 7;
+    const float2 minus = make_float2(-1.f, -1.f);
+    float l2 = 0.f, hop = 0.f;
+    int h = -1;
+    for (int64_t i = 0; i < x.count; ++i, next_chunk(p, u)) {
+        const int s = (int)(i & 1);
+        const int valid = chunk_tokens(u);
+        const bool full = valid == LF_C;
+        if (u.h != h || !full) {
+            h = u.h;
+            l2 = log2_decay(p, h);
+            __syncwarp();
+            sts_f32(pow + 4 * lane, exp2f(l2 * (float)(31 - lane)));   // (a short chunk puts its own weights there)
+            __syncwarp();
+            hop = exp2f(l2 * 32.f);
+            if (!full) h = -1;
+        }
+        if (!x.wait(FK + s, i >> 1)) break;
+        if (g == 0) {
+            // v is ready once it has landed and, in a short chunk, the values past its end are
+            // zeros: they count for nothing, whatever they hold.  (Every chunk waits here, so that
+            // this barrier never gets ahead of the value tile's use.)
+            if (!x.wait(FV + s, i >> 1)) break;
+            if (!full) {
+                const uint32_t v = x.base + s * STAGE + 2 * TILE;
+                for (int r = valid + warp; r < LF_C; r += 4) sts_u64(v + (lane >> 4) * HALF + r * 128 + (lane & 15) * 8, 0u, 0u);
+                fence_proxy_async_smem();
+            }
+            mx_arrive_warp(x.bar(VR + s));
+        }
+        bool ok = true;
+#pragma unroll 1
+        for (int b = g; b < 4; b += 2) {
+            const int64_t use = 2 * i + (b >> 1);
+            uint32_t kt = x.base + s * STAGE + TILE + (k >> 6) * HALF + (k & 7) * 2 + 32 * b * 128;
+            float f = b == 3 ? 1.f : b == 2 ? hop : b == 1 ? hop * hop : hop * hop * hop;   // a^(96 - 32 b)
+            if (!full) {
+                f = 1.f;
+                const int t = 32 * b + lane;
+                __syncwarp();
+                sts_f32(pow + 4 * lane, t < valid ? exp2f(l2 * (float)(valid - 1 - t)) : 0.f);
+                __syncwarp();
+            }
+            const float2 f2 = make_float2(f, f);
+            if (use > 0) ok = x.wait(KPE + g, use - 1);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int q = 0; q < 2; ++q, kt += 16 * 128) {
+                uint32_t raw[16];   // bf16 bits in the upper half
+#pragma unroll
+                for (int j = 0; j < 16; ++j) raw[j] = lds_u16(kt + j * 128 + ((kc ^ (j & 7)) << 4)) << 16;
+                if (!full) {   // keys past the end: zeros, whatever they hold
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (32 * b + 16 * q + j >= valid) raw[j] = 0u;
+                }
+                uint32_t hi[8], mid[8], lo[8];
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                    const float4 w4 = lds_f32x4(pow + 4 * (16 * q + j));
+#pragma unroll
+                    for (int d = 0; d < 4; d += 2) {
+                        const float2 w = __fmul2_rn(f2, d ? make_float2(w4.z, w4.w) : make_float2(w4.x, w4.y));
+                        const float2 y = __fmul2_rn(make_float2(mx_u2f(raw[j + d]), mx_u2f(raw[j + d + 1])), w);
+                        const uint32_t a = pack_bf16x2(y.x, y.y);
+                        const float2 r = __ffma2_rn(unpack2(a), minus, y);
+                        const uint32_t m = pack_bf16x2(r.x, r.y);
+                        const float2 t = __ffma2_rn(unpack2(m), minus, r);
+                        hi[(j + d) / 2] = a;
+                        mid[(j + d) / 2] = m;
+                        lo[(j + d) / 2] = pack_bf16x2(t.x, t.y);
+                    }
+                }
+                tmem_st8(kp + 8 * q, hi);
+                tmem_st8(kp + 16 + 8 * q, mid);
+                tmem_st8(kp + 32 + 8 * q, lo);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            mx_arrive_warp(x.bar(KPF + g));
+        }
+        if (!ok) break;
+        mx_arrive_warp(x.bar(EK + s));
     }
 }
 
@@ -578,17 +659,19 @@ __device__ void empty_units(const LinParams& p) {
 
 template <bool kStateOnly>
 __global__ void __launch_bounds__(LF_THREADS, 1) lin_fwd_kernel(const LinParams p, const __grid_constant__ LinMaps maps) {
-    extern __shared__ unsigned char smem_raw[];
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
     const int tid = threadIdx.x, warp = tid >> 5;
     Ctx x;
-    const uint32_t raw = smem_u32(smem_raw);
-    x.base = (raw + 1023u) & ~1023u;
-    x.g = smem_raw + (x.base - raw);
-    x.abort = reinterpret_cast<volatile uint32_t*>(x.g + OFF_MISC + 4);
+    x.base = smem_u32(smem_raw);
+    x.abort = x.base + OFF_ABORT;
     x.status = p.status;
-    Share share = find_share<kStateOnly>(p, reinterpret_cast<int64_t*>(x.g + OFF_S));
+    Share share = find_share<kStateOnly>(p, reinterpret_cast<int64_t*>(smem_raw + OFF_S));
     if (!kStateOnly && blockIdx.x == 0 && tid == 0) *p.status = share.bad ? KDA_DEVERR_CU_SEQLENS : 0u;
     if (share.bad) return;
+    if (x.base % 1024 != 0) {   // the tiles' swizzle counts from 1 KB boundaries
+        if (tid == 0) atomicOr(p.status, KDA_DEVERR_INTERNAL);
+        return;
+    }
     Cursor u = share.at;
     if (kStateOnly) {
         // the share's last chunks, if its end lies inside a unit; u is the chunk after them
@@ -603,35 +686,44 @@ __global__ void __launch_bounds__(LF_THREADS, 1) lin_fwd_kernel(const LinParams 
     }
     if (tid == 0) {
         for (int b = 0; b < NBAR; ++b) {
-            const bool warps = b == EQ || b == EQ + 1 || b == KPF || b == KPF + 1 || b == PF || b == OS || b == OE || b == SB;
-            const bool both = b == EK || b == EK + 1;   // the key tile: W's MMA and the four state warps
-            mbar_init(x.bar(b), warps ? 4 : both ? (kStateOnly ? 4 : 5) : 1);
+            const bool warps = b == EQ || b == EQ + 1 || b == KPF || b == KPF + 1 || b == VR || b == VR + 1 || b == PF || b == OS || b == OE || b == SB || b == KVE;
+            const bool both = b == EK || b == EK + 1;   // the key tile: W's MMA and the eight key warps
+            const bool twice = b == EV || b == EV + 1;  // the value tile: KV's and P V's MMAs
+            mbar_init(x.bar(b), warps ? 4 : both ? (kStateOnly ? 8 : 9) : twice ? (kStateOnly ? 1 : 2) : 1);
         }
         mbar_fence_init();
-        *x.abort = 0u;
+        sts_u32(x.abort, 0u);
         tma_prefetch_desc(&maps.q);
         tma_prefetch_desc(&maps.k);
         tma_prefetch_desc(&maps.v);
         tma_prefetch_desc(&maps.out);
     }
     if (warp == 0) {
-        tmem_alloc(x.base + OFF_MISC, 512);
+        tmem_alloc(x.base + OFF_TMEM, 512);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    x.tmem = *reinterpret_cast<volatile uint32_t*>(x.g + OFF_MISC);
-    // registers a thread: 168 at launch; 168 + 240 + 96 of the 3 x 168 that the block holds
+    x.tmem = lds_u32(x.base + OFF_TMEM);
+    // registers a thread: 80 at launch; 64 + 56 + 168 + 72 + 72 + 48 of the 6 x 80 that the block holds
     if (warp < 4) {
-        if (!kStateOnly) out_warps(p, maps, x, u);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if (!kStateOnly) score_warps(p, x, u);
     } else if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (!kStateOnly) out_warps(p, maps, x, u);
+    } else if (warp < 12) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
         state_warps<kStateOnly>(p, x, u, share);
+    } else if (warp < 20) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        key_warps(p, x, u, (warp - 12) >> 2);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-        if (warp == 8) load_warp<kStateOnly>(p, maps, x, u);
-        else if (warp == 9) mma_warp<kStateOnly>(p, x);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        if (warp == 20) load_warp<kStateOnly>(p, maps, x, u);
+        else if (warp == 21 && !kStateOnly) mma_out_warp(x);
+        else if (warp == 22) mma_state_warp(x);
     }
     tc_fence_before();
     __syncthreads();

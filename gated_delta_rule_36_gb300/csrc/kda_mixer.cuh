@@ -16,23 +16,80 @@ constexpr long long MX_WAIT_LIMIT = 4000000LL;
 constexpr long long MX_WAIT_LIMIT = 2000000000LL;   // SM cycles (~1 s) before a wait gives up
 #endif
 
+// Shared-memory accesses by window address: they stay shared-memory instructions wherever the
+// address comes from.
+__device__ __forceinline__ uint32_t lds_u16(uint32_t a) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ float lds_f32(uint32_t a) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ float4 lds_f32x4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];\n" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ void sts_f32(uint32_t a, float v) { asm volatile("st.shared.f32 [%0], %1;\n" ::"r"(a), "f"(v) : "memory"); }
+__device__ __forceinline__ void sts_u64(uint32_t a, uint32_t x, uint32_t y) {
+    asm volatile("st.shared.v2.b32 [%0], {%1,%2};\n" ::"r"(a), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ void sts_u128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_u32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ void sts_u32(uint32_t a, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(a), "r"(v) : "memory"); }
+
+// try_wait without a time hint suspends the warp in hardware; with one, the compiler builds a
+// polling loop, and a CTA's many waiting warps then take half of the issue slots.
+__device__ __forceinline__ bool mx_try_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // Wait for the phase with `parity`.  Returns false when the limit expires, or when another
-// warp of the CTA has given up (*abort): the caller then leaves its loop.  Every wait of these
+// warp of the CTA has given up (the shared word `abort`): the caller then leaves its loop.  Every wait of these
 // kernels is one of these and no named barrier is used, so a CTA always reaches its end.
-__device__ __forceinline__ bool mx_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort, uint32_t* status) {
-    bool ok = mbar_test_wait(bar, parity);
+__device__ __forceinline__ bool mx_wait(uint32_t bar, uint32_t parity, uint32_t abort, uint32_t* status) {
+    bool ok = mx_try_wait(bar, parity);
     if (!ok) {
         const long long t0 = clock64();
-        while (!(ok = mbar_try_wait(bar, parity))) {
-            if (*abort) break;
+        while (!(ok = mx_try_wait(bar, parity))) {
+            if (lds_u32(abort)) break;
             if (clock64() - t0 > MX_WAIT_LIMIT) {
                 atomicOr(status, KDA_DEVERR_TIMEOUT);
-                *abort = 1u;
+                sts_u32(abort, 1u);
                 break;
             }
         }
     }
     return __all_sync(0xffffffffu, ok);
+}
+// The same for one thread.
+__device__ __forceinline__ bool mx_wait_lane(uint32_t bar, uint32_t parity, uint32_t abort, uint32_t* status) {
+    if (mx_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!mx_try_wait(bar, parity)) {
+        if (lds_u32(abort)) return false;
+        if (clock64() - t0 > MX_WAIT_LIMIT) {
+            atomicOr(status, KDA_DEVERR_TIMEOUT);
+            sts_u32(abort, 1u);
+            return false;
+        }
+    }
+    return true;
 }
 
 // One arrival for a converged warp whose lanes' earlier work the arrival publishes.
@@ -48,6 +105,12 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int 
         " [%0], [%1, {%2, %3, %4, %5}], [%6];\n" ::"r"(dst),
         "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
         : "memory");
+}
+
+// 4 consecutive 32-bit TMEM columns of this thread's lane.
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
 }
 
 __device__ __forceinline__ float mx_u2f(uint32_t x) { return __uint_as_float(x); }
