@@ -43,8 +43,8 @@ constexpr uint32_t OFF_S = 2 * STAGE;
 constexpr uint32_t OFF_POW = OFF_S + TILE, OFF_KPOW = OFF_POW + 4 * 256;
 constexpr uint32_t OFF_BAR = OFF_KPOW + 8 * 128;
 enum { FQ = 0, FK = 2, FV = 4, EQ = 6, EK = 8, EV = 10, KPF = 12, KPE = 14, VR = 16, WF = 18, PF, QSF, OS, OF, OE, KVF, KVE, SB, DRAIN, DRAIN2, NBAR };
-constexpr uint32_t OFF_TMEM = OFF_BAR + NBAR * 8, OFF_ABORT = OFF_TMEM + 4;
-constexpr uint32_t LF_SMEM = OFF_ABORT + 4;   // no room to align the base: it has to be (and is checked to be) 1 KB aligned
+constexpr uint32_t OFF_TMEM = OFF_BAR + NBAR * 8;
+constexpr uint32_t LF_SMEM = OFF_TMEM + 8;   // no room to align the base: it has to be (and is checked to be) 1 KB aligned
 static_assert(LF_SMEM <= 232448, "one CTA's shared memory");
 // Tensor Memory columns: W then P; KV; O; two slots of K' (32 tokens: three terms of 16 columns)
 constexpr uint32_t TM_W = 0, TM_KV = 128, TM_O = 256, TM_KP = 384, KP_SLOT = 48;
@@ -56,16 +56,17 @@ struct LinMaps {
 // A chunk: sequence n, head h, chunk c of nc; the sequence's tokens [bos, bos + len).
 struct Cursor {
     int n, h, c, nc;
-    int64_t bos, len;
+    int bos, len;
 };
 
-__device__ __forceinline__ void seq_of(const LinParams& p, int n, int64_t& bos, int64_t& len) {
+// (all tokens are fewer than 2^31; what cu_seqlens holds beyond that is refused before it is used)
+__device__ __forceinline__ void seq_of(const LinParams& p, int n, int& bos, int& len) {
     if (p.cu_seqlens) {
-        bos = p.cu_seqlens[n];
-        len = p.cu_seqlens[n + 1] - bos;
+        bos = (int)p.cu_seqlens[n];
+        len = (int)p.cu_seqlens[n + 1] - bos;
     } else {
-        bos = n * p.T;
-        len = p.T;
+        len = (int)p.T;
+        bos = n * len;
     }
 }
 
@@ -77,13 +78,13 @@ __device__ __forceinline__ void next_chunk(const LinParams& p, Cursor& u) {
     do {
         if (++u.n >= p.nseq) return;
         seq_of(p, u.n, u.bos, u.len);
-        u.nc = (int)((u.len + LF_C - 1) / LF_C);
+        u.nc = (u.len + LF_C - 1) / LF_C;
     } while (u.nc == 0);
 }
 
 __device__ __forceinline__ int chunk_tokens(const Cursor& u) {
-    const int64_t left = u.len - (int64_t)u.c * LF_C;
-    return left < LF_C ? (int)left : LF_C;
+    const int left = u.len - u.c * LF_C;
+    return left < LF_C ? left : LF_C;
 }
 
 // log2 of the decay; -inf (forget everything) as a finite value, so that its 0th power is 1.
@@ -112,11 +113,12 @@ __device__ Share find_share(const LinParams& p, int64_t* scratch /* 32 */) {
     int64_t mine = 0;
     bool bad = false;
     for (int n = n0; n < n1; ++n) {
-        int64_t bos, len;
+        int bos, len;
         seq_of(p, n, bos, len);
-        bad |= len < 0;
+        if (p.cu_seqlens) bad |= p.cu_seqlens[n + 1] < p.cu_seqlens[n];
         mine += (len + LF_C - 1) / LF_C;
     }
+    // nondecreasing from 0 to at most T_total: every entry is then in range
     if (tid == 0 && p.cu_seqlens) bad |= p.cu_seqlens[0] != 0 || p.cu_seqlens[p.nseq] > p.T_total;
     int64_t sum = mine;
 #pragma unroll
@@ -147,7 +149,7 @@ __device__ Share find_share(const LinParams& p, int64_t* scratch /* 32 */) {
             Cursor u;
             u.n = n;
             seq_of(p, n, u.bos, u.len);
-            u.nc = (int)((u.len + LF_C - 1) / LF_C);
+            u.nc = (u.len + LF_C - 1) / LF_C;
             if (x < base + (int64_t)u.nc * p.H) {
                 u.h = (int)((x - base) / u.nc);
                 u.c = (int)((x - base) % u.nc);
@@ -164,41 +166,34 @@ __device__ Share find_share(const LinParams& p, int64_t* scratch /* 32 */) {
 }
 
 struct Ctx {
-    uint32_t base, tmem, abort;   // shared-window addresses, but tmem
-    uint32_t* status;
-    int64_t count;   // chunks to do
+    uint32_t base, tmem;   // shared-window address; Tensor Memory address
+    int count;             // chunks to do (a GPU's memory holds fewer than 2^31 in all)
     __device__ uint32_t bar(int b) const { return base + OFF_BAR + 8u * b; }
-    __device__ bool wait(int b, int64_t use) const { return mx_wait(bar(b), (uint32_t)(use & 1), abort, status); }
+    __device__ bool wait(int b, int use) const { return mx_wait(bar(b), (uint32_t)use & 1u); }
 };
 
 // ---------------------------------------------------------------- warp 20: loads
 template <bool kStateOnly>
-__device__ void load_warp(const LinParams& p, const LinMaps& maps, const Ctx& x, Cursor u) {
+__device__ bool load_warp(const LinParams& p, const LinMaps& maps, const Ctx& x, Cursor u) {
+    bool ok = true;
     if ((threadIdx.x & 31) == 0) {
-        int64_t i = 0;
-        for (; i < x.count; ++i, next_chunk(p, u)) {
-            const int s = (int)(i & 1);
-            const int t0 = (int)(u.bos + (int64_t)u.c * LF_C);
-            auto one = [&](int full, int empty, const CUtensorMap* m, uint32_t off) {
-                if (i >= 2 && !mx_wait_lane(x.bar(empty + s), (uint32_t)(((i >> 1) - 1) & 1), x.abort, x.status)) return false;
-                const uint32_t dst = x.base + s * STAGE + off;
-                mbar_arrive_expect_tx(x.bar(full + s), TILE);
-                tma_load_4d(dst, m, 0, u.h, t0, 0, x.bar(full + s));
-                tma_load_4d(dst + HALF, m, 64, u.h, t0, 0, x.bar(full + s));
-                return true;
-            };
-            if (!one(FK, EK, &maps.k, TILE)) break;
-            if (!kStateOnly && !one(FQ, EQ, &maps.q, 0)) break;
-            if (!one(FV, EV, &maps.v, 2 * TILE)) break;
-        }
-        // after a wait gave up: the copies in flight land before the CTA leaves (their phases
-        // complete by themselves; a phase not armed is not waited for long)
-        if (lds_u32(x.abort)) {
-            const long long c0 = clock64();
-            while (clock64() - c0 < 2000000LL) __nanosleep(1000);
+        auto one = [&](int i, int full, int empty, const CUtensorMap* m, uint32_t off) {
+            const int s = i & 1;
+            if (i >= 2 && !mx_wait_lane(x.bar(empty + s), (uint32_t)((i >> 1) - 1) & 1u)) return false;
+            const uint32_t dst = x.base + s * STAGE + off;
+            const int t0 = u.bos + u.c * LF_C;
+            mbar_arrive_expect_tx(x.bar(full + s), TILE);
+            tma_load_4d(dst, m, 0, u.h, t0, 0, x.bar(full + s));
+            tma_load_4d(dst + HALF, m, 64, u.h, t0, 0, x.bar(full + s));
+            return true;
+        };
+        for (int i = 0; i < x.count && ok; ++i, next_chunk(p, u)) {
+            ok = one(i, FK, EK, &maps.k, TILE);
+            if (!kStateOnly) ok = ok && one(i, FQ, EQ, &maps.q, 0);
+            ok = ok && one(i, FV, EV, &maps.v, 2 * TILE);
         }
     }
-    __syncwarp();
+    return __all_sync(0xffffffffu, ok);
 }
 
 // ---------------------------------------------------------------- warps 21 and 22: MMAs
@@ -209,23 +204,23 @@ constexpr uint32_t ID_KK = make_idesc_bf16_f32(128, 128);          // both opera
 constexpr uint32_t ID_MN = make_idesc_bf16_f32(128, 128, true);    // B MN-major
 
 // the MMAs in flight finish before the CTA frees Tensor Memory
-__device__ __forceinline__ void drain_mma(const Ctx& x, int bar) {
+__device__ __forceinline__ bool drain_mma(const Ctx& x, int bar) {
     __syncwarp();
     tc_commit_warp(x.bar(bar));
-    if (!mbar_wait_bounded(x.bar(bar), 0, x.status, KDA_DEVERR_TIMEOUT, MX_WAIT_LIMIT)) sts_u32(x.abort, 1u);
-    __syncwarp();
+    return x.wait(bar, 0);
 }
 
-__device__ void mma_out_warp(const Ctx& x) {
+__device__ bool mma_out_warp(const Ctx& x) {
     const uint32_t tm = x.tmem;
+    bool ok = true;
     const uint64_t dQ = make_sdesc_kmajor_sw128(x.base), dS = make_sdesc_mnmajor_sw128(x.base + OFF_S, HALF, 1024);
-    for (int64_t i = 0; i < x.count; ++i) {
-        const int s = (int)(i & 1);
-        const int64_t use = i >> 1;
+    for (int i = 0; i < x.count; ++i) {
+        const int s = i & 1;
+        const int use = i >> 1;
         const uint64_t q = dQ + s * D_STAGE, k = q + (TILE >> 4);
         // W = Q K^T, over the P that the previous chunk's product has read
-        if (i > 0 && !x.wait(OF, i - 1)) break;
-        if (!x.wait(FK + s, use) || !x.wait(FQ + s, use)) break;
+        ok = (i == 0 || x.wait(OF, i - 1)) && x.wait(FK + s, use) && x.wait(FQ + s, use);
+        if (!ok) break;
         tc_fence_after();
 #pragma unroll 1
         for (int half = 0; half < 2; ++half)
@@ -235,7 +230,8 @@ __device__ void mma_out_warp(const Ctx& x) {
         tc_commit_warp(x.bar(WF));
         tc_commit_warp(x.bar(EK + s));
         // O = Q S, once the state is in shared memory and the previous O has been read
-        if (!x.wait(SB, i) || (i > 0 && !x.wait(OE, i - 1))) break;
+        ok = x.wait(SB, i) && (i == 0 || x.wait(OE, i - 1));
+        if (!ok) break;
         tc_fence_after();
 #pragma unroll 1
         for (int half = 0; half < 2; ++half)
@@ -244,7 +240,8 @@ __device__ void mma_out_warp(const Ctx& x) {
                 tc_mma_ss_warp(tm + TM_O, q + half * K_HALF + kk * K_STEP, dS + (4 * half + kk) * MN_STEP, ID_MN, half + kk > 0);
         tc_commit_warp(x.bar(QSF));
         // O += P V
-        if (!x.wait(VR + s, use) || !x.wait(PF, i) || !x.wait(OS, i)) break;
+        ok = x.wait(VR + s, use) && x.wait(PF, i) && x.wait(OS, i);
+        if (!ok) break;
         tc_fence_after();
         const uint64_t v = make_sdesc_mnmajor_sw128(x.base + s * STAGE + 2 * TILE, HALF, 1024);
 #pragma unroll 1
@@ -255,17 +252,19 @@ __device__ void mma_out_warp(const Ctx& x) {
         tc_commit_warp(x.bar(OF));
         tc_commit_warp(x.bar(EV + s));
     }
-    drain_mma(x, DRAIN);
+    return drain_mma(x, DRAIN) && ok;
 }
 
 // KV = K'^T V, 32 tokens at a time as the key warps hand them over
-__device__ void mma_state_warp(const Ctx& x) {
+__device__ bool mma_state_warp(const Ctx& x) {
     const uint32_t tm = x.tmem;
-    for (int64_t i = 0; i < x.count; ++i) {
-        const int s = (int)(i & 1);
+    bool ok = true;
+    for (int i = 0; i < x.count; ++i) {
+        const int s = i & 1;
         const uint64_t v = make_sdesc_mnmajor_sw128(x.base + s * STAGE + 2 * TILE, HALF, 1024);
-        if (!x.wait(VR + s, i >> 1) || (i > 0 && !x.wait(KVE, i - 1))) break;
-        bool ok = true;
+        ok = x.wait(VR + s, i >> 1) && (i == 0 || x.wait(KVE, i - 1));
+        if (!ok) break;
+
 #pragma unroll 1
         for (int b = 0; b < 4; ++b) {
             const int slot = b & 1;
@@ -286,18 +285,18 @@ __device__ void mma_state_warp(const Ctx& x) {
         tc_commit_warp(x.bar(KVF));
         tc_commit_warp(x.bar(EV + s));
     }
-    drain_mma(x, DRAIN2);
+    return drain_mma(x, DRAIN2) && ok;
 }
 
 // ---------------------------------------------------------------- warps 0-3: P and the scale of O
-__device__ void score_warps(const LinParams& p, const Ctx& x, Cursor u) {
+__device__ bool score_warps(const LinParams& p, const Ctx& x, Cursor u) {
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(32 * warp) << 16;
     const uint32_t pow = x.base + OFF_POW + warp * 256;
     sts_f32(pow + 128 + 4 * lane, 0.f);
     float since = 0.f, left = 0.f, hop = 0.f;
     int h = -1;
-    for (int64_t i = 0; i < x.count; ++i, next_chunk(p, u)) {
+    for (int i = 0; i < x.count; ++i, next_chunk(p, u)) {
         if (u.h != h) {
             h = u.h;
             const float l2 = log2_decay(p, h);
@@ -312,7 +311,7 @@ __device__ void score_warps(const LinParams& p, const Ctx& x, Cursor u) {
         // P, in blocks of 32 columns (its 16 registers a block go over columns of W that have been
         // read): left of the diagonal block a^(i-j) is a power for the row times one for the column, all
         // exponents >= 0; in the diagonal block it is looked up; right of it P is zero
-        if (!x.wait(WF, i)) break;
+        if (!x.wait(WF, i)) return false;
         tc_fence_after();
         uint32_t w[32], y[16];
 #pragma unroll 1
@@ -349,7 +348,7 @@ __device__ void score_warps(const LinParams& p, const Ctx& x, Cursor u) {
         tc_fence_before();
         mx_arrive_warp(x.bar(PF));
         // O = Q S, each row scaled by scale a^(i+1)
-        if (!x.wait(QSF, i)) break;
+        if (!x.wait(QSF, i)) return false;
         tc_fence_after();
         const float2 s2 = make_float2(since, since);
 #pragma unroll 1
@@ -369,16 +368,17 @@ __device__ void score_warps(const LinParams& p, const Ctx& x, Cursor u) {
         tc_fence_before();
         mx_arrive_warp(x.bar(OS));
     }
+    return true;
 }
 
 // ---------------------------------------------------------------- warps 4-7: the output
-__device__ void out_warps(const LinParams& p, const LinMaps& maps, const Ctx& x, Cursor u) {
+__device__ bool out_warps(const LinParams& p, const LinMaps& maps, const Ctx& x, Cursor u) {
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(32 * warp) << 16;
-    for (int64_t i = 0; i < x.count; ++i, next_chunk(p, u)) {
-        const int s = (int)(i & 1);
+    for (int i = 0; i < x.count; ++i, next_chunk(p, u)) {
+        const int s = i & 1;
         const int valid = chunk_tokens(u);
-        if (!x.wait(OF, i)) break;
+        if (!x.wait(OF, i)) return false;
         tc_fence_after();
         // through this chunk's q buffer (both products have read it); a short chunk's rows go
         // straight to memory
@@ -425,6 +425,7 @@ __device__ void out_warps(const LinParams& p, const LinMaps& maps, const Ctx& x,
     }
     if (lane == 0) bulk_wait_all();
     __syncwarp();
+    return true;
 }
 
 // ---------------------------------------------------------------- warps 8-11: the state
@@ -435,13 +436,13 @@ __device__ __forceinline__ float state_at(const void* s, int f32, size_t off) {
 }
 
 template <bool kStateOnly>
-__device__ void state_warps(const LinParams& p, const Ctx& x, Cursor u, const Share& share) {
+__device__ bool state_warps(const LinParams& p, const Ctx& x, Cursor u, const Share& share) {
     const int warp = (threadIdx.x >> 5) & 3, k = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(32 * warp) << 16;
     float2 S[LF_C / 2];
     float l2 = 0.f, all = 0.f;
     bool fresh = true;   // a unit (or this share) starts
-    for (int64_t i = 0; i < x.count; ++i, next_chunk(p, u)) {
+    for (int i = 0; i < x.count; ++i, next_chunk(p, u)) {
         const int valid = chunk_tokens(u);
         const size_t unit = (size_t)u.n * p.H + u.h;
         if (fresh) {
@@ -461,7 +462,7 @@ __device__ void state_warps(const LinParams& p, const Ctx& x, Cursor u, const Sh
             }
             if (!kStateOnly && u.c > 0) {
                 // the shares before this one that hold earlier chunks of the unit
-                const int64_t first = share.x0 - u.c;
+                const int64_t first = share.x0 - u.c;   // the unit's first chunk
                 for (int b = (int)blockIdx.x - 1; b >= 0; --b) {
                     const int64_t end = share_start(share.total, b + 1, gridDim.x);
                     if (end <= first) break;
@@ -478,7 +479,7 @@ __device__ void state_warps(const LinParams& p, const Ctx& x, Cursor u, const Sh
         }
         if (!kStateOnly) {
             // the bf16 copy of the state, once the previous product with it is done
-            if (i > 0 && !x.wait(QSF, i - 1)) break;
+            if (i > 0 && !x.wait(QSF, i - 1)) return false;
             const uint32_t tile = x.base + OFF_S + k * 128;
 #pragma unroll
             for (int c = 0; c < 16; ++c)
@@ -489,7 +490,7 @@ __device__ void state_warps(const LinParams& p, const Ctx& x, Cursor u, const Sh
             mx_arrive_warp(x.bar(SB));
         }
         // S <- a^C S + KV
-        if (!x.wait(KVF, i)) break;
+        if (!x.wait(KVF, i)) return false;
         tc_fence_after();
         const float ac = valid == LF_C ? all : exp2f(l2 * (float)valid);
         const float2 ac2 = make_float2(ac, ac);
@@ -535,6 +536,7 @@ __device__ void state_warps(const LinParams& p, const Ctx& x, Cursor u, const Sh
             }
         }
     }
+    return true;
 }
 
 // ---------------------------------------------------------------- warps 12-19: K'
@@ -543,7 +545,7 @@ __device__ void state_warps(const LinParams& p, const Ctx& x, Cursor u, const Sh
 // g and g + 2 of each chunk and owns slot g.
 __device__ __forceinline__ float2 unpack2(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
 
-__device__ void key_warps(const LinParams& p, const Ctx& x, Cursor u, int g) {
+__device__ bool key_warps(const LinParams& p, const Ctx& x, Cursor u, int g) {
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, k = threadIdx.x & 127;
     const uint32_t kp = x.tmem + ((uint32_t)(32 * warp) << 16) + TM_KP + g * KP_SLOT;
     const uint32_t pow = x.base + OFF_KPOW + (4 * g + warp) * 128;
@@ -551,8 +553,8 @@ __device__ void key_warps(const LinParams& p, const Ctx& x, Cursor u, int g) {
     const float2 minus = make_float2(-1.f, -1.f);
     float l2 = 0.f, hop = 0.f;
     int h = -1;
-    for (int64_t i = 0; i < x.count; ++i, next_chunk(p, u)) {
-        const int s = (int)(i & 1);
+    for (int i = 0; i < x.count; ++i, next_chunk(p, u)) {
+        const int s = i & 1;
         const int valid = chunk_tokens(u);
         const bool full = valid == LF_C;
         if (u.h != h || !full) {
@@ -564,12 +566,12 @@ __device__ void key_warps(const LinParams& p, const Ctx& x, Cursor u, int g) {
             hop = exp2f(l2 * 32.f);
             if (!full) h = -1;
         }
-        if (!x.wait(FK + s, i >> 1)) break;
+        if (!x.wait(FK + s, i >> 1)) return false;
         if (g == 0) {
             // v is ready once it has landed and, in a short chunk, the values past its end are
             // zeros: they count for nothing, whatever they hold.  (Every chunk waits here, so that
             // this barrier never gets ahead of the value tile's use.)
-            if (!x.wait(FV + s, i >> 1)) break;
+            if (!x.wait(FV + s, i >> 1)) return false;
             if (!full) {
                 const uint32_t v = x.base + s * STAGE + 2 * TILE;
                 for (int r = valid + warp; r < LF_C; r += 4) sts_u64(v + (lane >> 4) * HALF + r * 128 + (lane & 15) * 8, 0u, 0u);
@@ -580,7 +582,7 @@ __device__ void key_warps(const LinParams& p, const Ctx& x, Cursor u, int g) {
         bool ok = true;
 #pragma unroll 1
         for (int b = g; b < 4; b += 2) {
-            const int64_t use = 2 * i + (b >> 1);
+            const int use = 2 * i + (b >> 1);
             uint32_t kt = x.base + s * STAGE + TILE + (k >> 6) * HALF + (k & 7) * 2 + 32 * b * 128;
             float f = b == 3 ? 1.f : b == 2 ? hop : b == 1 ? hop * hop : hop * hop * hop;   // a^(96 - 32 b)
             if (!full) {
@@ -592,7 +594,7 @@ __device__ void key_warps(const LinParams& p, const Ctx& x, Cursor u, int g) {
             }
             const float2 f2 = make_float2(f, f);
             if (use > 0) ok = x.wait(KPE + g, use - 1);
-            if (!ok) break;
+            if (!ok) return false;
             tc_fence_after();
 #pragma unroll 1
             for (int q = 0; q < 2; ++q, kt += 16 * 128) {
@@ -629,9 +631,10 @@ __device__ void key_warps(const LinParams& p, const Ctx& x, Cursor u, int g) {
             tc_fence_before();
             mx_arrive_warp(x.bar(KPF + g));
         }
-        if (!ok) break;
+        if (!ok) return false;
         mx_arrive_warp(x.bar(EK + s));
     }
+    return true;
 }
 
 // Units of no tokens: the final state is the initial one.
@@ -641,7 +644,7 @@ __device__ void empty_units(const LinParams& p) {
     for (int64_t u0 = (int64_t)blockIdx.x * LF_THREADS; u0 < units; u0 += (int64_t)gridDim.x * LF_THREADS) {
         for (int j = 0; j < LF_THREADS && u0 + j < units; ++j) {
             const int64_t unit = u0 + j;
-            int64_t bos, len;
+            int bos, len;
             seq_of(p, (int)(unit / p.H), bos, len);
             if (len != 0) {   // on to the next sequence's first unit
                 j += (int)min((int64_t)LF_THREADS, p.H - 1 - unit % p.H);
@@ -663,8 +666,6 @@ __global__ void __launch_bounds__(LF_THREADS, 1) lin_fwd_kernel(const LinParams 
     const int tid = threadIdx.x, warp = tid >> 5;
     Ctx x;
     x.base = smem_u32(smem_raw);
-    x.abort = x.base + OFF_ABORT;
-    x.status = p.status;
     Share share = find_share<kStateOnly>(p, reinterpret_cast<int64_t*>(smem_raw + OFF_S));
     if (!kStateOnly && blockIdx.x == 0 && tid == 0) *p.status = share.bad ? KDA_DEVERR_CU_SEQLENS : 0u;
     if (share.bad) return;
@@ -677,11 +678,11 @@ __global__ void __launch_bounds__(LF_THREADS, 1) lin_fwd_kernel(const LinParams 
         // the share's last chunks, if its end lies inside a unit; u is the chunk after them
         if (share.x1 == share.x0 || share.x1 >= share.total || u.c == 0) return;
         const int64_t own = share.x1 - share.x0;
-        x.count = own < u.c ? own : u.c;
-        u.c -= (int)x.count;
+        x.count = (int)own < u.c ? own : u.c;
+        u.c -= x.count;
     } else {
         empty_units(p);
-        x.count = share.x1 - share.x0;
+        x.count = (int)(share.x1 - share.x0);
         if (x.count == 0) return;
     }
     if (tid == 0) {
@@ -692,7 +693,6 @@ __global__ void __launch_bounds__(LF_THREADS, 1) lin_fwd_kernel(const LinParams 
             mbar_init(x.bar(b), warps ? 4 : both ? (kStateOnly ? 8 : 9) : twice ? (kStateOnly ? 1 : 2) : 1);
         }
         mbar_fence_init();
-        sts_u32(x.abort, 0u);
         tma_prefetch_desc(&maps.q);
         tma_prefetch_desc(&maps.k);
         tma_prefetch_desc(&maps.v);
@@ -707,24 +707,26 @@ __global__ void __launch_bounds__(LF_THREADS, 1) lin_fwd_kernel(const LinParams 
     tc_fence_after();
     x.tmem = lds_u32(x.base + OFF_TMEM);
     // registers a thread: 80 at launch; 64 + 56 + 168 + 72 + 72 + 48 of the 6 x 80 that the block holds
+    bool ok = true;
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        if (!kStateOnly) score_warps(p, x, u);
+        if (!kStateOnly) ok = score_warps(p, x, u);
     } else if (warp < 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        if (!kStateOnly) out_warps(p, maps, x, u);
+        if (!kStateOnly) ok = out_warps(p, maps, x, u);
     } else if (warp < 12) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
-        state_warps<kStateOnly>(p, x, u, share);
+        ok = state_warps<kStateOnly>(p, x, u, share);
     } else if (warp < 20) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        key_warps(p, x, u, (warp - 12) >> 2);
+        ok = key_warps(p, x, u, (warp - 12) >> 2);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-        if (warp == 20) load_warp<kStateOnly>(p, maps, x, u);
-        else if (warp == 21 && !kStateOnly) mma_out_warp(x);
-        else if (warp == 22) mma_state_warp(x);
+        if (warp == 20) ok = load_warp<kStateOnly>(p, maps, x, u);
+        else if (warp == 21 && !kStateOnly) ok = mma_out_warp(x);
+        else if (warp == 22) ok = mma_state_warp(x);
     }
+    if (!ok) mx_report(p.status);
     tc_fence_before();
     __syncthreads();
     if (warp == 0) {

@@ -10,10 +10,12 @@
 
 namespace kda {
 
+// Polls before a wait gives up.  A poll lasts about 100 SM cycles on GB300, so this is about a
+// second; the test build of the timeout path gives up after a few milliseconds.
 #ifdef KDA_WAIT_TEST
-constexpr long long MX_WAIT_LIMIT = 4000000LL;
+constexpr uint32_t MX_POLLS = 1u << 16;
 #else
-constexpr long long MX_WAIT_LIMIT = 2000000000LL;   // SM cycles (~1 s) before a wait gives up
+constexpr uint32_t MX_POLLS = 1u << 24;
 #endif
 
 // Shared-memory accesses by window address: they stay shared-memory instructions wherever the
@@ -59,37 +61,29 @@ __device__ __forceinline__ bool mx_try_wait(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
-// Wait for the phase with `parity`.  Returns false when the limit expires, or when another
-// warp of the CTA has given up (the shared word `abort`): the caller then leaves its loop.  Every wait of these
-// kernels is one of these and no named barrier is used, so a CTA always reaches its end.
-__device__ __forceinline__ bool mx_wait(uint32_t bar, uint32_t parity, uint32_t abort, uint32_t* status) {
-    bool ok = mx_try_wait(bar, parity);
-    if (!ok) {
-        const long long t0 = clock64();
-        while (!(ok = mx_try_wait(bar, parity))) {
-            if (lds_u32(abort)) break;
-            if (clock64() - t0 > MX_WAIT_LIMIT) {
-                atomicOr(status, KDA_DEVERR_TIMEOUT);
-                sts_u32(abort, 1u);
-                break;
-            }
-        }
-    }
+// Wait for the phase with `parity`; false when the limit expires.  The caller then leaves its
+// loop and reports it (mx_report), the roles that wait for it run into their own limits, and
+// since no named barrier is used every warp reaches the CTA's end.  The body is as small as it
+// can be: a CTA's roles run different code on the same schedulers, and what they share of the
+// instruction cache limits their pace (a version with a clock and an abort flag in the loop
+// cost 10 % of the linear attention forward).
+__device__ __forceinline__ bool mx_wait(uint32_t bar, uint32_t parity) {
+    uint32_t polls = 0;
+    bool ok;
+    while (!(ok = mx_try_wait(bar, parity)) && ++polls < MX_POLLS) {}
     return __all_sync(0xffffffffu, ok);
 }
 // The same for one thread.
-__device__ __forceinline__ bool mx_wait_lane(uint32_t bar, uint32_t parity, uint32_t abort, uint32_t* status) {
-    if (mx_try_wait(bar, parity)) return true;
-    const long long t0 = clock64();
-    while (!mx_try_wait(bar, parity)) {
-        if (lds_u32(abort)) return false;
-        if (clock64() - t0 > MX_WAIT_LIMIT) {
-            atomicOr(status, KDA_DEVERR_TIMEOUT);
-            sts_u32(abort, 1u);
-            return false;
-        }
-    }
-    return true;
+__device__ __forceinline__ bool mx_wait_lane(uint32_t bar, uint32_t parity) {
+    uint32_t polls = 0;
+    bool ok;
+    while (!(ok = mx_try_wait(bar, parity)) && ++polls < MX_POLLS) {}
+    return ok;
+}
+// A warp that gave up: the status bit, and time for its CTA's copies in flight to land.
+__device__ __forceinline__ void mx_report(uint32_t* status) {
+    atomicOr(status, KDA_DEVERR_TIMEOUT);
+    for (int i = 0; i < 2000; ++i) __nanosleep(1000);
 }
 
 // One arrival for a converged warp whose lanes' earlier work the arrival publishes.
