@@ -1,95 +1,645 @@
-// Causal softmax attention with grouped heads over packed prompts and caches.
+// Causal softmax attention with grouped heads over packed prompts and caches, on the
+// 5th-generation tensor cores: one pass over the keys with the running maximum and sum.
 //
-// One warp per (query, head): lane l holds channels 4 l .. 4 l + 3 of q and of the output, the
-// keys are visited once with the running maximum and sum of the softmax.  Bound by instruction issue.
-#include "kda_device.cuh"
-#include "kda_ops.h"
+// A query tile is 128 rows of (token, head) pairs that share a key/value head: floor(128 / G)
+// tokens with all G heads of the group.  A CTA works on two neighbouring tiles at a time and on
+// blocks of 128 keys:
+//   S_t = Q_t K^T   (128 x 128 x 128 each)     P_t = exp2(c S_t - c m) in bf16, over S_t in Tensor Memory
+//   O_t += P_t V                               l_t += row sums of P_t in fp32
+// The maximum m that the exponents refer to moves only when a row's maximum has grown by more
+// than 2^8 (then O and l are rescaled): P stays below 2^8 and the sums in fp32's range, and most
+// blocks skip the rescaling.
+//
+// All (sequence, key head, tile pair, key block) steps are one line that is cut into equal
+// shares, one for each SM: long prompts, ragged batches and single tokens over a long cache
+// all come out even.  A pair that lies in more than one share leaves unnormalised partial rows in
+// the workspace, and a second, small kernel joins them in the order of the keys.
+//
+// Warp roles: warps 0-3 and 4-7 are the softmax of the two tiles (thread = row) and write the
+// results; warp 8 loads q, k and v by TMA (a ring of five 32 KB tiles), warp 9 issues the MMAs,
+// alternating between the tiles so that one is multiplied while the other is exponentiated.
+//
+// Bound by the tensor cores for prompts (4 x 128 x 128 x 128 flop, 1,024 SM cycles, a tile and
+// key block), by HBM for single tokens.
+#include "kda_mixer.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int AT_THREADS = 128;
+constexpr int AT_THREADS = 384;
+constexpr int AT_MAX_CTAS = 160;
+constexpr int KB = 128;                       // keys a block
+constexpr uint32_t TILE = 128 * 256, HALF = TILE / 2;
+constexpr int RING = 5;
+constexpr uint32_t OFF_RING = 2 * TILE;       // behind the two query tiles
+constexpr uint32_t OFF_BAR = OFF_RING + RING * TILE;
+enum { FULL = 0, EMPTY = RING, QF = 2 * RING, QE, SF, PF = SF + 2, OF = PF + 2, DRAIN = OF + 2, NBAR };
+constexpr uint32_t OFF_TMEM = OFF_BAR + NBAR * 8;
+constexpr uint32_t AT_SMEM = OFF_TMEM + 8;
+static_assert(AT_SMEM <= 232448, "one CTA's shared memory");
+constexpr uint32_t TM_S = 0, TM_O = 256;      // two tiles of 128 columns each; P over the first 64 of S
 
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-    const uint2 w = *reinterpret_cast<const uint2*>(p);
-    return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+struct AttnMaps {
+    CUtensorMap q, k, v;
+};
+
+// Partial results: two for each share, of 256 rows each.
+struct Partials {
+    float* o;     // [2 * shares][256][128], not normalised
+    float2* ml;   // [2 * shares][256]: reference exponent (base 2) and sum
+};
+__host__ __device__ inline Partials partials(void* ws) {
+    Partials p;
+    p.ml = static_cast<float2*>(ws);
+    p.o = reinterpret_cast<float*>(static_cast<char*>(ws) + (size_t)2 * AT_MAX_CTAS * 256 * sizeof(float2));
+    return p;
 }
 
-__global__ void __launch_bounds__(AT_THREADS) attn_kernel(const AttnParams p) {
-    bool bad = false;
-    for (int i = threadIdx.x; i < p.nseq; i += AT_THREADS) {
-        if (p.cu_q) bad |= p.cu_q[i + 1] < p.cu_q[i];
-        if (p.cu_k) bad |= p.cu_k[i + 1] < p.cu_k[i];
-        if (p.seqlens_k) bad |= p.seqlens_k[i] < 0 || p.seqlens_k[i] > p.Tk;
+// How a sequence's steps are laid out: tiles of tq tokens in pairs; pair j sees blocks(j) key blocks.
+struct Seq {
+    int q0, lq, k0, lk;   // first query row and queries, first key row and keys
+};
+
+__device__ __forceinline__ Seq seq_of(const AttnParams& p, int n) {
+    Seq s;
+    if (p.cu_q) {
+        s.q0 = (int)p.cu_q[n];
+        s.lq = (int)p.cu_q[n + 1] - s.q0;
+    } else {
+        s.lq = (int)p.uniform_q;
+        s.q0 = n * s.lq;
     }
-    if (threadIdx.x == 0) {
+    if (p.cache) {
+        s.k0 = 0;
+        s.lk = (int)p.seqlens_k[n];
+    } else if (p.cu_k) {
+        s.k0 = (int)p.cu_k[n];
+        s.lk = (int)p.cu_k[n + 1] - s.k0;
+    } else {
+        s.k0 = 0;
+        s.lk = (int)p.Tk;
+    }
+    return s;
+}
+
+// Key blocks that the first `tokens` queries of a sequence see together (at least one: a query
+// that sees no key still has an answer to write).
+__device__ __forceinline__ int blocks_seen(const Seq& s, int tokens) {
+    const int seen = s.lk - (s.lq - min(tokens, s.lq));
+    return seen <= KB ? 1 : (seen - 1) / KB + 1;
+}
+
+__device__ __forceinline__ int pairs_of(const Seq& s, int tp) { return (s.lq + tp - 1) / tp; }
+
+// Steps of the sequence's first m pairs, m below pairs_of: the sum of blocks_seen((j + 1) tp), in
+// closed form from the sum of residues modulo 128, which repeat after 128 / gcd(tp, 128) pairs.
+__device__ int64_t steps_before(const Seq& s, int m, int tp) {
+    const int d = s.lk - s.lq;
+    int ones = d > KB ? 0 : (KB - d) / tp;   // pairs that see one block
+    ones = min(ones, m);
+    const int64_t n = m - ones;
+    if (n == 0) return ones;
+    const int64_t b = (int64_t)(ones + 1) * tp + d + KB - 1;   // floor((b + i tp) / 128), i < n
+    const int g = min(tp & -tp, KB), per = KB / g;
+    const int64_t full = n / per;
+    const int rest = (int)(n % per);
+    int64_t residues = full * ((int64_t)per * (b % g) + (int64_t)g * per * (per - 1) / 2);
+    for (int i = 0; i < rest; ++i) residues += (b + (int64_t)i * tp) & (KB - 1);
+    return ones + ((b * n + (int64_t)tp * (n * (n - 1) / 2) - residues) >> 7);
+}
+__device__ __forceinline__ int64_t steps_of(const Seq& s, int tp) {
+    const int m = pairs_of(s, tp);
+    return m == 0 ? 0 : steps_before(s, m - 1, tp) + blocks_seen(s, s.lq);
+}
+
+__device__ __forceinline__ int64_t share_start(int64_t total, int b, int ctas) {
+    return total / ctas * b + total % ctas * b / ctas;
+}
+
+// A step: pair `pair` of key head kh of sequence n, key block j of nb.
+struct Cursor {
+    int n, kh, pair, j;
+    Seq s;
+};
+
+// The whole block (of kThreads threads): checks the lengths, counts the steps and finds the step
+// x(total) among them, in the order (sequence, key head, pair, key block).
+template <int kThreads, class X>
+__device__ Cursor find_step(const AttnParams& p, int tp, int64_t* scratch /* 32 */, int64_t& total, bool& bad, X x_of) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (p.nseq + kThreads - 1) / kThreads;
+    const int n0 = min(tid * per, p.nseq), n1 = min(n0 + per, p.nseq);
+    // lengths first: nothing is computed from a bad one
+    bad = false;
+    for (int n = n0; n < n1; ++n) {
+        if (p.cu_q) bad |= p.cu_q[n + 1] < p.cu_q[n];
+        if (p.cu_k) bad |= p.cu_k[n + 1] < p.cu_k[n];
+        if (p.seqlens_k) bad |= p.seqlens_k[n] < 0 || p.seqlens_k[n] > p.Tk;
+    }
+    if (tid == 0) {
         if (p.cu_q) bad |= p.cu_q[0] != 0 || p.cu_q[p.nseq] > p.Tq;
         if (p.cu_k) bad |= p.cu_k[0] != 0 || p.cu_k[p.nseq] > p.Tk;
     }
     bad = __syncthreads_or(bad);
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = bad ? KDA_DEVERR_CU_SEQLENS : 0u;
-    if (bad) return;
-    const int64_t row = (int64_t)blockIdx.x * (AT_THREADS / 32) + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31, c0 = 4 * lane;
-    if (row >= p.Tq * p.Hq) return;
-    const int64_t t = row / p.Hq;
-    const int h = (int)(row % p.Hq), hk = h / (p.Hq / p.Hk);
-    int n = 0;
-    int64_t bos, eos;
-    if (p.cu_q) {
-        if (t >= p.cu_q[p.nseq]) return;
-        int lo = 0, hi = p.nseq;   // the last n with cu_q[n] <= t
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (p.cu_q[mid] <= t) lo = mid; else hi = mid;
-        }
-        n = lo;
-        bos = p.cu_q[n];
-        eos = p.cu_q[n + 1];
-    } else {
-        n = (int)(t / p.uniform_q);
-        bos = n * p.uniform_q;
-        eos = bos + p.uniform_q;
-    }
-    int64_t kbase = 0, lk = p.Tk;
-    if (p.cache) lk = p.seqlens_k[n];
-    else if (p.cu_k) kbase = p.cu_k[n], lk = p.cu_k[n + 1] - kbase;
-    const __nv_bfloat16* kp = p.k + (p.cache ? n * p.k_seq : 0) + kbase * p.k_row + hk * p.k_head + c0;
-    const __nv_bfloat16* vp = p.v + (p.cache ? n * p.v_seq : 0) + kbase * p.v_row + hk * p.v_head + c0;
-    int64_t seen = (t - bos) + 1 + lk - (eos - bos);
-    const float4 q = load4(p.q.data + t * p.q.row + h * p.q.head + c0);
-    const float sc = p.scale * LOG2E;
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int64_t j = 0; j < seen; ++j) {
-        const float4 k = load4(kp + j * p.k_row), v = load4(vp + j * p.v_row);
-        float s = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, q.w * k.w)));
+    total = 0;
+    Cursor u{};
+    if (bad) return u;
+    int64_t mine = 0;
+    for (int n = n0; n < n1; ++n) mine += steps_of(seq_of(p, n), tp) * p.Hk;
+    int64_t sum = mine;
 #pragma unroll
-        for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= sc;
-        const float m2 = fmaxf(m, s), f = exp2f(m - m2), e = exp2f(s - m2);
-        l = fmaf(l, f, e);
-        o.x = fmaf(o.x, f, e * v.x);
-        o.y = fmaf(o.y, f, e * v.y);
-        o.z = fmaf(o.z, f, e * v.z);
-        o.w = fmaf(o.w, f, e * v.w);
-        m = m2;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += y;
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    *reinterpret_cast<uint2*>(p.out.data + t * p.out.row + h * p.out.head + c0) =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (p.lse && lane == 0) p.lse[t * p.Hq + h] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    if (lane == 31) scratch[warp] = sum;
+    __syncthreads();
+    int64_t before = sum - mine;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        before += w < warp ? scratch[w] : 0;
+        total += scratch[w];
+    }
+    const int64_t x = x_of(total);
+    int64_t* found = scratch + 16;   // the sequence and the step within it
+    __syncthreads();
+    if (x >= before && x < before + mine) {
+        for (int n = n0; n < n1; ++n) {
+            const int64_t st = steps_of(seq_of(p, n), tp) * p.Hk;
+            if (x < before + st) {
+                found[0] = n;
+                found[1] = x - before;
+                break;
+            }
+            before += st;
+        }
+    }
+    if (tid == 0) found[2] = 0;
+    __syncthreads();
+    if (x >= total) return u;
+    u.n = (int)found[0];
+    u.s = seq_of(p, u.n);
+    const int64_t each = steps_of(u.s, tp);
+    u.kh = (int)(found[1] / each);
+    const int64_t at = found[1] % each;
+    // the last pair that starts at or before `at`: every thread tries some of them
+    const int m = pairs_of(u.s, tp);
+    int best = 0;
+    for (int lo = 0, width = m; width > 1;) {   // narrow [lo, lo + width)
+        const int step = (width + kThreads - 1) / kThreads;
+        const int c = lo + tid * step;
+        if (c < lo + width && steps_before(u.s, c, tp) <= at) atomicMax(reinterpret_cast<int*>(found + 2), c);
+        __syncthreads();
+        best = *reinterpret_cast<volatile int*>(found + 2);
+        __syncthreads();
+        width = min(step, lo + width - best);
+        lo = best;
+    }
+    u.pair = best;
+    u.j = (int)(at - steps_before(u.s, best, tp));
+    return u;
+}
+
+// A share's next piece: the blocks [j0, j1) of one pair.
+struct Piece {
+    int j0, j1, nb;     // of nb
+    int e0;             // the first tile's blocks end here (at most j1)
+    bool two;           // the second tile has tokens
+    bool whole;         // the share holds the whole pair
+};
+
+struct Ctx {
+    uint32_t base, tmem;
+    int64_t steps;      // of this share
+    int tq, tp, G;      // tokens of a tile and of a pair, heads of a group
+    __device__ uint32_t bar(int b) const { return base + OFF_BAR + 8u * b; }
+    __device__ bool wait(int b, uint32_t use) const { return mx_wait(bar(b), use & 1u); }
+};
+
+__device__ __forceinline__ Piece piece_at(const Ctx& x, const Cursor& u, int64_t left) {
+    Piece r;
+    r.nb = blocks_seen(u.s, (u.pair + 1) * x.tp);
+    r.j0 = u.j;
+    r.j1 = left < r.nb - u.j ? u.j + (int)left : r.nb;
+    r.two = u.pair * x.tp + x.tq < u.s.lq;
+    r.e0 = r.two ? min(r.j1, blocks_seen(u.s, u.pair * x.tp + x.tq)) : r.j1;
+    r.e0 = max(r.e0, r.j0);
+    r.whole = r.j0 == 0 && r.j1 == r.nb;
+    return r;
+}
+
+__device__ __forceinline__ void next_pair(const AttnParams& p, const Ctx& x, Cursor& u) {
+    u.j = 0;
+    if (++u.pair < pairs_of(u.s, x.tp)) return;
+    u.pair = 0;
+    if (++u.kh < p.Hk) return;
+    u.kh = 0;
+    do {
+        if (++u.n >= p.nseq) return;
+        u.s = seq_of(p, u.n);
+    } while (u.s.lq == 0);
+}
+
+// ---------------------------------------------------------------- warp 8: loads
+__device__ bool load_warp(const AttnParams& p, const AttnMaps& maps, const Ctx& x, Cursor u) {
+    bool ok = true;
+    if ((threadIdx.x & 31) == 0) {
+        int slot = 0;
+        uint32_t lap = 0, pieces = 0;
+        auto tile = [&](const CUtensorMap* m, int kh, int row, int n) {
+            if (lap > 0 && !mx_wait_lane(x.bar(EMPTY + slot), (lap - 1) & 1u)) return false;
+            const uint32_t dst = x.base + OFF_RING + slot * TILE, full = x.bar(FULL + slot);
+            if (p.Tk == 0) {   // no row to read: every key is masked and the values are set to zero
+                mbar_arrive(full);
+            } else {
+                mbar_arrive_expect_tx(full, TILE);
+                tma_load_4d(dst, m, 0, kh, row, n, full);
+                tma_load_4d(dst + HALF, m, 64, kh, row, n, full);
+            }
+            if (++slot == RING) slot = 0, ++lap;
+            return true;
+        };
+        for (int64_t left = x.steps; left > 0 && ok; next_pair(p, x, u), ++pieces) {
+            const Piece r = piece_at(x, u, left);
+            left -= r.j1 - r.j0;
+            if (pieces > 0) ok = mx_wait_lane(x.bar(QE), (pieces - 1) & 1u);
+            if (!ok) break;
+            const int t0 = u.s.q0 + u.pair * x.tp;
+            const uint32_t bytes = (uint32_t)(x.tq * x.G) * 256u;
+            mbar_arrive_expect_tx(x.bar(QF), r.two ? 2 * bytes : bytes);
+            for (int t = 0; t < (r.two ? 2 : 1); ++t) {
+                tma_load_4d(x.base + t * TILE, &maps.q, 0, u.kh * x.G, t0 + t * x.tq, 0, x.bar(QF));
+                tma_load_4d(x.base + t * TILE + HALF, &maps.q, 64, u.kh * x.G, t0 + t * x.tq, 0, x.bar(QF));
+            }
+            const int n = p.cache ? u.n : 0;
+            for (int j = r.j0; j < r.j1 && ok; ++j)
+                ok = tile(&maps.k, u.kh, u.s.k0 + j * KB, n) && tile(&maps.v, u.kh, u.s.k0 + j * KB, n);
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
+// ---------------------------------------------------------------- warp 9: MMAs
+constexpr uint64_t K_STEP = 32 >> 4, K_HALF = HALF >> 4, MN_STEP = 2048 >> 4, D_TILE = TILE >> 4;
+constexpr uint32_t ID_KK = make_idesc_bf16_f32(128, 128), ID_MN = make_idesc_bf16_f32(128, 128, true);
+
+__device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
+    const int lane = threadIdx.x & 31;
+    const uint64_t dQ = make_sdesc_kmajor_sw128(x.base), dK = make_sdesc_kmajor_sw128(x.base + OFF_RING);
+    const uint64_t dV = make_sdesc_mnmajor_sw128(x.base + OFF_RING, HALF, 1024);
+    int slot = 0;                 // of the next tile to be waited for: k and v alternate
+    uint32_t lap = 0, pieces = 0, nP[2] = {0, 0};
+    bool ok = true;
+    // the next tile of the ring has landed; its slot
+    auto landed = [&](int& s) {
+        s = slot;
+        const bool r = x.wait(FULL + slot, lap);
+        if (++slot == RING) slot = 0, ++lap;
+        return r;
+    };
+    auto scores = [&](int t, int s) {
+        const uint64_t q = dQ + t * D_TILE, k = dK + s * D_TILE;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+                tc_mma_ss_warp(x.tmem + TM_S + 128 * t, q + half * K_HALF + kk * K_STEP, k + half * K_HALF + kk * K_STEP, ID_KK, half + kk > 0);
+        tc_commit_warp(x.bar(SF + t));
+    };
+    auto values = [&](int t, int s, bool first) {
+        const uint64_t v = dV + s * D_TILE;
+        const uint32_t a = x.tmem + TM_S + 128 * t;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+                tc_mma_ts_warp(x.tmem + TM_O + 128 * t, a + (4 * half + kk) * 8, v + (4 * half + kk) * MN_STEP, ID_MN, !first || half + kk > 0);
+    };
+    for (int64_t left = x.steps; left > 0 && ok; next_pair(p, x, u), ++pieces) {
+        const Piece r = piece_at(x, u, left);
+        left -= r.j1 - r.j0;
+        const int e1 = r.two ? r.j1 : r.j0;
+        int ks, vs;
+        ok = x.wait(QF, pieces) && landed(ks);
+        if (!ok) break;
+        tc_fence_after();
+        // the scores of the first block
+        if (r.j0 < r.e0) scores(0, ks);
+        if (r.j0 < e1) scores(1, ks);
+        tc_commit_warp(x.bar(EMPTY + ks));
+        for (int j = r.j0; j < r.j1; ++j) {
+            ok = landed(vs);
+            if (!ok) break;
+            const int valid = u.s.lk - j * KB;
+            if (valid < KB) {   // values past the sequence's keys count for nothing, whatever they hold
+                const uint32_t v = x.base + OFF_RING + vs * TILE;
+                for (int row = max(valid, 0); row < KB; ++row) sts_u64(v + (lane >> 4) * HALF + row * 128 + (lane & 15) * 8, 0u, 0u);
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+            const bool more = j + 1 < r.j1;
+            bool have = false;   // the next keys have landed
+            // each tile in turn: O += P V of this block, then the next block's scores over P
+            // (the tensor core takes the MMAs of one thread in order)
+#pragma unroll 1
+            for (int t = 0; t < 2; ++t) {
+                const int e = t ? e1 : r.e0;
+                if (j >= e) continue;
+                ok = x.wait(PF + t, nP[t]);
+                if (!ok) break;
+                ++nP[t];
+                tc_fence_after();
+                values(t, vs, j == r.j0);
+                if (j + 1 == e) {
+                    tc_commit_warp(x.bar(OF + t));
+                } else {
+                    if (!have) ok = landed(ks);
+                    if (!ok) break;
+                    have = true;
+                    tc_fence_after();
+                    scores(t, ks);
+                }
+            }
+            if (!ok) break;
+            tc_commit_warp(x.bar(EMPTY + vs));
+            if (more) {
+                if (!have) ok = landed(ks);   // (not reached: the longer tile always goes on)
+                tc_commit_warp(x.bar(EMPTY + ks));
+            }
+        }
+        tc_commit_warp(x.bar(QE));
+    }
+    __syncwarp();
+    tc_commit_warp(x.bar(DRAIN));
+    return x.wait(DRAIN, 0) && ok;
+}
+
+// ---------------------------------------------------------------- warps 0-7: softmax and results
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+__device__ bool softmax_warps(const AttnParams& p, const Ctx& x, Cursor u, int t) {
+    const int row = threadIdx.x & 127;
+    const uint32_t tS = x.tmem + ((uint32_t)(row & ~31) << 16) + TM_S + 128 * t, tO = tS - TM_S + TM_O;
+    const float c = fmaxf(p.scale * LOG2E, 1e-30f);   // (a scale of 0 must not turn a masked -inf into NaN)
+    const Partials part = partials(p.workspace);
+    const int tok = row / x.G, head = row - tok * x.G;
+    uint32_t nS = 0, nO = 0;
+    bool first_piece = true;
+    for (int64_t left = x.steps; left > 0; next_pair(p, x, u), first_piece = false) {
+        const Piece r = piece_at(x, u, left);
+        left -= r.j1 - r.j0;
+        if (t == 1 && !r.two) continue;
+        const int end = t ? r.j1 : r.e0;
+        const int i = u.pair * x.tp + t * x.tq + tok;                  // query within the sequence
+        const bool mine = tok < x.tq && i < u.s.lq;
+        const int last = mine ? i + u.s.lk - u.s.lq : -1;              // the last key it sees
+        float m = -INFINITY, l = 0.f;
+        for (int j = r.j0; j < end; ++j) {
+            if (!x.wait(SF + t, nS)) return false;
+            ++nS;
+            tc_fence_after();
+            uint32_t s[128];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) tmem_ld32(tS + 32 * b, reinterpret_cast<uint32_t(&)[32]>(s[32 * b]));
+            tmem_wait_ld();
+            const int seen = last - j * KB;   // columns 0 .. seen
+            if (__any_sync(0xffffffffu, seen < KB - 1)) {
+#pragma unroll
+                for (int k = 0; k < 128; ++k) s[k] = k <= seen ? s[k] : 0xff800000u;
+            }
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int k = 0; k < 128; k += 8)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], mx_u2f(s[k + 2 * e]), mx_u2f(s[k + 2 * e + 1]));
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            const bool grown = (top - m) * c > 8.f;   // (m = -inf: whenever a key is seen)
+            if (__any_sync(0xffffffffu, grown)) {
+                const float f = grown ? exp2f((m - top) * c) : 1.f;
+                if (grown) m = top;
+                l *= f;
+                if (j > r.j0) {
+                    const float2 f2 = make_float2(f, f);
+#pragma unroll 1
+                    for (int b = 0; b < 8; ++b) {
+                        uint32_t o[16];
+                        tmem_ld16(tO + 16 * b, o);
+                        tmem_wait_ld_regs(o);
+#pragma unroll
+                        for (int k = 0; k < 16; k += 2) {
+                            const float2 y = __fmul2_rn(make_float2(mx_u2f(o[k]), mx_u2f(o[k + 1])), f2);
+                            o[k] = __float_as_uint(y.x);
+                            o[k + 1] = __float_as_uint(y.y);
+                        }
+                        tmem_st16(tO + 16 * b, o);
+                    }
+                }
+            }
+            const float mc = m == -INFINITY ? 0.f : -m * c;
+            const float2 c2 = make_float2(c, c), mc2 = make_float2(mc, mc);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                uint32_t y[16];
+#pragma unroll
+                for (int k = 0; k < 32; k += 2) {
+                    const float2 a = __ffma2_rn(make_float2(mx_u2f(s[32 * b + k]), mx_u2f(s[32 * b + k + 1])), c2, mc2);
+                    const float2 e = make_float2(ex2_approx(a.x), ex2_approx(a.y));
+                    sum[(k >> 1) & 1] = __fadd2_rn(sum[(k >> 1) & 1], e);
+                    y[k / 2] = pack_bf16x2(e.x, e.y);
+                }
+                tmem_st16(tS + 16 * b, y);
+            }
+            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            tmem_wait_st();
+            tc_fence_before();
+            mx_arrive_warp(x.bar(PF + t));
+        }
+        const int64_t q = u.s.q0 + i;
+        const int h = u.kh * x.G + head;
+        const size_t slot = (size_t)(2 * blockIdx.x + (first_piece ? 0 : 1)) * 256 + 128 * t + row;
+        if (end > r.j0) {
+            if (!x.wait(OF + t, nO)) return false;
+            ++nO;
+            tc_fence_after();
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            __nv_bfloat16* out = p.out.data + q * p.out.row + h * p.out.head;
+#pragma unroll 1
+            for (int b = 0; b < 4; ++b) {
+                uint32_t o[32];
+                tmem_ld32(tO + 32 * b, o);
+                tmem_wait_ld();
+                if (mine && r.whole) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t y[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) y[e] = pack_bf16x2(mx_u2f(o[8 * k + 2 * e]) * inv, mx_u2f(o[8 * k + 2 * e + 1]) * inv);
+                        *reinterpret_cast<uint4*>(out + 32 * b + 8 * k) = make_uint4(y[0], y[1], y[2], y[3]);
+                    }
+                } else if (mine) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        *reinterpret_cast<uint4*>(part.o + slot * HD + 32 * b + 4 * k) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+        }
+        if (mine) {
+            if (!r.whole) part.ml[slot] = make_float2(m * c, l);
+            else if (p.lse) p.lse[q * p.Hq + h] = l > 0.f ? (m * c + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        }
+    }
+    return true;
+}
+
+__global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const AttnParams p, const __grid_constant__ AttnMaps maps) {
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    const int tid = threadIdx.x, warp = tid >> 5;
+    asm volatile("griddepcontrol.launch_dependents;");
+    Ctx x;
+    x.base = smem_u32(smem_raw);
+    x.G = p.Hq / p.Hk;
+    x.tq = 128 / x.G;
+    x.tp = 2 * x.tq;
+    int64_t total, x0 = 0;
+    bool bad;
+    const Cursor u = find_step<AT_THREADS>(p, x.tp, reinterpret_cast<int64_t*>(smem_raw), total, bad, [&](int64_t tot) {
+        x0 = share_start(tot, blockIdx.x, gridDim.x);
+        return x0;
+    });
+    if (blockIdx.x == 0 && tid == 0) *p.status = bad ? KDA_DEVERR_CU_SEQLENS : x.base % 1024 != 0 ? KDA_DEVERR_INTERNAL : 0u;
+    x.steps = share_start(total, blockIdx.x + 1, gridDim.x) - x0;
+    if (bad || x.steps == 0 || x.base % 1024 != 0) return;   // (the tiles' swizzle counts from 1 KB boundaries)
+    __syncthreads();
+    if (tid == 0) {
+        for (int b = 0; b < NBAR; ++b) mbar_init(x.bar(b), b == PF || b == PF + 1 ? 4 : 1);
+        mbar_fence_init();
+        tma_prefetch_desc(&maps.q);
+        tma_prefetch_desc(&maps.k);
+        tma_prefetch_desc(&maps.v);
+    }
+    if (warp == 0) {
+        tmem_alloc(x.base + OFF_TMEM, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    x.tmem = lds_u32(x.base + OFF_TMEM);
+    bool ok = true;
+    // registers a thread: 168 at launch; 208 + 208 + 88 of the 3 x 168 that the block holds
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        ok = softmax_warps(p, x, u, warp >> 2);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == 8) ok = load_warp(p, maps, x, u);
+        else if (warp == 9) ok = mma_warp(p, x, u);
+    }
+    if (!ok) mx_report(p.status);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(x.tmem, 512);
+    }
+}
+
+// Joins the partial rows of the pairs that several shares hold.  Block b looks at the cut between
+// the shares b and b + 1, and takes the pair there if it is the pair's first cut.
+constexpr int JOIN_THREADS = 256;
+__global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParams p, int ctas) {
+    __shared__ int64_t scratch[32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int G = p.Hq / p.Hk, tq = 128 / G, tp = 2 * tq, b = blockIdx.x;
+    int64_t total, cut = 0;
+    bool bad;
+    const Cursor u = find_step<JOIN_THREADS>(p, tp, scratch, total, bad, [&](int64_t tot) {
+        cut = share_start(tot, b + 1, ctas);
+        return cut;
+    });
+    if (bad || cut >= total || u.j == 0) return;             // the cut lies between two pairs
+    const int64_t i0 = cut - u.j, i1 = i0 + blocks_seen(u.s, (u.pair + 1) * tp);
+    if (share_start(total, b, ctas) > i0) return;            // an earlier cut has the pair
+    if (share_start(total, b, ctas) == cut) return;          // an empty share: the cut before is the same one
+    const Partials part = partials(p.workspace);
+    // the shares that hold parts, in order: b (its last piece), then those that start inside the pair
+    int end = b + 1;
+    while (end < ctas && share_start(total, end, ctas) < i1) ++end;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int first_slot = share_start(total, b, ctas) == i0 ? 0 : 1;
+    for (int row = warp; row < 256; row += JOIN_THREADS / 32) {
+        const int t = row >> 7, tok = (row & 127) / G, head = (row & 127) - tok * G;
+        const int i = u.pair * tp + t * tq + tok;
+        if (tok >= tq || i >= u.s.lq) continue;
+        float m = -INFINITY;
+        for (int s = b; s < end; ++s) {
+            if (share_start(total, s, ctas) == share_start(total, s + 1, ctas)) continue;
+            const float2 ml = part.ml[(size_t)(2 * s + (s == b ? first_slot : 0)) * 256 + row];
+            if (ml.y > 0.f) m = fmaxf(m, ml.x);
+        }
+        float l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s = b; s < end; ++s) {
+            if (share_start(total, s, ctas) == share_start(total, s + 1, ctas)) continue;
+            const size_t slot = (size_t)(2 * s + (s == b ? first_slot : 0)) * 256 + row;
+            const float2 ml = part.ml[slot];
+            if (ml.y == 0.f) continue;   // a part that saw no key (its rows may not even be written)
+            const float f = exp2f(ml.x - m);
+            const float4 y = *reinterpret_cast<const float4*>(part.o + slot * HD + 4 * lane);
+            l = fmaf(f, ml.y, l);
+            o.x = fmaf(f, y.x, o.x);
+            o.y = fmaf(f, y.y, o.y);
+            o.z = fmaf(f, y.z, o.z);
+            o.w = fmaf(f, y.w, o.w);
+        }
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const int64_t q = u.s.q0 + i;
+        const int h = u.kh * G + head;
+        *reinterpret_cast<uint2*>(p.out.data + q * p.out.row + h * p.out.head + 4 * lane) =
+            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        if (p.lse && lane == 0) p.lse[q * p.Hq + h] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    }
 }
 
 }  // namespace
 
-size_t attn_workspace_bytes(int64_t, int, int) { return 0; }
+size_t attn_workspace_bytes(int64_t, int, int) {
+    return (size_t)2 * AT_MAX_CTAS * 256 * (sizeof(float2) + HD * sizeof(float));
+}
 
 cudaError_t launch_attn(const AttnParams& p, cudaStream_t stream) {
-    const int64_t blocks = (p.Tq * p.Hq + AT_THREADS / 32 - 1) / (AT_THREADS / 32);
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    attn_kernel<<<(unsigned)(blocks > 0 ? blocks : 1), AT_THREADS, 0, stream>>>(p);
-    return cudaGetLastError();
+    const int G = p.Hq / p.Hk, tq = 128 / G;
+    AttnMaps maps;
+    if (!mx_encode(&maps.q, p.q.data, p.Hq, p.Tq, 1, p.q.head, p.q.row, 0, G, tq) ||
+        !mx_encode(&maps.k, p.k, p.Hk, p.Tk, p.cache ? p.nseq : 1, p.k_head, p.k_row, p.k_seq, 1, KB) ||
+        !mx_encode(&maps.v, p.v, p.Hk, p.Tk, p.cache ? p.nseq : 1, p.v_head, p.v_row, p.v_seq, 1, KB))
+        return cudaErrorInvalidValue;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)AT_SMEM);
+    if (e != cudaSuccess) return e;
+    const int ctas = sms < AT_MAX_CTAS ? sms : AT_MAX_CTAS;
+    attn_kernel<<<ctas, AT_THREADS, AT_SMEM, stream>>>(p, maps);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || ctas < 2) return e;
+    // the join may be launched before the first kernel ends; it waits for its results itself
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(ctas - 1));
+    cfg.blockDim = dim3(JOIN_THREADS);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_join_kernel, p, ctas);
 }
 
 }  // namespace kda

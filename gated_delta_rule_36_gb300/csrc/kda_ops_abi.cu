@@ -253,7 +253,7 @@ kda_status kda_attn_fwd(const kda_view* q, const kda_view* k, const kda_view* v,
                         const kda_tensor* cu_seqlens_k, const kda_tensor* seqlens_k, void* workspace,
                         size_t workspace_bytes, kda_stream_t stream) {
     kda::set_last_error("");
-    if (!isfinite(scale)) return fail(KDA_ERR_INVALID_ARG, "scale must be finite");
+    if (!isfinite(scale) || scale < 0.f) return fail(KDA_ERR_INVALID_ARG, "scale must be finite and >= 0");
     KDA_TRY(check_head_dim("q", q, 3));
     if (!present(k)) return fail(KDA_ERR_INVALID_ARG, "k: missing");
     if (k->ndim != 3 && k->ndim != 4)
@@ -264,8 +264,8 @@ kda_status kda_attn_fwd(const kda_view* q, const kda_view* k, const kda_view* v,
     const int64_t Tk = k->shape[cache ? 1 : 0], Hk = k->shape[cache ? 2 : 1];
     if (Tq < 0 || Hq < 1 || Tk < 0 || Hk < 1) return fail(KDA_ERR_INVALID_ARG, "bad q or k shape");
     if (Hq % Hk != 0) return fail(KDA_ERR_INVALID_ARG, "%lld query heads do not divide into %lld key heads", (long long)Hq, (long long)Hk);
-    if (Tq > INT32_MAX || Tk > INT32_MAX || Hq > 65535 || Hq / Hk > 128)
-        return fail(KDA_ERR_UNSUPPORTED, "Tq and Tk must be < 2^31, Hq <= 65535 and Hq / Hk <= 128");
+    if (Tq > (1 << 30) || Tk > (1 << 30) || Hq > 65535 || Hq / Hk > 128)
+        return fail(KDA_ERR_UNSUPPORTED, "Tq and Tk must be <= 2^30, Hq <= 65535 and Hq / Hk <= 128");
     // the sequences
     int64_t nseq = -1;
     if (present(cu_seqlens_q)) {

@@ -393,7 +393,8 @@ size_t kda_attn_workspace_size(int64_t Tq, int Hq, int Hk);
  *   out_i = sum_j softmax_j(scale q_i . k_j) v_j,   lse_i = log sum_j exp(scale q_i . k_j)
  * A query that sees no key (Lq > Lk, or no keys) gets out = 0 and lse = -inf.
  *
- *   q, out         bf16 [Tq, Hq, 128] (views)
+ *   q, out         bf16 [Tq, Hq, 128] (views); at most 2^30 queries, and keys of a sequence
+ *   scale          finite, >= 0
  *   lse            fp32 [Tq, Hq], or NULL/absent
  *   k, v           packed: bf16 [Tk, Hk, 128];  cache: bf16 [N, S, Hk, 128] (views; Hk divides Hq,
  *                  Hq / Hk <= 128)
