@@ -43,16 +43,22 @@ struct AttnMaps {
     CUtensorMap q, k, v;
 };
 
+// Where a share starts, for the join: the pair that it starts in and how far into it.
+struct Cut {
+    int j, nb;          // starts at block j of nb (j = 0: between two pairs; nb = 0: an empty share)
+    int q0, lq, kh, pair;
+    int pad[2];
+};
 // Partial results: two for each share, of 256 rows each.
 struct Partials {
-    float* o;     // [2 * shares][256][128], not normalised
+    Cut* cut;     // [shares]
     float2* ml;   // [2 * shares][256]: reference exponent (base 2) and sum
+    float* o;     // [2 * shares][256][128], not normalised
 };
-__host__ __device__ inline Partials partials(void* ws) {
-    Partials p;
-    p.ml = static_cast<float2*>(ws);
-    p.o = reinterpret_cast<float*>(static_cast<char*>(ws) + (size_t)2 * AT_MAX_CTAS * 256 * sizeof(float2));
-    return p;
+constexpr size_t CUT_BYTES = AT_MAX_CTAS * sizeof(Cut), ML_BYTES = (size_t)2 * AT_MAX_CTAS * 256 * sizeof(float2);
+__device__ __forceinline__ Partials partials(void* ws) {
+    char* at = static_cast<char*>(ws);
+    return Partials{reinterpret_cast<Cut*>(at), reinterpret_cast<float2*>(at + CUT_BYTES), reinterpret_cast<float*>(at + CUT_BYTES + ML_BYTES)};
 }
 
 // How a sequence's steps are laid out: tiles of tq tokens in pairs; pair j sees blocks(j) key blocks.
@@ -514,6 +520,11 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const AttnParams p,
     });
     if (blockIdx.x == 0 && tid == 0) *p.status = bad ? KDA_DEVERR_CU_SEQLENS : x.base % 1024 != 0 ? KDA_DEVERR_INTERNAL : 0u;
     x.steps = share_start(total, blockIdx.x + 1, gridDim.x) - x0;
+    if (tid == 0) {
+        Cut c{};
+        if (x.steps > 0) c = Cut{u.j, blocks_seen(u.s, (u.pair + 1) * x.tp), u.s.q0, u.s.lq, u.kh, u.pair, {0, 0}};
+        partials(p.workspace).cut[blockIdx.x] = c;
+    }
     if (bad || x.steps == 0 || x.base % 1024 != 0) return;   // (the tiles' swizzle counts from 1 KB boundaries)
     __syncthreads();
     if (tid == 0) {
@@ -550,57 +561,75 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const AttnParams p,
     }
 }
 
-// Joins the partial rows of the pairs that several shares hold.  Block b looks at the cut between
-// the shares b and b + 1, and takes the pair there if it is the pair's first cut.
-constexpr int JOIN_THREADS = 256;
+// Joins the partial rows of the pairs that several shares hold.  Block (b, y) takes 32 rows of the
+// pair that share b + 1 starts in, if that is the pair's first cut; a warp takes four of them, all
+// their loads at once.
+constexpr int JOIN_THREADS = 256, JOIN_ROWS = 32;
 __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParams p, int ctas) {
-    __shared__ int64_t scratch[32];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int G = p.Hq / p.Hk, tq = 128 / G, tp = 2 * tq, b = blockIdx.x;
-    int64_t total, cut = 0;
-    bool bad;
-    const Cursor u = find_step<JOIN_THREADS>(p, tp, scratch, total, bad, [&](int64_t tot) {
-        cut = share_start(tot, b + 1, ctas);
-        return cut;
-    });
-    if (bad || cut >= total || u.j == 0) return;             // the cut lies between two pairs
-    const int64_t i0 = cut - u.j, i1 = i0 + blocks_seen(u.s, (u.pair + 1) * tp);
-    if (share_start(total, b, ctas) > i0) return;            // an earlier cut has the pair
-    if (share_start(total, b, ctas) == cut) return;          // an empty share: the cut before is the same one
     const Partials part = partials(p.workspace);
-    // the shares that hold parts, in order: b (its last piece), then those that start inside the pair
-    int end = b + 1;
-    while (end < ctas && share_start(total, end, ctas) < i1) ++end;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int first_slot = share_start(total, b, ctas) == i0 ? 0 : 1;
-    for (int row = warp; row < 256; row += JOIN_THREADS / 32) {
+    const int first = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Cut c = part.cut[first];
+    if (c.j == 0) return;                        // between two pairs, or nothing to do
+    // the share before it that is not empty starts at or before the pair, or that cut was the first
+    int b = first - 1;
+    while (b > 0 && part.cut[b].nb == 0) --b;
+    const Cut before = part.cut[b];
+    const bool same = before.q0 == c.q0 && before.lq == c.lq && before.kh == c.kh && before.pair == c.pair;
+    if (same && before.j > 0) return;
+    // the parts: share b's last piece, then the first pieces of the shares that start inside the pair
+    int end = ctas;
+    for (int at = first; at < ctas; at += 32) {
+        const Cut e = part.cut[min(at + lane, ctas - 1)];
+        const bool past = at + lane < ctas && e.nb != 0 && (e.j == 0 || e.q0 != c.q0 || e.lq != c.lq || e.kh != c.kh || e.pair != c.pair);
+        const uint32_t mask = __ballot_sync(0xffffffffu, past);
+        if (mask) {
+            end = at + __ffs(mask) - 1;
+            break;
+        }
+    }
+    const int G = p.Hq / p.Hk, tq = 128 / G;
+    auto slot = [&](int s) { return (size_t)(2 * s + (s == b && !same ? 1 : 0)) * 256; };
+    auto empty = [&](int s) { return s != b && part.cut[s].nb == 0; };
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int row = blockIdx.y * JOIN_ROWS + 8 * k + warp;
         const int t = row >> 7, tok = (row & 127) / G, head = (row & 127) - tok * G;
-        const int i = u.pair * tp + t * tq + tok;
-        if (tok >= tq || i >= u.s.lq) continue;
+        const int i = (2 * c.pair + t) * tq + tok;
+        if (tok >= tq || i >= c.lq) continue;
         float m = -INFINITY;
-        for (int s = b; s < end; ++s) {
-            if (share_start(total, s, ctas) == share_start(total, s + 1, ctas)) continue;
-            const float2 ml = part.ml[(size_t)(2 * s + (s == b ? first_slot : 0)) * 256 + row];
+        for (int s = b + lane; s < end; s += 32) {
+            if (empty(s)) continue;
+            const float2 ml = part.ml[slot(s) + row];
             if (ml.y > 0.f) m = fmaxf(m, ml.x);
         }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         float l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int s = b; s < end; ++s) {
-            if (share_start(total, s, ctas) == share_start(total, s + 1, ctas)) continue;
-            const size_t slot = (size_t)(2 * s + (s == b ? first_slot : 0)) * 256 + row;
-            const float2 ml = part.ml[slot];
-            if (ml.y == 0.f) continue;   // a part that saw no key (its rows may not even be written)
-            const float f = exp2f(ml.x - m);
-            const float4 y = *reinterpret_cast<const float4*>(part.o + slot * HD + 4 * lane);
-            l = fmaf(f, ml.y, l);
-            o.x = fmaf(f, y.x, o.x);
-            o.y = fmaf(f, y.y, o.y);
-            o.z = fmaf(f, y.z, o.z);
-            o.w = fmaf(f, y.w, o.w);
+        for (int s0 = b; s0 < end; s0 += 32) {
+            const int s = s0 + lane;
+            float w = 0.f;
+            if (s < end && !empty(s)) {
+                const float2 ml = part.ml[slot(s) + row];
+                if (ml.y > 0.f) w = exp2f(ml.x - m), l = fmaf(w, ml.y, l);
+            }
+#pragma unroll 4
+            for (int e = 0; e < min(32, end - s0); ++e) {
+                const float f = __shfl_sync(0xffffffffu, w, e);
+                if (f == 0.f) continue;   // a part that saw no key (its rows may not even be written), or counts for nothing
+                const float4 y = __ldg(reinterpret_cast<const float4*>(part.o + (slot(s0 + e) + row) * HD + 4 * lane));
+                o.x = fmaf(f, y.x, o.x);
+                o.y = fmaf(f, y.y, o.y);
+                o.z = fmaf(f, y.z, o.z);
+                o.w = fmaf(f, y.w, o.w);
+            }
         }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
         const float inv = l > 0.f ? 1.f / l : 0.f;
-        const int64_t q = u.s.q0 + i;
-        const int h = u.kh * G + head;
+        const int64_t q = c.q0 + i;
+        const int h = c.kh * G + head;
         *reinterpret_cast<uint2*>(p.out.data + q * p.out.row + h * p.out.head + 4 * lane) =
             make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
         if (p.lse && lane == 0) p.lse[q * p.Hq + h] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
@@ -610,7 +639,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParam
 }  // namespace
 
 size_t attn_workspace_bytes(int64_t, int, int) {
-    return (size_t)2 * AT_MAX_CTAS * 256 * (sizeof(float2) + HD * sizeof(float));
+    return CUT_BYTES + ML_BYTES + (size_t)2 * AT_MAX_CTAS * 256 * HD * sizeof(float);
 }
 
 cudaError_t launch_attn(const AttnParams& p, cudaStream_t stream) {
@@ -634,7 +663,7 @@ cudaError_t launch_attn(const AttnParams& p, cudaStream_t stream) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(ctas - 1));
+    cfg.gridDim = dim3((unsigned)(ctas - 1), 256 / JOIN_ROWS);
     cfg.blockDim = dim3(JOIN_THREADS);
     cfg.stream = stream;
     cfg.attrs = attr;
