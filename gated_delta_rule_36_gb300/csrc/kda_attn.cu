@@ -16,7 +16,7 @@
 // the workspace, and a second, small kernel joins them in the order of the keys.
 //
 // Warp roles: warps 0-3 and 4-7 are the softmax of the two tiles (thread = row) and write the
-// results; warp 8 loads q, k and v by TMA (a ring of five 32 KB tiles), warp 9 issues the MMAs,
+// results; warp 8 loads q, k and v by TMA (a ring of four 32 KB tiles), warp 9 issues the MMAs,
 // alternating between the tiles so that one is multiplied while the other is exponentiated.
 //
 // Bound by the tensor cores for prompts (4 x 128 x 128 x 128 flop, 1,024 SM cycles, a tile and
@@ -30,14 +30,17 @@ constexpr int AT_THREADS = 384;
 constexpr int AT_MAX_CTAS = 160;
 constexpr int KB = 128;                       // keys a block
 constexpr uint32_t TILE = 128 * 256, HALF = TILE / 2;
-constexpr int RING = 5;
+constexpr int RING = 4;
 constexpr uint32_t OFF_RING = 2 * TILE;       // behind the two query tiles
-constexpr uint32_t OFF_BAR = OFF_RING + RING * TILE;
+constexpr uint32_t OFF_STAGE = OFF_RING + RING * TILE;   // 4 KB for each softmax warp: 32 rows of 128 bytes
+constexpr uint32_t OFF_BAR = OFF_STAGE + 8 * 4096;
 enum { FULL = 0, EMPTY = RING, QF = 2 * RING, QE, SF, PF = SF + 2, OF = PF + 2, DRAIN = OF + 2, NBAR };
 constexpr uint32_t OFF_TMEM = OFF_BAR + NBAR * 8;
 constexpr uint32_t AT_SMEM = OFF_TMEM + 8;
 static_assert(AT_SMEM <= 232448, "one CTA's shared memory");
-constexpr uint32_t TM_S = 0, TM_O = 256;      // two tiles of 128 columns each; P over the first 64 of S
+// Tensor Memory (all 512 columns, so that its address is 0): two tiles of 128 columns each; P over
+// the first 64 of S
+constexpr uint32_t TM_S = 0, TM_O = 256;
 
 struct AttnMaps {
     CUtensorMap q, k, v;
@@ -106,10 +109,10 @@ __device__ int64_t steps_before(const Seq& s, int m, int tp) {
     const int64_t n = m - ones;
     if (n == 0) return ones;
     const int64_t b = (int64_t)(ones + 1) * tp + d + KB - 1;   // floor((b + i tp) / 128), i < n
-    const int g = min(tp & -tp, KB), per = KB / g;
-    const int64_t full = n / per;
-    const int rest = (int)(n % per);
-    int64_t residues = full * ((int64_t)per * (b % g) + (int64_t)g * per * (per - 1) / 2);
+    const int g = min(tp & -tp, KB), bits = 7 - (__ffs(g) - 1), per = 1 << bits;
+    const int64_t full = n >> bits;
+    const int rest = (int)n & (per - 1);
+    int64_t residues = full * ((int64_t)per * (b & (g - 1)) + (int64_t)g * per * (per - 1) / 2);
     for (int i = 0; i < rest; ++i) residues += (b + (int64_t)i * tp) & (KB - 1);
     return ones + ((b * n + (int64_t)tp * (n * (n - 1) / 2) - residues) >> 7);
 }
@@ -118,8 +121,9 @@ __device__ __forceinline__ int64_t steps_of(const Seq& s, int tp) {
     return m == 0 ? 0 : steps_before(s, m - 1, tp) + blocks_seen(s, s.lq);
 }
 
-__device__ __forceinline__ int64_t share_start(int64_t total, int b, int ctas) {
-    return total / ctas * b + total % ctas * b / ctas;
+// Where share b of `ctas` equal ones starts (recip = 2^64 / ctas, rounded up: no division).
+__device__ __forceinline__ int64_t share_start(int64_t total, int b, int ctas, uint64_t recip) {
+    return b == ctas ? total : (int64_t)__umul64hi((uint64_t)total * (uint64_t)b, recip);
 }
 
 // A step: pair `pair` of key head kh of sequence n, key block j of nb.
@@ -185,8 +189,8 @@ __device__ Cursor find_step(const AttnParams& p, int tp, int64_t* scratch /* 32 
     u.n = (int)found[0];
     u.s = seq_of(p, u.n);
     const int64_t each = steps_of(u.s, tp);
-    u.kh = (int)(found[1] / each);
-    const int64_t at = found[1] % each;
+    u.kh = (uint64_t)(found[1] | each) >> 32 ? (int)(found[1] / each) : (int)((uint32_t)found[1] / (uint32_t)each);
+    const int64_t at = found[1] - u.kh * each;
     // the last pair that starts at or before `at`: every thread tries some of them
     const int m = pairs_of(u.s, tp);
     int best = 0;
@@ -214,7 +218,7 @@ struct Piece {
 };
 
 struct Ctx {
-    uint32_t base, tmem;
+    uint32_t base;
     int64_t steps;      // of this share
     int tq, tp, G;      // tokens of a tile and of a pair, heads of a group
     __device__ uint32_t bar(int b) const { return base + OFF_BAR + 8u * b; }
@@ -290,6 +294,7 @@ constexpr uint32_t ID_KK = make_idesc_bf16_f32(128, 128), ID_MN = make_idesc_bf1
 
 __device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
     const int lane = threadIdx.x & 31;
+    const uint32_t lead = mx_leader();
     const uint64_t dQ = make_sdesc_kmajor_sw128(x.base), dK = make_sdesc_kmajor_sw128(x.base + OFF_RING);
     const uint64_t dV = make_sdesc_mnmajor_sw128(x.base + OFF_RING, HALF, 1024);
     int slot = 0;                 // of the next tile to be waited for: k and v alternate
@@ -304,24 +309,22 @@ __device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
     };
     auto scores = [&](int t, int s) {
         const uint64_t q = dQ + t * D_TILE, k = dK + s * D_TILE;
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half)
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-                tc_mma_ss_warp(x.tmem + TM_S + 128 * t, q + half * K_HALF + kk * K_STEP, k + half * K_HALF + kk * K_STEP, ID_KK, half + kk > 0);
-        tc_commit_warp(x.bar(SF + t));
+        for (int kk = 0; kk < 8; ++kk)
+            mx_mma_ss(lead, TM_S + 128 * t, q + (kk >> 2) * K_HALF + (kk & 3) * K_STEP, k + (kk >> 2) * K_HALF + (kk & 3) * K_STEP, ID_KK, kk > 0);
+        mx_commit(lead, x.bar(SF + t));
     };
     auto values = [&](int t, int s, bool first) {
         const uint64_t v = dV + s * D_TILE;
-        const uint32_t a = x.tmem + TM_S + 128 * t;
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half)
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-                tc_mma_ts_warp(x.tmem + TM_O + 128 * t, a + (4 * half + kk) * 8, v + (4 * half + kk) * MN_STEP, ID_MN, !first || half + kk > 0);
+        for (int kk = 0; kk < 8; ++kk)
+            mx_mma_ts(lead, TM_O + 128 * t, TM_S + 128 * t + kk * 8, v + kk * MN_STEP, ID_MN, kk > 0 || !first);
     };
+    u.n = mx_uniform(u.n), u.kh = mx_uniform(u.kh), u.pair = mx_uniform(u.pair), u.j = mx_uniform(u.j);
     for (int64_t left = x.steps; left > 0 && ok; next_pair(p, x, u), ++pieces) {
-        const Piece r = piece_at(x, u, left);
+        u.s.lq = mx_uniform(u.s.lq), u.s.lk = mx_uniform(u.s.lk);
+        Piece r = piece_at(x, u, left);
+        r.j0 = mx_uniform(r.j0), r.j1 = mx_uniform(r.j1), r.e0 = mx_uniform(r.e0);
         left -= r.j1 - r.j0;
         const int e1 = r.two ? r.j1 : r.j0;
         int ks, vs;
@@ -331,7 +334,7 @@ __device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
         // the scores of the first block
         if (r.j0 < r.e0) scores(0, ks);
         if (r.j0 < e1) scores(1, ks);
-        tc_commit_warp(x.bar(EMPTY + ks));
+        mx_commit(lead, x.bar(EMPTY + ks));
         for (int j = r.j0; j < r.j1; ++j) {
             ok = landed(vs);
             if (!ok) break;
@@ -356,7 +359,7 @@ __device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
                 tc_fence_after();
                 values(t, vs, j == r.j0);
                 if (j + 1 == e) {
-                    tc_commit_warp(x.bar(OF + t));
+                    mx_commit(lead, x.bar(OF + t));
                 } else {
                     if (!have) ok = landed(ks);
                     if (!ok) break;
@@ -366,16 +369,16 @@ __device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
                 }
             }
             if (!ok) break;
-            tc_commit_warp(x.bar(EMPTY + vs));
+            mx_commit(lead, x.bar(EMPTY + vs));
             if (more) {
                 if (!have) ok = landed(ks);   // (not reached: the longer tile always goes on)
-                tc_commit_warp(x.bar(EMPTY + ks));
+                mx_commit(lead, x.bar(EMPTY + ks));
             }
         }
-        tc_commit_warp(x.bar(QE));
+        mx_commit(lead, x.bar(QE));
     }
     __syncwarp();
-    tc_commit_warp(x.bar(DRAIN));
+    mx_commit(lead, x.bar(DRAIN));
     return x.wait(DRAIN, 0) && ok;
 }
 
@@ -388,7 +391,9 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 __device__ bool softmax_warps(const AttnParams& p, const Ctx& x, Cursor u, int t) {
     const int row = threadIdx.x & 127;
-    const uint32_t tS = x.tmem + ((uint32_t)(row & ~31) << 16) + TM_S + 128 * t, tO = tS - TM_S + TM_O;
+    const uint32_t tS = ((uint32_t)(row & ~31) << 16) + TM_S + 128 * t, tO = tS - TM_S + TM_O;
+    const int lane = threadIdx.x & 31;
+    const uint32_t stage = x.base + OFF_STAGE + (threadIdx.x >> 5) * 4096;
     const float c = fmaxf(p.scale * LOG2E, 1e-30f);   // (a scale of 0 must not turn a masked -inf into NaN)
     const Partials part = partials(p.workspace);
     const int tok = row / x.G, head = row - tok * x.G;
@@ -401,7 +406,8 @@ __device__ bool softmax_warps(const AttnParams& p, const Ctx& x, Cursor u, int t
         const int end = t ? r.j1 : r.e0;
         const int i = u.pair * x.tp + t * x.tq + tok;                  // query within the sequence
         const bool mine = tok < x.tq && i < u.s.lq;
-        const int last = mine ? i + u.s.lk - u.s.lq : -1;              // the last key it sees
+        // the last key it sees; a row that is no query's is left as it is, nothing reads its results
+        const int last = mine ? i + u.s.lk - u.s.lq : 0x7fffffff;
         float m = -INFINITY, l = 0.f;
         for (int j = r.j0; j < end; ++j) {
             if (!x.wait(SF + t, nS)) return false;
@@ -422,7 +428,7 @@ __device__ bool softmax_warps(const AttnParams& p, const Ctx& x, Cursor u, int t
 #pragma unroll
                 for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], mx_u2f(s[k + 2 * e]), mx_u2f(s[k + 2 * e + 1]));
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            const bool grown = (top - m) * c > 8.f;   // (m = -inf: whenever a key is seen)
+            const bool grown = mine && (top - m) * c > 8.f;   // (m = -inf: whenever a key is seen)
             if (__any_sync(0xffffffffu, grown)) {
                 const float f = grown ? exp2f((m - top) * c) : 1.f;
                 if (grown) m = top;
@@ -472,24 +478,38 @@ __device__ bool softmax_warps(const AttnParams& p, const Ctx& x, Cursor u, int t
             ++nO;
             tc_fence_after();
             const float inv = l > 0.f ? 1.f / l : 0.f;
-            __nv_bfloat16* out = p.out.data + q * p.out.row + h * p.out.head;
+            // 128 bytes of a row at a time (64 results in bf16, or 32 of a partial row in fp32) go through
+            // the warp's stage, so that eight lanes store a row's 128 bytes together
+            unsigned char* dst = r.whole ? reinterpret_cast<unsigned char*>(p.out.data + q * p.out.row + h * p.out.head)
+                                         : reinterpret_cast<unsigned char*>(part.o + slot * HD);
+            const uint32_t mask = __ballot_sync(0xffffffffu, mine);
 #pragma unroll 1
             for (int b = 0; b < 4; ++b) {
                 uint32_t o[32];
                 tmem_ld32(tO + 32 * b, o);
                 tmem_wait_ld();
-                if (mine && r.whole) {
+                if (r.whole) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         uint32_t y[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) y[e] = pack_bf16x2(mx_u2f(o[8 * k + 2 * e]) * inv, mx_u2f(o[8 * k + 2 * e + 1]) * inv);
-                        *reinterpret_cast<uint4*>(out + 32 * b + 8 * k) = make_uint4(y[0], y[1], y[2], y[3]);
+                        sts_u128(stage + lane * 128 + (((4 * (b & 1) + k) ^ (lane & 7)) << 4), y[0], y[1], y[2], y[3]);
                     }
-                } else if (mine) {
+                    if (!(b & 1)) continue;
+                } else {
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        *reinterpret_cast<uint4*>(part.o + slot * HD + 32 * b + 4 * k) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                        sts_u128(stage + lane * 128 + ((k ^ (lane & 7)) << 4), o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                }
+                __syncwarp();
+                const int at = r.whole ? (b >> 1) * 128 : b * 128;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int from = 4 * k + (lane >> 3);   // this lane's row in turn
+                    unsigned char* d = reinterpret_cast<unsigned char*>(__shfl_sync(0xffffffffu, (unsigned long long)dst, from));
+                    const uint4 y = lds_u128(stage + from * 128 + (((lane & 7) ^ (from & 7)) << 4));
+                    if (mask >> from & 1u) *reinterpret_cast<uint4*>(d + at + (lane & 7) * 16) = y;
                 }
                 __syncwarp();
             }
@@ -503,45 +523,47 @@ __device__ bool softmax_warps(const AttnParams& p, const Ctx& x, Cursor u, int t
     return true;
 }
 
-__global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const AttnParams p, const __grid_constant__ AttnMaps maps) {
+__global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const AttnParams p, const __grid_constant__ AttnMaps maps, uint64_t recip) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    const int tid = threadIdx.x, warp = tid >> 5;
+    const int tid = threadIdx.x, warp = mx_uniform(tid >> 5);
     asm volatile("griddepcontrol.launch_dependents;");
     Ctx x;
     x.base = smem_u32(smem_raw);
     x.G = p.Hq / p.Hk;
     x.tq = 128 / x.G;
     x.tp = 2 * x.tq;
-    int64_t total, x0 = 0;
-    bool bad;
-    const Cursor u = find_step<AT_THREADS>(p, x.tp, reinterpret_cast<int64_t*>(smem_raw), total, bad, [&](int64_t tot) {
-        x0 = share_start(tot, blockIdx.x, gridDim.x);
-        return x0;
-    });
-    if (blockIdx.x == 0 && tid == 0) *p.status = bad ? KDA_DEVERR_CU_SEQLENS : x.base % 1024 != 0 ? KDA_DEVERR_INTERNAL : 0u;
-    x.steps = share_start(total, blockIdx.x + 1, gridDim.x) - x0;
-    if (tid == 0) {
-        Cut c{};
-        if (x.steps > 0) c = Cut{u.j, blocks_seen(u.s, (u.pair + 1) * x.tp), u.s.q0, u.s.lq, u.kh, u.pair, {0, 0}};
-        partials(p.workspace).cut[blockIdx.x] = c;
-    }
-    if (bad || x.steps == 0 || x.base % 1024 != 0) return;   // (the tiles' swizzle counts from 1 KB boundaries)
-    __syncthreads();
-    if (tid == 0) {
-        for (int b = 0; b < NBAR; ++b) mbar_init(x.bar(b), b == PF || b == PF + 1 ? 4 : 1);
-        mbar_fence_init();
-        tma_prefetch_desc(&maps.q);
-        tma_prefetch_desc(&maps.k);
-        tma_prefetch_desc(&maps.v);
-    }
-    if (warp == 0) {
+    if (warp == 8) {
+        if ((tid & 31) == 0) {
+            for (int b = 0; b < NBAR; ++b) mbar_init(x.bar(b), b == PF || b == PF + 1 ? 4 : 1);
+            mbar_fence_init();
+            tma_prefetch_desc(&maps.q);
+            tma_prefetch_desc(&maps.k);
+            tma_prefetch_desc(&maps.v);
+        }
+        __syncwarp();
         tmem_alloc(x.base + OFF_TMEM, 512);
         tmem_relinquish();
     }
     tc_fence_before();
+    int64_t total, x0 = 0;
+    bool bad;
+    const Cursor u = find_step<AT_THREADS>(p, x.tp, reinterpret_cast<int64_t*>(smem_raw), total, bad, [&](int64_t tot) {
+        x0 = share_start(tot, blockIdx.x, gridDim.x, recip);
+        return x0;
+    });
     __syncthreads();
     tc_fence_after();
-    x.tmem = lds_u32(x.base + OFF_TMEM);
+    const uint32_t tmem = lds_u32(x.base + OFF_TMEM);
+    const bool sound = tmem == 0 && x.base % 1024 == 0;   // (the tiles' swizzle counts from 1 KB boundaries)
+    x.steps = share_start(total, blockIdx.x + 1, gridDim.x, recip) - x0;
+    if (tid == 0) {
+        if (blockIdx.x == 0) *p.status = bad ? KDA_DEVERR_CU_SEQLENS : 0u;
+        if (!sound) atomicOr(p.status, KDA_DEVERR_INTERNAL);
+        Cut c{};
+        if (x.steps > 0) c = Cut{u.j, blocks_seen(u.s, (u.pair + 1) * x.tp), u.s.q0, u.s.lq, u.kh, u.pair, {0, 0}};
+        partials(p.workspace).cut[blockIdx.x] = c;
+    }
+    if (bad || !sound) x.steps = 0;   // (bad lengths have no steps anyway)
     bool ok = true;
     // registers a thread: 168 at launch; 208 + 208 + 88 of the 3 x 168 that the block holds
     if (warp < 8) {
@@ -555,9 +577,9 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const AttnParams p,
     if (!ok) mx_report(p.status);
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) {
+    if (warp == 8) {
         tc_fence_after();
-        tmem_dealloc(x.tmem, 512);
+        tmem_dealloc(tmem, 512);
     }
 }
 
@@ -655,7 +677,7 @@ cudaError_t launch_attn(const AttnParams& p, cudaStream_t stream) {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)AT_SMEM);
     if (e != cudaSuccess) return e;
     const int ctas = sms < AT_MAX_CTAS ? sms : AT_MAX_CTAS;
-    attn_kernel<<<ctas, AT_THREADS, AT_SMEM, stream>>>(p, maps);
+    attn_kernel<<<ctas, AT_THREADS, AT_SMEM, stream>>>(p, maps, ctas > 1 ? ~0ull / (uint64_t)ctas + 1 : 0);
     e = cudaGetLastError();
     if (e != cudaSuccess || ctas < 2) return e;
     // the join may be launched before the first kernel ends; it waits for its results itself
