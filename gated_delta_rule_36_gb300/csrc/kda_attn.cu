@@ -157,55 +157,59 @@ __device__ Cursor find_step(const AttnParams& p, int tp, int64_t* scratch /* 32 
     int64_t mine = 0;
     for (int n = n0; n < n1; ++n) mine += steps_of(seq_of(p, n), tp) * p.Hk;
     int64_t sum = mine;
-#pragma unroll
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
         const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
         if (lane >= o) sum += y;
     }
     if (lane == 31) scratch[warp] = sum;
+    int* best = reinterpret_cast<int*>(scratch + 16);
+    int64_t* found = scratch + 17;   // the sequence, the step within it; later the pair's first step
+    if (tid == 0) *best = 0;
     __syncthreads();
     int64_t before = sum - mine;
+#pragma unroll 1
     for (int w = 0; w < kThreads / 32; ++w) {
         before += w < warp ? scratch[w] : 0;
         total += scratch[w];
     }
     const int64_t x = x_of(total);
-    int64_t* found = scratch + 16;   // the sequence and the step within it
-    __syncthreads();
-    if (x >= before && x < before + mine) {
-        for (int n = n0; n < n1; ++n) {
-            const int64_t st = steps_of(seq_of(p, n), tp) * p.Hk;
-            if (x < before + st) {
-                found[0] = n;
-                found[1] = x - before;
-                break;
-            }
-            before += st;
-        }
-    }
-    if (tid == 0) found[2] = 0;
-    __syncthreads();
     if (x >= total) return u;
+    if (x >= before && x < before + mine) {
+        int n = n0;
+        int64_t st = mine;
+        if (n1 - n0 > 1)
+            for (;; ++n, before += st) {
+                st = steps_of(seq_of(p, n), tp) * p.Hk;
+                if (x < before + st) break;
+            }
+        found[0] = n;
+        found[1] = x - before;
+    }
+    __syncthreads();
     u.n = (int)found[0];
     u.s = seq_of(p, u.n);
+    // the key head and the step within it; then the last pair that starts at or before that step:
+    // every thread tries some of them
     const int64_t each = steps_of(u.s, tp);
     u.kh = (uint64_t)(found[1] | each) >> 32 ? (int)(found[1] / each) : (int)((uint32_t)found[1] / (uint32_t)each);
     const int64_t at = found[1] - u.kh * each;
-    // the last pair that starts at or before `at`: every thread tries some of them
-    const int m = pairs_of(u.s, tp);
-    int best = 0;
-    for (int lo = 0, width = m; width > 1;) {   // narrow [lo, lo + width)
-        const int step = (width + kThreads - 1) / kThreads;
-        const int c = lo + tid * step;
-        if (c < lo + width && steps_before(u.s, c, tp) <= at) atomicMax(reinterpret_cast<int*>(found + 2), c);
+    int lo = 0, width = pairs_of(u.s, tp);
+    int64_t start = 0;
+    while (width > 1) {   // narrow [lo, lo + width)
+        const int step = (width + kThreads - 1) / kThreads, c = lo + tid * step;
+        const int64_t st = c < lo + width ? steps_before(u.s, c, tp) : at + 1;
+        if (st <= at) atomicMax(best, c);
         __syncthreads();
-        best = *reinterpret_cast<volatile int*>(found + 2);
+        const int b = *best;
+        if (c == b && st <= at) found[2] = st;
         __syncthreads();
-        width = min(step, lo + width - best);
-        lo = best;
+        start = found[2];
+        width = min(step, lo + width - b);
+        lo = b;
     }
-    u.pair = best;
-    u.j = (int)(at - steps_before(u.s, best, tp));
+    u.pair = lo;
+    u.j = (int)(at - start);
     return u;
 }
 
@@ -271,18 +275,21 @@ __device__ bool load_warp(const AttnParams& p, const AttnMaps& maps, const Ctx& 
         for (int64_t left = x.steps; left > 0 && ok; next_pair(p, x, u), ++pieces) {
             const Piece r = piece_at(x, u, left);
             left -= r.j1 - r.j0;
-            if (pieces > 0) ok = mx_wait_lane(x.bar(QE), (pieces - 1) & 1u);
-            if (!ok) break;
-            const int t0 = u.s.q0 + u.pair * x.tp;
-            const uint32_t bytes = (uint32_t)(x.tq * x.G) * 256u;
-            mbar_arrive_expect_tx(x.bar(QF), r.two ? 2 * bytes : bytes);
-            for (int t = 0; t < (r.two ? 2 : 1); ++t) {
-                tma_load_4d(x.base + t * TILE, &maps.q, 0, u.kh * x.G, t0 + t * x.tq, 0, x.bar(QF));
-                tma_load_4d(x.base + t * TILE + HALF, &maps.q, 64, u.kh * x.G, t0 + t * x.tq, 0, x.bar(QF));
-            }
             const int n = p.cache ? u.n : 0;
-            for (int j = r.j0; j < r.j1 && ok; ++j)
+            for (int j = r.j0; j < r.j1 && ok; ++j) {
                 ok = tile(&maps.k, u.kh, u.s.k0 + j * KB, n) && tile(&maps.v, u.kh, u.s.k0 + j * KB, n);
+                if (j > r.j0 || !ok) continue;
+                // the queries, once the last scores of the piece before are done
+                if (pieces > 0) ok = mx_wait_lane(x.bar(QE), (pieces - 1) & 1u);
+                if (!ok) break;
+                const int t0 = u.s.q0 + u.pair * x.tp;
+                const uint32_t bytes = (uint32_t)(x.tq * x.G) * 256u;
+                mbar_arrive_expect_tx(x.bar(QF), r.two ? 2 * bytes : bytes);
+                for (int t = 0; t < (r.two ? 2 : 1); ++t) {
+                    tma_load_4d(x.base + t * TILE, &maps.q, 0, u.kh * x.G, t0 + t * x.tq, 0, x.bar(QF));
+                    tma_load_4d(x.base + t * TILE + HALF, &maps.q, 64, u.kh * x.G, t0 + t * x.tq, 0, x.bar(QF));
+                }
+            }
         }
     }
     return __all_sync(0xffffffffu, ok);
@@ -298,7 +305,7 @@ __device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
     const uint64_t dQ = make_sdesc_kmajor_sw128(x.base), dK = make_sdesc_kmajor_sw128(x.base + OFF_RING);
     const uint64_t dV = make_sdesc_mnmajor_sw128(x.base + OFF_RING, HALF, 1024);
     int slot = 0;                 // of the next tile to be waited for: k and v alternate
-    uint32_t lap = 0, pieces = 0, nP[2] = {0, 0};
+    uint32_t lap = 0, pieces = 0, n0 = 0, n1 = 0;
     bool ok = true;
     // the next tile of the ring has landed; its slot
     auto landed = [&](int& s) {
@@ -346,34 +353,31 @@ __device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
                 __syncwarp();
             }
             const bool more = j + 1 < r.j1;
-            bool have = false;   // the next keys have landed
             // each tile in turn: O += P V of this block, then the next block's scores over P
             // (the tensor core takes the MMAs of one thread in order)
-#pragma unroll 1
-            for (int t = 0; t < 2; ++t) {
-                const int e = t ? e1 : r.e0;
-                if (j >= e) continue;
-                ok = x.wait(PF + t, nP[t]);
+            if (j < r.e0) {
+                ok = x.wait(PF, n0++);
                 if (!ok) break;
-                ++nP[t];
                 tc_fence_after();
-                values(t, vs, j == r.j0);
-                if (j + 1 == e) {
-                    mx_commit(lead, x.bar(OF + t));
-                } else {
-                    if (!have) ok = landed(ks);
-                    if (!ok) break;
-                    have = true;
-                    tc_fence_after();
-                    scores(t, ks);
-                }
+                values(0, vs, j == r.j0);
+                if (j + 1 == r.e0) mx_commit(lead, x.bar(OF));
             }
-            if (!ok) break;
-            mx_commit(lead, x.bar(EMPTY + vs));
             if (more) {
-                if (!have) ok = landed(ks);   // (not reached: the longer tile always goes on)
-                mx_commit(lead, x.bar(EMPTY + ks));
+                ok = landed(ks);
+                if (!ok) break;
+                tc_fence_after();
+                if (j + 1 < r.e0) scores(0, ks);
             }
+            if (j < e1) {
+                ok = x.wait(PF + 1, n1++);
+                if (!ok) break;
+                tc_fence_after();
+                values(1, vs, j == r.j0);
+                if (j + 1 == e1) mx_commit(lead, x.bar(OF + 1));
+                else scores(1, ks);
+            }
+            mx_commit(lead, x.bar(EMPTY + vs));
+            if (more) mx_commit(lead, x.bar(EMPTY + ks));
         }
         mx_commit(lead, x.bar(QE));
     }
@@ -583,10 +587,10 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const AttnParams p,
     }
 }
 
-// Joins the partial rows of the pairs that several shares hold.  Block (b, y) takes 32 rows of the
-// pair that share b + 1 starts in, if that is the pair's first cut; a warp takes four of them, all
-// their loads at once.
-constexpr int JOIN_THREADS = 256, JOIN_ROWS = 32;
+// Joins the partial rows of the pairs that several shares hold.  Block (b, y) takes eight rows of
+// the pair that share b + 1 starts in, if that is the pair's first cut; a warp takes one of them.
+// Bound by latency: little code (it is fetched cold) and few loads in a row.
+constexpr int JOIN_THREADS = 256, JOIN_ROWS = 8;
 __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParams p, int ctas) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Partials part = partials(p.workspace);
@@ -613,49 +617,45 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParam
     const int G = p.Hq / p.Hk, tq = 128 / G;
     auto slot = [&](int s) { return (size_t)(2 * s + (s == b && !same ? 1 : 0)) * 256; };
     auto empty = [&](int s) { return s != b && part.cut[s].nb == 0; };
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int row = blockIdx.y * JOIN_ROWS + 8 * k + warp;
-        const int t = row >> 7, tok = (row & 127) / G, head = (row & 127) - tok * G;
-        const int i = (2 * c.pair + t) * tq + tok;
-        if (tok >= tq || i >= c.lq) continue;
-        float m = -INFINITY;
-        for (int s = b + lane; s < end; s += 32) {
-            if (empty(s)) continue;
-            const float2 ml = part.ml[slot(s) + row];
-            if (ml.y > 0.f) m = fmaxf(m, ml.x);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        float l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int s0 = b; s0 < end; s0 += 32) {
-            const int s = s0 + lane;
-            float w = 0.f;
-            if (s < end && !empty(s)) {
-                const float2 ml = part.ml[slot(s) + row];
-                if (ml.y > 0.f) w = exp2f(ml.x - m), l = fmaf(w, ml.y, l);
-            }
+    const int row = blockIdx.y * JOIN_ROWS + warp;
+    const int t = row >> 7, tok = (row & 127) / G, head = (row & 127) - tok * G;
+    const int i = (2 * c.pair + t) * tq + tok;
+    if (tok >= tq || i >= c.lq) return;
+    float m = -INFINITY, l = 0.f;   // this lane's parts; then all
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = b; s0 < end; s0 += 32) {   // (more than 32 parts: the sums so far are rescaled)
+        const int s = s0 + lane;
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (s < end && !empty(s)) ml = part.ml[slot(s) + row];
+        float top = ml.y > 0.f ? ml.x : -INFINITY;   // a part that saw no key has a sum of 0
+#pragma unroll 1
+        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        top = fmaxf(top, m);
+        const float old = m == -INFINITY ? 0.f : exp2f(m - top);
+        m = top;
+        const float w = ml.y > 0.f ? exp2f(ml.x - m) : 0.f;
+        l = fmaf(l, old, w * ml.y);
+        o.x *= old, o.y *= old, o.z *= old, o.w *= old;
+        const int n = min(32, end - s0);
 #pragma unroll 4
-            for (int e = 0; e < min(32, end - s0); ++e) {
-                const float f = __shfl_sync(0xffffffffu, w, e);
-                if (f == 0.f) continue;   // a part that saw no key (its rows may not even be written), or counts for nothing
-                const float4 y = __ldg(reinterpret_cast<const float4*>(part.o + (slot(s0 + e) + row) * HD + 4 * lane));
-                o.x = fmaf(f, y.x, o.x);
-                o.y = fmaf(f, y.y, o.y);
-                o.z = fmaf(f, y.z, o.z);
-                o.w = fmaf(f, y.w, o.w);
-            }
+        for (int e = 0; e < n; ++e) {
+            const float f = __shfl_sync(0xffffffffu, w, e);
+            if (f == 0.f) continue;   // (the rows of a part that saw no key may not even be written)
+            const float4 y = __ldg(reinterpret_cast<const float4*>(part.o + (slot(s0 + e) + row) * HD + 4 * lane));
+            o.x = fmaf(f, y.x, o.x);
+            o.y = fmaf(f, y.y, o.y);
+            o.z = fmaf(f, y.z, o.z);
+            o.w = fmaf(f, y.w, o.w);
         }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        const int64_t q = c.q0 + i;
-        const int h = c.kh * G + head;
-        *reinterpret_cast<uint2*>(p.out.data + q * p.out.row + h * p.out.head + 4 * lane) =
-            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-        if (p.lse && lane == 0) p.lse[q * p.Hq + h] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
     }
+#pragma unroll 1
+    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const int64_t q = c.q0 + i;
+    const int h = c.kh * G + head;
+    *reinterpret_cast<uint2*>(p.out.data + q * p.out.row + h * p.out.head + 4 * lane) =
+        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (p.lse && lane == 0) p.lse[q * p.Hq + h] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
 }  // namespace
