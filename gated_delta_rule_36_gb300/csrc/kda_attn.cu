@@ -44,6 +44,7 @@ constexpr uint32_t TM_S = 0, TM_O = 256;
 
 struct AttnMaps {
     CUtensorMap q, k, v;
+    CUtensorMap out;   // boxes of a warp's 32 rows (used when G divides 32)
 };
 
 // Where a share starts, for the join: the pair that it starts in and how far into it.
@@ -56,12 +57,12 @@ struct Cut {
 struct Partials {
     Cut* cut;     // [shares]
     float2* ml;   // [2 * shares][256]: reference exponent (base 2) and sum
-    float* o;     // [2 * shares][256][128], not normalised
+    float4* o;    // [2 * shares][32][256]: four channels of every row, not normalised (a warp of rows writes 512 bytes together)
 };
 constexpr size_t CUT_BYTES = AT_MAX_CTAS * sizeof(Cut), ML_BYTES = (size_t)2 * AT_MAX_CTAS * 256 * sizeof(float2);
 __device__ __forceinline__ Partials partials(void* ws) {
     char* at = static_cast<char*>(ws);
-    return Partials{reinterpret_cast<Cut*>(at), reinterpret_cast<float2*>(at + CUT_BYTES), reinterpret_cast<float*>(at + CUT_BYTES + ML_BYTES)};
+    return Partials{reinterpret_cast<Cut*>(at), reinterpret_cast<float2*>(at + CUT_BYTES), reinterpret_cast<float4*>(at + CUT_BYTES + ML_BYTES)};
 }
 
 // How a sequence's steps are laid out: tiles of tq tokens in pairs; pair j sees blocks(j) key blocks.
@@ -131,30 +132,33 @@ struct Cursor {
     Seq s;
 };
 
-// The whole block (of kThreads threads): checks the lengths, counts the steps and finds the step
-// x(total) among them, in the order (sequence, key head, pair, key block).
-template <int kThreads, class X>
+// The whole block: checks the lengths, counts the steps and finds the step x_of(total) among them,
+// in the order (sequence, key head, pair, key block).  Every CTA starts with this, so it is short
+// in latency: one pass over the lengths, two block-wide exchanges, one parallel search.
+struct Found {
+    int64_t at, each;   // the step within its sequence; steps of one key head there
+    int n;
+    Seq s;
+};
+template <class X>
 __device__ Cursor find_step(const AttnParams& p, int tp, int64_t* scratch /* 32 */, int64_t& total, bool& bad, X x_of) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (p.nseq + kThreads - 1) / kThreads;
+    const int per = (p.nseq + AT_THREADS - 1) / AT_THREADS;
     const int n0 = min(tid * per, p.nseq), n1 = min(n0 + per, p.nseq);
-    // lengths first: nothing is computed from a bad one
+    Seq s{};
+    int64_t mine = 0, each = 0;
     bad = false;
-    for (int n = n0; n < n1; ++n) {
-        if (p.cu_q) bad |= p.cu_q[n + 1] < p.cu_q[n];
-        if (p.cu_k) bad |= p.cu_k[n + 1] < p.cu_k[n];
-        if (p.seqlens_k) bad |= p.seqlens_k[n] < 0 || p.seqlens_k[n] > p.Tk;
+#pragma unroll 1
+    for (int n = n0; n < n1; ++n) {   // nothing is computed from bad lengths
+        bool b = false;
+        if (p.cu_q) b |= p.cu_q[n + 1] < p.cu_q[n] || (n == 0 && p.cu_q[0] != 0) || (n + 1 == p.nseq && p.cu_q[n + 1] > p.Tq);
+        if (p.cu_k) b |= p.cu_k[n + 1] < p.cu_k[n] || (n == 0 && p.cu_k[0] != 0) || (n + 1 == p.nseq && p.cu_k[n + 1] > p.Tk);
+        if (p.seqlens_k) b |= p.seqlens_k[n] < 0 || p.seqlens_k[n] > p.Tk;
+        bad |= b;
+        s = seq_of(p, n);
+        each = b ? 0 : steps_of(s, tp);
+        mine += each * p.Hk;
     }
-    if (tid == 0) {
-        if (p.cu_q) bad |= p.cu_q[0] != 0 || p.cu_q[p.nseq] > p.Tq;
-        if (p.cu_k) bad |= p.cu_k[0] != 0 || p.cu_k[p.nseq] > p.Tk;
-    }
-    bad = __syncthreads_or(bad);
-    total = 0;
-    Cursor u{};
-    if (bad) return u;
-    int64_t mine = 0;
-    for (int n = n0; n < n1; ++n) mine += steps_of(seq_of(p, n), tp) * p.Hk;
     int64_t sum = mine;
 #pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
@@ -163,50 +167,54 @@ __device__ Cursor find_step(const AttnParams& p, int tp, int64_t* scratch /* 32 
     }
     if (lane == 31) scratch[warp] = sum;
     int* best = reinterpret_cast<int*>(scratch + 16);
-    int64_t* found = scratch + 17;   // the sequence, the step within it; later the pair's first step
     if (tid == 0) *best = 0;
-    __syncthreads();
+    bad = __syncthreads_or(bad);
+    total = 0;
     int64_t before = sum - mine;
 #pragma unroll 1
-    for (int w = 0; w < kThreads / 32; ++w) {
+    for (int w = 0; w < AT_THREADS / 32; ++w) {
         before += w < warp ? scratch[w] : 0;
         total += scratch[w];
     }
+    if (bad) total = 0;
     const int64_t x = x_of(total);
+    Cursor u{};
     if (x >= total) return u;
+    Found* found = reinterpret_cast<Found*>(scratch + 18);
     if (x >= before && x < before + mine) {
-        int n = n0;
-        int64_t st = mine;
-        if (n1 - n0 > 1)
-            for (;; ++n, before += st) {
-                st = steps_of(seq_of(p, n), tp) * p.Hk;
-                if (x < before + st) break;
+        int n = n1 - 1;
+        if (n > n0)
+            for (n = n0;; ++n) {
+                s = seq_of(p, n);
+                each = steps_of(s, tp);
+                if (x < before + each * p.Hk) break;
+                before += each * p.Hk;
             }
-        found[0] = n;
-        found[1] = x - before;
+        *found = Found{x - before, each, n, s};
     }
     __syncthreads();
-    u.n = (int)found[0];
-    u.s = seq_of(p, u.n);
+    u.n = found->n;
+    u.s = found->s;
     // the key head and the step within it; then the last pair that starts at or before that step:
     // every thread tries some of them
-    const int64_t each = steps_of(u.s, tp);
-    int64_t at = found[1];
+    int64_t at = found->at;
+    each = found->each;
     u.kh = (int)((float)at / (float)each);   // (within one of the quotient, which is below 2^16)
     at -= u.kh * each;
     if (at < 0) --u.kh, at += each;
     else if (at >= each) ++u.kh, at -= each;
     int lo = 0, width = pairs_of(u.s, tp);
     int64_t start = 0;
+#pragma unroll 1
     while (width > 1) {   // narrow [lo, lo + width)
-        const int step = (width + kThreads - 1) / kThreads, c = lo + tid * step;
+        const int step = (width + AT_THREADS - 1) / AT_THREADS, c = lo + tid * step;
         const int64_t st = c < lo + width ? steps_before(u.s.lq, u.s.lk, c, tp) : at + 1;
         if (st <= at) atomicMax(best, c);
         __syncthreads();
         const int b = *best;
-        if (c == b && st <= at) found[2] = st;
+        if (c == b && st <= at) scratch[17] = st;
         __syncthreads();
-        start = found[2];
+        start = scratch[17];
         width = min(step, lo + width - b);
         lo = b;
     }
@@ -416,7 +424,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
-__device__ bool softmax_warps(const AttnParams& p, const Ctx& x, Cursor u, int t) {
+__device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const Ctx& x, Cursor u, int t) {
     const int row = threadIdx.x & 127;
     const uint32_t tS = ((uint32_t)(row & ~31) << 16) + TM_S + 128 * t, tO = tS - TM_S + TM_O;
     const int lane = threadIdx.x & 31;
@@ -501,54 +509,78 @@ __device__ bool softmax_warps(const AttnParams& p, const Ctx& x, Cursor u, int t
         }
         const int64_t q = u.s.q0 + i;
         const int h = u.kh * x.G + head;
-        const size_t slot = (size_t)(2 * blockIdx.x + (first_piece ? 0 : 1)) * 256 + 128 * t + row;
+        const size_t part_slot = 2 * blockIdx.x + (first_piece ? 0 : 1);
+        const int part_row = 128 * t + row;
+        const uint32_t mask = __ballot_sync(0xffffffffu, mine);
         if (end > r.j0) {
             if (!x.wait(OF + t, nO)) return false;
             ++nO;
             tc_fence_after();
-            const float inv = l > 0.f ? 1.f / l : 0.f;
-            // 128 bytes of a row at a time (64 results in bf16, or 32 of a partial row in fp32) go through
-            // the warp's stage, so that eight lanes store a row's 128 bytes together
-            unsigned char* dst = r.whole ? reinterpret_cast<unsigned char*>(p.out.data + q * p.out.row + h * p.out.head)
-                                         : reinterpret_cast<unsigned char*>(part.o + slot * HD);
-            const uint32_t mask = __ballot_sync(0xffffffffu, mine);
+            if (!r.whole) {
+                float4* o = part.o + part_slot * 32 * 256 + part_row;
 #pragma unroll 1
-            for (int b = 0; b < 4; ++b) {
-                uint32_t o[32];
-                tmem_ld32(tO + 32 * b, o);
-                tmem_wait_ld();
-                if (r.whole) {
+                for (int b = mask ? 0 : 4; b < 4; ++b) {
+                    uint32_t w[32];
+                    tmem_ld32(tO + 32 * b, w);
+                    tmem_wait_ld();
+                    if (mine) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t y[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) y[e] = pack_bf16x2(mx_u2f(o[8 * k + 2 * e]) * inv, mx_u2f(o[8 * k + 2 * e + 1]) * inv);
-                        sts_u128(stage + lane * 128 + (((4 * (b & 1) + k) ^ (lane & 7)) << 4), y[0], y[1], y[2], y[3]);
+                        for (int k = 0; k < 8; ++k)
+                            o[(8 * b + k) * 256] = make_float4(mx_u2f(w[4 * k]), mx_u2f(w[4 * k + 1]), mx_u2f(w[4 * k + 2]), mx_u2f(w[4 * k + 3]));
                     }
+                    __syncwarp();
+                }
+            } else {
+                // 64 channels at a time through the warp's stage; then one tensor store of the warp's rows
+                // if they are whole tokens and all there, or eight lanes a row
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+                const float2 inv2 = make_float2(inv, inv);
+                const bool tensor = mask == 0xffffffffu && x.G <= 32 && (x.G & (x.G - 1)) == 0;
+                const unsigned long long dst = reinterpret_cast<unsigned long long>(p.out.data + q * p.out.row + h * p.out.head);
+#pragma unroll 1
+                for (int b = mask ? 0 : 4; b < 4; ++b) {
+                    uint32_t w[32];
+                    tmem_ld32(tO + 32 * b, w);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) {
+                        const float2 y = __fmul2_rn(make_float2(mx_u2f(w[k]), mx_u2f(w[k + 1])), inv2);
+                        w[k / 2] = pack_bf16x2(y.x, y.y);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        sts_u128(stage + lane * 128 + (((4 * (b & 1) + k) ^ (lane & 7)) << 4), w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
                     if (!(b & 1)) continue;
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        sts_u128(stage + lane * 128 + ((k ^ (lane & 7)) << 4), o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                    if (tensor) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_3d(&maps.out, stage, 32 * (b - 1), u.kh * x.G, (int)q);
+                            bulk_commit();
+                            bulk_wait_read_all();
+                        }
+                    } else {
+                        __syncwarp();
+#pragma unroll 1
+                        for (int k = 0; k < 8; ++k) {
+                            const int from = 4 * k + (lane >> 3);   // this lane's row in turn
+                            const unsigned long long d = __shfl_sync(0xffffffffu, dst, from);
+                            const uint4 y = lds_u128(stage + from * 128 + (((lane & 7) ^ (from & 7)) << 4));
+                            if (mask >> from & 1u) *reinterpret_cast<uint4*>(d + (b >> 1) * 128 + (lane & 7) * 16) = y;
+                        }
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
-                const int at = r.whole ? (b >> 1) * 128 : b * 128;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int from = 4 * k + (lane >> 3);   // this lane's row in turn
-                    unsigned char* d = reinterpret_cast<unsigned char*>(__shfl_sync(0xffffffffu, (unsigned long long)dst, from));
-                    const uint4 y = lds_u128(stage + from * 128 + (((lane & 7) ^ (from & 7)) << 4));
-                    if (mask >> from & 1u) *reinterpret_cast<uint4*>(d + at + (lane & 7) * 16) = y;
-                }
-                __syncwarp();
             }
             tc_fence_before();
         }
         if (mine) {
-            if (!r.whole) part.ml[slot] = make_float2(m * c, l);
+            if (!r.whole) part.ml[part_slot * 256 + part_row] = make_float2(m * c, l);
             else if (p.lse) p.lse[q * p.Hq + h] = l > 0.f ? (m * c + log2f(l)) * 0.6931471805599453f : -INFINITY;
         }
     }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
     return true;
 }
 
@@ -568,6 +600,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const AttnParams p,
             tma_prefetch_desc(&maps.q);
             tma_prefetch_desc(&maps.k);
             tma_prefetch_desc(&maps.v);
+            tma_prefetch_desc(&maps.out);
         }
         __syncwarp();
         tmem_alloc(x.base + OFF_TMEM, 512);
@@ -576,7 +609,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const AttnParams p,
     tc_fence_before();
     int64_t total, x0 = 0;
     bool bad;
-    const Cursor u = find_step<AT_THREADS>(p, x.tp, reinterpret_cast<int64_t*>(smem_raw), total, bad, [&](int64_t tot) {
+    const Cursor u = find_step(p, x.tp, reinterpret_cast<int64_t*>(smem_raw), total, bad, [&](int64_t tot) {
         x0 = share_start(tot, blockIdx.x, gridDim.x, recip);
         return x0;
     });
@@ -597,7 +630,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const AttnParams p,
     // registers a thread: 168 at launch; 208 + 208 + 88 of the 3 x 168 that the block holds
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-        ok = softmax_warps(p, x, u, warp >> 2);
+        ok = softmax_warps(p, maps, x, u, warp >> 2);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 8) ok = load_warp(p, maps, x, u);
@@ -612,75 +645,81 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const AttnParams p,
     }
 }
 
-// Joins the partial rows of the pairs that several shares hold.  Block (b, y) takes eight rows of
-// the pair that share b + 1 starts in, if that is the pair's first cut; a warp takes one of them.
-// Bound by latency: little code (it is fetched cold) and few loads in a row.
-constexpr int JOIN_THREADS = 256, JOIN_ROWS = 8;
+// Joins the partial rows of the pairs that several shares hold.  Block (b, y) takes 32 rows of the
+// pair that share b + 1 starts in, if that is the pair's first cut; a warp takes four of them, lane l
+// their channels 4 l .. 4 l + 3.  Bound by latency: little code (it is fetched cold) and few loads
+// in a row.
+constexpr int JOIN_THREADS = 256, JOIN_ROWS = 32;
 __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParams p, int ctas) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const Partials part = partials(p.workspace);
     const int first = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int G = p.Hq / p.Hk, tq = 128 / G;
+    const Partials part = partials(p.workspace);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const Cut c = part.cut[first];
+    Cut before = part.cut[first - 1];
+    Cut e = part.cut[min(first + lane, ctas - 1)];
     if (c.j == 0) return;                        // between two pairs, or nothing to do
     // the share before it that is not empty starts at or before the pair, or that cut was the first
     int b = first - 1;
-    while (b > 0 && part.cut[b].nb == 0) --b;
-    const Cut before = part.cut[b];
-    const bool same = before.q0 == c.q0 && before.lq == c.lq && before.kh == c.kh && before.pair == c.pair;
+    while (b > 0 && before.nb == 0) before = part.cut[--b];
+    auto inside = [&](const Cut& a) { return a.q0 == c.q0 && a.lq == c.lq && a.kh == c.kh && a.pair == c.pair; };
+    const bool same = inside(before);
     if (same && before.j > 0) return;
     // the parts: share b's last piece, then the first pieces of the shares that start inside the pair
-    int end = ctas;
-    for (int at = first; at < ctas; at += 32) {
-        const Cut e = part.cut[min(at + lane, ctas - 1)];
-        const bool past = at + lane < ctas && e.nb != 0 && (e.j == 0 || e.q0 != c.q0 || e.lq != c.lq || e.kh != c.kh || e.pair != c.pair);
-        const uint32_t mask = __ballot_sync(0xffffffffu, past);
-        if (mask) {
-            end = at + __ffs(mask) - 1;
+    int end = first;
+    for (;;) {
+        const uint32_t past = __ballot_sync(0xffffffffu, end + lane >= ctas || (e.nb != 0 && (e.j == 0 || !inside(e))));
+        if (past) {
+            end += __ffs(past) - 1;
             break;
         }
+        end += 32;
+        e = part.cut[min(end + lane, ctas - 1)];
     }
-    const int G = p.Hq / p.Hk, tq = 128 / G;
-    auto slot = [&](int s) { return (size_t)(2 * s + (s == b && !same ? 1 : 0)) * 256; };
-    auto empty = [&](int s) { return s != b && part.cut[s].nb == 0; };
-    const int row = blockIdx.y * JOIN_ROWS + warp;
-    const int t = row >> 7, tok = (row & 127) / G, head = (row & 127) - tok * G;
-    const int i = (2 * c.pair + t) * tq + tok;
-    if (tok >= tq || i >= c.lq) return;
-    float m = -INFINITY, l = 0.f;   // this lane's parts; then all
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = b; s0 < end; s0 += 32) {   // (more than 32 parts: the sums so far are rescaled)
-        const int s = s0 + lane;
-        float2 ml = make_float2(-INFINITY, 0.f);
-        if (s < end && !empty(s)) ml = part.ml[slot(s) + row];
-        float top = ml.y > 0.f ? ml.x : -INFINITY;   // a part that saw no key has a sum of 0
+    auto slot = [&](int s) { return (size_t)(2 * s + (s == b && !same ? 1 : 0)); };
 #pragma unroll 1
-        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        top = fmaxf(top, m);
-        const float old = m == -INFINITY ? 0.f : exp2f(m - top);
-        m = top;
-        const float w = ml.y > 0.f ? exp2f(ml.x - m) : 0.f;
-        l = fmaf(l, old, w * ml.y);
-        o.x *= old, o.y *= old, o.z *= old, o.w *= old;
-        const int n = min(32, end - s0);
+    for (int k = 0; k < JOIN_ROWS / 8; ++k) {
+        const int row = blockIdx.y * JOIN_ROWS + 8 * k + warp;
+        const int t = row >> 7, tok = (row & 127) / G, head = (row & 127) - tok * G;
+        const int i = (2 * c.pair + t) * tq + tok;
+        if (tok >= tq || i >= c.lq) continue;
+        float m = -INFINITY, l = 0.f;   // this lane's parts; then all
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int s0 = b; s0 < end; s0 += 32) {   // (more than 32 parts: the sums so far are rescaled)
+            const int s = s0 + lane;
+            float2 ml = make_float2(-INFINITY, 0.f);
+            if (s < end && (s == b || part.cut[s].nb != 0)) ml = part.ml[slot(s) * 256 + row];
+            float top = ml.y > 0.f ? ml.x : -INFINITY;   // a part that saw no key has a sum of 0
+#pragma unroll 1
+            for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            top = fmaxf(top, m);
+            const float old = m == -INFINITY ? 0.f : exp2f(m - top);
+            m = top;
+            const float w = ml.y > 0.f ? exp2f(ml.x - m) : 0.f;
+            l = fmaf(l, old, w * ml.y);
+            o.x *= old, o.y *= old, o.z *= old, o.w *= old;
+            const int n = min(32, end - s0);
 #pragma unroll 4
-        for (int e = 0; e < n; ++e) {
-            const float f = __shfl_sync(0xffffffffu, w, e);
-            if (f == 0.f) continue;   // (the rows of a part that saw no key may not even be written)
-            const float4 y = __ldg(reinterpret_cast<const float4*>(part.o + (slot(s0 + e) + row) * HD + 4 * lane));
-            o.x = fmaf(f, y.x, o.x);
-            o.y = fmaf(f, y.y, o.y);
-            o.z = fmaf(f, y.z, o.z);
-            o.w = fmaf(f, y.w, o.w);
+            for (int a = 0; a < n; ++a) {
+                const float f = __shfl_sync(0xffffffffu, w, a);
+                if (f == 0.f) continue;   // (the rows of a part that saw no key may not even be written)
+                const float4 y = __ldcg(part.o + (slot(s0 + a) * 32 + lane) * 256 + row);
+                o.x = fmaf(f, y.x, o.x);
+                o.y = fmaf(f, y.y, o.y);
+                o.z = fmaf(f, y.z, o.z);
+                o.w = fmaf(f, y.w, o.w);
+            }
         }
-    }
 #pragma unroll 1
-    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    const int64_t q = c.q0 + i;
-    const int h = c.kh * G + head;
-    *reinterpret_cast<uint2*>(p.out.data + q * p.out.row + h * p.out.head + 4 * lane) =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (p.lse && lane == 0) p.lse[q * p.Hq + h] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const int64_t q = c.q0 + i;
+        const int h = c.kh * G + head;
+        *reinterpret_cast<uint2*>(p.out.data + q * p.out.row + h * p.out.head + 4 * lane) =
+            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        if (p.lse && lane == 0) p.lse[q * p.Hq + h] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    }
 }
 
 }  // namespace
@@ -694,7 +733,8 @@ cudaError_t launch_attn(const AttnParams& p, cudaStream_t stream) {
     AttnMaps maps;
     if (!mx_encode(&maps.q, p.q.data, p.Hq, p.Tq, 1, p.q.head, p.q.row, 0, G, tq) ||
         !mx_encode(&maps.k, p.k, p.Hk, p.Tk, p.cache ? p.nseq : 1, p.k_head, p.k_row, p.k_seq, 1, KB) ||
-        !mx_encode(&maps.v, p.v, p.Hk, p.Tk, p.cache ? p.nseq : 1, p.v_head, p.v_row, p.v_seq, 1, KB))
+        !mx_encode(&maps.v, p.v, p.Hk, p.Tk, p.cache ? p.nseq : 1, p.v_head, p.v_row, p.v_seq, 1, KB) ||
+        !mx_encode_3d(&maps.out, p.out.data, p.Hq, p.Tq, p.out.head, p.out.row, G <= 32 ? G : 1, G <= 32 ? 32 / G : 1))
         return cudaErrorInvalidValue;
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);

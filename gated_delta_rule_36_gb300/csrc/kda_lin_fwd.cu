@@ -744,7 +744,7 @@ cudaError_t launch_lin_fwd(const LinParams& p, cudaStream_t stream) {
     if (!mx_encode(&maps.q, p.q.data, p.H, p.T_total, 1, p.q.head, p.q.row, 0, 1, LF_C) ||
         !mx_encode(&maps.k, p.k.data, p.H, p.T_total, 1, p.k.head, p.k.row, 0, 1, LF_C) ||
         !mx_encode(&maps.v, p.v.data, p.H, p.T_total, 1, p.v.head, p.v.row, 0, 1, LF_C) ||
-        !mx_encode_3d(&maps.out, p.out.data, p.H, p.T_total, p.out.head, p.out.row, 32))
+        !mx_encode_3d(&maps.out, p.out.data, p.H, p.T_total, p.out.head, p.out.row, 1, 32))
         return cudaErrorInvalidValue;
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);

@@ -179,14 +179,14 @@ inline bool mx_encode(CUtensorMap* m, const void* ptr, int64_t heads, int64_t ro
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The same tensor without the sequence dimension, for stores of 64 channels x 1 head x box_rows.
+// The same tensor without the sequence dimension, for stores of 64 channels x box_heads x box_rows.
 inline bool mx_encode_3d(CUtensorMap* m, const void* ptr, int64_t heads, int64_t rows, int64_t head_stride, int64_t row_stride,
-                         int box_rows) {
+                         int box_heads, int box_rows) {
     MxEncodeFn fn = mx_encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)HD, (cuuint64_t)heads, (cuuint64_t)(rows > 0 ? rows : 1)};
     const cuuint64_t strides[2] = {(cuuint64_t)head_stride * 2, (cuuint64_t)row_stride * 2};
-    const cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
     const cuuint32_t estr[3] = {1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
