@@ -132,22 +132,27 @@ struct Cursor {
     Seq s;
 };
 
-// The whole block: checks the lengths, counts the steps and finds the step x_of(total) among them,
-// in the order (sequence, key head, pair, key block).  Every CTA starts with this, so it is short
-// in latency: one pass over the lengths, two block-wide exchanges, one parallel search.
+// The whole block: checks the lengths, counts the steps and finds where share b starts and ends
+// among them, in the order (sequence, key head, pair, key block).  Every CTA starts with this, so
+// it is short in latency: one pass over the lengths, two block-wide exchanges, one parallel search.
 struct Found {
     int64_t at, each;   // the step within its sequence; steps of one key head there
     int n;
     Seq s;
 };
-template <class X>
-__device__ Cursor find_step(const AttnParams& p, int tp, int64_t* scratch /* 32 */, int64_t& total, bool& bad, X x_of) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+struct Share {
+    int64_t steps;
+    Cursor at;          // where it starts
+    bool bad;           // lengths that contradict the tensors
+};
+__device__ Share find_share(const AttnParams& p, int tq, int G, uint64_t recip, int64_t* scratch /* 48 */) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tp = 2 * tq;
     const int per = (p.nseq + AT_THREADS - 1) / AT_THREADS;
     const int n0 = min(tid * per, p.nseq), n1 = min(n0 + per, p.nseq);
     Seq s{};
     int64_t mine = 0, each = 0;
-    bad = false;
+    Share r{};
+    bool bad = false;
 #pragma unroll 1
     for (int n = n0; n < n1; ++n) {   // nothing is computed from bad lengths
         bool b = false;
@@ -166,61 +171,92 @@ __device__ Cursor find_step(const AttnParams& p, int tp, int64_t* scratch /* 32 
         if (lane >= o) sum += y;
     }
     if (lane == 31) scratch[warp] = sum;
-    int* best = reinterpret_cast<int*>(scratch + 16);
-    if (tid == 0) *best = 0;
-    bad = __syncthreads_or(bad);
-    total = 0;
-    int64_t before = sum - mine;
+    int* best = reinterpret_cast<int*>(scratch + 16);   // [2]
+    int64_t* start = scratch + 18;                      // [2]
+    Found* found = reinterpret_cast<Found*>(scratch + 20);   // [2]: the start, the end
+    if (tid < 2) best[tid] = 0, start[tid] = 0;
+    r.bad = __syncthreads_or(bad);
+    if (r.bad) return r;
+    int64_t total = 0, before = sum - mine;
 #pragma unroll 1
     for (int w = 0; w < AT_THREADS / 32; ++w) {
         before += w < warp ? scratch[w] : 0;
         total += scratch[w];
     }
-    if (bad) total = 0;
-    const int64_t x = x_of(total);
-    Cursor u{};
-    if (x >= total) return u;
-    Found* found = reinterpret_cast<Found*>(scratch + 18);
-    if (x >= before && x < before + mine) {
+    const int64_t x0 = share_start(total, blockIdx.x, gridDim.x, recip), x1 = share_start(total, blockIdx.x + 1, gridDim.x, recip);
+    if (x0 >= total) return r;
+#pragma unroll 1
+    for (int e = 0; e < 2; ++e) {
+        const int64_t x = e ? x1 : x0;
+        if (x < before || x >= before + mine) continue;
+        int64_t base = before;
         int n = n1 - 1;
         if (n > n0)
             for (n = n0;; ++n) {
                 s = seq_of(p, n);
                 each = steps_of(s, tp);
-                if (x < before + each * p.Hk) break;
-                before += each * p.Hk;
+                if (x < base + each * p.Hk) break;
+                base += each * p.Hk;
             }
-        *found = Found{x - before, each, n, s};
+        found[e] = Found{x - base, each, n, s};
     }
     __syncthreads();
-    u.n = found->n;
-    u.s = found->s;
-    // the key head and the step within it; then the last pair that starts at or before that step:
-    // every thread tries some of them
-    int64_t at = found->at;
-    each = found->each;
-    u.kh = (int)((float)at / (float)each);   // (within one of the quotient, which is below 2^16)
-    at -= u.kh * each;
-    if (at < 0) --u.kh, at += each;
-    else if (at >= each) ++u.kh, at -= each;
-    int lo = 0, width = pairs_of(u.s, tp);
-    int64_t start = 0;
+    // half of the threads for each end: the key head and the step within it; then the last pair that
+    // starts at or before that step, of which every thread tries some
+    const int e = tid >= AT_THREADS / 2;
+    const bool open = e && x1 >= total;   // the last share's end needs no search
+    const Found f = found[open ? 0 : e];
+    Cursor u;
+    u.n = f.n;
+    u.s = f.s;
+    int64_t at = f.at;
+    u.kh = (int)((float)at / (float)f.each);   // (within one of the quotient, which is below 2^16)
+    at -= u.kh * f.each;
+    if (at < 0) --u.kh, at += f.each;
+    else if (at >= f.each) ++u.kh, at -= f.each;
+    int lo = 0, width = open ? 1 : pairs_of(u.s, tp);
 #pragma unroll 1
-    while (width > 1) {   // narrow [lo, lo + width)
-        const int step = (width + AT_THREADS - 1) / AT_THREADS, c = lo + tid * step;
-        const int64_t st = c < lo + width ? steps_before(u.s.lq, u.s.lk, c, tp) : at + 1;
-        if (st <= at) atomicMax(best, c);
+    while (__syncthreads_or(width > 1)) {   // narrow [lo, lo + width)
+        const int step = (width + AT_THREADS / 2 - 1) / (AT_THREADS / 2), c = lo + (tid % (AT_THREADS / 2)) * step;
+        const int64_t st = width > 1 && c < lo + width ? steps_before(u.s.lq, u.s.lk, c, tp) : at + 1;
+        if (st <= at) atomicMax(best + e, c);
         __syncthreads();
-        const int b = *best;
-        if (c == b && st <= at) scratch[17] = st;
-        __syncthreads();
-        start = scratch[17];
-        width = min(step, lo + width - b);
-        lo = b;
+        const int b = best[e];
+        if (c == b && st <= at) start[e] = st;
+        if (width > 1) width = min(step, lo + width - b), lo = b;
     }
     u.pair = lo;
-    u.j = (int)(at - start);
-    return u;
+    u.j = open ? 0 : (int)(at - start[e]);
+    // A cut near the end of a pair moves there: a pair that is cut costs its rows' partial results,
+    // written and read again (about six steps' time for 256 rows).  Both neighbours find the same.
+    int64_t x = e ? x1 : x0;
+    const int nb = blocks_seen(u.s, (u.pair + 1) * tp), near = 6 * min(min(u.s.lq - u.pair * tp, tp) * G, 256) >> 8;
+    bool over = false;
+    if (u.j > 0 && !open) {
+        if (u.j <= near && u.j <= nb - u.j) x -= u.j, u.j = 0;
+        else if (nb - u.j <= near) x += nb - u.j, over = true;
+    }
+    if (over) {   // the next pair
+        u.j = 0;
+        if (++u.pair == pairs_of(u.s, tp)) {
+            u.pair = 0;
+            if (++u.kh == p.Hk) {
+                u.kh = 0;
+                while (++u.n < p.nseq) {
+                    u.s = seq_of(p, u.n);
+                    if (u.s.lq > 0) break;
+                }
+            }
+        }
+    }
+    __syncthreads();
+    Cursor* place = reinterpret_cast<Cursor*>(scratch + 20);
+    if (tid == 0) *place = u, start[0] = x;
+    if (tid == AT_THREADS / 2) start[1] = x;
+    __syncthreads();
+    r.at = *place;
+    r.steps = start[1] - start[0];
+    return r;
 }
 
 // A share's next piece: the blocks [j0, j1) of one pair.
@@ -607,25 +643,20 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const AttnParams p,
         tmem_relinquish();
     }
     tc_fence_before();
-    int64_t total, x0 = 0;
-    bool bad;
-    const Cursor u = find_step(p, x.tp, reinterpret_cast<int64_t*>(smem_raw), total, bad, [&](int64_t tot) {
-        x0 = share_start(tot, blockIdx.x, gridDim.x, recip);
-        return x0;
-    });
+    const Share share = find_share(p, x.tq, x.G, recip, reinterpret_cast<int64_t*>(smem_raw));
+    const Cursor u = share.at;
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = lds_u32(x.base + OFF_TMEM);
     const bool sound = tmem == 0 && x.base % 1024 == 0;   // (the tiles' swizzle counts from 1 KB boundaries)
-    x.steps = share_start(total, blockIdx.x + 1, gridDim.x, recip) - x0;
+    x.steps = sound ? share.steps : 0;                    // (bad lengths have none)
     if (tid == 0) {
-        if (blockIdx.x == 0) *p.status = bad ? KDA_DEVERR_CU_SEQLENS : 0u;
+        if (blockIdx.x == 0) *p.status = share.bad ? KDA_DEVERR_CU_SEQLENS : 0u;
         if (!sound) atomicOr(p.status, KDA_DEVERR_INTERNAL);
         Cut c{};
         if (x.steps > 0) c = Cut{u.j, blocks_seen(u.s, (u.pair + 1) * x.tp), u.s.q0, u.s.lq, u.kh, u.pair, {0, 0}};
         partials(p.workspace).cut[blockIdx.x] = c;
     }
-    if (bad || !sound) x.steps = 0;   // (bad lengths have no steps anyway)
     bool ok = true;
     // registers a thread: 168 at launch; 208 + 208 + 88 of the 3 x 168 that the block holds
     if (warp < 8) {
@@ -700,15 +731,24 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParam
             l = fmaf(l, old, w * ml.y);
             o.x *= old, o.y *= old, o.z *= old, o.w *= old;
             const int n = min(32, end - s0);
-#pragma unroll 4
-            for (int a = 0; a < n; ++a) {
-                const float f = __shfl_sync(0xffffffffu, w, a);
-                if (f == 0.f) continue;   // (the rows of a part that saw no key may not even be written)
-                const float4 y = __ldcg(part.o + (slot(s0 + a) * 32 + lane) * 256 + row);
-                o.x = fmaf(f, y.x, o.x);
-                o.y = fmaf(f, y.y, o.y);
-                o.z = fmaf(f, y.z, o.z);
-                o.w = fmaf(f, y.w, o.w);
+#pragma unroll 1
+            for (int a = 0; a < n; a += 4) {
+                float4 y[4];
+                float f[4];
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {   // (the rows of a part that saw no key may not even be written)
+                    f[d] = __shfl_sync(0xffffffffu, w, (a + d) & 31);
+                    if (a + d >= n) f[d] = 0.f;
+                    y[d] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (f[d] != 0.f) y[d] = __ldcg(part.o + (slot(s0 + a + d) * 32 + lane) * 256 + row);
+                }
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    o.x = fmaf(f[d], y[d].x, o.x);
+                    o.y = fmaf(f[d], y[d].y, o.y);
+                    o.z = fmaf(f[d], y[d].z, o.z);
+                    o.w = fmaf(f[d], y[d].w, o.w);
+                }
             }
         }
 #pragma unroll 1
