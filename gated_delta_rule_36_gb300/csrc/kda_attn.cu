@@ -732,18 +732,18 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParam
             o.x *= old, o.y *= old, o.z *= old, o.w *= old;
             const int n = min(32, end - s0);
 #pragma unroll 1
-            for (int a = 0; a < n; a += 4) {
-                float4 y[4];
-                float f[4];
+            for (int a = 0; a < n; a += 8) {
+                float4 y[8];
+                float f[8];
 #pragma unroll
-                for (int d = 0; d < 4; ++d) {   // (the rows of a part that saw no key may not even be written)
+                for (int d = 0; d < 8; ++d) {   // (the rows of a part that saw no key may not even be written)
                     f[d] = __shfl_sync(0xffffffffu, w, (a + d) & 31);
                     if (a + d >= n) f[d] = 0.f;
                     y[d] = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (f[d] != 0.f) y[d] = __ldcg(part.o + (slot(s0 + a + d) * 32 + lane) * 256 + row);
                 }
 #pragma unroll
-                for (int d = 0; d < 4; ++d) {
+                for (int d = 0; d < 8; ++d) {
                     o.x = fmaf(f[d], y[d].x, o.x);
                     o.y = fmaf(f[d], y[d].y, o.y);
                     o.z = fmaf(f[d], y[d].z, o.z);

@@ -46,7 +46,7 @@ enum { FQ = 0, FK = 2, FV = 4, EQ = 6, EK = 8, EV = 10, KPF = 12, KPE = 14, VR =
 constexpr uint32_t OFF_TMEM = OFF_BAR + NBAR * 8;
 constexpr uint32_t LF_SMEM = OFF_TMEM + 8;   // no room to align the base: it has to be (and is checked to be) 1 KB aligned
 static_assert(LF_SMEM <= 232448, "one CTA's shared memory");
-// Tensor Memory columns: W then P; KV; O; two slots of K' (32 tokens: three terms of 16 columns)
+// Tensor Memory columns (all are allocated, so that its address is 0): W then P; KV; O; two slots of K' (32 tokens: three terms of 16 columns)
 constexpr uint32_t TM_W = 0, TM_KV = 128, TM_O = 256, TM_KP = 384, KP_SLOT = 48;
 
 struct LinMaps {
@@ -166,7 +166,7 @@ __device__ Share find_share(const LinParams& p, int64_t* scratch /* 32 */) {
 }
 
 struct Ctx {
-    uint32_t base, tmem;   // shared-window address; Tensor Memory address
+    uint32_t base;         // shared-window address
     int count;             // chunks to do (a GPU's memory holds fewer than 2^31 in all)
     __device__ uint32_t bar(int b) const { return base + OFF_BAR + 8u * b; }
     __device__ bool wait(int b, int use) const { return mx_wait(bar(b), (uint32_t)use & 1u); }
@@ -204,88 +204,80 @@ constexpr uint32_t ID_KK = make_idesc_bf16_f32(128, 128);          // both opera
 constexpr uint32_t ID_MN = make_idesc_bf16_f32(128, 128, true);    // B MN-major
 
 // the MMAs in flight finish before the CTA frees Tensor Memory
-__device__ __forceinline__ bool drain_mma(const Ctx& x, int bar) {
+__device__ __forceinline__ bool drain_mma(const Ctx& x, uint32_t lead, int bar) {
     __syncwarp();
-    tc_commit_warp(x.bar(bar));
+    mx_commit(lead, x.bar(bar));
     return x.wait(bar, 0);
 }
 
 __device__ bool mma_out_warp(const Ctx& x) {
-    const uint32_t tm = x.tmem;
-    bool ok = true;
+    const uint32_t lead = mx_leader();
+    const int count = mx_uniform(x.count);
     const uint64_t dQ = make_sdesc_kmajor_sw128(x.base), dS = make_sdesc_mnmajor_sw128(x.base + OFF_S, HALF, 1024);
-    for (int i = 0; i < x.count; ++i) {
+    const uint64_t dV = make_sdesc_mnmajor_sw128(x.base + 2 * TILE, HALF, 1024);
+    bool ok = true;
+    for (int i = 0; i < count; ++i) {
         const int s = i & 1;
-        const int use = i >> 1;
-        const uint64_t q = dQ + s * D_STAGE, k = q + (TILE >> 4);
+        const uint32_t use = (uint32_t)i >> 1, par = i & 1;
+        const uint64_t q = dQ + s * D_STAGE, k = q + (TILE >> 4), v = dV + s * D_STAGE;
         // W = Q K^T, over the P that the previous chunk's product has read
-        ok = (i == 0 || x.wait(OF, i - 1)) && x.wait(FK + s, use) && x.wait(FQ + s, use);
+        ok = mx_wait_lane(x.bar(FK + s), use & 1u) && mx_wait_lane(x.bar(FQ + s), use & 1u) && (i == 0 || mx_wait_lane(x.bar(OF), par ^ 1u));
         if (!ok) break;
         tc_fence_after();
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half)
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-                tc_mma_ss_warp(tm + TM_W, q + half * K_HALF + kk * K_STEP, k + half * K_HALF + kk * K_STEP, ID_KK, half + kk > 0);
-        tc_commit_warp(x.bar(WF));
-        tc_commit_warp(x.bar(EK + s));
+        for (int kk = 0; kk < 8; ++kk)
+            mx_mma_ss(lead, TM_W, q + (kk >> 2) * K_HALF + (kk & 3) * K_STEP, k + (kk >> 2) * K_HALF + (kk & 3) * K_STEP, ID_KK, kk > 0);
+        mx_commit(lead, x.bar(WF));
+        mx_commit(lead, x.bar(EK + s));
         // O = Q S, once the state is in shared memory and the previous O has been read
-        ok = x.wait(SB, i) && (i == 0 || x.wait(OE, i - 1));
+        ok = mx_wait_lane(x.bar(SB), par) && (i == 0 || mx_wait_lane(x.bar(OE), par ^ 1u));
         if (!ok) break;
         tc_fence_after();
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half)
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-                tc_mma_ss_warp(tm + TM_O, q + half * K_HALF + kk * K_STEP, dS + (4 * half + kk) * MN_STEP, ID_MN, half + kk > 0);
-        tc_commit_warp(x.bar(QSF));
+        for (int kk = 0; kk < 8; ++kk)
+            mx_mma_ss(lead, TM_O, q + (kk >> 2) * K_HALF + (kk & 3) * K_STEP, dS + kk * MN_STEP, ID_MN, kk > 0);
+        mx_commit(lead, x.bar(QSF));
         // O += P V
-        ok = x.wait(VR + s, use) && x.wait(PF, i) && x.wait(OS, i);
+        ok = mx_wait_lane(x.bar(VR + s), use & 1u) && mx_wait_lane(x.bar(PF), par) && mx_wait_lane(x.bar(OS), par);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t v = make_sdesc_mnmajor_sw128(x.base + s * STAGE + 2 * TILE, HALF, 1024);
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half)
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-                tc_mma_ts_warp(tm + TM_O, tm + TM_W + (4 * half + kk) * 8, v + (4 * half + kk) * MN_STEP, ID_MN, 1u);
-        tc_commit_warp(x.bar(OF));
-        tc_commit_warp(x.bar(EV + s));
+        for (int kk = 0; kk < 8; ++kk) mx_mma_ts(lead, TM_O, TM_W + kk * 8, v + kk * MN_STEP, ID_MN, 1u);
+        mx_commit(lead, x.bar(OF));
+        mx_commit(lead, x.bar(EV + s));
     }
-    return drain_mma(x, DRAIN) && ok;
+    return drain_mma(x, lead, DRAIN) && ok;
 }
 
 // KV = K'^T V, 32 tokens at a time as the key warps hand them over
 __device__ bool mma_state_warp(const Ctx& x) {
-    const uint32_t tm = x.tmem;
+    const uint32_t lead = mx_leader();
+    const int count = mx_uniform(x.count);
+    const uint64_t dV = make_sdesc_mnmajor_sw128(x.base + 2 * TILE, HALF, 1024);
     bool ok = true;
-    for (int i = 0; i < x.count; ++i) {
+    for (int i = 0; i < count; ++i) {
         const int s = i & 1;
-        const uint64_t v = make_sdesc_mnmajor_sw128(x.base + s * STAGE + 2 * TILE, HALF, 1024);
-        ok = x.wait(VR + s, i >> 1) && (i == 0 || x.wait(KVE, i - 1));
+        ok = mx_wait_lane(x.bar(VR + s), (uint32_t)(i >> 1) & 1u) && (i == 0 || mx_wait_lane(x.bar(KVE), (uint32_t)(i - 1) & 1u));
         if (!ok) break;
-
-#pragma unroll 1
+#pragma unroll
         for (int b = 0; b < 4; ++b) {
             const int slot = b & 1;
-            ok = x.wait(KPF + slot, 2 * i + (b >> 1));
+            ok = ok && mx_wait_lane(x.bar(KPF + slot), (uint32_t)(b >> 1));
             if (!ok) break;
             tc_fence_after();
-            const uint32_t a = tm + TM_KP + slot * KP_SLOT;
-            const uint64_t vb = v + 2 * b * MN_STEP;
+            const uint64_t v = dV + s * D_STAGE + 2 * b * MN_STEP;
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                tc_mma_ts_warp(tm + TM_KV, a + 8 * kk, vb + kk * MN_STEP, ID_MN, b + kk > 0);
-                tc_mma_ts_warp(tm + TM_KV, a + 16 + 8 * kk, vb + kk * MN_STEP, ID_MN, 1u);
-                tc_mma_ts_warp(tm + TM_KV, a + 32 + 8 * kk, vb + kk * MN_STEP, ID_MN, 1u);
-            }
-            tc_commit_warp(x.bar(KPE + slot));
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int term = 0; term < 3; ++term)
+                    mx_mma_ts(lead, TM_KV, TM_KP + slot * KP_SLOT + term * 16 + 8 * kk, v + kk * MN_STEP, ID_MN, b + kk + term > 0);
+            mx_commit(lead, x.bar(KPE + slot));
         }
         if (!ok) break;
-        tc_commit_warp(x.bar(KVF));
-        tc_commit_warp(x.bar(EV + s));
+        mx_commit(lead, x.bar(KVF));
+        mx_commit(lead, x.bar(EV + s));
     }
-    return drain_mma(x, DRAIN2) && ok;
+    return drain_mma(x, lead, DRAIN2) && ok;
 }
 
 // ---------------------------------------------------------------- warps 0-3: P and the scale of O
@@ -316,7 +308,7 @@ __device__ bool score_warps(const LinParams& p, const Ctx& x, Cursor u) {
         uint32_t w[32], y[16];
 #pragma unroll 1
         for (int b = 0; b < warp; ++b) {
-            tmem_ld32(x.tmem + lanes + TM_W + 32 * b, w);
+            tmem_ld32(lanes + TM_W + 32 * b, w);
             const int e = warp - 1 - b;
             const float f = e == 0 ? left : e == 1 ? left * hop : left * hop * hop;
             const float2 f2 = make_float2(f, f);
@@ -329,9 +321,9 @@ __device__ bool score_warps(const LinParams& p, const Ctx& x, Cursor u) {
                 y[j / 2] = pack_bf16x2(y0.x, y0.y);
                 y[j / 2 + 1] = pack_bf16x2(y1.x, y1.y);
             }
-            tmem_st16(x.tmem + lanes + TM_W + 16 * b, y);
+            tmem_st16(lanes + TM_W + 16 * b, y);
         }
-        tmem_ld32(x.tmem + lanes + TM_W + 32 * warp, w);
+        tmem_ld32(lanes + TM_W + 32 * warp, w);
         tmem_wait_ld();
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {   // a^(lane - j) is power 31 - lane + j of the table, zeros follow
@@ -339,11 +331,11 @@ __device__ bool score_warps(const LinParams& p, const Ctx& x, Cursor u) {
             const float a1 = mx_u2f(w[j + 1]) * (p.scale * lds_f32(pow + 4 * (32 + j) - 4 * lane));
             y[j / 2] = pack_bf16x2(j <= lane ? a0 : 0.f, j < lane ? a1 : 0.f);   // whatever W holds there
         }
-        tmem_st16(x.tmem + lanes + TM_W + 16 * warp, y);
+        tmem_st16(lanes + TM_W + 16 * warp, y);
 #pragma unroll
         for (int j = 0; j < 16; ++j) y[j] = 0u;
 #pragma unroll 1
-        for (int b = warp + 1; b < 4; ++b) tmem_st16(x.tmem + lanes + TM_W + 16 * b, y);
+        for (int b = warp + 1; b < 4; ++b) tmem_st16(lanes + TM_W + 16 * b, y);
         tmem_wait_st();
         tc_fence_before();
         mx_arrive_warp(x.bar(PF));
@@ -354,7 +346,7 @@ __device__ bool score_warps(const LinParams& p, const Ctx& x, Cursor u) {
 #pragma unroll 1
         for (int b = 0; b < 4; ++b) {
             uint32_t w[32];
-            tmem_ld32(x.tmem + lanes + TM_O + 32 * b, w);
+            tmem_ld32(lanes + TM_O + 32 * b, w);
             tmem_wait_ld();
 #pragma unroll
             for (int j = 0; j < 32; j += 2) {
@@ -362,7 +354,7 @@ __device__ bool score_warps(const LinParams& p, const Ctx& x, Cursor u) {
                 w[j] = __float_as_uint(y.x);
                 w[j + 1] = __float_as_uint(y.y);
             }
-            tmem_st32(x.tmem + lanes + TM_O + 32 * b, w);
+            tmem_st32(lanes + TM_O + 32 * b, w);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -390,7 +382,7 @@ __device__ bool out_warps(const LinParams& p, const LinMaps& maps, const Ctx& x,
 #pragma unroll 1
         for (int b = 0; b < 4; ++b) {
             uint32_t w[32];
-            tmem_ld32(x.tmem + lanes + TM_O + 32 * b, w);
+            tmem_ld32(lanes + TM_O + 32 * b, w);
             tmem_wait_ld();
             uint32_t o[16];
 #pragma unroll
@@ -497,7 +489,7 @@ __device__ bool state_warps(const LinParams& p, const Ctx& x, Cursor u, const Sh
 #pragma unroll
         for (int b = 0; b < 8; ++b) {
             uint32_t w[16];
-            tmem_ld16(x.tmem + lanes + TM_KV + 16 * b, w);
+            tmem_ld16(lanes + TM_KV + 16 * b, w);
             tmem_wait_ld();
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -547,7 +539,7 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) { return make_float2(bf16_
 
 __device__ bool key_warps(const LinParams& p, const Ctx& x, Cursor u, int g) {
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, k = threadIdx.x & 127;
-    const uint32_t kp = x.tmem + ((uint32_t)(32 * warp) << 16) + TM_KP + g * KP_SLOT;
+    const uint32_t kp = ((uint32_t)(32 * warp) << 16) + TM_KP + g * KP_SLOT;
     const uint32_t pow = x.base + OFF_KPOW + (4 * g + warp) * 128;
     const int kc = (k >> 3) & 7;
     const float2 minus = make_float2(-1.f, -1.f);
@@ -663,7 +655,7 @@ __device__ void empty_units(const LinParams& p) {
 template <bool kStateOnly>
 __global__ void __launch_bounds__(LF_THREADS, 1) lin_fwd_kernel(const LinParams p, const __grid_constant__ LinMaps maps) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    const int tid = threadIdx.x, warp = tid >> 5;
+    const int tid = threadIdx.x, warp = mx_uniform(tid >> 5);
     Ctx x;
     x.base = smem_u32(smem_raw);
     Share share = find_share<kStateOnly>(p, reinterpret_cast<int64_t*>(smem_raw + OFF_S));
@@ -705,7 +697,11 @@ __global__ void __launch_bounds__(LF_THREADS, 1) lin_fwd_kernel(const LinParams 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    x.tmem = lds_u32(x.base + OFF_TMEM);
+    const uint32_t tmem = lds_u32(x.base + OFF_TMEM);   // all 512 columns: 0
+    if (tmem != 0) {
+        if (tid == 0) atomicOr(p.status, KDA_DEVERR_INTERNAL);
+        x.count = 0;
+    }
     // registers a thread: 80 at launch; 64 + 56 + 168 + 72 + 72 + 48 of the 6 x 80 that the block holds
     bool ok = true;
     if (warp < 4) {
@@ -731,7 +727,7 @@ __global__ void __launch_bounds__(LF_THREADS, 1) lin_fwd_kernel(const LinParams 
     __syncthreads();
     if (warp == 0) {
         tc_fence_after();
-        tmem_dealloc(x.tmem, 512);
+        tmem_dealloc(tmem, 512);
     }
 }
 
