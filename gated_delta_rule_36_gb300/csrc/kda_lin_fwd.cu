@@ -13,9 +13,12 @@
 // every step).  Its bf16 copy in shared memory is O's operand only.
 //
 // One persistent CTA per SM takes an equal, contiguous share of all chunks of all (sequence,
-// head) units.  A share that starts inside a unit needs the state before it: a first launch
-// (kStateOnly) sums v k^T over the share ends that a later share continues, and the second
-// starts from their decayed sum.
+// head) units, in the order (n, h, c).  A share that starts inside a unit needs the state before
+// it.  Where the unit lies in two shares, the first one takes its part of that unit first of all
+// and publishes the state, and the second one takes its part last of all, when the state has
+// long been there: no chunk is read twice and nobody waits.  Units that lie in more than two
+// shares (few heads, long prompts) would make a chain of waits; for them a first launch
+// (kStateOnly) sums v k^T over each share's part, and the second starts from their decayed sum.
 //
 // Warp roles: warps 0-3 turn W into P and scale O (thread = token row); warps 4-7 write the
 // output out; warps 8-11 carry the state (thread = key channel); warps 12-15 and 16-19 make K',
@@ -43,8 +46,8 @@ constexpr uint32_t OFF_S = 2 * STAGE;
 constexpr uint32_t OFF_POW = OFF_S + TILE, OFF_KPOW = OFF_POW + 4 * 256;
 constexpr uint32_t OFF_BAR = OFF_KPOW + 8 * 128;
 enum { FQ = 0, FK = 2, FV = 4, EQ = 6, EK = 8, EV = 10, KPF = 12, KPE = 14, VR = 16, WF = 18, PF, QSF, OS, OF, OE, KVF, KVE, SB, DRAIN, DRAIN2, NBAR };
-constexpr uint32_t OFF_TMEM = OFF_BAR + NBAR * 8;
-constexpr uint32_t LF_SMEM = OFF_TMEM + 8;   // no room to align the base: it has to be (and is checked to be) 1 KB aligned
+constexpr uint32_t OFF_TMEM = OFF_BAR + NBAR * 8, OFF_SEG = OFF_TMEM + 8;
+constexpr uint32_t LF_SMEM = OFF_SEG + 3 * 24;   // no room to align the base: it has to be (and is checked to be) 1 KB aligned
 static_assert(LF_SMEM <= 232448, "one CTA's shared memory");
 // Tensor Memory columns (all are allocated, so that its address is 0): W then P; KV; O; two slots of K' (32 tokens: three terms of 16 columns)
 constexpr uint32_t TM_W = 0, TM_KV = 128, TM_O = 256, TM_KP = 384, KP_SLOT = 48;
@@ -93,90 +96,122 @@ __device__ __forceinline__ float log2_decay(const LinParams& p, int h) {
     return d < -1e30f ? -1e30f : d;
 }
 
-struct Share {
-    int64_t total, x0, x1;   // chunks of the whole batch; this CTA's share
-    Cursor at;               // where it starts
-    bool bad;                // cu_seqlens do not describe the tokens
-};
-
-__device__ __forceinline__ int64_t share_start(int64_t total, int b, int ctas) {
-    return total / ctas * b + total % ctas * b / ctas;
+// Where share b of `ctas` equal ones starts (recip = 2^64 / ctas, rounded up: no division).
+__device__ __forceinline__ int64_t share_start(int64_t total, int b, int ctas, uint64_t recip) {
+    return b >= ctas ? total : b <= 0 ? 0 : (int64_t)__umul64hi((uint64_t)total * (uint64_t)b, recip);
 }
 
-// The whole CTA: checks cu_seqlens, counts the chunks and finds the chunk `x0` (of the share's
-// start, or with kEnd of its end) among the units in the order (n, h, c).
-template <bool kEnd>
-__device__ Share find_share(const LinParams& p, int64_t* scratch /* 32 */) {
+struct Share {
+    int64_t total, x0, x1;   // chunks of the whole batch; this share's
+    Cursor first, end;    // the chunk x0; the chunk x1 (if there is one)
+    bool bad;             // cu_seqlens do not describe the tokens
+    bool head, tail;      // x0 / x1 lies inside a unit that has no other share than the two there
+    bool cut;             // x1 lies inside a unit
+    bool empties;         // there are sequences of no tokens
+};
+
+// The whole CTA: checks cu_seqlens, counts the chunks and finds the share's ends.  Every CTA
+// starts with this: one pass over the lengths and two block-wide exchanges.
+__device__ Share find_share(const LinParams& p, uint64_t recip, int64_t* scratch /* 48 */) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (p.nseq + LF_THREADS - 1) / LF_THREADS;
     const int n0 = min(tid * per, p.nseq), n1 = min(n0 + per, p.nseq);
+    Cursor u{};
     int64_t mine = 0;
-    bool bad = false;
+    int what = 0;   // 1: bad, 2: a sequence of no tokens
+#pragma unroll 1
     for (int n = n0; n < n1; ++n) {
-        int bos, len;
-        seq_of(p, n, bos, len);
-        if (p.cu_seqlens) bad |= p.cu_seqlens[n + 1] < p.cu_seqlens[n];
-        mine += (len + LF_C - 1) / LF_C;
+        // nondecreasing from 0 to at most T_total: every entry is then in range
+        if (p.cu_seqlens && (p.cu_seqlens[n + 1] < p.cu_seqlens[n] || (n == 0 && p.cu_seqlens[0] != 0) ||
+                             (n + 1 == p.nseq && p.cu_seqlens[n + 1] > p.T_total)))
+            what |= 1;
+        seq_of(p, n, u.bos, u.len);
+        u.n = n;
+        u.nc = (u.len + LF_C - 1) / LF_C;
+        if (u.len == 0) what |= 2;
+        mine += u.nc;
     }
-    // nondecreasing from 0 to at most T_total: every entry is then in range
-    if (tid == 0 && p.cu_seqlens) bad |= p.cu_seqlens[0] != 0 || p.cu_seqlens[p.nseq] > p.T_total;
     int64_t sum = mine;
-#pragma unroll
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
         const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
         if (lane >= o) sum += y;
     }
     if (lane == 31) scratch[warp] = sum;
-    bad = __syncthreads_or(bad);
-    int64_t before = 0, all = 0;
-#pragma unroll
+    Share s{};
+    s.bad = __syncthreads_or(what & 1);
+    if (s.bad) return s;
+    s.empties = __syncthreads_or(what & 2);
+    int64_t before = sum - mine, all = 0;
+#pragma unroll 1
     for (int w = 0; w < LF_THREADS / 32; ++w) {
         before += w < warp ? scratch[w] : 0;
         all += scratch[w];
     }
-    before += sum - mine;
-    Share s;
-    s.bad = bad;
-    s.total = bad ? 0 : all * p.H;
-    s.x0 = share_start(s.total, blockIdx.x, gridDim.x);
-    s.x1 = share_start(s.total, blockIdx.x + 1, gridDim.x);
-    const int64_t x = kEnd ? s.x1 : s.x0;
-    __syncthreads();
-    Cursor* out = reinterpret_cast<Cursor*>(scratch);
-    if (!bad && mine > 0 && x >= before * p.H && x < (before + mine) * p.H) {
-        int64_t base = before * p.H;
-        for (int n = n0; n < n1; ++n) {
-            Cursor u;
-            u.n = n;
-            seq_of(p, n, u.bos, u.len);
-            u.nc = (u.len + LF_C - 1) / LF_C;
-            if (x < base + (int64_t)u.nc * p.H) {
-                u.h = (int)((x - base) / u.nc);
-                u.c = (int)((x - base) % u.nc);
-                *out = u;
-                break;
+    const int64_t total = s.total = all * p.H;
+    const int b = blockIdx.x, ctas = gridDim.x;
+    s.x0 = share_start(total, b, ctas, recip);
+    s.x1 = share_start(total, b + 1, ctas, recip);
+    Cursor* place = reinterpret_cast<Cursor*>(scratch + 24);   // [2]
+#pragma unroll 1
+    for (int e = 0; e < 2; ++e) {
+        int64_t at = (e ? s.x1 : s.x0) - before * p.H;
+        if (at < 0 || at >= mine * p.H) continue;
+        if (n1 - n0 > 1)
+            for (u.n = n0;; ++u.n) {
+                seq_of(p, u.n, u.bos, u.len);
+                u.nc = (u.len + LF_C - 1) / LF_C;
+                if (at < (int64_t)u.nc * p.H) break;
+                at -= (int64_t)u.nc * p.H;
             }
-            base += (int64_t)u.nc * p.H;
-        }
+        u.h = (int)((float)at / (float)u.nc);   // (within one of the quotient, which is below 2^16)
+        at -= (int64_t)u.h * u.nc;
+        if (at < 0) --u.h, at += u.nc;
+        else if (at >= u.nc) ++u.h, at -= u.nc;
+        u.c = (int)at;
+        place[e] = u;
     }
     __syncthreads();
-    s.at = *out;
+    s.first = place[0];
+    s.end = place[1];
     __syncthreads();
+    s.cut = s.x1 < total && s.x1 > s.x0 && s.end.c > 0;
+    const int64_t eu = s.x1 - s.end.c, su = s.x0 - s.first.c;   // where the units there start
+    s.tail = s.cut && eu >= s.x0 && eu + s.end.nc <= share_start(total, b + 2, ctas, recip);
+    s.head = s.x1 > s.x0 && s.first.c > 0 && su >= share_start(total, b - 1, ctas, recip) && su + s.first.nc <= s.x1;
     return s;
 }
 
 struct Ctx {
     uint32_t base;         // shared-window address
     int count;             // chunks to do (a GPU's memory holds fewer than 2^31 in all)
+    // in this order: nA chunks of the unit that the next share ends, then up to nAB, then the rest of
+    // the unit that the share before began
+    int nA, nAB;
+    const Cursor* seg;     // where the three parts start (in shared memory)
     __device__ uint32_t bar(int b) const { return base + OFF_BAR + 8u * b; }
     __device__ bool wait(int b, int use) const { return mx_wait(bar(b), (uint32_t)use & 1u); }
 };
 
+__device__ __forceinline__ Cursor first_chunk(const Ctx& x) { return x.seg[x.nA > 0 ? 0 : x.nAB > 0 ? 1 : 2]; }
+// From chunk i of the share to chunk i + 1.
+__device__ __forceinline__ void advance(const LinParams& p, const Ctx& x, Cursor& u, int i) {
+    if (i + 1 == x.nA || i + 1 == x.nAB) u = x.seg[i + 1 < x.nAB ? 1 : 2];
+    else next_chunk(p, u);
+}
+
+// Workspace: a partial or published state for each share, then a flag for each.
+__device__ __forceinline__ float* share_state(const LinParams& p, int b) { return static_cast<float*>(p.workspace) + (size_t)b * HD * HD; }
+__device__ __forceinline__ uint32_t* share_flag(const LinParams& p, int b) {
+    return reinterpret_cast<uint32_t*>(static_cast<float*>(p.workspace) + (size_t)LF_MAX_CTAS * HD * HD) + b;
+}
+
 // ---------------------------------------------------------------- warp 20: loads
 template <bool kStateOnly>
-__device__ bool load_warp(const LinParams& p, const LinMaps& maps, const Ctx& x, Cursor u) {
+__device__ bool load_warp(const LinParams& p, const LinMaps& maps, const Ctx& x) {
     bool ok = true;
     if ((threadIdx.x & 31) == 0) {
+        Cursor u = first_chunk(x);
         auto one = [&](int i, int full, int empty, const CUtensorMap* m, uint32_t off) {
             const int s = i & 1;
             if (i >= 2 && !mx_wait_lane(x.bar(empty + s), (uint32_t)((i >> 1) - 1) & 1u)) return false;
@@ -187,7 +222,7 @@ __device__ bool load_warp(const LinParams& p, const LinMaps& maps, const Ctx& x,
             tma_load_4d(dst + HALF, m, 64, u.h, t0, 0, x.bar(full + s));
             return true;
         };
-        for (int i = 0; i < x.count && ok; ++i, next_chunk(p, u)) {
+        for (int i = 0; i < x.count && ok; advance(p, x, u, i), ++i) {
             ok = one(i, FK, EK, &maps.k, TILE);
             if (!kStateOnly) ok = ok && one(i, FQ, EQ, &maps.q, 0);
             ok = ok && one(i, FV, EV, &maps.v, 2 * TILE);
@@ -281,14 +316,15 @@ __device__ bool mma_state_warp(const Ctx& x) {
 }
 
 // ---------------------------------------------------------------- warps 0-3: P and the scale of O
-__device__ bool score_warps(const LinParams& p, const Ctx& x, Cursor u) {
+__device__ bool score_warps(const LinParams& p, const Ctx& x) {
+    Cursor u = first_chunk(x);
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(32 * warp) << 16;
     const uint32_t pow = x.base + OFF_POW + warp * 256;
     sts_f32(pow + 128 + 4 * lane, 0.f);
     float since = 0.f, left = 0.f, hop = 0.f;
     int h = -1;
-    for (int i = 0; i < x.count; ++i, next_chunk(p, u)) {
+    for (int i = 0; i < x.count; advance(p, x, u, i), ++i) {
         if (u.h != h) {
             h = u.h;
             const float l2 = log2_decay(p, h);
@@ -364,10 +400,11 @@ __device__ bool score_warps(const LinParams& p, const Ctx& x, Cursor u) {
 }
 
 // ---------------------------------------------------------------- warps 4-7: the output
-__device__ bool out_warps(const LinParams& p, const LinMaps& maps, const Ctx& x, Cursor u) {
+__device__ bool out_warps(const LinParams& p, const LinMaps& maps, const Ctx& x) {
+    Cursor u = first_chunk(x);
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(32 * warp) << 16;
-    for (int i = 0; i < x.count; ++i, next_chunk(p, u)) {
+    for (int i = 0; i < x.count; advance(p, x, u, i), ++i) {
         const int s = i & 1;
         const int valid = chunk_tokens(u);
         if (!x.wait(OF, i)) return false;
@@ -423,48 +460,64 @@ __device__ bool out_warps(const LinParams& p, const LinMaps& maps, const Ctx& x,
 // ---------------------------------------------------------------- warps 8-11: the state
 // Thread k holds S[k][0 .. 127] (column v).  Global states are [V][K]: the 32 lanes of a warp
 // read and write 32 neighbouring k of one v.
-__device__ __forceinline__ float state_at(const void* s, int f32, size_t off) {
-    return f32 ? __ldg(static_cast<const float*>(s) + off) : __bfloat162float(static_cast<const __nv_bfloat16*>(s)[off]);
+template <class T>
+__device__ __forceinline__ void load_state(const T* s, float2 (&S)[LF_C / 2]) {
+#pragma unroll
+    for (int v = 0; v < LF_C / 2; ++v) S[v] = make_float2((float)__ldg(s + (2 * v) * HD), (float)__ldg(s + (2 * v + 1) * HD));
 }
 
 template <bool kStateOnly>
-__device__ bool state_warps(const LinParams& p, const Ctx& x, Cursor u, const Share& share) {
-    const int warp = (threadIdx.x >> 5) & 3, k = threadIdx.x & 127;
+__device__ bool state_warps(const LinParams& p, const Ctx& x, const Share& share, uint64_t recip) {
+    Cursor u = first_chunk(x);
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, k = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(32 * warp) << 16;
     float2 S[LF_C / 2];
     float l2 = 0.f, all = 0.f;
-    bool fresh = true;   // a unit (or this share) starts
-    for (int i = 0; i < x.count; ++i, next_chunk(p, u)) {
+    bool fresh = true;   // a unit or a part of one starts
+    for (int i = 0; i < x.count; advance(p, x, u, i), ++i) {
         const int valid = chunk_tokens(u);
         const size_t unit = (size_t)u.n * p.H + u.h;
         if (fresh) {
             fresh = false;
             l2 = log2_decay(p, u.h);
             all = exp2f(l2 * (float)LF_C);
-            if (kStateOnly || p.init_state == nullptr) {
+            if (!kStateOnly && u.c > 0 && i >= x.nAB) {
+                // the share before published this unit's state: its four warps have arrived at its flag
+                const uint32_t* flag = share_flag(p, blockIdx.x - 1);
+                uint32_t seen = 0, polls = 0;
+                while (seen != 4 && ++polls < MX_POLLS) asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(flag) : "memory");
+                if (!__all_sync(0xffffffffu, seen == 4)) return false;
+                const float* s = share_state(p, blockIdx.x - 1) + k;
 #pragma unroll
-                for (int v = 0; v < LF_C / 2; ++v) S[v] = make_float2(0.f, 0.f);
+                for (int v = 0; v < LF_C / 2; ++v) S[v] = make_float2(__ldcg(s + (2 * v) * HD), __ldcg(s + (2 * v + 1) * HD));
             } else {
-                const float f = exp2f(l2 * (float)u.c * (float)LF_C);
                 const size_t off = unit * HD * HD + k;
+                if (kStateOnly || p.init_state == nullptr) {
 #pragma unroll
-                for (int v = 0; v < LF_C / 2; ++v)
-                    S[v] = make_float2(f * state_at(p.init_state, p.init_f32, off + (size_t)(2 * v) * HD),
-                                       f * state_at(p.init_state, p.init_f32, off + (size_t)(2 * v + 1) * HD));
-            }
-            if (!kStateOnly && u.c > 0) {
-                // the shares before this one that hold earlier chunks of the unit
-                const int64_t first = share.x0 - u.c;   // the unit's first chunk
-                for (int b = (int)blockIdx.x - 1; b >= 0; --b) {
-                    const int64_t end = share_start(share.total, b + 1, gridDim.x);
-                    if (end <= first) break;
-                    if (share_start(share.total, b, gridDim.x) == end) continue;
-                    const float g = exp2f(l2 * (float)(share.x0 - end) * (float)LF_C);
-                    const float* part = static_cast<const float*>(p.workspace) + (size_t)b * HD * HD + k;
+                    for (int v = 0; v < LF_C / 2; ++v) S[v] = make_float2(0.f, 0.f);
+                } else if (p.init_f32) {
+                    load_state(static_cast<const float*>(p.init_state) + off, S);
+                } else {
+                    load_state(static_cast<const __nv_bfloat16*>(p.init_state) + off, S);
+                }
+                if (!kStateOnly && u.c > 0) {
+                    // decayed to here, plus what the shares before this one summed over the unit's chunks
+                    const float f = exp2f(l2 * (float)u.c * (float)LF_C);
 #pragma unroll
-                    for (int v = 0; v < LF_C / 2; ++v) {
-                        S[v].x = fmaf(g, __ldg(part + (2 * v) * HD), S[v].x);
-                        S[v].y = fmaf(g, __ldg(part + (2 * v + 1) * HD), S[v].y);
+                    for (int v = 0; v < LF_C / 2; ++v) S[v].x *= f, S[v].y *= f;
+                    const int64_t begin = share.x0 - u.c;   // the unit's first chunk
+#pragma unroll 1
+                    for (int b = (int)blockIdx.x - 1; b >= 0; --b) {
+                        const int64_t end = share_start(share.total, b + 1, gridDim.x, recip);
+                        if (end <= begin) break;
+                        if (share_start(share.total, b, gridDim.x, recip) == end) continue;
+                        const float g = exp2f(l2 * (float)(share.x0 - end) * (float)LF_C);
+                        const float* part = share_state(p, b) + k;
+#pragma unroll
+                        for (int v = 0; v < LF_C / 2; ++v) {
+                            S[v].x = fmaf(g, __ldcg(part + (2 * v) * HD), S[v].x);
+                            S[v].y = fmaf(g, __ldcg(part + (2 * v + 1) * HD), S[v].y);
+                        }
                     }
                 }
             }
@@ -497,16 +550,21 @@ __device__ bool state_warps(const LinParams& p, const Ctx& x, Cursor u, const Sh
         }
         tc_fence_before();
         mx_arrive_warp(x.bar(KVE));
-        if (kStateOnly) {
-            if (i + 1 == x.count) {
-                float* part = static_cast<float*>(p.workspace) + (size_t)blockIdx.x * HD * HD + k;
+        if (kStateOnly ? i + 1 == x.count : i + 1 == x.nA) {
+            // this share's part of a unit that the next share goes on with
+            float* part = share_state(p, blockIdx.x) + k;
 #pragma unroll
-                for (int v = 0; v < LF_C / 2; ++v) {
-                    part[(2 * v) * HD] = S[v].x;
-                    part[(2 * v + 1) * HD] = S[v].y;
-                }
+            for (int v = 0; v < LF_C / 2; ++v) {
+                part[(2 * v) * HD] = S[v].x;
+                part[(2 * v + 1) * HD] = S[v].y;
             }
-        } else if (u.c + 1 == u.nc) {
+            if (!kStateOnly) {
+                __threadfence();
+                __syncwarp();
+                if (lane == 0) asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(share_flag(p, blockIdx.x)) : "memory");
+            }
+            fresh = true;
+        } else if (!kStateOnly && u.c + 1 == u.nc) {
             fresh = true;
             if (p.final_state) {
                 const size_t off = unit * HD * HD + k;
@@ -537,7 +595,8 @@ __device__ bool state_warps(const LinParams& p, const Ctx& x, Cursor u, const Sh
 // g and g + 2 of each chunk and owns slot g.
 __device__ __forceinline__ float2 unpack2(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
 
-__device__ bool key_warps(const LinParams& p, const Ctx& x, Cursor u, int g) {
+__device__ bool key_warps(const LinParams& p, const Ctx& x, int g) {
+    Cursor u = first_chunk(x);
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, k = threadIdx.x & 127;
     const uint32_t kp = ((uint32_t)(32 * warp) << 16) + TM_KP + g * KP_SLOT;
     const uint32_t pow = x.base + OFF_KPOW + (4 * g + warp) * 128;
@@ -545,7 +604,7 @@ __device__ bool key_warps(const LinParams& p, const Ctx& x, Cursor u, int g) {
     const float2 minus = make_float2(-1.f, -1.f);
     float l2 = 0.f, hop = 0.f;
     int h = -1;
-    for (int i = 0; i < x.count; ++i, next_chunk(p, u)) {
+    for (int i = 0; i < x.count; advance(p, x, u, i), ++i) {
         const int s = i & 1;
         const int valid = chunk_tokens(u);
         const bool full = valid == LF_C;
@@ -632,100 +691,103 @@ __device__ bool key_warps(const LinParams& p, const Ctx& x, Cursor u, int g) {
 // Units of no tokens: the final state is the initial one.
 __device__ void empty_units(const LinParams& p) {
     if (!p.final_state) return;
-    const int64_t units = (int64_t)p.nseq * p.H;
-    for (int64_t u0 = (int64_t)blockIdx.x * LF_THREADS; u0 < units; u0 += (int64_t)gridDim.x * LF_THREADS) {
-        for (int j = 0; j < LF_THREADS && u0 + j < units; ++j) {
-            const int64_t unit = u0 + j;
-            int bos, len;
-            seq_of(p, (int)(unit / p.H), bos, len);
-            if (len != 0) {   // on to the next sequence's first unit
-                j += (int)min((int64_t)LF_THREADS, p.H - 1 - unit % p.H);
-                continue;
-            }
-            for (int e = threadIdx.x; e < HD * HD; e += LF_THREADS) {
-                const size_t off = (size_t)unit * HD * HD + e;
-                const float v = p.init_state ? state_at(p.init_state, p.init_f32, off) : 0.f;
-                if (p.final_f32) static_cast<float*>(p.final_state)[off] = v;
-                else static_cast<__nv_bfloat16*>(p.final_state)[off] = __float2bfloat16_rn(v);
-            }
+    for (int n = blockIdx.x; n < p.nseq; n += gridDim.x) {
+        int bos, len;
+        seq_of(p, n, bos, len);
+        if (len != 0) continue;
+        for (size_t e = threadIdx.x; e < (size_t)p.H * HD * HD; e += LF_THREADS) {
+            const size_t off = (size_t)n * p.H * HD * HD + e;
+            const float v = !p.init_state ? 0.f : p.init_f32 ? static_cast<const float*>(p.init_state)[off]
+                                                             : __bfloat162float(static_cast<const __nv_bfloat16*>(p.init_state)[off]);
+            if (p.final_f32) static_cast<float*>(p.final_state)[off] = v;
+            else static_cast<__nv_bfloat16*>(p.final_state)[off] = __float2bfloat16_rn(v);
         }
     }
 }
 
 template <bool kStateOnly>
-__global__ void __launch_bounds__(LF_THREADS, 1) lin_fwd_kernel(const LinParams p, const __grid_constant__ LinMaps maps) {
+__global__ void __launch_bounds__(LF_THREADS, 1) lin_fwd_kernel(const LinParams p, const __grid_constant__ LinMaps maps, uint64_t recip) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const int tid = threadIdx.x, warp = mx_uniform(tid >> 5);
     Ctx x;
     x.base = smem_u32(smem_raw);
-    Share share = find_share<kStateOnly>(p, reinterpret_cast<int64_t*>(smem_raw + OFF_S));
-    if (!kStateOnly && blockIdx.x == 0 && tid == 0) *p.status = share.bad ? KDA_DEVERR_CU_SEQLENS : 0u;
-    if (share.bad) return;
-    if (x.base % 1024 != 0) {   // the tiles' swizzle counts from 1 KB boundaries
-        if (tid == 0) atomicOr(p.status, KDA_DEVERR_INTERNAL);
-        return;
-    }
-    Cursor u = share.at;
-    if (kStateOnly) {
-        // the share's last chunks, if its end lies inside a unit; u is the chunk after them
-        if (share.x1 == share.x0 || share.x1 >= share.total || u.c == 0) return;
-        const int64_t own = share.x1 - share.x0;
-        x.count = (int)own < u.c ? own : u.c;
-        u.c -= x.count;
-    } else {
-        empty_units(p);
-        x.count = (int)(share.x1 - share.x0);
-        if (x.count == 0) return;
-    }
-    if (tid == 0) {
-        for (int b = 0; b < NBAR; ++b) {
-            const bool warps = b == EQ || b == EQ + 1 || b == KPF || b == KPF + 1 || b == VR || b == VR + 1 || b == PF || b == OS || b == OE || b == SB || b == KVE;
-            const bool both = b == EK || b == EK + 1;   // the key tile: W's MMA and the eight key warps
-            const bool twice = b == EV || b == EV + 1;  // the value tile: KV's and P V's MMAs
-            mbar_init(x.bar(b), warps ? 4 : both ? (kStateOnly ? 8 : 9) : twice ? (kStateOnly ? 1 : 2) : 1);
+    if (warp == 20) {
+        if ((tid & 31) == 0) {
+            for (int b = 0; b < NBAR; ++b) {
+                const bool warps = b == EQ || b == EQ + 1 || b == KPF || b == KPF + 1 || b == VR || b == VR + 1 || b == PF || b == OS || b == OE || b == SB || b == KVE;
+                const bool both = b == EK || b == EK + 1;   // the key tile: W's MMA and the eight key warps
+                const bool twice = b == EV || b == EV + 1;  // the value tile: KV's and P V's MMAs
+                mbar_init(x.bar(b), warps ? 4 : both ? (kStateOnly ? 8 : 9) : twice ? (kStateOnly ? 1 : 2) : 1);
+            }
+            mbar_fence_init();
+            tma_prefetch_desc(&maps.q);
+            tma_prefetch_desc(&maps.k);
+            tma_prefetch_desc(&maps.v);
+            tma_prefetch_desc(&maps.out);
         }
-        mbar_fence_init();
-        tma_prefetch_desc(&maps.q);
-        tma_prefetch_desc(&maps.k);
-        tma_prefetch_desc(&maps.v);
-        tma_prefetch_desc(&maps.out);
-    }
-    if (warp == 0) {
+        __syncwarp();
         tmem_alloc(x.base + OFF_TMEM, 512);
         tmem_relinquish();
     }
     tc_fence_before();
+    const Share share = find_share(p, recip, reinterpret_cast<int64_t*>(smem_raw + OFF_S));
+    if (!kStateOnly && share.empties && !share.bad) empty_units(p);
+    Cursor* seg = reinterpret_cast<Cursor*>(smem_raw + OFF_SEG);
+    x.seg = seg;
+    x.nA = x.nAB = x.count = 0;
+    if (kStateOnly) {
+        if (tid == 0) *share_flag(p, blockIdx.x) = 0u;
+        if (share.cut && !share.tail) {   // the share's last chunks, of a unit in more than two shares
+            const int64_t own = share.x1 - share.x0;
+            x.nAB = x.count = own < share.end.c ? (int)own : share.end.c;
+            if (tid == 0) seg[1] = share.end, seg[1].c -= x.count;
+        }
+    } else {
+        x.count = (int)(share.x1 - share.x0);
+        x.nA = share.tail ? share.end.c : 0;
+        x.nAB = x.count - (share.head ? share.first.nc - share.first.c : 0);
+        if (tid == 0) {
+            seg[0] = share.end, seg[0].c = 0;
+            seg[1] = seg[2] = share.first;
+            if (share.head) {
+                seg[1].c = seg[1].nc - 1;
+                if (x.nAB > x.nA) next_chunk(p, seg[1]);
+            }
+        }
+    }
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = lds_u32(x.base + OFF_TMEM);   // all 512 columns: 0
-    if (tmem != 0) {
-        if (tid == 0) atomicOr(p.status, KDA_DEVERR_INTERNAL);
-        x.count = 0;
+    const uint32_t tmem = lds_u32(x.base + OFF_TMEM);
+    const bool sound = tmem == 0 && x.base % 1024 == 0;   // (the tiles' swizzle counts from 1 KB boundaries)
+    if (tid == 0) {
+        if (!kStateOnly && blockIdx.x == 0) *p.status = share.bad ? KDA_DEVERR_CU_SEQLENS : 0u;
+        if (!kStateOnly && !sound) atomicOr(p.status, KDA_DEVERR_INTERNAL);
     }
-    // registers a thread: 80 at launch; 64 + 56 + 168 + 72 + 72 + 48 of the 6 x 80 that the block holds
+    if (!sound) x.count = 0;   // (bad lengths have no chunks)
     bool ok = true;
+    // registers a thread: 80 at launch; 64 + 56 + 168 + 72 + 72 + 48 of the 6 x 80 that the block holds
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        if (!kStateOnly) ok = score_warps(p, x, u);
+        if (!kStateOnly) ok = score_warps(p, x);
     } else if (warp < 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        if (!kStateOnly) ok = out_warps(p, maps, x, u);
+        if (!kStateOnly) ok = out_warps(p, maps, x);
     } else if (warp < 12) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
-        ok = state_warps<kStateOnly>(p, x, u, share);
+        ok = state_warps<kStateOnly>(p, x, share, recip);
     } else if (warp < 20) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        ok = key_warps(p, x, u, (warp - 12) >> 2);
+        ok = key_warps(p, x, (warp - 12) >> 2);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-        if (warp == 20) ok = load_warp<kStateOnly>(p, maps, x, u);
+        if (warp == 20) ok = load_warp<kStateOnly>(p, maps, x);
         else if (warp == 21 && !kStateOnly) ok = mma_out_warp(x);
         else if (warp == 22) ok = mma_state_warp(x);
     }
     if (!ok) mx_report(p.status);
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) {
+    if (warp == 20) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -733,7 +795,7 @@ __global__ void __launch_bounds__(LF_THREADS, 1) lin_fwd_kernel(const LinParams 
 
 }  // namespace
 
-size_t lin_workspace_bytes(int64_t, int, int) { return (size_t)LF_MAX_CTAS * HD * HD * sizeof(float); }
+size_t lin_workspace_bytes(int64_t, int, int) { return (size_t)LF_MAX_CTAS * (HD * HD * sizeof(float) + sizeof(uint32_t)); }
 
 cudaError_t launch_lin_fwd(const LinParams& p, cudaStream_t stream) {
     LinMaps maps;
@@ -749,12 +811,26 @@ cudaError_t launch_lin_fwd(const LinParams& p, cudaStream_t stream) {
     const int64_t most = (p.T_total / LF_C + p.nseq) * p.H;   // chunks at most
     int ctas = sms < LF_MAX_CTAS ? sms : LF_MAX_CTAS;
     if (most < ctas) ctas = most > 0 ? (int)most : 1;
+    const uint64_t recip = ctas > 1 ? ~0ull / (uint64_t)ctas + 1 : 0;
     for (auto k : {lin_fwd_kernel<true>, lin_fwd_kernel<false>}) {
         e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LF_SMEM);
         if (e != cudaSuccess) return e;
-        k<<<ctas, LF_THREADS, LF_SMEM, stream>>>(p, maps);
+        // cooperative: a share may wait for the state that the share before it publishes, so all of
+        // them are resident
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeCooperative;
+        attr[0].val.cooperative = 1;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)ctas);
+        cfg.blockDim = dim3(LF_THREADS);
+        cfg.dynamicSmemBytes = LF_SMEM;
+        cfg.stream = stream;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, k, p, maps, recip);
+        if (e != cudaSuccess) return e;
     }
-    return cudaGetLastError();
+    return cudaSuccess;
 }
 
 }  // namespace kda
