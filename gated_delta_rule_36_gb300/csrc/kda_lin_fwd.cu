@@ -12,8 +12,10 @@
 // rounding to nearest (accumulating a whole sequence in the tensor core would truncate at
 // every step).  Its bf16 copy in shared memory is O's operand only.
 //
-// One persistent CTA per SM takes an equal, contiguous share of all chunks of all (sequence,
-// head) units, in the order (n, h, c).  A share that starts inside a unit needs the state before
+// One persistent CTA per SM takes a contiguous share of all chunks of all (sequence, head)
+// units, in the order (n, h, c); the shares are equal in chunks plus `extra` for each unit that
+// starts there (reading and writing an fp32 state is a chunk's traffic, and changing units costs
+// about another one).  A share that starts inside a unit needs the state before
 // it.  Where the unit lies in two shares, the first one takes its part of that unit first of all
 // and publishes the state, and the second one takes its part last of all, when the state has
 // long been there: no chunk is read twice and nobody waits.  Units that lie in more than two
@@ -96,13 +98,15 @@ __device__ __forceinline__ float log2_decay(const LinParams& p, int h) {
     return d < -1e30f ? -1e30f : d;
 }
 
-// Where share b of `ctas` equal ones starts (recip = 2^64 / ctas, rounded up: no division).
+// Where, by weight, share b of `ctas` equal ones starts (recip = 2^64 / ctas, rounded up: no division).
 __device__ __forceinline__ int64_t share_start(int64_t total, int b, int ctas, uint64_t recip) {
     return b >= ctas ? total : b <= 0 ? 0 : (int64_t)__umul64hi((uint64_t)total * (uint64_t)b, recip);
 }
 
 struct Share {
-    int64_t total, x0, x1;   // chunks of the whole batch; this share's
+    int64_t total;        // weight of the whole batch
+    int64_t x0, x1;       // the share's chunks, counted over the whole batch
+    int64_t unit;         // where, by weight, the chunks of x0's unit start
     Cursor first, end;    // the chunk x0; the chunk x1 (if there is one)
     bool bad;             // cu_seqlens do not describe the tokens
     bool head, tail;      // x0 / x1 lies inside a unit that has no other share than the two there
@@ -112,10 +116,11 @@ struct Share {
 
 // The whole CTA: checks cu_seqlens, counts the chunks and finds the share's ends.  Every CTA
 // starts with this: one pass over the lengths and two block-wide exchanges.
-__device__ Share find_share(const LinParams& p, uint64_t recip, int64_t* scratch /* 48 */) {
+__device__ Share find_share(const LinParams& p, uint64_t recip, int64_t* scratch /* 64 */) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (p.nseq + LF_THREADS - 1) / LF_THREADS;
     const int n0 = min(tid * per, p.nseq), n1 = min(n0 + per, p.nseq);
+    // sequences that are not empty (upper 20 bits) and chunks (lower 44)
     Cursor u{};
     int64_t mine = 0;
     int what = 0;   // 1: bad, 2: a sequence of no tokens
@@ -129,7 +134,7 @@ __device__ Share find_share(const LinParams& p, uint64_t recip, int64_t* scratch
         u.n = n;
         u.nc = (u.len + LF_C - 1) / LF_C;
         if (u.len == 0) what |= 2;
-        mine += u.nc;
+        else mine += (1LL << 44) + u.nc;
     }
     int64_t sum = mine;
 #pragma unroll 1
@@ -148,37 +153,51 @@ __device__ Share find_share(const LinParams& p, uint64_t recip, int64_t* scratch
         before += w < warp ? scratch[w] : 0;
         all += scratch[w];
     }
-    const int64_t total = s.total = all * p.H;
+    const int extra = 1 + (p.init_state != nullptr || p.final_state != nullptr);
+    auto weight = [&](int64_t v) { return ((v & ((1LL << 44) - 1)) + (v >> 44) * extra) * p.H; };
+    const int64_t total = s.total = weight(all);
     const int b = blockIdx.x, ctas = gridDim.x;
-    s.x0 = share_start(total, b, ctas, recip);
-    s.x1 = share_start(total, b + 1, ctas, recip);
-    Cursor* place = reinterpret_cast<Cursor*>(scratch + 24);   // [2]
+    const int64_t y0 = share_start(total, b, ctas, recip), y1 = share_start(total, b + 1, ctas, recip);
+    struct Place {
+        Cursor at;
+        int64_t x, unit;
+    };
+    Place* place = reinterpret_cast<Place*>(scratch + 32);   // [2]
+    if (tid == 0) place[1].x = (all & ((1LL << 44) - 1)) * p.H;   // the end of the last share
+    __syncthreads();
 #pragma unroll 1
     for (int e = 0; e < 2; ++e) {
-        int64_t at = (e ? s.x1 : s.x0) - before * p.H;
-        if (at < 0 || at >= mine * p.H) continue;
+        int64_t at = (e ? y1 : y0) - weight(before), done = (before & ((1LL << 44) - 1)) * p.H;
+        if (at < 0 || at >= weight(mine)) continue;
         if (n1 - n0 > 1)
             for (u.n = n0;; ++u.n) {
                 seq_of(p, u.n, u.bos, u.len);
                 u.nc = (u.len + LF_C - 1) / LF_C;
-                if (at < (int64_t)u.nc * p.H) break;
-                at -= (int64_t)u.nc * p.H;
+                const int64_t w = u.nc > 0 ? (int64_t)(u.nc + extra) * p.H : 0;
+                if (at < w) break;
+                at -= w;
+                done += (int64_t)u.nc * p.H;
             }
-        u.h = (int)((float)at / (float)u.nc);   // (within one of the quotient, which is below 2^16)
-        at -= (int64_t)u.h * u.nc;
-        if (at < 0) --u.h, at += u.nc;
-        else if (at >= u.nc) ++u.h, at -= u.nc;
-        u.c = (int)at;
-        place[e] = u;
+        const int w = u.nc + extra;
+        u.h = (int)((float)at / (float)w);   // (within one of the quotient, which is below 2^16)
+        at -= (int64_t)u.h * w;
+        if (at < 0) --u.h, at += w;
+        else if (at >= w) ++u.h, at -= w;
+        u.c = at > extra ? (int)at - extra : 0;
+        place[e] = Place{u, done + (int64_t)u.h * u.nc + u.c, (e ? y1 : y0) - at + extra};
     }
     __syncthreads();
-    s.first = place[0];
-    s.end = place[1];
+    s.first = place[0].at;
+    s.end = place[1].at;
+    s.x0 = y0 < total ? place[0].x : place[1].x;
+    s.x1 = place[1].x;
+    s.unit = place[0].unit;
+    const int64_t end_unit = place[1].unit;
     __syncthreads();
-    s.cut = s.x1 < total && s.x1 > s.x0 && s.end.c > 0;
-    const int64_t eu = s.x1 - s.end.c, su = s.x0 - s.first.c;   // where the units there start
-    s.tail = s.cut && eu >= s.x0 && eu + s.end.nc <= share_start(total, b + 2, ctas, recip);
-    s.head = s.x1 > s.x0 && s.first.c > 0 && su >= share_start(total, b - 1, ctas, recip) && su + s.first.nc <= s.x1;
+    // (chunks of a unit, by weight: [unit, unit + nc))
+    s.cut = y1 < total && s.x1 > s.x0 && s.end.c > 0;
+    s.tail = s.cut && end_unit >= y0 && end_unit + s.end.nc <= share_start(total, b + 2, ctas, recip);
+    s.head = s.x1 > s.x0 && s.first.c > 0 && s.unit >= share_start(total, b - 1, ctas, recip) && s.unit + s.first.nc <= y1;
     return s;
 }
 
@@ -223,6 +242,11 @@ __device__ bool load_warp(const LinParams& p, const LinMaps& maps, const Ctx& x)
             return true;
         };
         for (int i = 0; i < x.count && ok; advance(p, x, u, i), ++i) {
+            if (!kStateOnly && u.c == 0 && p.init_state) {   // the state warps will want it soon
+                const uint32_t bytes = HD * HD * (p.init_f32 ? 4 : 2);
+                const char* from = static_cast<const char*>(p.init_state) + ((size_t)u.n * p.H + u.h) * bytes;
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(bytes) : "memory");
+            }
             ok = one(i, FK, EK, &maps.k, TILE);
             if (!kStateOnly) ok = ok && one(i, FQ, EQ, &maps.q, 0);
             ok = ok && one(i, FV, EV, &maps.v, 2 * TILE);
@@ -473,7 +497,14 @@ __device__ bool state_warps(const LinParams& p, const Ctx& x, const Share& share
     const uint32_t lanes = (uint32_t)(32 * warp) << 16;
     float2 S[LF_C / 2];
     float l2 = 0.f, all = 0.f;
-    bool fresh = true;   // a unit or a part of one starts
+    bool fresh = true;      // a unit or a part of one starts
+    bool publish = false;   // this share's part of a unit is written but not yet announced
+    auto announce = [&]() {
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(share_flag(p, blockIdx.x)) : "memory");
+        publish = false;
+    };
     for (int i = 0; i < x.count; advance(p, x, u, i), ++i) {
         const int valid = chunk_tokens(u);
         const size_t unit = (size_t)u.n * p.H + u.h;
@@ -505,13 +536,12 @@ __device__ bool state_warps(const LinParams& p, const Ctx& x, const Share& share
                     const float f = exp2f(l2 * (float)u.c * (float)LF_C);
 #pragma unroll
                     for (int v = 0; v < LF_C / 2; ++v) S[v].x *= f, S[v].y *= f;
-                    const int64_t begin = share.x0 - u.c;   // the unit's first chunk
 #pragma unroll 1
                     for (int b = (int)blockIdx.x - 1; b >= 0; --b) {
-                        const int64_t end = share_start(share.total, b + 1, gridDim.x, recip);
-                        if (end <= begin) break;
-                        if (share_start(share.total, b, gridDim.x, recip) == end) continue;
-                        const float g = exp2f(l2 * (float)(share.x0 - end) * (float)LF_C);
+                        const int64_t end = share_start(share.total, b + 1, gridDim.x, recip) - share.unit;   // chunks up to there
+                        if (end <= 0) break;
+                        if (share_start(share.total, b, gridDim.x, recip) - share.unit == end) continue;
+                        const float g = exp2f(l2 * (float)(u.c - end) * (float)LF_C);
                         const float* part = share_state(p, b) + k;
 #pragma unroll
                         for (int v = 0; v < LF_C / 2; ++v) {
@@ -550,6 +580,7 @@ __device__ bool state_warps(const LinParams& p, const Ctx& x, const Share& share
         }
         tc_fence_before();
         mx_arrive_warp(x.bar(KVE));
+        if (!kStateOnly && publish) announce();   // a chunk later: its stores have long been done
         if (kStateOnly ? i + 1 == x.count : i + 1 == x.nA) {
             // this share's part of a unit that the next share goes on with
             float* part = share_state(p, blockIdx.x) + k;
@@ -558,11 +589,7 @@ __device__ bool state_warps(const LinParams& p, const Ctx& x, const Share& share
                 part[(2 * v) * HD] = S[v].x;
                 part[(2 * v + 1) * HD] = S[v].y;
             }
-            if (!kStateOnly) {
-                __threadfence();
-                __syncwarp();
-                if (lane == 0) asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(share_flag(p, blockIdx.x)) : "memory");
-            }
+            publish = true;
             fresh = true;
         } else if (!kStateOnly && u.c + 1 == u.nc) {
             fresh = true;
@@ -586,6 +613,7 @@ __device__ bool state_warps(const LinParams& p, const Ctx& x, const Share& share
             }
         }
     }
+    if (!kStateOnly && publish) announce();
     return true;
 }
 
