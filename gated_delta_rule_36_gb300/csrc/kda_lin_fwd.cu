@@ -47,12 +47,15 @@ constexpr uint32_t OFF_S = 2 * STAGE;
 // alone (a short chunk puts its own weights there)
 constexpr uint32_t OFF_POW = OFF_S + TILE, OFF_KPOW = OFF_POW + 4 * 256;
 constexpr uint32_t OFF_BAR = OFF_KPOW + 8 * 128;
-enum { FQ = 0, FK = 2, FV = 4, EQ = 6, EK = 8, EV = 10, KPF = 12, KPE = 14, VR = 16, WF = 18, PF, QSF, OS, OF, OE, KVF, KVE, SB, DRAIN, DRAIN2, NBAR };
+enum { FQ = 0, FK = 2, FV = 4, EQ = 6, EK = 8, EV = 10, KPF = 12, KPE = 16, VR = 20, WF = 22, PF, QSF, OS, OF, OE, KVF, KVE, SB, DRAIN, DRAIN2, NBAR };
 constexpr uint32_t OFF_TMEM = OFF_BAR + NBAR * 8, OFF_SEG = OFF_TMEM + 8;
 constexpr uint32_t LF_SMEM = OFF_SEG + 3 * 24;   // no room to align the base: it has to be (and is checked to be) 1 KB aligned
 static_assert(LF_SMEM <= 232448, "one CTA's shared memory");
 // Tensor Memory columns (all are allocated, so that its address is 0): W then P; KV; O; two slots of K' (32 tokens: three terms of 16 columns)
 constexpr uint32_t TM_W = 0, TM_KV = 128, TM_O = 256, TM_KP = 384, KP_SLOT = 48;
+
+// The launch that only sums needs no W: its place takes two more slots, for two more groups.
+__device__ __forceinline__ uint32_t kp_slot(int s) { return s < 2 ? TM_KP + s * KP_SLOT : TM_W + (s - 2) * KP_SLOT; }
 
 struct LinMaps {
     CUtensorMap q, k, v, out;
@@ -309,6 +312,7 @@ __device__ bool mma_out_warp(const Ctx& x) {
 }
 
 // KV = K'^T V, 32 tokens at a time as the key warps hand them over
+template <bool kStateOnly>
 __device__ bool mma_state_warp(const Ctx& x) {
     const uint32_t lead = mx_leader();
     const int count = mx_uniform(x.count);
@@ -320,8 +324,8 @@ __device__ bool mma_state_warp(const Ctx& x) {
         if (!ok) break;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            const int slot = b & 1;
-            ok = ok && mx_wait_lane(x.bar(KPF + slot), (uint32_t)(b >> 1));
+            const int slot = kStateOnly ? b : b & 1;
+            ok = ok && mx_wait_lane(x.bar(KPF + slot), kStateOnly ? i & 1u : (uint32_t)(b >> 1));
             if (!ok) break;
             tc_fence_after();
             const uint64_t v = dV + s * D_STAGE + 2 * b * MN_STEP;
@@ -329,7 +333,7 @@ __device__ bool mma_state_warp(const Ctx& x) {
             for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
                 for (int term = 0; term < 3; ++term)
-                    mx_mma_ts(lead, TM_KV, TM_KP + slot * KP_SLOT + term * 16 + 8 * kk, v + kk * MN_STEP, ID_MN, b + kk + term > 0);
+                    mx_mma_ts(lead, TM_KV, kp_slot(slot) + term * 16 + 8 * kk, v + kk * MN_STEP, ID_MN, b + kk + term > 0);
             mx_commit(lead, x.bar(KPE + slot));
         }
         if (!ok) break;
@@ -620,14 +624,16 @@ __device__ bool state_warps(const LinParams& p, const Ctx& x, const Share& share
 // ---------------------------------------------------------------- warps 12-19: K'
 // Thread k reads column k of the key tile, weighs it by a^(C-1-j) and leaves each value as a
 // sum of three bf16 in lane k of Tensor Memory, 32 tokens at a time; group g takes the parts
-// g and g + 2 of each chunk and owns slot g.
+// g and g + 2 of each chunk and owns slot g.  (In the launch that only sums, the warps of the
+// scores and of the output are groups 2 and 3, and each group takes one part.)
 __device__ __forceinline__ float2 unpack2(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
 
+template <bool kStateOnly>
 __device__ bool key_warps(const LinParams& p, const Ctx& x, int g) {
     Cursor u = first_chunk(x);
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, k = threadIdx.x & 127;
-    const uint32_t kp = ((uint32_t)(32 * warp) << 16) + TM_KP + g * KP_SLOT;
-    const uint32_t pow = x.base + OFF_KPOW + (4 * g + warp) * 128;
+    const uint32_t kp = ((uint32_t)(32 * warp) << 16) + kp_slot(g);
+    const uint32_t pow = x.base + (g < 2 ? OFF_KPOW : OFF_POW) + (4 * (g & 1) + warp) * 128;
     const int kc = (k >> 3) & 7;
     const float2 minus = make_float2(-1.f, -1.f);
     float l2 = 0.f, hop = 0.f;
@@ -660,8 +666,8 @@ __device__ bool key_warps(const LinParams& p, const Ctx& x, int g) {
         }
         bool ok = true;
 #pragma unroll 1
-        for (int b = g; b < 4; b += 2) {
-            const int use = 2 * i + (b >> 1);
+        for (int b = g; b < 4; b += kStateOnly ? 4 : 2) {
+            const int use = kStateOnly ? i : 2 * i + (b >> 1);
             uint32_t kt = x.base + s * STAGE + TILE + (k >> 6) * HALF + (k & 7) * 2 + 32 * b * 128;
             float f = b == 3 ? 1.f : b == 2 ? hop : b == 1 ? hop * hop : hop * hop * hop;   // a^(96 - 32 b)
             if (!full) {
@@ -742,10 +748,10 @@ __global__ void __launch_bounds__(LF_THREADS, 1) lin_fwd_kernel(const LinParams 
     if (warp == 20) {
         if ((tid & 31) == 0) {
             for (int b = 0; b < NBAR; ++b) {
-                const bool warps = b == EQ || b == EQ + 1 || b == KPF || b == KPF + 1 || b == VR || b == VR + 1 || b == PF || b == OS || b == OE || b == SB || b == KVE;
-                const bool both = b == EK || b == EK + 1;   // the key tile: W's MMA and the eight key warps
+                const bool warps = b == EQ || b == EQ + 1 || (b >= KPF && b < KPF + 4) || b == VR || b == VR + 1 || b == PF || b == OS || b == OE || b == SB || b == KVE;
+                const bool both = b == EK || b == EK + 1;   // the key tile: W's MMA and the key warps
                 const bool twice = b == EV || b == EV + 1;  // the value tile: KV's and P V's MMAs
-                mbar_init(x.bar(b), warps ? 4 : both ? (kStateOnly ? 8 : 9) : twice ? (kStateOnly ? 1 : 2) : 1);
+                mbar_init(x.bar(b), warps ? 4 : both ? (kStateOnly ? 16 : 9) : twice ? (kStateOnly ? 1 : 2) : 1);
             }
             mbar_fence_init();
             tma_prefetch_desc(&maps.q);
@@ -793,24 +799,37 @@ __global__ void __launch_bounds__(LF_THREADS, 1) lin_fwd_kernel(const LinParams 
     }
     if (!sound) x.count = 0;   // (bad lengths have no chunks)
     bool ok = true;
-    // registers a thread: 80 at launch; 64 + 56 + 168 + 72 + 72 + 48 of the 6 x 80 that the block holds
+    // registers a thread: 80 at launch; 64 + 56 + 168 + 72 + 72 + 48 of the 6 x 80 that the block holds,
+    // or 72 + 72 + 152 + 72 + 72 + 40
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        if (!kStateOnly) ok = score_warps(p, x);
+        if (kStateOnly) {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+            ok = key_warps<kStateOnly>(p, x, 2);
+        } else {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+            ok = score_warps(p, x);
+        }
     } else if (warp < 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        if (!kStateOnly) ok = out_warps(p, maps, x);
+        if (kStateOnly) {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+            ok = key_warps<kStateOnly>(p, x, 3);
+        } else {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+            ok = out_warps(p, maps, x);
+        }
     } else if (warp < 12) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+        if (kStateOnly) asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
         ok = state_warps<kStateOnly>(p, x, share, recip);
     } else if (warp < 20) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        ok = key_warps(p, x, (warp - 12) >> 2);
+        ok = key_warps<kStateOnly>(p, x, (warp - 12) >> 2);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        if (kStateOnly) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         if (warp == 20) ok = load_warp<kStateOnly>(p, maps, x);
         else if (warp == 21 && !kStateOnly) ok = mma_out_warp(x);
-        else if (warp == 22) ok = mma_state_warp(x);
+        else if (warp == 22) ok = mma_state_warp<kStateOnly>(x);
     }
     if (!ok) mx_report(p.status);
     tc_fence_before();
