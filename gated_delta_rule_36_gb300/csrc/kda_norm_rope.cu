@@ -126,8 +126,9 @@ cudaError_t launch(const NormRopeParams& p, cudaStream_t stream) {
 cudaError_t launch_norm_rope(const NormRopeParams& p, cudaStream_t stream) {
     const int64_t rows = p.tokens * (p.heads[0] + p.heads[1]);
     if (rows == 0) return cudaSuccess;
-    // Rows a half-warp takes: four once that still gives every SM a few blocks.
-    if (rows >= 152 * 4 * NR_HALVES * 4) return launch<4>(p, stream);
+    // Rows a half-warp takes: eight once that still gives every SM a few blocks (32,768 tokens x 72
+    // heads: 203 us, against 222 with four and 305 with two), else one, for the latency of small calls.
+    if (rows >= 152 * 4 * NR_HALVES * 8) return launch<8>(p, stream);
     return launch<1>(p, stream);
 }
 
