@@ -15,6 +15,11 @@
 // all come out even.  A pair that lies in more than one share leaves unnormalised partial rows in
 // the workspace, and a second, small kernel joins them in the order of the keys.
 //
+// A pair of at most one tile's rows (single tokens, short prompts) alternates its one tile between
+// the two places for scores, so that the next block's scores are there when this one's are done.
+// (Those blocks have barriers of their own, SX and PX: a warp that counts a barrier's phases has to
+// wait for every one of them.)
+//
 // Warp roles: warps 0-3 and 4-7 are the softmax of the two tiles (thread = row) and write the
 // results; warp 8 loads q, k and v by TMA (a ring of four 32 KB tiles); warp 9 issues the MMAs,
 // alternating between the tiles so that one is multiplied while the other is exponentiated.
@@ -34,7 +39,7 @@ constexpr int RING = 4;
 constexpr uint32_t OFF_RING = 2 * TILE;       // behind the two query tiles
 constexpr uint32_t OFF_STAGE = OFF_RING + RING * TILE;   // 4 KB for each softmax warp: 32 rows of 128 bytes
 constexpr uint32_t OFF_BAR = OFF_STAGE + 8 * 4096;
-enum { FULL = 0, EMPTY = RING, QF = 2 * RING, QE, SF, PF = SF + 2, OF = PF + 4, DRAIN = OF + 2, NBAR };
+enum { FULL = 0, EMPTY = RING, QF = 2 * RING, QE, SF, PF = SF + 2, OF = PF + 4, SX = OF + 2, PX, PV = PX + 2, DRAIN, NBAR };
 constexpr uint32_t OFF_TMEM = OFF_BAR + NBAR * 8;
 constexpr uint32_t AT_SMEM = OFF_TMEM + 8;
 static_assert(AT_SMEM <= 232448, "one CTA's shared memory");
@@ -356,32 +361,28 @@ __device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
     const uint32_t lead = mx_leader();
     const uint64_t dQ = make_sdesc_kmajor_sw128(x.base), dK = make_sdesc_kmajor_sw128(x.base + OFF_RING);
     const uint64_t dV = make_sdesc_mnmajor_sw128(x.base + OFF_RING, HALF, 1024);
-    int slot = 0;                 // of the next tile to be waited for: k and v alternate
-    uint32_t lap = 0, pieces = 0, n0 = 0, n1 = 0;
+    uint32_t it = 0;              // tiles of the ring before this piece: k and v alternate
+    uint32_t pieces = 0, n0 = 0, n1 = 0, nX = 0;
     bool ok = true;
-    // the next tile of the ring has landed; its slot
-    auto landed = [&](int& s) {
-        s = slot;
-        const bool r = mx_wait_lane(x.bar(FULL + slot), lap & 1u);
-        if (++slot == RING) slot = 0, ++lap;
-        return r;
-    };
-    auto scores = [&](int t, int s) {
-        const uint64_t q = dQ + t * D_TILE, k = dK + s * D_TILE;
+    // tile i of the piece has landed; its slot
+    auto landed = [&](uint32_t i) { return mx_wait_lane(x.bar(FULL + ((it + i) & (RING - 1))), (it + i) / RING & 1u); };
+    auto slot = [&](uint32_t i) { return (int)((it + i) & (RING - 1)); };
+    auto scores = [&](int q, int t, int s, int done) {   // of query tile q, into place t
+        const uint64_t a = dQ + q * D_TILE, k = dK + s * D_TILE;
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-            mx_mma_ss(lead, TM_S + 128 * t, q + (kk >> 2) * K_HALF + (kk & 3) * K_STEP, k + (kk >> 2) * K_HALF + (kk & 3) * K_STEP, ID_KK, kk > 0);
-        mx_commit(lead, x.bar(SF + t));
+            mx_mma_ss(lead, TM_S + 128 * t, a + (kk >> 2) * K_HALF + (kk & 3) * K_STEP, k + (kk >> 2) * K_HALF + (kk & 3) * K_STEP, ID_KK, kk > 0);
+        mx_commit(lead, x.bar(done));
     };
-    auto values = [&](int t, int s, int half, bool first) {
+    auto values = [&](int o, int t, int s, int half, bool first) {   // weights in place t, onto output o
         const uint64_t v = dV + s * D_TILE;
 #pragma unroll
         for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-            mx_mma_ts(lead, TM_O + 128 * t, TM_S + 128 * t + kk * 8, v + kk * MN_STEP, ID_MN, kk > 0 || !first);
+            mx_mma_ts(lead, TM_O + 128 * o, TM_S + 128 * t + kk * 8, v + kk * MN_STEP, ID_MN, kk > 0 || !first);
     };
-    // half of tile t's P is in place (the n-th block of the tile)
-    auto weights = [&](int t, int half, uint32_t n) {
-        const bool r = mx_wait_lane(x.bar(PF + 2 * t + half), n & 1u);
+    // (half of) the weights are in place, for the n-th time
+    auto weights = [&](int done, uint32_t n) {
+        const bool r = mx_wait_lane(x.bar(done), n & 1u);
         tc_fence_after();
         return r;
     };
@@ -391,15 +392,14 @@ __device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
         Piece r = piece_at(x, u, left);
         r.j0 = mx_uniform(r.j0), r.j1 = mx_uniform(r.j1), r.e0 = mx_uniform(r.e0);
         left -= r.j1 - r.j0;
-        const int e0 = r.e0, e1 = r.two ? r.j1 : r.j0;   // where the tiles' blocks end
-        int ks, vs;
-        // the next values have landed; those past the sequence's keys count for nothing, whatever
-        // they hold
+        const int count = r.j1 - r.j0, c0 = r.e0 - r.j0;   // blocks; the first tile's
+        // the values of block j have landed; those past the sequence's keys count for nothing,
+        // whatever they hold
         auto next_values = [&](int j) {
-            if (!landed(vs)) return false;
-            const int valid = u.s.lk - j * KB;
+            if (!landed(2 * j + 1)) return false;
+            const int valid = u.s.lk - (r.j0 + j) * KB;
             if (valid < KB) {
-                const uint32_t at = x.base + OFF_RING + vs * TILE;
+                const uint32_t at = x.base + OFF_RING + slot(2 * j + 1) * TILE;
 #pragma unroll 1
                 for (int row = max(valid, 0); row < KB; ++row) sts_u64(at + (lane >> 4) * HALF + row * 128 + (lane & 15) * 8, 0u, 0u);
                 fence_proxy_async_smem();
@@ -407,45 +407,81 @@ __device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
             }
             return true;
         };
-        ok = x.wait(QF, pieces) && landed(ks);
+        ok = x.wait(QF, pieces) && landed(0);
         if (!ok) break;
-        if (r.j0 < e0) scores(0, ks);
-        if (r.j0 < e1) scores(1, ks);
-        mx_commit(lead, x.bar(EMPTY + ks));
-        ok = next_values(r.j0);
-        for (int j = r.j0; ok; ++j) {
-            const bool more = j + 1 < r.j1, first = j == r.j0;
-            if (j < e0) {
-                ok = weights(0, 0, n0);
+        if (!r.two) {
+            // one tile: its scores alternate between the two places, so that the next block's are there
+            // when the tile's softmax has done with this one's
+            scores(0, 0, slot(0), SF);
+            mx_commit(lead, x.bar(EMPTY + slot(0)));
+            if (count > 1) {
+                ok = landed(2);
                 if (!ok) break;
-                values(0, vs, 0, first);
-                ok = weights(0, 1, n0++);
-                if (!ok) break;
-                values(0, vs, 1, first);
-                if (j + 1 == e0) mx_commit(lead, x.bar(OF));
+                scores(0, 1, slot(2), SX);
+                mx_commit(lead, x.bar(EMPTY + slot(2)));
             }
-            if (more) {
-                ok = landed(ks);
+#pragma unroll 1
+            for (int j = 0; j < count; ++j) {
+                const int t = j & 1;
+                const uint32_t n = t ? nX++ : n0++;
+                const int done = t ? PX : PF;
+                ok = next_values(j) && weights(done, n);
                 if (!ok) break;
-                if (j + 1 < e0) scores(0, ks);
+                values(0, t, slot(2 * j + 1), 0, j == 0);
+                ok = weights(done + 1, n);
+                if (!ok) break;
+                values(0, t, slot(2 * j + 1), 1, j == 0);
+                mx_commit(lead, x.bar(j + 1 == count ? OF : PV));
+                mx_commit(lead, x.bar(EMPTY + slot(2 * j + 1)));
+                if (j + 2 < count) {
+                    ok = landed(2 * j + 4);
+                    if (!ok) break;
+                    scores(0, t, slot(2 * j + 4), t ? SX : SF);
+                    mx_commit(lead, x.bar(EMPTY + slot(2 * j + 4)));
+                }
             }
-            if (j < e1) {
-                ok = weights(1, 0, n1);
+        } else {
+            if (c0 > 0) scores(0, 0, slot(0), SF);
+            scores(1, 1, slot(0), SF + 1);
+            mx_commit(lead, x.bar(EMPTY + slot(0)));
+            ok = next_values(0);
+#pragma unroll 1
+            for (int j = 0; ok; ++j) {
+                const bool more = j + 1 < count;
+                const int vs = slot(2 * j + 1), ks = slot(2 * j + 2);
+                if (j < c0) {
+                    ok = weights(PF, n0);
+                    if (!ok) break;
+                    values(0, 0, vs, 0, j == 0);
+                    ok = weights(PF + 1, n0++);
+                    if (!ok) break;
+                    values(0, 0, vs, 1, j == 0);
+                    if (j + 1 == c0) mx_commit(lead, x.bar(OF));
+                }
+                if (more) {
+                    ok = landed(2 * j + 2);
+                    if (!ok) break;
+                    if (j + 1 < c0) scores(0, 0, ks, SF);
+                }
+                ok = weights(PF + 2, n1);
                 if (!ok) break;
-                values(1, vs, 0, first);
-                ok = weights(1, 1, n1++);
+                values(1, 1, vs, 0, j == 0);
+                ok = weights(PF + 3, n1++);
                 if (!ok) break;
-                values(1, vs, 1, first);
-                if (j + 1 == e1) mx_commit(lead, x.bar(OF + 1));
+                values(1, 1, vs, 1, j == 0);
+                mx_commit(lead, x.bar(EMPTY + vs));
+                if (!more) {
+                    mx_commit(lead, x.bar(OF + 1));
+                    break;
+                }
+                ok = next_values(j + 1);
+                if (!ok) break;
+                scores(1, 1, ks, SF + 1);
+                mx_commit(lead, x.bar(EMPTY + ks));
             }
-            mx_commit(lead, x.bar(EMPTY + vs));
-            if (!more) break;
-            ok = next_values(j + 1);
-            if (!ok) break;
-            if (j + 1 < e1) scores(1, ks);
-            mx_commit(lead, x.bar(EMPTY + ks));
         }
         if (!ok) break;
+        it += 2 * count;
         mx_commit(lead, x.bar(QE));
     }
     __syncwarp();
@@ -462,28 +498,29 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 __device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const Ctx& x, Cursor u, int t) {
     const int row = threadIdx.x & 127;
-    const uint32_t tS = ((uint32_t)(row & ~31) << 16) + TM_S + 128 * t, tO = tS - TM_S + TM_O;
+    const uint32_t lanes = (uint32_t)(row & ~31) << 16, tO = lanes + TM_O + 128 * t;
     const int lane = threadIdx.x & 31;
     const uint32_t stage = x.base + OFF_STAGE + (threadIdx.x >> 5) * 4096;
     const float c = fmaxf(p.scale * LOG2E, 1e-30f);   // (a scale of 0 must not turn a masked -inf into NaN)
     const Partials part = partials(p.workspace);
     const int tok = row / x.G, head = row - tok * x.G;
-    uint32_t nS = 0, nO = 0;
+    uint32_t nS = 0, nX = 0, nO = 0, nV = 0;   // uses so far of SF, SX, OF and PV
     bool first_piece = true;
     for (int64_t left = x.steps; left > 0; next_pair(p, x, u), first_piece = false) {
         const Piece r = piece_at(x, u, left);
         left -= r.j1 - r.j0;
         if (t == 1 && !r.two) continue;
         const int end = t ? r.j1 : r.e0;
+        bool other = false;   // this block's scores are in the other tile's place
         const int i = u.pair * x.tp + t * x.tq + tok;                  // query within the sequence
         const bool mine = tok < x.tq && i < u.s.lq;
         // the last key it sees; a row that is no query's is left as it is, nothing reads its results
         const int last = mine ? i + u.s.lk - u.s.lq : 0x7fffffff;
         float m = -INFINITY, l = 0.f;
         for (int j = r.j0; j < end; ++j) {
-            if (!x.wait(SF + t, nS)) return false;
-            ++nS;
+            if (!x.wait(other ? SX : SF + t, other ? nX++ : nS++)) return false;
             tc_fence_after();
+            const uint32_t tS = lanes + TM_S + 128 * (t + other);
             uint32_t s[128];
 #pragma unroll
             for (int b = 0; b < 4; ++b) tmem_ld32(tS + 32 * b, reinterpret_cast<uint32_t(&)[32]>(s[32 * b]));
@@ -499,6 +536,9 @@ __device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const C
 #pragma unroll
                 for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], mx_u2f(s[k + 2 * e]), mx_u2f(s[k + 2 * e + 1]));
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            // the output has to hold all earlier products before it is scaled: with two tiles these scores
+            // came after them; with one they did not, and the product before has a barrier of its own
+            if (!r.two && j > r.j0 && !x.wait(PV, nV++)) return false;
             const bool grown = mine && (top - m) * c > 8.f;   // (m = -inf: whenever a key is seen)
             if (__any_sync(0xffffffffu, grown)) {
                 const float f = grown ? exp2f((m - top) * c) : 1.f;
@@ -538,10 +578,11 @@ __device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const C
                 if (b & 1) {   // half of P: the tensor core can start on it
                     tmem_wait_st();
                     tc_fence_before();
-                    mx_arrive_warp(x.bar(PF + 2 * t + (b >> 1)));
+                    mx_arrive_warp(x.bar((other ? PX : PF + 2 * t) + (b >> 1)));
                 }
             }
             l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            other = !r.two && !other;
         }
         const int64_t q = u.s.q0 + i;
         const int h = u.kh * x.G + head;
@@ -631,7 +672,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const AttnParams p,
     x.tp = 2 * x.tq;
     if (warp == 8) {
         if ((tid & 31) == 0) {
-            for (int b = 0; b < NBAR; ++b) mbar_init(x.bar(b), b >= PF && b < PF + 4 ? 4 : 1);
+            for (int b = 0; b < NBAR; ++b) mbar_init(x.bar(b), (b >= PF && b < PF + 4) || b == PX || b == PX + 1 ? 4 : 1);
             mbar_fence_init();
             tma_prefetch_desc(&maps.q);
             tma_prefetch_desc(&maps.k);
