@@ -12,7 +12,8 @@
 //
 // All (sequence, key head, tile pair, key block) steps are one line that is cut into equal
 // shares, one for each SM: long prompts, ragged batches and single tokens over a long cache
-// all come out even.  A pair that lies in more than one share leaves unnormalised partial rows in
+// all come out even.  What a pair costs by itself (its queries' way in, its results' way out, a
+// softmax that waits for its first scores) counts as PIECE steps in front of it.  A pair that lies in more than one share leaves unnormalised partial rows in
 // the workspace, and a second, small kernel joins them in the order of the keys.
 //
 // A pair of at most one tile's rows (single tokens, short prompts) alternates its one tile between
@@ -36,6 +37,7 @@ constexpr int AT_MAX_CTAS = 160;
 constexpr int KB = 128;                       // keys a block
 constexpr uint32_t TILE = 128 * 256, HALF = TILE / 2;
 constexpr int RING = 4;
+constexpr int PIECE = 2;                      // a pair's own weight, in steps
 constexpr uint32_t OFF_RING = 2 * TILE;       // behind the two query tiles
 constexpr uint32_t OFF_STAGE = OFF_RING + RING * TILE;   // 4 KB for each softmax warp: 32 rows of 128 bytes
 constexpr uint32_t OFF_BAR = OFF_STAGE + 8 * 4096;
@@ -106,24 +108,24 @@ __device__ __forceinline__ int blocks_seen(const Seq& s, int tokens) {
 
 __device__ __forceinline__ int pairs_of(const Seq& s, int tp) { return (s.lq + tp - 1) / tp; }
 
-// Steps of the sequence's first m pairs, m below pairs_of: the sum of blocks_seen((j + 1) tp), in
-// closed form from the sum of residues modulo 128, which repeat after 128 / gcd(tp, 128) pairs.
-__device__ __noinline__ int64_t steps_before(int lq, int lk, int m, int tp) {
+// Weight of the sequence's first m pairs, m below pairs_of: the sum of PIECE + blocks_seen((j + 1) tp),
+// in closed form from the sum of residues modulo 128, which repeat after 128 / gcd(tp, 128) pairs.
+__device__ __noinline__ int64_t weight_before(int lq, int lk, int m, int tp) {
     const int d = lk - lq;
     int ones = d > KB ? 0 : (KB - d) / tp;   // pairs that see one block
     ones = min(ones, m);
     const int n = m - ones;
-    if (n == 0) return ones;
+    if (n == 0) return ones + m * (int64_t)PIECE;
     const int b = (ones + 1) * tp + d + KB - 1;   // floor((b + i tp) / 128), i < n
     const int g = min(tp & -tp, KB), bits = 7 - (__ffs(g) - 1), per = 1 << bits;
     int64_t residues = (int64_t)(n >> bits) * (per * (b & (g - 1)) + g * per * (per - 1) / 2);
 #pragma unroll 1
     for (int i = 0, r = b; i < (n & (per - 1)); ++i, r += tp) residues += r & (KB - 1);
-    return ones + (((int64_t)b * n + tp * ((int64_t)n * (n - 1) / 2) - residues) >> 7);
+    return ones + m * (int64_t)PIECE + (((int64_t)b * n + tp * ((int64_t)n * (n - 1) / 2) - residues) >> 7);
 }
-__device__ __forceinline__ int64_t steps_of(const Seq& s, int tp) {
+__device__ __forceinline__ int64_t weight_of(const Seq& s, int tp) {
     const int m = pairs_of(s, tp);
-    return m == 0 ? 0 : steps_before(s.lq, s.lk, m - 1, tp) + blocks_seen(s, s.lq);
+    return m == 0 ? 0 : weight_before(s.lq, s.lk, m - 1, tp) + PIECE + blocks_seen(s, s.lq);
 }
 
 // Where share b of `ctas` equal ones starts (recip = 2^64 / ctas, rounded up: no division).
@@ -141,12 +143,12 @@ struct Cursor {
 // among them, in the order (sequence, key head, pair, key block).  Every CTA starts with this, so
 // it is short in latency: one pass over the lengths, two block-wide exchanges, one parallel search.
 struct Found {
-    int64_t at, each;   // the step within its sequence; steps of one key head there
+    int64_t at, each;   // how far into its sequence; the weight of one key head there
     int n;
     Seq s;
 };
 struct Share {
-    int64_t steps;
+    int64_t weight;
     Cursor at;          // where it starts
     bool bad;           // lengths that contradict the tensors
 };
@@ -166,7 +168,7 @@ __device__ Share find_share(const AttnParams& p, int tq, int G, uint64_t recip, 
         if (p.seqlens_k) b |= p.seqlens_k[n] < 0 || p.seqlens_k[n] > p.Tk;
         bad |= b;
         s = seq_of(p, n);
-        each = b ? 0 : steps_of(s, tp);
+        each = b ? 0 : weight_of(s, tp);
         mine += each * p.Hk;
     }
     int64_t sum = mine;
@@ -199,7 +201,7 @@ __device__ Share find_share(const AttnParams& p, int tq, int G, uint64_t recip, 
         if (n > n0)
             for (n = n0;; ++n) {
                 s = seq_of(p, n);
-                each = steps_of(s, tp);
+                each = weight_of(s, tp);
                 if (x < base + each * p.Hk) break;
                 base += each * p.Hk;
             }
@@ -223,7 +225,7 @@ __device__ Share find_share(const AttnParams& p, int tq, int G, uint64_t recip, 
 #pragma unroll 1
     while (__syncthreads_or(width > 1)) {   // narrow [lo, lo + width)
         const int step = (width + AT_THREADS / 2 - 1) / (AT_THREADS / 2), c = lo + (tid % (AT_THREADS / 2)) * step;
-        const int64_t st = width > 1 && c < lo + width ? steps_before(u.s.lq, u.s.lk, c, tp) : at + 1;
+        const int64_t st = width > 1 && c < lo + width ? weight_before(u.s.lq, u.s.lk, c, tp) : at + 1;
         if (st <= at) atomicMax(best + e, c);
         __syncthreads();
         const int b = best[e];
@@ -231,14 +233,15 @@ __device__ Share find_share(const AttnParams& p, int tq, int G, uint64_t recip, 
         if (width > 1) width = min(step, lo + width - b), lo = b;
     }
     u.pair = lo;
-    u.j = open ? 0 : (int)(at - start[e]);
+    const int from = open ? 0 : (int)(at - start[e]);   // the pair's own weight is at its front
+    u.j = max(from - PIECE, 0);
     // A cut near the end of a pair moves there: a pair that is cut costs its rows' partial results,
     // written and read again (about six steps' time for 256 rows).  Both neighbours find the same.
-    int64_t x = e ? x1 : x0;
+    int64_t x = (e ? x1 : x0) - (u.j > 0 ? 0 : from);
     const int nb = blocks_seen(u.s, (u.pair + 1) * tp), near = 6 * min(min(u.s.lq - u.pair * tp, tp) * G, 256) >> 8;
     bool over = false;
     if (u.j > 0 && !open) {
-        if (u.j <= near && u.j <= nb - u.j) x -= u.j, u.j = 0;
+        if (u.j <= near && u.j <= nb - u.j) x -= from, u.j = 0;
         else if (nb - u.j <= near) x += nb - u.j, over = true;
     }
     if (over) {   // the next pair
@@ -260,13 +263,14 @@ __device__ Share find_share(const AttnParams& p, int tq, int G, uint64_t recip, 
     if (tid == AT_THREADS / 2) start[1] = x;
     __syncthreads();
     r.at = *place;
-    r.steps = start[1] - start[0];
+    r.weight = start[1] - start[0];
     return r;
 }
 
 // A share's next piece: the blocks [j0, j1) of one pair.
 struct Piece {
     int j0, j1, nb;     // of nb
+    int weight;
     int e0;             // the first tile's blocks end here (at most j1)
     bool two;           // the second tile has tokens
     bool whole;         // the share holds the whole pair
@@ -274,7 +278,7 @@ struct Piece {
 
 struct Ctx {
     uint32_t base;
-    int64_t steps;      // of this share
+    int64_t weight;     // of this share
     int tq, tp, G;      // tokens of a tile and of a pair, heads of a group
     __device__ uint32_t bar(int b) const { return base + OFF_BAR + 8u * b; }
     __device__ bool wait(int b, uint32_t use) const { return mx_wait(bar(b), use & 1u); }
@@ -284,7 +288,9 @@ __device__ __forceinline__ Piece piece_at(const Ctx& x, const Cursor& u, int64_t
     Piece r;
     r.nb = blocks_seen(u.s, (u.pair + 1) * x.tp);
     r.j0 = u.j;
-    r.j1 = left < r.nb - u.j ? u.j + (int)left : r.nb;
+    const int own = u.j == 0 ? PIECE : 0;
+    r.j1 = left - own < r.nb - u.j ? u.j + (int)left - own : r.nb;
+    r.weight = r.j1 - u.j + own;
     r.two = u.pair * x.tp + x.tq < u.s.lq;
     r.e0 = r.two ? min(r.j1, blocks_seen(u.s, u.pair * x.tp + x.tq)) : r.j1;
     r.e0 = max(r.e0, r.j0);
@@ -323,9 +329,9 @@ __device__ bool load_warp(const AttnParams& p, const AttnMaps& maps, const Ctx& 
             if (++slot == RING) slot = 0, ++lap;
             return true;
         };
-        for (int64_t left = x.steps; left > 0 && ok; next_pair(p, x, u), ++pieces) {
+        for (int64_t left = x.weight; left > 0 && ok; next_pair(p, x, u), ++pieces) {
             const Piece r = piece_at(x, u, left);
-            left -= r.j1 - r.j0;
+            left -= r.weight;
             const int n = p.cache ? u.n : 0;
             for (int j = r.j0; j < r.j1 && ok; ++j) {
                 ok = tile(&maps.k, u.kh, u.s.k0 + j * KB, n) && tile(&maps.v, u.kh, u.s.k0 + j * KB, n);
@@ -387,11 +393,11 @@ __device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
         return r;
     };
     u.n = mx_uniform(u.n), u.kh = mx_uniform(u.kh), u.pair = mx_uniform(u.pair), u.j = mx_uniform(u.j);
-    for (int64_t left = x.steps; left > 0; next_pair(p, x, u), ++pieces) {
+    for (int64_t left = x.weight; left > 0; next_pair(p, x, u), ++pieces) {
         u.s.lq = mx_uniform(u.s.lq), u.s.lk = mx_uniform(u.s.lk);
         Piece r = piece_at(x, u, left);
         r.j0 = mx_uniform(r.j0), r.j1 = mx_uniform(r.j1), r.e0 = mx_uniform(r.e0);
-        left -= r.j1 - r.j0;
+        left -= r.weight;
         const int count = r.j1 - r.j0, c0 = r.e0 - r.j0;   // blocks; the first tile's
         // the values of block j have landed; those past the sequence's keys count for nothing,
         // whatever they hold
@@ -407,18 +413,23 @@ __device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
             }
             return true;
         };
+        // the keys in slot s, of block j, are used; after the last ones the queries are too
+        auto scored = [&](int j, int s) {
+            mx_commit(lead, x.bar(EMPTY + s));
+            if (j + 1 == count) mx_commit(lead, x.bar(QE));
+        };
         ok = x.wait(QF, pieces) && landed(0);
         if (!ok) break;
         if (!r.two) {
             // one tile: its scores alternate between the two places, so that the next block's are there
             // when the tile's softmax has done with this one's
             scores(0, 0, slot(0), SF);
-            mx_commit(lead, x.bar(EMPTY + slot(0)));
+            scored(0, slot(0));
             if (count > 1) {
                 ok = landed(2);
                 if (!ok) break;
                 scores(0, 1, slot(2), SX);
-                mx_commit(lead, x.bar(EMPTY + slot(2)));
+                scored(1, slot(2));
             }
 #pragma unroll 1
             for (int j = 0; j < count; ++j) {
@@ -437,13 +448,13 @@ __device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
                     ok = landed(2 * j + 4);
                     if (!ok) break;
                     scores(0, t, slot(2 * j + 4), t ? SX : SF);
-                    mx_commit(lead, x.bar(EMPTY + slot(2 * j + 4)));
+                    scored(j + 2, slot(2 * j + 4));
                 }
             }
         } else {
             if (c0 > 0) scores(0, 0, slot(0), SF);
             scores(1, 1, slot(0), SF + 1);
-            mx_commit(lead, x.bar(EMPTY + slot(0)));
+            scored(0, slot(0));
             ok = next_values(0);
 #pragma unroll 1
             for (int j = 0; ok; ++j) {
@@ -477,12 +488,11 @@ __device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
                 ok = next_values(j + 1);
                 if (!ok) break;
                 scores(1, 1, ks, SF + 1);
-                mx_commit(lead, x.bar(EMPTY + ks));
+                scored(j + 1, ks);
             }
         }
         if (!ok) break;
         it += 2 * count;
-        mx_commit(lead, x.bar(QE));
     }
     __syncwarp();
     mx_commit(lead, x.bar(DRAIN));
@@ -506,9 +516,9 @@ __device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const C
     const int tok = row / x.G, head = row - tok * x.G;
     uint32_t nS = 0, nX = 0, nO = 0, nV = 0;   // uses so far of SF, SX, OF and PV
     bool first_piece = true;
-    for (int64_t left = x.steps; left > 0; next_pair(p, x, u), first_piece = false) {
+    for (int64_t left = x.weight; left > 0; next_pair(p, x, u), first_piece = false) {
         const Piece r = piece_at(x, u, left);
-        left -= r.j1 - r.j0;
+        left -= r.weight;
         if (t == 1 && !r.two) continue;
         const int end = t ? r.j1 : r.e0;
         bool other = false;   // this block's scores are in the other tile's place
@@ -690,12 +700,12 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const AttnParams p,
     tc_fence_after();
     const uint32_t tmem = lds_u32(x.base + OFF_TMEM);
     const bool sound = tmem == 0 && x.base % 1024 == 0;   // (the tiles' swizzle counts from 1 KB boundaries)
-    x.steps = sound ? share.steps : 0;                    // (bad lengths have none)
+    x.weight = sound ? share.weight : 0;                  // (bad lengths have none)
     if (tid == 0) {
         if (blockIdx.x == 0) *p.status = share.bad ? KDA_DEVERR_CU_SEQLENS : 0u;
         if (!sound) atomicOr(p.status, KDA_DEVERR_INTERNAL);
         Cut c{};
-        if (x.steps > 0) c = Cut{u.j, blocks_seen(u.s, (u.pair + 1) * x.tp), u.s.q0, u.s.lq, u.kh, u.pair, {0, 0}};
+        if (x.weight > 0) c = Cut{u.j, blocks_seen(u.s, (u.pair + 1) * x.tp), u.s.q0, u.s.lq, u.kh, u.pair, {0, 0}};
         partials(p.workspace).cut[blockIdx.x] = c;
     }
     bool ok = true;
