@@ -106,7 +106,11 @@ __device__ __forceinline__ int blocks_seen(const Seq& s, int tokens) {
     return seen <= KB ? 1 : (seen - 1) / KB + 1;
 }
 
+// A sequence's pairs are taken from both ends in turn, 0, m - 1, 1, m - 2, ...: the number of blocks
+// grows with the pair, and two neighbours then have about as many as any others, so that shares of
+// a few whole pairs come out alike.
 __device__ __forceinline__ int pairs_of(const Seq& s, int tp) { return (s.lq + tp - 1) / tp; }
+__device__ __forceinline__ int pair_in_turn(int i, int m) { return i & 1 ? m - 1 - (i >> 1) : i >> 1; }
 
 // Weight of the sequence's first m pairs, m below pairs_of: the sum of PIECE + blocks_seen((j + 1) tp),
 // in closed form from the sum of residues modulo 128, which repeat after 128 / gcd(tp, 128) pairs.
@@ -128,14 +132,20 @@ __device__ __forceinline__ int64_t weight_of(const Seq& s, int tp) {
     return m == 0 ? 0 : weight_before(s.lq, s.lk, m - 1, tp) + PIECE + blocks_seen(s, s.lq);
 }
 
+// ... of the first i in turn; `all` is the weight of all m.
+__device__ __noinline__ int64_t weight_in_turn(int lq, int lk, int i, int tp, int m, int64_t all) {
+    const int64_t front = weight_before(lq, lk, (i + 1) >> 1, tp);
+    return i < 2 ? front : front + all - weight_before(lq, lk, m - (i >> 1), tp);
+}
+
 // Where share b of `ctas` equal ones starts (recip = 2^64 / ctas, rounded up: no division).
 __device__ __forceinline__ int64_t share_start(int64_t total, int b, int ctas, uint64_t recip) {
     return b == ctas ? total : (int64_t)__umul64hi((uint64_t)total * (uint64_t)b, recip);
 }
 
-// A step: pair `pair` of key head kh of sequence n, key block j of nb.
+// A step: pair `pair` (the turn-th to be taken) of key head kh of sequence n, key block j.
 struct Cursor {
-    int n, kh, pair, j;
+    int n, kh, turn, pair, j;
     Seq s;
 };
 
@@ -221,18 +231,20 @@ __device__ Share find_share(const AttnParams& p, int tq, int G, uint64_t recip, 
     at -= u.kh * f.each;
     if (at < 0) --u.kh, at += f.each;
     else if (at >= f.each) ++u.kh, at -= f.each;
-    int lo = 0, width = open ? 1 : pairs_of(u.s, tp);
+    const int m = open ? 1 : pairs_of(u.s, tp);
+    int lo = 0, width = m;
 #pragma unroll 1
     while (__syncthreads_or(width > 1)) {   // narrow [lo, lo + width)
         const int step = (width + AT_THREADS / 2 - 1) / (AT_THREADS / 2), c = lo + (tid % (AT_THREADS / 2)) * step;
-        const int64_t st = width > 1 && c < lo + width ? weight_before(u.s.lq, u.s.lk, c, tp) : at + 1;
+        const int64_t st = width > 1 && c < lo + width ? weight_in_turn(u.s.lq, u.s.lk, c, tp, m, f.each) : at + 1;
         if (st <= at) atomicMax(best + e, c);
         __syncthreads();
         const int b = best[e];
         if (c == b && st <= at) start[e] = st;
         if (width > 1) width = min(step, lo + width - b), lo = b;
     }
-    u.pair = lo;
+    u.turn = lo;
+    u.pair = pair_in_turn(lo, m);
     const int from = open ? 0 : (int)(at - start[e]);   // the pair's own weight is at its front
     u.j = max(from - PIECE, 0);
     // A cut near the end of a pair moves there: a pair that is cut costs its rows' partial results,
@@ -246,8 +258,10 @@ __device__ Share find_share(const AttnParams& p, int tq, int G, uint64_t recip, 
     }
     if (over) {   // the next pair
         u.j = 0;
-        if (++u.pair == pairs_of(u.s, tp)) {
-            u.pair = 0;
+        if (++u.turn < m) {
+            u.pair = pair_in_turn(u.turn, m);
+        } else {
+            u.turn = u.pair = 0;
             if (++u.kh == p.Hk) {
                 u.kh = 0;
                 while (++u.n < p.nseq) {
@@ -300,8 +314,10 @@ __device__ __forceinline__ Piece piece_at(const Ctx& x, const Cursor& u, int64_t
 
 __device__ __forceinline__ void next_pair(const AttnParams& p, const Ctx& x, Cursor& u) {
     u.j = 0;
-    if (++u.pair < pairs_of(u.s, x.tp)) return;
-    u.pair = 0;
+    const int m = pairs_of(u.s, x.tp);
+    u.pair = pair_in_turn(++u.turn, m);
+    if (u.turn < m) return;
+    u.turn = u.pair = 0;
     if (++u.kh < p.Hk) return;
     u.kh = 0;
     do {
@@ -392,7 +408,7 @@ __device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
         tc_fence_after();
         return r;
     };
-    u.n = mx_uniform(u.n), u.kh = mx_uniform(u.kh), u.pair = mx_uniform(u.pair), u.j = mx_uniform(u.j);
+    u.n = mx_uniform(u.n), u.kh = mx_uniform(u.kh), u.turn = mx_uniform(u.turn), u.pair = mx_uniform(u.pair), u.j = mx_uniform(u.j);
     for (int64_t left = x.weight; left > 0; next_pair(p, x, u), ++pieces) {
         u.s.lq = mx_uniform(u.s.lq), u.s.lk = mx_uniform(u.s.lk);
         Piece r = piece_at(x, u, left);
