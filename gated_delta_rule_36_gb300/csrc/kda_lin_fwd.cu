@@ -19,8 +19,9 @@
 // it.  Where the unit lies in two shares, the first one takes its part of that unit first of all
 // and publishes the state, and the second one takes its part last of all, when the state has
 // long been there: no chunk is read twice and nobody waits.  Units that lie in more than two
-// shares (few heads, long prompts) would make a chain of waits; for them a first launch
-// (kStateOnly) sums v k^T over each share's part, and the second starts from their decayed sum.
+// shares (few heads, long prompts) would make a chain of waits; there every share first sums k v^T
+// over its last chunks, if the unit goes on behind them (kSum: keys and values only, and K' made by
+// two more groups), publishes that, and starts its own chunks from the decayed sums before it.
 //
 // Warp roles: warps 0-3 turn W into P and scale O (thread = token row); warps 4-7 write the
 // output out; warps 8-11 carry the state (thread = key channel); warps 12-15 and 16-19 make K',
@@ -47,14 +48,15 @@ constexpr uint32_t OFF_S = 2 * STAGE;
 // alone (a short chunk puts its own weights there)
 constexpr uint32_t OFF_POW = OFF_S + TILE, OFF_KPOW = OFF_POW + 4 * 256;
 constexpr uint32_t OFF_BAR = OFF_KPOW + 8 * 128;
+// (the barriers; then as many for the chunks that are only summed)
 enum { FQ = 0, FK = 2, FV = 4, EQ = 6, EK = 8, EV = 10, KPF = 12, KPE = 16, VR = 20, WF = 22, PF, QSF, OS, OF, OE, KVF, KVE, SB, DRAIN, DRAIN2, NBAR };
-constexpr uint32_t OFF_TMEM = OFF_BAR + NBAR * 8, OFF_SEG = OFF_TMEM + 8;
-constexpr uint32_t LF_SMEM = OFF_SEG + 3 * 24;   // no room to align the base: it has to be (and is checked to be) 1 KB aligned
+constexpr uint32_t OFF_TMEM = OFF_BAR + 2 * NBAR * 8, OFF_SEG = OFF_TMEM + 8;
+constexpr uint32_t LF_SMEM = OFF_SEG + 5 * 24;   // no room to align the base: it has to be (and is checked to be) 1 KB aligned
 static_assert(LF_SMEM <= 232448, "one CTA's shared memory");
 // Tensor Memory columns (all are allocated, so that its address is 0): W then P; KV; O; two slots of K' (32 tokens: three terms of 16 columns)
 constexpr uint32_t TM_W = 0, TM_KV = 128, TM_O = 256, TM_KP = 384, KP_SLOT = 48;
 
-// The launch that only sums needs no W: its place takes two more slots, for two more groups.
+// Summing alone needs no W: its place takes two more slots, for two more groups.
 __device__ __forceinline__ uint32_t kp_slot(int s) { return s < 2 ? TM_KP + s * KP_SLOT : TM_W + (s - 2) * KP_SLOT; }
 
 struct LinMaps {
@@ -204,6 +206,7 @@ __device__ Share find_share(const LinParams& p, uint64_t recip, int64_t* scratch
     return s;
 }
 
+template <bool kSum>
 struct Ctx {
     uint32_t base;         // shared-window address
     int count;             // chunks to do (a GPU's memory holds fewer than 2^31 in all)
@@ -211,26 +214,28 @@ struct Ctx {
     // the unit that the share before began
     int nA, nAB;
     const Cursor* seg;     // where the three parts start (in shared memory)
-    __device__ uint32_t bar(int b) const { return base + OFF_BAR + 8u * b; }
+    __device__ uint32_t bar(int b) const { return base + OFF_BAR + 8u * (b + (kSum ? NBAR : 0)); }
     __device__ bool wait(int b, int use) const { return mx_wait(bar(b), (uint32_t)use & 1u); }
 };
 
-__device__ __forceinline__ Cursor first_chunk(const Ctx& x) { return x.seg[x.nA > 0 ? 0 : x.nAB > 0 ? 1 : 2]; }
+template <bool kSum>
+__device__ __forceinline__ Cursor first_chunk(const Ctx<kSum>& x) { return x.seg[x.nA > 0 ? 0 : x.nAB > 0 ? 1 : 2]; }
 // From chunk i of the share to chunk i + 1.
-__device__ __forceinline__ void advance(const LinParams& p, const Ctx& x, Cursor& u, int i) {
+template <bool kSum>
+__device__ __forceinline__ void advance(const LinParams& p, const Ctx<kSum>& x, Cursor& u, int i) {
     if (i + 1 == x.nA || i + 1 == x.nAB) u = x.seg[i + 1 < x.nAB ? 1 : 2];
     else next_chunk(p, u);
 }
 
 // Workspace: a partial or published state for each share, then a flag for each.
 __device__ __forceinline__ float* share_state(const LinParams& p, int b) { return static_cast<float*>(p.workspace) + (size_t)b * HD * HD; }
-__device__ __forceinline__ uint32_t* share_flag(const LinParams& p, int b) {
+__host__ __device__ __forceinline__ uint32_t* share_flag(const LinParams& p, int b) {
     return reinterpret_cast<uint32_t*>(static_cast<float*>(p.workspace) + (size_t)LF_MAX_CTAS * HD * HD) + b;
 }
 
 // ---------------------------------------------------------------- warp 20: loads
-template <bool kStateOnly>
-__device__ bool load_warp(const LinParams& p, const LinMaps& maps, const Ctx& x) {
+template <bool kSum>
+__device__ bool load_warp(const LinParams& p, const LinMaps& maps, const Ctx<kSum>& x) {
     bool ok = true;
     if ((threadIdx.x & 31) == 0) {
         Cursor u = first_chunk(x);
@@ -245,13 +250,13 @@ __device__ bool load_warp(const LinParams& p, const LinMaps& maps, const Ctx& x)
             return true;
         };
         for (int i = 0; i < x.count && ok; advance(p, x, u, i), ++i) {
-            if (!kStateOnly && u.c == 0 && p.init_state) {   // the state warps will want it soon
+            if (!kSum && u.c == 0 && p.init_state) {   // the state warps will want it soon
                 const uint32_t bytes = HD * HD * (p.init_f32 ? 4 : 2);
                 const char* from = static_cast<const char*>(p.init_state) + ((size_t)u.n * p.H + u.h) * bytes;
                 asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(bytes) : "memory");
             }
             ok = one(i, FK, EK, &maps.k, TILE);
-            if (!kStateOnly) ok = ok && one(i, FQ, EQ, &maps.q, 0);
+            if (!kSum) ok = ok && one(i, FQ, EQ, &maps.q, 0);
             ok = ok && one(i, FV, EV, &maps.v, 2 * TILE);
         }
     }
@@ -266,13 +271,14 @@ constexpr uint32_t ID_KK = make_idesc_bf16_f32(128, 128);          // both opera
 constexpr uint32_t ID_MN = make_idesc_bf16_f32(128, 128, true);    // B MN-major
 
 // the MMAs in flight finish before the CTA frees Tensor Memory
-__device__ __forceinline__ bool drain_mma(const Ctx& x, uint32_t lead, int bar) {
+template <bool kSum>
+__device__ __forceinline__ bool drain_mma(const Ctx<kSum>& x, uint32_t lead, int bar) {
     __syncwarp();
     mx_commit(lead, x.bar(bar));
     return x.wait(bar, 0);
 }
 
-__device__ bool mma_out_warp(const Ctx& x) {
+__device__ bool mma_out_warp(const Ctx<false>& x) {
     const uint32_t lead = mx_leader();
     const int count = mx_uniform(x.count);
     const uint64_t dQ = make_sdesc_kmajor_sw128(x.base), dS = make_sdesc_mnmajor_sw128(x.base + OFF_S, HALF, 1024);
@@ -312,8 +318,8 @@ __device__ bool mma_out_warp(const Ctx& x) {
 }
 
 // KV = K'^T V, 32 tokens at a time as the key warps hand them over
-template <bool kStateOnly>
-__device__ bool mma_state_warp(const Ctx& x) {
+template <bool kSum>
+__device__ bool mma_state_warp(const Ctx<kSum>& x) {
     const uint32_t lead = mx_leader();
     const int count = mx_uniform(x.count);
     const uint64_t dV = make_sdesc_mnmajor_sw128(x.base + 2 * TILE, HALF, 1024);
@@ -324,8 +330,8 @@ __device__ bool mma_state_warp(const Ctx& x) {
         if (!ok) break;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            const int slot = kStateOnly ? b : b & 1;
-            ok = ok && mx_wait_lane(x.bar(KPF + slot), kStateOnly ? i & 1u : (uint32_t)(b >> 1));
+            const int slot = kSum ? b : b & 1;
+            ok = ok && mx_wait_lane(x.bar(KPF + slot), kSum ? i & 1u : (uint32_t)(b >> 1));
             if (!ok) break;
             tc_fence_after();
             const uint64_t v = dV + s * D_STAGE + 2 * b * MN_STEP;
@@ -344,7 +350,7 @@ __device__ bool mma_state_warp(const Ctx& x) {
 }
 
 // ---------------------------------------------------------------- warps 0-3: P and the scale of O
-__device__ bool score_warps(const LinParams& p, const Ctx& x) {
+__device__ bool score_warps(const LinParams& p, const Ctx<false>& x) {
     Cursor u = first_chunk(x);
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(32 * warp) << 16;
@@ -428,7 +434,7 @@ __device__ bool score_warps(const LinParams& p, const Ctx& x) {
 }
 
 // ---------------------------------------------------------------- warps 4-7: the output
-__device__ bool out_warps(const LinParams& p, const LinMaps& maps, const Ctx& x) {
+__device__ bool out_warps(const LinParams& p, const LinMaps& maps, const Ctx<false>& x) {
     Cursor u = first_chunk(x);
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(32 * warp) << 16;
@@ -494,8 +500,8 @@ __device__ __forceinline__ void load_state(const T* s, float2 (&S)[LF_C / 2]) {
     for (int v = 0; v < LF_C / 2; ++v) S[v] = make_float2((float)__ldg(s + (2 * v) * HD), (float)__ldg(s + (2 * v + 1) * HD));
 }
 
-template <bool kStateOnly>
-__device__ bool state_warps(const LinParams& p, const Ctx& x, const Share& share, uint64_t recip) {
+template <bool kSum>
+__device__ bool state_warps(const LinParams& p, const Ctx<kSum>& x, const Share& share, uint64_t recip) {
     Cursor u = first_chunk(x);
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, k = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(32 * warp) << 16;
@@ -509,6 +515,12 @@ __device__ bool state_warps(const LinParams& p, const Ctx& x, const Share& share
         if (lane == 0) asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(share_flag(p, blockIdx.x)) : "memory");
         publish = false;
     };
+    auto published = [&](int b) {   // by all four warps of share b
+        const uint32_t* flag = share_flag(p, b);
+        uint32_t seen = 0, polls = 0;
+        while (seen != 4 && ++polls < MX_POLLS) asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(flag) : "memory");
+        return (bool)__all_sync(0xffffffffu, seen == 4);
+    };
     for (int i = 0; i < x.count; advance(p, x, u, i), ++i) {
         const int valid = chunk_tokens(u);
         const size_t unit = (size_t)u.n * p.H + u.h;
@@ -516,18 +528,15 @@ __device__ bool state_warps(const LinParams& p, const Ctx& x, const Share& share
             fresh = false;
             l2 = log2_decay(p, u.h);
             all = exp2f(l2 * (float)LF_C);
-            if (!kStateOnly && u.c > 0 && i >= x.nAB) {
-                // the share before published this unit's state: its four warps have arrived at its flag
-                const uint32_t* flag = share_flag(p, blockIdx.x - 1);
-                uint32_t seen = 0, polls = 0;
-                while (seen != 4 && ++polls < MX_POLLS) asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(flag) : "memory");
-                if (!__all_sync(0xffffffffu, seen == 4)) return false;
+            if (!kSum && u.c > 0 && i >= x.nAB) {
+                // the share before published this unit's state
+                if (!published(blockIdx.x - 1)) return false;
                 const float* s = share_state(p, blockIdx.x - 1) + k;
 #pragma unroll
                 for (int v = 0; v < LF_C / 2; ++v) S[v] = make_float2(__ldcg(s + (2 * v) * HD), __ldcg(s + (2 * v + 1) * HD));
             } else {
                 const size_t off = unit * HD * HD + k;
-                if (kStateOnly || p.init_state == nullptr) {
+                if (kSum || p.init_state == nullptr) {
 #pragma unroll
                     for (int v = 0; v < LF_C / 2; ++v) S[v] = make_float2(0.f, 0.f);
                 } else if (p.init_f32) {
@@ -535,7 +544,7 @@ __device__ bool state_warps(const LinParams& p, const Ctx& x, const Share& share
                 } else {
                     load_state(static_cast<const __nv_bfloat16*>(p.init_state) + off, S);
                 }
-                if (!kStateOnly && u.c > 0) {
+                if (!kSum && u.c > 0) {
                     // decayed to here, plus what the shares before this one summed over the unit's chunks
                     const float f = exp2f(l2 * (float)u.c * (float)LF_C);
 #pragma unroll
@@ -545,6 +554,7 @@ __device__ bool state_warps(const LinParams& p, const Ctx& x, const Share& share
                         const int64_t end = share_start(share.total, b + 1, gridDim.x, recip) - share.unit;   // chunks up to there
                         if (end <= 0) break;
                         if (share_start(share.total, b, gridDim.x, recip) - share.unit == end) continue;
+                        if (!published(b)) return false;
                         const float g = exp2f(l2 * (float)(u.c - end) * (float)LF_C);
                         const float* part = share_state(p, b) + k;
 #pragma unroll
@@ -556,7 +566,7 @@ __device__ bool state_warps(const LinParams& p, const Ctx& x, const Share& share
                 }
             }
         }
-        if (!kStateOnly) {
+        if (!kSum) {
             // the bf16 copy of the state, once the previous product with it is done
             if (i > 0 && !x.wait(QSF, i - 1)) return false;
             const uint32_t tile = x.base + OFF_S + k * 128;
@@ -584,8 +594,8 @@ __device__ bool state_warps(const LinParams& p, const Ctx& x, const Share& share
         }
         tc_fence_before();
         mx_arrive_warp(x.bar(KVE));
-        if (!kStateOnly && publish) announce();   // a chunk later: its stores have long been done
-        if (kStateOnly ? i + 1 == x.count : i + 1 == x.nA) {
+        if (!kSum && publish) announce();   // a chunk later: its stores have long been done
+        if (kSum ? i + 1 == x.count : i + 1 == x.nA) {
             // this share's part of a unit that the next share goes on with
             float* part = share_state(p, blockIdx.x) + k;
 #pragma unroll
@@ -595,7 +605,7 @@ __device__ bool state_warps(const LinParams& p, const Ctx& x, const Share& share
             }
             publish = true;
             fresh = true;
-        } else if (!kStateOnly && u.c + 1 == u.nc) {
+        } else if (!kSum && u.c + 1 == u.nc) {
             fresh = true;
             if (p.final_state) {
                 const size_t off = unit * HD * HD + k;
@@ -617,19 +627,19 @@ __device__ bool state_warps(const LinParams& p, const Ctx& x, const Share& share
             }
         }
     }
-    if (!kStateOnly && publish) announce();
+    if (publish) announce();
     return true;
 }
 
 // ---------------------------------------------------------------- warps 12-19: K'
 // Thread k reads column k of the key tile, weighs it by a^(C-1-j) and leaves each value as a
 // sum of three bf16 in lane k of Tensor Memory, 32 tokens at a time; group g takes the parts
-// g and g + 2 of each chunk and owns slot g.  (In the launch that only sums, the warps of the
+// g and g + 2 of each chunk and owns slot g.  (While chunks are only summed, the warps of the
 // scores and of the output are groups 2 and 3, and each group takes one part.)
 __device__ __forceinline__ float2 unpack2(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
 
-template <bool kStateOnly>
-__device__ bool key_warps(const LinParams& p, const Ctx& x, int g) {
+template <bool kSum>
+__device__ bool key_warps(const LinParams& p, const Ctx<kSum>& x, int g) {
     Cursor u = first_chunk(x);
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, k = threadIdx.x & 127;
     const uint32_t kp = ((uint32_t)(32 * warp) << 16) + kp_slot(g);
@@ -666,8 +676,8 @@ __device__ bool key_warps(const LinParams& p, const Ctx& x, int g) {
         }
         bool ok = true;
 #pragma unroll 1
-        for (int b = g; b < 4; b += kStateOnly ? 4 : 2) {
-            const int use = kStateOnly ? i : 2 * i + (b >> 1);
+        for (int b = g; b < 4; b += kSum ? 4 : 2) {
+            const int use = kSum ? i : 2 * i + (b >> 1);
             uint32_t kt = x.base + s * STAGE + TILE + (k >> 6) * HALF + (k & 7) * 2 + 32 * b * 128;
             float f = b == 3 ? 1.f : b == 2 ? hop : b == 1 ? hop * hop : hop * hop * hop;   // a^(96 - 32 b)
             if (!full) {
@@ -739,21 +749,27 @@ __device__ void empty_units(const LinParams& p) {
     }
 }
 
-template <bool kStateOnly>
+template <bool kSum>
+__device__ __forceinline__ void init_barriers(const Ctx<kSum>& x, int lane) {
+    for (int b = lane; b < NBAR; b += 32) {
+        const bool warps = b == EQ || b == EQ + 1 || (b >= KPF && b < KPF + 4) || b == VR || b == VR + 1 || b == PF || b == OS || b == OE || b == SB || b == KVE;
+        const bool both = b == EK || b == EK + 1;   // the key tile: W's MMA and the key warps
+        const bool twice = b == EV || b == EV + 1;  // the value tile: KV's and P V's MMAs
+        mbar_init(x.bar(b), warps ? 4 : both ? (kSum ? 16 : 9) : twice ? (kSum ? 1 : 2) : 1);
+    }
+}
+
 __global__ void __launch_bounds__(LF_THREADS, 1) lin_fwd_kernel(const LinParams p, const __grid_constant__ LinMaps maps, uint64_t recip) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const int tid = threadIdx.x, warp = mx_uniform(tid >> 5);
-    Ctx x;
-    x.base = smem_u32(smem_raw);
+    Ctx<false> x;   // the share's chunks
+    Ctx<true> y;    // those that are summed before
+    x.base = y.base = smem_u32(smem_raw);
     if (warp == 20) {
+        init_barriers(x, tid & 31);
+        init_barriers(y, tid & 31);
+        mbar_fence_init();
         if ((tid & 31) == 0) {
-            for (int b = 0; b < NBAR; ++b) {
-                const bool warps = b == EQ || b == EQ + 1 || (b >= KPF && b < KPF + 4) || b == VR || b == VR + 1 || b == PF || b == OS || b == OE || b == SB || b == KVE;
-                const bool both = b == EK || b == EK + 1;   // the key tile: W's MMA and the key warps
-                const bool twice = b == EV || b == EV + 1;  // the value tile: KV's and P V's MMAs
-                mbar_init(x.bar(b), warps ? 4 : both ? (kStateOnly ? 16 : 9) : twice ? (kStateOnly ? 1 : 2) : 1);
-            }
-            mbar_fence_init();
             tma_prefetch_desc(&maps.q);
             tma_prefetch_desc(&maps.k);
             tma_prefetch_desc(&maps.v);
@@ -765,71 +781,75 @@ __global__ void __launch_bounds__(LF_THREADS, 1) lin_fwd_kernel(const LinParams 
     }
     tc_fence_before();
     const Share share = find_share(p, recip, reinterpret_cast<int64_t*>(smem_raw + OFF_S));
-    if (!kStateOnly && share.empties && !share.bad) empty_units(p);
+    if (share.empties && !share.bad) empty_units(p);
     Cursor* seg = reinterpret_cast<Cursor*>(smem_raw + OFF_SEG);
     x.seg = seg;
-    x.nA = x.nAB = x.count = 0;
-    if (kStateOnly) {
-        if (tid == 0) *share_flag(p, blockIdx.x) = 0u;
-        if (share.cut && !share.tail) {   // the share's last chunks, of a unit in more than two shares
-            const int64_t own = share.x1 - share.x0;
-            x.nAB = x.count = own < share.end.c ? (int)own : share.end.c;
-            if (tid == 0) seg[1] = share.end, seg[1].c -= x.count;
+    y.seg = seg + 2;   // (its one part is number 1; number 2 is only read)
+    x.count = (int)(share.x1 - share.x0);
+    x.nA = share.tail ? share.end.c : 0;
+    x.nAB = x.count - (share.head ? share.first.nc - share.first.c : 0);
+    // the share's last chunks, of a unit in more than two shares
+    y.nA = 0;
+    y.nAB = y.count = share.cut && !share.tail ? min(x.count, share.end.c) : 0;
+    if (tid == 0) {
+        seg[0] = share.end, seg[0].c = 0;
+        seg[1] = seg[2] = share.first;
+        if (share.head) {
+            seg[1].c = seg[1].nc - 1;
+            if (x.nAB > x.nA) next_chunk(p, seg[1]);
         }
-    } else {
-        x.count = (int)(share.x1 - share.x0);
-        x.nA = share.tail ? share.end.c : 0;
-        x.nAB = x.count - (share.head ? share.first.nc - share.first.c : 0);
-        if (tid == 0) {
-            seg[0] = share.end, seg[0].c = 0;
-            seg[1] = seg[2] = share.first;
-            if (share.head) {
-                seg[1].c = seg[1].nc - 1;
-                if (x.nAB > x.nA) next_chunk(p, seg[1]);
-            }
-        }
+        seg[3] = share.end, seg[3].c -= y.count;
     }
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = lds_u32(x.base + OFF_TMEM);
     const bool sound = tmem == 0 && x.base % 1024 == 0;   // (the tiles' swizzle counts from 1 KB boundaries)
     if (tid == 0) {
-        if (!kStateOnly && blockIdx.x == 0) *p.status = share.bad ? KDA_DEVERR_CU_SEQLENS : 0u;
-        if (!kStateOnly && !sound) atomicOr(p.status, KDA_DEVERR_INTERNAL);
+        if (blockIdx.x == 0) *p.status = share.bad ? KDA_DEVERR_CU_SEQLENS : 0u;
+        if (!sound) atomicOr(p.status, KDA_DEVERR_INTERNAL);
     }
-    if (!sound) x.count = 0;   // (bad lengths have no chunks)
+    if (!sound) x.count = y.count = 0;   // (bad lengths have no chunks)
     bool ok = true;
-    // registers a thread: 80 at launch; 64 + 56 + 168 + 72 + 72 + 48 of the 6 x 80 that the block holds,
-    // or 72 + 72 + 152 + 72 + 72 + 40
+    // registers a thread: 80 at launch; of the 6 x 80 that the block holds 72 + 72 + 144 + 72 + 72 + 48
+    // while it only sums, then 64 + 56 + 168 + 72 + 72 + 48.  (The last group keeps its 48: with 40 first and
+    // an increase after, the compiler gave its loops fewer, and eight prompts of 1k to 9k took 579 us, not 547.)
+    if (y.count > 0) {
+        if (warp < 8) {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+            ok = key_warps<true>(p, y, 2 + (warp >> 2));
+        } else if (warp < 12) {
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+            ok = state_warps<true>(p, y, share, recip);
+        } else if (warp < 20) {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+            ok = key_warps<true>(p, y, (warp - 12) >> 2);
+        } else {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+            if (warp == 20) ok = load_warp<true>(p, maps, y);
+            else if (warp == 22) ok = mma_state_warp<true>(y);
+        }
+        tc_fence_before();
+        ok = __syncthreads_and(ok);
+        tc_fence_after();
+        if (!ok) x.count = 0;
+    }
     if (warp < 4) {
-        if (kStateOnly) {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-            ok = key_warps<kStateOnly>(p, x, 2);
-        } else {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-            ok = score_warps(p, x);
-        }
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        ok = score_warps(p, x) && ok;
     } else if (warp < 8) {
-        if (kStateOnly) {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-            ok = key_warps<kStateOnly>(p, x, 3);
-        } else {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-            ok = out_warps(p, maps, x);
-        }
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        ok = out_warps(p, maps, x) && ok;
     } else if (warp < 12) {
-        if (kStateOnly) asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
-        else asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
-        ok = state_warps<kStateOnly>(p, x, share, recip);
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+        ok = state_warps<false>(p, x, share, recip) && ok;
     } else if (warp < 20) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        ok = key_warps<kStateOnly>(p, x, (warp - 12) >> 2);
+        ok = key_warps<false>(p, x, (warp - 12) >> 2) && ok;
     } else {
-        if (kStateOnly) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-        if (warp == 20) ok = load_warp<kStateOnly>(p, maps, x);
-        else if (warp == 21 && !kStateOnly) ok = mma_out_warp(x);
-        else if (warp == 22) ok = mma_state_warp<kStateOnly>(x);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        if (warp == 20) ok = load_warp<false>(p, maps, x) && ok;
+        else if (warp == 21) ok = mma_out_warp(x) && ok;
+        else if (warp == 22) ok = mma_state_warp<false>(x) && ok;
     }
     if (!ok) mx_report(p.status);
     tc_fence_before();
@@ -859,25 +879,21 @@ cudaError_t launch_lin_fwd(const LinParams& p, cudaStream_t stream) {
     int ctas = sms < LF_MAX_CTAS ? sms : LF_MAX_CTAS;
     if (most < ctas) ctas = most > 0 ? (int)most : 1;
     const uint64_t recip = ctas > 1 ? ~0ull / (uint64_t)ctas + 1 : 0;
-    for (auto k : {lin_fwd_kernel<true>, lin_fwd_kernel<false>}) {
-        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LF_SMEM);
-        if (e != cudaSuccess) return e;
-        // cooperative: a share may wait for the state that the share before it publishes, so all of
-        // them are resident
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeCooperative;
-        attr[0].val.cooperative = 1;
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3((unsigned)ctas);
-        cfg.blockDim = dim3(LF_THREADS);
-        cfg.dynamicSmemBytes = LF_SMEM;
-        cfg.stream = stream;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, k, p, maps, recip);
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
+    e = cudaFuncSetAttribute(lin_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LF_SMEM);
+    if (e == cudaSuccess) e = cudaMemsetAsync(share_flag(p, 0), 0, (size_t)ctas * sizeof(uint32_t), stream);
+    if (e != cudaSuccess) return e;
+    // cooperative: a share may wait for what the shares before it publish, so all of them are resident
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(LF_THREADS);
+    cfg.dynamicSmemBytes = LF_SMEM;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, lin_fwd_kernel, p, maps, recip);
 }
 
 }  // namespace kda
