@@ -636,7 +636,7 @@ __device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const C
             } else {
                 // 64 channels at a time through the warp's stage; then one tensor store of the warp's rows
                 // if they are whole tokens and all there, or eight lanes a row
-                const float inv = l > 0.f ? 1.f / l : 0.f;
+                const float inv = l == 0.f ? 0.f : 1.f / l;
                 const float2 inv2 = make_float2(inv, inv);
                 const bool tensor = mask == 0xffffffffu && x.G <= 32 && (x.G & (x.G - 1)) == 0;
                 const unsigned long long dst = reinterpret_cast<unsigned long long>(p.out.data + q * p.out.row + h * p.out.head);
@@ -679,7 +679,7 @@ __device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const C
         }
         if (mine) {
             if (!r.whole) part.ml[part_slot * 256 + part_row] = make_float2(m * c, l);
-            else if (p.lse) p.lse[q * p.Hq + h] = l > 0.f ? (m * c + log2f(l)) * 0.6931471805599453f : -INFINITY;
+            else if (p.lse) p.lse[q * p.Hq + h] = l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.6931471805599453f;
         }
     }
     if (lane == 0) bulk_wait_all();
@@ -788,13 +788,13 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParam
             const int s = s0 + lane;
             float2 ml = make_float2(-INFINITY, 0.f);
             if (s < end && (s == b || part.cut[s].nb != 0)) ml = part.ml[slot(s) * 256 + row];
-            float top = ml.y > 0.f ? ml.x : -INFINITY;   // a part that saw no key has a sum of 0
+            float top = ml.y != 0.f ? ml.x : -INFINITY;   // a part that saw no key has a sum of 0 (a NaN goes on into the results)
 #pragma unroll 1
             for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
             top = fmaxf(top, m);
             const float old = m == -INFINITY ? 0.f : exp2f(m - top);
             m = top;
-            const float w = ml.y > 0.f ? exp2f(ml.x - m) : 0.f;
+            const float w = ml.y != 0.f ? exp2f(ml.x - m) : 0.f;
             l = fmaf(l, old, w * ml.y);
             o.x *= old, o.y *= old, o.z *= old, o.w *= old;
             const int n = min(32, end - s0);
@@ -820,12 +820,12 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParam
         }
 #pragma unroll 1
         for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
         const int64_t q = c.q0 + i;
         const int h = c.kh * G + head;
         *reinterpret_cast<uint2*>(p.out.data + q * p.out.row + h * p.out.head + 4 * lane) =
             make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-        if (p.lse && lane == 0) p.lse[q * p.Hq + h] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        if (p.lse && lane == 0) p.lse[q * p.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
     }
 }
 
