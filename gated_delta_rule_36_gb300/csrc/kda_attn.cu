@@ -551,6 +551,8 @@ __device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const C
 #pragma unroll
             for (int b = 0; b < 4; ++b) tmem_ld32(tS + 32 * b, reinterpret_cast<uint32_t(&)[32]>(s[32 * b]));
             tmem_wait_ld();
+#pragma unroll
+            for (int b = 0; b < 4; ++b) mx_loaded(reinterpret_cast<uint32_t(&)[32]>(s[32 * b]));
             const int seen = last - j * KB;   // columns 0 .. seen
             if (__any_sync(0xffffffffu, seen < KB - 1)) {
 #pragma unroll
@@ -626,6 +628,7 @@ __device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const C
                     uint32_t w[32];
                     tmem_ld32(tO + 32 * b, w);
                     tmem_wait_ld();
+                    mx_loaded(w);
                     if (mine) {
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
@@ -645,6 +648,7 @@ __device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const C
                     uint32_t w[32];
                     tmem_ld32(tO + 32 * b, w);
                     tmem_wait_ld();
+                    mx_loaded(w);
 #pragma unroll
                     for (int k = 0; k < 32; k += 2) {
                         const float2 y = __fmul2_rn(make_float2(mx_u2f(w[k]), mx_u2f(w[k + 1])), inv2);

@@ -383,6 +383,7 @@ __device__ bool score_warps(const LinParams& p, const Ctx<false>& x) {
             const float f = e == 0 ? left : e == 1 ? left * hop : left * hop * hop;
             const float2 f2 = make_float2(f, f);
             tmem_wait_ld();
+            mx_loaded(w);
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
                 const float4 c = lds_f32x4(pow + 4 * j);
@@ -395,6 +396,7 @@ __device__ bool score_warps(const LinParams& p, const Ctx<false>& x) {
         }
         tmem_ld32(lanes + TM_W + 32 * warp, w);
         tmem_wait_ld();
+        mx_loaded(w);
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {   // a^(lane - j) is power 31 - lane + j of the table, zeros follow
             const float a0 = mx_u2f(w[j]) * (p.scale * lds_f32(pow + 4 * (31 + j) - 4 * lane));
@@ -418,6 +420,7 @@ __device__ bool score_warps(const LinParams& p, const Ctx<false>& x) {
             uint32_t w[32];
             tmem_ld32(lanes + TM_O + 32 * b, w);
             tmem_wait_ld();
+            mx_loaded(w);
 #pragma unroll
             for (int j = 0; j < 32; j += 2) {
                 const float2 y = __fmul2_rn(make_float2(mx_u2f(w[j]), mx_u2f(w[j + 1])), s2);
@@ -455,6 +458,7 @@ __device__ bool out_warps(const LinParams& p, const LinMaps& maps, const Ctx<fal
             uint32_t w[32];
             tmem_ld32(lanes + TM_O + 32 * b, w);
             tmem_wait_ld();
+            mx_loaded(w);
             uint32_t o[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) o[j] = pack_bf16x2(mx_u2f(w[2 * j]), mx_u2f(w[2 * j + 1]));
@@ -588,6 +592,7 @@ __device__ bool state_warps(const LinParams& p, const Ctx<kSum>& x, const Share&
             uint32_t w[16];
             tmem_ld16(lanes + TM_KV + 16 * b, w);
             tmem_wait_ld();
+            mx_loaded(w);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 S[8 * b + j] = __ffma2_rn(ac2, S[8 * b + j], make_float2(mx_u2f(w[2 * j]), mx_u2f(w[2 * j + 1])));

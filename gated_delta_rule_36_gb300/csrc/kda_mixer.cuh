@@ -138,6 +138,17 @@ __device__ __forceinline__ void mx_commit(uint32_t leader, uint32_t bar) {
         : "memory");
 }
 
+// No use of these registers, which a load from Tensor Memory wrote, moves above this point (behind
+// its wait).
+__device__ __forceinline__ void mx_loaded(uint32_t (&r)[16]) {
+    asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                      "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
+__device__ __forceinline__ void mx_loaded(uint32_t (&r)[32]) {
+    mx_loaded(reinterpret_cast<uint32_t(&)[16]>(r[0]));
+    mx_loaded(reinterpret_cast<uint32_t(&)[16]>(r[16]));
+}
+
 // 4 consecutive 32-bit TMEM columns of this thread's lane.
 __device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
