@@ -408,7 +408,7 @@ def _device(t, name):
 
 def _stream(stream, device):
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(device)   # (a Stream object would cost a microsecond)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
