@@ -7,15 +7,19 @@
 // It stays with one token for up to kRows heads, loads all their rows at once and reads the
 // token's position, table row and weight once for them.
 //
-// Bound by HBM: each row is read once and written once.
+// Bound by HBM: each row is read once and written once, past the caches.  What it takes is bytes in
+// flight: 28 warps an SM with eight rows a half-warp are 112 KB of loads.  32,768 tokens x 72 heads
+// (1.22 GB): 208 us, 5.9 TB/s (blocks of 128 threads, 7 an SM; with 6 218, with 8, which spill,
+// 244; 256 threads at 3 an SM 225; plain instead of streaming loads and stores 10 % slower each).
 #include "kda_device.cuh"
 #include "kda_ops.h"
 
 namespace kda {
 namespace {
 
-constexpr int NR_THREADS = 256;
+constexpr int NR_THREADS = 128;
 constexpr int NR_HALVES = NR_THREADS / 16;
+constexpr int NR_BLOCKS = 7;   // an SM: 72 registers a thread
 
 __device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
     const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
@@ -25,7 +29,7 @@ __device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
 
 // groups[i]: groups of kRows heads of q (0) and k (1), the last one possibly partial
 template <bool kInterleaved, int kRows>
-__global__ void __launch_bounds__(NR_THREADS) norm_rope_kernel(const NormRopeParams p, int groups_q, int groups) {
+__global__ void __launch_bounds__(NR_THREADS, NR_BLOCKS) norm_rope_kernel(const NormRopeParams p, int groups_q, int groups) {
     const int lane = threadIdx.x & 15;
     const int64_t item = (int64_t)blockIdx.x * NR_HALVES + (threadIdx.x >> 4);
     const int64_t t = item / groups;
@@ -127,8 +131,8 @@ cudaError_t launch_norm_rope(const NormRopeParams& p, cudaStream_t stream) {
     const int64_t rows = p.tokens * (p.heads[0] + p.heads[1]);
     if (rows == 0) return cudaSuccess;
     // Rows a half-warp takes: eight once that still gives every SM a few blocks (32,768 tokens x 72
-    // heads: 203 us, against 222 with four and 305 with two), else one, for the latency of small calls.
-    if (rows >= 152 * 4 * NR_HALVES * 8) return launch<8>(p, stream);
+    // heads: 208 us, against 238 with four and 305 with two), else one, for the latency of small calls.
+    if (rows >= 152 * NR_BLOCKS * NR_HALVES * 8) return launch<8>(p, stream);
     return launch<1>(p, stream);
 }
 
