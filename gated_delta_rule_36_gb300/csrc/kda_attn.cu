@@ -195,7 +195,7 @@ __device__ Share find_share(const AttnParams& p, int tq, int G, uint64_t recip, 
     r.bad = __syncthreads_or(bad);
     if (r.bad) return r;
     int64_t total = 0, before = sum - mine;
-#pragma unroll 1
+#pragma unroll
     for (int w = 0; w < AT_THREADS / 32; ++w) {
         before += w < warp ? scratch[w] : 0;
         total += scratch[w];

@@ -153,7 +153,7 @@ __device__ Share find_share(const LinParams& p, uint64_t recip, int64_t* scratch
     if (s.bad) return s;
     s.empties = __syncthreads_or(what & 2);
     int64_t before = sum - mine, all = 0;
-#pragma unroll 1
+#pragma unroll
     for (int w = 0; w < LF_THREADS / 32; ++w) {
         before += w < warp ? scratch[w] : 0;
         all += scratch[w];
