@@ -610,6 +610,8 @@ __device__ bool state_warps(const LinParams& p, const Ctx<kSum>& x, const Share&
             }
             publish = true;
             fresh = true;
+        } else if (!kSum && i + 1 == x.nAB && u.c + 1 < u.nc) {
+            fresh = true;   // (the shares behind go on from the sums; here the last part follows)
         } else if (!kSum && u.c + 1 == u.nc) {
             fresh = true;
             if (p.final_state) {

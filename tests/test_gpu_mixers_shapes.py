@@ -111,6 +111,50 @@ def test_lin_units_over_many_shares_beside_short_ones():
         a += L
 
 
+def chunked_lin(q, k, v, ld, scale, lens, init):
+    """ref_lin of test_gpu_mixers.py with the recurrence unrolled over 64 tokens at a time."""
+    outs, bounds, finals, finals_abs, a = [], [], [], [], 0
+    d = ld.double()[:, None]
+    for n, L in enumerate(lens):
+        s = init[n].double()
+        t = s.abs()
+        for c in range(a, a + L, 64):
+            m = min(64, a + L - c)
+            i = torch.arange(m, device="cuda")
+            qc, kc, vc = (x[c:c + m].double().transpose(0, 1) for x in (q, k, v))
+            low = torch.exp(d[..., None] * (i[:, None] - i).clamp(min=0)) * (i[:, None] >= i)
+            into, w, f = torch.exp(d * (i + 1))[..., None], torch.exp(d * (m - 1 - i))[..., None], torch.exp(d * m)[..., None]
+            outs.append(scale * ((qc @ kc.mT * low) @ vc + into * (qc @ s.mT)).transpose(0, 1))
+            bounds.append(scale * ((qc.abs() @ kc.abs().mT * low) @ vc.abs() + into * (qc.abs() @ t.mT)).transpose(0, 1))
+            s = f * s + (vc * w).mT @ kc
+            t = f * t + (vc * w).abs().mT @ kc.abs()
+        a += L
+        finals.append(s)
+        finals_abs.append(t)
+    return torch.cat(outs), torch.cat(bounds), torch.stack(finals), torch.stack(finals_abs)
+
+
+DIVIDED = [([94, 1407], 64), ([2018, 3165, 32], 40), ([18, 2659, 278, 2, 260], 48), ([1212, 3, 4993], 16), ([2738, 6000], 8), ([5000], 5)]
+for _seed in range(10):
+    _r = random.Random(_seed)
+    DIVIDED.append(([int(2 ** _r.uniform(0, 12)) for _ in range(_r.randint(1, 7))], _r.choice([1, 3, 7, 16, 30, 64])))
+
+
+@pytest.mark.parametrize("lens,h", DIVIDED, ids=[f"{'-'.join(map(str, a))}x{b}" for a, b in DIVIDED])
+def test_lin_however_the_units_are_divided(lens, h):
+    """Shares that end one unit, hold others and begin a third, each of them in one, two or more shares."""
+    g = gen_of(sum(lens) + h)
+    q, k, v = (rand(g, 1, sum(lens), h, D) for _ in range(3))
+    ld = -(2.0 ** (-10.0 * torch.arange(1, h + 1) / h)).cuda()
+    init, final = rand(g, len(lens), h, D, D, dtype=torch.float32), torch.full((len(lens), h, D, D), NAN, device="cuda")
+    out = torch.full_like(q, NAN)
+    ws = kda.kda_lin_fwd(q, k, v, ld, 0.1, out, initial_state=init, final_state=final, cu_seqlens=cu_of(lens))
+    assert kda.kda_read_device_status(ws) == 0
+    o, A, s, t = chunked_lin(q[0], k[0], v[0], ld, 0.1, lens, init)
+    check_lin_out(out[0], o, A)
+    check_state("final_state", final, s, t)
+
+
 def test_mixers_in_a_graph():
     """One capture of all four, replayed on new inputs: the bits of plain calls."""
     hq, hk, lens, S = 8, 2, [150, 61, 700], 600
