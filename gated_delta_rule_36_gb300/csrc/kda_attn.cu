@@ -8,7 +8,9 @@
 //   O_t += P_t V                               l_t += row sums of P_t in fp32
 // The maximum m that the exponents refer to moves only when a row's maximum has grown by more
 // than 2^8 (then O and l are rescaled): P stays below 2^8 and the sums in fp32's range, and most
-// blocks skip the rescaling.
+// blocks skip the rescaling.  P is rounded to bf16, the type of V in the same MMA; l sums the
+// unrounded weights in fp32.  The roundings are independent: against 64 bits the output is off by 0.0020
+// of its norm, 0.0016 of which is its own rounding to bf16.
 //
 // All (sequence, key head, tile pair, key block) steps are one line that is cut into equal
 // shares, one for each SM: long prompts, ragged batches and single tokens over a long cache
@@ -26,7 +28,19 @@
 // alternating between the tiles so that one is multiplied while the other is exponentiated.
 //
 // Bound by the tensor cores for prompts (4 x 128 x 128 x 128 flop, 1,024 SM cycles, a tile and
-// key block), by HBM for single tokens.
+// key block), by HBM for single tokens.  Measured: one prompt of 8,192 tokens, 64 heads on 8: 690 to
+// 745 us (new inputs each time; 1.48 PFLOP/s; a pair's step lasts about 2,800 cycles for its 2,048 of MMAs: the
+// softmax of one tile, a chain of 1,250 cycles and more, does not fit under the other's products);
+// 32 single tokens over caches of 67 to 8,189, 32 heads on 8: 102 us (5.3 TB/s: about 7 us until
+// the first block has arrived and 8 us for the join, HBM speed between); one token over 32,767:
+// 43 us; prompts of 300, 700 and 1,024 tokens: 32 us.
+//
+// Why so: two tiles a CTA share every key block, which halves the traffic from L2 and lets one
+// tile's products hide the other's exponentials; a second warp for the MMAs fell into step with
+// the first (984 against 890 us at the time).  Joining inside this kernel (the last of a pair's
+// shares) was slower than the second launch: 59 against 46 us for one token, since the code
+// that writes and joins is cold.  The maximum of half the scores while the other half loads:
+// 704 against 696 us.
 #include "kda_mixer.cuh"
 
 namespace kda {
@@ -37,7 +51,9 @@ constexpr int AT_MAX_CTAS = 160;
 constexpr int KB = 128;                       // keys a block
 constexpr uint32_t TILE = 128 * 256, HALF = TILE / 2;
 constexpr int RING = 4;
-constexpr int PIECE = 2;                      // a pair's own weight, in steps
+// A pair's own weight, in steps.  With 0, 1, 2 and 3: long prompt 803, 733, 705 and 710 us, 32 single
+// tokens 128, 105, 105 and 106 us.
+constexpr int PIECE = 2;
 constexpr uint32_t OFF_RING = 2 * TILE;       // behind the two query tiles
 constexpr uint32_t OFF_STAGE = OFF_RING + RING * TILE;   // 4 KB for each softmax warp: 32 rows of 128 bytes
 constexpr uint32_t OFF_BAR = OFF_STAGE + 8 * 4096;
@@ -108,7 +124,7 @@ __device__ __forceinline__ int blocks_seen(const Seq& s, int tokens) {
 
 // A sequence's pairs are taken from both ends in turn, 0, m - 1, 1, m - 2, ...: the number of blocks
 // grows with the pair, and two neighbours then have about as many as any others, so that shares of
-// a few whole pairs come out alike.
+// a few whole pairs come out alike (three prompts 39.6 -> 34.7 us, the long one 705 -> 695 us).
 __device__ __forceinline__ int pairs_of(const Seq& s, int tp) { return (s.lq + tp - 1) / tp; }
 __device__ __forceinline__ int pair_in_turn(int i, int m) { return i & 1 ? m - 1 - (i >> 1) : i >> 1; }
 
