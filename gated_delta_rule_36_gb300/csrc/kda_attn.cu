@@ -730,6 +730,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const AttnParams p,
         tmem_relinquish();
     }
     tc_fence_before();
+    await_stream();
     const Share share = find_share(p, x.tq, x.G, recip, reinterpret_cast<int64_t*>(smem_raw));
     const Cursor u = share.at;
     __syncthreads();
@@ -772,7 +773,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParam
     const int first = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int G = p.Hq / p.Hk, tq = 128 / G;
     const Partials part = partials(p.workspace);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    await_stream();
     const Cut c = part.cut[first];
     Cut before = part.cut[first - 1];
     Cut e = part.cut[min(first + lane, ctas - 1)];
@@ -869,20 +870,9 @@ cudaError_t launch_attn(const AttnParams& p, cudaStream_t stream) {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)AT_SMEM);
     if (e != cudaSuccess) return e;
     const int ctas = sms < AT_MAX_CTAS ? sms : AT_MAX_CTAS;
-    attn_kernel<<<ctas, AT_THREADS, AT_SMEM, stream>>>(p, maps, ctas > 1 ? ~0ull / (uint64_t)ctas + 1 : 0);
-    e = cudaGetLastError();
+    e = launch_early(attn_kernel, dim3((unsigned)ctas), AT_THREADS, AT_SMEM, stream, p, maps, ctas > 1 ? ~0ull / (uint64_t)ctas + 1 : (uint64_t)0);
     if (e != cudaSuccess || ctas < 2) return e;
-    // the join may be launched before the first kernel ends; it waits for its results itself
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(ctas - 1), 256 / JOIN_ROWS);
-    cfg.blockDim = dim3(JOIN_THREADS);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_join_kernel, p, ctas);
+    return launch_early(attn_join_kernel, dim3((unsigned)(ctas - 1), 256 / JOIN_ROWS), JOIN_THREADS, 0, stream, p, ctas);
 }
 
 }  // namespace kda

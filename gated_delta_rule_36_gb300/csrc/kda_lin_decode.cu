@@ -21,6 +21,7 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
 }
 
 __global__ void __launch_bounds__(LD_THREADS) lin_decode_kernel(const LinParams p) {
+    await_stream();
     const int unit = blockIdx.x / LD_BLOCKS_PER_UNIT, rb = blockIdx.x % LD_BLOCKS_PER_UNIT;
     const int b = unit / p.H, h = unit % p.H;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c0 = 4 * lane;
@@ -76,8 +77,7 @@ __global__ void __launch_bounds__(LD_THREADS) lin_decode_kernel(const LinParams 
 cudaError_t launch_lin_decode(const LinParams& p, cudaStream_t stream) {
     const int64_t blocks = (int64_t)p.nseq * p.H * LD_BLOCKS_PER_UNIT;
     if (blocks == 0) return cudaSuccess;
-    lin_decode_kernel<<<(unsigned)blocks, LD_THREADS, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_early(lin_decode_kernel, dim3((unsigned)blocks), LD_THREADS, 0, stream, p);
 }
 
 }  // namespace kda

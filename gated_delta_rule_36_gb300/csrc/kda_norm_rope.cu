@@ -30,6 +30,7 @@ __device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
 // groups[i]: groups of kRows heads of q (0) and k (1), the last one possibly partial
 template <bool kInterleaved, int kRows>
 __global__ void __launch_bounds__(NR_THREADS, NR_BLOCKS) norm_rope_kernel(const NormRopeParams p, int groups_q, int groups) {
+    await_stream();
     const int lane = threadIdx.x & 15;
     const int64_t item = (int64_t)blockIdx.x * NR_HALVES + (threadIdx.x >> 4);
     const int64_t t = item / groups;
@@ -120,9 +121,8 @@ cudaError_t launch(const NormRopeParams& p, cudaStream_t stream) {
     const int gq = (p.heads[0] + kRows - 1) / kRows, groups = gq + (p.heads[1] + kRows - 1) / kRows;
     const int64_t blocks = (p.tokens * groups + NR_HALVES - 1) / NR_HALVES;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    if (p.interleaved) norm_rope_kernel<true, kRows><<<(unsigned)blocks, NR_THREADS, 0, stream>>>(p, gq, groups);
-    else norm_rope_kernel<false, kRows><<<(unsigned)blocks, NR_THREADS, 0, stream>>>(p, gq, groups);
-    return cudaGetLastError();
+    return launch_early(p.interleaved ? norm_rope_kernel<true, kRows> : norm_rope_kernel<false, kRows>, dim3((unsigned)blocks), NR_THREADS, 0, stream, p,
+                        gq, groups);
 }
 
 }  // namespace
