@@ -28,19 +28,21 @@
 // alternating between the tiles so that one is multiplied while the other is exponentiated.
 //
 // Bound by the tensor cores for prompts (4 x 128 x 128 x 128 flop, 1,024 SM cycles, a tile and
-// key block), by HBM for single tokens.  Measured: one prompt of 8,192 tokens, 64 heads on 8: 690 to
-// 745 us (new inputs each time; 1.48 PFLOP/s; a pair's step lasts about 2,800 cycles for its 2,048 of MMAs: the
+// key block), by HBM for single tokens.  Measured: one prompt of 8,192 tokens, 64 heads on 8: 680 to
+// 735 us (the latter with new inputs each time, 1.50 PFLOP/s; a pair's step lasts about 2,800 cycles for its 2,048 of MMAs: the
 // softmax of one tile, a chain of 1,250 cycles and more, does not fit under the other's products);
-// 32 single tokens over caches of 67 to 8,189, 32 heads on 8: 102 us (5.3 TB/s: about 7 us until
+// 32 single tokens over caches of 67 to 8,189, 32 heads on 8: 99 us (5.4 TB/s: about 7 us until
 // the first block has arrived and 8 us for the join, HBM speed between); one token over 32,767:
-// 43 us; prompts of 300, 700 and 1,024 tokens: 32 us.
+// 40 us; prompts of 300, 700 and 1,024 tokens: 30 us.
 //
 // Why so: two tiles a CTA share every key block, which halves the traffic from L2 and lets one
 // tile's products hide the other's exponentials; a second warp for the MMAs fell into step with
 // the first (984 against 890 us at the time).  Joining inside this kernel (the last of a pair's
 // shares) was slower than the second launch: 59 against 46 us for one token, since the code
 // that writes and joins is cold.  The maximum of half the scores while the other half loads:
-// 704 against 696 us.
+// 704 against 696 us.  Two threads a row, each with half of the keys: 784 against 677 us; an
+// exponential with its scaling, sum and packing takes 7.3 cycles from one warp of a scheduler and 5.5 from
+// two, so that halves gain less than exchanging their maxima costs.
 #include "kda_mixer.cuh"
 
 namespace kda {

@@ -3,7 +3,7 @@
 //
 // The state's rows (V index) are independent: out_r = scale (a S_r + v_r k) . q, so one pass
 // reads and writes each row once.  Bound by HBM (the state's traffic): 64 sequences x 64 heads with
-// fp32 states, 541 MB, take 80 us, 6.7 TB/s; one sequence x 32 heads is a launch's latency.
+// fp32 states, 541 MB, take 78 us, 6.9 TB/s; one sequence x 32 heads is a launch's latency.
 //
 // One CTA of 4 warps per (unit, block of 32 rows); a warp takes 8 rows with all their loads in
 // flight, lane l the key channels 4 l .. 4 l + 3.

@@ -9,7 +9,7 @@
 //
 // Bound by HBM: each row is read once and written once, past the caches.  What it takes is bytes in
 // flight: 28 warps an SM with eight rows a half-warp are 112 KB of loads.  32,768 tokens x 72 heads
-// (1.22 GB): 208 us, 5.9 TB/s (blocks of 128 threads, 7 an SM; with 6 218, with 8, which spill,
+// (1.22 GB): 200 us, 6.1 TB/s (blocks of 128 threads, 7 an SM; with 6 218, with 8, which spill,
 // 244; 256 threads at 3 an SM 225; plain instead of streaming loads and stores 10 % slower each).
 #include "kda_device.cuh"
 #include "kda_ops.h"
