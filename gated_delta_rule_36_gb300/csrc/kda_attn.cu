@@ -624,6 +624,9 @@ __device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const C
                 if (b & 1) {   // half of P: the tensor core can start on it
                     tmem_wait_st();
                     tc_fence_before();
+#ifdef KDA_WAIT_TEST
+                    if ((int)blockIdx.x == p.test_skip) continue;
+#endif
                     mx_arrive_warp(x.bar((other ? PX : PF + 2 * t) + (b >> 1)));
                 }
             }

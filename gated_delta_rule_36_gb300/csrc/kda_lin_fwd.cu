@@ -526,6 +526,9 @@ __device__ bool state_warps(const LinParams& p, const Ctx<kSum>& x, const Share&
     bool fresh = true;      // a unit or a part of one starts
     bool publish = false;   // this share's part of a unit is written but not yet announced
     auto announce = [&]() {
+#ifdef KDA_WAIT_TEST
+        if ((int)blockIdx.x == p.test_skip) return;
+#endif
         __threadfence();
         __syncwarp();
         if (lane == 0) asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(share_flag(p, blockIdx.x)) : "memory");

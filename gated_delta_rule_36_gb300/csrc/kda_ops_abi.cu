@@ -3,6 +3,7 @@
 #include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
+#include <stdlib.h>
 #include <string.h>
 
 #include "kda.h"
@@ -10,6 +11,14 @@
 #include "kda_ops.h"
 
 namespace {
+
+// The test-only build of the timeout path: the share that withholds an arrival.
+int test_skip() {
+#ifdef KDA_WAIT_TEST
+    if (const char* sk = getenv("KDA_TEST_SKIP_SHARE")) return atoi(sk);
+#endif
+    return -1;
+}
 
 kda_status fail(kda_status s, const char* fmt, ...) {
     char msg[512];
@@ -342,6 +351,7 @@ kda_status kda_attn_fwd(const kda_view* q, const kda_view* k, const kda_view* v,
     p.scale = scale;
     p.status = static_cast<uint32_t*>(workspace);
     p.workspace = static_cast<char*>(workspace) + kHeaderBytes;
+    p.test_skip = test_skip();
     const cudaError_t e = kda::launch_attn(p, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(KDA_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
     return KDA_OK;
@@ -407,6 +417,7 @@ kda_status kda_lin_fwd(const kda_view* q, const kda_view* k, const kda_view* v, 
     p.scale = scale;
     p.status = static_cast<uint32_t*>(workspace);
     p.workspace = static_cast<char*>(workspace) + kHeaderBytes;
+    p.test_skip = test_skip();
     const cudaError_t e = kda::launch_lin_fwd(p, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(KDA_ERR_CUDA, "linear attention launch: %s", cudaGetErrorString(e));
     return KDA_OK;
