@@ -33,15 +33,15 @@
 //
 // Bound by HBM: 1,024 bytes a token-head against 4 x 128 x 128 x 2 (+ 2 x the state's extra
 // terms) flop; a chunk at HBM speed lasts about 5,700 SM cycles, its MMAs 3,072.  Measured: eight
-// prompts of 63 to 9,088 tokens, 64 heads, fp32 states: 541 to 592 us (the latter with new inputs
-// each time), 5.7 to 5.2 TB/s; prompts of 300, 700 and 1,024 tokens, 96 heads: 66 us, of which about 10
-// are the start (finding the share, the first loads) and about 4 each change of unit; one
-// prompt of 32,768, 32 heads: 300 to 316 us, about 95 of it for the sums, which read the keys and
+// prompts of 63 to 9,088 tokens, 64 heads, fp32 states: 541 to 583 us (the latter with new inputs
+// each time), 5.7 to 5.2 TB/s; prompts of 300, 700 and 1,024 tokens, 96 heads: 66 us, of which 7 pass
+// between two calls (a cooperative launch and a memset), 4 until the share is found, and the shares
+// end between 39 and 58; one prompt of 32,768, 32 heads: 300 to 314 us, about 95 of it for the sums, which read the keys and
 // values once more (a 225 us floor for this way; a chain of waits would read nothing twice but
 // leave four of five SMs waiting).
 //
 // Why so: 128 tokens fill an MMA's rows and make the state's update, whose cost does not depend on
-// the chunk, cheap; K' from Tensor Memory in three terms costs 8 more MMAs each but no
+// the chunk, cheap; K' from Tensor Memory in three terms costs 8 more MMAs a term but no
 // rounding that a plain fp32 evaluation would not have; one group more for the output (seven in
 // all) leaves too few registers each: 75 and 703 us for the first two at the time, against 78 and 575.
 #include "kda_mixer.cuh"
@@ -170,6 +170,8 @@ __device__ Share find_share(const LinParams& p, uint64_t recip, int64_t* scratch
         before += w < warp ? scratch[w] : 0;
         all += scratch[w];
     }
+    // (0, 1, 2 and 3 with fp32 states: three prompts 64.7, 64.5, 66.5 and 69.5 us, eight long ones, 64 short units
+    // among theirs, 657, 556, 544 and 544)
     const int extra = 1 + (p.init_state != nullptr || p.final_state != nullptr);
     auto weight = [&](int64_t v) { return ((v & ((1LL << 44) - 1)) + (v >> 44) * extra) * p.H; };
     const int64_t total = s.total = weight(all);
