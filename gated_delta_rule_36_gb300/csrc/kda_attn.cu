@@ -30,7 +30,8 @@
 // Bound by the tensor cores for prompts (4 x 128 x 128 x 128 flop, 1,024 SM cycles, a tile and
 // key block), by HBM for single tokens.  Measured: one prompt of 8,192 tokens, 64 heads on 8: 680 to
 // 735 us (the latter with new inputs each time, 1.50 PFLOP/s; a pair's step lasts about 2,800 cycles for its 2,048 of MMAs: the
-// softmax of one tile, a chain of 1,250 cycles and more, does not fit under the other's products);
+// softmax of one tile, a chain of 1,250 cycles and more, does not fit under the other's products, but
+// 400 cycles less of it gained 1 %: the plain product sustains 1.71 PFLOP/s on this card);
 // 32 single tokens over caches of 67 to 8,189, 32 heads on 8: 99 us (5.4 TB/s: about 7 us until
 // the first block has arrived and 8 us for the join, HBM speed between); one token over 32,767:
 // 40 us; prompts of 300, 700 and 1,024 tokens: 30 us.
