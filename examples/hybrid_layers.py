@@ -37,7 +37,7 @@ class Cache:
 
 
 class Model:
-    def __init__(self, kinds=("kda", "linear", "attention"), hidden=256, heads=8, kv_heads=2, reach=4096, seed=0):
+    def __init__(self, kinds=("kda", "linear", "attention"), hidden=256, heads=6, kv_heads=2, reach=4096, seed=0):
         g = torch.Generator().manual_seed(seed)
         self.kinds, self.heads, self.kv_heads = kinds, heads, kv_heads
         rand = lambda *shape, mul: (torch.randn(shape, generator=g) * mul).cuda()
