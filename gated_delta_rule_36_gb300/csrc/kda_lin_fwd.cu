@@ -22,7 +22,10 @@
 // long been there: no chunk is read twice and nobody waits.  Units that lie in more than two
 // shares (few heads, long prompts) would make a chain of waits; there every share first sums k v^T
 // over its last chunks, if the unit goes on behind them (kSum: keys and values only, and K' made by
-// two more groups), publishes that, and starts its own chunks from the decayed sums before it.
+// two more groups), publishes that, and starts its own chunks from the decayed sums before it.  All of them
+// read the unit's initial state in their own time, and the last one writes the final state: where that
+// takes the initial one's place, the share that begins the unit copies it before it publishes its sum, and
+// they read the copy.
 //
 // Warp roles: warps 0-3 turn W into P and scale O (thread = token row); warps 4-7 write the
 // output out; warps 8-11 carry the state (thread = key channel); warps 12-15 and 16-19 make K',
@@ -227,6 +230,7 @@ struct Ctx {
     // in this order: nA chunks of the unit that the next share ends, then up to nAB, then the rest of
     // the unit that the share before began
     int nA, nAB;
+    int kept;              // the chunk that starts a unit whose initial state the sums keep in the workspace, or -1
     const Cursor* seg;     // where the three parts start (in shared memory)
     __device__ uint32_t bar(int b) const { return base + OFF_BAR + 8u * (b + (kSum ? NBAR : 0)); }
     __device__ bool wait(int b, int use) const { return mx_wait(bar(b), (uint32_t)use & 1u); }
@@ -241,11 +245,15 @@ __device__ __forceinline__ void advance(const LinParams& p, const Ctx<kSum>& x, 
     else next_chunk(p, u);
 }
 
-// Workspace: a partial or published state for each share, then a flag for each.
+// Workspace: a partial or published state for each share, a kept initial state for every second one (shares
+// that begin a unit of more than two shares are never neighbours), then a flag for each share.
+constexpr size_t LF_STATES = LF_MAX_CTAS + LF_MAX_CTAS / 2;
 __device__ __forceinline__ float* share_state(const LinParams& p, int b) { return static_cast<float*>(p.workspace) + (size_t)b * HD * HD; }
+__device__ __forceinline__ void* kept_state(const LinParams& p, int b) { return share_state(p, LF_MAX_CTAS + (b >> 1)); }
 __host__ __device__ __forceinline__ uint32_t* share_flag(const LinParams& p, int b) {
-    return reinterpret_cast<uint32_t*>(static_cast<float*>(p.workspace) + (size_t)LF_MAX_CTAS * HD * HD) + b;
+    return reinterpret_cast<uint32_t*>(static_cast<float*>(p.workspace) + LF_STATES * HD * HD) + b;
 }
+__device__ __forceinline__ bool in_place(const LinParams& p) { return p.init_state != nullptr && p.init_state == p.final_state; }
 
 // ---------------------------------------------------------------- warp 20: loads
 template <bool kSum>
@@ -511,11 +519,12 @@ __device__ bool out_warps(const LinParams& p, const LinMaps& maps, const Ctx<fal
 
 // ---------------------------------------------------------------- warps 8-11: the state
 // Thread k holds S[k][0 .. 127] (column v).  Global states are [V][K]: the 32 lanes of a warp
-// read and write 32 neighbouring k of one v.
+// read and write 32 neighbouring k of one v.  (Not by way of the read-only cache: a state that is updated in
+// place is written by the same kernel, after it has been read.)
 template <class T>
 __device__ __forceinline__ void load_state(const T* s, float2 (&S)[LF_C / 2]) {
 #pragma unroll
-    for (int v = 0; v < LF_C / 2; ++v) S[v] = make_float2((float)__ldg(s + (2 * v) * HD), (float)__ldg(s + (2 * v + 1) * HD));
+    for (int v = 0; v < LF_C / 2; ++v) S[v] = make_float2((float)__ldcg(s + (2 * v) * HD), (float)__ldcg(s + (2 * v + 1) * HD));
 }
 
 template <bool kSum>
@@ -556,14 +565,37 @@ __device__ bool state_warps(const LinParams& p, const Ctx<kSum>& x, const Share&
 #pragma unroll
                 for (int v = 0; v < LF_C / 2; ++v) S[v] = make_float2(__ldcg(s + (2 * v) * HD), __ldcg(s + (2 * v + 1) * HD));
             } else {
-                const size_t off = unit * HD * HD + k;
-                if (kSum || p.init_state == nullptr) {
+                size_t off = unit * HD * HD + k;
+                const void* init = p.init_state;
+                if (kSum && i == x.kept) {
+                    const size_t bytes = HD * HD * (p.init_f32 ? 4 : 2);
+                    const uint4* from = reinterpret_cast<const uint4*>(static_cast<const char*>(init) + unit * bytes) + k;
+                    uint4* to = static_cast<uint4*>(kept_state(p, blockIdx.x)) + k;
+#pragma unroll 1
+                    for (int n = 0; n < (int)(bytes / 16); n += 16 * 128) {
+                        uint4 r[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) r[e] = __ldcg(from + n + 128 * e);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) to[n + 128 * e] = r[e];
+                    }
+                } else if (!kSum && i == x.kept) {
+                    init = kept_state(p, blockIdx.x);
+                    off = k;
+                } else if (!kSum && u.c > 0 && in_place(p)) {   // the share that begins the unit has a copy
+                    int b = (int)blockIdx.x - 1;
+                    while (share_start(share.total, b, gridDim.x, recip) > share.unit) --b;
+                    if (!published(b)) return false;
+                    init = kept_state(p, b);
+                    off = k;
+                }
+                if (kSum || init == nullptr) {
 #pragma unroll
                     for (int v = 0; v < LF_C / 2; ++v) S[v] = make_float2(0.f, 0.f);
                 } else if (p.init_f32) {
-                    load_state(static_cast<const float*>(p.init_state) + off, S);
+                    load_state(static_cast<const float*>(init) + off, S);
                 } else {
-                    load_state(static_cast<const __nv_bfloat16*>(p.init_state) + off, S);
+                    load_state(static_cast<const __nv_bfloat16*>(init) + off, S);
                 }
                 if (!kSum && u.c > 0) {
                     // decayed to here, plus what the shares before this one summed over the unit's chunks
@@ -815,6 +847,10 @@ __global__ void __launch_bounds__(LF_THREADS, 1) lin_fwd_kernel(const LinParams 
     // the share's last chunks, of a unit in more than two shares
     y.nA = 0;
     y.nAB = y.count = share.cut && !share.tail ? min(x.count, share.end.c) : 0;
+    // a summed unit that begins here and whose state is updated in place
+    const bool keep = in_place(p) && y.count > 0 && y.count == share.end.c;
+    x.kept = keep ? x.nAB - y.count : -1;
+    y.kept = keep ? 0 : -1;
     if (tid == 0) {
         seg[0] = share.end, seg[0].c = 0;
         seg[1] = seg[2] = share.first;
@@ -886,7 +922,7 @@ __global__ void __launch_bounds__(LF_THREADS, 1) lin_fwd_kernel(const LinParams 
 
 }  // namespace
 
-size_t lin_workspace_bytes(int64_t, int, int) { return (size_t)LF_MAX_CTAS * (HD * HD * sizeof(float) + sizeof(uint32_t)); }
+size_t lin_workspace_bytes(int64_t, int, int) { return LF_STATES * HD * HD * sizeof(float) + LF_MAX_CTAS * sizeof(uint32_t); }
 
 cudaError_t launch_lin_fwd(const LinParams& p, cudaStream_t stream) {
     LinMaps maps;
