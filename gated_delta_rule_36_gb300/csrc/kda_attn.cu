@@ -60,7 +60,7 @@ constexpr int PIECE = 2;
 constexpr uint32_t OFF_RING = 2 * TILE;       // behind the two query tiles
 constexpr uint32_t OFF_STAGE = OFF_RING + RING * TILE;   // 4 KB for each softmax warp: 32 rows of 128 bytes
 constexpr uint32_t OFF_BAR = OFF_STAGE + 8 * 4096;
-enum { FULL = 0, EMPTY = RING, QF = 2 * RING, QE, SF, PF = SF + 2, OF = PF + 4, SX = OF + 2, PX, PV = PX + 2, DRAIN, NBAR };
+enum { FULL = 0, EMPTY = RING, QF = 2 * RING, QE, SF, PF = SF + 2, OF = PF + 4, SX = OF + 2, PX, PV = PX + 2, VZ, DRAIN, NBAR };
 constexpr uint32_t OFF_TMEM = OFF_BAR + NBAR * 8;
 constexpr uint32_t AT_SMEM = OFF_TMEM + 8;
 static_assert(AT_SMEM <= 232448, "one CTA's shared memory");
@@ -403,7 +403,9 @@ __device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
     const uint64_t dQ = make_sdesc_kmajor_sw128(x.base), dK = make_sdesc_kmajor_sw128(x.base + OFF_RING);
     const uint64_t dV = make_sdesc_mnmajor_sw128(x.base + OFF_RING, HALF, 1024);
     uint32_t it = 0;              // tiles of the ring before this piece: k and v alternate
-    uint32_t pieces = 0, n0 = 0, n1 = 0, nX = 0;
+    uint32_t pieces = 0, n0 = 0, n1 = 0, nX = 0, nZ = 0;
+    // A wait's verdict is the lane's own (a vote each time would cost 3.5 % of a long prompt), so within a piece
+    // nothing that the whole warp has to reach follows; the warp agrees at the piece's end.
     bool ok = true;
     // tile i of the piece has landed; its slot
     auto landed = [&](uint32_t i) { return mx_wait_lane(x.bar(FULL + ((it + i) & (RING - 1))), (it + i) / RING & 1u); };
@@ -444,7 +446,8 @@ __device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
 #pragma unroll 1
                 for (int row = max(valid, 0); row < KB; ++row) sts_u64(at + (lane >> 4) * HALF + row * 128 + (lane & 15) * 8, 0u, 0u);
                 fence_proxy_async_smem();
-                __syncwarp();
+                mbar_arrive(x.bar(VZ));
+                return mx_wait_lane(x.bar(VZ), nZ++ & 1u);
             }
             return true;
         };
@@ -453,7 +456,7 @@ __device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
             mx_commit(lead, x.bar(EMPTY + s));
             if (j + 1 == count) mx_commit(lead, x.bar(QE));
         };
-        ok = x.wait(QF, pieces) && landed(0);
+        ok = x.wait(QF, pieces) && __all_sync(0xffffffffu, landed(0));
         if (!ok) break;
         if (!r.two) {
             // one tile: its scores alternate between the two places, so that the next block's are there
@@ -526,6 +529,7 @@ __device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
                 scored(j + 1, ks);
             }
         }
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         it += 2 * count;
     }
@@ -724,7 +728,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const AttnParams p,
     x.tp = 2 * x.tq;
     if (warp == 8) {
         if ((tid & 31) == 0) {
-            for (int b = 0; b < NBAR; ++b) mbar_init(x.bar(b), (b >= PF && b < PF + 4) || b == PX || b == PX + 1 ? 4 : 1);
+            for (int b = 0; b < NBAR; ++b) mbar_init(x.bar(b), b == VZ ? 32 : (b >= PF && b < PF + 4) || b == PX || b == PX + 1 ? 4 : 1);
             mbar_fence_init();
             tma_prefetch_desc(&maps.q);
             tma_prefetch_desc(&maps.k);
