@@ -548,7 +548,7 @@ __device__ bool state_warps(const LinParams& p, const Ctx<kSum>& x, const Share&
     auto published = [&](int b) {   // by all four warps of share b
         const uint32_t* flag = share_flag(p, b);
         uint32_t seen = 0, polls = 0;
-        while (seen != 4 && ++polls < MX_POLLS) asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(flag) : "memory");
+        while (seen != 4 && ++polls < MX_MEMORY_POLLS) asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(flag) : "memory");
         return (bool)__all_sync(0xffffffffu, seen == 4);
     };
     for (int i = 0; i < x.count; advance(p, x, u, i), ++i) {

@@ -10,12 +10,13 @@
 
 namespace kda {
 
-// Polls before a wait gives up.  A poll lasts about 100 SM cycles on GB300, so this is about a
-// second; the test build of the timeout path gives up after a few milliseconds.
+// Polls before a wait gives up, after about a second: a poll of a barrier that does not complete lasts
+// 4.0 us on GB300 (the hardware suspends the warp that long), one of a word in memory 0.22 us alone and 0.6 with
+// 23 warps an SM.  The test build of the timeout path gives up after some milliseconds.
 #ifdef KDA_WAIT_TEST
-constexpr uint32_t MX_POLLS = 1u << 16;
+constexpr uint32_t MX_POLLS = 1u << 10, MX_MEMORY_POLLS = 1u << 14;
 #else
-constexpr uint32_t MX_POLLS = 1u << 24;
+constexpr uint32_t MX_POLLS = 1u << 18, MX_MEMORY_POLLS = 1u << 22;
 #endif
 
 // Shared-memory accesses by window address: they stay shared-memory instructions wherever the
