@@ -59,7 +59,11 @@ constexpr int RING = 4;
 constexpr int PIECE = 2;
 constexpr uint32_t OFF_RING = 2 * TILE;       // behind the two query tiles
 constexpr uint32_t OFF_STAGE = OFF_RING + RING * TILE;   // 4 KB for each softmax warp: 32 rows of 128 bytes
+// The search for the shares works here: its ordinary stores must not meet a tile's bulk loads, which
+// nothing but a proxy fence would order behind them.
+constexpr uint32_t OFF_SCRATCH = OFF_STAGE;
 constexpr uint32_t OFF_BAR = OFF_STAGE + 8 * 4096;
+static_assert(OFF_SCRATCH >= OFF_RING + RING * TILE && OFF_SCRATCH + 48 * 8 <= OFF_BAR, "outside what bulk loads fill");
 enum { FULL = 0, EMPTY = RING, QF = 2 * RING, QE, SF, PF = SF + 2, OF = PF + 4, SX = OF + 2, PX, PV = PX + 2, VZ, DRAIN, NBAR };
 constexpr uint32_t OFF_TMEM = OFF_BAR + NBAR * 8;
 constexpr uint32_t AT_SMEM = OFF_TMEM + 8;
@@ -741,7 +745,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const AttnParams p,
     }
     tc_fence_before();
     await_stream();
-    const Share share = find_share(p, x.tq, x.G, recip, reinterpret_cast<int64_t*>(smem_raw));
+    const Share share = find_share(p, x.tq, x.G, recip, reinterpret_cast<int64_t*>(smem_raw + OFF_SCRATCH));
     const Cursor u = share.at;
     __syncthreads();
     tc_fence_after();
