@@ -77,11 +77,12 @@ struct AttnMaps {
     CUtensorMap out;   // boxes of a warp's 32 rows (used when G divides 32)
 };
 
-// Where a share starts, for the join: the pair that it starts in and how far into it.
+// What a share leaves for the join: the pair that it starts in and how far into it, and its status bits.
 struct Cut {
     int j, nb;          // starts at block j of nb (j = 0: between two pairs; nb = 0: an empty share)
     int q0, lq, kh, pair;
-    int pad[2];
+    uint32_t status;
+    int pad;
 };
 // Partial results: two for each share, of 256 rows each.
 struct Partials {
@@ -750,13 +751,15 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const AttnParams p,
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = lds_u32(x.base + OFF_TMEM);
-    const bool sound = tmem == 0 && x.base % 1024 == 0;   // (the tiles' swizzle counts from 1 KB boundaries)
+    bool sound = tmem == 0 && x.base % 1024 == 0;   // (the tiles' swizzle counts from 1 KB boundaries)
+#ifdef KDA_WAIT_TEST
+    sound = sound && p.test_skip != -2 - (int)blockIdx.x;
+#endif
     x.weight = sound ? share.weight : 0;                  // (bad lengths have none)
     if (tid == 0) {
-        if (blockIdx.x == 0) *p.status = share.bad ? KDA_DEVERR_CU_SEQLENS : 0u;
-        if (!sound) atomicOr(p.status, KDA_DEVERR_INTERNAL);
         Cut c{};
-        if (x.weight > 0) c = Cut{u.j, blocks_seen(u.s, (u.pair + 1) * x.tp), u.s.q0, u.s.lq, u.kh, u.pair, {0, 0}};
+        if (x.weight > 0) c = Cut{u.j, blocks_seen(u.s, (u.pair + 1) * x.tp), u.s.q0, u.s.lq, u.kh, u.pair};
+        c.status = (share.bad ? KDA_DEVERR_CU_SEQLENS : 0u) | (sound ? 0u : KDA_DEVERR_INTERNAL);
         partials(p.workspace).cut[blockIdx.x] = c;
     }
     bool ok = true;
@@ -769,16 +772,18 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const AttnParams p,
         if (warp == 8) ok = load_warp(p, maps, x, u);
         else if (warp == 9) ok = mma_warp(p, x, u);
     }
-    if (!ok) mx_report(p.status);
+    if (!ok) mx_wind_down();
     tc_fence_before();
-    __syncthreads();
+    ok = __syncthreads_and(ok);
+    if (!ok && tid == 0) atomicOr(&partials(p.workspace).cut[blockIdx.x].status, KDA_DEVERR_TIMEOUT);
     if (warp == 8) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
 }
 
-// Joins the partial rows of the pairs that several shares hold.  Block (b, y) takes 32 rows of the
+// Joins the partial rows of the pairs that several shares hold (and, the last block, the shares' status bits: one store,
+// so that none is lost).  Block (b, y) takes 32 rows of the
 // pair that share b + 1 starts in, if that is the pair's first cut; a warp takes four of them, lane l
 // their channels 4 l .. 4 l + 3.  Bound by latency: little code (it is fetched cold) and few loads
 // in a row.
@@ -788,6 +793,14 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParam
     const int G = p.Hq / p.Hk, tq = 128 / G;
     const Partials part = partials(p.workspace);
     await_stream();
+    if (first == ctas) {
+        if (blockIdx.y != 0 || warp != 0) return;
+        uint32_t status = 0;
+        for (int s = lane; s < ctas; s += 32) status |= part.cut[s].status;
+        status = __reduce_or_sync(0xffffffffu, status);
+        if (lane == 0) *p.status = status;
+        return;
+    }
     const Cut c = part.cut[first];
     Cut before = part.cut[first - 1];
     Cut e = part.cut[min(first + lane, ctas - 1)];
@@ -885,8 +898,8 @@ cudaError_t launch_attn(const AttnParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const int ctas = sms < AT_MAX_CTAS ? sms : AT_MAX_CTAS;
     e = launch_early(attn_kernel, dim3((unsigned)ctas), AT_THREADS, AT_SMEM, stream, p, maps, ctas > 1 ? ~0ull / (uint64_t)ctas + 1 : (uint64_t)0);
-    if (e != cudaSuccess || ctas < 2) return e;
-    return launch_early(attn_join_kernel, dim3((unsigned)(ctas - 1), 256 / JOIN_ROWS), JOIN_THREADS, 0, stream, p, ctas);
+    if (e != cudaSuccess) return e;
+    return launch_early(attn_join_kernel, dim3((unsigned)ctas, 256 / JOIN_ROWS), JOIN_THREADS, 0, stream, p, ctas);
 }
 
 }  // namespace kda

@@ -245,14 +245,16 @@ __device__ __forceinline__ void advance(const LinParams& p, const Ctx<kSum>& x, 
     else next_chunk(p, u);
 }
 
-// Workspace: a partial or published state for each share, a kept initial state for every second one (shares
-// that begin a unit of more than two shares are never neighbours), then a flag for each share.
-constexpr size_t LF_STATES = LF_MAX_CTAS + LF_MAX_CTAS / 2;
-__device__ __forceinline__ float* share_state(const LinParams& p, int b) { return static_cast<float*>(p.workspace) + (size_t)b * HD * HD; }
-__device__ __forceinline__ void* kept_state(const LinParams& p, int b) { return share_state(p, LF_MAX_CTAS + (b >> 1)); }
-__host__ __device__ __forceinline__ uint32_t* share_flag(const LinParams& p, int b) {
-    return reinterpret_cast<uint32_t*>(static_cast<float*>(p.workspace) + LF_STATES * HD * HD) + b;
+// Workspace: a flag for each share (right behind the status word's 256 bytes: one launch clears them all), then
+// a partial or published state for each share and a kept initial state for every second one (shares that begin a
+// unit of more than two shares are never neighbours).
+constexpr size_t LF_STATES = LF_MAX_CTAS + LF_MAX_CTAS / 2, LF_FLAG_BYTES = LF_MAX_CTAS * sizeof(uint32_t);
+static_assert(LF_FLAG_BYTES % 16 == 0, "the states are read and written in 16 bytes");
+__host__ __device__ __forceinline__ uint32_t* share_flag(const LinParams& p, int b) { return static_cast<uint32_t*>(p.workspace) + b; }
+__device__ __forceinline__ float* share_state(const LinParams& p, int b) {
+    return reinterpret_cast<float*>(share_flag(p, LF_MAX_CTAS)) + (size_t)b * HD * HD;
 }
+__device__ __forceinline__ void* kept_state(const LinParams& p, int b) { return share_state(p, LF_MAX_CTAS + (b >> 1)); }
 __device__ __forceinline__ bool in_place(const LinParams& p) { return p.init_state != nullptr && p.init_state == p.final_state; }
 
 // ---------------------------------------------------------------- warp 20: loads
@@ -863,9 +865,12 @@ __global__ void __launch_bounds__(LF_THREADS, 1) lin_fwd_kernel(const LinParams 
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = lds_u32(x.base + OFF_TMEM);
-    const bool sound = tmem == 0 && x.base % 1024 == 0;   // (the tiles' swizzle counts from 1 KB boundaries)
+    bool sound = tmem == 0 && x.base % 1024 == 0;   // (the tiles' swizzle counts from 1 KB boundaries)
+#ifdef KDA_WAIT_TEST
+    sound = sound && p.test_skip != -2 - (int)blockIdx.x;
+#endif
     if (tid == 0) {
-        if (blockIdx.x == 0) *p.status = share.bad ? KDA_DEVERR_CU_SEQLENS : 0u;
+        if (share.bad) atomicOr(p.status, KDA_DEVERR_CU_SEQLENS);
         if (!sound) atomicOr(p.status, KDA_DEVERR_INTERNAL);
     }
     if (!sound) x.count = y.count = 0;   // (bad lengths have no chunks)
@@ -911,7 +916,10 @@ __global__ void __launch_bounds__(LF_THREADS, 1) lin_fwd_kernel(const LinParams 
         else if (warp == 21) ok = mma_out_warp(x) && ok;
         else if (warp == 22) ok = mma_state_warp<false>(x) && ok;
     }
-    if (!ok) mx_report(p.status);
+    if (!ok) {
+        atomicOr(p.status, KDA_DEVERR_TIMEOUT);
+        mx_wind_down();
+    }
     tc_fence_before();
     __syncthreads();
     if (warp == 20) {
@@ -922,7 +930,7 @@ __global__ void __launch_bounds__(LF_THREADS, 1) lin_fwd_kernel(const LinParams 
 
 }  // namespace
 
-size_t lin_workspace_bytes(int64_t, int, int) { return LF_STATES * HD * HD * sizeof(float) + LF_MAX_CTAS * sizeof(uint32_t); }
+size_t lin_workspace_bytes(int64_t, int, int) { return LF_FLAG_BYTES + LF_STATES * HD * HD * sizeof(float); }
 
 cudaError_t launch_lin_fwd(const LinParams& p, cudaStream_t stream) {
     LinMaps maps;
@@ -940,7 +948,9 @@ cudaError_t launch_lin_fwd(const LinParams& p, cudaStream_t stream) {
     if (most < ctas) ctas = most > 0 ? (int)most : 1;
     const uint64_t recip = ctas > 1 ? ~0ull / (uint64_t)ctas + 1 : 0;
     e = cudaFuncSetAttribute(lin_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LF_SMEM);
-    if (e == cudaSuccess) e = cudaMemsetAsync(share_flag(p, 0), 0, (size_t)ctas * sizeof(uint32_t), stream);
+    // the status word and the flags: before the kernel, so that no share's report can be overwritten
+    char* cleared = reinterpret_cast<char*>(p.status);
+    if (e == cudaSuccess) e = cudaMemsetAsync(cleared, 0, (size_t)(reinterpret_cast<char*>(share_flag(p, ctas)) - cleared), stream);
     if (e != cudaSuccess) return e;
     // cooperative: a share may wait for what the shares before it publish, so all of them are resident
     cudaLaunchAttribute attr[1];

@@ -68,7 +68,7 @@ __device__ __forceinline__ bool mx_try_wait(uint32_t bar, uint32_t parity) {
 }
 
 // Wait for the phase with `parity`; false when the limit expires.  The caller then leaves its
-// loop and reports it (mx_report), the roles that wait for it run into their own limits, and
+// loop and its CTA reports it, the roles that wait for it run into their own limits, and
 // since no named barrier is used every warp reaches the CTA's end.  The body is as small as it
 // can be: a CTA's roles run different code on the same schedulers, and what they share of the
 // instruction cache limits their pace (a version with a clock and an abort flag in the loop
@@ -86,9 +86,8 @@ __device__ __forceinline__ bool mx_wait_lane(uint32_t bar, uint32_t parity) {
     while (!(ok = mx_try_wait(bar, parity)) && ++polls < MX_POLLS) {}
     return ok;
 }
-// A warp that gave up: the status bit, and time for its CTA's copies in flight to land.
-__device__ __forceinline__ void mx_report(uint32_t* status) {
-    atomicOr(status, KDA_DEVERR_TIMEOUT);
+// A warp that gave up: time for its CTA's copies in flight to land.
+__device__ __forceinline__ void mx_wind_down() {
     for (int i = 0; i < 2000; ++i) __nanosleep(1000);
 }
 

@@ -47,7 +47,7 @@ struct AttnParams {
     float scale;
     uint32_t* status;
     void* workspace;                // behind the status word
-    int test_skip;                  // the test-only build of the timeout path: a share that withholds an arrival, -1 for none
+    int test_skip;                  // the test-only build: the share b that withholds an arrival, -2 - b: that finds itself unsound; -1 for none
 };
 
 struct LinParams {
@@ -62,7 +62,7 @@ struct LinParams {
     float scale;
     uint32_t* status;
     void* workspace;
-    int test_skip;                  // the test-only build of the timeout path: a share that withholds an arrival, -1 for none
+    int test_skip;                  // the test-only build: the share b that withholds an arrival, -2 - b: that finds itself unsound; -1 for none
 };
 
 cudaError_t launch_norm_rope(const NormRopeParams& p, cudaStream_t stream);

@@ -12,7 +12,8 @@
 
 namespace {
 
-// The test-only build of the timeout path: the share that withholds an arrival.
+// The test-only build of the timeout path: the share b that withholds an arrival, or -2 - b: one that
+// finds itself unsound (and reports KDA_DEVERR_INTERNAL).
 int test_skip() {
 #ifdef KDA_WAIT_TEST
     if (const char* sk = getenv("KDA_TEST_SKIP_SHARE")) return atoi(sk);

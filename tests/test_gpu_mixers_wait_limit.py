@@ -1,5 +1,6 @@
-"""A mixer's wait for another share's state in memory has the limit of its other waits: in a child
-process with the test-only build (tests/wait_limit_mixers.py), which has a time limit.
+"""A mixer's wait for another share's state in memory has the limit of its other waits, and no share's report is
+lost: in child processes with the test-only build (tests/wait_limit_mixers.py, tests/wait_status_mixers.py), which have
+a time limit.
 """
 import os
 import subprocess
@@ -13,10 +14,11 @@ pytestmark = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
-def test_waits_for_memory_end_in_time():
+@pytest.mark.parametrize("tests", ["wait_limit_mixers.py", "wait_status_mixers.py"])
+def test_with_the_test_only_build(tests):
     env = dict(os.environ, KDA_LIBRARY=kbuild.build(variant="waittest"))
     env.pop("KDA_TEST_SKIP_SHARE", None)
     r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-s", "-m", "gpu", "-p", "no:cacheprovider",
-                        "tests/wait_limit_mixers.py"], env=env, cwd=ROOT, capture_output=True, text=True, timeout=300)
+                        f"tests/{tests}"], env=env, cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stdout[-4000:] + r.stderr[-2000:]
     assert " passed" in r.stdout
