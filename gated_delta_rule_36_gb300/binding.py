@@ -401,9 +401,13 @@ def _dense(t, name, device):
 
 
 def _device(t, name):
+    """The device of a call: the first tensor's, which has to be the current one (the kernels go there)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    return t.get_device()
+    device = t.get_device()
+    if device >= 0 and device != torch._C._cuda_getDevice():
+        raise ValueError(f"{name}: on cuda:{device}, which is not the current device")
+    return device
 
 
 def _stream(stream, device):
@@ -419,9 +423,9 @@ def _workspace(workspace, nbytes, device, stream):
         if stream is not None:
             workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
                                     else torch.cuda.ExternalStream(_stream(stream, device), device=device))
-    elif not (isinstance(workspace, torch.Tensor) and workspace.is_cuda and workspace.dtype == torch.uint8
+    elif not (isinstance(workspace, torch.Tensor) and workspace.get_device() == device and workspace.dtype == torch.uint8
               and workspace.is_contiguous()):
-        raise ValueError("workspace: must be a contiguous uint8 CUDA tensor")
+        raise ValueError("workspace: must be a contiguous uint8 CUDA tensor on the other tensors' device")
     return workspace
 
 
@@ -433,8 +437,9 @@ def kda_qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, q_out, k_out,
     bytes whose first word collects KDA_DEVERR_POSITION (see kda_read_device_status)."""
     lib = _lib or load()
     dev = _device(q, "q")
-    if status is not None and not (status.is_cuda and status.dtype == torch.uint8 and status.numel() >= 4):
-        raise ValueError("status: must be a uint8 CUDA tensor of at least 4 bytes")
+    if status is not None and not (isinstance(status, torch.Tensor) and status.get_device() == dev
+                                   and status.dtype == torch.uint8 and status.numel() >= 4):
+        raise ValueError("status: must be a uint8 CUDA tensor of at least 4 bytes on the other tensors' device")
     st = lib.kda_qk_norm_rope(_view(q, "q", dev), _view(k, "k", dev), _dense(q_weight, "q_weight", dev),
                               _dense(k_weight, "k_weight", dev), eps, _dense(cos_sin, "cos_sin", dev),
                               _dense(positions, "positions", dev), _view(q_out, "q_out", dev), _view(k_out, "k_out", dev),
