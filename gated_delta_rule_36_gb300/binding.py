@@ -417,12 +417,15 @@ def _stream(stream, device):
 
 
 def _workspace(workspace, nbytes, device, stream):
-    """The caller's workspace, or one from torch that lives until the work on ``stream`` is done."""
+    """The caller's workspace, or one from torch that belongs to ``stream``: neither what its memory held
+    before nor what it holds after the call is in use on another stream."""
     if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
-        if stream is not None:
-            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                                    else torch.cuda.ExternalStream(_stream(stream, device), device=device))
+        if stream is None:
+            return torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(_stream(stream, device), device=device)
+        with torch.cuda.stream(stream):
+            return torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
     elif not (isinstance(workspace, torch.Tensor) and workspace.get_device() == device and workspace.dtype == torch.uint8
               and workspace.is_contiguous()):
         raise ValueError("workspace: must be a contiguous uint8 CUDA tensor on the other tensors' device")
