@@ -404,9 +404,13 @@ kda_status kda_lin_fwd(const kda_view* q, const kda_view* k, const kda_view* v, 
         if (overlap(o, extent(views[i]))) return fail(KDA_ERR_ALIAS, "out overlaps %s", names[i]);
     for (const kda_tensor* t : {log_decay, initial_state, final_state, cu_seqlens})
         if (present(t) && overlap(o, extent(t))) return fail(KDA_ERR_ALIAS, "out overlaps another tensor");
-    if (present(final_state))
+    if (present(final_state)) {   // (the lengths are read until the last unit is done)
         for (int i = 0; i < 3; ++i)
             if (overlap(extent(final_state), extent(views[i]))) return fail(KDA_ERR_ALIAS, "final_state overlaps %s", names[i]);
+        for (const kda_tensor* t : {log_decay, cu_seqlens})
+            if (present(t) && overlap(extent(final_state), extent(t)))
+                return fail(KDA_ERR_ALIAS, "final_state overlaps log_decay or cu_seqlens");
+    }
     KDA_TRY(check_workspace(workspace, workspace_bytes, kda_lin_workspace_size(B * T, (int)H, (int)nseq)));
     p.log_decay = static_cast<const float*>(log_decay->data);
     fill_states(p, initial_state, final_state);
@@ -452,6 +456,8 @@ kda_status kda_lin_decode(const kda_view* q, const kda_view* k, const kda_view* 
         if (present(final_state) && overlap(extent(final_state), extent(views[i])))
             return fail(KDA_ERR_ALIAS, "final_state overlaps %s", names[i]);
     }
+    if (present(final_state) && overlap(extent(final_state), extent(log_decay)))
+        return fail(KDA_ERR_ALIAS, "final_state overlaps log_decay");
     for (const kda_tensor* t : {log_decay, initial_state, final_state})
         if (present(t) && overlap(o, extent(t))) return fail(KDA_ERR_ALIAS, "out overlaps another tensor");
     p.log_decay = static_cast<const float*>(log_decay->data);
