@@ -71,6 +71,9 @@ kda_status check_view(const char* name, const kda_view* t, int ndim, const int64
         if (t->stride[i] < KDA_HEAD_DIM || t->stride[i] % 8 != 0 || t->stride[i] >= (1LL << 38))
             return fail(KDA_ERR_INVALID_ARG, "%s: stride %lld of dim %d must be a multiple of 8, at least %d", name,
                         (long long)t->stride[i], i, KDA_HEAD_DIM);
+        if (t->shape[i] > (1LL << 48) / t->stride[i])
+            return fail(KDA_ERR_INVALID_ARG, "%s: dim %d of %lld elements with stride %lld fits no memory", name, i,
+                        (long long)t->shape[i], (long long)t->stride[i]);
     }
     if ((uintptr_t)t->data % 16 != 0) return fail(KDA_ERR_INVALID_ARG, "%s: data pointer not 16-byte aligned", name);
     return KDA_OK;
@@ -86,42 +89,72 @@ kda_status check_head_dim(const char* name, const kda_view* t, int ndim) {
     return KDA_OK;
 }
 
-// A view's elements as bytes: where they start, their extent, and the step and width of one
-// index of the first dimension.
+// A tensor's elements as bytes: runs of `run` bytes, repeated n[i] times with stride step[i] for each of `dims`
+// dimensions, the innermost first (dimensions that continue one another are one).  width[i]: from the first
+// to the last byte of what lies below dimension i.
 struct Extent {
-    uintptr_t at;
-    uint64_t bytes, step, width;
+    int64_t at = 0, run = 0;
+    int dims = 0;
+    int64_t n[4], step[4], width[5];
 };
 
-Extent extent(const kda_view* t) {
-    Extent e{(uintptr_t)t->data, 0, 0, 0};
-    const uint64_t es = elem_size(t->dtype);
-    bool empty = false;
-    e.width = es;
-    for (int i = 1; i < t->ndim; ++i) {
-        empty |= t->shape[i] == 0;
-        if (t->shape[i] > 1) e.width += (uint64_t)(t->shape[i] - 1) * (uint64_t)t->stride[i] * es;
+Extent extent(const void* data, int64_t es, int ndim, const int64_t* shape, const int64_t* stride) {
+    Extent e;
+    e.at = (int64_t)(uintptr_t)data;
+    e.run = es;
+    int64_t n[4], step[4];
+    int dims = 0;
+    for (int i = ndim - 1; i >= 0; --i) {
+        if (shape[i] == 0) {
+            e.run = 0;
+            return e;
+        }
+        if (shape[i] == 1) continue;
+        int at = dims++;
+        for (; at > 0 && step[at - 1] > stride[i] * es; --at) n[at] = n[at - 1], step[at] = step[at - 1];
+        n[at] = shape[i];
+        step[at] = stride[i] * es;
     }
-    empty |= t->shape[0] == 0;
-    e.step = t->shape[0] > 1 ? (uint64_t)t->stride[0] * es : 0;
-    e.bytes = empty ? 0 : e.width + (t->shape[0] > 1 ? (uint64_t)(t->shape[0] - 1) * e.step : 0);
+    for (int i = 0; i < dims; ++i) {
+        if (e.dims == 0 && step[i] == e.run) {
+            e.run *= n[i];
+        } else if (e.dims > 0 && step[i] == e.step[e.dims - 1] * e.n[e.dims - 1]) {
+            e.n[e.dims - 1] *= n[i];
+        } else {
+            e.n[e.dims] = n[i];
+            e.step[e.dims++] = step[i];
+        }
+    }
+    e.width[0] = e.run;
+    for (int i = 0; i < e.dims; ++i) e.width[i + 1] = e.width[i] + (e.n[i] - 1) * e.step[i];
     return e;
 }
 
+Extent extent(const kda_view* t) { return extent(t->data, (int64_t)elem_size(t->dtype), t->ndim, t->shape, t->stride); }
+
 Extent extent(const kda_tensor* t) {
-    uint64_t n = elem_size(t->dtype);
-    for (int i = 0; i < t->ndim; ++i) n *= (uint64_t)t->shape[i];
-    return Extent{(uintptr_t)t->data, n, 0, n};
+    int64_t stride[4], n = 1;
+    for (int i = t->ndim - 1; i >= 0; --i) stride[i] = n, n *= t->shape[i];
+    return extent(t->data, (int64_t)elem_size(t->dtype), t->ndim, t->shape, stride);
 }
 
-// Whether two tensors may share memory.  Views whose rows have the same step (columns of one
-// buffer) only meet if their columns do; anything else that interleaves counts as meeting.
+// Whether the first i dimensions of a at 0 and the first j of b at `off` may share a byte.  Of the wider step,
+// say a's, b is seen from the repetition of a that it starts in: if neither is wider than the step, it meets that one
+// and the next, or none.  Parts of one buffer (columns, heads in turn, planes) are told apart like that;
+// anything that does not nest counts as meeting.
+bool meet(const Extent& a, int i, const Extent& b, int j, int64_t off) {
+    if (off >= a.width[i] || -off >= b.width[j]) return false;
+    if (i == 0 && j == 0) return true;
+    if (i == 0 || (j > 0 && b.step[j - 1] > a.step[i - 1])) return meet(b, j, a, i, -off);
+    const int64_t step = a.step[i - 1];
+    const int k = j > 0 && b.step[j - 1] == step ? j - 1 : j;
+    if (a.width[i - 1] > step || b.width[k] > step) return true;
+    const int64_t d = (off % step + step) % step;
+    return meet(a, i - 1, b, k, d) || meet(a, i - 1, b, k, d - step);
+}
+
 bool overlap(const Extent& a, const Extent& b) {
-    if (a.bytes == 0 || b.bytes == 0 || a.at >= b.at + b.bytes || b.at >= a.at + a.bytes) return false;
-    const uint64_t step = a.step ? a.step : b.step;
-    if (step == 0 || (a.step && b.step && a.step != b.step) || a.width > step || b.width > step) return true;
-    const uint64_t d = b.at >= a.at ? (b.at - a.at) % step : (step - (a.at - b.at) % step) % step;
-    return !(a.width <= d && d + b.width <= step);
+    return a.run > 0 && b.run > 0 && meet(a, a.dims, b, b.dims, b.at - a.at);
 }
 
 bool same_view(const kda_view* a, const kda_view* b) {
@@ -226,7 +259,8 @@ kda_status kda_qk_norm_rope(const kda_view* q, const kda_view* k, const kda_tens
         const int64_t R = cos_sin->shape[1];
         if (R < 16 || R > KDA_HEAD_DIM || R % 16 != 0)
             return fail(KDA_ERR_UNSUPPORTED, "cos_sin: R = %lld, must be a multiple of 16 in [16, 128]", (long long)R);
-        if (cos_sin->shape[0] < 0) return fail(KDA_ERR_INVALID_ARG, "cos_sin: negative shape");
+        if (cos_sin->shape[0] < 0 || cos_sin->shape[0] > (1LL << 40))
+            return fail(KDA_ERR_INVALID_ARG, "cos_sin: bad shape [%lld,%lld]", (long long)cos_sin->shape[0], (long long)R);
         if ((uintptr_t)cos_sin->data % 16 != 0) return fail(KDA_ERR_INVALID_ARG, "cos_sin: data pointer not 16-byte aligned");
         KDA_TRY(check_i64("positions", positions, q->shape[0]));
         p.cos_sin = static_cast<const float*>(cos_sin->data);
