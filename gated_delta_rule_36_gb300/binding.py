@@ -464,7 +464,7 @@ def kda_attn_fwd(q, k, v, scale, out, lse=None, cu_seqlens_q=None, cu_seqlens_k=
     lib = _lib or load()
     dev = _device(q, "q")
     dq, dk = _view(q, "q", dev), _view(k, "k", dev)
-    if workspace is None and q.dim() == 3 and k.dim() in (3, 4):
+    if workspace is None and q.dim() == 3 and k is not None and k.dim() in (3, 4):
         nbytes = lib.kda_attn_workspace_size(q.shape[0], q.shape[1], k.shape[-2]) or 256   # 0: refused below
         workspace = _workspace(None, nbytes, dev, stream)
     else:

@@ -71,3 +71,12 @@ def test_workspaces_and_status_words_on_another_device(name):
 def test_one_device_reaches_the_library(name):
     with pytest.raises(AssertionError, match="was called"):
         calls(On0, ws(On0), ws(On0))[name]()
+
+
+def test_missing_keys_are_the_library_s_refusal(monkeypatch):
+    monkeypatch.setattr(kb, "_lib", None)
+    t = tensors(On0, (4, 2, D))[0]
+    for workspace in (None, ws(On0)):
+        monkeypatch.setattr(kb, "_workspace", lambda *a: ws(On0))
+        with pytest.raises(kb.KDAError, match="k: missing"):
+            kb.kda_attn_fwd(t, None, t, 1.0, t, workspace=workspace, stream=0)
