@@ -130,9 +130,13 @@ cudaError_t launch(const NormRopeParams& p, cudaStream_t stream) {
 cudaError_t launch_norm_rope(const NormRopeParams& p, cudaStream_t stream) {
     const int64_t rows = p.tokens * (p.heads[0] + p.heads[1]);
     if (rows == 0) return cudaSuccess;
-    // Rows a half-warp takes: eight once that still gives every SM a few blocks (32,768 tokens x 72
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    // Rows a half-warp takes: eight once that still gives every SM its seven blocks (32,768 tokens x 72
     // heads: 208 us, against 238 with four and 305 with two), else one, for the latency of small calls.
-    if (rows >= 152 * NR_BLOCKS * NR_HALVES * 8) return launch<8>(p, stream);
+    if (rows >= (int64_t)sms * NR_BLOCKS * NR_HALVES * 8) return launch<8>(p, stream);
     return launch<1>(p, stream);
 }
 
