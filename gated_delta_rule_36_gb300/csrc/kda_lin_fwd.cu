@@ -36,10 +36,10 @@
 //
 // Bound by HBM: 1,024 bytes a token-head against 4 x 128 x 128 x 2 (+ 2 x the state's extra
 // terms) flop; a chunk at HBM speed lasts about 5,700 SM cycles, its MMAs 3,072.  Measured: eight
-// prompts of 63 to 9,088 tokens, 64 heads, fp32 states: 541 to 583 us (the latter with new inputs
-// each time), 5.7 to 5.2 TB/s; prompts of 300, 700 and 1,024 tokens, 96 heads: 66 us, of which 7 pass
+// prompts of 63 to 9,088 tokens, 64 heads, fp32 states: 552 to 589 us (the latter with new inputs
+// each time), 5.5 to 5.2 TB/s; prompts of 300, 700 and 1,024 tokens, 96 heads: 66 us, of which 7 pass
 // between two calls (a cooperative launch and a memset), 4 until the share is found, and the shares
-// end between 39 and 58; one prompt of 32,768, 32 heads: 300 to 314 us, about 95 of it for the sums, which read the keys and
+// end between 39 and 58; one prompt of 32,768, 32 heads: 302 to 316 us (305 with a state in place), about 95 of it for the sums, which read the keys and
 // values once more (a 225 us floor for this way; a chain of waits would read nothing twice but
 // leave four of five SMs waiting).
 //

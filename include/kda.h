@@ -341,8 +341,10 @@ size_t kda_fwd_host_workspace_offset(int64_t B, int64_t T, int H, int64_t N, int
 
 /* A strided device tensor: strides in elements, the innermost one 1.  q, k and v may be
  * columns of one projection buffer, or a cache in any order of its outer dimensions.  Data
- * is 16-byte aligned and every outer stride a multiple of 8 elements (a dimension of size 1
- * may carry any stride). */
+ * is 16-byte aligned and every outer stride a multiple of 8 elements and at least 128 (a
+ * dimension of size 1 may carry any stride).  "Overlap" below means a shared element: parts of one
+ * buffer that lie between one another (columns, heads in turn, planes) do not overlap; strides that do
+ * not nest in one another count as overlapping where their extents do. */
 typedef struct {
     void* data;
     int32_t dtype;     /* kda_dtype */
@@ -372,8 +374,8 @@ typedef struct {
  *   status     device word (4-byte aligned) that error bits are added to, or NULL
  *   flags      KDA_FLAG_ROPE_INTERLEAVED or 0
  * q_out may be exactly q, and k_out exactly k (same data and strides): in place.  Any other
- * overlap of an output with an input or the other output is KDA_ERR_ALIAS; columns of one
- * buffer that do not meet are no overlap.  Arithmetic is fp32, rounded once at the end.
+ * overlap of an output with an input or the other output is KDA_ERR_ALIAS.  Arithmetic is fp32,
+ * rounded once at the end.
  */
 kda_status kda_qk_norm_rope(const kda_view* q, const kda_view* k, const kda_tensor* q_weight,
                             const kda_tensor* k_weight, float eps, const kda_tensor* cos_sin,
@@ -382,7 +384,8 @@ kda_status kda_qk_norm_rope(const kda_view* q, const kda_view* k, const kda_tens
 
 /*
  * Bytes of workspace kda_attn_fwd needs for Tq query tokens, Hq query heads and Hk key/value
- * heads.  Its contents need no initialisation.  Returns 0 for invalid arguments.
+ * heads: 43 MB at present, whatever the sizes (partial results of every SM).  Its contents need no
+ * initialisation.  Returns 0 for invalid arguments.
  */
 size_t kda_attn_workspace_size(int64_t Tq, int Hq, int Hk);
 
@@ -404,6 +407,7 @@ size_t kda_attn_workspace_size(int64_t Tq, int Hq, int Hk);
  *                  or, without that either, N = 1.  Must be absent with a cache
  *   seqlens_k      cache: int64 [N], sequence n's keys are k[n, 0 .. seqlens_k[n]); required with a
  *                  cache, absent otherwise
+ *                  (N at most 32,767: KDA_ERR_UNSUPPORTED)
  *   workspace      >= kda_attn_workspace_size(Tq, Hq, Hk) bytes, 256-byte aligned
  * Rows past a sequence's keys are never used, whatever they hold (NaN included); the keys and
  * values inside a sequence are taken to be finite.  Query rows that belong to no sequence are not
@@ -419,8 +423,8 @@ kda_status kda_attn_fwd(const kda_view* q, const kda_view* k, const kda_view* v,
 
 /*
  * Bytes of workspace kda_lin_fwd needs for T_total = B*T tokens, H heads and N sequences
- * (as for kda_workspace_size).  Its contents need no initialisation.  Returns 0 for negative
- * arguments.
+ * (as for kda_workspace_size): 16 MB at present, whatever the sizes (states that SMs hand to one
+ * another).  Its contents need no initialisation.  Returns 0 for negative arguments.
  */
 size_t kda_lin_workspace_size(int64_t T_total, int H, int N);
 
@@ -428,14 +432,17 @@ size_t kda_lin_workspace_size(int64_t T_total, int H, int N);
  * Linear attention with a decay for each head, over whole prompts: per (sequence, head) and
  * per token,   S <- exp(log_decay[h]) S + v k^T,   out = scale S q   (S is V x K, as in kda_fwd).
  *
- *   q, k, v        bf16 [B, T, H, 128] (views);  out  bf16 [B, T, H, 128] (view)
+ *   q, k, v        bf16 [B, T, H, 128] (views);  out  bf16 [B, T, H, 128] (view).  With B > 1 the batch rows
+ *                  follow one another: the batch stride is T times the token stride
  *   log_decay      fp32 [H], the natural log of the decay (<= 0 in use; -inf forgets everything)
  *   initial_state, final_state, cu_seqlens, workspace   as for kda_fwd, the workspace of
- *                  kda_lin_workspace_size(B*T, H, Nseq) bytes
+ *                  kda_lin_workspace_size(B*T, H, Nseq) bytes; at most 32,767 sequences (KDA_ERR_UNSUPPORTED)
  * Rows of tokens that belong to no sequence are not written; bad cu_seqlens contents set
- * KDA_DEVERR_CU_SEQLENS, and then nothing is written.  out must overlap no other tensor
- * (KDA_ERR_ALIAS).  Values past a sequence's end are never used, whatever they hold.  The
- * state is kept and updated to fp32 accuracy across the whole sequence.
+ * KDA_DEVERR_CU_SEQLENS, and then nothing is written.  out must overlap no other tensor, and
+ * final_state none but exactly initial_state (KDA_ERR_ALIAS).  Values past a sequence's end are never used,
+ * whatever they hold.  The state is kept and updated to fp32 accuracy across the whole sequence.  The
+ * outputs are summed in fp32 from the scaled scores q.k of up to 128 tokens and a copy of the state before
+ * them, both rounded to bf16.  The same inputs give the same bits, in place or not.
  */
 kda_status kda_lin_fwd(const kda_view* q, const kda_view* k, const kda_view* v, const kda_tensor* log_decay,
                        float scale, const kda_view* out, const kda_tensor* initial_state,
