@@ -215,13 +215,13 @@ def _own_gated(s):
 
 def _own_append(s):
     import gated_delta_rule_36_gb300 as kda
-    kda.kda_kv4_append(s["k"], s["v"], s["cache"], s["lens_k"], cu_seqlens=s["cu_q"], k_out=s["k_out"], v_out=s["v_out"])
+    kda.kda_qcache_append(s["k"], s["v"], s["cache"], s["lens_k"], cu_seqlens=s["cu_q"], k_out=s["k_out"], v_out=s["v_out"])
     return (s["cache"],) if s["k_out"] is None else (s["cache"], s["k_out"], s["v_out"])
 
 
 def _own_attn(s):
     import gated_delta_rule_36_gb300 as kda
-    kda.kda_attn_kv4_fwd(s["q"], s["cache"], s["scale"], s["out"], s["lens_k"], lse=s["lse"], cu_seqlens_q=s["cu_q"])
+    kda.kda_attn_qcache_fwd(s["q"], s["cache"], s["scale"], s["out"], s["lens_k"], lse=s["lse"], cu_seqlens_q=s["cu_q"])
     return (s["out"],) if s["lse"] is None else (s["out"], s["lse"])
 
 
