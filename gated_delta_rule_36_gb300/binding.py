@@ -18,7 +18,7 @@ import torch
 from . import build as _build
 
 KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_ALIAS, KDA_ERR_WORKSPACE, KDA_ERR_CUDA = range(6)
-KDA_BF16, KDA_F32, KDA_I64 = 0, 1, 2
+KDA_BF16, KDA_F32, KDA_I64, KDA_U8 = 0, 1, 2, 3
 KDA_DEVERR_CU_SEQLENS, KDA_DEVERR_TIMEOUT, KDA_DEVERR_INTERNAL = 0x1, 0x2, 0x4
 HEAD_DIM = 128
 
@@ -27,7 +27,8 @@ EXPORTED = ("kda_workspace_size", "kda_fwd", "kda_status_string", "kda_last_erro
             "kda_read_device_status", "kda_fwd_no_alloc", "kda_fwd_host_device_bytes", "kda_fwd_host",
             "kda_fwd_host_workspace_offset", "kda_decode", "kda_fwd_ex", "kda_decode_ex", "kda_fwd_schedule",
             "kda_fwd_set_trace", "kda_qk_norm_rope", "kda_attn_workspace_size", "kda_attn_fwd", "kda_lin_workspace_size",
-            "kda_lin_fwd", "kda_lin_decode")
+            "kda_lin_fwd", "kda_lin_decode", "kda_qcache_append", "kda_attn_qcache_workspace_size", "kda_attn_qcache_fwd",
+            "kda_gated_norm", "kda_residual_norm")
 KDA_FLAG_BETA_LOGIT, KDA_FLAG_GATE_SOFTPLUS = 0x1, 0x2
 KDA_FLAG_KERNEL_MASK = 0xF00
 KDA_KERNEL_DEFAULT, KDA_KERNEL_CHUNK16, KDA_KERNEL_REGISTER_STATE, KDA_KERNEL_BF16_STATE = 0x000, 0x100, 0x200, 0x300
@@ -36,6 +37,9 @@ KDA_SCHEDULE_TWO_PER_SM, KDA_SCHEDULE_ONE_PER_SM, KDA_SCHEDULE_CLUSTER, KDA_SCHE
 KDA_TRACE_POINTS = 8
 KDA_DEVERR_POSITION = 0x8
 KDA_FLAG_ROPE_INTERLEAVED = 0x1
+KDA_FLAG_GATE_SILU = 0x1
+KDA_QCACHE_ROW = 144
+KDA_RESIDUAL_MAX_DIM = 16384
 
 _DTYPE = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32, torch.int64: KDA_I64}
 
@@ -121,6 +125,16 @@ def load(path: Optional[str] = None):
         lib.kda_lin_fwd.argtypes = [D, D, D, D, F, D, D, D, D, V, ctypes.c_size_t, V]
         lib.kda_lin_decode.restype = ctypes.c_int
         lib.kda_lin_decode.argtypes = [D, D, D, D, F, D, D, D, V]
+        lib.kda_qcache_append.restype = ctypes.c_int
+        lib.kda_qcache_append.argtypes = [D, D, D, D, D, D, D, V, V]
+        lib.kda_attn_qcache_workspace_size.restype = ctypes.c_size_t
+        lib.kda_attn_qcache_workspace_size.argtypes = [ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int]
+        lib.kda_attn_qcache_fwd.restype = ctypes.c_int
+        lib.kda_attn_qcache_fwd.argtypes = [D, D, F, D, D, D, D, V, ctypes.c_size_t, V]
+        lib.kda_gated_norm.restype = ctypes.c_int
+        lib.kda_gated_norm.argtypes = [D, D, D, D, F, ctypes.c_uint32, V]
+        lib.kda_residual_norm.restype = ctypes.c_int
+        lib.kda_residual_norm.argtypes = [D, D, D, D, F, D, D, D, F, V]
         if path is None:
             _lib = lib
         return lib
@@ -387,6 +401,23 @@ def _view(t, name, device):
     return _PACK_VIEW(t.data_ptr() or 16, dtype, len(shape), *shape, *pad, *t.stride(), *pad)
 
 
+def _bytes_view(t, name, device):
+    """The packed kda_view of a uint8 CUDA tensor of any strides (a cache in 4 bits)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dtype != torch.uint8 or t.get_device() != device or device < 0 or t.dim() != 4:
+        raise ValueError(f"{name}: must be a uint8 CUDA tensor [N, S, Hk, {KDA_QCACHE_ROW}] on the other tensors' device")
+    return _PACK_VIEW(t.data_ptr() or 16, KDA_U8, 4, *t.shape, *t.stride())
+
+
+def _status_word(status, device):
+    if status is None:
+        return None
+    if not (isinstance(status, torch.Tensor) and status.get_device() == device and status.dtype == torch.uint8 and status.numel() >= 4):
+        raise ValueError("status: must be a uint8 CUDA tensor of at least 4 bytes on the other tensors' device")
+    return status.data_ptr()
+
+
 def _dense(t, name, device):
     """The packed kda_tensor of a contiguous CUDA tensor."""
     if t is None:
@@ -514,5 +545,72 @@ def kda_lin_decode(q, k, v, log_decay, scale, out, initial_state=None, final_sta
                             _dense(log_decay, "log_decay", dev), scale, _view(out, "out", dev),
                             _dense(initial_state, "initial_state", dev), _dense(final_state, "final_state", dev),
                             _stream(stream, dev))
+    if st:
+        _check(lib, st)
+
+
+# ---------------------------------------------------------------------------
+# Around the mixers: a cache in 4 bits and the attention over it, and the norms between the blocks.
+# ---------------------------------------------------------------------------
+def kda_qcache_append(k, v, cache, seqlens_k, cu_seqlens=None, k_out=None, v_out=None, status=None, stream=None):
+    """Append keys and values k, v [T, Hk, 128] to a cache in 4 bits, uint8 [N, S, Hk, KDA_QCACHE_ROW]: sequence n's
+    new tokens end at position seqlens_k[n].  ``k_out`` / ``v_out`` (may be k / v themselves) receive the
+    values that the cache now stands for.  ``status``: a CUDA uint8 tensor of at least 4 bytes whose first word
+    collects KDA_DEVERR_CU_SEQLENS (see kda_read_device_status).  Tensors as in ``include/kda.h``."""
+    lib = _lib or load()
+    dev = _device(k, "k")
+    dc, word = _bytes_view(cache, "cache", dev), _status_word(status, dev)
+    st = lib.kda_qcache_append(_view(k, "k", dev), _view(v, "v", dev), dc, _dense(seqlens_k, "seqlens_k", dev),
+                               _dense(cu_seqlens, "cu_seqlens", dev), _view(k_out, "k_out", dev), _view(v_out, "v_out", dev), word,
+                               _stream(stream, dev))
+    if st:
+        _check(lib, st)
+
+
+def kda_attn_qcache_workspace_size(Tq: int, Hq: int, Hk: int, N: int) -> int:
+    return int(load().kda_attn_qcache_workspace_size(int(Tq), int(Hq), int(Hk), int(N)))
+
+
+def kda_attn_qcache_fwd(q, cache, scale, out, seqlens_k, lse=None, cu_seqlens_q=None, workspace=None, stream=None):
+    """Causal softmax attention with grouped heads over a cache in 4 bits: q, out [Tq, Hq, 128], cache uint8
+    [N, S, Hk, KDA_QCACHE_ROW], seqlens_k [N].  Modes as kda_attn_fwd's over a cache, tensors as in
+    ``include/kda.h``.  Returns the workspace (its first word is the device status)."""
+    lib = _lib or load()
+    dev = _device(q, "q")
+    dq, dc = _view(q, "q", dev), _bytes_view(cache, "cache", dev)
+    if workspace is None and q.dim() == 3:
+        n = cache.shape[0] if cu_seqlens_q is None else max(cu_seqlens_q.numel() - 1, 0)
+        nbytes = lib.kda_attn_qcache_workspace_size(q.shape[0], q.shape[1], cache.shape[2], n) or 256   # 0: refused below
+        workspace = _workspace(None, nbytes, dev, stream)
+    else:
+        workspace = _workspace(workspace, 256, dev, stream)
+    st = lib.kda_attn_qcache_fwd(dq, dc, scale, _view(out, "out", dev), _dense(seqlens_k, "seqlens_k", dev), _dense(lse, "lse", dev),
+                                 _dense(cu_seqlens_q, "cu_seqlens_q", dev), workspace.data_ptr(), workspace.numel(),
+                                 _stream(stream, dev))
+    if st:
+        _check(lib, st)
+    return workspace
+
+
+def kda_gated_norm(x, gate, weight, out, eps=1e-6, flags=0, stream=None):
+    """RMS norm of every head of x [T, H, 128] times sigmoid(gate) (g sigmoid(g) with KDA_FLAG_GATE_SILU); out may be
+    x or gate itself.  Tensors as in ``include/kda.h``; all may be strided views."""
+    lib = _lib or load()
+    dev = _device(x, "x")
+    st = lib.kda_gated_norm(_view(x, "x", dev), _view(gate, "gate", dev), _dense(weight, "weight", dev), _view(out, "out", dev), eps,
+                            flags, _stream(stream, dev))
+    if st:
+        _check(lib, st)
+
+
+def kda_residual_norm(y, residual, pre_weight, out, residual_out=None, post_weight=None, gate=None, scale=1.0, eps=1e-6, stream=None):
+    """r = residual + scale * gate * norm(y) (the norm with ``post_weight``, the gate if given) into ``residual_out``, and
+    norm(r) * pre_weight into ``out``: y, out bf16 [T, D], the stream bf16 or fp32.  With y None: the norm of the
+    stream alone.  Tensors as in ``include/kda.h``."""
+    lib = _lib or load()
+    dev = _device(residual, "residual")
+    st = lib.kda_residual_norm(_view(y, "y", dev), _view(residual, "residual", dev), _dense(post_weight, "post_weight", dev),
+                               _view(gate, "gate", dev), scale, _dense(pre_weight, "pre_weight", dev),
+                               _view(residual_out, "residual_out", dev), _view(out, "out", dev), eps, _stream(stream, dev))
     if st:
         _check(lib, st)

@@ -1,5 +1,6 @@
 // Launch parameters and internal entry points of the token-mixer operators beside KDA
-// (include/kda.h: kda_qk_norm_rope, kda_attn_fwd, kda_lin_fwd, kda_lin_decode).
+// (include/kda.h: kda_qk_norm_rope, kda_attn_fwd, kda_lin_fwd, kda_lin_decode) and of those around
+// them (kda_qcache_append, kda_attn_qcache_fwd, kda_gated_norm, kda_residual_norm).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -65,6 +66,64 @@ struct LinParams {
     int test_skip;                  // the test-only build: the share b that withholds an arrival, -2 - b: that finds itself unsound; -1 for none
 };
 
+// A cache in 4 bits, [sequences, rows, heads, 144] bytes: strides in bytes.
+struct QcacheView {
+    uint8_t* data;
+    int64_t seq, row, head;
+};
+
+struct QcacheAppendParams {
+    RowsView k, v, k_out, v_out;    // k_out.data, v_out.data: nullptr = not stored
+    QcacheView cache;
+    const int64_t* seqlens_k;       // [nseq]
+    const int64_t* cu;              // [nseq + 1] or nullptr: `uniform` tokens each
+    int64_t uniform;
+    int64_t T, S;
+    int nseq, Hk;
+    uint32_t* status;               // or nullptr
+};
+
+struct QcacheAttnParams {
+    RowsView q, out;
+    QcacheView cache;
+    float* lse;                     // [Tq, Hq] or nullptr
+    const int64_t* cu_q;            // [nseq + 1] or nullptr: uniform_q queries each
+    const int64_t* seqlens_k;       // [nseq]
+    int64_t uniform_q;
+    int64_t Tq, S;
+    int nseq, Hq, Hk;
+    float scale;
+    uint32_t* status;
+    void* workspace;                // behind the status word
+};
+
+struct GatedNormParams {
+    RowsView x, gate, out;
+    const float* weight;            // nullptr = 1
+    int64_t tokens;
+    int heads;
+    float eps;
+    int silu;
+};
+
+struct ResidualNormParams {
+    const __nv_bfloat16* y;         // nullptr: r = residual
+    const __nv_bfloat16* gate;      // nullptr = 1
+    const void* residual;
+    void* residual_out;             // nullptr = not stored
+    __nv_bfloat16* out;
+    const float *post_weight, *pre_weight;   // nullptr: no norm after the block; 1
+    int64_t y_row, gate_row, residual_row, residual_out_row, out_row;   // strides in elements
+    int64_t tokens;
+    int dim, f32;                   // f32: the residual stream is fp32
+    float scale, eps;
+};
+
+cudaError_t launch_qcache_append(const QcacheAppendParams& p, cudaStream_t stream);
+cudaError_t launch_attn_qcache(const QcacheAttnParams& p, cudaStream_t stream);
+size_t attn_qcache_workspace_bytes(int64_t Tq, int Hq, int Hk, int nseq);
+cudaError_t launch_gated_norm(const GatedNormParams& p, cudaStream_t stream);
+cudaError_t launch_residual_norm(const ResidualNormParams& p, cudaStream_t stream);
 cudaError_t launch_norm_rope(const NormRopeParams& p, cudaStream_t stream);
 cudaError_t launch_attn(const AttnParams& p, cudaStream_t stream);
 size_t attn_workspace_bytes(int64_t Tq, int Hq, int Hk);

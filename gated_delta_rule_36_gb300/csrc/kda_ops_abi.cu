@@ -40,7 +40,7 @@ kda_status fail(kda_status s, const char* fmt, ...) {
 template <class T>
 bool present(const T* t) { return t != nullptr && t->data != nullptr; }
 
-size_t elem_size(int32_t dt) { return dt == KDA_F32 ? 4 : dt == KDA_I64 ? 8 : 2; }
+size_t elem_size(int32_t dt) { return dt == KDA_F32 ? 4 : dt == KDA_I64 ? 8 : dt == KDA_U8 ? 1 : 2; }
 
 kda_status check_tensor(const char* name, const kda_tensor* t, int32_t dtype, int ndim, const int64_t* shape,
                         size_t align) {
@@ -200,6 +200,78 @@ kda_status check_workspace(void* workspace, size_t bytes, size_t need) {
     if (workspace == nullptr || (uintptr_t)workspace % 256 != 0)
         return fail(KDA_ERR_WORKSPACE, "workspace must be a 256-byte aligned device pointer");
     if (bytes < need) return fail(KDA_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", bytes, need);
+    return KDA_OK;
+}
+
+// A cache in 4 bits, [nseq, S, Hk, 144] bytes.  Its last dimension and rank first, before the others are used.
+kda_status check_qcache_rank(const kda_view* t) {
+    if (!present(t)) return fail(KDA_ERR_INVALID_ARG, "cache: missing");
+    if (t->dtype != KDA_U8) return fail(KDA_ERR_INVALID_ARG, "cache: dtype %d, expected uint8", t->dtype);
+    if (t->ndim != 4 || t->shape[3] != KDA_QCACHE_ROW)
+        return fail(KDA_ERR_INVALID_ARG, "cache: expected uint8 [N,S,Hk,%d]", KDA_QCACHE_ROW);
+    return KDA_OK;
+}
+kda_status check_qcache(const kda_view* t, int64_t nseq, int64_t Hk) {
+    if (t->shape[0] != nseq || t->shape[2] != Hk)
+        return fail(KDA_ERR_INVALID_ARG, "cache: [%lld,%lld,%lld,144] for %lld sequences and %lld key heads", (long long)t->shape[0],
+                    (long long)t->shape[1], (long long)t->shape[2], (long long)nseq, (long long)Hk);
+    if (t->shape[1] < 0) return fail(KDA_ERR_INVALID_ARG, "cache: bad shape");
+    if (t->shape[1] > (1 << 30)) return fail(KDA_ERR_UNSUPPORTED, "cache: more than 2^30 rows for a sequence");
+    if (t->stride[3] != 1) return fail(KDA_ERR_INVALID_ARG, "cache: the innermost stride must be 1");
+    for (int i = 0; i < 3; ++i) {
+        if (t->shape[i] <= 1) continue;
+        if (t->stride[i] < KDA_QCACHE_ROW || t->stride[i] % 16 != 0 || t->stride[i] >= (1LL << 39))
+            return fail(KDA_ERR_INVALID_ARG, "cache: stride %lld of dim %d must be a multiple of 16, at least %d", (long long)t->stride[i],
+                        i, KDA_QCACHE_ROW);
+        if (t->shape[i] > (1LL << 48) / t->stride[i])
+            return fail(KDA_ERR_INVALID_ARG, "cache: dim %d of %lld rows with stride %lld fits no memory", i, (long long)t->shape[i],
+                        (long long)t->stride[i]);
+    }
+    if ((uintptr_t)t->data % 16 != 0) return fail(KDA_ERR_INVALID_ARG, "cache: data pointer not 16-byte aligned");
+    return KDA_OK;
+}
+kda::QcacheView qcache_view(const kda_view* t) {
+    kda::QcacheView r;
+    r.data = static_cast<uint8_t*>(t->data);
+    r.head = t->shape[2] > 1 ? t->stride[2] : KDA_QCACHE_ROW;
+    r.row = t->shape[1] > 1 ? t->stride[1] : r.head * t->shape[2];
+    r.seq = t->shape[0] > 1 ? t->stride[0] : r.row * t->shape[1];
+    return r;
+}
+
+// A [T, D] view of rows of 16-byte groups; with `repeat` a token stride of 0 is taken too.
+kda_status check_rows(const char* name, const kda_view* t, int32_t dtype, int64_t T, int64_t D, bool repeat, int64_t* row) {
+    if (!present(t)) return fail(KDA_ERR_INVALID_ARG, "%s: missing", name);
+    if (t->dtype != dtype) return fail(KDA_ERR_INVALID_ARG, "%s: dtype %d, expected %d", name, t->dtype, dtype);
+    if (t->ndim != 2 || t->shape[0] != T || t->shape[1] != D)
+        return fail(KDA_ERR_INVALID_ARG, "%s: expected [%lld,%lld]", name, (long long)T, (long long)D);
+    if (t->stride[1] != 1) return fail(KDA_ERR_INVALID_ARG, "%s: the innermost stride must be 1", name);
+    *row = 0;
+    if (T > 1 && !(repeat && t->stride[0] == 0)) {
+        if (t->stride[0] < D || t->stride[0] % 8 != 0 || T > (1LL << 48) / t->stride[0])
+            return fail(KDA_ERR_INVALID_ARG, "%s: token stride %lld must be a multiple of 8, at least %lld", name, (long long)t->stride[0],
+                        (long long)D);
+        *row = t->stride[0];
+    }
+    if ((uintptr_t)t->data % 16 != 0) return fail(KDA_ERR_INVALID_ARG, "%s: data pointer not 16-byte aligned", name);
+    return KDA_OK;
+}
+
+// The sequences of packed tokens: N from cu or from the cache; `uniform` tokens each without cu.
+kda_status check_sequences(const char* name, const kda_tensor* cu, const kda_view* cache, int64_t tokens, int64_t* nseq, int64_t* uniform) {
+    *nseq = cache->shape[0];
+    if (present(cu)) {
+        if (cu->ndim != 1 || cu->shape[0] < 1) return fail(KDA_ERR_INVALID_ARG, "%s: expected int64 [N+1]", name);
+        *nseq = cu->shape[0] - 1;
+    }
+    if (*nseq < 0 || *nseq > INT32_MAX / 65536) return fail(KDA_ERR_UNSUPPORTED, "too many sequences");
+    if (present(cu)) {
+        KDA_TRY(check_i64(name, cu, *nseq + 1));
+    } else if (*nseq == 0 ? tokens != 0 : tokens % *nseq != 0) {
+        return fail(KDA_ERR_INVALID_ARG, "without %s the %lld tokens must divide into %lld sequences", name, (long long)tokens,
+                    (long long)*nseq);
+    }
+    *uniform = *nseq > 0 ? tokens / *nseq : 0;
     return KDA_OK;
 }
 
@@ -503,6 +575,216 @@ kda_status kda_lin_decode(const kda_view* q, const kda_view* k, const kda_view* 
     p.scale = scale;
     const cudaError_t e = kda::launch_lin_decode(p, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(KDA_ERR_CUDA, "linear attention step launch: %s", cudaGetErrorString(e));
+    return KDA_OK;
+}
+
+kda_status kda_qcache_append(const kda_view* k, const kda_view* v, const kda_view* cache, const kda_tensor* seqlens_k,
+                             const kda_tensor* cu_seqlens, const kda_view* k_out, const kda_view* v_out, uint32_t* status,
+                             kda_stream_t stream) {
+    kda::set_last_error("");
+    if ((uintptr_t)status % 4 != 0) return fail(KDA_ERR_INVALID_ARG, "status: not 4-byte aligned");
+    KDA_TRY(check_head_dim("k", k, 3));
+    const int64_t T = k->shape[0], Hk = k->shape[1];
+    if (T < 0 || Hk < 1) return fail(KDA_ERR_INVALID_ARG, "k: bad shape [%lld,%lld,128]", (long long)T, (long long)Hk);
+    if (T > (1 << 30) || Hk > 65535) return fail(KDA_ERR_UNSUPPORTED, "T must be <= 2^30 and Hk <= 65535");
+    const int64_t shape[3] = {T, Hk, KDA_HEAD_DIM};
+    KDA_TRY(check_view("k", k, 3, shape));
+    KDA_TRY(check_view("v", v, 3, shape));
+    KDA_TRY(check_qcache_rank(cache));
+    int64_t nseq, uniform;
+    KDA_TRY(check_sequences("cu_seqlens", cu_seqlens, cache, T, &nseq, &uniform));
+    KDA_TRY(check_qcache(cache, nseq, Hk));
+    KDA_TRY(check_i64("seqlens_k", seqlens_k, nseq));
+    if (present(k_out) != present(v_out)) return fail(KDA_ERR_INVALID_ARG, "k_out and v_out must both be given, or neither");
+    if (present(k_out)) {
+        KDA_TRY(check_view("k_out", k_out, 3, shape));
+        KDA_TRY(check_view("v_out", v_out, 3, shape));
+    }
+    const kda_view* written[3] = {cache, k_out, v_out};
+    const char* names[3] = {"cache", "k_out", "v_out"};
+    for (int i = 0; i < 3; ++i) {
+        if (!present(written[i])) continue;
+        const Extent o = extent(written[i]);
+        for (int j = 0; j < 2; ++j)
+            if (overlap(o, extent(j ? v : k)) && !(i == j + 1 && same_view(written[i], j ? v : k)))
+                return fail(KDA_ERR_ALIAS, "%s overlaps %s", names[i], j ? "v" : "k");
+        for (int j = i + 1; j < 3; ++j)
+            if (present(written[j]) && overlap(o, extent(written[j]))) return fail(KDA_ERR_ALIAS, "%s and %s overlap", names[i], names[j]);
+        for (const kda_tensor* t : {seqlens_k, cu_seqlens})
+            if (present(t) && overlap(o, extent(t))) return fail(KDA_ERR_ALIAS, "%s overlaps the lengths", names[i]);
+    }
+    kda::QcacheAppendParams p;
+    memset(&p, 0, sizeof(p));
+    p.k = rows_view(k, 0);
+    p.v = rows_view(v, 0);
+    if (present(k_out)) {
+        p.k_out = rows_view(k_out, 0);
+        p.v_out = rows_view(v_out, 0);
+    }
+    p.cache = qcache_view(cache);
+    p.seqlens_k = static_cast<const int64_t*>(seqlens_k->data);
+    p.cu = present(cu_seqlens) ? static_cast<const int64_t*>(cu_seqlens->data) : nullptr;
+    p.uniform = uniform;
+    p.T = T;
+    p.S = cache->shape[1];
+    p.nseq = (int)nseq;
+    p.Hk = (int)Hk;
+    p.status = status;
+    const cudaError_t e = kda::launch_qcache_append(p, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(KDA_ERR_CUDA, "cache append launch: %s", cudaGetErrorString(e));
+    return KDA_OK;
+}
+
+size_t kda_attn_qcache_workspace_size(int64_t Tq, int Hq, int Hk, int N) {
+    if (Tq < 0 || Hq < 1 || Hk < 1 || Hq % Hk != 0 || N < 0) return 0;
+    return kHeaderBytes + kda::attn_qcache_workspace_bytes(Tq, Hq, Hk, N);
+}
+
+kda_status kda_attn_qcache_fwd(const kda_view* q, const kda_view* cache, float scale, const kda_view* out,
+                               const kda_tensor* seqlens_k, const kda_tensor* lse, const kda_tensor* cu_seqlens_q,
+                               void* workspace, size_t workspace_bytes, kda_stream_t stream) {
+    kda::set_last_error("");
+    if (!isfinite(scale) || scale < 0.f) return fail(KDA_ERR_INVALID_ARG, "scale must be finite and >= 0");
+    KDA_TRY(check_head_dim("q", q, 3));
+    KDA_TRY(check_qcache_rank(cache));
+    const int64_t Tq = q->shape[0], Hq = q->shape[1], Hk = cache->shape[2];
+    if (Tq < 0 || Hq < 1 || Hk < 1) return fail(KDA_ERR_INVALID_ARG, "bad q or cache shape");
+    if (Hq % Hk != 0) return fail(KDA_ERR_INVALID_ARG, "%lld query heads do not divide into %lld key heads", (long long)Hq, (long long)Hk);
+    if (Tq > (1 << 30) || Hq > 65535 || Hq / Hk > 128)
+        return fail(KDA_ERR_UNSUPPORTED, "Tq must be <= 2^30, Hq <= 65535 and Hq / Hk <= 128");
+    int64_t nseq, uniform;
+    KDA_TRY(check_sequences("cu_seqlens_q", cu_seqlens_q, cache, Tq, &nseq, &uniform));
+    KDA_TRY(check_qcache(cache, nseq, Hk));
+    KDA_TRY(check_i64("seqlens_k", seqlens_k, nseq));
+    const int64_t qshape[3] = {Tq, Hq, KDA_HEAD_DIM};
+    KDA_TRY(check_view("q", q, 3, qshape));
+    KDA_TRY(check_view("out", out, 3, qshape));
+    if (present(lse)) {
+        const int64_t lshape[2] = {Tq, Hq};
+        KDA_TRY(check_tensor("lse", lse, KDA_F32, 2, lshape, 4));
+    }
+    for (const kda_view* t : {q, cache})
+        if (overlap(extent(out), extent(t)) || (present(lse) && overlap(extent(lse), extent(t))))
+            return fail(KDA_ERR_ALIAS, "out or lse overlaps an input");
+    for (const kda_tensor* t : {cu_seqlens_q, seqlens_k})
+        if (present(t) && (overlap(extent(out), extent(t)) || (present(lse) && overlap(extent(lse), extent(t)))))
+            return fail(KDA_ERR_ALIAS, "out or lse overlaps the lengths");
+    if (present(lse) && overlap(extent(out), extent(lse))) return fail(KDA_ERR_ALIAS, "out and lse overlap");
+    KDA_TRY(check_workspace(workspace, workspace_bytes, kda_attn_qcache_workspace_size(Tq, (int)Hq, (int)Hk, (int)nseq)));
+    kda::QcacheAttnParams p;
+    memset(&p, 0, sizeof(p));
+    p.q = rows_view(q, 0);
+    p.out = rows_view(out, 0);
+    p.cache = qcache_view(cache);
+    p.lse = present(lse) ? static_cast<float*>(lse->data) : nullptr;
+    p.cu_q = present(cu_seqlens_q) ? static_cast<const int64_t*>(cu_seqlens_q->data) : nullptr;
+    p.seqlens_k = static_cast<const int64_t*>(seqlens_k->data);
+    p.uniform_q = uniform;
+    p.Tq = Tq;
+    p.S = cache->shape[1];
+    p.nseq = (int)nseq;
+    p.Hq = (int)Hq;
+    p.Hk = (int)Hk;
+    p.scale = scale;
+    p.status = static_cast<uint32_t*>(workspace);
+    p.workspace = static_cast<char*>(workspace) + kHeaderBytes;
+    const cudaError_t e = kda::launch_attn_qcache(p, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(KDA_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
+    return KDA_OK;
+}
+
+kda_status kda_gated_norm(const kda_view* x, const kda_view* gate, const kda_tensor* weight, const kda_view* out, float eps,
+                          uint32_t flags, kda_stream_t stream) {
+    kda::set_last_error("");
+    if (flags & ~KDA_FLAG_GATE_SILU) return fail(KDA_ERR_INVALID_ARG, "flags: unknown bits 0x%x", flags & ~KDA_FLAG_GATE_SILU);
+    if (!isfinite(eps) || eps < 0.f) return fail(KDA_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    KDA_TRY(check_head_dim("x", x, 3));
+    const int64_t T = x->shape[0], H = x->shape[1];
+    if (T < 0 || H < 1) return fail(KDA_ERR_INVALID_ARG, "x: bad shape [%lld,%lld,128]", (long long)T, (long long)H);
+    if (T > INT32_MAX || H > 65535) return fail(KDA_ERR_UNSUPPORTED, "T must be < 2^31 and H <= 65535");
+    const int64_t shape[3] = {T, H, KDA_HEAD_DIM}, wshape[1] = {KDA_HEAD_DIM};
+    KDA_TRY(check_view("x", x, 3, shape));
+    KDA_TRY(check_view("gate", gate, 3, shape));
+    KDA_TRY(check_view("out", out, 3, shape));
+    if (present(weight)) KDA_TRY(check_tensor("weight", weight, KDA_F32, 1, wshape, 16));
+    const Extent o = extent(out);
+    if (overlap(o, extent(x)) && !same_view(out, x)) return fail(KDA_ERR_ALIAS, "out overlaps x and is not exactly the same view");
+    if (overlap(o, extent(gate)) && !same_view(out, gate)) return fail(KDA_ERR_ALIAS, "out overlaps gate and is not exactly the same view");
+    if (present(weight) && overlap(o, extent(weight))) return fail(KDA_ERR_ALIAS, "out overlaps weight");
+    kda::GatedNormParams p;
+    memset(&p, 0, sizeof(p));
+    p.x = rows_view(x, 0);
+    p.gate = rows_view(gate, 0);
+    p.out = rows_view(out, 0);
+    p.weight = present(weight) ? static_cast<const float*>(weight->data) : nullptr;
+    p.tokens = T;
+    p.heads = (int)H;
+    p.eps = eps;
+    p.silu = (flags & KDA_FLAG_GATE_SILU) != 0;
+    const cudaError_t e = kda::launch_gated_norm(p, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(KDA_ERR_CUDA, "gated norm launch: %s", cudaGetErrorString(e));
+    return KDA_OK;
+}
+
+kda_status kda_residual_norm(const kda_view* y, const kda_view* residual, const kda_tensor* post_weight, const kda_view* gate,
+                             float scale, const kda_tensor* pre_weight, const kda_view* residual_out, const kda_view* out,
+                             float eps, kda_stream_t stream) {
+    kda::set_last_error("");
+    if (!isfinite(scale)) return fail(KDA_ERR_INVALID_ARG, "scale must be finite");
+    if (!isfinite(eps) || eps < 0.f) return fail(KDA_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    if (!present(residual)) return fail(KDA_ERR_INVALID_ARG, "residual: missing");
+    if (residual->dtype != KDA_BF16 && residual->dtype != KDA_F32) return fail(KDA_ERR_INVALID_ARG, "residual: dtype must be bf16 or fp32");
+    if (residual->ndim != 2) return fail(KDA_ERR_INVALID_ARG, "residual: expected [T,D]");
+    const int64_t T = residual->shape[0], D = residual->shape[1];
+    if (T < 0 || D < 1) return fail(KDA_ERR_INVALID_ARG, "residual: bad shape [%lld,%lld]", (long long)T, (long long)D);
+    if (T > INT32_MAX || D % 8 != 0 || D > KDA_RESIDUAL_MAX_DIM)
+        return fail(KDA_ERR_UNSUPPORTED, "T must be < 2^31, and D a multiple of 8 up to %d", KDA_RESIDUAL_MAX_DIM);
+    if (!present(y) && (present(post_weight) || present(gate) || present(residual_out)))
+        return fail(KDA_ERR_INVALID_ARG, "without y, post_weight, gate and residual_out must be absent too");
+    kda::ResidualNormParams p;
+    memset(&p, 0, sizeof(p));
+    if (present(y)) KDA_TRY(check_rows("y", y, KDA_BF16, T, D, false, &p.y_row));
+    KDA_TRY(check_rows("residual", residual, residual->dtype, T, D, false, &p.residual_row));
+    if (present(gate)) KDA_TRY(check_rows("gate", gate, KDA_BF16, T, D, true, &p.gate_row));
+    if (present(residual_out)) KDA_TRY(check_rows("residual_out", residual_out, residual->dtype, T, D, false, &p.residual_out_row));
+    KDA_TRY(check_rows("out", out, KDA_BF16, T, D, false, &p.out_row));
+    const int64_t wshape[1] = {D};
+    if (present(post_weight)) KDA_TRY(check_tensor("post_weight", post_weight, KDA_F32, 1, wshape, 16));
+    if (present(pre_weight)) KDA_TRY(check_tensor("pre_weight", pre_weight, KDA_F32, 1, wshape, 16));
+    // every token is read before it is written, by the threads that write it
+    const kda_view* written[2] = {out, residual_out};
+    const char* names[2] = {"out", "residual_out"};
+    for (int i = 0; i < 2; ++i) {
+        if (!present(written[i])) continue;
+        const Extent o = extent(written[i]);
+        const bool over_y = i == 0, over_residual = i == 1 || (!present(residual_out) && residual->dtype == KDA_BF16);
+        if (present(y) && overlap(o, extent(y)) && !(over_y && same_view(written[i], y)))
+            return fail(KDA_ERR_ALIAS, "%s overlaps y", names[i]);
+        if (overlap(o, extent(residual)) && !(over_residual && same_view(written[i], residual)))
+            return fail(KDA_ERR_ALIAS, "%s overlaps residual", names[i]);
+        if (present(gate)) {
+            kda_view g = *gate;
+            if (p.gate_row == 0) g.shape[0] = T > 0 ? 1 : 0;   // (one row, repeated)
+            if (overlap(o, extent(&g))) return fail(KDA_ERR_ALIAS, "%s overlaps gate", names[i]);
+        }
+        for (const kda_tensor* t : {post_weight, pre_weight})
+            if (present(t) && overlap(o, extent(t))) return fail(KDA_ERR_ALIAS, "%s overlaps a weight", names[i]);
+    }
+    if (present(residual_out) && overlap(extent(out), extent(residual_out))) return fail(KDA_ERR_ALIAS, "out and residual_out overlap");
+    p.y = present(y) ? static_cast<const __nv_bfloat16*>(y->data) : nullptr;
+    p.gate = present(gate) ? static_cast<const __nv_bfloat16*>(gate->data) : nullptr;
+    p.residual = residual->data;
+    p.residual_out = present(residual_out) ? residual_out->data : nullptr;
+    p.out = static_cast<__nv_bfloat16*>(out->data);
+    p.post_weight = present(post_weight) ? static_cast<const float*>(post_weight->data) : nullptr;
+    p.pre_weight = present(pre_weight) ? static_cast<const float*>(pre_weight->data) : nullptr;
+    p.tokens = T;
+    p.dim = (int)D;
+    p.f32 = residual->dtype == KDA_F32;
+    p.scale = scale;
+    p.eps = eps;
+    const cudaError_t e = kda::launch_residual_norm(p, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(KDA_ERR_CUDA, "residual norm launch: %s", cudaGetErrorString(e));
     return KDA_OK;
 }
 

@@ -48,7 +48,7 @@ typedef enum {
     KDA_ERR_CUDA = 5           /* a CUDA runtime/driver call or kernel launch failed            */
 } kda_status;
 
-typedef enum { KDA_BF16 = 0, KDA_F32 = 1, KDA_I64 = 2 } kda_dtype;
+typedef enum { KDA_BF16 = 0, KDA_F32 = 1, KDA_I64 = 2, KDA_U8 = 3 } kda_dtype;
 
 /* A dense, contiguous (row-major) device tensor.  data == NULL marks an absent
  * optional tensor; the descriptor pointer itself may also be NULL for those. */
@@ -458,6 +458,112 @@ kda_status kda_lin_fwd(const kda_view* q, const kda_view* k, const kda_view* v, 
 kda_status kda_lin_decode(const kda_view* q, const kda_view* k, const kda_view* v, const kda_tensor* log_decay,
                           float scale, const kda_view* out, const kda_tensor* initial_state,
                           const kda_tensor* final_state, kda_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Around the mixers: a key/value cache held in 4 bits and the attention over it, the norm and gate
+ * of a mixer's output, and the norms, gate and residual sum between two blocks.  Same manner.
+ * ------------------------------------------------------------------------------------ */
+
+/*
+ * A cache in 4 bits is a byte tensor [N, S, Hk, 144] (KDA_U8): one row for each sequence, position and
+ * key head.  Its strides are multiples of 16 (and at least 144), its data 16-byte aligned; N and S
+ * outside or inside Hk as the caller likes ([N, Hk, S, 144] in memory makes the keys of a head contiguous).
+ *   bytes   0 ..  63   codes of the key: byte i holds channel 2 i in bits 0-3 and 2 i + 1 in bits 4-7
+ *   bytes  64 .. 127   codes of the value, likewise
+ *   bytes 128 .. 143   eight bf16: scale and zero of the key's channels 0-63, of its channels 64-127,
+ *                      then the same four of the value
+ * Channel c stands for scale * code + zero.  kda_qcache_append takes, for each 64 channels x,
+ *   zero = min x,  scale = bf16((max x - min x) / 15),  code = (x - zero) / scale to the nearest, ties to even
+ * (scale 0: code 0), exactly: the quotients are rounded as if computed without error.  A group that holds a
+ * NaN or an infinity gets scale and zero NaN.
+ */
+#define KDA_QCACHE_ROW 144
+
+/*
+ * Append new keys and values to such a cache.  Sequence n has L_n new tokens; token i of them goes to
+ * position seqlens_k[n] - L_n + i, so that seqlens_k counts the new ones already (as kda_attn_qcache_fwd
+ * takes it afterwards).
+ *
+ *   k, v          bf16 [T, Hk, 128] (views)
+ *   cache         uint8 [N, S, Hk, 144] (view)
+ *   seqlens_k     int64 [N]
+ *   cu_seqlens    int64 [N + 1]; NULL/absent: T / N new tokens each
+ *   k_out, v_out  both absent, or bf16 [T, Hk, 128] (views): the values that the cache now stands for,
+ *                 rounded to bf16 (what attention over the new tokens themselves should read to agree with
+ *                 later reads of the cache).  k_out may be exactly k, and v_out exactly v
+ *   status        device word (4-byte aligned) that error bits are added to, or NULL
+ * Any other overlap of a written tensor is KDA_ERR_ALIAS.  Tokens that belong to no sequence are passed
+ * over.  Lengths that contradict the tensors (also L_n > seqlens_k[n] or seqlens_k[n] > S) set
+ * KDA_DEVERR_CU_SEQLENS in *status; nothing of that sequence is written.
+ */
+kda_status kda_qcache_append(const kda_view* k, const kda_view* v, const kda_view* cache,
+                             const kda_tensor* seqlens_k, const kda_tensor* cu_seqlens, const kda_view* k_out,
+                             const kda_view* v_out, uint32_t* status, kda_stream_t stream);
+
+/*
+ * Bytes of workspace kda_attn_qcache_fwd needs for Tq query tokens, Hq query heads, Hk key/value heads
+ * and N sequences.  Its contents need no initialisation.  Returns 0 for invalid arguments.
+ */
+size_t kda_attn_qcache_workspace_size(int64_t Tq, int Hq, int Hk, int N);
+
+/*
+ * kda_attn_fwd over a cache in 4 bits: the same formulas, masks and errors, with the keys and values that
+ * its rows stand for.
+ *   q, out         bf16 [Tq, Hq, 128] (views)
+ *   cache          uint8 [N, S, Hk, 144] (view); Hk divides Hq, Hq / Hk <= 128
+ *   seqlens_k      int64 [N], sequence n's keys are positions 0 .. seqlens_k[n] - 1
+ *   lse            fp32 [Tq, Hq], or NULL/absent
+ *   cu_seqlens_q   int64 [N + 1]; NULL/absent: Tq / N queries each
+ *   workspace      >= kda_attn_qcache_workspace_size(Tq, Hq, Hk, N) bytes, 256-byte aligned
+ * Cache rows past a sequence's keys are never used, whatever they hold; the scales and zeros inside a
+ * sequence are taken to be finite.
+ */
+kda_status kda_attn_qcache_fwd(const kda_view* q, const kda_view* cache, float scale, const kda_view* out,
+                               const kda_tensor* seqlens_k, const kda_tensor* lse, const kda_tensor* cu_seqlens_q,
+                               void* workspace, size_t workspace_bytes, kda_stream_t stream);
+
+/* kda_gated_norm: the gate g acts as g sigmoid(g) instead of sigmoid(g). */
+#define KDA_FLAG_GATE_SILU 0x1u
+
+/*
+ * RMS norm of every head of a mixer's output, times its activated gate:
+ *   out = x / sqrt(mean(x^2) + eps) * weight * sigmoid(gate)
+ *
+ *   x, gate, out  bf16 [T, H, 128] (views); out may be exactly x, or exactly gate (any other overlap:
+ *                 KDA_ERR_ALIAS)
+ *   weight        fp32 [128], or NULL/absent (= 1)
+ *   eps           finite, >= 0
+ *   flags         KDA_FLAG_GATE_SILU or 0
+ * Arithmetic is fp32, rounded once at the end.
+ */
+kda_status kda_gated_norm(const kda_view* x, const kda_view* gate, const kda_tensor* weight, const kda_view* out,
+                          float eps, uint32_t flags, kda_stream_t stream);
+
+/* The widest residual stream of kda_residual_norm. */
+#define KDA_RESIDUAL_MAX_DIM 16384
+
+/*
+ * Between two blocks of a residual stack, in one pass: the norm after the first, its gate and residual
+ * scale, the sum with the stream, and the norm before the second:
+ *   u = y / sqrt(mean(y^2) + eps) * post_weight      (y itself without post_weight)
+ *   r = residual + scale * gate * u                  (without the gate: scale * u)
+ *   residual_out = r,   out = r / sqrt(mean(r^2) + eps) * pre_weight
+ *
+ *   y, out         bf16 [T, D] (views); D a multiple of 8 up to KDA_RESIDUAL_MAX_DIM.  y absent: r = residual
+ *                  (post_weight, gate and residual_out absent too)
+ *   residual       bf16 or fp32 [T, D] (view)
+ *   residual_out   as residual, or absent (not stored); may be exactly residual
+ *   gate           bf16 [T, D] (view; a token stride of 0 repeats one row), or absent
+ *   post_weight, pre_weight   fp32 [D], or absent (post: no norm after the block; pre: 1)
+ *   scale          finite;  eps  finite, >= 0
+ * These views have rows of 16-byte aligned elements: data 16-byte aligned, token strides multiples of
+ * 8 elements and at least D.  out may be exactly y, or exactly residual where both are bf16 and residual_out
+ * is absent; any other overlap of a written tensor is KDA_ERR_ALIAS.  Arithmetic is fp32, out is computed
+ * from the unrounded r, and each output is rounded once.
+ */
+kda_status kda_residual_norm(const kda_view* y, const kda_view* residual, const kda_tensor* post_weight,
+                             const kda_view* gate, float scale, const kda_tensor* pre_weight,
+                             const kda_view* residual_out, const kda_view* out, float eps, kda_stream_t stream);
 
 #ifdef __cplusplus
 }
