@@ -1,76 +1,679 @@
-// Causal softmax attention with grouped heads over a cache held in 4 bits: a plain kernel, one warp for each
-// query and head, one pass over the keys with the running maximum and sum.
+// Causal softmax attention with grouped heads over a cache held in 4 bits, for few queries a sequence (single
+// tokens, drafts): one pass over the keys with the running maximum and sum, mma.sync on codes that never
+// leave registers.
+//
+// A tile is 8 kN rows of (token, head) pairs that share a key head, a slice 32 keys (4,608 bytes).  A warp takes
+// every eighth slice by bulk copies into its own small ring and waits for no other warp until the tile is done:
+//   A_h = Y_h Q_h^T       (keys x queries) for the two halves h of the channels, Y = 1 + code / 16 in bf16, which
+//                         is the code's bits put into the mantissa of 1: a shift and a mask for two codes
+//   s = sum_h 16 scale_h A_h + (zero_h - 16 scale_h) sum_c q_c     in fp32
+//   p = exp2(c s - m),  l += p,  R_h = bf16(p scale'_h),  z_h += p (zero'_h + 7.5 scale'_h)   (the values' numbers)
+//   O_h += Y'_h^T R_h,  u_h += 1^T R_h
+//   out_h = (16 (O_h - 1.46875 u_h) + z_h) / l
+// so that codes count from their middle (7.5): a weight's rounding to bf16 then moves the output by 2^-9 of
+// what the value deviates from its group's middle, and the middle itself is summed in fp32.
+// The maximum m that the exponents refer to moves only when a score exceeds it by more than 8 (base 2), so that
+// most slices need no exchange between lanes.
+//
+// All (sequence, key head, tile, slice) steps are one line that is cut into equal shares, two for each SM; a tile
+// that lies in more than one share leaves unnormalised partial rows in the workspace, and a second, small kernel
+// joins them in the order of the keys.
+#include "kda_mixer.cuh"
 #include "kda_qcache.cuh"
 
 namespace kda {
 namespace {
 
-__global__ void qcache_lengths_kernel(const QcacheAttnParams p) {
-    await_stream();
-    bool bad = false;
-    for (int n = threadIdx.x; n < p.nseq; n += blockDim.x) {
-        if (p.cu_q) bad |= p.cu_q[n + 1] < p.cu_q[n] || (n == 0 && p.cu_q[0] != 0) || (n + 1 == p.nseq && p.cu_q[n + 1] > p.Tq);
-        bad |= p.seqlens_k[n] < 0 || p.seqlens_k[n] > p.S;
-    }
-    bad = __syncthreads_or(bad);
-    if (threadIdx.x == 0) *p.status = bad ? KDA_DEVERR_CU_SEQLENS : 0u;
+constexpr int QS_WARPS = 8, QS_THREADS = 32 * QS_WARPS;
+constexpr int QS_MAX_CTAS = 320;
+constexpr int SLICE = 32;                          // keys
+constexpr uint32_t SLICE_BYTES = SLICE * QC_ROW;
+constexpr int QS_MAX_ROWS = 16;                    // of a tile
+constexpr int PIECE = 6;                           // a tile's own weight, in slices
+
+// What a share leaves for the join: the tile that it starts in and how far into it, and its status bits.
+struct QsCut {
+    int j, some;        // starts at slice j (0: between two tiles); not an empty share
+    int n, kh, tile;
+    int q0, lq;
+    uint32_t status;
+};
+struct QsPartials {
+    QsCut* cut;         // [shares]
+    float2* ml;         // [2 * shares][QS_MAX_ROWS]: reference exponent (base 2) and sum
+    float* o;           // [2 * shares][QS_MAX_ROWS][128], not normalised
+};
+constexpr size_t QS_CUT_BYTES = QS_MAX_CTAS * sizeof(QsCut), QS_ML_BYTES = (size_t)2 * QS_MAX_CTAS * QS_MAX_ROWS * sizeof(float2);
+__device__ __forceinline__ QsPartials qs_partials(void* ws) {
+    char* at = static_cast<char*>(ws);
+    return QsPartials{reinterpret_cast<QsCut*>(at), reinterpret_cast<float2*>(at + QS_CUT_BYTES), reinterpret_cast<float*>(at + QS_CUT_BYTES + QS_ML_BYTES)};
 }
 
-__global__ void __launch_bounds__(128) attn_qcache_kernel(const QcacheAttnParams p) {
-    await_stream();
-    if (*p.status) return;
-    const int lane = threadIdx.x & 31;
-    const int64_t item = ((int64_t)blockIdx.x * 128 + threadIdx.x) >> 5;
-    const int64_t t = item / p.Hq;
-    const int h = (int)(item - t * p.Hq);
-    if (t >= p.Tq) return;
-    const int n = p.cu_q ? sequence_of(p.cu_q, p.nseq, t) : (int)(t / p.uniform_q);
-    const int64_t c1 = p.cu_q ? p.cu_q[n + 1] : (n + 1) * p.uniform_q;
-    if (t >= c1) return;
-    const int64_t keys = p.seqlens_k[n] - (c1 - 1 - t);   // that this query sees
-    const uint2 raw = *reinterpret_cast<const uint2*>(p.q.data + t * p.q.row + h * p.q.head + 4 * lane);
-    const float c = p.scale * LOG2E;
-    const float q[4] = {bf16_lo(raw.x), bf16_hi(raw.x), bf16_lo(raw.y), bf16_hi(raw.y)};
-    const uint8_t* row = p.cache.data + n * p.cache.seq + (h / (p.Hq / p.Hk)) * p.cache.head;
-    float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int64_t j = 0; j < keys; ++j, row += p.cache.row) {
-        const uint32_t kc = *reinterpret_cast<const uint16_t*>(row + 2 * lane), vc = *reinterpret_cast<const uint16_t*>(row + 64 + 2 * lane);
-        const uint32_t kn = *reinterpret_cast<const uint32_t*>(row + QC_NUMBERS + (lane >> 4) * 4);
-        const uint32_t vn = *reinterpret_cast<const uint32_t*>(row + QC_NUMBERS + 8 + (lane >> 4) * 4);
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s = fmaf(q[i], fmaf((float)(kc >> (4 * i) & 15u), bf16_lo(kn), bf16_hi(kn)), s);
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        s *= c;
-        if (!(s <= m)) {
-            const float f = m == -INFINITY ? 0.f : exp2f(m - s);
-            m = s;
-            l *= f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] *= f;
-        }
-        const float w = exp2f(s - m);
-        l += w;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = fmaf(w, fmaf((float)(vc >> (4 * i) & 15u), bf16_lo(vn), bf16_hi(vn)), o[i]);
+struct QsSeq {
+    int q0, lq, lk;
+};
+__device__ __forceinline__ QsSeq qs_seq(const QcacheAttnParams& p, int n) {
+    QsSeq s;
+    if (p.cu_q) {
+        s.q0 = (int)p.cu_q[n];
+        s.lq = (int)p.cu_q[n + 1] - s.q0;
+    } else {
+        s.lq = (int)p.uniform_q;
+        s.q0 = n * s.lq;
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    *reinterpret_cast<uint2*>(p.out.data + t * p.out.row + h * p.out.head + 4 * lane) =
-        make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
-    if (p.lse && lane == 0) p.lse[t * p.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    s.lk = (int)p.seqlens_k[n];
+    return s;
+}
+__device__ __forceinline__ int qs_tiles(const QsSeq& s, int G, int rows) { return (int)(((int64_t)s.lq * G + rows - 1) / rows); }
+__device__ __forceinline__ int qs_slices(const QsSeq& s) { return (s.lk + SLICE - 1) / SLICE; }
+
+// A step: slice j of tile `tile` of key head kh of sequence n.
+struct QsCursor {
+    int n, kh, tile, j;
+    QsSeq s;
+};
+struct QsShare {
+    QsCursor at;
+    int64_t weight;
+    bool bad;
+};
+
+// Where share b of `shares` equal ones starts.
+__device__ __forceinline__ int64_t qs_share_start(int64_t total, int b, int shares) {
+    if (b >= shares) return total;
+    if (total < (1LL << 22)) return (int64_t)((uint32_t)total * (uint32_t)b / (uint32_t)shares);   // (b < 2^10)
+    return total / shares * b + total % shares * b / shares;
+}
+
+// The whole block: checks the lengths, counts the steps and finds where share b starts and ends among them.
+__device__ QsShare qs_find_share(const QcacheAttnParams& p, int G, int rows, int64_t* scratch /* 32 */) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (p.nseq + QS_THREADS - 1) / QS_THREADS;
+    const int n0 = min(tid * per, p.nseq), n1 = min(n0 + per, p.nseq);
+    QsSeq s{};
+    int64_t mine = 0, each = 0;
+    bool bad = false;
+#pragma unroll 1
+    for (int n = n0; n < n1; ++n) {   // nothing is computed from bad lengths
+        bool b = false;
+        if (p.cu_q) b |= p.cu_q[n + 1] < p.cu_q[n] || (n == 0 && p.cu_q[0] != 0) || (n + 1 == p.nseq && p.cu_q[n + 1] > p.Tq);
+        b |= p.seqlens_k[n] < 0 || p.seqlens_k[n] > p.S;
+        bad |= b;
+        s = qs_seq(p, n);
+        each = b ? 0 : (int64_t)qs_tiles(s, G, rows) * p.Hk * (qs_slices(s) + PIECE);
+        mine += each;
+    }
+    int64_t sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += y;
+    }
+    if (lane == 31) scratch[warp] = sum;
+    QsShare r{};
+    r.bad = __syncthreads_or(bad);
+    if (r.bad) return r;
+    int64_t total = 0, before = sum - mine;
+#pragma unroll
+    for (int w = 0; w < QS_WARPS; ++w) {
+        before += w < warp ? scratch[w] : 0;
+        total += scratch[w];
+    }
+    // (fewer shares than CTAs where a share would not give every warp a slice)
+    const int shares = (int)min((int64_t)gridDim.x, max(total / QS_WARPS, (int64_t)1));
+    const int64_t x0 = qs_share_start(total, blockIdx.x, shares), x1 = qs_share_start(total, blockIdx.x + 1, shares);
+    QsCursor* place = reinterpret_cast<QsCursor*>(scratch + 16);
+    if (tid == 0) scratch[8] = x0, scratch[9] = x1;
+    __syncthreads();
+#pragma unroll 1
+    for (int e = 0; e < 2; ++e) {
+        const int64_t x = e ? x1 : x0;
+        if (x < before || x >= before + mine) continue;
+        int64_t base = before;
+        int n = n1 - 1;
+        if (n > n0)
+            for (n = n0;; ++n) {
+                s = qs_seq(p, n);
+                each = (int64_t)qs_tiles(s, G, rows) * p.Hk * (qs_slices(s) + PIECE);
+                if (x < base + each) break;
+                base += each;
+            }
+        const int64_t at = x - base;
+        const int w = qs_slices(s) + PIECE, tiles = qs_tiles(s, G, rows);
+        const int64_t unit = (at >> 31) == 0 ? (int64_t)((uint32_t)at / (uint32_t)w) : at / w;
+        const int from = (int)(at - unit * w), j = max(from - PIECE, 0);   // the tile's own weight is at its front
+        scratch[8 + e] = x - (j > 0 ? 0 : from);                          // (a cut inside it moves to the tile's start)
+        if (e == 0) *place = QsCursor{n, (int)(unit / tiles), (int)(unit % tiles), j, s};
+    }
+    __syncthreads();
+    if (x0 < total) {
+        r.at = *place;
+        r.weight = scratch[9] - scratch[8];
+    }
+    return r;
+}
+
+__device__ __forceinline__ void qs_next_tile(const QcacheAttnParams& p, int G, int rows, QsCursor& u) {
+    u.j = 0;
+    if (++u.tile < qs_tiles(u.s, G, rows)) return;
+    u.tile = 0;
+    if (++u.kh < p.Hk) return;
+    u.kh = 0;
+    do {
+        if (++u.n >= p.nseq) return;
+        u.s = qs_seq(p, u.n);
+    } while (u.s.lq == 0);
+}
+
+// A share's next piece: the slices [j0, j1) of one tile.
+struct QsPiece {
+    int j0, j1, nb, weight;
+};
+__device__ __forceinline__ QsPiece qs_piece(const QsCursor& u, int64_t left) {
+    QsPiece r;
+    r.nb = qs_slices(u.s);
+    r.j0 = u.j;
+    const int own = u.j == 0 ? PIECE : 0;
+    r.j1 = left - own < r.nb - u.j ? u.j + (int)left - own : r.nb;
+    r.weight = r.j1 - u.j + own;
+    return r;
+}
+
+// Two codes (bits 0-3 and 16-19 of x, moved there by a shift of 4 e bits) as 1 + code / 16 in bf16.
+template <int e>
+__device__ __forceinline__ uint32_t codes2(uint32_t x) {
+    const uint32_t y = e == 0 ? x << 3 : x >> (4 * e - 3);
+    return (y & 0x00780078u) | 0x3f803f80u;
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {   // of an 8 x 8 matrix of 16-bit numbers
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+// Row of a slice's 16 keys that row i of an operand stands for: neighbouring rows of 144 bytes lie four banks
+// apart, these eight.
+__device__ __forceinline__ int key_row(int i) { return (i & 8) | (i & 3) << 1 | (i >> 2 & 1); }
+
+constexpr int QS_STAGES = 2;
+template <int kN>
+struct QsLayout {
+    static constexpr uint32_t ROWS = 8 * kN;
+    static constexpr uint32_t OFF_SUMS = QS_WARPS * QS_STAGES * SLICE_BYTES;          // [warps][rows][128] fp32
+    static constexpr uint32_t OFF_ML = OFF_SUMS + QS_WARPS * ROWS * 512;              // [warps][rows] float2
+    static constexpr uint32_t OFF_BAR = OFF_ML + QS_WARPS * ROWS * 8;
+    static constexpr uint32_t OFF_SCRATCH = OFF_BAR + QS_WARPS * QS_STAGES * 8;
+    static constexpr uint32_t BYTES = OFF_SCRATCH + 32 * 8;
+};
+
+template <int kN>
+__global__ void __launch_bounds__(QS_THREADS, kN == 1 ? 2 : 1) attn_qcache_kernel(const QcacheAttnParams p, const __grid_constant__ CUtensorMap map) {
+    using L = QsLayout<kN>;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    const uint32_t base = smem_u32(smem_raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = mx_uniform(tid >> 5), g = lane >> 2, t = lane & 3;
+    const int G = p.Hq / p.Hk, rows = L::ROWS;
+    asm volatile("griddepcontrol.launch_dependents;");
+    const uint32_t ring = base + warp * QS_STAGES * SLICE_BYTES, bars = base + L::OFF_BAR + warp * QS_STAGES * 8;
+    if (lane == 0) {
+        for (int i = 0; i < QS_STAGES; ++i) mbar_init(bars + 8 * i, 1);
+        mbar_fence_init();
+        tma_prefetch_desc(&map);
+    }
+    __syncwarp();
+    await_stream();
+    const QsShare share = qs_find_share(p, G, rows, reinterpret_cast<int64_t*>(smem_raw + L::OFF_SCRATCH));
+    QsPartials part = qs_partials(p.workspace);
+    QsCursor u = share.at;
+    if (tid == 0) {
+        QsCut c{};
+        if (share.weight > 0) c = QsCut{u.j, 1, u.n, u.kh, u.tile, u.s.q0, u.s.lq, 0};
+        c.status = share.bad ? KDA_DEVERR_CU_SEQLENS : 0u;
+        part.cut[blockIdx.x] = c;
+    }
+    // the warp's slices of the share, in order: loads run QS_STAGES ahead
+    QsCursor lu = u;                     // the loads' cursor, piece and slice
+    int64_t lleft = share.weight;
+    QsPiece lr{};
+    int lj = 0, loaded = 0;
+    if (lleft > 0) lr = qs_piece(lu, lleft), lj = lr.j0 + warp;
+    auto load_next = [&]() {             // (one slice, if there is one left)
+        while (lleft > 0 && lj >= lr.j1) {
+            lleft -= lr.weight;
+            if (lleft <= 0) break;
+            qs_next_tile(p, G, rows, lu);
+            lr = qs_piece(lu, lleft);
+            lj = lr.j0 + warp;
+        }
+        if (lleft <= 0) return;
+        if (lane == 0) {
+            const int stage = loaded % QS_STAGES;
+            mbar_arrive_expect_tx(bars + 8 * stage, SLICE_BYTES);
+            tma_load_4d(ring + stage * SLICE_BYTES, &map, 0, lu.kh, lj * SLICE, lu.n, bars + 8 * stage);
+        }
+        ++loaded;
+        lj += QS_WARPS;
+    };
+#pragma unroll 1
+    for (int i = 0; i < QS_STAGES; ++i) load_next();
+
+    const float c = p.scale * LOG2E;
+    int used = 0;
+    bool ok = true, first_piece = true;
+#pragma unroll 1
+    for (int64_t left = share.weight; left > 0; qs_next_tile(p, G, rows, u), first_piece = false) {
+        const QsPiece r = qs_piece(u, left);
+        left -= r.weight;
+        // ---- the tile's queries: lane (g, t) holds channels 16 t .. 16 t + 15 of both halves of row g, as pairs
+        // (e, e + 4) of each eight, the order in which the codes come
+        uint32_t q[kN][8][2];
+        float qs[kN][2][2];              // sums over each half's channels, of rows 2 t and 2 t + 1
+        // the tile's first row is (token, head) (tok0, head0); row i is head (head0 + i) % G of (head0 + i) / G tokens on
+        const int64_t total = (int64_t)u.s.lq * G, row0 = (int64_t)u.tile * rows;
+        const int tok0 = (int)(row0 / G);
+        const uint32_t head0 = (uint32_t)(row0 - (int64_t)tok0 * G);
+        const int have = (int)min((int64_t)rows, total - row0);   // rows that are there
+#pragma unroll
+        for (int b = 0; b < kN; ++b) {
+            const uint32_t on = (head0 + 8 * b + g) / (uint32_t)G, head = head0 + 8 * b + g - on * G;
+            const __nv_bfloat16* src = p.q.data + ((int64_t)u.s.q0 + tok0 + on) * p.q.row + ((int64_t)u.kh * G + head) * p.q.head + 16 * t;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+                if (8 * b + g < have) {
+                    x[0] = *reinterpret_cast<const uint4*>(src + 64 * h);
+                    x[1] = *reinterpret_cast<const uint4*>(src + 64 * h + 8);
+                }
+                float sum = 0.f;
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    sum += (bf16_lo(x[w].x) + bf16_hi(x[w].x)) + (bf16_lo(x[w].y) + bf16_hi(x[w].y)) +
+                           ((bf16_lo(x[w].z) + bf16_hi(x[w].z)) + (bf16_lo(x[w].w) + bf16_hi(x[w].w)));
+                    q[b][4 * h + 2 * w][0] = __byte_perm(x[w].x, x[w].z, 0x5410);       // channels 0, 4
+                    q[b][4 * h + 2 * w][1] = __byte_perm(x[w].x, x[w].z, 0x7632);       // 1, 5
+                    q[b][4 * h + 2 * w + 1][0] = __byte_perm(x[w].y, x[w].w, 0x5410);   // 2, 6
+                    q[b][4 * h + 2 * w + 1][1] = __byte_perm(x[w].y, x[w].w, 0x7632);   // 3, 7
+                }
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                qs[b][h][0] = __shfl_sync(0xffffffffu, sum, 8 * t);
+                qs[b][h][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+            }
+        }
+        // the last key that rows 2 t and 2 t + 1 see, and that the tile's first row sees
+        int last[kN][2];
+#pragma unroll
+        for (int b = 0; b < kN; ++b)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) last[b][i] = min(tok0 + (int)((head0 + 8 * b + 2 * t + i) / (uint32_t)G), u.s.lq - 1) + u.s.lk - u.s.lq;
+        const int all_see = tok0 + u.s.lk - u.s.lq;
+
+        float o[kN][2][4][4];            // [half][tile of channels]: channels 8 g + i and 8 g + 4 + i of the half, rows 2 t and 2 t + 1
+        float ones[kN][2][4], z[kN][2][2], m[kN][2], l[kN][2];
+#pragma unroll
+        for (int b = 0; b < kN; ++b)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                m[b][i] = -INFINITY;
+                l[b][i] = 0.f;
+                z[b][0][i] = z[b][1][i] = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    ones[b][i][e] = 0.f;
+#pragma unroll
+                    for (int f = 0; f < 4; ++f) o[b][i][f][e] = 0.f;
+                }
+            }
+#pragma unroll 1
+        for (int j = r.j0 + warp; j < r.j1; j += QS_WARPS) {
+            const int stage = used % QS_STAGES;
+            if (ok) ok = mx_wait(bars + 8 * stage, (used / QS_STAGES) & 1);
+            const uint32_t at = ring + stage * SLICE_BYTES;
+            float s[kN][2][4];
+            uint4 num[2][2];             // the numbers of rows g and g + 8 of each 16 keys
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+                uint2 w[2][2];           // [row g, g + 8][half]
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t row = at + (16 * a + key_row(g + 8 * i)) * QC_ROW;
+                    num[a][i] = lds_u128(row + QC_NUMBERS);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];\n" : "=r"(w[i][h].x), "=r"(w[i][h].y) : "r"(row + 32 * h + 8 * t));
+                }
+                float acc[kN][2][4];
+#pragma unroll
+                for (int b = 0; b < kN; ++b)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[b][h][e] = 0.f;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int v = 0; v < 2; ++v) {
+                        const uint32_t x0 = v ? w[0][h].y : w[0][h].x, x1 = v ? w[1][h].y : w[1][h].x;
+                        const uint32_t ya[4] = {codes2<0>(x0), codes2<0>(x1), codes2<1>(x0), codes2<1>(x1)};
+                        const uint32_t yb[4] = {codes2<2>(x0), codes2<2>(x1), codes2<3>(x0), codes2<3>(x1)};
+#pragma unroll
+                        for (int b = 0; b < kN; ++b) {
+                            mma_bf16_16816(acc[b][h], ya, q[b][4 * h + 2 * v][0], q[b][4 * h + 2 * v][1]);
+                            mma_bf16_16816(acc[b][h], yb, q[b][4 * h + 2 * v + 1][0], q[b][4 * h + 2 * v + 1][1]);
+                        }
+                    }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float s0 = 16.f * c * bf16_lo(num[a][i].x), s1 = 16.f * c * bf16_lo(num[a][i].y);
+                    const float z0 = fmaf(c, bf16_hi(num[a][i].x), -s0), z1 = fmaf(c, bf16_hi(num[a][i].y), -s1);
+#pragma unroll
+                    for (int b = 0; b < kN; ++b)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            s[b][a][2 * i + e] = fmaf(s0, acc[b][0][2 * i + e], s1 * acc[b][1][2 * i + e]) + fmaf(z0, qs[b][0][e], z1 * qs[b][1][e]);
+                }
+            }
+            if (SLICE * j + SLICE - 1 > all_see) {
+#pragma unroll
+                for (int a = 0; a < 2; ++a)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int key = SLICE * j + 16 * a + key_row(g + 8 * i);
+#pragma unroll
+                        for (int b = 0; b < kN; ++b)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                if (key > last[b][e]) s[b][a][2 * i + e] = -INFINITY;
+                        if (key >= u.s.lk) num[a][i].z = num[a][i].w = 0u;   // whatever such a row holds
+                    }
+            }
+            // ---- the maximum, when a score has passed it by far
+            bool grown = false;
+            float top[kN][2];
+#pragma unroll
+            for (int b = 0; b < kN; ++b)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    top[b][e] = fmaxf(fmaxf(s[b][0][e], s[b][0][2 + e]), fmaxf(s[b][1][e], s[b][1][2 + e]));
+                    grown |= top[b][e] - m[b][e] > 8.f;   // (m = -inf: whenever a key is seen)
+                }
+            if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+                for (int b = 0; b < kN; ++b)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float x = top[b][e];
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+                        x = fmaxf(x, m[b][e]);
+                        const float f = m[b][e] == -INFINITY ? 0.f : ex2_approx(m[b][e] - x);
+                        m[b][e] = x;
+                        l[b][e] *= f;
+                        z[b][0][e] *= f;
+                        z[b][1][e] *= f;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            ones[b][h][e] *= f;
+                            ones[b][h][2 + e] *= f;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                o[b][h][i][e] *= f;
+                                o[b][h][i][2 + e] *= f;
+                            }
+                        }
+                    }
+            }
+            // ---- weights, and the values
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+                uint32_t rw[kN][2][2];       // [half][keys 0-7, 8-15]: weights times scale, transposed
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float s0 = bf16_lo(num[a][i].z), s1 = bf16_lo(num[a][i].w);
+                    const float m0 = fmaf(7.5f, s0, bf16_hi(num[a][i].z)), m1 = fmaf(7.5f, s1, bf16_hi(num[a][i].w));
+#pragma unroll
+                    for (int b = 0; b < kN; ++b) {
+                        float w[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            w[e] = ex2_approx(s[b][a][2 * i + e] - (m[b][e] == -INFINITY ? 0.f : m[b][e]));
+                            l[b][e] += w[e];
+                            z[b][0][e] = fmaf(w[e], m0, z[b][0][e]);
+                            z[b][1][e] = fmaf(w[e], m1, z[b][1][e]);
+                        }
+                        rw[b][0][i] = transposed(pack_bf16x2(w[0] * s0, w[1] * s0));
+                        rw[b][1][i] = transposed(pack_bf16x2(w[0] * s1, w[1] * s1));
+                    }
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t lo[2], hi[2];   // [keys 2 t and 2 t + 1, and 8 more]: codes 0-3 and 4-7 of the two keys' words
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t x0 = lds_u32(at + (16 * a + key_row(2 * t + 8 * i)) * QC_ROW + 64 + 32 * h + 4 * g);
+                        const uint32_t x1 = lds_u32(at + (16 * a + key_row(2 * t + 1 + 8 * i)) * QC_ROW + 64 + 32 * h + 4 * g);
+                        lo[i] = __byte_perm(x0, x1, 0x5410);
+                        hi[i] = __byte_perm(x0, x1, 0x7632);
+                    }
+                    const uint32_t y0[4] = {codes2<0>(lo[0]), codes2<0>(hi[0]), codes2<0>(lo[1]), codes2<0>(hi[1])};
+                    const uint32_t y1[4] = {codes2<1>(lo[0]), codes2<1>(hi[0]), codes2<1>(lo[1]), codes2<1>(hi[1])};
+                    const uint32_t y2[4] = {codes2<2>(lo[0]), codes2<2>(hi[0]), codes2<2>(lo[1]), codes2<2>(hi[1])};
+                    const uint32_t y3[4] = {codes2<3>(lo[0]), codes2<3>(hi[0]), codes2<3>(lo[1]), codes2<3>(hi[1])};
+                    const uint32_t one[4] = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
+#pragma unroll
+                    for (int b = 0; b < kN; ++b) {
+                        mma_bf16_16816(o[b][h][0], y0, rw[b][h][0], rw[b][h][1]);
+                        mma_bf16_16816(o[b][h][1], y1, rw[b][h][0], rw[b][h][1]);
+                        mma_bf16_16816(o[b][h][2], y2, rw[b][h][0], rw[b][h][1]);
+                        mma_bf16_16816(o[b][h][3], y3, rw[b][h][0], rw[b][h][1]);
+                        mma_bf16_16816(ones[b][h], one, rw[b][h][0], rw[b][h][1]);
+                    }
+                }
+            }
+            __syncwarp();
+            ++used;
+            load_next();
+        }
+        // ---- the warps' results: reference and sum of every row, then the rows themselves
+        float2* ml = reinterpret_cast<float2*>(smem_raw + L::OFF_ML);
+        float* sums = reinterpret_cast<float*>(smem_raw + L::OFF_SUMS);
+#pragma unroll
+        for (int b = 0; b < kN; ++b)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) {
+                    l[b][e] += __shfl_xor_sync(0xffffffffu, l[b][e], d);
+                    z[b][0][e] += __shfl_xor_sync(0xffffffffu, z[b][0][e], d);
+                    z[b][1][e] += __shfl_xor_sync(0xffffffffu, z[b][1][e], d);
+                }
+                if (g == 0) ml[warp * rows + 8 * b + 2 * t + e] = make_float2(m[b][e], l[b][e]);
+            }
+        __syncthreads();
+#pragma unroll
+        for (int b = 0; b < kN; ++b)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int row = 8 * b + 2 * t + e;
+                float top = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < QS_WARPS; ++w) top = fmaxf(top, ml[w * rows + row].x);
+                const float f = m[b][e] == -INFINITY ? 0.f : ex2_approx(m[b][e] - top);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float y[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        y[i] = f * fmaf(16.f, fmaf(-1.46875f, ones[b][h][e], o[b][h][i][e]), z[b][h][e]);
+                        y[4 + i] = f * fmaf(16.f, fmaf(-1.46875f, ones[b][h][e], o[b][h][i][2 + e]), z[b][h][e]);
+                    }
+                    float4* dst = reinterpret_cast<float4*>(sums + (warp * rows + row) * 128 + 64 * h + 8 * g);
+                    dst[0] = make_float4(y[0], y[1], y[2], y[3]);
+                    dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+                }
+            }
+        __syncthreads();
+        const bool whole = r.j0 == 0 && r.j1 == r.nb;
+        const size_t slot = 2 * blockIdx.x + (first_piece ? 0 : 1);
+#pragma unroll
+        for (int b = 0; b < kN; ++b) {   // a warp takes a row, a lane four channels
+            const int row = 8 * b + warp;
+            if (row >= have) continue;
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+            float top = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < QS_WARPS; ++w) {
+                const float4 x = *reinterpret_cast<const float4*>(sums + (w * rows + row) * 128 + 4 * lane);
+                y.x += x.x, y.y += x.y, y.z += x.z, y.w += x.w;
+                top = fmaxf(top, ml[w * rows + row].x);
+            }
+#pragma unroll
+            for (int w = 0; w < QS_WARPS; ++w) {
+                const float2 x = ml[w * rows + row];
+                sum += x.x == -INFINITY ? 0.f : x.y * ex2_approx(x.x - top);
+            }
+            if (!whole) {
+                *reinterpret_cast<float4*>(part.o + (slot * QS_MAX_ROWS + row) * 128 + 4 * lane) = y;
+                if (lane == 0) part.ml[slot * QS_MAX_ROWS + row] = make_float2(top, sum);
+            } else {
+                const uint32_t on = (head0 + row) / (uint32_t)G;
+                const int64_t tok = (int64_t)u.s.q0 + tok0 + on;
+                const int64_t head = (int64_t)u.kh * G + (head0 + row - on * G);
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                *reinterpret_cast<uint2*>(p.out.data + tok * p.out.row + head * p.out.head + 4 * lane) =
+                    make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
+                if (p.lse && lane == 0) p.lse[tok * p.Hq + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+            }
+        }
+    }
+    if (!ok) {
+        mx_wind_down();
+        if (lane == 0) atomicOr(&part.cut[blockIdx.x].status, KDA_DEVERR_TIMEOUT);
+    }
+}
+
+// Joins the partial rows of the tiles that several shares hold (and, the last block, the shares' status bits: one
+// store, so that none is lost).  Block b takes the tile that share b + 1 starts in, if that is the tile's first cut; a
+// warp takes a row, lane l its channels 4 l .. 4 l + 3.
+__global__ void __launch_bounds__(QS_THREADS) attn_qcache_join_kernel(const QcacheAttnParams p, int ctas, int rows) {
+    const int first = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = p.Hq / p.Hk;
+    const QsPartials part = qs_partials(p.workspace);
+    await_stream();
+    if (first == ctas) {
+        if (warp != 0) return;
+        uint32_t status = 0;
+        for (int s = lane; s < ctas; s += 32) status |= part.cut[s].status;
+        status = __reduce_or_sync(0xffffffffu, status);
+        if (lane == 0) *p.status = status;
+        return;
+    }
+    const QsCut c = part.cut[first];
+    if (c.j == 0) return;   // between two tiles, or nothing to do
+    auto inside = [&](const QsCut& a) { return a.n == c.n && a.kh == c.kh && a.tile == c.tile; };
+    int b = first - 1;      // the share before it that is not empty
+    QsCut before = part.cut[b];
+    while (b > 0 && before.some == 0) before = part.cut[--b];
+    const bool same = inside(before);
+    if (same && before.j > 0) return;
+    // the parts: share b's last piece, then the first pieces of the shares that start inside the tile (empty ones between)
+    int end = first + 1;
+    for (;;) {
+        const int s = end + lane;
+        bool past = s >= ctas;
+        if (!past) {
+            const QsCut a = part.cut[s];
+            past = a.some && !(a.j > 0 && inside(a));
+        }
+        const uint32_t at = __ballot_sync(0xffffffffu, past);
+        if (at) {
+            end += __ffs(at) - 1;
+            break;
+        }
+        end += 32;
+    }
+    auto slot = [&](int s) { return (size_t)(2 * s + (s == b && !same ? 1 : 0)); };
+#pragma unroll 1
+    for (int row = warp; row < rows; row += QS_WARPS) {
+        const int64_t at = (int64_t)c.tile * rows + row;
+        if (at >= (int64_t)c.lq * G) return;
+        float m = -INFINITY, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int s0 = b; s0 < end; s0 += 32) {   // (more than 32 parts: the sums so far are rescaled)
+            const int s = s0 + lane;
+            float2 ml = make_float2(-INFINITY, 0.f);
+            if (s < end && (s == b || part.cut[s].some)) ml = part.ml[slot(s) * QS_MAX_ROWS + row];
+            float top = ml.x;
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            top = fmaxf(top, m);
+            const float old = m == -INFINITY ? 0.f : ex2_approx(m - top);
+            m = top;
+            const float w = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);   // (a part that saw no key, or an empty share)
+            l = fmaf(l, old, w * ml.y);
+            o.x *= old, o.y *= old, o.z *= old, o.w *= old;
+            const int n = min(32, end - s0);
+#pragma unroll 1
+            for (int a = 0; a < n; a += 8) {
+                float4 y[8];
+                float f[8];
+#pragma unroll
+                for (int d = 0; d < 8; ++d) {
+                    f[d] = __shfl_sync(0xffffffffu, w, (a + d) & 31);
+                    if (a + d >= n) f[d] = 0.f;
+                    y[d] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (f[d] != 0.f) y[d] = __ldcg(reinterpret_cast<const float4*>(part.o + (slot(s0 + a + d) * QS_MAX_ROWS + row) * 128 + 4 * lane));
+                }
+#pragma unroll
+                for (int d = 0; d < 8; ++d) {
+                    o.x = fmaf(f[d], y[d].x, o.x);
+                    o.y = fmaf(f[d], y[d].y, o.y);
+                    o.z = fmaf(f[d], y[d].z, o.z);
+                    o.w = fmaf(f[d], y[d].w, o.w);
+                }
+            }
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int64_t tok = c.q0 + at / G, head = (int64_t)c.kh * G + at % G;
+        *reinterpret_cast<uint2*>(p.out.data + tok * p.out.row + head * p.out.head + 4 * lane) =
+            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        if (p.lse && lane == 0) p.lse[tok * p.Hq + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    }
+}
+
+// The cache in boxes of 144 bytes x 1 head x `rows` rows.
+bool encode_cache(CUtensorMap* m, const QcacheAttnParams& p, int rows) {
+    MxEncodeFn fn = mx_encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)QC_ROW, (cuuint64_t)p.Hk, (cuuint64_t)(p.S > 0 ? p.S : 1), (cuuint64_t)(p.nseq > 0 ? p.nseq : 1)};
+    const cuuint64_t strides[3] = {(cuuint64_t)p.cache.head, (cuuint64_t)p.cache.row, (cuuint64_t)(p.cache.seq > 0 ? p.cache.seq : QC_ROW)};
+    const cuuint32_t box[4] = {(cuuint32_t)QC_ROW, 1, (cuuint32_t)rows, 1}, estr[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, p.cache.data, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int kN>
+cudaError_t launch(const QcacheAttnParams& p, int sms, cudaStream_t stream) {
+    CUtensorMap map;
+    if (!encode_cache(&map, p, SLICE)) return cudaErrorInvalidValue;
+    const int ctas = min(sms * (kN == 1 ? 2 : 1), QS_MAX_CTAS);
+    cudaError_t e = cudaFuncSetAttribute(attn_qcache_kernel<kN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)QsLayout<kN>::BYTES);
+    if (e == cudaSuccess) e = launch_early(attn_qcache_kernel<kN>, dim3((unsigned)ctas), QS_THREADS, QsLayout<kN>::BYTES, stream, p, map);
+    if (e == cudaSuccess) e = launch_early(attn_qcache_join_kernel, dim3((unsigned)ctas), QS_THREADS, 0, stream, p, ctas, 8 * kN);
+    return e;
 }
 
 }  // namespace
 
-size_t attn_qcache_workspace_bytes(int64_t, int, int, int) { return 0; }
+size_t attn_qcache_workspace_bytes(int64_t, int, int, int) { return QS_CUT_BYTES + QS_ML_BYTES + (size_t)2 * QS_MAX_CTAS * QS_MAX_ROWS * HD * sizeof(float); }
 
 cudaError_t launch_attn_qcache(const QcacheAttnParams& p, cudaStream_t stream) {
-    cudaError_t e = launch_early(qcache_lengths_kernel, dim3(1), 256, 0, stream, p);
-    const int64_t blocks = (p.Tq * p.Hq + 3) / 4;
-    if (e != cudaSuccess || blocks == 0) return e;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    return launch_early(attn_qcache_kernel, dim3((unsigned)blocks), 128, 0, stream, p);
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    if (p.Tq * (p.Hq / p.Hk) <= 8 * (int64_t)p.nseq) return launch<1>(p, sms, stream);
+    return launch<2>(p, sms, stream);
 }
 
 }  // namespace kda

@@ -2,8 +2,12 @@
 against a plain evaluation of its formulas in 64 bits.
 
 Bounds of the attention, per element, with u = 2^-8 the unit roundoff of bf16:
-  few rows     u |o| + u sum_j p_j |v_j|: the output's rounding and the weights', which take the values' scales
-               with them; what the codes stand for is not rounded
+  few rows     u |o| + u sum_j p_j |v_j - w_j|: the output's rounding and the weights', which take the values' scales
+               with them.  w_j = zero_j + 7.5 scale_j is the middle of the value's group: the products are
+               sum_j (p_j scale_j (1 + d_j)) (code_j - 7.5), |d_j| <= u, beside sum_j p_j w_j in fp32, and
+               scale_j (code_j - 7.5) = v_j - w_j; so a weight's rounding moves the output by p_j d_j (v_j - w_j),
+               which may be more than p_j u |v_j| where a value lies near zero and its group's middle does not.
+               What the codes stand for is not rounded
   many rows    (more than 32 (token, head) rows that share a key head, on average) keys and values are rounded to
                bf16 too: u sum_j p_j |v_j| for the values, and a score is off by at most u b_ij, b_ij = scale
                sum_c |q_ic k_jc|, which moves the weight p_j by p_j u (b_ij + sum_k p_k b_ik) to first order.  An
@@ -172,10 +176,11 @@ def test_append_of_nothing():
 
 # ------------------------------------------------------------------ attention
 def ref_attn(q, cache, scale, lens_q, lens_k):
-    """(out, sum_j p_j |v_j|, what rounded keys move, lse, largest sum of |q k|) over the packed queries, in 64 bits."""
+    """(out, sum_j p_j |v_j|, sum_j p_j |v_j - w_j|, what rounded keys move, lse, largest sum of |q k|) over the packed
+    queries, in 64 bits."""
     hq, hk = q.shape[1], cache.shape[2]
     shape = (sum(lens_q), hq, D)
-    out, size, moved = (torch.zeros(shape, dtype=torch.float64, device="cuda") for _ in range(3))
+    out, size, spread, moved = (torch.zeros(shape, dtype=torch.float64, device="cuda") for _ in range(4))
     lse, most = torch.full(shape[:2], -math.inf, dtype=torch.float64, device="cuda"), torch.zeros(shape[:2], dtype=torch.float64, device="cuda")
     a = 0
     for n, (lq, lk) in enumerate(zip(lens_q, lens_k)):
@@ -191,12 +196,19 @@ def ref_attn(q, cache, scale, lens_q, lens_k):
             p = torch.where(torch.isfinite(l)[..., None], (w - l[..., None]).exp(), 0.0)
             out[a:a + lq, g] = torch.einsum("hij,jd->ihd", p, v)
             size[a:a + lq, g] = torch.einsum("hij,jd->ihd", p, v.abs())
+            spread[a:a + lq, g] = torch.einsum("hij,jd->ihd", p, (v - middles(cache[n, :lk, h])).abs())
             moved[a:a + lq, g] = torch.einsum("hij,jd->ihd", p * (b + (p * b).sum(-1, keepdim=True)), v.abs())
             lse[a:a + lq, g] = l.T
             if lk:
                 most[a:a + lq, g] = (b * seen).amax(-1).T
         a += lq
-    return out, size, moved, lse, most
+    return out, size, spread, moved, lse, most
+
+
+def middles(rows):
+    """zero + 7.5 scale of the values' groups, for every channel."""
+    numbers = rows[..., 136:].contiguous().view(torch.bfloat16).double()
+    return (numbers[..., 1::2] + 7.5 * numbers[..., 0::2]).repeat_interleave(D // 2, -1)
 
 
 def filled(g, lens_k, hk, order, room=None):
@@ -209,12 +221,10 @@ def filled(g, lens_k, hk, order, room=None):
 
 
 def check(got, lse, ref, many, total):
-    out, size, moved, rlse, most = ref
+    out, size, spread, moved, rlse, most = ref
     got = got[:total].double()
     assert torch.isfinite(got).all()
-    bound = U * (out.abs() + size) + 2.0 ** -14 * (size + moved) + 1e-30
-    if many:
-        bound += U * (size + moved) * 1.01
+    bound = U * (out.abs() + (2 * size + moved if many else spread)) * 1.01 + 2.0 ** -14 * (size + spread + moved) + 1e-30
     over = (got - out).abs() - bound
     assert over.numel() == 0 or over.max().item() <= 0, f"{over.max().item():.3e} past its bound, {(over > 0).sum().item()} of {over.numel()}"
     if out.norm() > 0 and out.numel() > 4096:
@@ -283,10 +293,10 @@ def test_attention_of_scores_that_matter(lens_q, lens_k, hq, hk):
         if scale <= 1e-6:
             check(out, lse, ref_attn(q, cache, scale, lens_q, lens_k), many_rows(lens_q, hq, hk), T)
         else:       # scores in the hundreds: the weights' relative error is the scores' absolute one
-            ref, size, moved, rlse, most = ref_attn(q, cache, scale, lens_q, lens_k)
+            ref, size, spread, moved, rlse, most = ref_attn(q, cache, scale, lens_q, lens_k)
             unit = 2.0 ** -14 + (U if many_rows(lens_q, hq, hk) else 0)
             err = (unit * most).clamp(max=40.0)[..., None]
-            assert ((out.double() - ref).abs() <= U * (ref.abs() + 2 * size) + 1.01 * (err.exp() - (-err).exp()) * largest(cache, lens_q, lens_k, hq) + 1e-30).all()
+            assert ((out.double() - ref).abs() <= U * (ref.abs() + 2 * size + spread) + 1.01 * (err.exp() - (-err).exp()) * largest(cache, lens_q, lens_k, hq) + 1e-30).all()
 
 
 def largest(cache, lens_q, lens_k, hq):
@@ -420,6 +430,8 @@ def test_a_cache_past_32_bits():
         zeros = lens_k[i] - 40
         l = torch.logsumexp(torch.cat([w, torch.full((8, 1), math.log(zeros) if zeros else -math.inf, device="cuda", dtype=torch.float64)], 1), -1)
         ref = torch.einsum("hj,jhd->hd", (w - l[:, None]).exp(), vv)
-        size = torch.einsum("hj,jhd->hd", (w - l[:, None]).exp(), vv.abs())
-        assert ((out[i].double() - ref).abs() <= U * (ref.abs() + size) + 2.0 ** -13 * size).all()
+        p = (w - l[:, None]).exp()
+        size = torch.einsum("hj,jhd->hd", p, vv.abs())
+        spread = torch.einsum("hj,jhd->hd", p, (vv - middles(want[40 * i:40 * i + 40]).repeat_interleave(4, 1)).abs())
+        assert ((out[i].double() - ref).abs() <= U * (ref.abs() + spread) + 2.0 ** -13 * (size + spread)).all()
         assert ((lse[i].double() - l).abs() <= 2.0 ** -12).all()
