@@ -4,20 +4,27 @@
 //
 // A tile is 8 kN rows of (token, head) pairs that share a key head, a slice 32 keys (4,608 bytes).  A warp takes
 // every eighth slice by bulk copies into its own small ring and waits for no other warp until the tile is done:
-//   A_h = Y_h Q_h^T       (keys x queries) for the two halves h of the channels, Y = 1 + code / 16 in bf16, which
-//                         is the code's bits put into the mantissa of 1: a shift and a mask for two codes
-//   s = sum_h 16 scale_h A_h + (zero_h - 16 scale_h) sum_c q_c     in fp32
+//   A_h = Y_h Q_h^T       (keys x queries) for the two halves h of the channels, Y the codes
+//   s = sum_h scale_h A_h + zero_h sum_c q_c     in fp32
 //   p = exp2(c s - m),  l += p,  R_h = bf16(p scale'_h),  z_h += p (zero'_h + 7.5 scale'_h)   (the values' numbers)
 //   O_h += Y'_h^T R_h,  u_h += 1^T R_h
-//   out_h = (16 (O_h - 1.46875 u_h) + z_h) / l
+//   out_h = (O_h - 7.5 u_h + z_h) / l
 // so that codes count from their middle (7.5): a weight's rounding to bf16 then moves the output by 2^-9 of
 // what the value deviates from its group's middle, and the middle itself is summed in fp32.
+//
+// A code becomes a bf16 operand by a mask alone: in the lowest eight bits (seven of the fraction and one of the
+// exponent, whose first step continues the subnormal numbers) bf16 counts linearly, so four bits there are
+// code 2^-133 or, four places higher, code 2^-129.  The other operands carry the powers of two that bring the
+// products back: q 2^64 against the first and 2^60 against the second, weights 2^60.  (A shift and a mask for
+// two codes, 1 + code / 16, is 8 instead of 5 instructions for eight codes, on the pipe that bounds this kernel;
+// e4m3, where a byte 0 .. 15 is code 2^-9, would be 3, but its mma.sync is no single instruction here: 30 % more in all.)
 // The maximum m that the exponents refer to moves only when a score exceeds it by more than 8 (base 2), so that
 // most slices need no exchange between lanes.
 //
 // All (sequence, key head, tile, slice) steps are one line that is cut into equal shares, two for each SM; a tile
 // that lies in more than one share leaves unnormalised partial rows in the workspace, and a second, small kernel
 // joins them in the order of the keys.
+
 #include "kda_mixer.cuh"
 #include "kda_qcache.cuh"
 
@@ -29,7 +36,11 @@ constexpr int QS_MAX_CTAS = 320;
 constexpr int SLICE = 32;                          // keys
 constexpr uint32_t SLICE_BYTES = SLICE * QC_ROW;
 constexpr int QS_MAX_ROWS = 16;                    // of a tile
-constexpr int PIECE = 6;                           // a tile's own weight, in slices
+constexpr int PIECE = 16;                          // a tile's own weight, in slices
+constexpr float LIFT = 60.f;                       // weights are carried as p 2^60
+constexpr float NO_KEY = -3e38f;                   // (finite, so that a masked -inf less this is -inf)
+constexpr float UNLIFT = 0x1p-60f, CODE = 0x1p73f; // a product of a value's code and a weight, brought back
+constexpr float KEY_CODE = 0x1p-69f;               // a product of a key's code and a query, of 1 and 1
 
 // What a share leaves for the join: the tile that it starts in and how far into it, and its status bits.
 struct QsCut {
@@ -179,20 +190,42 @@ __device__ __forceinline__ QsPiece qs_piece(const QsCursor& u, int64_t left) {
     return r;
 }
 
-// Two codes (bits 0-3 and 16-19 of x, moved there by a shift of 4 e bits) as 1 + code / 16 in bf16.
-template <int e>
-__device__ __forceinline__ uint32_t codes2(uint32_t x) {
-    const uint32_t y = e == 0 ? x << 3 : x >> (4 * e - 3);
-    return (y & 0x00780078u) | 0x3f803f80u;
-}
+// Codes 2 e and 2 e + 1 (e: byte) of both halves of x, as bf16 numbers code 2^-133 and code 2^-129.
+struct Codes {
+    uint32_t y[4];
+    __device__ __forceinline__ explicit Codes(uint32_t x) {
+        const uint32_t z = x >> 8;
+        y[0] = x & 0x000f000fu;
+        y[1] = x & 0x00f000f0u;
+        y[2] = z & 0x000f000fu;
+        y[3] = z & 0x00f000f0u;
+    }
+};
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {   // of an 8 x 8 matrix of 16-bit numbers
     uint32_t y;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
 // Row of a slice's 16 keys that row i of an operand stands for: neighbouring rows of 144 bytes lie four banks
-// apart, these eight.
+// apart, these eight.  key_row(i + 8) = key_row(i) + 8, key_row(2 i + 1) = key_row(2 i) + 2.
 __device__ __forceinline__ int key_row(int i) { return (i & 8) | (i & 3) << 1 | (i >> 2 & 1); }
+
+// D = A B + C; without `volatile`, so that the compiler may order them (a C of zeros costs no registers).
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0, float c1, float c2, float c3) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};\n"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    mma_bf16(d, a, b0, b1, d[0], d[1], d[2], d[3]);
+}
+// Both numbers of a pair times 2^n.
+template <int n>
+__device__ __forceinline__ uint32_t lifted(uint32_t x) {
+    const __nv_bfloat162 f = __float2bfloat162_rn((float)(1ull << n));
+    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), f);
+    return *reinterpret_cast<const uint32_t*>(&y);
+}
 
 constexpr int QS_STAGES = 2;
 template <int kN>
@@ -230,43 +263,39 @@ __global__ void __launch_bounds__(QS_THREADS, kN == 1 ? 2 : 1) attn_qcache_kerne
         c.status = share.bad ? KDA_DEVERR_CU_SEQLENS : 0u;
         part.cut[blockIdx.x] = c;
     }
-    // the warp's slices of the share, in order: loads run QS_STAGES ahead
-    QsCursor lu = u;                     // the loads' cursor, piece and slice
-    int64_t lleft = share.weight;
-    QsPiece lr{};
-    int lj = 0, loaded = 0;
-    if (lleft > 0) lr = qs_piece(lu, lleft), lj = lr.j0 + warp;
-    auto load_next = [&]() {             // (one slice, if there is one left)
-        while (lleft > 0 && lj >= lr.j1) {
-            lleft -= lr.weight;
-            if (lleft <= 0) break;
-            qs_next_tile(p, G, rows, lu);
-            lr = qs_piece(lu, lleft);
-            lj = lr.j0 + warp;
-        }
-        if (lleft <= 0) return;
+    // the warp's slices: loads run QS_STAGES ahead within a piece, and the next piece's first ones are under way while
+    // the warps put this one's results together
+    uint32_t used = 0;
+    auto load = [&](int kh, int n, int j, uint32_t count) {   // slice j, the count-th of this warp
         if (lane == 0) {
-            const int stage = loaded % QS_STAGES;
+            const uint32_t stage = count % QS_STAGES;
             mbar_arrive_expect_tx(bars + 8 * stage, SLICE_BYTES);
-            tma_load_4d(ring + stage * SLICE_BYTES, &map, 0, lu.kh, lj * SLICE, lu.n, bars + 8 * stage);
+            tma_load_4d(ring + stage * SLICE_BYTES, &map, 0, kh, j * SLICE, n, bars + 8 * stage);
         }
-        ++loaded;
-        lj += QS_WARPS;
     };
-#pragma unroll 1
-    for (int i = 0; i < QS_STAGES; ++i) load_next();
+    auto load_first = [&](const QsCursor& v, const QsPiece& r) {
+#pragma unroll
+        for (int i = 0; i < QS_STAGES; ++i)
+            if (r.j0 + warp + i * QS_WARPS < r.j1) load(v.kh, v.n, r.j0 + warp + i * QS_WARPS, used + i);
+    };
+    int64_t left = share.weight;
+    QsPiece r{};
+    if (left > 0) {
+        r = qs_piece(u, left);
+        load_first(u, r);
+    }
 
-    const float c = p.scale * LOG2E;
-    int used = 0;
+    // what turns s into an exponent of base 2 (a scale of 0 must not turn a masked -inf into NaN)
+    const float cq = fmaxf(p.scale * LOG2E, 1e-30f) / KEY_CODE;
+    // this lane's keys and its values' codes in a slice
+    const unsigned char* krow = smem_raw + warp * QS_STAGES * SLICE_BYTES + key_row(g) * QC_ROW;
+    const unsigned char* vrow = smem_raw + warp * QS_STAGES * SLICE_BYTES + key_row(2 * t) * QC_ROW + 64 + 4 * g;
     bool ok = true, first_piece = true;
 #pragma unroll 1
-    for (int64_t left = share.weight; left > 0; qs_next_tile(p, G, rows, u), first_piece = false) {
-        const QsPiece r = qs_piece(u, left);
-        left -= r.weight;
-        // ---- the tile's queries: lane (g, t) holds channels 16 t .. 16 t + 15 of both halves of row g, as pairs
-        // (e, e + 4) of each eight, the order in which the codes come
-        uint32_t q[kN][8][2];
-        float qs[kN][2][2];              // sums over each half's channels, of rows 2 t and 2 t + 1
+    while (left > 0) {
+        // ---- the tile's queries: lane (g, t) holds channels 16 t .. 16 t + 15 of both halves of row g
+        uint32_t q[kN][8][2];            // pairs (e, e + 4) of each eight, the order in which the codes come
+        uint32_t qz[kN];                 // sums over the halves' channels, each as three bf16 terms
         // the tile's first row is (token, head) (tok0, head0); row i is head (head0 + i) % G of (head0 + i) / G tokens on
         const int64_t total = (int64_t)u.s.lq * G, row0 = (int64_t)u.tile * rows;
         const int tok0 = (int)(row0 / G);
@@ -276,6 +305,7 @@ __global__ void __launch_bounds__(QS_THREADS, kN == 1 ? 2 : 1) attn_qcache_kerne
         for (int b = 0; b < kN; ++b) {
             const uint32_t on = (head0 + 8 * b + g) / (uint32_t)G, head = head0 + 8 * b + g - on * G;
             const __nv_bfloat16* src = p.q.data + ((int64_t)u.s.q0 + tok0 + on) * p.q.row + ((int64_t)u.kh * G + head) * p.q.head + 16 * t;
+            float sum[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
@@ -283,37 +313,38 @@ __global__ void __launch_bounds__(QS_THREADS, kN == 1 ? 2 : 1) attn_qcache_kerne
                     x[0] = *reinterpret_cast<const uint4*>(src + 64 * h);
                     x[1] = *reinterpret_cast<const uint4*>(src + 64 * h + 8);
                 }
-                float sum = 0.f;
+                sum[h] = 0.f;
 #pragma unroll
                 for (int w = 0; w < 2; ++w) {
-                    sum += (bf16_lo(x[w].x) + bf16_hi(x[w].x)) + (bf16_lo(x[w].y) + bf16_hi(x[w].y)) +
-                           ((bf16_lo(x[w].z) + bf16_hi(x[w].z)) + (bf16_lo(x[w].w) + bf16_hi(x[w].w)));
-                    q[b][4 * h + 2 * w][0] = __byte_perm(x[w].x, x[w].z, 0x5410);       // channels 0, 4
-                    q[b][4 * h + 2 * w][1] = __byte_perm(x[w].x, x[w].z, 0x7632);       // 1, 5
-                    q[b][4 * h + 2 * w + 1][0] = __byte_perm(x[w].y, x[w].w, 0x5410);   // 2, 6
-                    q[b][4 * h + 2 * w + 1][1] = __byte_perm(x[w].y, x[w].w, 0x7632);   // 3, 7
+                    sum[h] += (bf16_lo(x[w].x) + bf16_hi(x[w].x)) + (bf16_lo(x[w].y) + bf16_hi(x[w].y)) +
+                              ((bf16_lo(x[w].z) + bf16_hi(x[w].z)) + (bf16_lo(x[w].w) + bf16_hi(x[w].w)));
+                    q[b][4 * h + 2 * w][0] = lifted<60>(lifted<4>(__byte_perm(x[w].x, x[w].z, 0x5410)));       // channels 0, 4
+                    q[b][4 * h + 2 * w][1] = lifted<60>(__byte_perm(x[w].x, x[w].z, 0x7632));                  // 1, 5
+                    q[b][4 * h + 2 * w + 1][0] = lifted<60>(lifted<4>(__byte_perm(x[w].y, x[w].w, 0x5410)));   // 2, 6
+                    q[b][4 * h + 2 * w + 1][1] = lifted<60>(__byte_perm(x[w].y, x[w].w, 0x7632));              // 3, 7
                 }
-                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                qs[b][h][0] = __shfl_sync(0xffffffffu, sum, 8 * t);
-                qs[b][h][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+                sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
+                sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
+                sum[h] *= KEY_CODE;
+            }
+            qz[b] = 0;
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {   // lane t takes the terms number t
+                const uint32_t term = pack_bf16x2(sum[0], sum[1]);
+                if (t == i) qz[b] = term;
+                sum[0] -= bf16_lo(term);
+                sum[1] -= bf16_hi(term);
             }
         }
-        // the last key that rows 2 t and 2 t + 1 see, and that the tile's first row sees
-        int last[kN][2];
-#pragma unroll
-        for (int b = 0; b < kN; ++b)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) last[b][i] = min(tok0 + (int)((head0 + 8 * b + 2 * t + i) / (uint32_t)G), u.s.lq - 1) + u.s.lk - u.s.lq;
-        const int all_see = tok0 + u.s.lk - u.s.lq;
+        const int all_see = tok0 + u.s.lk - u.s.lq;   // the last key that the tile's first row sees
 
         float o[kN][2][4][4];            // [half][tile of channels]: channels 8 g + i and 8 g + 4 + i of the half, rows 2 t and 2 t + 1
-        float ones[kN][2][4], z[kN][2][2], m[kN][2], l[kN][2];
+        float ones[kN][2][4], z[kN][2][2], l[kN][2], low[kN][2];   // low: what the exponents refer to, less LIFT
 #pragma unroll
         for (int b = 0; b < kN; ++b)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                m[b][i] = -INFINITY;
+                low[b][i] = NO_KEY;
                 l[b][i] = 0.f;
                 z[b][0][i] = z[b][1][i] = 0.f;
 #pragma unroll
@@ -325,64 +356,70 @@ __global__ void __launch_bounds__(QS_THREADS, kN == 1 ? 2 : 1) attn_qcache_kerne
             }
 #pragma unroll 1
         for (int j = r.j0 + warp; j < r.j1; j += QS_WARPS) {
-            const int stage = used % QS_STAGES;
+            const uint32_t stage = used % QS_STAGES;
             if (ok) ok = mx_wait(bars + 8 * stage, (used / QS_STAGES) & 1);
-            const uint32_t at = ring + stage * SLICE_BYTES;
+            const unsigned char* kat = krow + stage * SLICE_BYTES;
+            const unsigned char* vat = vrow + stage * SLICE_BYTES;
             float s[kN][2][4];
-            uint4 num[2][2];             // the numbers of rows g and g + 8 of each 16 keys
+            uint2 num[2][2];             // the values' numbers of rows g and g + 8 of each 16 keys
 #pragma unroll
             for (int a = 0; a < 2; ++a) {
                 uint2 w[2][2];           // [row g, g + 8][half]
+                uint2 n[2];              // their scales and zeros
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const uint32_t row = at + (16 * a + key_row(g + 8 * i)) * QC_ROW;
-                    num[a][i] = lds_u128(row + QC_NUMBERS);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];\n" : "=r"(w[i][h].x), "=r"(w[i][h].y) : "r"(row + 32 * h + 8 * t));
+                    const unsigned char* row = kat + (16 * a + 8 * i) * QC_ROW;
+                    const uint4 x = *reinterpret_cast<const uint4*>(row + QC_NUMBERS);
+                    n[i] = make_uint2(x.x, x.y);
+                    num[a][i] = make_uint2(x.z, x.w);
+                    w[i][0] = *reinterpret_cast<const uint2*>(row + 8 * t);
+                    w[i][1] = *reinterpret_cast<const uint2*>(row + 8 * t + 32);
                 }
-                float acc[kN][2][4];
-#pragma unroll
-                for (int b = 0; b < kN; ++b)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[b][h][e] = 0.f;
+                float acc[kN][2][4], zero[kN][4];
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int v = 0; v < 2; ++v) {
                         const uint32_t x0 = v ? w[0][h].y : w[0][h].x, x1 = v ? w[1][h].y : w[1][h].x;
-                        const uint32_t ya[4] = {codes2<0>(x0), codes2<0>(x1), codes2<1>(x0), codes2<1>(x1)};
-                        const uint32_t yb[4] = {codes2<2>(x0), codes2<2>(x1), codes2<3>(x0), codes2<3>(x1)};
+                        const Codes c0(x0), c1(x1);
+                        const uint32_t ya[4] = {c0.y[0], c1.y[0], c0.y[1], c1.y[1]}, yb[4] = {c0.y[2], c1.y[2], c0.y[3], c1.y[3]};
 #pragma unroll
                         for (int b = 0; b < kN; ++b) {
-                            mma_bf16_16816(acc[b][h], ya, q[b][4 * h + 2 * v][0], q[b][4 * h + 2 * v][1]);
-                            mma_bf16_16816(acc[b][h], yb, q[b][4 * h + 2 * v + 1][0], q[b][4 * h + 2 * v + 1][1]);
+                            if (v == 0) mma_bf16(acc[b][h], ya, q[b][4 * h][0], q[b][4 * h][1], 0.f, 0.f, 0.f, 0.f);
+                            else mma_bf16(acc[b][h], ya, q[b][4 * h + 2][0], q[b][4 * h + 2][1]);
+                            mma_bf16(acc[b][h], yb, q[b][4 * h + 2 * v + 1][0], q[b][4 * h + 2 * v + 1][1]);
                         }
                     }
+                // the zeros of row g and g + 8, for each of the three terms of the channels' sums
+                const uint32_t z[4] = {__byte_perm(n[0].x, n[0].y, 0x7632), __byte_perm(n[1].x, n[1].y, 0x7632), 0u, 0u};
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float s0 = 16.f * c * bf16_lo(num[a][i].x), s1 = 16.f * c * bf16_lo(num[a][i].y);
-                    const float z0 = fmaf(c, bf16_hi(num[a][i].x), -s0), z1 = fmaf(c, bf16_hi(num[a][i].y), -s1);
+                for (int b = 0; b < kN; ++b) {
+                    mma_bf16(zero[b], z, qz[b], 0u, 0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                    for (int b = 0; b < kN; ++b)
+                    for (int i = 0; i < 2; ++i)
 #pragma unroll
                         for (int e = 0; e < 2; ++e)
-                            s[b][a][2 * i + e] = fmaf(s0, acc[b][0][2 * i + e], s1 * acc[b][1][2 * i + e]) + fmaf(z0, qs[b][0][e], z1 * qs[b][1][e]);
+                            s[b][a][2 * i + e] = fmaf(bf16_lo(n[i].x), acc[b][0][2 * i + e], fmaf(bf16_lo(n[i].y), acc[b][1][2 * i + e], zero[b][2 * i + e]));
                 }
             }
             if (SLICE * j + SLICE - 1 > all_see) {
+#pragma unroll
+                for (int b = 0; b < kN; ++b)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int last = min(tok0 + (int)((head0 + 8 * b + 2 * t + e) / (uint32_t)G), u.s.lq - 1) + u.s.lk - u.s.lq;
+#pragma unroll
+                        for (int a = 0; a < 2; ++a)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                if (SLICE * j + 16 * a + key_row(g + 8 * i) > last) s[b][a][2 * i + e] = -INFINITY;
+                    }
 #pragma unroll
                 for (int a = 0; a < 2; ++a)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int key = SLICE * j + 16 * a + key_row(g + 8 * i);
-#pragma unroll
-                        for (int b = 0; b < kN; ++b)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e)
-                                if (key > last[b][e]) s[b][a][2 * i + e] = -INFINITY;
-                        if (key >= u.s.lk) num[a][i].z = num[a][i].w = 0u;   // whatever such a row holds
+                        if (key >= u.s.lk) num[a][i] = make_uint2(0u, 0u);   // whatever such a row holds
                     }
             }
             // ---- the maximum, when a score has passed it by far
@@ -392,8 +429,8 @@ __global__ void __launch_bounds__(QS_THREADS, kN == 1 ? 2 : 1) attn_qcache_kerne
             for (int b = 0; b < kN; ++b)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    top[b][e] = fmaxf(fmaxf(s[b][0][e], s[b][0][2 + e]), fmaxf(s[b][1][e], s[b][1][2 + e]));
-                    grown |= top[b][e] - m[b][e] > 8.f;   // (m = -inf: whenever a key is seen)
+                    top[b][e] = cq * fmaxf(fmaxf(s[b][0][e], s[b][0][2 + e]), fmaxf(s[b][1][e], s[b][1][2 + e]));
+                    grown |= top[b][e] - low[b][e] > LIFT + 8.f;
                 }
             if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
@@ -403,9 +440,9 @@ __global__ void __launch_bounds__(QS_THREADS, kN == 1 ? 2 : 1) attn_qcache_kerne
                         float x = top[b][e];
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-                        x = fmaxf(x, m[b][e]);
-                        const float f = m[b][e] == -INFINITY ? 0.f : ex2_approx(m[b][e] - x);
-                        m[b][e] = x;
+                        x = fmaxf(x - LIFT, low[b][e]);
+                        const float f = ex2_approx(low[b][e] - x);
+                        low[b][e] = x;
                         l[b][e] *= f;
                         z[b][0][e] *= f;
                         z[b][1][e] *= f;
@@ -424,17 +461,24 @@ __global__ void __launch_bounds__(QS_THREADS, kN == 1 ? 2 : 1) attn_qcache_kerne
             // ---- weights, and the values
 #pragma unroll
             for (int a = 0; a < 2; ++a) {
+                uint32_t x[2][2][2];         // the words of keys 2 t and 2 t + 1 and of eight keys on: [half][i][key]
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) x[h][i][k] = *reinterpret_cast<const uint32_t*>(vat + (16 * a + 8 * i + 2 * k) * QC_ROW + 32 * h);
                 uint32_t rw[kN][2][2];       // [half][keys 0-7, 8-15]: weights times scale, transposed
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const float s0 = bf16_lo(num[a][i].z), s1 = bf16_lo(num[a][i].w);
-                    const float m0 = fmaf(7.5f, s0, bf16_hi(num[a][i].z)), m1 = fmaf(7.5f, s1, bf16_hi(num[a][i].w));
+                    const float s0 = bf16_lo(num[a][i].x), s1 = bf16_lo(num[a][i].y);
+                    const float m0 = fmaf(7.5f, s0, bf16_hi(num[a][i].x)), m1 = fmaf(7.5f, s1, bf16_hi(num[a][i].y));
 #pragma unroll
                     for (int b = 0; b < kN; ++b) {
                         float w[2];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            w[e] = ex2_approx(s[b][a][2 * i + e] - (m[b][e] == -INFINITY ? 0.f : m[b][e]));
+                            w[e] = ex2_approx(fmaf(cq, s[b][a][2 * i + e], -low[b][e]));
                             l[b][e] += w[e];
                             z[b][0][e] = fmaf(w[e], m0, z[b][0][e]);
                             z[b][1][e] = fmaf(w[e], m1, z[b][1][e]);
@@ -445,32 +489,33 @@ __global__ void __launch_bounds__(QS_THREADS, kN == 1 ? 2 : 1) attn_qcache_kerne
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    uint32_t lo[2], hi[2];   // [keys 2 t and 2 t + 1, and 8 more]: codes 0-3 and 4-7 of the two keys' words
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t x0 = lds_u32(at + (16 * a + key_row(2 * t + 8 * i)) * QC_ROW + 64 + 32 * h + 4 * g);
-                        const uint32_t x1 = lds_u32(at + (16 * a + key_row(2 * t + 1 + 8 * i)) * QC_ROW + 64 + 32 * h + 4 * g);
-                        lo[i] = __byte_perm(x0, x1, 0x5410);
-                        hi[i] = __byte_perm(x0, x1, 0x7632);
-                    }
-                    const uint32_t y0[4] = {codes2<0>(lo[0]), codes2<0>(hi[0]), codes2<0>(lo[1]), codes2<0>(hi[1])};
-                    const uint32_t y1[4] = {codes2<1>(lo[0]), codes2<1>(hi[0]), codes2<1>(lo[1]), codes2<1>(hi[1])};
-                    const uint32_t y2[4] = {codes2<2>(lo[0]), codes2<2>(hi[0]), codes2<2>(lo[1]), codes2<2>(hi[1])};
-                    const uint32_t y3[4] = {codes2<3>(lo[0]), codes2<3>(hi[0]), codes2<3>(lo[1]), codes2<3>(hi[1])};
+                    // codes 0-3 and 4-7 of the two keys' words
+                    const Codes l0(__byte_perm(x[h][0][0], x[h][0][1], 0x5410)), h0(__byte_perm(x[h][0][0], x[h][0][1], 0x7632));
+                    const Codes l1(__byte_perm(x[h][1][0], x[h][1][1], 0x5410)), h1(__byte_perm(x[h][1][0], x[h][1][1], 0x7632));
                     const uint32_t one[4] = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
 #pragma unroll
                     for (int b = 0; b < kN; ++b) {
-                        mma_bf16_16816(o[b][h][0], y0, rw[b][h][0], rw[b][h][1]);
-                        mma_bf16_16816(o[b][h][1], y1, rw[b][h][0], rw[b][h][1]);
-                        mma_bf16_16816(o[b][h][2], y2, rw[b][h][0], rw[b][h][1]);
-                        mma_bf16_16816(o[b][h][3], y3, rw[b][h][0], rw[b][h][1]);
-                        mma_bf16_16816(ones[b][h], one, rw[b][h][0], rw[b][h][1]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t y[4] = {l0.y[i], h0.y[i], l1.y[i], h1.y[i]};
+                            mma_bf16(o[b][h][i], y, rw[b][h][0], rw[b][h][1]);
+                        }
+                        mma_bf16(ones[b][h], one, rw[b][h][0], rw[b][h][1]);
                     }
                 }
             }
             __syncwarp();
+            if (j + QS_STAGES * QS_WARPS < r.j1) load(u.kh, u.n, j + QS_STAGES * QS_WARPS, used + QS_STAGES);
             ++used;
-            load_next();
+        }
+        // ---- on to the next piece, whose loads start here
+        const bool whole = r.j0 == 0 && r.j1 == r.nb;
+        const int q0 = u.s.q0, kh = u.kh;
+        left -= r.weight;
+        if (left > 0) {
+            qs_next_tile(p, G, rows, u);
+            r = qs_piece(u, left);
+            load_first(u, r);
         }
         // ---- the warps' results: reference and sum of every row, then the rows themselves
         float2* ml = reinterpret_cast<float2*>(smem_raw + L::OFF_ML);
@@ -485,7 +530,7 @@ __global__ void __launch_bounds__(QS_THREADS, kN == 1 ? 2 : 1) attn_qcache_kerne
                     z[b][0][e] += __shfl_xor_sync(0xffffffffu, z[b][0][e], d);
                     z[b][1][e] += __shfl_xor_sync(0xffffffffu, z[b][1][e], d);
                 }
-                if (g == 0) ml[warp * rows + 8 * b + 2 * t + e] = make_float2(m[b][e], l[b][e]);
+                if (g == 0) ml[warp * rows + 8 * b + 2 * t + e] = make_float2(l[b][e] == 0.f ? -INFINITY : low[b][e] + LIFT, UNLIFT * l[b][e]);
             }
         __syncthreads();
 #pragma unroll
@@ -496,14 +541,15 @@ __global__ void __launch_bounds__(QS_THREADS, kN == 1 ? 2 : 1) attn_qcache_kerne
                 float top = -INFINITY;
 #pragma unroll
                 for (int w = 0; w < QS_WARPS; ++w) top = fmaxf(top, ml[w * rows + row].x);
-                const float f = m[b][e] == -INFINITY ? 0.f : ex2_approx(m[b][e] - top);
+                const float f = l[b][e] == 0.f ? 0.f : ex2_approx(low[b][e] + LIFT - top);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float y[8];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        y[i] = f * fmaf(16.f, fmaf(-1.46875f, ones[b][h][e], o[b][h][i][e]), z[b][h][e]);
-                        y[4 + i] = f * fmaf(16.f, fmaf(-1.46875f, ones[b][h][e], o[b][h][i][2 + e]), z[b][h][e]);
+                    for (int i = 0; i < 4; ++i) {   // (codes 1 and 3 were four places higher)
+                        const float back = i & 1 ? CODE / 16.f : CODE, rest = UNLIFT * fmaf(-7.5f, ones[b][h][e], z[b][h][e]);
+                        y[i] = f * fmaf(back, o[b][h][i][e], rest);
+                        y[4 + i] = f * fmaf(back, o[b][h][i][2 + e], rest);
                     }
                     float4* dst = reinterpret_cast<float4*>(sums + (warp * rows + row) * 128 + 64 * h + 8 * g);
                     dst[0] = make_float4(y[0], y[1], y[2], y[3]);
@@ -511,7 +557,6 @@ __global__ void __launch_bounds__(QS_THREADS, kN == 1 ? 2 : 1) attn_qcache_kerne
                 }
             }
         __syncthreads();
-        const bool whole = r.j0 == 0 && r.j1 == r.nb;
         const size_t slot = 2 * blockIdx.x + (first_piece ? 0 : 1);
 #pragma unroll
         for (int b = 0; b < kN; ++b) {   // a warp takes a row, a lane four channels
@@ -535,14 +580,14 @@ __global__ void __launch_bounds__(QS_THREADS, kN == 1 ? 2 : 1) attn_qcache_kerne
                 if (lane == 0) part.ml[slot * QS_MAX_ROWS + row] = make_float2(top, sum);
             } else {
                 const uint32_t on = (head0 + row) / (uint32_t)G;
-                const int64_t tok = (int64_t)u.s.q0 + tok0 + on;
-                const int64_t head = (int64_t)u.kh * G + (head0 + row - on * G);
+                const int64_t tok = (int64_t)q0 + tok0 + on, head = (int64_t)kh * G + (head0 + row - on * G);
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
                 *reinterpret_cast<uint2*>(p.out.data + tok * p.out.row + head * p.out.head + 4 * lane) =
                     make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
                 if (p.lse && lane == 0) p.lse[tok * p.Hq + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
             }
         }
+        first_piece = false;
     }
     if (!ok) {
         mx_wind_down();
