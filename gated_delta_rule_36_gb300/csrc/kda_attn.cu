@@ -44,12 +44,14 @@
 // 704 against 696 us.  Two threads a row, each with half of the keys: 784 against 677 us; an
 // exponential with its scaling, sum and packing takes 7.3 cycles from one warp of a scheduler and 5.5 from
 // two, so that halves gain less than exchanging their maxima costs.
+#include <string.h>
+
 #include "kda_mixer.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int AT_THREADS = 384;
+constexpr int AT_THREADS = 384, AT_CODES_THREADS = 512;   // (four more warps where the cache holds codes)
 constexpr int AT_MAX_CTAS = 160;
 constexpr int KB = 128;                       // keys a block
 constexpr uint32_t TILE = 128 * 256, HALF = TILE / 2;
@@ -186,9 +188,10 @@ struct Share {
     Cursor at;          // where it starts
     bool bad;           // lengths that contradict the tensors
 };
+template <int kThreads>
 __device__ Share find_share(const AttnParams& p, int tq, int G, uint64_t recip, int64_t* scratch /* 48 */) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tp = 2 * tq;
-    const int per = (p.nseq + AT_THREADS - 1) / AT_THREADS;
+    const int per = (p.nseq + kThreads - 1) / kThreads;
     const int n0 = min(tid * per, p.nseq), n1 = min(n0 + per, p.nseq);
     Seq s{};
     int64_t mine = 0, each = 0;
@@ -220,7 +223,7 @@ __device__ Share find_share(const AttnParams& p, int tq, int G, uint64_t recip, 
     if (r.bad) return r;
     int64_t total = 0, before = sum - mine;
 #pragma unroll
-    for (int w = 0; w < AT_THREADS / 32; ++w) {
+    for (int w = 0; w < kThreads / 32; ++w) {
         before += w < warp ? scratch[w] : 0;
         total += scratch[w];
     }
@@ -244,7 +247,7 @@ __device__ Share find_share(const AttnParams& p, int tq, int G, uint64_t recip, 
     __syncthreads();
     // half of the threads for each end: the key head and the step within it; then the last pair that
     // starts at or before that step, of which every thread tries some
-    const int e = tid >= AT_THREADS / 2;
+    const int e = tid >= kThreads / 2;
     const bool open = e && x1 >= total;   // the last share's end needs no search
     const Found f = found[open ? 0 : e];
     Cursor u;
@@ -259,7 +262,7 @@ __device__ Share find_share(const AttnParams& p, int tq, int G, uint64_t recip, 
     int lo = 0, width = m;
 #pragma unroll 1
     while (__syncthreads_or(width > 1)) {   // narrow [lo, lo + width)
-        const int step = (width + AT_THREADS / 2 - 1) / (AT_THREADS / 2), c = lo + (tid % (AT_THREADS / 2)) * step;
+        const int step = (width + kThreads / 2 - 1) / (kThreads / 2), c = lo + (tid % (kThreads / 2)) * step;
         const int64_t st = width > 1 && c < lo + width ? weight_in_turn(u.s.lq, u.s.lk, c, tp, m, f.each) : at + 1;
         if (st <= at) atomicMax(best + e, c);
         __syncthreads();
@@ -298,7 +301,7 @@ __device__ Share find_share(const AttnParams& p, int tq, int G, uint64_t recip, 
     __syncthreads();
     Cursor* place = reinterpret_cast<Cursor*>(scratch + 20);
     if (tid == 0) *place = u, start[0] = x;
-    if (tid == AT_THREADS / 2) start[1] = x;
+    if (tid == kThreads / 2) start[1] = x;
     __syncthreads();
     r.at = *place;
     r.weight = start[1] - start[0];
@@ -351,6 +354,7 @@ __device__ __forceinline__ void next_pair(const AttnParams& p, const Ctx& x, Cur
 }
 
 // ---------------------------------------------------------------- warp 8: loads
+template <bool kCodes>
 __device__ bool load_warp(const AttnParams& p, const AttnMaps& maps, const Ctx& x, Cursor u) {
     bool ok = true;
     if ((threadIdx.x & 31) == 0) {
@@ -373,8 +377,8 @@ __device__ bool load_warp(const AttnParams& p, const AttnMaps& maps, const Ctx& 
             const Piece r = piece_at(x, u, left);
             left -= r.weight;
             const int n = p.cache ? u.n : 0;
-            for (int j = r.j0; j < r.j1 && ok; ++j) {
-                ok = tile(&maps.k, u.kh, u.s.k0 + j * KB, n) && tile(&maps.v, u.kh, u.s.k0 + j * KB, n);
+            for (int j = r.j0; j < (kCodes ? r.j0 + 1 : r.j1) && ok; ++j) {   // (codes are warps 12-15's)
+                if (!kCodes) ok = tile(&maps.k, u.kh, u.s.k0 + j * KB, n) && tile(&maps.v, u.kh, u.s.k0 + j * KB, n);
                 if (j > r.j0 || !ok) continue;
                 // the queries, once the last scores of the piece before are done
                 if (pieces > 0) ok = mx_wait_lane(x.bar(QE), (pieces - 1) & 1u);
@@ -392,6 +396,89 @@ __device__ bool load_warp(const AttnParams& p, const AttnMaps& maps, const Ctx& 
     return __all_sync(0xffffffffu, ok);
 }
 
+// ---------------------------------------------------------------- warps 12-15: keys and values from codes
+// A cache in 4 bits: the tiles of the ring are written here, in the layout that the bulk loads would give them.  Lane
+// l of warp w takes rows 32 w + 8 i + l % 8, i < 4, and of their codes 16 bytes, channels 32 (l / 8) on: eight lanes
+// that store together then store to different banks.  Keys and values are rounded to bf16, code scale + zero in one
+// rounding.  The rows of the next tile are loaded as this one's are written; rows past the sequence's keys are zeros,
+// whatever the cache holds there.
+constexpr int CODES_NUMBERS = 128;   // where a row's scales and zeros are
+
+// Two codes, bytes `sel` of x and x >> 4, times scale plus zero.
+template <uint32_t sel>
+__device__ __forceinline__ uint32_t expand2(uint32_t x, uint32_t x4, __nv_bfloat162 scale, __nv_bfloat162 zero) {
+    const uint32_t y = (__byte_perm(x, x4, sel) & 0x000f000fu) | 0x43004300u;   // 128 + code
+    const __nv_bfloat162 n = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&y), __float2bfloat162_rn(128.f));
+    const __nv_bfloat162 v = __hfma2(n, scale, zero);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ bool codes_warps(const AttnParams& p, const Ctx& x, Cursor u) {
+    const int lane = threadIdx.x & 31, row = 32 * (int)((threadIdx.x >> 5) & 3) + (lane & 7), quarter = lane >> 3;
+    const char* base = reinterpret_cast<const char*>(p.k);
+    const uint32_t dst = x.base + OFF_RING + (quarter >> 1) * HALF + row * 128;
+    int64_t left = x.weight;
+    if (left <= 0) return true;
+    Piece r = piece_at(x, u, left);
+    int j = r.j0, values = 0;   // what is loaded next
+    uint4 raw[4];
+    uint32_t num[4];
+    auto load = [&](int i) {
+        const int key = j * KB + row + 8 * i;
+        raw[i] = make_uint4(0, 0, 0, 0);
+        num[i] = 0;
+        if (key >= u.s.lk) return;
+        const char* at = base + u.n * p.k_seq + u.kh * p.k_head + key * p.k_row;
+        raw[i] = __ldcg(reinterpret_cast<const uint4*>(at + 64 * values + 16 * quarter));
+        num[i] = __ldcg(reinterpret_cast<const uint32_t*>(at + CODES_NUMBERS + 8 * values + 4 * (quarter >> 1)));
+    };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load(i);
+    int slot = 0;
+    uint32_t lap = 0;
+    bool more = true;
+#pragma unroll 1
+    while (more) {
+        // on to the next tile: the values of this block, or the keys of the next one
+        if (values) {
+            values = 0;
+            if (++j == r.j1) {
+                left -= r.weight;
+                more = left > 0;
+                if (more) {
+                    next_pair(p, x, u);
+                    r = piece_at(x, u, left);
+                    j = r.j0;
+                }
+            }
+        } else {
+            values = 1;
+        }
+        if (lap > 0 && !x.wait(EMPTY + slot, lap - 1)) return false;
+        const uint32_t at = dst + slot * TILE;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            __nv_bfloat162 scale, zero;
+            {
+                const uint32_t s2 = __byte_perm(num[i], 0, 0x1010), z2 = __byte_perm(num[i], 0, 0x3232);
+                scale = *reinterpret_cast<const __nv_bfloat162*>(&s2);
+                zero = *reinterpret_cast<const __nv_bfloat162*>(&z2);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t w = k == 0 ? raw[i].x : k == 1 ? raw[i].y : k == 2 ? raw[i].z : raw[i].w, w4 = w >> 4;
+                sts_u128(at + i * 1024 + (((4 * (quarter & 1) + k) ^ (lane & 7)) << 4), expand2<0x0400>(w, w4, scale, zero),
+                         expand2<0x0501>(w, w4, scale, zero), expand2<0x0602>(w, w4, scale, zero), expand2<0x0703>(w, w4, scale, zero));
+            }
+            if (more) load(i);
+        }
+        fence_proxy_async_smem();
+        mx_arrive_warp(x.bar(FULL + slot));
+        if (++slot == RING) slot = 0, ++lap;
+    }
+    return true;
+}
+
 // ---------------------------------------------------------------- warp 9: MMAs
 constexpr uint64_t K_STEP = 32 >> 4, K_HALF = HALF >> 4, MN_STEP = 2048 >> 4, D_TILE = TILE >> 4;
 constexpr uint32_t ID_KK = make_idesc_bf16_f32(128, 128), ID_MN = make_idesc_bf16_f32(128, 128, true);
@@ -402,6 +489,7 @@ constexpr uint32_t ID_KK = make_idesc_bf16_f32(128, 128), ID_MN = make_idesc_bf1
 // exponentiated: 984 against 890 us on 8,192 tokens x 64 heads.)  MMAs with both
 // operands in shared memory are issued one by one as they execute, those with A in Tensor Memory
 // queue up; so the waits stand behind the latter where they can.
+template <bool kCodes>
 __device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
     const int lane = threadIdx.x & 31;
     const uint32_t lead = mx_leader();
@@ -446,7 +534,7 @@ __device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
         auto next_values = [&](int j) {
             if (!landed(2 * j + 1)) return false;
             const int valid = u.s.lk - (r.j0 + j) * KB;
-            if (valid < KB) {
+            if (!kCodes && valid < KB) {
                 const uint32_t at = x.base + OFF_RING + slot(2 * j + 1) * TILE;
 #pragma unroll 1
                 for (int row = max(valid, 0); row < KB; ++row) sts_u64(at + (lane >> 4) * HALF + row * 128 + (lane & 15) * 8, 0u, 0u);
@@ -722,7 +810,8 @@ __device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const C
     return true;
 }
 
-__global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const AttnParams p, const __grid_constant__ AttnMaps maps, uint64_t recip) {
+template <bool kCodes>
+__global__ void __launch_bounds__(kCodes ? AT_CODES_THREADS : AT_THREADS, 1) attn_kernel(const AttnParams p, const __grid_constant__ AttnMaps maps, uint64_t recip) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const int tid = threadIdx.x, warp = mx_uniform(tid >> 5);
     asm volatile("griddepcontrol.launch_dependents;");
@@ -733,11 +822,11 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const AttnParams p,
     x.tp = 2 * x.tq;
     if (warp == 8) {
         if ((tid & 31) == 0) {
-            for (int b = 0; b < NBAR; ++b) mbar_init(x.bar(b), b == VZ ? 32 : (b >= PF && b < PF + 4) || b == PX || b == PX + 1 ? 4 : 1);
+            for (int b = 0; b < NBAR; ++b) mbar_init(x.bar(b), b == VZ ? 32 : (b >= PF && b < PF + 4) || b == PX || b == PX + 1 || (kCodes && b < FULL + RING) ? 4 : 1);
             mbar_fence_init();
             tma_prefetch_desc(&maps.q);
-            tma_prefetch_desc(&maps.k);
-            tma_prefetch_desc(&maps.v);
+            if (!kCodes) tma_prefetch_desc(&maps.k);
+            if (!kCodes) tma_prefetch_desc(&maps.v);
             tma_prefetch_desc(&maps.out);
         }
         __syncwarp();
@@ -746,7 +835,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const AttnParams p,
     }
     tc_fence_before();
     await_stream();
-    const Share share = find_share(p, x.tq, x.G, recip, reinterpret_cast<int64_t*>(smem_raw + OFF_SCRATCH));
+    const Share share = find_share<kCodes ? AT_CODES_THREADS : AT_THREADS>(p, x.tq, x.G, recip, reinterpret_cast<int64_t*>(smem_raw + OFF_SCRATCH));
     const Cursor u = share.at;
     __syncthreads();
     tc_fence_after();
@@ -764,13 +853,17 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const AttnParams p,
     }
     bool ok = true;
     // registers a thread: 168 at launch; 208 + 208 + 88 of the 3 x 168 that the block holds
+    // (with codes 128 at launch; 200 + 200 + 56 + 56 of 4 x 128)
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        if (kCodes) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         ok = softmax_warps(p, maps, x, u, warp >> 2);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-        if (warp == 8) ok = load_warp(p, maps, x, u);
-        else if (warp == 9) ok = mma_warp(p, x, u);
+        if (kCodes) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == 8) ok = load_warp<kCodes>(p, maps, x, u);
+        else if (warp == 9) ok = mma_warp<kCodes>(p, x, u);
+        else if (kCodes && warp >= 12) ok = codes_warps(p, x, u);
     }
     if (!ok) mx_wind_down();
     tc_fence_before();
@@ -883,23 +976,29 @@ size_t attn_workspace_bytes(int64_t, int, int) {
     return CUT_BYTES + ML_BYTES + (size_t)2 * AT_MAX_CTAS * 256 * HD * sizeof(float);
 }
 
-cudaError_t launch_attn(const AttnParams& p, cudaStream_t stream) {
+template <bool kCodes>
+static cudaError_t launch(const AttnParams& p, cudaStream_t stream) {
     const int G = p.Hq / p.Hk, tq = 128 / G;
     AttnMaps maps;
+    memset(&maps, 0, sizeof(maps));
     if (!mx_encode(&maps.q, p.q.data, p.Hq, p.Tq, 1, p.q.head, p.q.row, 0, G, tq) ||
-        !mx_encode(&maps.k, p.k, p.Hk, p.Tk, p.cache ? p.nseq : 1, p.k_head, p.k_row, p.k_seq, 1, KB) ||
-        !mx_encode(&maps.v, p.v, p.Hk, p.Tk, p.cache ? p.nseq : 1, p.v_head, p.v_row, p.v_seq, 1, KB) ||
+        (!kCodes && (!mx_encode(&maps.k, p.k, p.Hk, p.Tk, p.cache ? p.nseq : 1, p.k_head, p.k_row, p.k_seq, 1, KB) ||
+                     !mx_encode(&maps.v, p.v, p.Hk, p.Tk, p.cache ? p.nseq : 1, p.v_head, p.v_row, p.v_seq, 1, KB))) ||
         !mx_encode_3d(&maps.out, p.out.data, p.Hq, p.Tq, p.out.head, p.out.row, G <= 32 ? G : 1, G <= 32 ? 32 / G : 1))
         return cudaErrorInvalidValue;
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)AT_SMEM);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(attn_kernel<kCodes>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)AT_SMEM);
     if (e != cudaSuccess) return e;
     const int ctas = sms < AT_MAX_CTAS ? sms : AT_MAX_CTAS;
-    e = launch_early(attn_kernel, dim3((unsigned)ctas), AT_THREADS, AT_SMEM, stream, p, maps, ctas > 1 ? ~0ull / (uint64_t)ctas + 1 : (uint64_t)0);
+    e = launch_early(attn_kernel<kCodes>, dim3((unsigned)ctas), kCodes ? AT_CODES_THREADS : AT_THREADS, AT_SMEM, stream, p, maps,
+                     ctas > 1 ? ~0ull / (uint64_t)ctas + 1 : (uint64_t)0);
     if (e != cudaSuccess) return e;
     return launch_early(attn_join_kernel, dim3((unsigned)ctas, 256 / JOIN_ROWS), JOIN_THREADS, 0, stream, p, ctas);
 }
+
+cudaError_t launch_attn(const AttnParams& p, cudaStream_t stream) { return launch<false>(p, stream); }
+cudaError_t launch_attn_codes(const AttnParams& p, cudaStream_t stream) { return launch<true>(p, stream); }
 
 }  // namespace kda

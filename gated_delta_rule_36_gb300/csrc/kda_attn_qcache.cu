@@ -25,6 +25,8 @@
 // that lies in more than one share leaves unnormalised partial rows in the workspace, and a second, small kernel
 // joins them in the order of the keys.
 
+#include <string.h>
+
 #include "kda_mixer.cuh"
 #include "kda_qcache.cuh"
 
@@ -694,7 +696,7 @@ bool encode_cache(CUtensorMap* m, const QcacheAttnParams& p, int rows) {
     const cuuint64_t strides[3] = {(cuuint64_t)p.cache.head, (cuuint64_t)p.cache.row, (cuuint64_t)(p.cache.seq > 0 ? p.cache.seq : QC_ROW)};
     const cuuint32_t box[4] = {(cuuint32_t)QC_ROW, 1, (cuuint32_t)rows, 1}, estr[4] = {1, 1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, p.cache.data, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int kN>
@@ -710,9 +712,40 @@ cudaError_t launch(const QcacheAttnParams& p, int sms, cudaStream_t stream) {
 
 }  // namespace
 
-size_t attn_qcache_workspace_bytes(int64_t, int, int, int) { return QS_CUT_BYTES + QS_ML_BYTES + (size_t)2 * QS_MAX_CTAS * QS_MAX_ROWS * HD * sizeof(float); }
+// Few rows: this file's kernel; many: the tensor cores' of kda_attn.cu, which expands the codes on its way.
+static bool few_rows(int64_t Tq, int Hq, int Hk, int nseq) { return Tq * (Hq / Hk) <= 32 * (int64_t)nseq; }
+
+size_t attn_qcache_workspace_bytes(int64_t Tq, int Hq, int Hk, int nseq) {
+    if (few_rows(Tq, Hq, Hk, nseq)) return QS_CUT_BYTES + QS_ML_BYTES + (size_t)2 * QS_MAX_CTAS * QS_MAX_ROWS * HD * sizeof(float);
+    return attn_workspace_bytes(Tq, Hq, Hk);
+}
 
 cudaError_t launch_attn_qcache(const QcacheAttnParams& p, cudaStream_t stream) {
+    if (!few_rows(p.Tq, p.Hq, p.Hk, p.nseq)) {
+        AttnParams a;
+        memset(&a, 0, sizeof(a));
+        a.q = p.q;
+        a.out = p.out;
+        a.k = reinterpret_cast<__nv_bfloat16*>(p.cache.data);
+        a.k_seq = p.cache.seq;
+        a.k_row = p.cache.row;
+        a.k_head = p.cache.head;
+        a.lse = p.lse;
+        a.cu_q = p.cu_q;
+        a.seqlens_k = p.seqlens_k;
+        a.uniform_q = p.uniform_q;
+        a.Tq = p.Tq;
+        a.Tk = p.S;
+        a.nseq = p.nseq;
+        a.Hq = p.Hq;
+        a.Hk = p.Hk;
+        a.cache = 1;
+        a.scale = p.scale;
+        a.status = p.status;
+        a.workspace = p.workspace;
+        a.test_skip = -1;
+        return launch_attn_codes(a, stream);
+    }
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);

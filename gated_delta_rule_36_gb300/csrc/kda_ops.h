@@ -126,6 +126,8 @@ cudaError_t launch_gated_norm(const GatedNormParams& p, cudaStream_t stream);
 cudaError_t launch_residual_norm(const ResidualNormParams& p, cudaStream_t stream);
 cudaError_t launch_norm_rope(const NormRopeParams& p, cudaStream_t stream);
 cudaError_t launch_attn(const AttnParams& p, cudaStream_t stream);
+// The same over a cache in 4 bits: p.k its bytes, p.k_seq, p.k_row and p.k_head strides in bytes, p.v not used.
+cudaError_t launch_attn_codes(const AttnParams& p, cudaStream_t stream);
 size_t attn_workspace_bytes(int64_t Tq, int Hq, int Hk);
 cudaError_t launch_lin_fwd(const LinParams& p, cudaStream_t stream);
 size_t lin_workspace_bytes(int64_t T_total, int H, int nseq);
