@@ -128,7 +128,7 @@ def load(path: Optional[str] = None):
         lib.kda_qcache_append.restype = ctypes.c_int
         lib.kda_qcache_append.argtypes = [D, D, D, D, D, D, D, V, V]
         lib.kda_attn_qcache_workspace_size.restype = ctypes.c_size_t
-        lib.kda_attn_qcache_workspace_size.argtypes = [ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int]
+        lib.kda_attn_qcache_workspace_size.argtypes = [ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int64]
         lib.kda_attn_qcache_fwd.restype = ctypes.c_int
         lib.kda_attn_qcache_fwd.argtypes = [D, D, F, D, D, D, D, V, ctypes.c_size_t, V]
         lib.kda_gated_norm.restype = ctypes.c_int
@@ -567,8 +567,8 @@ def kda_qcache_append(k, v, cache, seqlens_k, cu_seqlens=None, k_out=None, v_out
         _check(lib, st)
 
 
-def kda_attn_qcache_workspace_size(Tq: int, Hq: int, Hk: int, N: int) -> int:
-    return int(load().kda_attn_qcache_workspace_size(int(Tq), int(Hq), int(Hk), int(N)))
+def kda_attn_qcache_workspace_size(Tq: int, Hq: int, Hk: int, N: int, S: int) -> int:
+    return int(load().kda_attn_qcache_workspace_size(int(Tq), int(Hq), int(Hk), int(N), int(S)))
 
 
 def kda_attn_qcache_fwd(q, cache, scale, out, seqlens_k, lse=None, cu_seqlens_q=None, workspace=None, stream=None):
@@ -580,7 +580,7 @@ def kda_attn_qcache_fwd(q, cache, scale, out, seqlens_k, lse=None, cu_seqlens_q=
     dq, dc = _view(q, "q", dev), _bytes_view(cache, "cache", dev)
     if workspace is None and q.dim() == 3:
         n = cache.shape[0] if cu_seqlens_q is None else max(cu_seqlens_q.numel() - 1, 0)
-        nbytes = lib.kda_attn_qcache_workspace_size(q.shape[0], q.shape[1], cache.shape[2], n) or 256   # 0: refused below
+        nbytes = lib.kda_attn_qcache_workspace_size(q.shape[0], q.shape[1], cache.shape[2], n, cache.shape[1]) or 256   # 0: refused below
         workspace = _workspace(None, nbytes, dev, stream)
     else:
         workspace = _workspace(workspace, 256, dev, stream)

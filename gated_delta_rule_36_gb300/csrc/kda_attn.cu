@@ -44,6 +44,7 @@
 // 704 against 696 us.  Two threads a row, each with half of the keys: 784 against 677 us; an
 // exponential with its scaling, sum and packing takes 7.3 cycles from one warp of a scheduler and 5.5 from
 // two, so that halves gain less than exchanging their maxima costs.
+#include <cuda_fp16.h>
 #include <string.h>
 
 #include "kda_mixer.cuh"
@@ -51,31 +52,38 @@
 namespace kda {
 namespace {
 
-constexpr int AT_THREADS = 384, AT_CODES_THREADS = 512;   // (four more warps where the cache holds codes)
 constexpr int AT_MAX_CTAS = 160;
 constexpr int KB = 128;                       // keys a block
+constexpr int AT_THREADS = 384;
 constexpr uint32_t TILE = 128 * 256, HALF = TILE / 2;
-constexpr int RING = 4;
 // A pair's own weight, in steps.  With 0, 1, 2 and 3: long prompt 803, 733, 705 and 710 us, 32 single
 // tokens 128, 105, 105 and 106 us.
 constexpr int PIECE = 2;
 constexpr uint32_t OFF_RING = 2 * TILE;       // behind the two query tiles
-constexpr uint32_t OFF_STAGE = OFF_RING + RING * TILE;   // 4 KB for each softmax warp: 32 rows of 128 bytes
-// The search for the shares works here: its ordinary stores must not meet a tile's bulk loads, which
-// nothing but a proxy fence would order behind them.
-constexpr uint32_t OFF_SCRATCH = OFF_STAGE;
-constexpr uint32_t OFF_BAR = OFF_STAGE + 8 * 4096;
-static_assert(OFF_SCRATCH >= OFF_RING + RING * TILE && OFF_SCRATCH + 48 * 8 <= OFF_BAR, "outside what bulk loads fill");
-enum { FULL = 0, EMPTY = RING, QF = 2 * RING, QE, SF, PF = SF + 2, OF = PF + 4, SX = OF + 2, PX, PV = PX + 2, VZ, DRAIN, NBAR };
-constexpr uint32_t OFF_TMEM = OFF_BAR + NBAR * 8;
-constexpr uint32_t AT_SMEM = OFF_TMEM + 8;
-static_assert(AT_SMEM <= 232448, "one CTA's shared memory");
+constexpr int MAX_RING = 5;
+enum { FULL = 0, EMPTY = MAX_RING, QF = 2 * MAX_RING, QE, SF, PF = SF + 2, OF = PF + 4, SX = OF + 2, PX, PV = PX + 2, VZ, DRAIN, NBAR };
+// k and v of a block take two tiles of a ring of four; where the keys come as two terms (kSplit), three of five, which
+// leaves no room for staged results.
+template <bool kSplit>
+struct Layout {
+    static constexpr int RING = kSplit ? 5 : 4, PER = kSplit ? 3 : 2;
+    static constexpr uint32_t OFF_STAGE = OFF_RING + RING * TILE;           // 4 KB for each softmax warp: 32 rows of 128 bytes
+    // The search for the shares works here: its ordinary stores must not meet a tile's bulk loads, which
+    // nothing but a proxy fence would order behind them.
+    static constexpr uint32_t OFF_SCRATCH = OFF_STAGE;
+    static constexpr uint32_t OFF_BAR = OFF_STAGE + (kSplit ? 512 : 8 * 4096);
+    static constexpr uint32_t OFF_TMEM = OFF_BAR + NBAR * 8;
+    static constexpr uint32_t SMEM = OFF_TMEM + 8;
+    static_assert(OFF_SCRATCH >= OFF_RING + RING * TILE && OFF_SCRATCH + 48 * 8 <= OFF_BAR, "outside what bulk loads fill");
+    static_assert(SMEM <= 232448, "one CTA's shared memory");
+};
 // Tensor Memory (all 512 columns, so that its address is 0): two tiles of 128 columns each; P over
 // the first 64 of S
 constexpr uint32_t TM_S = 0, TM_O = 256;
 
 struct AttnMaps {
     CUtensorMap q, k, v;
+    CUtensorMap k_low; // split keys: the second terms
     CUtensorMap out;   // boxes of a warp's 32 rows (used when G divides 32)
 };
 
@@ -188,10 +196,9 @@ struct Share {
     Cursor at;          // where it starts
     bool bad;           // lengths that contradict the tensors
 };
-template <int kThreads>
 __device__ Share find_share(const AttnParams& p, int tq, int G, uint64_t recip, int64_t* scratch /* 48 */) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tp = 2 * tq;
-    const int per = (p.nseq + kThreads - 1) / kThreads;
+    const int per = (p.nseq + AT_THREADS - 1) / AT_THREADS;
     const int n0 = min(tid * per, p.nseq), n1 = min(n0 + per, p.nseq);
     Seq s{};
     int64_t mine = 0, each = 0;
@@ -202,7 +209,7 @@ __device__ Share find_share(const AttnParams& p, int tq, int G, uint64_t recip, 
         bool b = false;
         if (p.cu_q) b |= p.cu_q[n + 1] < p.cu_q[n] || (n == 0 && p.cu_q[0] != 0) || (n + 1 == p.nseq && p.cu_q[n + 1] > p.Tq);
         if (p.cu_k) b |= p.cu_k[n + 1] < p.cu_k[n] || (n == 0 && p.cu_k[0] != 0) || (n + 1 == p.nseq && p.cu_k[n + 1] > p.Tk);
-        if (p.seqlens_k) b |= p.seqlens_k[n] < 0 || p.seqlens_k[n] > p.Tk;
+        if (p.seqlens_k) b |= p.seqlens_k[n] < 0 || p.seqlens_k[n] > p.keys;
         bad |= b;
         s = seq_of(p, n);
         each = b ? 0 : weight_of(s, tp);
@@ -223,7 +230,7 @@ __device__ Share find_share(const AttnParams& p, int tq, int G, uint64_t recip, 
     if (r.bad) return r;
     int64_t total = 0, before = sum - mine;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
+    for (int w = 0; w < AT_THREADS / 32; ++w) {
         before += w < warp ? scratch[w] : 0;
         total += scratch[w];
     }
@@ -247,7 +254,7 @@ __device__ Share find_share(const AttnParams& p, int tq, int G, uint64_t recip, 
     __syncthreads();
     // half of the threads for each end: the key head and the step within it; then the last pair that
     // starts at or before that step, of which every thread tries some
-    const int e = tid >= kThreads / 2;
+    const int e = tid >= AT_THREADS / 2;
     const bool open = e && x1 >= total;   // the last share's end needs no search
     const Found f = found[open ? 0 : e];
     Cursor u;
@@ -262,7 +269,7 @@ __device__ Share find_share(const AttnParams& p, int tq, int G, uint64_t recip, 
     int lo = 0, width = m;
 #pragma unroll 1
     while (__syncthreads_or(width > 1)) {   // narrow [lo, lo + width)
-        const int step = (width + kThreads / 2 - 1) / (kThreads / 2), c = lo + (tid % (kThreads / 2)) * step;
+        const int step = (width + AT_THREADS / 2 - 1) / (AT_THREADS / 2), c = lo + (tid % (AT_THREADS / 2)) * step;
         const int64_t st = width > 1 && c < lo + width ? weight_in_turn(u.s.lq, u.s.lk, c, tp, m, f.each) : at + 1;
         if (st <= at) atomicMax(best + e, c);
         __syncthreads();
@@ -301,7 +308,7 @@ __device__ Share find_share(const AttnParams& p, int tq, int G, uint64_t recip, 
     __syncthreads();
     Cursor* place = reinterpret_cast<Cursor*>(scratch + 20);
     if (tid == 0) *place = u, start[0] = x;
-    if (tid == kThreads / 2) start[1] = x;
+    if (tid == AT_THREADS / 2) start[1] = x;
     __syncthreads();
     r.at = *place;
     r.weight = start[1] - start[0];
@@ -318,10 +325,10 @@ struct Piece {
 };
 
 struct Ctx {
-    uint32_t base;
+    uint32_t base, bars;
     int64_t weight;     // of this share
     int tq, tp, G;      // tokens of a tile and of a pair, heads of a group
-    __device__ uint32_t bar(int b) const { return base + OFF_BAR + 8u * b; }
+    __device__ uint32_t bar(int b) const { return bars + 8u * b; }
     __device__ bool wait(int b, uint32_t use) const { return mx_wait(bar(b), use & 1u); }
 };
 
@@ -354,7 +361,7 @@ __device__ __forceinline__ void next_pair(const AttnParams& p, const Ctx& x, Cur
 }
 
 // ---------------------------------------------------------------- warp 8: loads
-template <bool kCodes>
+template <bool kSplit>
 __device__ bool load_warp(const AttnParams& p, const AttnMaps& maps, const Ctx& x, Cursor u) {
     bool ok = true;
     if ((threadIdx.x & 31) == 0) {
@@ -370,15 +377,15 @@ __device__ bool load_warp(const AttnParams& p, const AttnMaps& maps, const Ctx& 
                 tma_load_4d(dst, m, 0, kh, row, n, full);
                 tma_load_4d(dst + HALF, m, 64, kh, row, n, full);
             }
-            if (++slot == RING) slot = 0, ++lap;
+            if (++slot == Layout<kSplit>::RING) slot = 0, ++lap;
             return true;
         };
         for (int64_t left = x.weight; left > 0 && ok; next_pair(p, x, u), ++pieces) {
             const Piece r = piece_at(x, u, left);
             left -= r.weight;
             const int n = p.cache ? u.n : 0;
-            for (int j = r.j0; j < (kCodes ? r.j0 + 1 : r.j1) && ok; ++j) {   // (codes are warps 12-15's)
-                if (!kCodes) ok = tile(&maps.k, u.kh, u.s.k0 + j * KB, n) && tile(&maps.v, u.kh, u.s.k0 + j * KB, n);
+            for (int j = r.j0; j < r.j1 && ok; ++j) {
+                ok = tile(&maps.k, u.kh, u.s.k0 + j * KB, n) && (!kSplit || tile(&maps.k_low, u.kh, u.s.k0 + j * KB, n)) && tile(&maps.v, u.kh, u.s.k0 + j * KB, n);
                 if (j > r.j0 || !ok) continue;
                 // the queries, once the last scores of the piece before are done
                 if (pieces > 0) ok = mx_wait_lane(x.bar(QE), (pieces - 1) & 1u);
@@ -396,92 +403,10 @@ __device__ bool load_warp(const AttnParams& p, const AttnMaps& maps, const Ctx& 
     return __all_sync(0xffffffffu, ok);
 }
 
-// ---------------------------------------------------------------- warps 12-15: keys and values from codes
-// A cache in 4 bits: the tiles of the ring are written here, in the layout that the bulk loads would give them.  Lane
-// l of warp w takes rows 32 w + 8 i + l % 8, i < 4, and of their codes 16 bytes, channels 32 (l / 8) on: eight lanes
-// that store together then store to different banks.  Keys and values are rounded to bf16, code scale + zero in one
-// rounding.  The rows of the next tile are loaded as this one's are written; rows past the sequence's keys are zeros,
-// whatever the cache holds there.
-constexpr int CODES_NUMBERS = 128;   // where a row's scales and zeros are
-
-// Two codes, bytes `sel` of x and x >> 4, times scale plus zero.
-template <uint32_t sel>
-__device__ __forceinline__ uint32_t expand2(uint32_t x, uint32_t x4, __nv_bfloat162 scale, __nv_bfloat162 zero) {
-    const uint32_t y = (__byte_perm(x, x4, sel) & 0x000f000fu) | 0x43004300u;   // 128 + code
-    const __nv_bfloat162 n = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&y), __float2bfloat162_rn(128.f));
-    const __nv_bfloat162 v = __hfma2(n, scale, zero);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-__device__ bool codes_warps(const AttnParams& p, const Ctx& x, Cursor u) {
-    const int lane = threadIdx.x & 31, row = 32 * (int)((threadIdx.x >> 5) & 3) + (lane & 7), quarter = lane >> 3;
-    const char* base = reinterpret_cast<const char*>(p.k);
-    const uint32_t dst = x.base + OFF_RING + (quarter >> 1) * HALF + row * 128;
-    int64_t left = x.weight;
-    if (left <= 0) return true;
-    Piece r = piece_at(x, u, left);
-    int j = r.j0, values = 0;   // what is loaded next
-    uint4 raw[4];
-    uint32_t num[4];
-    auto load = [&](int i) {
-        const int key = j * KB + row + 8 * i;
-        raw[i] = make_uint4(0, 0, 0, 0);
-        num[i] = 0;
-        if (key >= u.s.lk) return;
-        const char* at = base + u.n * p.k_seq + u.kh * p.k_head + key * p.k_row;
-        raw[i] = __ldcg(reinterpret_cast<const uint4*>(at + 64 * values + 16 * quarter));
-        num[i] = __ldcg(reinterpret_cast<const uint32_t*>(at + CODES_NUMBERS + 8 * values + 4 * (quarter >> 1)));
-    };
-#pragma unroll
-    for (int i = 0; i < 4; ++i) load(i);
-    int slot = 0;
-    uint32_t lap = 0;
-    bool more = true;
-#pragma unroll 1
-    while (more) {
-        // on to the next tile: the values of this block, or the keys of the next one
-        if (values) {
-            values = 0;
-            if (++j == r.j1) {
-                left -= r.weight;
-                more = left > 0;
-                if (more) {
-                    next_pair(p, x, u);
-                    r = piece_at(x, u, left);
-                    j = r.j0;
-                }
-            }
-        } else {
-            values = 1;
-        }
-        if (lap > 0 && !x.wait(EMPTY + slot, lap - 1)) return false;
-        const uint32_t at = dst + slot * TILE;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            __nv_bfloat162 scale, zero;
-            {
-                const uint32_t s2 = __byte_perm(num[i], 0, 0x1010), z2 = __byte_perm(num[i], 0, 0x3232);
-                scale = *reinterpret_cast<const __nv_bfloat162*>(&s2);
-                zero = *reinterpret_cast<const __nv_bfloat162*>(&z2);
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t w = k == 0 ? raw[i].x : k == 1 ? raw[i].y : k == 2 ? raw[i].z : raw[i].w, w4 = w >> 4;
-                sts_u128(at + i * 1024 + (((4 * (quarter & 1) + k) ^ (lane & 7)) << 4), expand2<0x0400>(w, w4, scale, zero),
-                         expand2<0x0501>(w, w4, scale, zero), expand2<0x0602>(w, w4, scale, zero), expand2<0x0703>(w, w4, scale, zero));
-            }
-            if (more) load(i);
-        }
-        fence_proxy_async_smem();
-        mx_arrive_warp(x.bar(FULL + slot));
-        if (++slot == RING) slot = 0, ++lap;
-    }
-    return true;
-}
-
 // ---------------------------------------------------------------- warp 9: MMAs
 constexpr uint64_t K_STEP = 32 >> 4, K_HALF = HALF >> 4, MN_STEP = 2048 >> 4, D_TILE = TILE >> 4;
 constexpr uint32_t ID_KK = make_idesc_bf16_f32(128, 128), ID_MN = make_idesc_bf16_f32(128, 128, true);
+constexpr uint32_t ID_MN_F16 = ID_MN & ~(1u << 7 | 1u << 10);   // weights and values in fp16
 
 // One warp for both tiles, strictly in turn: for each block P V of tile 0, the next scores of tile
 // 0 (over P: the MMAs of a thread go in order), P V of tile 1, the next scores of tile 1.  (Two
@@ -489,32 +414,38 @@ constexpr uint32_t ID_KK = make_idesc_bf16_f32(128, 128), ID_MN = make_idesc_bf1
 // exponentiated: 984 against 890 us on 8,192 tokens x 64 heads.)  MMAs with both
 // operands in shared memory are issued one by one as they execute, those with A in Tensor Memory
 // queue up; so the waits stand behind the latter where they can.
-template <bool kCodes>
+template <bool kSplit>
 __device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
     const int lane = threadIdx.x & 31;
     const uint32_t lead = mx_leader();
     const uint64_t dQ = make_sdesc_kmajor_sw128(x.base), dK = make_sdesc_kmajor_sw128(x.base + OFF_RING);
     const uint64_t dV = make_sdesc_mnmajor_sw128(x.base + OFF_RING, HALF, 1024);
-    uint32_t it = 0;              // tiles of the ring before this piece: k and v alternate
+    constexpr uint32_t RING = Layout<kSplit>::RING, PER = Layout<kSplit>::PER;
+    uint32_t it = 0;              // tiles of the ring before this piece: k (its two terms) and v alternate
     uint32_t pieces = 0, n0 = 0, n1 = 0, nX = 0, nZ = 0;
     // A wait's verdict is the lane's own (a vote each time would cost 3.5 % of a long prompt), so within a piece
     // nothing that the whole warp has to reach follows; the warp agrees at the piece's end.
     bool ok = true;
     // tile i of the piece has landed; its slot
-    auto landed = [&](uint32_t i) { return mx_wait_lane(x.bar(FULL + ((it + i) & (RING - 1))), (it + i) / RING & 1u); };
-    auto slot = [&](uint32_t i) { return (int)((it + i) & (RING - 1)); };
-    auto scores = [&](int q, int t, int s, int done) {   // of query tile q, into place t
-        const uint64_t a = dQ + q * D_TILE, k = dK + s * D_TILE;
+    auto landed = [&](uint32_t i) { return mx_wait_lane(x.bar(FULL + (it + i) % RING), (it + i) / RING & 1u); };
+    auto keys_landed = [&](uint32_t j) { return landed(PER * j) && (!kSplit || landed(PER * j + 1)); };   // of block j
+    auto slot = [&](uint32_t i) { return (int)((it + i) % RING); };
+    auto scores = [&](int q, int t, int j, int done) {   // of query tile q with the keys of block j, into place t
+        const uint64_t a = dQ + q * D_TILE;
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-            mx_mma_ss(lead, TM_S + 128 * t, a + (kk >> 2) * K_HALF + (kk & 3) * K_STEP, k + (kk >> 2) * K_HALF + (kk & 3) * K_STEP, ID_KK, kk > 0);
+        for (int term = 0; term < (kSplit ? 2 : 1); ++term) {
+            const uint64_t k = dK + slot(PER * j + term) * D_TILE;
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+                mx_mma_ss(lead, TM_S + 128 * t, a + (kk >> 2) * K_HALF + (kk & 3) * K_STEP, k + (kk >> 2) * K_HALF + (kk & 3) * K_STEP, ID_KK, kk > 0 || term > 0);
+        }
         mx_commit(lead, x.bar(done));
     };
     auto values = [&](int o, int t, int s, int half, bool first) {   // weights in place t, onto output o
         const uint64_t v = dV + s * D_TILE;
 #pragma unroll
         for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-            mx_mma_ts(lead, TM_O + 128 * o, TM_S + 128 * t + kk * 8, v + kk * MN_STEP, ID_MN, kk > 0 || !first);
+            mx_mma_ts(lead, TM_O + 128 * o, TM_S + 128 * t + kk * 8, v + kk * MN_STEP, kSplit ? ID_MN_F16 : ID_MN, kk > 0 || !first);
     };
     // (half of) the weights are in place, for the n-th time
     auto weights = [&](int done, uint32_t n) {
@@ -532,10 +463,10 @@ __device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
         // the values of block j have landed; those past the sequence's keys count for nothing,
         // whatever they hold
         auto next_values = [&](int j) {
-            if (!landed(2 * j + 1)) return false;
+            if (!landed(PER * j + PER - 1)) return false;
             const int valid = u.s.lk - (r.j0 + j) * KB;
-            if (!kCodes && valid < KB) {
-                const uint32_t at = x.base + OFF_RING + slot(2 * j + 1) * TILE;
+            if (!kSplit && valid < KB) {   // (split keys and values: their rows are zeros there)
+                const uint32_t at = x.base + OFF_RING + slot(PER * j + PER - 1) * TILE;
 #pragma unroll 1
                 for (int row = max(valid, 0); row < KB; ++row) sts_u64(at + (lane >> 4) * HALF + row * 128 + (lane & 15) * 8, 0u, 0u);
                 fence_proxy_async_smem();
@@ -544,23 +475,24 @@ __device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
             }
             return true;
         };
-        // the keys in slot s, of block j, are used; after the last ones the queries are too
-        auto scored = [&](int j, int s) {
-            mx_commit(lead, x.bar(EMPTY + s));
+        // the keys of block j are used; after the last ones the queries are too
+        auto scored = [&](int j) {
+            mx_commit(lead, x.bar(EMPTY + slot(PER * j)));
+            if (kSplit) mx_commit(lead, x.bar(EMPTY + slot(PER * j + 1)));
             if (j + 1 == count) mx_commit(lead, x.bar(QE));
         };
-        ok = x.wait(QF, pieces) && __all_sync(0xffffffffu, landed(0));
+        ok = x.wait(QF, pieces) && __all_sync(0xffffffffu, keys_landed(0));
         if (!ok) break;
         if (!r.two) {
             // one tile: its scores alternate between the two places, so that the next block's are there
             // when the tile's softmax has done with this one's
-            scores(0, 0, slot(0), SF);
-            scored(0, slot(0));
+            scores(0, 0, 0, SF);
+            scored(0);
             if (count > 1) {
-                ok = landed(2);
+                ok = keys_landed(1);
                 if (!ok) break;
-                scores(0, 1, slot(2), SX);
-                scored(1, slot(2));
+                scores(0, 1, 1, SX);
+                scored(1);
             }
 #pragma unroll 1
             for (int j = 0; j < count; ++j) {
@@ -569,28 +501,28 @@ __device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
                 const int done = t ? PX : PF;
                 ok = next_values(j) && weights(done, n);
                 if (!ok) break;
-                values(0, t, slot(2 * j + 1), 0, j == 0);
+                values(0, t, slot(PER * j + PER - 1), 0, j == 0);
                 ok = weights(done + 1, n);
                 if (!ok) break;
-                values(0, t, slot(2 * j + 1), 1, j == 0);
+                values(0, t, slot(PER * j + PER - 1), 1, j == 0);
                 mx_commit(lead, x.bar(j + 1 == count ? OF : PV));
-                mx_commit(lead, x.bar(EMPTY + slot(2 * j + 1)));
+                mx_commit(lead, x.bar(EMPTY + slot(PER * j + PER - 1)));
                 if (j + 2 < count) {
-                    ok = landed(2 * j + 4);
+                    ok = keys_landed(j + 2);
                     if (!ok) break;
-                    scores(0, t, slot(2 * j + 4), t ? SX : SF);
-                    scored(j + 2, slot(2 * j + 4));
+                    scores(0, t, j + 2, t ? SX : SF);
+                    scored(j + 2);
                 }
             }
         } else {
-            if (c0 > 0) scores(0, 0, slot(0), SF);
-            scores(1, 1, slot(0), SF + 1);
-            scored(0, slot(0));
+            if (c0 > 0) scores(0, 0, 0, SF);
+            scores(1, 1, 0, SF + 1);
+            scored(0);
             ok = next_values(0);
 #pragma unroll 1
             for (int j = 0; ok; ++j) {
                 const bool more = j + 1 < count;
-                const int vs = slot(2 * j + 1), ks = slot(2 * j + 2);
+                const int vs = slot(PER * j + PER - 1);
                 if (j < c0) {
                     ok = weights(PF, n0);
                     if (!ok) break;
@@ -601,9 +533,9 @@ __device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
                     if (j + 1 == c0) mx_commit(lead, x.bar(OF));
                 }
                 if (more) {
-                    ok = landed(2 * j + 2);
+                    ok = keys_landed(j + 1);
                     if (!ok) break;
-                    if (j + 1 < c0) scores(0, 0, ks, SF);
+                    if (j + 1 < c0) scores(0, 0, j + 1, SF);
                 }
                 ok = weights(PF + 2, n1);
                 if (!ok) break;
@@ -618,13 +550,13 @@ __device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
                 }
                 ok = next_values(j + 1);
                 if (!ok) break;
-                scores(1, 1, ks, SF + 1);
-                scored(j + 1, ks);
+                scores(1, 1, j + 1, SF + 1);
+                scored(j + 1);
             }
         }
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        it += 2 * count;
+        it += PER * count;
     }
     __syncwarp();
     mx_commit(lead, x.bar(DRAIN));
@@ -638,11 +570,17 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+template <bool kSplit>
 __device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const Ctx& x, Cursor u, int t) {
     const int row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(row & ~31) << 16, tO = lanes + TM_O + 128 * t;
     const int lane = threadIdx.x & 31;
-    const uint32_t stage = x.base + OFF_STAGE + (threadIdx.x >> 5) * 4096;
+    const uint32_t stage = x.base + Layout<kSplit>::OFF_STAGE + (threadIdx.x >> 5) * 4096;
     const float c = fmaxf(p.scale * LOG2E, 1e-30f);   // (a scale of 0 must not turn a masked -inf into NaN)
     const Partials part = partials(p.workspace);
     const int tok = row / x.G, head = row - tok * x.G;
@@ -659,7 +597,11 @@ __device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const C
         // the last key it sees; a row that is no query's is left as it is, nothing reads its results
         const int last = mine ? i + u.s.lk - u.s.lq : 0x7fffffff;
         float m = -INFINITY, l = 0.f;
+        // split: a block's values are scaled by a power of two of its own (top[j]); the output by the largest so far
+        const int* tops = kSplit ? p.top + ((int64_t)u.n * p.Hk + u.kh) * p.top_blocks : nullptr;
+        int top_v = 0;
         for (int j = r.j0; j < end; ++j) {
+            const int top_j = kSplit ? __ldg(tops + j) : 0;
             if (!x.wait(other ? SX : SF + t, other ? nX++ : nS++)) return false;
             tc_fence_after();
             const uint32_t tS = lanes + TM_S + 128 * (t + other);
@@ -684,10 +626,16 @@ __device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const C
             // came after them; with one they did not, and the product before has a barrier of its own
             if (!r.two && j > r.j0 && !x.wait(PV, nV++)) return false;
             const bool grown = mine && (top - m) * c > 8.f;   // (m = -inf: whenever a key is seen)
-            if (__any_sync(0xffffffffu, grown)) {
-                const float f = grown ? exp2f((m - top) * c) : 1.f;
+            float lower = 1.f;
+            if (kSplit) {
+                if (j > r.j0 && top_j > top_v) lower = __uint_as_float((uint32_t)max(127 + top_v - top_j, 1) << 23);
+                top_v = max(top_v, top_j);
+            }
+            if (__any_sync(0xffffffffu, grown || (kSplit && lower != 1.f))) {
+                float f = grown ? exp2f((m - top) * c) : 1.f;
                 if (grown) m = top;
                 l *= f;
+                if (kSplit) f *= lower;
                 if (j > r.j0) {
                     const float2 f2 = make_float2(f, f);
 #pragma unroll 1
@@ -705,7 +653,9 @@ __device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const C
                     }
                 }
             }
-            const float mc = m == -INFINITY ? 0.f : -m * c;
+            float mc = m == -INFINITY ? 0.f : -m * c;
+            const int less = kSplit ? max(top_j - top_v, -60) : 0;   // the weights take the difference of the powers
+            if (kSplit) mc += (float)less;
             const float2 c2 = make_float2(c, c), mc2 = make_float2(mc, mc);
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -716,7 +666,7 @@ __device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const C
                     const float2 a = __ffma2_rn(make_float2(mx_u2f(s[32 * b + k]), mx_u2f(s[32 * b + k + 1])), c2, mc2);
                     const float2 e = make_float2(ex2_approx(a.x), ex2_approx(a.y));
                     sum[(k >> 1) & 1] = __fadd2_rn(sum[(k >> 1) & 1], e);
-                    y[k / 2] = pack_bf16x2(e.x, e.y);
+                    y[k / 2] = kSplit ? pack_half2(e.x, e.y) : pack_bf16x2(e.x, e.y);
                 }
                 tmem_st16(tS + 16 * b, y);
                 if (b & 1) {   // half of P: the tensor core can start on it
@@ -728,7 +678,8 @@ __device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const C
                     mx_arrive_warp(x.bar((other ? PX : PF + 2 * t) + (b >> 1)));
                 }
             }
-            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            const float all = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            l += kSplit ? all * __uint_as_float((uint32_t)(127 - less) << 23) : all;
             other = !r.two && !other;
         }
         const int64_t q = u.s.q0 + i;
@@ -740,6 +691,7 @@ __device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const C
             if (!x.wait(OF + t, nO)) return false;
             ++nO;
             tc_fence_after();
+            const float back = kSplit ? __uint_as_float((uint32_t)(top_v - SPLIT_TOP) << 23) : 1.f;   // of the values' scaling
             if (!r.whole) {
                 float4* o = part.o + part_slot * 32 * 256 + part_row;
 #pragma unroll 1
@@ -749,6 +701,10 @@ __device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const C
                     tmem_wait_ld();
                     mx_loaded(w);
                     if (mine) {
+                        if (kSplit) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) w[k] = __float_as_uint(back * mx_u2f(w[k]));
+                        }
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
                             o[(8 * b + k) * 256] = make_float4(mx_u2f(w[4 * k]), mx_u2f(w[4 * k + 1]), mx_u2f(w[4 * k + 2]), mx_u2f(w[4 * k + 3]));
@@ -758,9 +714,9 @@ __device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const C
             } else {
                 // 64 channels at a time through the warp's stage; then one tensor store of the warp's rows
                 // if they are whole tokens and all there, or eight lanes a row
-                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const float inv = l == 0.f ? 0.f : kSplit ? back / l : 1.f / l;
                 const float2 inv2 = make_float2(inv, inv);
-                const bool tensor = mask == 0xffffffffu && x.G <= 32 && (x.G & (x.G - 1)) == 0;
+                const bool tensor = !kSplit && mask == 0xffffffffu && x.G <= 32 && (x.G & (x.G - 1)) == 0;
                 const unsigned long long dst = reinterpret_cast<unsigned long long>(p.out.data + q * p.out.row + h * p.out.head);
 #pragma unroll 1
                 for (int b = mask ? 0 : 4; b < 4; ++b) {
@@ -773,26 +729,34 @@ __device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const C
                         const float2 y = __fmul2_rn(make_float2(mx_u2f(w[k]), mx_u2f(w[k + 1])), inv2);
                         w[k / 2] = pack_bf16x2(y.x, y.y);
                     }
+                    if constexpr (kSplit) {   // (no room for a stage: each thread its own row)
+                        if (mine) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        sts_u128(stage + lane * 128 + (((4 * (b & 1) + k) ^ (lane & 7)) << 4), w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
-                    if (!(b & 1)) continue;
-                    if (tensor) {
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            tma_store_3d(&maps.out, stage, 32 * (b - 1), u.kh * x.G, (int)q);
-                            bulk_commit();
-                            bulk_wait_read_all();
+                            for (int k = 0; k < 4; ++k)
+                                *reinterpret_cast<uint4*>(dst + 64 * b + 16 * k) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
                         }
                     } else {
-                        __syncwarp();
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            sts_u128(stage + lane * 128 + (((4 * (b & 1) + k) ^ (lane & 7)) << 4), w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+                        if (!(b & 1)) continue;
+                        if (tensor) {
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) {
+                                tma_store_3d(&maps.out, stage, 32 * (b - 1), u.kh * x.G, (int)q);
+                                bulk_commit();
+                                bulk_wait_read_all();
+                            }
+                        } else {
+                            __syncwarp();
 #pragma unroll 1
-                        for (int k = 0; k < 8; ++k) {
-                            const int from = 4 * k + (lane >> 3);   // this lane's row in turn
-                            const unsigned long long d = __shfl_sync(0xffffffffu, dst, from);
-                            const uint4 y = lds_u128(stage + from * 128 + (((lane & 7) ^ (from & 7)) << 4));
-                            if (mask >> from & 1u) *reinterpret_cast<uint4*>(d + (b >> 1) * 128 + (lane & 7) * 16) = y;
+                            for (int k = 0; k < 8; ++k) {
+                                const int from = 4 * k + (lane >> 3);   // this lane's row in turn
+                                const unsigned long long d = __shfl_sync(0xffffffffu, dst, from);
+                                const uint4 y = lds_u128(stage + from * 128 + (((lane & 7) ^ (from & 7)) << 4));
+                                if (mask >> from & 1u) *reinterpret_cast<uint4*>(d + (b >> 1) * 128 + (lane & 7) * 16) = y;
+                            }
                         }
                     }
                     __syncwarp();
@@ -802,7 +766,7 @@ __device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const C
         }
         if (mine) {
             if (!r.whole) part.ml[part_slot * 256 + part_row] = make_float2(m * c, l);
-            else if (p.lse) p.lse[q * p.Hq + h] = l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.6931471805599453f;
+            else if (p.lse) p.lse[q * p.lse_row + h] = l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.6931471805599453f;
         }
     }
     if (lane == 0) bulk_wait_all();
@@ -810,36 +774,38 @@ __device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const C
     return true;
 }
 
-template <bool kCodes>
-__global__ void __launch_bounds__(kCodes ? AT_CODES_THREADS : AT_THREADS, 1) attn_kernel(const AttnParams p, const __grid_constant__ AttnMaps maps, uint64_t recip) {
+template <bool kSplit>
+__global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const AttnParams p, const __grid_constant__ AttnMaps maps, uint64_t recip) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const int tid = threadIdx.x, warp = mx_uniform(tid >> 5);
     asm volatile("griddepcontrol.launch_dependents;");
+    using L = Layout<kSplit>;
     Ctx x;
     x.base = smem_u32(smem_raw);
+    x.bars = x.base + L::OFF_BAR;
     x.G = p.Hq / p.Hk;
     x.tq = 128 / x.G;
     x.tp = 2 * x.tq;
     if (warp == 8) {
         if ((tid & 31) == 0) {
-            for (int b = 0; b < NBAR; ++b) mbar_init(x.bar(b), b == VZ ? 32 : (b >= PF && b < PF + 4) || b == PX || b == PX + 1 || (kCodes && b < FULL + RING) ? 4 : 1);
+            for (int b = 0; b < NBAR; ++b) mbar_init(x.bar(b), b == VZ ? 32 : (b >= PF && b < PF + 4) || b == PX || b == PX + 1 ? 4 : 1);
             mbar_fence_init();
             tma_prefetch_desc(&maps.q);
-            if (!kCodes) tma_prefetch_desc(&maps.k);
-            if (!kCodes) tma_prefetch_desc(&maps.v);
+            tma_prefetch_desc(&maps.k);
+            tma_prefetch_desc(&maps.v);
             tma_prefetch_desc(&maps.out);
         }
         __syncwarp();
-        tmem_alloc(x.base + OFF_TMEM, 512);
+        tmem_alloc(x.base + L::OFF_TMEM, 512);
         tmem_relinquish();
     }
     tc_fence_before();
     await_stream();
-    const Share share = find_share<kCodes ? AT_CODES_THREADS : AT_THREADS>(p, x.tq, x.G, recip, reinterpret_cast<int64_t*>(smem_raw + OFF_SCRATCH));
+    const Share share = find_share(p, x.tq, x.G, recip, reinterpret_cast<int64_t*>(smem_raw + L::OFF_SCRATCH));
     const Cursor u = share.at;
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = lds_u32(x.base + OFF_TMEM);
+    const uint32_t tmem = lds_u32(x.base + L::OFF_TMEM);
     bool sound = tmem == 0 && x.base % 1024 == 0;   // (the tiles' swizzle counts from 1 KB boundaries)
 #ifdef KDA_WAIT_TEST
     sound = sound && p.test_skip != -2 - (int)blockIdx.x;
@@ -853,17 +819,13 @@ __global__ void __launch_bounds__(kCodes ? AT_CODES_THREADS : AT_THREADS, 1) att
     }
     bool ok = true;
     // registers a thread: 168 at launch; 208 + 208 + 88 of the 3 x 168 that the block holds
-    // (with codes 128 at launch; 200 + 200 + 56 + 56 of 4 x 128)
     if (warp < 8) {
-        if (kCodes) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-        else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-        ok = softmax_warps(p, maps, x, u, warp >> 2);
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        ok = softmax_warps<kSplit>(p, maps, x, u, warp >> 2);
     } else {
-        if (kCodes) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-        if (warp == 8) ok = load_warp<kCodes>(p, maps, x, u);
-        else if (warp == 9) ok = mma_warp<kCodes>(p, x, u);
-        else if (kCodes && warp >= 12) ok = codes_warps(p, x, u);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == 8) ok = load_warp<kSplit>(p, maps, x, u);
+        else if (warp == 9) ok = mma_warp<kSplit>(p, x, u);
     }
     if (!ok) mx_wind_down();
     tc_fence_before();
@@ -891,7 +853,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParam
         uint32_t status = 0;
         for (int s = lane; s < ctas; s += 32) status |= part.cut[s].status;
         status = __reduce_or_sync(0xffffffffu, status);
-        if (lane == 0) *p.status = status;
+        if (lane == 0) *p.status = p.keep_status ? *p.status | status : status;
         return;
     }
     const Cut c = part.cut[first];
@@ -966,7 +928,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParam
         const int h = c.kh * G + head;
         *reinterpret_cast<uint2*>(p.out.data + q * p.out.row + h * p.out.head + 4 * lane) =
             make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-        if (p.lse && lane == 0) p.lse[q * p.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+        if (p.lse && lane == 0) p.lse[q * p.lse_row + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
     }
 }
 
@@ -976,29 +938,31 @@ size_t attn_workspace_bytes(int64_t, int, int) {
     return CUT_BYTES + ML_BYTES + (size_t)2 * AT_MAX_CTAS * 256 * HD * sizeof(float);
 }
 
-template <bool kCodes>
+template <bool kSplit>
 static cudaError_t launch(const AttnParams& p, cudaStream_t stream) {
     const int G = p.Hq / p.Hk, tq = 128 / G;
     AttnMaps maps;
     memset(&maps, 0, sizeof(maps));
+    const int seqs = p.cache ? p.nseq : 1;
     if (!mx_encode(&maps.q, p.q.data, p.Hq, p.Tq, 1, p.q.head, p.q.row, 0, G, tq) ||
-        (!kCodes && (!mx_encode(&maps.k, p.k, p.Hk, p.Tk, p.cache ? p.nseq : 1, p.k_head, p.k_row, p.k_seq, 1, KB) ||
-                     !mx_encode(&maps.v, p.v, p.Hk, p.Tk, p.cache ? p.nseq : 1, p.v_head, p.v_row, p.v_seq, 1, KB))) ||
+        !mx_encode(&maps.k, p.k, p.Hk, p.Tk, seqs, p.k_head, p.k_row, p.k_seq, 1, KB) ||
+        (kSplit && !mx_encode(&maps.k_low, p.k_low, p.Hk, p.Tk, seqs, p.k_head, p.k_row, p.k_seq, 1, KB)) ||
+        !mx_encode(&maps.v, p.v, p.Hk, p.Tk, seqs, p.v_head, p.v_row, p.v_seq, 1, KB) ||
         !mx_encode_3d(&maps.out, p.out.data, p.Hq, p.Tq, p.out.head, p.out.row, G <= 32 ? G : 1, G <= 32 ? 32 / G : 1))
         return cudaErrorInvalidValue;
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(attn_kernel<kCodes>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)AT_SMEM);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(attn_kernel<kSplit>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<kSplit>::SMEM);
     if (e != cudaSuccess) return e;
     const int ctas = sms < AT_MAX_CTAS ? sms : AT_MAX_CTAS;
-    e = launch_early(attn_kernel<kCodes>, dim3((unsigned)ctas), kCodes ? AT_CODES_THREADS : AT_THREADS, AT_SMEM, stream, p, maps,
+    e = launch_early(attn_kernel<kSplit>, dim3((unsigned)ctas), AT_THREADS, Layout<kSplit>::SMEM, stream, p, maps,
                      ctas > 1 ? ~0ull / (uint64_t)ctas + 1 : (uint64_t)0);
     if (e != cudaSuccess) return e;
     return launch_early(attn_join_kernel, dim3((unsigned)ctas, 256 / JOIN_ROWS), JOIN_THREADS, 0, stream, p, ctas);
 }
 
 cudaError_t launch_attn(const AttnParams& p, cudaStream_t stream) { return launch<false>(p, stream); }
-cudaError_t launch_attn_codes(const AttnParams& p, cudaStream_t stream) { return launch<true>(p, stream); }
+cudaError_t launch_attn_split(const AttnParams& p, cudaStream_t stream) { return launch<true>(p, stream); }
 
 }  // namespace kda

@@ -25,6 +25,7 @@
 // that lies in more than one share leaves unnormalised partial rows in the workspace, and a second, small kernel
 // joins them in the order of the keys.
 
+#include <cuda_fp16.h>
 #include <string.h>
 
 #include "kda_mixer.cuh"
@@ -710,42 +711,175 @@ cudaError_t launch(const QcacheAttnParams& p, int sms, cudaStream_t stream) {
     return e;
 }
 
-}  // namespace
+// ---------------------------------------------------------------- many rows: expanded once, then the tensor cores
+// Many rows read a block of keys many times (a pair of query tiles each), so the codes are expanded once, for some key
+// heads at a time, into the workspace, and the kernel of kda_attn.cu runs on that.
+//   keys     scale code + zero in fp32, as two bf16 terms that both meet the queries: a single rounding of the keys would
+//            move the scores by up to 2^-9 of sum |q k| (measured: results off by 0.0042 of their norm, now 0.0017)
+//   values   in fp16, as are the weights that meet them (11 bits instead of 8: both roundings vanish beside the output's),
+//            a block of 128 scaled by the power of two that brings its largest below 2^(SPLIT_TOP + 1)
+// A CTA takes a block of keys of a head: half a warp a row, a lane eight channels of the key and of the value.  Bound by HBM
+// (144 bytes read and 768 written for each key and head).
+constexpr int EX_THREADS = 256, EX_BLOCK = 128, EX_ROWS = EX_BLOCK * 16 / EX_THREADS;   // rows of a thread
 
-// Few rows: this file's kernel; many: the tensor cores' of kda_attn.cu, which expands the codes on its way.
-static bool few_rows(int64_t Tq, int Hq, int Hk, int nseq) { return Tq * (Hq / Hk) <= 32 * (int64_t)nseq; }
+struct ExpandParams {
+    QcacheView cache;
+    const int64_t* seqlens_k;
+    int64_t S;
+    int head0, heads, blocks;       // blocks of a sequence
+    __nv_bfloat16 *k, *k_low;       // [nseq][heads][blocks * 128][128]
+    __half* v;
+    int* top;                       // [nseq][heads][blocks]
+};
 
-size_t attn_qcache_workspace_bytes(int64_t Tq, int Hq, int Hk, int nseq) {
-    if (few_rows(Tq, Hq, Hk, nseq)) return QS_CUT_BYTES + QS_ML_BYTES + (size_t)2 * QS_MAX_CTAS * QS_MAX_ROWS * HD * sizeof(float);
-    return attn_workspace_bytes(Tq, Hq, Hk);
+__device__ __forceinline__ float code_at(uint32_t x, int bit) { return __uint_as_float((x >> bit & 15u) | 0x4b000000u) - 8388608.f; }
+
+__global__ void __launch_bounds__(EX_THREADS) qcache_expand_kernel(const ExpandParams p) {
+    __shared__ uint32_t most[EX_THREADS / 32];
+    await_stream();
+    const int block = blockIdx.x, h = blockIdx.y, n = blockIdx.z;
+    const int64_t lk = min(max(p.seqlens_k[n], (int64_t)0), p.S);
+    if (block > 0 && (int64_t)block * EX_BLOCK >= lk) return;   // (block 0 is read even if there are no keys)
+    const int lane = threadIdx.x & 15, row0 = threadIdx.x >> 4;
+    const uint8_t* src = p.cache.data + n * p.cache.seq + (int64_t)(p.head0 + h) * p.cache.head;
+    uint32_t kc[EX_ROWS], vc[EX_ROWS];
+    uint4 num[EX_ROWS];
+#pragma unroll
+    for (int i = 0; i < EX_ROWS; ++i) {
+        const int64_t key = (int64_t)block * EX_BLOCK + row0 + i * (EX_THREADS / 16);
+        kc[i] = vc[i] = 0;
+        num[i] = make_uint4(0, 0, 0, 0);
+        if (key < lk) {
+            const uint8_t* at = src + key * p.cache.row;
+            kc[i] = __ldcs(reinterpret_cast<const uint32_t*>(at) + lane);
+            vc[i] = __ldcs(reinterpret_cast<const uint32_t*>(at + 64) + lane);
+            num[i] = *reinterpret_cast<const uint4*>(at + QC_NUMBERS);
+        }
+    }
+    float big = 0.f;
+#pragma unroll
+    for (int i = 0; i < EX_ROWS; ++i)
+        for (const uint32_t w : {num[i].z, num[i].w}) big = fmaxf(big, fmaxf(fabsf(bf16_hi(w)), fabsf(fmaf(15.f, bf16_lo(w), bf16_hi(w)))));
+    uint32_t all = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
+    if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = all;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < EX_THREADS / 32; ++w) all = max(all, most[w]);
+    const int top = max((int)(all >> 23), SPLIT_LEAST);
+    const int64_t unit = (int64_t)n * p.heads + h;
+    if (threadIdx.x == 0) p.top[unit * p.blocks + block] = top;
+    const float lift = __uint_as_float((uint32_t)(127 + SPLIT_TOP + 127 - top) << 23);
+#pragma unroll
+    for (int i = 0; i < EX_ROWS; ++i) {
+        const int64_t at = ((unit * p.blocks + block) * EX_BLOCK + row0 + i * (EX_THREADS / 16)) * HD + 8 * lane;
+        const bool upper = lane >= 8;
+        const uint32_t kn = upper ? num[i].y : num[i].x, vn = upper ? num[i].w : num[i].z;
+        const float ks = bf16_lo(kn), kz = bf16_hi(kn), vs = lift * bf16_lo(vn), vz = lift * bf16_hi(vn);
+        uint32_t hi[4], lo[4], v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float a = fmaf(code_at(kc[i], 8 * e), ks, kz), b = fmaf(code_at(kc[i], 8 * e + 4), ks, kz);
+            hi[e] = pack_bf16x2(a, b);
+            lo[e] = pack_bf16x2(a - bf16_lo(hi[e]), b - bf16_hi(hi[e]));
+            const __half2 y = __floats2half2_rn(fmaf(code_at(vc[i], 8 * e), vs, vz), fmaf(code_at(vc[i], 8 * e + 4), vs, vz));
+            v[e] = *reinterpret_cast<const uint32_t*>(&y);
+        }
+        *reinterpret_cast<uint4*>(p.k + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(p.k_low + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        *reinterpret_cast<uint4*>(p.v + at) = make_uint4(v[0], v[1], v[2], v[3]);
+    }
 }
 
-cudaError_t launch_attn_qcache(const QcacheAttnParams& p, cudaStream_t stream) {
-    if (!few_rows(p.Tq, p.Hq, p.Hk, p.nseq)) {
+}  // namespace
+
+// Few rows: this file's kernel; many: that of kda_attn.cu on expanded keys and values.
+static bool few_rows(int64_t Tq, int Hq, int Hk, int nseq) { return Tq * (Hq / Hk) <= 32 * (int64_t)nseq; }
+
+// Expanded keys and values for as many key heads at a time as fit into 1 GB, one at least.
+constexpr int64_t EX_MOST = 1LL << 30;
+struct Expanded {
+    int64_t blocks, unit;   // of a sequence; bytes of one (sequence, head)
+    int heads;              // at a time
+};
+static Expanded expanded(int64_t S, int Hk, int nseq) {
+    Expanded x;
+    x.blocks = S > 0 ? (S + EX_BLOCK - 1) / EX_BLOCK : 1;
+    x.unit = x.blocks * (3 * EX_BLOCK * HD * 2 + 16);   // (16: a block's exponent, with what keeps the arrays aligned)
+    const int64_t fit = EX_MOST / (x.unit * (nseq > 0 ? nseq : 1));
+    x.heads = (int)(fit < 1 ? 1 : fit < Hk ? fit : Hk);
+    return x;
+}
+
+size_t attn_qcache_workspace_bytes(int64_t Tq, int Hq, int Hk, int nseq, int64_t S) {
+    if (few_rows(Tq, Hq, Hk, nseq)) return QS_CUT_BYTES + QS_ML_BYTES + (size_t)2 * QS_MAX_CTAS * QS_MAX_ROWS * HD * sizeof(float);
+    const Expanded x = expanded(S, Hk, nseq);
+    return attn_workspace_bytes(Tq, Hq, Hk) + 256 + (size_t)(x.unit * nseq * x.heads);
+}
+
+static cudaError_t launch_many_rows(const QcacheAttnParams& p, cudaStream_t stream) {
+    const Expanded x = expanded(p.S, p.Hk, p.nseq);
+    const int G = p.Hq / p.Hk;
+    char* ex = static_cast<char*>(p.workspace) + attn_workspace_bytes(p.Tq, p.Hq, p.Hk);
+    ex += -(uintptr_t)ex & 255;
+    const int64_t rows = x.blocks * EX_BLOCK, units = (int64_t)p.nseq * x.heads;
+    if (p.nseq > 65535) return cudaErrorInvalidValue;
+    for (int h0 = 0; h0 < p.Hk; h0 += x.heads) {
+        const int heads = min(x.heads, p.Hk - h0);
+        ExpandParams e;
+        memset(&e, 0, sizeof(e));
+        e.cache = p.cache;
+        e.seqlens_k = p.seqlens_k;
+        e.S = p.S;
+        e.head0 = h0;
+        e.heads = heads;
+        e.blocks = (int)x.blocks;
+        e.k = reinterpret_cast<__nv_bfloat16*>(ex);
+        e.k_low = e.k + units * rows * HD;
+        e.v = reinterpret_cast<__half*>(e.k_low + units * rows * HD);
+        e.top = reinterpret_cast<int*>(e.v + units * rows * HD);
+        if (p.nseq > 0) {
+            const cudaError_t err = launch_early(qcache_expand_kernel, dim3((unsigned)x.blocks, (unsigned)heads, (unsigned)p.nseq), EX_THREADS, 0, stream, e);
+            if (err != cudaSuccess) return err;
+        }
         AttnParams a;
         memset(&a, 0, sizeof(a));
         a.q = p.q;
+        a.q.data += (int64_t)h0 * G * p.q.head;
         a.out = p.out;
-        a.k = reinterpret_cast<__nv_bfloat16*>(p.cache.data);
-        a.k_seq = p.cache.seq;
-        a.k_row = p.cache.row;
-        a.k_head = p.cache.head;
-        a.lse = p.lse;
+        a.out.data += (int64_t)h0 * G * p.out.head;
+        a.k = e.k;
+        a.k_low = e.k_low;
+        a.v = reinterpret_cast<__nv_bfloat16*>(e.v);
+        a.top = e.top;
+        a.top_blocks = x.blocks;
+        a.k_row = a.v_row = HD;
+        a.k_head = a.v_head = rows * HD;
+        a.k_seq = a.v_seq = rows * HD * heads;
+        a.lse = p.lse ? p.lse + h0 * G : nullptr;
+        a.lse_row = p.Hq;
         a.cu_q = p.cu_q;
         a.seqlens_k = p.seqlens_k;
         a.uniform_q = p.uniform_q;
         a.Tq = p.Tq;
-        a.Tk = p.S;
+        a.Tk = rows;
+        a.keys = p.S;
+        a.keep_status = h0 > 0;
         a.nseq = p.nseq;
-        a.Hq = p.Hq;
-        a.Hk = p.Hk;
+        a.Hq = heads * G;
+        a.Hk = heads;
         a.cache = 1;
         a.scale = p.scale;
         a.status = p.status;
         a.workspace = p.workspace;
         a.test_skip = -1;
-        return launch_attn_codes(a, stream);
+        const cudaError_t err = launch_attn_split(a, stream);
+        if (err != cudaSuccess) return err;
     }
+    return cudaSuccess;
+}
+
+cudaError_t launch_attn_qcache(const QcacheAttnParams& p, cudaStream_t stream) {
+    if (!few_rows(p.Tq, p.Hq, p.Hk, p.nseq)) return launch_many_rows(p, stream);
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);

@@ -35,14 +35,23 @@ struct NormRopeParams {
 struct AttnParams {
     RowsView q, out;
     __nv_bfloat16 *k, *v;
+    // launch_attn_split: the keys are k + k_low, both bf16 with the strides of k, and a block of 128 values is v in fp16 times
+    // 2^(top - 127 - SPLIT_TOP), with its own top[sequence * Hk + head][block], at least SPLIT_LEAST; rows of the last
+    // block past the sequence's keys hold zeros
+    __nv_bfloat16* k_low;
+    const int* top;
+    int64_t top_blocks;
     int64_t k_seq, k_row, k_head;   // strides in elements; k_seq = 0 for packed keys
     int64_t v_seq, v_row, v_head;
-    float* lse;                     // [Tq, Hq] or nullptr
+    float* lse;                     // [Tq, Hq] in rows of lse_row, or nullptr
+    int64_t lse_row;
     const int64_t* cu_q;            // [nseq + 1] or nullptr: uniform_q queries each
     const int64_t* cu_k;            // packed keys: [nseq + 1], or nullptr: one sequence of Tk
     const int64_t* seqlens_k;       // cache: [nseq]
     int64_t uniform_q;
     int64_t Tq, Tk;                 // Tk: packed key rows, or the cache's rows for each sequence
+    int64_t keys;                   // a cache: most keys that a sequence may have
+    int keep_status;                // bits are added to the status word (a call of several launches)
     int nseq, Hq, Hk;
     int cache;
     float scale;
@@ -50,6 +59,8 @@ struct AttnParams {
     void* workspace;                // behind the status word
     int test_skip;                  // the test-only build: the share b that withholds an arrival, -2 - b: that finds itself unsound; -1 for none
 };
+
+constexpr int SPLIT_TOP = 13, SPLIT_LEAST = 27;
 
 struct LinParams {
     RowsView q, k, v, out;
@@ -121,13 +132,13 @@ struct ResidualNormParams {
 
 cudaError_t launch_qcache_append(const QcacheAppendParams& p, cudaStream_t stream);
 cudaError_t launch_attn_qcache(const QcacheAttnParams& p, cudaStream_t stream);
-size_t attn_qcache_workspace_bytes(int64_t Tq, int Hq, int Hk, int nseq);
+size_t attn_qcache_workspace_bytes(int64_t Tq, int Hq, int Hk, int nseq, int64_t S);
 cudaError_t launch_gated_norm(const GatedNormParams& p, cudaStream_t stream);
 cudaError_t launch_residual_norm(const ResidualNormParams& p, cudaStream_t stream);
 cudaError_t launch_norm_rope(const NormRopeParams& p, cudaStream_t stream);
 cudaError_t launch_attn(const AttnParams& p, cudaStream_t stream);
-// The same over a cache in 4 bits: p.k its bytes, p.k_seq, p.k_row and p.k_head strides in bytes, p.v not used.
-cudaError_t launch_attn_codes(const AttnParams& p, cudaStream_t stream);
+// The same over expanded keys and values (k, k_low and v of AttnParams).
+cudaError_t launch_attn_split(const AttnParams& p, cudaStream_t stream);
 size_t attn_workspace_bytes(int64_t Tq, int Hq, int Hk);
 cudaError_t launch_lin_fwd(const LinParams& p, cudaStream_t stream);
 size_t lin_workspace_bytes(int64_t T_total, int H, int nseq);

@@ -445,6 +445,8 @@ kda_status kda_attn_fwd(const kda_view* q, const kda_view* k, const kda_view* v,
     p.v_head = vr.head;
     p.v_seq = !cache ? 0 : v->shape[0] > 1 ? v->stride[0] : vr.row * Tk;
     p.lse = present(lse) ? static_cast<float*>(lse->data) : nullptr;
+    p.lse_row = Hq;
+    p.keys = Tk;
     p.cu_q = present(cu_seqlens_q) ? static_cast<const int64_t*>(cu_seqlens_q->data) : nullptr;
     p.uniform_q = nseq > 0 ? Tq / nseq : 0;
     p.cu_k = cache ? nullptr : present(cu_seqlens_k) ? static_cast<const int64_t*>(cu_seqlens_k->data) : p.cu_q;
@@ -635,9 +637,9 @@ kda_status kda_qcache_append(const kda_view* k, const kda_view* v, const kda_vie
     return KDA_OK;
 }
 
-size_t kda_attn_qcache_workspace_size(int64_t Tq, int Hq, int Hk, int N) {
-    if (Tq < 0 || Hq < 1 || Hk < 1 || Hq % Hk != 0 || N < 0) return 0;
-    return kHeaderBytes + kda::attn_qcache_workspace_bytes(Tq, Hq, Hk, N);
+size_t kda_attn_qcache_workspace_size(int64_t Tq, int Hq, int Hk, int N, int64_t S) {
+    if (Tq < 0 || Tq > (1 << 30) || Hq < 1 || Hk < 1 || Hq % Hk != 0 || N < 0 || S < 0 || S > (1 << 30)) return 0;
+    return kHeaderBytes + kda::attn_qcache_workspace_bytes(Tq, Hq, Hk, N, S);
 }
 
 kda_status kda_attn_qcache_fwd(const kda_view* q, const kda_view* cache, float scale, const kda_view* out,
@@ -670,7 +672,7 @@ kda_status kda_attn_qcache_fwd(const kda_view* q, const kda_view* cache, float s
         if (present(t) && (overlap(extent(out), extent(t)) || (present(lse) && overlap(extent(lse), extent(t)))))
             return fail(KDA_ERR_ALIAS, "out or lse overlaps the lengths");
     if (present(lse) && overlap(extent(out), extent(lse))) return fail(KDA_ERR_ALIAS, "out and lse overlap");
-    KDA_TRY(check_workspace(workspace, workspace_bytes, kda_attn_qcache_workspace_size(Tq, (int)Hq, (int)Hk, (int)nseq)));
+    KDA_TRY(check_workspace(workspace, workspace_bytes, kda_attn_qcache_workspace_size(Tq, (int)Hq, (int)Hk, (int)nseq, cache->shape[1])));
     kda::QcacheAttnParams p;
     memset(&p, 0, sizeof(p));
     p.q = rows_view(q, 0);

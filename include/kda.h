@@ -502,9 +502,12 @@ kda_status kda_qcache_append(const kda_view* k, const kda_view* v, const kda_vie
 
 /*
  * Bytes of workspace kda_attn_qcache_fwd needs for Tq query tokens, Hq query heads, Hk key/value heads
- * and N sequences.  Its contents need no initialisation.  Returns 0 for invalid arguments.
+ * and N sequences with room for S keys each.  Its contents need no initialisation.  At present 11 MB where the
+ * sequences have at most 32 (token, head) rows for a key head on average, Tq Hq / Hk <= 32 N.  Beyond that the keys and
+ * values are expanded there, 768 bytes for each row of the cache: for as many key heads at a time as fit into 1 GB (one at
+ * least), and 43 MB.  Returns 0 for invalid arguments.
  */
-size_t kda_attn_qcache_workspace_size(int64_t Tq, int Hq, int Hk, int N);
+size_t kda_attn_qcache_workspace_size(int64_t Tq, int Hq, int Hk, int N, int64_t S);
 
 /*
  * kda_attn_fwd over a cache in 4 bits: the same formulas, masks and errors, with the keys and values that
@@ -514,7 +517,7 @@ size_t kda_attn_qcache_workspace_size(int64_t Tq, int Hq, int Hk, int N);
  *   seqlens_k      int64 [N], sequence n's keys are positions 0 .. seqlens_k[n] - 1
  *   lse            fp32 [Tq, Hq], or NULL/absent
  *   cu_seqlens_q   int64 [N + 1]; NULL/absent: Tq / N queries each
- *   workspace      >= kda_attn_qcache_workspace_size(Tq, Hq, Hk, N) bytes, 256-byte aligned
+ *   workspace      >= kda_attn_qcache_workspace_size(Tq, Hq, Hk, N, S) bytes, 256-byte aligned
  * Cache rows past a sequence's keys are never used, whatever they hold; the scales and zeros inside a
  * sequence are taken to be finite.
  */

@@ -364,7 +364,7 @@ def test_captured_and_replayed(T, lens_k, hq):
     k, v, q = rand(g, T, hk, D), rand(g, T, hk, D), rand(g, T, hq, D)
     lens, cu = i64(lens_k), cu_of(per)
     out = torch.zeros_like(q)
-    ws = torch.empty(kda.kda_attn_qcache_workspace_size(T, hq, hk, n), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(kda.kda_attn_qcache_workspace_size(T, hq, hk, n, 5600), dtype=torch.uint8, device="cuda")
 
     def both(o):
         kda.kda_qcache_append(k, v, cache, lens, cu_seqlens=cu)

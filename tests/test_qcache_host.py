@@ -91,10 +91,10 @@ def test_attention_refusals(lib, over, want):  # noqa: F811
 
 
 def test_attention_workspace_size(lib):  # noqa: F811
-    for bad in ((-1, 8, 2, 1), (1, 0, 1, 1), (1, 8, 0, 1), (1, 8, 3, 1), (1, 8, 2, -1)):
+    for bad in ((-1, 8, 2, 1, 1), (1, 0, 1, 1, 1), (1, 8, 0, 1, 1), (1, 8, 3, 1, 1), (1, 8, 2, -1, 1), (1, 8, 2, 1, -1), (1, 8, 2, 1, 1 << 40)):
         assert kb.kda_attn_qcache_workspace_size(*bad) == 0
-    assert kb.kda_attn_qcache_workspace_size(0, 8, 2, 0) >= 256
-    need = kb.kda_attn_qcache_workspace_size(T, HQ, HK, N)
+    assert kb.kda_attn_qcache_workspace_size(0, 8, 2, 0, 0) >= 256
+    need = kb.kda_attn_qcache_workspace_size(T, HQ, HK, N, S)
     assert attn(lib, nbytes=need - 1) == WORKSPACE
 
 
