@@ -599,14 +599,17 @@ __global__ void __launch_bounds__(QS_THREADS, kN == 1 ? 2 : 1) attn_qcache_kerne
 }
 
 // Joins the partial rows of the tiles that several shares hold (and, the last block, the shares' status bits: one
-// store, so that none is lost).  Block b takes the tile that share b + 1 starts in, if that is the tile's first cut; a
-// warp takes a row, lane l its channels 4 l .. 4 l + 3.
+// store, so that none is lost).  Block (b, y) takes row y of the tile that share b + 1 starts in, if that is the tile's
+// first cut; its warps take the parts in turn, lane l their channels 4 l .. 4 l + 3.  Bound by latency: what it reads
+// is asked for at once (a warp a row, part after part, cost one token over 32,767 keys 6 us more).
 __global__ void __launch_bounds__(QS_THREADS) attn_qcache_join_kernel(const QcacheAttnParams p, int ctas, int rows) {
-    const int first = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = p.Hq / p.Hk;
+    __shared__ float4 sums[QS_WARPS][32];
+    __shared__ float2 refs[QS_WARPS];
+    const int first = blockIdx.x + 1, row = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = p.Hq / p.Hk;
     const QsPartials part = qs_partials(p.workspace);
     await_stream();
     if (first == ctas) {
-        if (warp != 0) return;
+        if (warp != 0 || row != 0) return;
         uint32_t status = 0;
         for (int s = lane; s < ctas; s += 32) status |= part.cut[s].status;
         status = __reduce_or_sync(0xffffffffu, status);
@@ -614,79 +617,80 @@ __global__ void __launch_bounds__(QS_THREADS) attn_qcache_join_kernel(const Qcac
         return;
     }
     const QsCut c = part.cut[first];
+    QsCut before = part.cut[first - 1], e = part.cut[min(first + 1 + lane, ctas - 1)];
     if (c.j == 0) return;   // between two tiles, or nothing to do
+    const int64_t at = (int64_t)c.tile * rows + row;
+    if (at >= (int64_t)c.lq * G) return;
     auto inside = [&](const QsCut& a) { return a.n == c.n && a.kh == c.kh && a.tile == c.tile; };
     int b = first - 1;      // the share before it that is not empty
-    QsCut before = part.cut[b];
     while (b > 0 && before.some == 0) before = part.cut[--b];
     const bool same = inside(before);
     if (same && before.j > 0) return;
     // the parts: share b's last piece, then the first pieces of the shares that start inside the tile (empty ones between)
     int end = first + 1;
     for (;;) {
-        const int s = end + lane;
-        bool past = s >= ctas;
-        if (!past) {
-            const QsCut a = part.cut[s];
-            past = a.some && !(a.j > 0 && inside(a));
-        }
-        const uint32_t at = __ballot_sync(0xffffffffu, past);
-        if (at) {
-            end += __ffs(at) - 1;
+        const uint32_t past = __ballot_sync(0xffffffffu, end + lane >= ctas || (e.some && !(e.j > 0 && inside(e))));
+        if (past) {
+            end += __ffs(past) - 1;
             break;
         }
         end += 32;
+        e = part.cut[min(end + lane, ctas - 1)];
     }
-    auto slot = [&](int s) { return (size_t)(2 * s + (s == b && !same ? 1 : 0)); };
+    auto slot = [&](int s) { return (size_t)(2 * s + (s == b && !same ? 1 : 0)) * QS_MAX_ROWS + row; };
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-    for (int row = warp; row < rows; row += QS_WARPS) {
-        const int64_t at = (int64_t)c.tile * rows + row;
-        if (at >= (int64_t)c.lq * G) return;
-        float m = -INFINITY, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-        for (int s0 = b; s0 < end; s0 += 32) {   // (more than 32 parts: the sums so far are rescaled)
-            const int s = s0 + lane;
-            float2 ml = make_float2(-INFINITY, 0.f);
-            if (s < end && (s == b || part.cut[s].some)) ml = part.ml[slot(s) * QS_MAX_ROWS + row];
-            float top = ml.x;
+    for (int s0 = b + warp; s0 < end; s0 += 4 * QS_WARPS) {
+        float2 ml[4];
+        float4 y[4];
 #pragma unroll
-            for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            top = fmaxf(top, m);
-            const float old = m == -INFINITY ? 0.f : ex2_approx(m - top);
-            m = top;
-            const float w = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);   // (a part that saw no key, or an empty share)
-            l = fmaf(l, old, w * ml.y);
-            o.x *= old, o.y *= old, o.z *= old, o.w *= old;
-            const int n = min(32, end - s0);
-#pragma unroll 1
-            for (int a = 0; a < n; a += 8) {
-                float4 y[8];
-                float f[8];
-#pragma unroll
-                for (int d = 0; d < 8; ++d) {
-                    f[d] = __shfl_sync(0xffffffffu, w, (a + d) & 31);
-                    if (a + d >= n) f[d] = 0.f;
-                    y[d] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (f[d] != 0.f) y[d] = __ldcg(reinterpret_cast<const float4*>(part.o + (slot(s0 + a + d) * QS_MAX_ROWS + row) * 128 + 4 * lane));
-                }
-#pragma unroll
-                for (int d = 0; d < 8; ++d) {
-                    o.x = fmaf(f[d], y[d].x, o.x);
-                    o.y = fmaf(f[d], y[d].y, o.y);
-                    o.z = fmaf(f[d], y[d].z, o.z);
-                    o.w = fmaf(f[d], y[d].w, o.w);
-                }
+        for (int d = 0; d < 4; ++d) {
+            const int s = s0 + d * QS_WARPS;
+            ml[d] = make_float2(-INFINITY, 0.f);
+            y[d] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (s < end && (s == b || part.cut[s].some)) {
+                ml[d] = __ldcg(part.ml + slot(s));
+                y[d] = __ldcg(reinterpret_cast<const float4*>(part.o + slot(s) * 128 + 4 * lane));
             }
         }
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int64_t tok = c.q0 + at / G, head = (int64_t)c.kh * G + at % G;
-        *reinterpret_cast<uint2*>(p.out.data + tok * p.out.row + head * p.out.head + 4 * lane) =
-            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-        if (p.lse && lane == 0) p.lse[tok * p.Hq + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+        for (int d = 0; d < 4; ++d) {
+            if (ml[d].x == -INFINITY) continue;   // a part that saw no key, or none
+            const float top = fmaxf(m, ml[d].x), old = m == -INFINITY ? 0.f : ex2_approx(m - top), w = ex2_approx(ml[d].x - top);
+            m = top;
+            l = fmaf(l, old, w * ml[d].y);
+            o.x = fmaf(o.x, old, w * y[d].x);
+            o.y = fmaf(o.y, old, w * y[d].y);
+            o.z = fmaf(o.z, old, w * y[d].z);
+            o.w = fmaf(o.w, old, w * y[d].w);
+        }
     }
+    sums[warp][lane] = o;
+    if (lane == 0) refs[warp] = make_float2(m, l);
+    __syncthreads();
+    if (warp != 0) return;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < QS_WARPS; ++w) top = fmaxf(top, refs[w].x);
+    l = 0.f;
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < QS_WARPS; ++w) {
+        const float2 r = refs[w];
+        const float4 y = sums[w][lane];
+        const float f = r.x == -INFINITY ? 0.f : ex2_approx(r.x - top);
+        l = fmaf(f, r.y, l);
+        o.x = fmaf(f, y.x, o.x);
+        o.y = fmaf(f, y.y, o.y);
+        o.z = fmaf(f, y.z, o.z);
+        o.w = fmaf(f, y.w, o.w);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int64_t tok = c.q0 + at / G, head = (int64_t)c.kh * G + at % G;
+    *reinterpret_cast<uint2*>(p.out.data + tok * p.out.row + head * p.out.head + 4 * lane) =
+        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (p.lse && lane == 0) p.lse[tok * p.Hq + head] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
 }
 
 // The cache in boxes of 144 bytes x 1 head x `rows` rows.
@@ -707,7 +711,7 @@ cudaError_t launch(const QcacheAttnParams& p, int sms, cudaStream_t stream) {
     const int ctas = min(sms * (kN == 1 ? 2 : 1), QS_MAX_CTAS);
     cudaError_t e = cudaFuncSetAttribute(attn_qcache_kernel<kN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)QsLayout<kN>::BYTES);
     if (e == cudaSuccess) e = launch_early(attn_qcache_kernel<kN>, dim3((unsigned)ctas), QS_THREADS, QsLayout<kN>::BYTES, stream, p, map);
-    if (e == cudaSuccess) e = launch_early(attn_qcache_join_kernel, dim3((unsigned)ctas), QS_THREADS, 0, stream, p, ctas, 8 * kN);
+    if (e == cudaSuccess) e = launch_early(attn_qcache_join_kernel, dim3((unsigned)ctas, (unsigned)(8 * kN)), QS_THREADS, 0, stream, p, ctas, 8 * kN);
     return e;
 }
 
