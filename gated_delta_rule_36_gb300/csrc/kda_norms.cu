@@ -75,93 +75,138 @@ cudaError_t launch_gated(const GatedNormParams& p, cudaStream_t stream) {
 }
 
 // ---------------------------------------------------------------- between two blocks
-// kThreads threads take a token's row, each with kChunks groups of 8 elements, and hold it in
-// registers from the loads to the stores.
-template <int kThreads>
+// A block takes a token's row, each thread kChunks groups of 8 elements (where a warp is enough: a warp a row, four of them a
+// block), and holds it in registers from the loads to the stores; the next row that it takes is loaded meanwhile.
+constexpr int RN_WARP_ROWS = 4;
+
+template <bool kWarp>
 __device__ __forceinline__ float row_sum(float x, float* shared) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    if (kThreads == 32) return x;
+    if (kWarp) return x;
     if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = x;
     __syncthreads();
-    x = 0.f;
+    const int from = threadIdx.x & 15;   // (at most 16 warps; both halves of a warp add them up)
+    x = from < (int)(blockDim.x >> 5) ? shared[from] : 0.f;
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) x += shared[i];
+    for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
 }
 
-template <int kThreads, int kChunks, bool kF32>
-__global__ void __launch_bounds__(kThreads < 128 ? 128 : kThreads) residual_norm_kernel(const ResidualNormParams p) {
-    __shared__ float shared[2][32];
-    constexpr int kRowsHere = kThreads < 128 ? 128 / kThreads : 1;
-    await_stream();
-    const int tid = threadIdx.x % kThreads;
-    const int64_t t = (int64_t)blockIdx.x * kRowsHere + threadIdx.x / kThreads;
-    if (t >= p.tokens) return;   // (whole warps, and whole blocks where a row takes more than one)
-    float r[kChunks][8], u[kChunks][8];
-    float ss = 0.f;
+template <int kChunks, bool kF32, bool kGate>
+struct RawRow {
+    uint4 y[kChunks], r[kChunks][kF32 ? 2 : 1], g[kGate ? kChunks : 1];
+    __device__ __forceinline__ void load(const ResidualNormParams& p, int64_t t, int tid, int threads) {
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-        const int at = 8 * (tid + c * kThreads);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) r[c][j] = u[c][j] = 0.f;
-        if (at >= p.dim) continue;
-        if (kF32) load8(static_cast<const float*>(p.residual) + t * p.residual_row + at, r[c]);
-        else unpack8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.residual) + t * p.residual_row + at), r[c]);
-        if (p.y) unpack8(*reinterpret_cast<const uint4*>(p.y + t * p.y_row + at), u[c]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(u[c][j], u[c][j], ss);
-    }
-    const float mean = 1.f / (float)p.dim;
-    float f = p.scale;
-    if (p.post_weight) f *= rsqrtf(row_sum<kThreads>(ss, shared[0]) * mean + p.eps);
-    ss = 0.f;
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-        const int at = 8 * (tid + c * kThreads);
-        if (at >= p.dim) continue;
-        if (p.y) {
-            float w[8], g[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = g[j] = 1.f;
-            if (p.post_weight) load8(p.post_weight + at, w);
-            if (p.gate) unpack8(*reinterpret_cast<const uint4*>(p.gate + t * p.gate_row + at), g);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) r[c][j] = fmaf(u[c][j] * f, w[j] * g[j], r[c][j]);
-        }
-        if (p.residual_out) {
+        for (int c = 0; c < kChunks; ++c) {
+            const int at = 8 * (tid + c * threads);
+            y[c] = r[c][0] = make_uint4(0, 0, 0, 0);
+            if (kF32) r[c][kF32 ? 1 : 0] = make_uint4(0, 0, 0, 0);
+            if (t >= p.tokens || at >= p.dim) continue;
+            if (p.y) y[c] = __ldcs(reinterpret_cast<const uint4*>(p.y + t * p.y_row + at));
             if (kF32) {
-                float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.residual_out) + t * p.residual_out_row + at);
-                o[0] = make_float4(r[c][0], r[c][1], r[c][2], r[c][3]);
-                o[1] = make_float4(r[c][4], r[c][5], r[c][6], r[c][7]);
+                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const float*>(p.residual) + t * p.residual_row + at);
+                r[c][0] = __ldcs(src);
+                r[c][kF32 ? 1 : 0] = __ldcs(src + 1);
             } else {
-                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.residual_out) + t * p.residual_out_row + at) = pack8(r[c]);
+                r[c][0] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.residual) + t * p.residual_row + at));
             }
+            if (kGate) g[c] = *reinterpret_cast<const uint4*>(p.gate + t * p.gate_row + at);   // (it may be one row for all)
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(r[c][j], r[c][j], ss);
     }
-    const float f2 = rsqrtf(row_sum<kThreads>(ss, shared[1]) * mean + p.eps);
+};
+
+template <int kChunks, bool kF32, bool kGate, bool kWarp, int kMost>
+__global__ void __launch_bounds__(kMost) residual_norm_kernel(const ResidualNormParams p) {
+    __shared__ float shared[3][32];
+    await_stream();
+    const int threads = kWarp ? 32 : blockDim.x, tid = kWarp ? threadIdx.x & 31 : threadIdx.x;
+    const int64_t stride = (int64_t)gridDim.x * (kWarp ? RN_WARP_ROWS : 1);
+    int64_t t = kWarp ? (int64_t)blockIdx.x * RN_WARP_ROWS + (threadIdx.x >> 5) : blockIdx.x;
+    const float mean = 1.f / (float)p.dim;
+    RawRow<kChunks, kF32, kGate> next;
+    next.load(p, t, tid, threads);
+#pragma unroll 1
+    for (int parity = 1; t < p.tokens; t += stride, parity ^= 3) {
+        const RawRow<kChunks, kF32, kGate> row = next;
+        next.load(p, t + stride, tid, threads);
+        float f = p.scale;
+        if (p.post_weight) {
+            float ss = 0.f;
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-        const int at = 8 * (tid + c * kThreads);
-        if (at >= p.dim) continue;
-        float w[8];
+            for (int c = 0; c < kChunks; ++c) {
+                float u[8];
+                unpack8(row.y[c], u);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = 1.f;
-        if (p.pre_weight) load8(p.pre_weight + at, w);
+                for (int j = 0; j < 8; ++j) ss = fmaf(u[j], u[j], ss);
+            }
+            f *= rsqrtf(row_sum<kWarp>(ss, shared[0]) * mean + p.eps);
+        }
+        float r[kChunks][8];
+        float ss = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] *= r[c][j] * f2;
-        *reinterpret_cast<uint4*>(p.out + t * p.out_row + at) = pack8(w);
+        for (int c = 0; c < kChunks; ++c) {
+            const int at = 8 * (tid + c * threads);
+            if (kF32) {
+                const uint4 a = row.r[c][0], b = row.r[c][kF32 ? 1 : 0];
+                r[c][0] = __uint_as_float(a.x); r[c][1] = __uint_as_float(a.y); r[c][2] = __uint_as_float(a.z); r[c][3] = __uint_as_float(a.w);
+                r[c][4] = __uint_as_float(b.x); r[c][5] = __uint_as_float(b.y); r[c][6] = __uint_as_float(b.z); r[c][7] = __uint_as_float(b.w);
+            } else {
+                unpack8(row.r[c][0], r[c]);
+            }
+            if (at >= p.dim) continue;
+            if (p.y) {
+                float u[8], w[8], g[8];
+                unpack8(row.y[c], u);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = 1.f;
+                if (p.post_weight) load8(p.post_weight + at, w);
+                if (kGate) {
+                    unpack8(row.g[c], g);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) w[j] *= g[j];
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) r[c][j] = fmaf(u[j] * f, w[j], r[c][j]);
+            }
+            if (p.residual_out) {
+                if (kF32) {
+                    float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.residual_out) + t * p.residual_out_row + at);
+                    __stcs(o, make_float4(r[c][0], r[c][1], r[c][2], r[c][3]));
+                    __stcs(o + 1, make_float4(r[c][4], r[c][5], r[c][6], r[c][7]));
+                } else {
+                    __stcs(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.residual_out) + t * p.residual_out_row + at), pack8(r[c]));
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ss = fmaf(r[c][j], r[c][j], ss);
+        }
+        const float f2 = rsqrtf(row_sum<kWarp>(ss, shared[parity]) * mean + p.eps);   // (a buffer of its own for two rows in turn)
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            const int at = 8 * (tid + c * threads);
+            if (at >= p.dim) continue;
+            float w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = 1.f;
+            if (p.pre_weight) load8(p.pre_weight + at, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] *= r[c][j] * f2;
+            __stcs(reinterpret_cast<uint4*>(p.out + t * p.out_row + at), pack8(w));
+        }
     }
 }
 
-template <int kThreads, int kChunks>
-cudaError_t launch_residual(const ResidualNormParams& p, cudaStream_t stream) {
-    constexpr int block = kThreads < 128 ? 128 : kThreads;
-    const int64_t blocks = (p.tokens * kThreads + block - 1) / block;
-    return launch_early(p.f32 ? residual_norm_kernel<kThreads, kChunks, true> : residual_norm_kernel<kThreads, kChunks, false>,
-                        dim3((unsigned)blocks), block, 0, stream, p);
+template <int kChunks, bool kWarp, int kMost>
+cudaError_t launch_residual(const ResidualNormParams& p, int sms, cudaStream_t stream) {
+    const int groups = p.dim / 8, threads = kWarp ? 32 * RN_WARP_ROWS : (groups + 32 * kChunks - 1) / (32 * kChunks) * 32;
+    void (*const kernel)(ResidualNormParams) = p.f32 ? (p.gate ? residual_norm_kernel<kChunks, true, true, kWarp, kMost> : residual_norm_kernel<kChunks, true, false, kWarp, kMost>)
+                                                     : (p.gate ? residual_norm_kernel<kChunks, false, true, kWarp, kMost> : residual_norm_kernel<kChunks, false, false, kWarp, kMost>);
+    int per = 1;
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, 0);
+    if (e != cudaSuccess) return e;
+    const int64_t blocks = kWarp ? (p.tokens + RN_WARP_ROWS - 1) / RN_WARP_ROWS : p.tokens, most = (int64_t)sms * per;
+    return launch_early(kernel, dim3((unsigned)(blocks < most ? blocks : most)), threads, 0, stream, p);
 }
 
 }  // namespace
@@ -174,13 +219,15 @@ cudaError_t launch_gated_norm(const GatedNormParams& p, cudaStream_t stream) {
 
 cudaError_t launch_residual_norm(const ResidualNormParams& p, cudaStream_t stream) {
     if (p.tokens == 0) return cudaSuccess;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
     const int groups = p.dim / 8;
-    if (groups <= 32) return launch_residual<32, 1>(p, stream);
-    if (groups <= 128) return launch_residual<128, 1>(p, stream);
-    if (groups <= 256) return launch_residual<256, 1>(p, stream);
-    if (groups <= 512) return launch_residual<512, 1>(p, stream);
-    if (groups <= 1024) return launch_residual<512, 2>(p, stream);
-    return launch_residual<1024, 2>(p, stream);
+    if (groups <= 32) return launch_residual<1, true, 128>(p, sms, stream);
+    if (groups <= 128) return launch_residual<1, false, 128>(p, sms, stream);
+    if (groups <= 512) return launch_residual<2, false, 256>(p, sms, stream);
+    return launch_residual<4, false, 512>(p, sms, stream);
 }
 
 }  // namespace kda

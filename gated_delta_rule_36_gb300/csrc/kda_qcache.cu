@@ -1,14 +1,17 @@
 // New keys and values into a cache held in 4 bits (the row's layout: include/kda.h).
 //   zero = min x, scale = bf16((max x - min x) / 15), code = (x - zero) / scale to the nearest, ties to even
-// over each 64 channels.  A warp takes a (token, head): its lower half the key, its upper half the value,
-// 8 channels a lane; minimum and maximum are three shuffles.
+// over each 64 channels.  A warp takes a token's heads, one after another: its lower half the key, its upper half the
+// value, 8 channels a lane; minimum and maximum travel together as a pair of bf16 numbers, three shuffles.
 //
 // The codes are those of exact arithmetic.  The scale is: two bf16 numbers and a quotient by 15 cannot come
 // so close to the middle of two bf16 numbers, without lying on it, that the two fp32 roundings decide.  For
-// the codes the quotient rounds right as long as the difference is exact (a scale has 8 bits, a border between
-// codes 5, so the border times the scale has 13, and a quotient of 24 bits is never moved onto it).  The
-// difference is inexact where the two numbers are more than 16 binades apart; it is then rounded to odd, which
-// keeps it on its side of every number of 13 bits.
+// the codes a correctly rounded quotient rounds right as long as the difference is exact (a scale has 8 bits, a border between
+// codes 5, so the border times the scale has 13, and a quotient of 24 bits is never moved onto it).  The quotient is made from
+// the reciprocal and one correction by its remainder, which is correctly rounded where nothing leaves fp32's range
+// (Markstein's theorem); so the usual path asks for scales within 2^-60 and 2^60 and for numbers that are zero or at most 15
+// binades below the largest, which makes the differences exact.  Other rows go a longer way: division,
+// differences rounded to odd (which keeps them on their side of every number of 13 bits), and halves where the
+// range passes fp32's.
 #include "kda_qcache.cuh"
 
 namespace kda {
@@ -23,7 +26,33 @@ __device__ __forceinline__ float add_to_odd(float a, float b) {
     return err != 0.f && !(i & 1) ? __int_as_float(i + (err > 0.f ? 1 : -1)) : s;
 }
 
-__global__ void __launch_bounds__(QA_THREADS) qcache_append_kernel(const QcacheAppendParams p) {
+// The long way: codes of one lane's eight numbers, one in each four bits, for any finite numbers.
+__device__ __noinline__ uint32_t codes_of_any(const uint4 raw, float lo, bool wide, float scale) {
+    const float f = wide ? 0.5f : 1.f, step = scale * f;
+    const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
+    uint32_t word = 0;
+#pragma unroll 1
+    for (int j = 0; j < 8; ++j) {
+        const float x = j & 1 ? bf16_hi(in[j >> 1]) : bf16_lo(in[j >> 1]);
+        const float d = add_to_odd(x * f, -lo * f);
+        const float c = step > 0.f ? fminf(rintf(d / step), 15.f) : 0.f;
+        word |= (uint32_t)c << (4 * j);
+    }
+    return word;
+}
+
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 m = __hmin2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&m);
+}
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&m);
+}
+
+// kHeads: heads of a token that a warp takes, all loaded at once
+template <int kHeads>
+__global__ void __launch_bounds__(QA_THREADS) qcache_append_kernel(const QcacheAppendParams p, int groups) {
     await_stream();
     const int lane = threadIdx.x & 31, half = lane >> 4;
     const int64_t item = ((int64_t)blockIdx.x * QA_THREADS + threadIdx.x) >> 5;
@@ -34,11 +63,14 @@ __global__ void __launch_bounds__(QA_THREADS) qcache_append_kernel(const QcacheA
         const bool bad = c0 < 0 || (n == 0 && c0 != 0) || c1 < c0 || c1 > p.T || s > p.S || s < c1 - c0;
         if (bad && p.status) atomicOr(p.status, KDA_DEVERR_CU_SEQLENS);
     }
-    const int64_t t = item / p.Hk;
-    const int h = (int)(item - t * p.Hk);
+    const int64_t t = item / groups;
     if (t >= p.T) return;
+    const int h0 = (int)(item - t * groups) * kHeads, heads = min(p.Hk - h0, kHeads);
     const RowsView& in = half ? p.v : p.k;
-    const uint4 raw = *reinterpret_cast<const uint4*>(in.data + t * in.row + h * in.head + 8 * (lane & 15));
+    const __nv_bfloat16* src = in.data + t * in.row + h0 * in.head + 8 * (lane & 15);
+    uint4 raws[kHeads];
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) raws[i] = i < heads ? __ldcs(reinterpret_cast<const uint4*>(src + i * in.head)) : make_uint4(0, 0, 0, 0);
     int n;
     int64_t c0, c1;
     if (p.cu) {
@@ -52,56 +84,79 @@ __global__ void __launch_bounds__(QA_THREADS) qcache_append_kernel(const QcacheA
     }
     const int64_t s = p.seqlens_k[n];
     if (c0 < 0 || (n == 0 && c0 != 0) || t < c0 || t >= c1 || c1 > p.T || s > p.S || s < c1 - c0) return;
-    const int64_t pos = s - (c1 - t);
-
-    float x[8] = {bf16_lo(raw.x), bf16_hi(raw.x), bf16_lo(raw.y), bf16_hi(raw.y), bf16_lo(raw.z), bf16_hi(raw.z), bf16_lo(raw.w), bf16_hi(raw.w)};
-    float lo = x[0], hi = x[0];
-    bool finite = true;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        lo = fminf(lo, x[j]);
-        hi = fmaxf(hi, x[j]);
-        finite &= fabsf(x[j]) < INFINITY;
-    }
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    }
-    finite = (__ballot_sync(0xffffffffu, finite) >> (lane & 24) & 0xffu) == 0xffu;
-    lo += 0.f;   // (-0 and 0 are one zero)
-    const bool wide = hi - lo == INFINITY;   // the range passes fp32's: everything halved
-    const float f = wide ? 0.5f : 1.f;
-    const float range = hi * f - lo * f;
-    const uint32_t sz = finite ? pack_bf16x2(wide ? range / 7.5f : range / 15.f, lo) : 0x7fc07fc0u;
-    const float scale = bf16_lo(sz), zero = bf16_hi(sz), step = scale * f;
-    uint32_t word = 0;
-    float y[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float d = add_to_odd(x[j] * f, -lo * f);
-        const float c = step > 0.f ? fminf(rintf(d / step), 15.f) : 0.f;
-        word |= (uint32_t)c << (4 * j);
-        y[j] = fmaf(c, scale, zero);
-    }
-    uint8_t* row = p.cache.data + n * p.cache.seq + pos * p.cache.row + h * p.cache.head;
-    *reinterpret_cast<uint32_t*>(row + 4 * lane) = word;
-    if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(row + QC_NUMBERS + (lane >> 1)) = sz;
+    uint8_t* row = p.cache.data + n * p.cache.seq + (s - (c1 - t)) * p.cache.row + h0 * p.cache.head;
     const RowsView& out = half ? p.v_out : p.k_out;
-    if (out.data)
-        *reinterpret_cast<uint4*>(out.data + t * out.row + h * out.head + 8 * (lane & 15)) =
-            make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+    __nv_bfloat16* dst = out.data ? out.data + t * out.row + h0 * out.head + 8 * (lane & 15) : nullptr;
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+        if (i >= heads) break;
+        const uint4 raw = raws[i];
+        const uint32_t l2 = min2(min2(raw.x, raw.y), min2(raw.z, raw.w)), h2 = max2(max2(raw.x, raw.y), max2(raw.z, raw.w));
+        // (the smallest, minus the largest) in one register
+        uint32_t both = __byte_perm(min2(l2, l2 >> 16), max2(h2, h2 >> 16) ^ 0x8000u, 0x5410);
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) both = min2(both, __shfl_xor_sync(0xffffffffu, both, o));
+        const float lo = bf16_lo(both) + 0.f, hi = -bf16_hi(both);   // (-0 and 0 are one zero)
+        float x[8] = {bf16_lo(raw.x), bf16_hi(raw.x), bf16_lo(raw.y), bf16_hi(raw.y), bf16_lo(raw.z), bf16_hi(raw.z), bf16_lo(raw.w), bf16_hi(raw.w)};
+        const float least = 0x1p-15f * fmaxf(fabsf(lo), fabsf(hi));
+        bool finite = true, plain = true;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            finite &= fabsf(x[j]) < INFINITY;
+            plain &= fabsf(x[j]) >= least || x[j] == 0.f;
+        }
+        finite = (__ballot_sync(0xffffffffu, finite) >> (lane & 24) & 0xffu) == 0xffu;
+        const bool wide = hi - lo == INFINITY;   // the range passes fp32's: everything halved
+        const uint32_t sz = finite ? pack_bf16x2(wide ? (hi * 0.5f - lo * 0.5f) / 7.5f : (hi - lo) / 15.f, lo) : 0x7fc07fc0u;
+        const float scale = bf16_lo(sz), zero = bf16_hi(sz);
+        plain &= finite && scale >= 0x1p-60f && scale <= 0x1p60f;
+        uint32_t word;
+        if (__all_sync(0xffffffffu, plain)) {
+            const float r = 1.f / scale;
+            uint32_t sum = 0;
+#pragma unroll
+            for (int j = 7; j >= 0; --j) {
+                const float d = x[j] - lo, q0 = d * r, q = fmaf(fmaf(-q0, scale, d), r, q0);
+                sum = sum * 16 + __float_as_uint(q + 12582912.f);   // (2^23 + 2^22: the last bits are the rounded quotient)
+            }
+            word = sum - 0x4b400000u * 0x11111111u;
+        } else {
+            word = codes_of_any(raw, lo, wide, scale);
+        }
+        *reinterpret_cast<uint32_t*>(row + i * p.cache.head + 4 * lane) = word;
+        if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(row + i * p.cache.head + QC_NUMBERS + (lane >> 1)) = sz;
+        if (dst) {
+            uint32_t y[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float a = __uint_as_float((word >> (8 * j) & 15u) | 0x4b000000u) - 8388608.f, b = __uint_as_float((word >> (8 * j + 4) & 15u) | 0x4b000000u) - 8388608.f;
+                y[j] = pack_bf16x2(fmaf(a, scale, zero), fmaf(b, scale, zero));
+            }
+            __stcs(reinterpret_cast<uint4*>(dst + i * out.head), make_uint4(y[0], y[1], y[2], y[3]));
+        }
+    }
+}
+
+template <int kHeads>
+cudaError_t launch(const QcacheAppendParams& p, cudaStream_t stream) {
+    const int groups = (p.Hk + kHeads - 1) / kHeads;
+    int64_t blocks = (p.T * groups * 32 + QA_THREADS - 1) / QA_THREADS;
+    if (blocks == 0) blocks = 1;   // (the lengths are checked all the same)
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    return launch_early(qcache_append_kernel<kHeads>, dim3((unsigned)blocks), QA_THREADS, 0, stream, p, groups);
 }
 
 }  // namespace
 
 cudaError_t launch_qcache_append(const QcacheAppendParams& p, cudaStream_t stream) {
     if (p.nseq == 0) return cudaSuccess;
-    const int64_t rows = p.T * p.Hk;
-    int64_t blocks = (rows * 32 + QA_THREADS - 1) / QA_THREADS;
-    if (blocks == 0) blocks = 1;   // (the lengths are checked all the same)
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    return launch_early(qcache_append_kernel, dim3((unsigned)blocks), QA_THREADS, 0, stream, p);
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    // four heads a warp once that still gives every SM 16 warps, else one, for the latency of small calls
+    if (p.T * p.Hk >= (int64_t)sms * 16 * 4) return launch<4>(p, stream);
+    return launch<1>(p, stream);
 }
 
 }  // namespace kda
