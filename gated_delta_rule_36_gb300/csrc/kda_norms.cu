@@ -202,10 +202,13 @@ cudaError_t launch_residual(const ResidualNormParams& p, int sms, cudaStream_t s
     const int groups = p.dim / 8, threads = kWarp ? 32 * RN_WARP_ROWS : (groups + 32 * kChunks - 1) / (32 * kChunks) * 32;
     void (*const kernel)(ResidualNormParams) = p.f32 ? (p.gate ? residual_norm_kernel<kChunks, true, true, kWarp, kMost> : residual_norm_kernel<kChunks, true, false, kWarp, kMost>)
                                                      : (p.gate ? residual_norm_kernel<kChunks, false, true, kWarp, kMost> : residual_norm_kernel<kChunks, false, false, kWarp, kMost>);
+    const int64_t blocks = kWarp ? (p.tokens + RN_WARP_ROWS - 1) / RN_WARP_ROWS : p.tokens;
     int per = 1;
-    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, 0);
-    if (e != cudaSuccess) return e;
-    const int64_t blocks = kWarp ? (p.tokens + RN_WARP_ROWS - 1) / RN_WARP_ROWS : p.tokens, most = (int64_t)sms * per;
+    if (blocks > sms) {
+        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, 0);
+        if (e != cudaSuccess) return e;
+    }
+    const int64_t most = (int64_t)sms * per;
     return launch_early(kernel, dim3((unsigned)(blocks < most ? blocks : most)), threads, 0, stream, p);
 }
 

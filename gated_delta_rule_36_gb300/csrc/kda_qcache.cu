@@ -6,9 +6,10 @@
 // The codes are those of exact arithmetic.  The scale is: two bf16 numbers and a quotient by 15 cannot come
 // so close to the middle of two bf16 numbers, without lying on it, that the two fp32 roundings decide.  For
 // the codes a correctly rounded quotient rounds right as long as the difference is exact (a scale has 8 bits, a border between
-// codes 5, so the border times the scale has 13, and a quotient of 24 bits is never moved onto it).  The quotient is made from
-// the reciprocal and one correction by its remainder, which is correctly rounded where nothing leaves fp32's range
-// (Markstein's theorem); so the usual path asks for scales within 2^-60 and 2^60 and for numbers that are zero or at most 15
+// codes 5, so the border times the scale has 13, and a quotient of 24 bits is never moved onto it).  Both quotients are made
+// from an approximate reciprocal and one correction by the remainder, which fma gives exactly: what is left then is some 2^-22 of the quotient's
+// last place, and a quotient by a number of 8 bits is either on the middle of two neighbours or 2^-9 of a place away from it.
+// That asks for scales within 2^-60 and 2^60, and for numbers that are zero or at most 15
 // binades below the largest, which makes the differences exact.  Other rows go a longer way: division,
 // differences rounded to odd (which keeps them on their side of every number of 13 bits), and halves where the
 // range passes fp32's.
@@ -42,11 +43,11 @@ __device__ __noinline__ uint32_t codes_of_any(const uint4 raw, float lo, bool wi
 }
 
 __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
-    const __nv_bfloat162 m = __hmin2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    const __nv_bfloat162 m = __hmin2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
     return *reinterpret_cast<const uint32_t*>(&m);
 }
 __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
-    const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    const __nv_bfloat162 m = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
     return *reinterpret_cast<const uint32_t*>(&m);
 }
 
@@ -96,23 +97,25 @@ __global__ void __launch_bounds__(QA_THREADS) qcache_append_kernel(const QcacheA
         uint32_t both = __byte_perm(min2(l2, l2 >> 16), max2(h2, h2 >> 16) ^ 0x8000u, 0x5410);
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) both = min2(both, __shfl_xor_sync(0xffffffffu, both, o));
-        const float lo = bf16_lo(both) + 0.f, hi = -bf16_hi(both);   // (-0 and 0 are one zero)
-        float x[8] = {bf16_lo(raw.x), bf16_hi(raw.x), bf16_lo(raw.y), bf16_hi(raw.y), bf16_lo(raw.z), bf16_hi(raw.z), bf16_lo(raw.w), bf16_hi(raw.w)};
-        const float least = 0x1p-15f * fmaxf(fabsf(lo), fabsf(hi));
-        bool finite = true, plain = true;
+        const float lo = bf16_lo(both) + 0.f, hi = -bf16_hi(both);   // (-0 and 0 are one zero; a NaN makes both NaN)
+        const float most = fmaxf(fabsf(lo), fabsf(hi));
+        const bool finite = fabsf(lo) < INFINITY && fabsf(hi) < INFINITY;
+        // all eight numbers zero or at least 2^-15 of the largest
+        const __nv_bfloat162 least = __float2bfloat162_rn(0x1p-15f * most);
+        uint32_t plain2 = 0xffffffffu;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            finite &= fabsf(x[j]) < INFINITY;
-            plain &= fabsf(x[j]) >= least || x[j] == 0.f;
+        for (const uint32_t w : {raw.x, raw.y, raw.z, raw.w}) {
+            const uint32_t m = w & 0x7fff7fffu;
+            const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&m);
+            plain2 &= __hge2_mask(v, least) | __heq2_mask(v, __float2bfloat162_rn(0.f));
         }
-        finite = (__ballot_sync(0xffffffffu, finite) >> (lane & 24) & 0xffu) == 0xffu;
-        const bool wide = hi - lo == INFINITY;   // the range passes fp32's: everything halved
-        const uint32_t sz = finite ? pack_bf16x2(wide ? (hi * 0.5f - lo * 0.5f) / 7.5f : (hi - lo) / 15.f, lo) : 0x7fc07fc0u;
-        const float scale = bf16_lo(sz), zero = bf16_hi(sz);
-        plain &= finite && scale >= 0x1p-60f && scale <= 0x1p60f;
+        const float range = hi - lo, by15 = range * (1.f / 15.f);
+        uint32_t sz = pack_bf16x2(fmaf(fmaf(-by15, 15.f, range), 1.f / 15.f, by15), lo);
+        const bool plain = plain2 == 0xffffffffu && finite && bf16_lo(sz) >= 0x1p-60f && bf16_lo(sz) <= 0x1p60f;
         uint32_t word;
         if (__all_sync(0xffffffffu, plain)) {
-            const float r = 1.f / scale;
+            const float scale = bf16_lo(sz), r = rcp_approx(scale);
+            const float x[8] = {bf16_lo(raw.x), bf16_hi(raw.x), bf16_lo(raw.y), bf16_hi(raw.y), bf16_lo(raw.z), bf16_hi(raw.z), bf16_lo(raw.w), bf16_hi(raw.w)};
             uint32_t sum = 0;
 #pragma unroll
             for (int j = 7; j >= 0; --j) {
@@ -121,11 +124,14 @@ __global__ void __launch_bounds__(QA_THREADS) qcache_append_kernel(const QcacheA
             }
             word = sum - 0x4b400000u * 0x11111111u;
         } else {
-            word = codes_of_any(raw, lo, wide, scale);
+            const bool wide = range == INFINITY;   // the range passes fp32's: everything halved
+            sz = finite ? pack_bf16x2(wide ? (hi * 0.5f - lo * 0.5f) / 7.5f : range / 15.f, lo) : 0x7fc07fc0u;
+            word = codes_of_any(raw, lo, wide, bf16_lo(sz));
         }
         *reinterpret_cast<uint32_t*>(row + i * p.cache.head + 4 * lane) = word;
         if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(row + i * p.cache.head + QC_NUMBERS + (lane >> 1)) = sz;
         if (dst) {
+            const float scale = bf16_lo(sz), zero = bf16_hi(sz);
             uint32_t y[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
