@@ -9,8 +9,8 @@
 // codes 5, so the border times the scale has 13, and a quotient of 24 bits is never moved onto it).  Both quotients are made
 // from an approximate reciprocal and one correction by the remainder, which fma gives exactly: what is left then is some 2^-22 of the quotient's
 // last place, and a quotient by a number of 8 bits is either on the middle of two neighbours or 2^-9 of a place away from it.
-// That asks for scales within 2^-60 and 2^60, and for numbers that are zero or at most 15
-// binades below the largest, which makes the differences exact.  Other rows go a longer way: division,
+// That asks for scales within 2^-60 and 2^60, and for numbers at most 15 binades below
+// the largest, which makes the differences exact.  Other rows go a longer way: division,
 // differences rounded to odd (which keeps them on their side of every number of 13 bits), and halves where the
 // range passes fp32's.
 #include "kda_qcache.cuh"
@@ -42,6 +42,13 @@ __device__ __noinline__ uint32_t codes_of_any(const uint4 raw, float lo, bool wi
     return word;
 }
 
+__device__ __noinline__ uint4 values_of(uint32_t word, float scale, float zero) {
+    float c[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c[j] = fmaf((float)(word >> (4 * j) & 15u), scale, zero);
+    return make_uint4(pack_bf16x2(c[0], c[1]), pack_bf16x2(c[2], c[3]), pack_bf16x2(c[4], c[5]), pack_bf16x2(c[6], c[7]));
+}
+
 __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
     const __nv_bfloat162 m = __hmin2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
     return *reinterpret_cast<const uint32_t*>(&m);
@@ -53,20 +60,19 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
 
 // kHeads: heads of a token that a warp takes, all loaded at once
 template <int kHeads>
-__global__ void __launch_bounds__(QA_THREADS) qcache_append_kernel(const QcacheAppendParams p, int groups) {
+__global__ void __launch_bounds__(QA_THREADS) qcache_append_kernel(const QcacheAppendParams p) {
     await_stream();
     const int lane = threadIdx.x & 31, half = lane >> 4;
-    const int64_t item = ((int64_t)blockIdx.x * QA_THREADS + threadIdx.x) >> 5;
     // every sequence's lengths, whether it has tokens or not
     const int64_t threads = (int64_t)gridDim.x * QA_THREADS;
-    for (int64_t n = (int64_t)blockIdx.x * QA_THREADS + threadIdx.x; n < p.nseq; n += threads) {
+    for (int64_t n = (int64_t)blockIdx.x * QA_THREADS + threadIdx.x; n < p.nseq && blockIdx.y == 0; n += threads) {
         const int64_t c0 = p.cu ? p.cu[n] : n * p.uniform, c1 = p.cu ? p.cu[n + 1] : c0 + p.uniform, s = p.seqlens_k[n];
         const bool bad = c0 < 0 || (n == 0 && c0 != 0) || c1 < c0 || c1 > p.T || s > p.S || s < c1 - c0;
         if (bad && p.status) atomicOr(p.status, KDA_DEVERR_CU_SEQLENS);
     }
-    const int64_t t = item / groups;
+    const int64_t t = (int64_t)blockIdx.x * (QA_THREADS / 32) + (threadIdx.x >> 5);
     if (t >= p.T) return;
-    const int h0 = (int)(item - t * groups) * kHeads, heads = min(p.Hk - h0, kHeads);
+    const int h0 = blockIdx.y * kHeads, heads = min(p.Hk - h0, kHeads);
     const RowsView& in = half ? p.v : p.k;
     const __nv_bfloat16* src = in.data + t * in.row + h0 * in.head + 8 * (lane & 15);
     uint4 raws[kHeads];
@@ -100,56 +106,45 @@ __global__ void __launch_bounds__(QA_THREADS) qcache_append_kernel(const QcacheA
         const float lo = bf16_lo(both) + 0.f, hi = -bf16_hi(both);   // (-0 and 0 are one zero; a NaN makes both NaN)
         const float most = fmaxf(fabsf(lo), fabsf(hi));
         const bool finite = fabsf(lo) < INFINITY && fabsf(hi) < INFINITY;
-        // all eight numbers zero or at least 2^-15 of the largest
-        const __nv_bfloat162 least = __float2bfloat162_rn(0x1p-15f * most);
-        uint32_t plain2 = 0xffffffffu;
-#pragma unroll
-        for (const uint32_t w : {raw.x, raw.y, raw.z, raw.w}) {
-            const uint32_t m = w & 0x7fff7fffu;
-            const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&m);
-            plain2 &= __hge2_mask(v, least) | __heq2_mask(v, __float2bfloat162_rn(0.f));
-        }
+        // all eight numbers at least 2^-15 of the largest
+        const uint32_t small = min2(min2(raw.x & 0x7fff7fffu, raw.y & 0x7fff7fffu), min2(raw.z & 0x7fff7fffu, raw.w & 0x7fff7fffu));
+        const bool near = __hbge2(*reinterpret_cast<const __nv_bfloat162*>(&small), __float2bfloat162_rn(0x1p-15f * most));
         const float range = hi - lo, by15 = range * (1.f / 15.f);
         uint32_t sz = pack_bf16x2(fmaf(fmaf(-by15, 15.f, range), 1.f / 15.f, by15), lo);
-        const bool plain = plain2 == 0xffffffffu && finite && bf16_lo(sz) >= 0x1p-60f && bf16_lo(sz) <= 0x1p60f;
+        const bool plain = near && finite && bf16_lo(sz) >= 0x1p-60f && bf16_lo(sz) <= 0x1p60f;
         uint32_t word;
+        uint4 y;   // the values that the codes stand for
         if (__all_sync(0xffffffffu, plain)) {
             const float scale = bf16_lo(sz), r = rcp_approx(scale);
             const float x[8] = {bf16_lo(raw.x), bf16_hi(raw.x), bf16_lo(raw.y), bf16_hi(raw.y), bf16_lo(raw.z), bf16_hi(raw.z), bf16_lo(raw.w), bf16_hi(raw.w)};
             uint32_t sum = 0;
+            float c[8];
 #pragma unroll
             for (int j = 7; j >= 0; --j) {
-                const float d = x[j] - lo, q0 = d * r, q = fmaf(fmaf(-q0, scale, d), r, q0);
-                sum = sum * 16 + __float_as_uint(q + 12582912.f);   // (2^23 + 2^22: the last bits are the rounded quotient)
+                const float d = x[j] - lo, q0 = d * r, q = fmaf(fmaf(-q0, scale, d), r, q0) + 12582912.f;
+                sum = sum * 16 + __float_as_uint(q);   // (2^23 + 2^22: the last bits are the rounded quotient)
+                c[j] = fmaf(q - 12582912.f, scale, lo);
             }
             word = sum - 0x4b400000u * 0x11111111u;
+            y = make_uint4(pack_bf16x2(c[0], c[1]), pack_bf16x2(c[2], c[3]), pack_bf16x2(c[4], c[5]), pack_bf16x2(c[6], c[7]));
         } else {
             const bool wide = range == INFINITY;   // the range passes fp32's: everything halved
             sz = finite ? pack_bf16x2(wide ? (hi * 0.5f - lo * 0.5f) / 7.5f : range / 15.f, lo) : 0x7fc07fc0u;
             word = codes_of_any(raw, lo, wide, bf16_lo(sz));
+            y = values_of(word, bf16_lo(sz), bf16_hi(sz));
         }
         *reinterpret_cast<uint32_t*>(row + i * p.cache.head + 4 * lane) = word;
         if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(row + i * p.cache.head + QC_NUMBERS + (lane >> 1)) = sz;
-        if (dst) {
-            const float scale = bf16_lo(sz), zero = bf16_hi(sz);
-            uint32_t y[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float a = __uint_as_float((word >> (8 * j) & 15u) | 0x4b000000u) - 8388608.f, b = __uint_as_float((word >> (8 * j + 4) & 15u) | 0x4b000000u) - 8388608.f;
-                y[j] = pack_bf16x2(fmaf(a, scale, zero), fmaf(b, scale, zero));
-            }
-            __stcs(reinterpret_cast<uint4*>(dst + i * out.head), make_uint4(y[0], y[1], y[2], y[3]));
-        }
+        if (dst) __stcs(reinterpret_cast<uint4*>(dst + i * out.head), y);
     }
 }
 
 template <int kHeads>
 cudaError_t launch(const QcacheAppendParams& p, cudaStream_t stream) {
-    const int groups = (p.Hk + kHeads - 1) / kHeads;
-    int64_t blocks = (p.T * groups * 32 + QA_THREADS - 1) / QA_THREADS;
+    int64_t blocks = (p.T * 32 + QA_THREADS - 1) / QA_THREADS;
     if (blocks == 0) blocks = 1;   // (the lengths are checked all the same)
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    return launch_early(qcache_append_kernel<kHeads>, dim3((unsigned)blocks), QA_THREADS, 0, stream, p, groups);
+    return launch_early(qcache_append_kernel<kHeads>, dim3((unsigned)blocks, (unsigned)((p.Hk + kHeads - 1) / kHeads)), QA_THREADS, 0, stream, p);
 }
 
 }  // namespace
