@@ -39,7 +39,7 @@ constexpr int QS_MAX_CTAS = 320;
 constexpr int SLICE = 32;                          // keys
 constexpr uint32_t SLICE_BYTES = SLICE * QC_ROW;
 constexpr int QS_MAX_ROWS = 16;                    // of a tile
-constexpr int PIECE = 16;                          // a tile's own weight, in slices
+constexpr int PIECE[3] = {0, 18, 34};              // a tile's own weight, in slices, by kN
 constexpr float LIFT = 60.f;                       // weights are carried as p 2^60
 constexpr float NO_KEY = -3e38f;                   // (finite, so that a masked -inf less this is -inf)
 constexpr float UNLIFT = 0x1p-60f, CODE = 0x1p73f; // a product of a value's code and a weight, brought back
@@ -100,7 +100,9 @@ __device__ __forceinline__ int64_t qs_share_start(int64_t total, int b, int shar
 }
 
 // The whole block: checks the lengths, counts the steps and finds where share b starts and ends among them.
-__device__ QsShare qs_find_share(const QcacheAttnParams& p, int G, int rows, int64_t* scratch /* 32 */) {
+template <int kN>
+__device__ QsShare qs_find_share(const QcacheAttnParams& p, int G, int64_t* scratch /* 32 */) {
+    constexpr int own = PIECE[kN], rows = 8 * kN;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (p.nseq + QS_THREADS - 1) / QS_THREADS;
     const int n0 = min(tid * per, p.nseq), n1 = min(n0 + per, p.nseq);
@@ -114,7 +116,7 @@ __device__ QsShare qs_find_share(const QcacheAttnParams& p, int G, int rows, int
         b |= p.seqlens_k[n] < 0 || p.seqlens_k[n] > p.S;
         bad |= b;
         s = qs_seq(p, n);
-        each = b ? 0 : (int64_t)qs_tiles(s, G, rows) * p.Hk * (qs_slices(s) + PIECE);
+        each = b ? 0 : (int64_t)qs_tiles(s, G, rows) * p.Hk * (qs_slices(s) + own);
         mine += each;
     }
     int64_t sum = mine;
@@ -148,14 +150,14 @@ __device__ QsShare qs_find_share(const QcacheAttnParams& p, int G, int rows, int
         if (n > n0)
             for (n = n0;; ++n) {
                 s = qs_seq(p, n);
-                each = (int64_t)qs_tiles(s, G, rows) * p.Hk * (qs_slices(s) + PIECE);
+                each = (int64_t)qs_tiles(s, G, rows) * p.Hk * (qs_slices(s) + own);
                 if (x < base + each) break;
                 base += each;
             }
         const int64_t at = x - base;
-        const int w = qs_slices(s) + PIECE, tiles = qs_tiles(s, G, rows);
+        const int w = qs_slices(s) + own, tiles = qs_tiles(s, G, rows);
         const int64_t unit = (at >> 31) == 0 ? (int64_t)((uint32_t)at / (uint32_t)w) : at / w;
-        const int from = (int)(at - unit * w), j = max(from - PIECE, 0);   // the tile's own weight is at its front
+        const int from = (int)(at - unit * w), j = max(from - own, 0);   // the tile's own weight is at its front
         scratch[8 + e] = x - (j > 0 ? 0 : from);                          // (a cut inside it moves to the tile's start)
         if (e == 0) *place = QsCursor{n, (int)(unit / tiles), (int)(unit % tiles), j, s};
     }
@@ -183,11 +185,13 @@ __device__ __forceinline__ void qs_next_tile(const QcacheAttnParams& p, int G, i
 struct QsPiece {
     int j0, j1, nb, weight;
 };
+template <int kN>
 __device__ __forceinline__ QsPiece qs_piece(const QsCursor& u, int64_t left) {
     QsPiece r;
     r.nb = qs_slices(u.s);
     r.j0 = u.j;
-    const int own = u.j == 0 ? PIECE : 0;
+    constexpr int piece = PIECE[kN];
+    const int own = u.j == 0 ? piece : 0;
     r.j1 = left - own < r.nb - u.j ? u.j + (int)left - own : r.nb;
     r.weight = r.j1 - u.j + own;
     return r;
@@ -257,7 +261,7 @@ __global__ void __launch_bounds__(QS_THREADS, kN == 1 ? 2 : 1) attn_qcache_kerne
     }
     __syncwarp();
     await_stream();
-    const QsShare share = qs_find_share(p, G, rows, reinterpret_cast<int64_t*>(smem_raw + L::OFF_SCRATCH));
+    const QsShare share = qs_find_share<kN>(p, G, reinterpret_cast<int64_t*>(smem_raw + L::OFF_SCRATCH));
     QsPartials part = qs_partials(p.workspace);
     QsCursor u = share.at;
     if (tid == 0) {
@@ -284,7 +288,7 @@ __global__ void __launch_bounds__(QS_THREADS, kN == 1 ? 2 : 1) attn_qcache_kerne
     int64_t left = share.weight;
     QsPiece r{};
     if (left > 0) {
-        r = qs_piece(u, left);
+        r = qs_piece<kN>(u, left);
         load_first(u, r);
     }
 
@@ -517,7 +521,7 @@ __global__ void __launch_bounds__(QS_THREADS, kN == 1 ? 2 : 1) attn_qcache_kerne
         left -= r.weight;
         if (left > 0) {
             qs_next_tile(p, G, rows, u);
-            r = qs_piece(u, left);
+            r = qs_piece<kN>(u, left);
             load_first(u, r);
         }
         // ---- the warps' results: reference and sum of every row, then the rows themselves
@@ -797,7 +801,7 @@ __global__ void __launch_bounds__(EX_THREADS) qcache_expand_kernel(const ExpandP
 }  // namespace
 
 // Few rows: this file's kernel; many: that of kda_attn.cu on expanded keys and values.
-static bool few_rows(int64_t Tq, int Hq, int Hk, int nseq) { return Tq * (Hq / Hk) <= 32 * (int64_t)nseq; }
+static bool few_rows(int64_t Tq, int Hq, int Hk, int nseq) { return Tq * (Hq / Hk) <= 128 * (int64_t)nseq; }
 
 // Expanded keys and values for as many key heads at a time as fit into 1 GB, one at least.
 constexpr int64_t EX_MOST = 1LL << 30;

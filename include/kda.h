@@ -503,7 +503,7 @@ kda_status kda_qcache_append(const kda_view* k, const kda_view* v, const kda_vie
 /*
  * Bytes of workspace kda_attn_qcache_fwd needs for Tq query tokens, Hq query heads, Hk key/value heads
  * and N sequences with room for S keys each.  Its contents need no initialisation.  At present 11 MB where the
- * sequences have at most 32 (token, head) rows for a key head on average, Tq Hq / Hk <= 32 N.  Beyond that the keys and
+ * sequences have at most 128 (token, head) rows for a key head on average, Tq Hq / Hk <= 128 N.  Beyond that the keys and
  * values are expanded there, 768 bytes for each row of the cache: for as many key heads at a time as fit into 1 GB (one at
  * least), and 43 MB.  Returns 0 for invalid arguments.
  */
