@@ -34,7 +34,7 @@
 namespace kda {
 namespace {
 
-constexpr int QS_WARPS = 8, QS_THREADS = 32 * QS_WARPS;
+constexpr int QS_WARPS[3] = {0, 8, 8};             // by kN (16 rows: ten and twelve warps spill, 81 and 101 us against 48 on drafts)
 constexpr int QS_MAX_CTAS = 320;
 constexpr int SLICE = 32;                          // keys
 constexpr uint32_t SLICE_BYTES = SLICE * QC_ROW;
@@ -102,9 +102,9 @@ __device__ __forceinline__ int64_t qs_share_start(int64_t total, int b, int shar
 // The whole block: checks the lengths, counts the steps and finds where share b starts and ends among them.
 template <int kN>
 __device__ QsShare qs_find_share(const QcacheAttnParams& p, int G, int64_t* scratch /* 32 */) {
-    constexpr int own = PIECE[kN], rows = 8 * kN;
+    constexpr int own = PIECE[kN], rows = 8 * kN, warps = QS_WARPS[kN], threads = 32 * warps;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (p.nseq + QS_THREADS - 1) / QS_THREADS;
+    const int per = (p.nseq + threads - 1) / threads;
     const int n0 = min(tid * per, p.nseq), n1 = min(n0 + per, p.nseq);
     QsSeq s{};
     int64_t mine = 0, each = 0;
@@ -131,15 +131,15 @@ __device__ QsShare qs_find_share(const QcacheAttnParams& p, int G, int64_t* scra
     if (r.bad) return r;
     int64_t total = 0, before = sum - mine;
 #pragma unroll
-    for (int w = 0; w < QS_WARPS; ++w) {
+    for (int w = 0; w < warps; ++w) {
         before += w < warp ? scratch[w] : 0;
         total += scratch[w];
     }
     // (fewer shares than CTAs where a share would not give every warp a slice)
-    const int shares = (int)min((int64_t)gridDim.x, max(total / QS_WARPS, (int64_t)1));
+    const int shares = (int)min((int64_t)gridDim.x, max(total / warps, (int64_t)1));
     const int64_t x0 = qs_share_start(total, blockIdx.x, shares), x1 = qs_share_start(total, blockIdx.x + 1, shares);
-    QsCursor* place = reinterpret_cast<QsCursor*>(scratch + 16);
-    if (tid == 0) scratch[8] = x0, scratch[9] = x1;
+    QsCursor* place = reinterpret_cast<QsCursor*>(scratch + 20);
+    if (tid == 0) scratch[16] = x0, scratch[17] = x1;
     __syncthreads();
 #pragma unroll 1
     for (int e = 0; e < 2; ++e) {
@@ -156,15 +156,17 @@ __device__ QsShare qs_find_share(const QcacheAttnParams& p, int G, int64_t* scra
             }
         const int64_t at = x - base;
         const int w = qs_slices(s) + own, tiles = qs_tiles(s, G, rows);
-        const int64_t unit = (at >> 31) == 0 ? (int64_t)((uint32_t)at / (uint32_t)w) : at / w;
+        const bool small = (at >> 31) == 0;   // (64-bit divisions take long)
+        const int64_t unit = small ? (int64_t)((uint32_t)at / (uint32_t)w) : at / w;
+        const int head = tiles == 1 ? (int)unit : small ? (int)((uint32_t)unit / (uint32_t)tiles) : (int)(unit / tiles);
         const int from = (int)(at - unit * w), j = max(from - own, 0);   // the tile's own weight is at its front
-        scratch[8 + e] = x - (j > 0 ? 0 : from);                          // (a cut inside it moves to the tile's start)
-        if (e == 0) *place = QsCursor{n, (int)(unit / tiles), (int)(unit % tiles), j, s};
+        scratch[16 + e] = x - (j > 0 ? 0 : from);                          // (a cut inside it moves to the tile's start)
+        if (e == 0) *place = QsCursor{n, head, (int)(unit - (int64_t)head * tiles), j, s};
     }
     __syncthreads();
     if (x0 < total) {
         r.at = *place;
-        r.weight = scratch[9] - scratch[8];
+        r.weight = scratch[17] - scratch[16];
     }
     return r;
 }
@@ -234,20 +236,25 @@ __device__ __forceinline__ uint32_t lifted(uint32_t x) {
     return *reinterpret_cast<const uint32_t*>(&y);
 }
 
+// Where a row's 16-byte groups are kept among the warps' results: with rows 2 t and 2 t + 1 from lane (g, t), groups 2 g and
+// 2 g + 1, bits 0 and 2 of the group's number spread the four t, bit 1 the neighbouring g.
+__device__ __forceinline__ int row_swizzle(int row) { return (row >> 1 & 1) | (row & 4); }
+
 constexpr int QS_STAGES = 2;
 template <int kN>
 struct QsLayout {
-    static constexpr uint32_t ROWS = 8 * kN;
-    static constexpr uint32_t OFF_SUMS = QS_WARPS * QS_STAGES * SLICE_BYTES;          // [warps][rows][128] fp32
-    static constexpr uint32_t OFF_ML = OFF_SUMS + QS_WARPS * ROWS * 512;              // [warps][rows] float2
-    static constexpr uint32_t OFF_BAR = OFF_ML + QS_WARPS * ROWS * 8;
-    static constexpr uint32_t OFF_SCRATCH = OFF_BAR + QS_WARPS * QS_STAGES * 8;
+    static constexpr uint32_t ROWS = 8 * kN, WARPS = QS_WARPS[kN], THREADS = 32 * WARPS;
+    static constexpr uint32_t OFF_SUMS = WARPS * QS_STAGES * SLICE_BYTES;          // [warps][rows][128] fp32
+    static constexpr uint32_t OFF_ML = OFF_SUMS + WARPS * ROWS * 512;              // [warps][rows] float2
+    static constexpr uint32_t OFF_BAR = OFF_ML + WARPS * ROWS * 8;
+    static constexpr uint32_t OFF_SCRATCH = OFF_BAR + WARPS * QS_STAGES * 8;
     static constexpr uint32_t BYTES = OFF_SCRATCH + 32 * 8;
 };
 
 template <int kN>
-__global__ void __launch_bounds__(QS_THREADS, kN == 1 ? 2 : 1) attn_qcache_kernel(const QcacheAttnParams p, const __grid_constant__ CUtensorMap map) {
+__global__ void __launch_bounds__(QsLayout<kN>::THREADS, kN == 1 ? 2 : 1) attn_qcache_kernel(const QcacheAttnParams p, const __grid_constant__ CUtensorMap map) {
     using L = QsLayout<kN>;
+    constexpr int WARPS = L::WARPS;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t base = smem_u32(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = mx_uniform(tid >> 5), g = lane >> 2, t = lane & 3;
@@ -283,7 +290,7 @@ __global__ void __launch_bounds__(QS_THREADS, kN == 1 ? 2 : 1) attn_qcache_kerne
     auto load_first = [&](const QsCursor& v, const QsPiece& r) {
 #pragma unroll
         for (int i = 0; i < QS_STAGES; ++i)
-            if (r.j0 + warp + i * QS_WARPS < r.j1) load(v.kh, v.n, r.j0 + warp + i * QS_WARPS, used + i);
+            if (r.j0 + warp + i * WARPS < r.j1) load(v.kh, v.n, r.j0 + warp + i * WARPS, used + i);
     };
     int64_t left = share.weight;
     QsPiece r{};
@@ -362,7 +369,7 @@ __global__ void __launch_bounds__(QS_THREADS, kN == 1 ? 2 : 1) attn_qcache_kerne
                 }
             }
 #pragma unroll 1
-        for (int j = r.j0 + warp; j < r.j1; j += QS_WARPS) {
+        for (int j = r.j0 + warp; j < r.j1; j += WARPS) {
             const uint32_t stage = used % QS_STAGES;
             if (ok) ok = mx_wait(bars + 8 * stage, (used / QS_STAGES) & 1);
             const unsigned char* kat = krow + stage * SLICE_BYTES;
@@ -512,7 +519,7 @@ __global__ void __launch_bounds__(QS_THREADS, kN == 1 ? 2 : 1) attn_qcache_kerne
                 }
             }
             __syncwarp();
-            if (j + QS_STAGES * QS_WARPS < r.j1) load(u.kh, u.n, j + QS_STAGES * QS_WARPS, used + QS_STAGES);
+            if (j + QS_STAGES * WARPS < r.j1) load(u.kh, u.n, j + QS_STAGES * WARPS, used + QS_STAGES);
             ++used;
         }
         // ---- on to the next piece, whose loads start here
@@ -547,7 +554,7 @@ __global__ void __launch_bounds__(QS_THREADS, kN == 1 ? 2 : 1) attn_qcache_kerne
                 const int row = 8 * b + 2 * t + e;
                 float top = -INFINITY;
 #pragma unroll
-                for (int w = 0; w < QS_WARPS; ++w) top = fmaxf(top, ml[w * rows + row].x);
+                for (int w = 0; w < WARPS; ++w) top = fmaxf(top, ml[w * rows + row].x);
                 const float f = l[b][e] == 0.f ? 0.f : ex2_approx(low[b][e] + LIFT - top);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -558,27 +565,26 @@ __global__ void __launch_bounds__(QS_THREADS, kN == 1 ? 2 : 1) attn_qcache_kerne
                         y[i] = f * fmaf(back, o[b][h][i][e], rest);
                         y[4 + i] = f * fmaf(back, o[b][h][i][2 + e], rest);
                     }
-                    float4* dst = reinterpret_cast<float4*>(sums + (warp * rows + row) * 128 + 64 * h + 8 * g);
-                    dst[0] = make_float4(y[0], y[1], y[2], y[3]);
-                    dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+                    // (eight lanes that store together store to different banks: see row_swizzle)
+                    float4* dst = reinterpret_cast<float4*>(sums + (warp * rows + row) * 128);
+                    dst[(16 * h + 2 * g) ^ row_swizzle(row)] = make_float4(y[0], y[1], y[2], y[3]);
+                    dst[(16 * h + 2 * g + 1) ^ row_swizzle(row)] = make_float4(y[4], y[5], y[6], y[7]);
                 }
             }
         __syncthreads();
         const size_t slot = 2 * blockIdx.x + (first_piece ? 0 : 1);
-#pragma unroll
-        for (int b = 0; b < kN; ++b) {   // a warp takes a row, a lane four channels
-            const int row = 8 * b + warp;
-            if (row >= have) continue;
+#pragma unroll 1
+        for (int row = warp; row < have; row += WARPS) {   // a warp takes a row, a lane four channels
             float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
             float top = -INFINITY, sum = 0.f;
 #pragma unroll
-            for (int w = 0; w < QS_WARPS; ++w) {
-                const float4 x = *reinterpret_cast<const float4*>(sums + (w * rows + row) * 128 + 4 * lane);
+            for (int w = 0; w < WARPS; ++w) {
+                const float4 x = reinterpret_cast<const float4*>(sums + (w * rows + row) * 128)[lane ^ row_swizzle(row)];
                 y.x += x.x, y.y += x.y, y.z += x.z, y.w += x.w;
                 top = fmaxf(top, ml[w * rows + row].x);
             }
 #pragma unroll
-            for (int w = 0; w < QS_WARPS; ++w) {
+            for (int w = 0; w < WARPS; ++w) {
                 const float2 x = ml[w * rows + row];
                 sum += x.x == -INFINITY ? 0.f : x.y * ex2_approx(x.x - top);
             }
@@ -606,9 +612,10 @@ __global__ void __launch_bounds__(QS_THREADS, kN == 1 ? 2 : 1) attn_qcache_kerne
 // store, so that none is lost).  Block (b, y) takes row y of the tile that share b + 1 starts in, if that is the tile's
 // first cut; its warps take the parts in turn, lane l their channels 4 l .. 4 l + 3.  Bound by latency: what it reads
 // is asked for at once (a warp a row, part after part, cost one token over 32,767 keys 6 us more).
-__global__ void __launch_bounds__(QS_THREADS) attn_qcache_join_kernel(const QcacheAttnParams p, int ctas, int rows) {
-    __shared__ float4 sums[QS_WARPS][32];
-    __shared__ float2 refs[QS_WARPS];
+constexpr int QJ_WARPS = 8;
+__global__ void __launch_bounds__(32 * QJ_WARPS) attn_qcache_join_kernel(const QcacheAttnParams p, int ctas, int rows) {
+    __shared__ float4 sums[QJ_WARPS][32];
+    __shared__ float2 refs[QJ_WARPS];
     const int first = blockIdx.x + 1, row = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = p.Hq / p.Hk;
     const QsPartials part = qs_partials(p.workspace);
     await_stream();
@@ -645,12 +652,12 @@ __global__ void __launch_bounds__(QS_THREADS) attn_qcache_join_kernel(const Qcac
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-    for (int s0 = b + warp; s0 < end; s0 += 4 * QS_WARPS) {
+    for (int s0 = b + warp; s0 < end; s0 += 4 * QJ_WARPS) {
         float2 ml[4];
         float4 y[4];
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
-            const int s = s0 + d * QS_WARPS;
+            const int s = s0 + d * QJ_WARPS;
             ml[d] = make_float2(-INFINITY, 0.f);
             y[d] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (s < end && (s == b || part.cut[s].some)) {
@@ -676,11 +683,11 @@ __global__ void __launch_bounds__(QS_THREADS) attn_qcache_join_kernel(const Qcac
     if (warp != 0) return;
     float top = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < QS_WARPS; ++w) top = fmaxf(top, refs[w].x);
+    for (int w = 0; w < QJ_WARPS; ++w) top = fmaxf(top, refs[w].x);
     l = 0.f;
     o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < QS_WARPS; ++w) {
+    for (int w = 0; w < QJ_WARPS; ++w) {
         const float2 r = refs[w];
         const float4 y = sums[w][lane];
         const float f = r.x == -INFINITY ? 0.f : ex2_approx(r.x - top);
@@ -714,8 +721,8 @@ cudaError_t launch(const QcacheAttnParams& p, int sms, cudaStream_t stream) {
     if (!encode_cache(&map, p, SLICE)) return cudaErrorInvalidValue;
     const int ctas = min(sms * (kN == 1 ? 2 : 1), QS_MAX_CTAS);
     cudaError_t e = cudaFuncSetAttribute(attn_qcache_kernel<kN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)QsLayout<kN>::BYTES);
-    if (e == cudaSuccess) e = launch_early(attn_qcache_kernel<kN>, dim3((unsigned)ctas), QS_THREADS, QsLayout<kN>::BYTES, stream, p, map);
-    if (e == cudaSuccess) e = launch_early(attn_qcache_join_kernel, dim3((unsigned)ctas, (unsigned)(8 * kN)), QS_THREADS, 0, stream, p, ctas, 8 * kN);
+    if (e == cudaSuccess) e = launch_early(attn_qcache_kernel<kN>, dim3((unsigned)ctas), QsLayout<kN>::THREADS, QsLayout<kN>::BYTES, stream, p, map);
+    if (e == cudaSuccess) e = launch_early(attn_qcache_join_kernel, dim3((unsigned)ctas, (unsigned)(8 * kN)), 32 * QJ_WARPS, 0, stream, p, ctas, 8 * kN);
     return e;
 }
 
