@@ -838,12 +838,14 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const AttnParams p,
 }
 
 // Joins the partial rows of the pairs that several shares hold (and, the last block, the shares' status bits: one store,
-// so that none is lost).  Block (b, y) takes 32 rows of the
+// so that none is lost).  Block (b, y) takes `rows` rows of the
 // pair that share b + 1 starts in, if that is the pair's first cut; a warp takes four of them, lane l
 // their channels 4 l .. 4 l + 3.  Bound by latency: little code (it is fetched cold) and few loads
 // in a row.
-constexpr int JOIN_THREADS = 256, JOIN_ROWS = 32;
-__global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParams p, int ctas) {
+// (With split keys a block takes 8 rows: continued prompts 743 -> 730 us; single tokens over a bf16 cache
+// 43 -> 50 us, so elsewhere it is 32.)
+constexpr int JOIN_THREADS = 256;
+__global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParams p, int ctas, int rows) {
     const int first = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int G = p.Hq / p.Hk, tq = 128 / G;
     const Partials part = partials(p.workspace);
@@ -879,8 +881,8 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParam
     }
     auto slot = [&](int s) { return (size_t)(2 * s + (s == b && !same ? 1 : 0)); };
 #pragma unroll 1
-    for (int k = 0; k < JOIN_ROWS / 8; ++k) {
-        const int row = blockIdx.y * JOIN_ROWS + 8 * k + warp;
+    for (int k = 0; k < rows; k += 8) {
+        const int row = blockIdx.y * rows + k + warp;
         const int t = row >> 7, tok = (row & 127) / G, head = (row & 127) - tok * G;
         const int i = (2 * c.pair + t) * tq + tok;
         if (tok >= tq || i >= c.lq) continue;
@@ -959,7 +961,8 @@ static cudaError_t launch(const AttnParams& p, cudaStream_t stream) {
     e = launch_early(attn_kernel<kSplit>, dim3((unsigned)ctas), AT_THREADS, Layout<kSplit>::SMEM, stream, p, maps,
                      ctas > 1 ? ~0ull / (uint64_t)ctas + 1 : (uint64_t)0);
     if (e != cudaSuccess) return e;
-    return launch_early(attn_join_kernel, dim3((unsigned)ctas, 256 / JOIN_ROWS), JOIN_THREADS, 0, stream, p, ctas);
+    const int rows = kSplit ? 8 : 32;
+    return launch_early(attn_join_kernel, dim3((unsigned)ctas, 256 / rows), JOIN_THREADS, 0, stream, p, ctas, rows);
 }
 
 cudaError_t launch_attn(const AttnParams& p, cudaStream_t stream) { return launch<false>(p, stream); }

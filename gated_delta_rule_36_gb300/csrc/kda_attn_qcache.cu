@@ -38,7 +38,7 @@ constexpr int QS_WARPS[3] = {0, 8, 8};             // by kN (16 rows: ten and tw
 constexpr int QS_MAX_CTAS = 320;
 constexpr int SLICE = 32;                          // keys
 constexpr uint32_t SLICE_BYTES = SLICE * QC_ROW;
-constexpr int QS_MAX_ROWS = 16;                    // of a tile
+constexpr int QS_MAX_ROWS = 16;                    // of a tile of 8 rows for the heads that go together (16 rows: 32)
 constexpr int PIECE[3] = {0, 18, 34};              // a tile's own weight, in slices, by kN
 constexpr float LIFT = 60.f;                       // weights are carried as p 2^60
 constexpr float NO_KEY = -3e38f;                   // (finite, so that a masked -inf less this is -inf)
@@ -54,8 +54,8 @@ struct QsCut {
 };
 struct QsPartials {
     QsCut* cut;         // [shares]
-    float2* ml;         // [2 * shares][QS_MAX_ROWS]: reference exponent (base 2) and sum
-    float* o;           // [2 * shares][QS_MAX_ROWS][128], not normalised
+    float2* ml;         // [2 * shares][kN * QS_MAX_ROWS]: reference exponent (base 2) and sum
+    float* o;           // [2 * shares][kN * QS_MAX_ROWS][128], not normalised
 };
 constexpr size_t QS_CUT_BYTES = QS_MAX_CTAS * sizeof(QsCut), QS_ML_BYTES = (size_t)2 * QS_MAX_CTAS * QS_MAX_ROWS * sizeof(float2);
 __device__ __forceinline__ QsPartials qs_partials(void* ws) {
@@ -81,7 +81,7 @@ __device__ __forceinline__ QsSeq qs_seq(const QcacheAttnParams& p, int n) {
 __device__ __forceinline__ int qs_tiles(const QsSeq& s, int G, int rows) { return (int)(((int64_t)s.lq * G + rows - 1) / rows); }
 __device__ __forceinline__ int qs_slices(const QsSeq& s) { return (s.lk + SLICE - 1) / SLICE; }
 
-// A step: slice j of tile `tile` of key head kh of sequence n.
+// A step: slice j of tile `tile` of the 2^hg key heads from kh << hg on, of sequence n.
 struct QsCursor {
     int n, kh, tile, j;
     QsSeq s;
@@ -100,9 +100,9 @@ __device__ __forceinline__ int64_t qs_share_start(int64_t total, int b, int shar
 }
 
 // The whole block: checks the lengths, counts the steps and finds where share b starts and ends among them.
-template <int kN>
+template <int kN, int kHg>
 __device__ QsShare qs_find_share(const QcacheAttnParams& p, int G, int64_t* scratch /* 32 */) {
-    constexpr int own = PIECE[kN], rows = 8 * kN, warps = QS_WARPS[kN], threads = 32 * warps;
+    constexpr int own = PIECE[kN] >> kHg, rows = 8 * kN, warps = QS_WARPS[kN], threads = 32 * warps;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (p.nseq + threads - 1) / threads;
     const int n0 = min(tid * per, p.nseq), n1 = min(n0 + per, p.nseq);
@@ -116,7 +116,7 @@ __device__ QsShare qs_find_share(const QcacheAttnParams& p, int G, int64_t* scra
         b |= p.seqlens_k[n] < 0 || p.seqlens_k[n] > p.S;
         bad |= b;
         s = qs_seq(p, n);
-        each = b ? 0 : (int64_t)qs_tiles(s, G, rows) * p.Hk * (qs_slices(s) + own);
+        each = b ? 0 : (int64_t)qs_tiles(s, G, rows) * (p.Hk >> kHg) * (qs_slices(s) + own);
         mine += each;
     }
     int64_t sum = mine;
@@ -136,7 +136,7 @@ __device__ QsShare qs_find_share(const QcacheAttnParams& p, int G, int64_t* scra
         total += scratch[w];
     }
     // (fewer shares than CTAs where a share would not give every warp a slice)
-    const int shares = (int)min((int64_t)gridDim.x, max(total / warps, (int64_t)1));
+    const int shares = (int)min((int64_t)gridDim.x, max(total / (warps >> kHg), (int64_t)1));
     const int64_t x0 = qs_share_start(total, blockIdx.x, shares), x1 = qs_share_start(total, blockIdx.x + 1, shares);
     QsCursor* place = reinterpret_cast<QsCursor*>(scratch + 20);
     if (tid == 0) scratch[16] = x0, scratch[17] = x1;
@@ -150,7 +150,7 @@ __device__ QsShare qs_find_share(const QcacheAttnParams& p, int G, int64_t* scra
         if (n > n0)
             for (n = n0;; ++n) {
                 s = qs_seq(p, n);
-                each = (int64_t)qs_tiles(s, G, rows) * p.Hk * (qs_slices(s) + own);
+                each = (int64_t)qs_tiles(s, G, rows) * (p.Hk >> kHg) * (qs_slices(s) + own);
                 if (x < base + each) break;
                 base += each;
             }
@@ -171,11 +171,12 @@ __device__ QsShare qs_find_share(const QcacheAttnParams& p, int G, int64_t* scra
     return r;
 }
 
+template <int kHg>
 __device__ __forceinline__ void qs_next_tile(const QcacheAttnParams& p, int G, int rows, QsCursor& u) {
     u.j = 0;
     if (++u.tile < qs_tiles(u.s, G, rows)) return;
     u.tile = 0;
-    if (++u.kh < p.Hk) return;
+    if (++u.kh < p.Hk >> kHg) return;
     u.kh = 0;
     do {
         if (++u.n >= p.nseq) return;
@@ -187,12 +188,12 @@ __device__ __forceinline__ void qs_next_tile(const QcacheAttnParams& p, int G, i
 struct QsPiece {
     int j0, j1, nb, weight;
 };
-template <int kN>
+template <int kN, int kHg>
 __device__ __forceinline__ QsPiece qs_piece(const QsCursor& u, int64_t left) {
     QsPiece r;
     r.nb = qs_slices(u.s);
     r.j0 = u.j;
-    constexpr int piece = PIECE[kN];
+    constexpr int piece = PIECE[kN] >> kHg;
     const int own = u.j == 0 ? piece : 0;
     r.j1 = left - own < r.nb - u.j ? u.j + (int)left - own : r.nb;
     r.weight = r.j1 - u.j + own;
@@ -251,7 +252,7 @@ struct QsLayout {
     static constexpr uint32_t BYTES = OFF_SCRATCH + 32 * 8;
 };
 
-template <int kN>
+template <int kN, int kHg>
 __global__ void __launch_bounds__(QsLayout<kN>::THREADS, kN == 1 ? 2 : 1) attn_qcache_kernel(const QcacheAttnParams p, const __grid_constant__ CUtensorMap map) {
     using L = QsLayout<kN>;
     constexpr int WARPS = L::WARPS;
@@ -260,6 +261,9 @@ __global__ void __launch_bounds__(QsLayout<kN>::THREADS, kN == 1 ? 2 : 1) attn_q
     const int tid = threadIdx.x, lane = tid & 31, warp = mx_uniform(tid >> 5), g = lane >> 2, t = lane & 3;
     const int G = p.Hq / p.Hk, rows = L::ROWS;
     asm volatile("griddepcontrol.launch_dependents;");
+    // this warp's head of those that go together, and its slices of it
+    constexpr int heads = (1 << kHg) - 1, step = WARPS >> kHg;
+    const int mine = warp & heads, from = warp >> kHg;
     const uint32_t ring = base + warp * QS_STAGES * SLICE_BYTES, bars = base + L::OFF_BAR + warp * QS_STAGES * 8;
     if (lane == 0) {
         for (int i = 0; i < QS_STAGES; ++i) mbar_init(bars + 8 * i, 1);
@@ -268,7 +272,7 @@ __global__ void __launch_bounds__(QsLayout<kN>::THREADS, kN == 1 ? 2 : 1) attn_q
     }
     __syncwarp();
     await_stream();
-    const QsShare share = qs_find_share<kN>(p, G, reinterpret_cast<int64_t*>(smem_raw + L::OFF_SCRATCH));
+    const QsShare share = qs_find_share<kN, kHg>(p, G, reinterpret_cast<int64_t*>(smem_raw + L::OFF_SCRATCH));
     QsPartials part = qs_partials(p.workspace);
     QsCursor u = share.at;
     if (tid == 0) {
@@ -290,12 +294,12 @@ __global__ void __launch_bounds__(QsLayout<kN>::THREADS, kN == 1 ? 2 : 1) attn_q
     auto load_first = [&](const QsCursor& v, const QsPiece& r) {
 #pragma unroll
         for (int i = 0; i < QS_STAGES; ++i)
-            if (r.j0 + warp + i * WARPS < r.j1) load(v.kh, v.n, r.j0 + warp + i * WARPS, used + i);
+            if (r.j0 + from + i * step < r.j1) load((v.kh << kHg) + mine, v.n, r.j0 + from + i * step, used + i);
     };
     int64_t left = share.weight;
     QsPiece r{};
     if (left > 0) {
-        r = qs_piece<kN>(u, left);
+        r = qs_piece<kN, kHg>(u, left);
         load_first(u, r);
     }
 
@@ -307,6 +311,7 @@ __global__ void __launch_bounds__(QsLayout<kN>::THREADS, kN == 1 ? 2 : 1) attn_q
     bool ok = true, first_piece = true;
 #pragma unroll 1
     while (left > 0) {
+        const int kh = (u.kh << kHg) + mine;
         // ---- the tile's queries: lane (g, t) holds channels 16 t .. 16 t + 15 of both halves of row g
         uint32_t q[kN][8][2];            // pairs (e, e + 4) of each eight, the order in which the codes come
         uint32_t qz[kN];                 // sums over the halves' channels, each as three bf16 terms
@@ -318,7 +323,7 @@ __global__ void __launch_bounds__(QsLayout<kN>::THREADS, kN == 1 ? 2 : 1) attn_q
 #pragma unroll
         for (int b = 0; b < kN; ++b) {
             const uint32_t on = (head0 + 8 * b + g) / (uint32_t)G, head = head0 + 8 * b + g - on * G;
-            const __nv_bfloat16* src = p.q.data + ((int64_t)u.s.q0 + tok0 + on) * p.q.row + ((int64_t)u.kh * G + head) * p.q.head + 16 * t;
+            const __nv_bfloat16* src = p.q.data + ((int64_t)u.s.q0 + tok0 + on) * p.q.row + ((int64_t)kh * G + head) * p.q.head + 16 * t;
             float sum[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -369,7 +374,7 @@ __global__ void __launch_bounds__(QsLayout<kN>::THREADS, kN == 1 ? 2 : 1) attn_q
                 }
             }
 #pragma unroll 1
-        for (int j = r.j0 + warp; j < r.j1; j += WARPS) {
+        for (int j = r.j0 + from; j < r.j1; j += step) {
             const uint32_t stage = used % QS_STAGES;
             if (ok) ok = mx_wait(bars + 8 * stage, (used / QS_STAGES) & 1);
             const unsigned char* kat = krow + stage * SLICE_BYTES;
@@ -519,16 +524,16 @@ __global__ void __launch_bounds__(QsLayout<kN>::THREADS, kN == 1 ? 2 : 1) attn_q
                 }
             }
             __syncwarp();
-            if (j + QS_STAGES * WARPS < r.j1) load(u.kh, u.n, j + QS_STAGES * WARPS, used + QS_STAGES);
+            if (j + QS_STAGES * step < r.j1) load(kh, u.n, j + QS_STAGES * step, used + QS_STAGES);
             ++used;
         }
         // ---- on to the next piece, whose loads start here
         const bool whole = r.j0 == 0 && r.j1 == r.nb;
-        const int q0 = u.s.q0, kh = u.kh;
+        const int q0 = u.s.q0, kh0 = u.kh << kHg;
         left -= r.weight;
         if (left > 0) {
-            qs_next_tile(p, G, rows, u);
-            r = qs_piece<kN>(u, left);
+            qs_next_tile<kHg>(p, G, rows, u);
+            r = qs_piece<kN, kHg>(u, left);
             load_first(u, r);
         }
         // ---- the warps' results: reference and sum of every row, then the rows themselves
@@ -554,7 +559,7 @@ __global__ void __launch_bounds__(QsLayout<kN>::THREADS, kN == 1 ? 2 : 1) attn_q
                 const int row = 8 * b + 2 * t + e;
                 float top = -INFINITY;
 #pragma unroll
-                for (int w = 0; w < WARPS; ++w) top = fmaxf(top, ml[w * rows + row].x);
+                for (int w = 0; w < step; ++w) top = fmaxf(top, ml[((w << kHg) + mine) * rows + row].x);   // (this head's warps)
                 const float f = l[b][e] == 0.f ? 0.f : ex2_approx(low[b][e] + LIFT - top);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -572,28 +577,30 @@ __global__ void __launch_bounds__(QsLayout<kN>::THREADS, kN == 1 ? 2 : 1) attn_q
                 }
             }
         __syncthreads();
-        const size_t slot = 2 * blockIdx.x + (first_piece ? 0 : 1);
+        const size_t slot = (size_t)(2 * blockIdx.x + (first_piece ? 0 : 1)) * kN * QS_MAX_ROWS;
 #pragma unroll 1
-        for (int row = warp; row < have; row += WARPS) {   // a warp takes a row, a lane four channels
+        for (int i = warp; i < rows << kHg; i += WARPS) {   // a warp takes a row of a head, a lane four channels
+            const int hh = i & heads, row = i >> kHg;
+            if (row >= have) break;
             float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
             float top = -INFINITY, sum = 0.f;
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w) {
-                const float4 x = reinterpret_cast<const float4*>(sums + (w * rows + row) * 128)[lane ^ row_swizzle(row)];
+            for (int w = 0; w < step; ++w) {
+                const float4 x = reinterpret_cast<const float4*>(sums + (((w << kHg) + hh) * rows + row) * 128)[lane ^ row_swizzle(row)];
                 y.x += x.x, y.y += x.y, y.z += x.z, y.w += x.w;
-                top = fmaxf(top, ml[w * rows + row].x);
+                top = fmaxf(top, ml[((w << kHg) + hh) * rows + row].x);
             }
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w) {
-                const float2 x = ml[w * rows + row];
+            for (int w = 0; w < step; ++w) {
+                const float2 x = ml[((w << kHg) + hh) * rows + row];
                 sum += x.x == -INFINITY ? 0.f : x.y * ex2_approx(x.x - top);
             }
             if (!whole) {
-                *reinterpret_cast<float4*>(part.o + (slot * QS_MAX_ROWS + row) * 128 + 4 * lane) = y;
-                if (lane == 0) part.ml[slot * QS_MAX_ROWS + row] = make_float2(top, sum);
+                *reinterpret_cast<float4*>(part.o + (slot + i) * 128 + 4 * lane) = y;
+                if (lane == 0) part.ml[slot + i] = make_float2(top, sum);
             } else {
                 const uint32_t on = (head0 + row) / (uint32_t)G;
-                const int64_t tok = (int64_t)q0 + tok0 + on, head = (int64_t)kh * G + (head0 + row - on * G);
+                const int64_t tok = (int64_t)q0 + tok0 + on, head = (int64_t)(kh0 + hh) * G + (head0 + row - on * G);
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
                 *reinterpret_cast<uint2*>(p.out.data + tok * p.out.row + head * p.out.head + 4 * lane) =
                     make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
@@ -609,18 +616,20 @@ __global__ void __launch_bounds__(QsLayout<kN>::THREADS, kN == 1 ? 2 : 1) attn_q
 }
 
 // Joins the partial rows of the tiles that several shares hold (and, the last block, the shares' status bits: one
-// store, so that none is lost).  Block (b, y) takes row y of the tile that share b + 1 starts in, if that is the tile's
-// first cut; its warps take the parts in turn, lane l their channels 4 l .. 4 l + 3.  Bound by latency: what it reads
-// is asked for at once (a warp a row, part after part, cost one token over 32,767 keys 6 us more).
+// store, so that none is lost).  Block (b, y) takes the rows (of the heads in turn) from y * take on of the tile that share b + 1 starts
+// in, if that is the tile's first cut; 8 / take warps share a row's parts, lane l takes channels 4 l .. 4 l + 3.  Bound by
+// latency: what it reads is asked for at once (a warp a row, part after part, cost one token over 32,767 keys 6 us more), and
+// blocks are few (one for each row of eight heads: 19 us more).
 constexpr int QJ_WARPS = 8;
-__global__ void __launch_bounds__(32 * QJ_WARPS) attn_qcache_join_kernel(const QcacheAttnParams p, int ctas, int rows) {
+__global__ void __launch_bounds__(32 * QJ_WARPS) attn_qcache_join_kernel(const QcacheAttnParams p, int ctas, int rows, int hg, int take) {
     __shared__ float4 sums[QJ_WARPS][32];
     __shared__ float2 refs[QJ_WARPS];
-    const int first = blockIdx.x + 1, row = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = p.Hq / p.Hk;
+    const int first = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = p.Hq / p.Hk;
+    const int group = QJ_WARPS / take, i = blockIdx.y * take + warp / group, row = i >> hg;   // of the tile's rows and heads
     const QsPartials part = qs_partials(p.workspace);
     await_stream();
     if (first == ctas) {
-        if (warp != 0 || row != 0) return;
+        if (warp != 0 || blockIdx.y != 0) return;
         uint32_t status = 0;
         for (int s = lane; s < ctas; s += 32) status |= part.cut[s].status;
         status = __reduce_or_sync(0xffffffffu, status);
@@ -631,7 +640,7 @@ __global__ void __launch_bounds__(32 * QJ_WARPS) attn_qcache_join_kernel(const Q
     QsCut before = part.cut[first - 1], e = part.cut[min(first + 1 + lane, ctas - 1)];
     if (c.j == 0) return;   // between two tiles, or nothing to do
     const int64_t at = (int64_t)c.tile * rows + row;
-    if (at >= (int64_t)c.lq * G) return;
+    const bool there = at < (int64_t)c.lq * G;
     auto inside = [&](const QsCut& a) { return a.n == c.n && a.kh == c.kh && a.tile == c.tile; };
     int b = first - 1;      // the share before it that is not empty
     while (b > 0 && before.some == 0) before = part.cut[--b];
@@ -648,16 +657,16 @@ __global__ void __launch_bounds__(32 * QJ_WARPS) attn_qcache_join_kernel(const Q
         end += 32;
         e = part.cut[min(end + lane, ctas - 1)];
     }
-    auto slot = [&](int s) { return (size_t)(2 * s + (s == b && !same ? 1 : 0)) * QS_MAX_ROWS + row; };
+    auto slot = [&](int s) { return (size_t)(2 * s + (s == b && !same ? 1 : 0)) * (rows / 8) * QS_MAX_ROWS + i; };
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-    for (int s0 = b + warp; s0 < end; s0 += 4 * QJ_WARPS) {
+    for (int s0 = b + warp % group; s0 < end && there; s0 += 4 * group) {
         float2 ml[4];
         float4 y[4];
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
-            const int s = s0 + d * QJ_WARPS;
+            const int s = s0 + d * group;
             ml[d] = make_float2(-INFINITY, 0.f);
             y[d] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (s < end && (s == b || part.cut[s].some)) {
@@ -680,14 +689,13 @@ __global__ void __launch_bounds__(32 * QJ_WARPS) attn_qcache_join_kernel(const Q
     sums[warp][lane] = o;
     if (lane == 0) refs[warp] = make_float2(m, l);
     __syncthreads();
-    if (warp != 0) return;
+    if (warp % group != 0 || !there) return;
     float top = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < QJ_WARPS; ++w) top = fmaxf(top, refs[w].x);
+    for (int w = warp; w < warp + group; ++w) top = fmaxf(top, refs[w].x);
     l = 0.f;
     o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < QJ_WARPS; ++w) {
+#pragma unroll 4
+    for (int w = warp; w < warp + group; ++w) {
         const float2 r = refs[w];
         const float4 y = sums[w][lane];
         const float f = r.x == -INFINITY ? 0.f : ex2_approx(r.x - top);
@@ -698,7 +706,7 @@ __global__ void __launch_bounds__(32 * QJ_WARPS) attn_qcache_join_kernel(const Q
         o.w = fmaf(f, y.w, o.w);
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int64_t tok = c.q0 + at / G, head = (int64_t)c.kh * G + at % G;
+    const int64_t tok = c.q0 + at / G, head = (int64_t)((c.kh << hg) + (i & ((1 << hg) - 1))) * G + at % G;
     *reinterpret_cast<uint2*>(p.out.data + tok * p.out.row + head * p.out.head + 4 * lane) =
         make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
     if (p.lse && lane == 0) p.lse[tok * p.Hq + head] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
@@ -715,14 +723,17 @@ bool encode_cache(CUtensorMap* m, const QcacheAttnParams& p, int rows) {
               CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kN>
+template <int kN, int kHg>
 cudaError_t launch(const QcacheAttnParams& p, int sms, cudaStream_t stream) {
     CUtensorMap map;
     if (!encode_cache(&map, p, SLICE)) return cudaErrorInvalidValue;
-    const int ctas = min(sms * (kN == 1 ? 2 : 1), QS_MAX_CTAS);
-    cudaError_t e = cudaFuncSetAttribute(attn_qcache_kernel<kN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)QsLayout<kN>::BYTES);
-    if (e == cudaSuccess) e = launch_early(attn_qcache_kernel<kN>, dim3((unsigned)ctas), QsLayout<kN>::THREADS, QsLayout<kN>::BYTES, stream, p, map);
-    if (e == cudaSuccess) e = launch_early(attn_qcache_join_kernel, dim3((unsigned)ctas, (unsigned)(8 * kN)), 32 * QJ_WARPS, 0, stream, p, ctas, 8 * kN);
+    const int ctas = min(sms * (kN == 1 ? 2 : 1), QS_MAX_CTAS / kN);
+    cudaError_t e = cudaFuncSetAttribute(attn_qcache_kernel<kN, kHg>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)QsLayout<kN>::BYTES);
+    if (e == cudaSuccess) e = launch_early(attn_qcache_kernel<kN, kHg>, dim3((unsigned)ctas), QsLayout<kN>::THREADS, QsLayout<kN>::BYTES, stream, p, map);
+    // eight warps a row where a tile may lie in many shares, else one
+    const int take = ctas > 8 * (int64_t)p.nseq * (p.Hk >> kHg) ? 1 : QJ_WARPS;
+    if (e == cudaSuccess)
+        e = launch_early(attn_qcache_join_kernel, dim3((unsigned)ctas, (unsigned)((8 * kN << kHg) / take)), 32 * QJ_WARPS, 0, stream, p, ctas, 8 * kN, kHg, take);
     return e;
 }
 
@@ -826,7 +837,7 @@ static Expanded expanded(int64_t S, int Hk, int nseq) {
 }
 
 size_t attn_qcache_workspace_bytes(int64_t Tq, int Hq, int Hk, int nseq, int64_t S) {
-    if (few_rows(Tq, Hq, Hk, nseq)) return QS_CUT_BYTES + QS_ML_BYTES + (size_t)2 * QS_MAX_CTAS * QS_MAX_ROWS * HD * sizeof(float);
+    if (few_rows(Tq, Hq, Hk, nseq)) return QS_CUT_BYTES + QS_ML_BYTES + (size_t)2 * QS_MAX_CTAS * QS_MAX_ROWS * HD * sizeof(float);   // (16 rows a tile: half as many CTAs)
     const Expanded x = expanded(S, Hk, nseq);
     return attn_workspace_bytes(Tq, Hq, Hk) + 256 + (size_t)(x.unit * nseq * x.heads);
 }
@@ -899,8 +910,14 @@ cudaError_t launch_attn_qcache(const QcacheAttnParams& p, cudaStream_t stream) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    if (p.Tq * (p.Hq / p.Hk) <= 8 * (int64_t)p.nseq) return launch<1>(p, sms, stream);
-    return launch<2>(p, sms, stream);
+    const bool single = p.Tq * (p.Hq / p.Hk) <= 8 * (int64_t)p.nseq;
+    // Two key heads together where the heads lie inside the rows (their bytes come with one another: 16 single tokens over up to
+    // 32,767, 102 -> 89 us) or a tile has 16 rows (half as many pieces: 24 x 4 drafts 47 -> 44 us), once there are enough
+    // (sequence, head) units that cutting them does not cost more (one token over 32,767: 23 -> 27 us; 8 over up to
+    // 16,000 28 -> 33; 128 units even)
+    if ((p.cache.head < p.cache.row || !single) && p.Hk % 2 == 0 && (int64_t)p.nseq * p.Hk >= 128)
+        return single ? launch<1, 1>(p, sms, stream) : launch<2, 1>(p, sms, stream);
+    return single ? launch<1, 0>(p, sms, stream) : launch<2, 0>(p, sms, stream);
 }
 
 }  // namespace kda
