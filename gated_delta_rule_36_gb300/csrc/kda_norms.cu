@@ -216,7 +216,12 @@ cudaError_t launch_residual(const ResidualNormParams& p, int sms, cudaStream_t s
 
 cudaError_t launch_gated_norm(const GatedNormParams& p, cudaStream_t stream) {
     if (p.tokens == 0) return cudaSuccess;
-    if (p.tokens * p.heads >= 152 * 64 * 4) return launch_gated<4>(p, stream);
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    // rows a half-warp takes: four once that still gives every SM eight blocks, else one, for the latency of small calls
+    if (p.tokens * p.heads >= (int64_t)sms * 8 * GN_HALVES * 4) return launch_gated<4>(p, stream);
     return launch_gated<1>(p, stream);
 }
 

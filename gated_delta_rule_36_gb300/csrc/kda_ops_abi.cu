@@ -157,6 +157,14 @@ bool overlap(const Extent& a, const Extent& b) {
     return a.run > 0 && b.run > 0 && meet(a, a.dims, b, b.dims, b.at - a.at);
 }
 
+// Whether a view may meet itself: a dimension steps by less than what lies below it.  Nothing is written through one.
+kda_status check_written(const char* name, const kda_view* t) {
+    const Extent e = extent(t);
+    for (int i = 0; i < e.dims && e.run > 0; ++i)
+        if (e.width[i] > e.step[i]) return fail(KDA_ERR_ALIAS, "%s: its elements overlap one another", name);
+    return KDA_OK;
+}
+
 bool same_view(const kda_view* a, const kda_view* b) {
     if (a->data != b->data || a->ndim != b->ndim) return false;
     for (int i = 0; i < a->ndim; ++i)
@@ -606,6 +614,7 @@ kda_status kda_qcache_append(const kda_view* k, const kda_view* v, const kda_vie
     const char* names[3] = {"cache", "k_out", "v_out"};
     for (int i = 0; i < 3; ++i) {
         if (!present(written[i])) continue;
+        KDA_TRY(check_written(names[i], written[i]));
         const Extent o = extent(written[i]);
         for (int j = 0; j < 2; ++j)
             if (overlap(o, extent(j ? v : k)) && !(i == j + 1 && same_view(written[i], j ? v : k)))
@@ -665,6 +674,7 @@ kda_status kda_attn_qcache_fwd(const kda_view* q, const kda_view* cache, float s
         const int64_t lshape[2] = {Tq, Hq};
         KDA_TRY(check_tensor("lse", lse, KDA_F32, 2, lshape, 4));
     }
+    KDA_TRY(check_written("out", out));
     for (const kda_view* t : {q, cache})
         if (overlap(extent(out), extent(t)) || (present(lse) && overlap(extent(lse), extent(t))))
             return fail(KDA_ERR_ALIAS, "out or lse overlaps an input");
@@ -709,6 +719,7 @@ kda_status kda_gated_norm(const kda_view* x, const kda_view* gate, const kda_ten
     KDA_TRY(check_view("gate", gate, 3, shape));
     KDA_TRY(check_view("out", out, 3, shape));
     if (present(weight)) KDA_TRY(check_tensor("weight", weight, KDA_F32, 1, wshape, 16));
+    KDA_TRY(check_written("out", out));
     const Extent o = extent(out);
     if (overlap(o, extent(x)) && !same_view(out, x)) return fail(KDA_ERR_ALIAS, "out overlaps x and is not exactly the same view");
     if (overlap(o, extent(gate)) && !same_view(out, gate)) return fail(KDA_ERR_ALIAS, "out overlaps gate and is not exactly the same view");

@@ -519,7 +519,9 @@ size_t kda_attn_qcache_workspace_size(int64_t Tq, int Hq, int Hk, int N, int64_t
  *   cu_seqlens_q   int64 [N + 1]; NULL/absent: Tq / N queries each
  *   workspace      >= kda_attn_qcache_workspace_size(Tq, Hq, Hk, N, S) bytes, 256-byte aligned
  * Cache rows past a sequence's keys are never used, whatever they hold; the scales and zeros inside a
- * sequence are taken to be finite.
+ * sequence are taken to be finite.  Queries are taken to be below 2^60 in size, scales and zeros below 2^50; values' scales
+ * below 2^-40 lose accuracy.  Weights are rounded to bf16 (few rows, see the workspace) or fp16 for the product with the
+ * values' codes or values; scores, softmax sums and the output's accumulation are fp32.  The same inputs give the same bits.
  */
 kda_status kda_attn_qcache_fwd(const kda_view* q, const kda_view* cache, float scale, const kda_view* out,
                                const kda_tensor* seqlens_k, const kda_tensor* lse, const kda_tensor* cu_seqlens_q,

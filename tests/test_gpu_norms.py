@@ -162,3 +162,26 @@ def test_residual_norm_of_zeros_nothing_and_bad_values():
     graph.replay()
     kda.kda_residual_norm(y2, z, None, want)
     assert torch.equal(out, want)
+
+
+def test_captured_and_replayed_over_many_tokens():
+    """More rows than one wave of blocks, in one graph, replayed on new inputs."""
+    g = gen_of(5)
+    T, dim, h = 3000, 1024, 40
+    y, res, w = rand(g, T, dim), rand(g, T, dim, dtype=torch.float32), rand(g, dim, dtype=torch.float32)
+    x, gate, out, out2 = rand(g, T, h, D), rand(g, T, h, D), nan(T, dim), nan(T, h, D)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kda.kda_residual_norm(y, res, w, out, scale=0.5)
+        kda.kda_gated_norm(x, gate, None, out2)
+    for t in (y, res, x, gate):
+        t.copy_(rand(g, *t.shape))
+    graph.replay()
+    want, want2 = nan(T, dim), nan(T, h, D)
+    kda.kda_residual_norm(y, res, w, want, scale=0.5)
+    kda.kda_gated_norm(x, gate, None, want2)
+    assert torch.equal(out, want) and torch.equal(out2, want2)
+    _, _, o, ob = ref_residual(y, res, None, None, 0.5, w, 1e-6)
+    within("out", out, o, ob)
+    ref, bound = ref_gated(x, gate, None, 1e-6, False)
+    within("gated", out2, ref, bound)

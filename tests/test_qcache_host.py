@@ -47,6 +47,8 @@ APPEND = [
     (dict(OUT, vo=view((T, HK, 128), 0)), ALIAS),
     (dict(OUT, ko=view((T, HK, 128), 256)), ALIAS),                                                             # k shifted
     (dict(OUT, vo=OUT["ko"]), ALIAS), (dict(OUT, ko=view((T, HK, 128), 20 * MB)), ALIAS), (dict(cache=cache(at=0)), ALIAS), (dict(cache=cache(at=MB)), ALIAS),
+    (dict(cache=cache(stride=(ROW, HK * ROW, ROW, 1))), ALIAS), (dict(cache=cache(stride=(S * HK * ROW, ROW, ROW, 1))), ALIAS),      # rows on one another
+    (dict(OUT, ko=view((T, HK, 128), 4 * MB, (128, 128, 1))), ALIAS),
     (dict(cache=cache(at=2 * MB - 1024)), ALIAS), (dict(cache=cache(at=3 * MB - 1024)), ALIAS), (dict(OUT, vo=view((T, HK, 128), 2 * MB - 256)), ALIAS),
 ]
 
@@ -80,6 +82,7 @@ ATTN = [
     (dict(out=view((T, HQ, 128), 0)), ALIAS), (dict(out=view((T, HQ, 128), 20 * MB)), ALIAS), (dict(out=view((T, HQ, 128), 2 * MB - 256)), ALIAS),
     (dict(out=view((T, HQ, 128), 3 * MB - 256)), ALIAS), (dict(out=view((T, HQ, 128), 4 * MB - 256)), ALIAS), (dict(lse=dense((T, HQ), 0)), ALIAS),
     (dict(lse=dense((T, HQ), 20 * MB)), ALIAS), (dict(lse=dense((T, HQ), 2 * MB - 16)), ALIAS),
+    (dict(out=view((T, HQ, 128), MB, (136, 128, 1))), ALIAS),                                       # heads of neighbouring tokens overlap
     (dict(ws=None), WORKSPACE), (dict(ws=BASE + 64 * MB + 16), WORKSPACE), (dict(nbytes=128), WORKSPACE),
 ]
 
@@ -111,6 +114,7 @@ GATED = [
     (dict(gate=view((T, HK, 128), MB + 8)), INVALID), (dict(out=view((T, HK, 128), 3 * MB, (0, 128, 1))), INVALID), (dict(w=dense((64,), 2 * MB)), INVALID),
     (dict(w=dense((128,), 2 * MB, BF)), INVALID), (dict(out=view((T, HK, 128), 256)), ALIAS), (dict(out=view((T, HK, 128), MB + 256)), ALIAS),
     (dict(out=view((T, HK, 128), 2 * MB)), ALIAS), (dict(x=view((T, 65536, 128), 0)), UNSUPPORTED),
+    (dict(out=view((T, HK, 128), 3 * MB, (128, 128, 1))), ALIAS),
 ]
 
 
