@@ -44,6 +44,10 @@
 // 704 against 696 us.  Two threads a row, each with half of the keys: 784 against 677 us; an
 // exponential with its scaling, sum and packing takes 7.3 cycles from one warp of a scheduler and 5.5 from
 // two, so that halves gain less than exchanging their maxima costs.
+//
+// Split keys (kSplit, launch_attn_split): the keys are two bf16 terms in two tiles, whose products with the queries go onto
+// the same scores, and the values are in fp16, scaled by a power of two for each block of keys; so are the weights then.
+// Half as many MMAs again.  The outputs carry the largest power so far; a block's weights take the difference.
 #include <cuda_fp16.h>
 #include <string.h>
 

@@ -1,5 +1,10 @@
 // The norms around a mixer: RMS norm of every head of its output times its activated gate, and the
-// norm after a block, its gate and residual scale, the residual sum and the norm before the next block.
+// norm after a block, its gate and residual scale, the residual sum and the norm before the next block.  Both are
+// bound by HBM: each number is read once and written once.
+//
+// 45,661 tokens x 64 heads (2.24 GB): 327 us, 6.9 TB/s (part of the writes is still in L2 at the end).  A stream of
+// 32,768 x 4,096 in bf16 with both norms (1.07 GB): 171 us, 6.3 TB/s; without the next row in flight, a block of 512 threads a row,
+// 211 us.  2,024 x 2,304 in fp32 with a gate (65 MB): 12 us, about half of it the start and the last rows.
 #include "kda_device.cuh"
 #include "kda_ops.h"
 

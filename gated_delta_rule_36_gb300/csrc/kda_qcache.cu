@@ -13,6 +13,10 @@
 // the largest, which makes the differences exact.  Other rows go a longer way: division,
 // differences rounded to odd (which keeps them on their side of every number of 13 bits), and halves where the
 // range passes fp32's.
+//
+// Bound by the instructions (issue 74 %, 190 for each key and value) about as much as by HBM: 45,661 tokens x 8 heads with the
+// values returned (427 MB) 78 us, 5.4 TB/s.  228 us with divisions, rounding to odd for every number and a search for each
+// row; 106 with four rows a warp, 93 with packed checks.
 #include "kda_qcache.cuh"
 
 namespace kda {
