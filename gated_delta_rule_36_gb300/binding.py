@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import struct
+import sys
 import threading
 from typing import Optional
 
@@ -463,6 +464,31 @@ def _workspace(workspace, nbytes, device, stream):
     return workspace
 
 
+# Workspaces of attention over a 4-bit cache: an allocation between two launches costs 8 us of host time, more than the
+# rest of the call, so the last one of every stream is kept (if it is small) and taken again once nobody else holds it.
+_KEPT, _KEPT_MOST = {}, 32 << 20
+_storage_uses = getattr(torch._C, "_storage_Use_Count", None)
+
+
+def _kept_workspace(nbytes, device, stream):
+    """A workspace from torch for a call on ``stream``.  On the current stream it is that of the stream's call before, if
+    neither the caller nor a view keeps it: what it held is used by earlier work of that stream only.  Calls that are
+    captured into a graph get their own, as memory of the graph."""
+    if stream is not None or nbytes > _KEPT_MOST or _storage_uses is None or torch._C._cuda_isCurrentStreamCapturing():
+        return _workspace(None, nbytes, device, stream)
+    key = (device, torch._C._cuda_getCurrentRawStream(device))
+    kept = _KEPT.get(key)
+    if kept is not None:
+        ws, uses = kept
+        # (the pair's reference, this one and the count's own; views hold the storage)
+        if ws.shape[0] >= nbytes and sys.getrefcount(ws) <= 3 and _storage_uses(ws.untyped_storage()._cdata) <= uses:
+            return ws
+    ws = _workspace(None, nbytes, device, None)
+    _storage_uses(ws.untyped_storage()._cdata)   # (asking once may make an object that stays)
+    _KEPT[key] = ws, _storage_uses(ws.untyped_storage()._cdata)
+    return ws
+
+
 def kda_qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, q_out, k_out, eps=1e-6, status=None, flags=0,
                      stream=None):
     """RMS norm of every head of q [T, Hq, 128] and k [T, Hk, 128] and the rotary rotation, in
@@ -571,17 +597,27 @@ def kda_attn_qcache_workspace_size(Tq: int, Hq: int, Hk: int, N: int, S: int) ->
     return int(load().kda_attn_qcache_workspace_size(int(Tq), int(Hq), int(Hk), int(N), int(S)))
 
 
+_QCACHE_SIZES = {}   # (Tq, Hq, Hk, N, S): bytes
+
+
 def kda_attn_qcache_fwd(q, cache, scale, out, seqlens_k, lse=None, cu_seqlens_q=None, workspace=None, stream=None):
     """Causal softmax attention with grouped heads over a cache in 4 bits: q, out [Tq, Hq, 128], cache uint8
     [N, S, Hk, KDA_QCACHE_ROW], seqlens_k [N].  Modes as kda_attn_fwd's over a cache, tensors as in
-    ``include/kda.h``.  Returns the workspace (its first word is the device status)."""
+    ``include/kda.h``.  Returns the workspace (its first word is the device status); one that is allocated here
+    serves the stream's next such call once it is dropped."""
     lib = _lib or load()
     dev = _device(q, "q")
     dq, dc = _view(q, "q", dev), _bytes_view(cache, "cache", dev)
     if workspace is None and q.dim() == 3:
-        n = cache.shape[0] if cu_seqlens_q is None else max(cu_seqlens_q.numel() - 1, 0)
-        nbytes = lib.kda_attn_qcache_workspace_size(q.shape[0], q.shape[1], cache.shape[2], n, cache.shape[1]) or 256   # 0: refused below
-        workspace = _workspace(None, nbytes, dev, stream)
+        nseq, S, Hk, _ = cache.shape
+        n = nseq if cu_seqlens_q is None else max(cu_seqlens_q.numel() - 1, 0)
+        sizes = (q.shape[0], q.shape[1], Hk, n, S)
+        nbytes = _QCACHE_SIZES.get(sizes)
+        if nbytes is None:
+            if len(_QCACHE_SIZES) > 4096:
+                _QCACHE_SIZES.clear()
+            nbytes = _QCACHE_SIZES[sizes] = lib.kda_attn_qcache_workspace_size(*sizes) or 256   # 0: refused below
+        workspace = _kept_workspace(nbytes, dev, stream)
     else:
         workspace = _workspace(workspace, 256, dev, stream)
     st = lib.kda_attn_qcache_fwd(dq, dc, scale, _view(out, "out", dev), _dense(seqlens_k, "seqlens_k", dev), _dense(lse, "lse", dev),

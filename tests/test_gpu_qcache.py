@@ -452,6 +452,42 @@ def test_on_another_stream():
         assert kda.kda_read_device_status(ws, stream=s) == 0 and torch.equal(out, want)
 
 
+def test_workspaces_are_kept_only_when_nobody_holds_them():
+    g = gen_of(26)
+    lens_k = [900, 33, 5000]
+    cache, q, lens = filled(g, lens_k, 4, "heads"), rand(g, 3, 16, D), i64(lens_k)
+    out = torch.empty_like(q)
+    call = lambda **kw: kda.kda_attn_qcache_fwd(q, cache, 0.1, out, lens, **kw)
+    at = call().data_ptr()
+    assert call().data_ptr() == at                                   # dropped: taken again
+    held = call()
+    second = call()
+    assert second.data_ptr() != held.data_ptr()
+    view, ptr = second[:4], second.data_ptr()
+    del second
+    assert call().data_ptr() != ptr                                  # a view keeps it too
+    bad = i64([1 << 40, 1, 1])
+    first = kda.kda_attn_qcache_fwd(q, cache, 0.1, out, bad)
+    call()
+    assert kda.kda_read_device_status(first) == BITS                 # a later call does not overwrite a status that is held
+    assert kda.kda_read_device_status(view) == 0
+    mine = call().data_ptr()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        other = call().data_ptr()
+        assert call().data_ptr() == other != mine                    # a stream's own
+    torch.cuda.synchronize()
+    assert call(stream=s).data_ptr() not in (mine, other)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = call().data_ptr()
+    assert captured not in (mine, other)
+    want = out.clone()
+    graph.replay()
+    assert torch.equal(out, want)
+
+
 def test_a_cache_past_32_bits():
     """Rows whose byte offsets pass 2^32, in both the sequence and the row direction."""
     g = gen_of(23)
