@@ -842,51 +842,68 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const AttnParams p,
 }
 
 // Joins the partial rows of the pairs that several shares hold (and, the last block, the shares' status bits: one store,
-// so that none is lost).  Block (b, y) takes `rows` rows of the
+// so that none is lost).  Block (b, y) takes 32 rows of the
 // pair that share b + 1 starts in, if that is the pair's first cut; a warp takes four of them, lane l
 // their channels 4 l .. 4 l + 3.  Bound by latency: little code (it is fetched cold) and few loads
 // in a row.
-// (With split keys a block takes 8 rows: continued prompts 743 -> 730 us; single tokens over a bf16 cache
-// 43 -> 50 us, so elsewhere it is 32.)
-constexpr int JOIN_THREADS = 256;
-__global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParams p, int ctas, int rows) {
+constexpr int JOIN_THREADS = 256, JOIN_ROWS = 32;
+// The parts of the pair that share `first` starts in, if that is the pair's first cut: share b's last piece (or its first one: `same`),
+// then the first pieces of the shares before `end`, empty ones between.
+struct Parts {
+    Cut c;
+    int b, end;
+    bool same;
+    __device__ size_t slot(int s) const { return (size_t)(2 * s + (s == b && !same ? 1 : 0)); }
+};
+__device__ __forceinline__ bool find_parts(const Partials& part, int first, int ctas, Parts& r) {
+    const int lane = threadIdx.x & 31;
+    r.c = part.cut[first];
+    Cut before = part.cut[first - 1];
+    Cut e = part.cut[min(first + lane, ctas - 1)];
+    if (r.c.j == 0) return false;                // between two pairs, or nothing to do
+    // the share before it that is not empty starts at or before the pair, or that cut was the first
+    r.b = first - 1;
+    while (r.b > 0 && before.nb == 0) before = part.cut[--r.b];
+    auto inside = [&](const Cut& a) { return a.q0 == r.c.q0 && a.lq == r.c.lq && a.kh == r.c.kh && a.pair == r.c.pair; };
+    r.same = inside(before);
+    if (r.same && before.j > 0) return false;
+    r.end = first;
+    for (;;) {
+        const uint32_t past = __ballot_sync(0xffffffffu, r.end + lane >= ctas || (e.nb != 0 && (e.j == 0 || !inside(e))));
+        if (past) {
+            r.end += __ffs(past) - 1;
+            return true;
+        }
+        r.end += 32;
+        e = part.cut[min(r.end + lane, ctas - 1)];
+    }
+}
+// The shares' status bits.
+__device__ __forceinline__ void join_status(const AttnParams& p, const Partials& part, int ctas) {
+    const int lane = threadIdx.x & 31;
+    uint32_t status = 0;
+    for (int s = lane; s < ctas; s += 32) status |= part.cut[s].status;
+    status = __reduce_or_sync(0xffffffffu, status);
+    if (lane == 0) *p.status = p.keep_status ? *p.status | status : status;
+}
+
+__global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParams p, int ctas) {
     const int first = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int G = p.Hq / p.Hk, tq = 128 / G;
     const Partials part = partials(p.workspace);
     await_stream();
     if (first == ctas) {
-        if (blockIdx.y != 0 || warp != 0) return;
-        uint32_t status = 0;
-        for (int s = lane; s < ctas; s += 32) status |= part.cut[s].status;
-        status = __reduce_or_sync(0xffffffffu, status);
-        if (lane == 0) *p.status = p.keep_status ? *p.status | status : status;
+        if (blockIdx.y == 0 && warp == 0) join_status(p, part, ctas);
         return;
     }
-    const Cut c = part.cut[first];
-    Cut before = part.cut[first - 1];
-    Cut e = part.cut[min(first + lane, ctas - 1)];
-    if (c.j == 0) return;                        // between two pairs, or nothing to do
-    // the share before it that is not empty starts at or before the pair, or that cut was the first
-    int b = first - 1;
-    while (b > 0 && before.nb == 0) before = part.cut[--b];
-    auto inside = [&](const Cut& a) { return a.q0 == c.q0 && a.lq == c.lq && a.kh == c.kh && a.pair == c.pair; };
-    const bool same = inside(before);
-    if (same && before.j > 0) return;
-    // the parts: share b's last piece, then the first pieces of the shares that start inside the pair
-    int end = first;
-    for (;;) {
-        const uint32_t past = __ballot_sync(0xffffffffu, end + lane >= ctas || (e.nb != 0 && (e.j == 0 || !inside(e))));
-        if (past) {
-            end += __ffs(past) - 1;
-            break;
-        }
-        end += 32;
-        e = part.cut[min(end + lane, ctas - 1)];
-    }
-    auto slot = [&](int s) { return (size_t)(2 * s + (s == b && !same ? 1 : 0)); };
+    Parts r;
+    if (!find_parts(part, first, ctas, r)) return;
+    const Cut c = r.c;
+    const int b = r.b, end = r.end;
+    auto slot = [&](int s) { return r.slot(s); };
 #pragma unroll 1
-    for (int k = 0; k < rows; k += 8) {
-        const int row = blockIdx.y * rows + k + warp;
+    for (int k = 0; k < JOIN_ROWS / 8; ++k) {
+        const int row = blockIdx.y * JOIN_ROWS + 8 * k + warp;
         const int t = row >> 7, tok = (row & 127) / G, head = (row & 127) - tok * G;
         const int i = (2 * c.pair + t) * tq + tok;
         if (tok >= tq || i >= c.lq) continue;
@@ -938,6 +955,56 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParam
     }
 }
 
+// The same for pairs of many rows and few parts: a thread takes a row, block (b, y) its channels 16 y .. 16 y + 15, so that a
+// warp reads 512 bytes together, as they were written, and a row gets a whole sector.  (Continued prompts 740 -> 710 us; the join above took
+// some 40.)
+__global__ void __launch_bounds__(JOIN_THREADS, 4) attn_join_rows_kernel(const AttnParams p, int ctas) {
+    const int first = blockIdx.x + 1, row = threadIdx.x, G = p.Hq / p.Hk, tq = 128 / G;
+    const Partials part = partials(p.workspace);
+    await_stream();
+    if (first == ctas) {
+        if (blockIdx.y == 0 && row < 32) join_status(p, part, ctas);
+        return;
+    }
+    Parts r;
+    if (!find_parts(part, first, ctas, r)) return;
+    const int t = row >> 7, tok = (row & 127) / G, head = (row & 127) - tok * G, i = (2 * r.c.pair + t) * tq + tok;
+    if (tok >= tq || i >= r.c.lq) return;
+    float m = -INFINITY, l = 0.f;
+#pragma unroll 4
+    for (int s = r.b; s < r.end; ++s) {
+        if (s != r.b && part.cut[s].nb == 0) continue;
+        const float2 ml = part.ml[r.slot(s) * 256 + row];
+        if (ml.y != 0.f) m = fmaxf(m, ml.x);   // a part that saw no key has a sum of 0 (a NaN goes on into the results)
+    }
+    float4 o[4] = {};
+#pragma unroll 2
+    for (int s = r.b; s < r.end; ++s) {
+        if (s != r.b && part.cut[s].nb == 0) continue;
+        const float2 ml = part.ml[r.slot(s) * 256 + row];
+        if (ml.y == 0.f) continue;             // (its rows may not even be written)
+        const float w = exp2f(ml.x - m);
+        l = fmaf(w, ml.y, l);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float4 y = __ldcg(part.o + (r.slot(s) * 32 + 4 * blockIdx.y + k) * 256 + row);
+            o[k].x = fmaf(w, y.x, o[k].x);
+            o[k].y = fmaf(w, y.y, o[k].y);
+            o[k].z = fmaf(w, y.z, o[k].z);
+            o[k].w = fmaf(w, y.w, o[k].w);
+        }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int64_t q = r.c.q0 + i;
+    const int h = r.c.kh * G + head;
+    uint4* dst = reinterpret_cast<uint4*>(p.out.data + q * p.out.row + h * p.out.head + 16 * blockIdx.y);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        dst[k] = make_uint4(pack_bf16x2(o[2 * k].x * inv, o[2 * k].y * inv), pack_bf16x2(o[2 * k].z * inv, o[2 * k].w * inv),
+                            pack_bf16x2(o[2 * k + 1].x * inv, o[2 * k + 1].y * inv), pack_bf16x2(o[2 * k + 1].z * inv, o[2 * k + 1].w * inv));
+    if (p.lse && blockIdx.y == 0) p.lse[q * p.lse_row + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
 }  // namespace
 
 size_t attn_workspace_bytes(int64_t, int, int) {
@@ -965,8 +1032,7 @@ static cudaError_t launch(const AttnParams& p, cudaStream_t stream) {
     e = launch_early(attn_kernel<kSplit>, dim3((unsigned)ctas), AT_THREADS, Layout<kSplit>::SMEM, stream, p, maps,
                      ctas > 1 ? ~0ull / (uint64_t)ctas + 1 : (uint64_t)0);
     if (e != cudaSuccess) return e;
-    const int rows = kSplit ? 8 : 32;
-    return launch_early(attn_join_kernel, dim3((unsigned)ctas, 256 / rows), JOIN_THREADS, 0, stream, p, ctas, rows);
+    return launch_early(kSplit ? attn_join_rows_kernel : attn_join_kernel, dim3((unsigned)ctas, kSplit ? HD / 16 : 256 / JOIN_ROWS), JOIN_THREADS, 0, stream, p, ctas);
 }
 
 cudaError_t launch_attn(const AttnParams& p, cudaStream_t stream) { return launch<false>(p, stream); }
