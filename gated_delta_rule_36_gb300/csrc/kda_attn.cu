@@ -200,6 +200,7 @@ struct Share {
     Cursor at;          // where it starts
     bool bad;           // lengths that contradict the tensors
 };
+template <bool kSplit>
 __device__ Share find_share(const AttnParams& p, int tq, int G, uint64_t recip, int64_t* scratch /* 48 */) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tp = 2 * tq;
     const int per = (p.nseq + AT_THREADS - 1) / AT_THREADS;
@@ -286,9 +287,10 @@ __device__ Share find_share(const AttnParams& p, int tq, int G, uint64_t recip, 
     const int from = open ? 0 : (int)(at - start[e]);   // the pair's own weight is at its front
     u.j = max(from - PIECE, 0);
     // A cut near the end of a pair moves there: a pair that is cut costs its rows' partial results,
-    // written and read again (about six steps' time for 256 rows).  Both neighbours find the same.
+    // written and read again (about six steps' time for 256 rows; with the steps and the join of split keys two: a prompt of
+    // 1,000 behind 15,000, 8 heads on one, 87 -> 78 us).  Both neighbours find the same.
     int64_t x = (e ? x1 : x0) - (u.j > 0 ? 0 : from);
-    const int nb = blocks_seen(u.s, (u.pair + 1) * tp), near = 6 * min(min(u.s.lq - u.pair * tp, tp) * G, 256) >> 8;
+    const int nb = blocks_seen(u.s, (u.pair + 1) * tp), near = (kSplit ? 2 : 6) * min(min(u.s.lq - u.pair * tp, tp) * G, 256) >> 8;
     bool over = false;
     if (u.j > 0 && !open) {
         if (u.j <= near && u.j <= nb - u.j) x -= from, u.j = 0;
@@ -805,7 +807,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_kernel(const AttnParams p,
     }
     tc_fence_before();
     await_stream();
-    const Share share = find_share(p, x.tq, x.G, recip, reinterpret_cast<int64_t*>(smem_raw + L::OFF_SCRATCH));
+    const Share share = find_share<kSplit>(p, x.tq, x.G, recip, reinterpret_cast<int64_t*>(smem_raw + L::OFF_SCRATCH));
     const Cursor u = share.at;
     __syncthreads();
     tc_fence_after();
@@ -955,9 +957,9 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParam
     }
 }
 
-// The same for pairs of many rows and few parts: a thread takes a row, block (b, y) its channels 16 y .. 16 y + 15, so that a
-// warp reads 512 bytes together, as they were written, and a row gets a whole sector.  (Continued prompts 740 -> 710 us; the join above took
-// some 40.)
+// The same for pairs of many rows: a thread takes a row, block (b, y) its channels 8 y .. 8 y + 7, so that a
+// warp reads 512 bytes together, as they were written; four parts are asked for at once.  (Continued prompts 740 -> 703 us; the join
+// above took some 40.)
 __global__ void __launch_bounds__(JOIN_THREADS, 4) attn_join_rows_kernel(const AttnParams p, int ctas) {
     const int first = blockIdx.x + 1, row = threadIdx.x, G = p.Hq / p.Hk, tq = 128 / G;
     const Partials part = partials(p.workspace);
@@ -971,37 +973,49 @@ __global__ void __launch_bounds__(JOIN_THREADS, 4) attn_join_rows_kernel(const A
     const int t = row >> 7, tok = (row & 127) / G, head = (row & 127) - tok * G, i = (2 * r.c.pair + t) * tq + tok;
     if (tok >= tq || i >= r.c.lq) return;
     float m = -INFINITY, l = 0.f;
-#pragma unroll 4
-    for (int s = r.b; s < r.end; ++s) {
-        if (s != r.b && part.cut[s].nb == 0) continue;
-        const float2 ml = part.ml[r.slot(s) * 256 + row];
-        if (ml.y != 0.f) m = fmaxf(m, ml.x);   // a part that saw no key has a sum of 0 (a NaN goes on into the results)
-    }
-    float4 o[4] = {};
-#pragma unroll 2
-    for (int s = r.b; s < r.end; ++s) {
-        if (s != r.b && part.cut[s].nb == 0) continue;
-        const float2 ml = part.ml[r.slot(s) * 256 + row];
-        if (ml.y == 0.f) continue;             // (its rows may not even be written)
-        const float w = exp2f(ml.x - m);
-        l = fmaf(w, ml.y, l);
+    float4 o[2] = {};
+#pragma unroll 1
+    for (int s0 = r.b; s0 < r.end; s0 += 4) {
+        float2 ml[4];
+        float4 y[4][2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float4 y = __ldcg(part.o + (r.slot(s) * 32 + 4 * blockIdx.y + k) * 256 + row);
-            o[k].x = fmaf(w, y.x, o[k].x);
-            o[k].y = fmaf(w, y.y, o[k].y);
-            o[k].z = fmaf(w, y.z, o[k].z);
-            o[k].w = fmaf(w, y.w, o[k].w);
+        for (int d = 0; d < 4; ++d) {
+            const int s = s0 + d;
+            ml[d] = make_float2(-INFINITY, 0.f);
+            if (s < r.end && (s == r.b || part.cut[s].nb != 0)) {
+                ml[d] = __ldcg(part.ml + r.slot(s) * 256 + row);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) y[d][k] = __ldcg(part.o + (r.slot(s) * 32 + 2 * blockIdx.y + k) * 256 + row);
+            }
+        }
+        float top = m;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) top = ml[d].y != 0.f ? fmaxf(top, ml[d].x) : top;   // a part that saw no key has a sum of 0 (a NaN goes on into the results)
+        const float old = m == -INFINITY ? 0.f : exp2f(m - top);
+        m = top;
+        l *= old;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) o[k].x *= old, o[k].y *= old, o[k].z *= old, o[k].w *= old;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            if (ml[d].y == 0.f) continue;   // (its rows may not even be written)
+            const float w = exp2f(ml[d].x - m);
+            l = fmaf(w, ml[d].y, l);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                o[k].x = fmaf(w, y[d][k].x, o[k].x);
+                o[k].y = fmaf(w, y[d][k].y, o[k].y);
+                o[k].z = fmaf(w, y[d][k].z, o[k].z);
+                o[k].w = fmaf(w, y[d][k].w, o[k].w);
+            }
         }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const int64_t q = r.c.q0 + i;
     const int h = r.c.kh * G + head;
-    uint4* dst = reinterpret_cast<uint4*>(p.out.data + q * p.out.row + h * p.out.head + 16 * blockIdx.y);
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-        dst[k] = make_uint4(pack_bf16x2(o[2 * k].x * inv, o[2 * k].y * inv), pack_bf16x2(o[2 * k].z * inv, o[2 * k].w * inv),
-                            pack_bf16x2(o[2 * k + 1].x * inv, o[2 * k + 1].y * inv), pack_bf16x2(o[2 * k + 1].z * inv, o[2 * k + 1].w * inv));
+    *reinterpret_cast<uint4*>(p.out.data + q * p.out.row + h * p.out.head + 8 * blockIdx.y) =
+        make_uint4(pack_bf16x2(o[0].x * inv, o[0].y * inv), pack_bf16x2(o[0].z * inv, o[0].w * inv), pack_bf16x2(o[1].x * inv, o[1].y * inv),
+                   pack_bf16x2(o[1].z * inv, o[1].w * inv));
     if (p.lse && blockIdx.y == 0) p.lse[q * p.lse_row + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
@@ -1032,7 +1046,7 @@ static cudaError_t launch(const AttnParams& p, cudaStream_t stream) {
     e = launch_early(attn_kernel<kSplit>, dim3((unsigned)ctas), AT_THREADS, Layout<kSplit>::SMEM, stream, p, maps,
                      ctas > 1 ? ~0ull / (uint64_t)ctas + 1 : (uint64_t)0);
     if (e != cudaSuccess) return e;
-    return launch_early(kSplit ? attn_join_rows_kernel : attn_join_kernel, dim3((unsigned)ctas, kSplit ? HD / 16 : 256 / JOIN_ROWS), JOIN_THREADS, 0, stream, p, ctas);
+    return launch_early(kSplit ? attn_join_rows_kernel : attn_join_kernel, dim3((unsigned)ctas, kSplit ? HD / 8 : 256 / JOIN_ROWS), JOIN_THREADS, 0, stream, p, ctas);
 }
 
 cudaError_t launch_attn(const AttnParams& p, cudaStream_t stream) { return launch<false>(p, stream); }
