@@ -289,6 +289,10 @@ __global__ void __launch_bounds__(QsLayout<kN>::THREADS, kN == 1 ? 2 : 1) attn_q
         c.status = share.bad ? KDA_DEVERR_CU_SEQLENS : 0u;
         part.cut[blockIdx.x] = c;
     }
+    if (share.weight == 0) {   // (an empty share may lie between the parts of a tile)
+        if (tid < kN * QS_MAX_ROWS) part.ml[(size_t)2 * blockIdx.x * kN * QS_MAX_ROWS + tid] = make_float2(-INFINITY, 0.f);
+        return;
+    }
     // the warp's slices: loads run QS_STAGES ahead within a piece, and the next piece's first ones are under way while
     // the warps put this one's results together
     uint32_t used = 0;
@@ -624,20 +628,19 @@ __global__ void __launch_bounds__(QsLayout<kN>::THREADS, kN == 1 ? 2 : 1) attn_q
 }
 
 // Joins the partial rows of the tiles that several shares hold (and, the last block, the shares' status bits: one
-// store, so that none is lost).  Block (b, y) takes the rows (of the heads in turn) from y * take on of the tile that share b + 1 starts
-// in, if that is the tile's first cut; 8 / take warps share a row's parts, lane l takes channels 4 l .. 4 l + 3.  Bound by
-// latency: what it reads is asked for at once (a warp a row, part after part, cost one token over 32,767 keys 6 us more), and
-// blocks are few (one for each row of eight heads: 19 us more).
-constexpr int QJ_WARPS = 8;
-__global__ void __launch_bounds__(32 * QJ_WARPS) attn_qcache_join_kernel(const QcacheAttnParams p, int ctas, int rows, int hg, int take) {
-    __shared__ float4 sums[QJ_WARPS][32];
-    __shared__ float2 refs[QJ_WARPS];
+// store, so that none is lost).  Block b takes the tile that share b + 1 starts in, if that is the tile's first cut; a warp
+// takes a row of a head (two warps where there are more), lane l its channels 4 l .. 4 l + 3.  Bound by latency: what it
+// needs of the shares is asked for at once, then kParts parts at once, and blocks are few (one for each row: 2 to 7 us more;
+// reading part after part: one token over 32,767 6 us more).
+template <int kWarps, int kParts>
+__global__ void __launch_bounds__(32 * kWarps, 2) attn_qcache_join_kernel(const QcacheAttnParams p, int ctas, int rows, int hg) {
+    __shared__ float4 sums[kWarps][32];
+    __shared__ float2 refs[kWarps];
     const int first = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = p.Hq / p.Hk;
-    const int group = QJ_WARPS / take, i = blockIdx.y * take + warp / group, row = i >> hg;   // of the tile's rows and heads
     const QsPartials part = qs_partials(p.workspace);
     await_stream();
     if (first == ctas) {
-        if (warp != 0 || blockIdx.y != 0) return;
+        if (warp != 0) return;
         uint32_t status = 0;
         for (int s = lane; s < ctas; s += 32) status |= part.cut[s].status;
         status = __reduce_or_sync(0xffffffffu, status);
@@ -645,79 +648,106 @@ __global__ void __launch_bounds__(32 * QJ_WARPS) attn_qcache_join_kernel(const Q
         return;
     }
     const QsCut c = part.cut[first];
-    QsCut before = part.cut[first - 1], e = part.cut[min(first + 1 + lane, ctas - 1)];
+    QsCut before = part.cut[max(first - 1 - lane, 0)], e = part.cut[min(first + 1 + lane, ctas - 1)];
     if (c.j == 0) return;   // between two tiles, or nothing to do
-    const int64_t at = (int64_t)c.tile * rows + row;
-    const bool there = at < (int64_t)c.lq * G;
     auto inside = [&](const QsCut& a) { return a.n == c.n && a.kh == c.kh && a.tile == c.tile; };
-    int b = first - 1;      // the share before it that is not empty
-    while (b > 0 && before.some == 0) before = part.cut[--b];
-    const bool same = inside(before);
-    if (same && before.j > 0) return;
-    // the parts: share b's last piece, then the first pieces of the shares that start inside the tile (empty ones between)
-    int end = first + 1;
+    // the share before it that is not empty: it holds the tile's part before this one
+    int b = first - 1;
+    bool same = false;
     for (;;) {
-        const uint32_t past = __ballot_sync(0xffffffffu, end + lane >= ctas || (e.some && !(e.j > 0 && inside(e))));
-        if (past) {
-            end += __ffs(past) - 1;
+        const uint32_t some = __ballot_sync(0xffffffffu, b - lane >= 0 && before.some);
+        if (some) {
+            const int d = __ffs(some) - 1;
+            b -= d;
+            same = __shfl_sync(0xffffffffu, (int)inside(before), d);
+            if (same && __shfl_sync(0xffffffffu, before.j, d) > 0) return;   // an earlier cut's
             break;
         }
-        end += 32;
-        e = part.cut[min(end + lane, ctas - 1)];
+        b -= 32;
+        if (b < 0) return;   // (there is one)
+        before = part.cut[max(b - lane, 0)];
     }
-    auto slot = [&](int s) { return (size_t)(2 * s + (s == b && !same ? 1 : 0)) * (rows / 8) * QS_MAX_ROWS + i; };
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    // the parts: share b's last piece, then the first pieces of the shares that start inside the tile (empty ones between, which
+    // have left sums of zero)
+    int end = first + 1;
+    for (int base = first + 1;; base += 32) {
+        const bool part_of = base + lane < ctas && e.some && e.j > 0 && inside(e);
+        const uint32_t past = __ballot_sync(0xffffffffu, base + lane >= ctas || (e.some && !part_of));
+        const uint32_t parts = __ballot_sync(0xffffffffu, part_of) & (past ? (past & -past) - 1u : 0xffffffffu);
+        if (parts) end = base + 32 - __clz(parts);
+        if (past) break;
+        e = part.cut[min(base + 32 + lane, ctas - 1)];
+    }
+    const int count = 1 + end - first, group = rows << hg < kWarps ? kWarps / (rows << hg) : 1;
 #pragma unroll 1
-    for (int s0 = b + warp % group; s0 < end && there; s0 += 4 * group) {
-        float2 ml[4];
-        float4 y[4];
+    for (int i0 = 0; i0 < rows << hg; i0 += kWarps / group) {   // (one turn with 8 rows and 8 warps)
+        const int i = i0 + warp / group, row = i >> hg;
+        const int64_t at = (int64_t)c.tile * rows + row;
+        const bool there = at < (int64_t)c.lq * G;
+        auto slot = [&](int k) {
+            return (size_t)(k == 0 ? 2 * b + (same ? 0 : 1) : 2 * (first + k - 1)) * (rows / 8) * QS_MAX_ROWS + i;
+        };
+        float m = -INFINITY, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int k0 = warp % group; k0 < count && there; k0 += kParts * group) {
+            float2 ml[kParts];
+            float4 y[kParts];
 #pragma unroll
-        for (int d = 0; d < 4; ++d) {
-            const int s = s0 + d * group;
-            ml[d] = make_float2(-INFINITY, 0.f);
-            y[d] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (s < end && (s == b || part.cut[s].some)) {
-                ml[d] = __ldcg(part.ml + slot(s));
-                y[d] = __ldcg(reinterpret_cast<const float4*>(part.o + slot(s) * 128 + 4 * lane));
+            for (int d = 0; d < kParts; ++d) {
+                const int k = k0 + d * group;
+                ml[d] = make_float2(-INFINITY, 0.f);
+                if (k < count) {
+                    ml[d] = __ldcg(part.ml + slot(k));
+                    y[d] = __ldcg(reinterpret_cast<const float4*>(part.o + slot(k) * 128 + 4 * lane));
+                }
+            }
+            float top = m;
+#pragma unroll
+            for (int d = 0; d < kParts; ++d) top = fmaxf(top, ml[d].x);
+            const float old = m == -INFINITY ? 0.f : ex2_approx(m - top);
+            m = top;
+            l *= old;
+            o.x *= old, o.y *= old, o.z *= old, o.w *= old;
+#pragma unroll
+            for (int d = 0; d < kParts; ++d) {
+                if (ml[d].x == -INFINITY) continue;   // a part that saw no key, or an empty share
+                const float w = ex2_approx(ml[d].x - m);
+                l = fmaf(w, ml[d].y, l);
+                o.x = fmaf(w, y[d].x, o.x);
+                o.y = fmaf(w, y[d].y, o.y);
+                o.z = fmaf(w, y[d].z, o.z);
+                o.w = fmaf(w, y[d].w, o.w);
             }
         }
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-            if (ml[d].x == -INFINITY) continue;   // a part that saw no key, or none
-            const float top = fmaxf(m, ml[d].x), old = m == -INFINITY ? 0.f : ex2_approx(m - top), w = ex2_approx(ml[d].x - top);
-            m = top;
-            l = fmaf(l, old, w * ml[d].y);
-            o.x = fmaf(o.x, old, w * y[d].x);
-            o.y = fmaf(o.y, old, w * y[d].y);
-            o.z = fmaf(o.z, old, w * y[d].z);
-            o.w = fmaf(o.w, old, w * y[d].w);
+        if (group > 1) {   // the row's warps, in order
+            sums[warp][lane] = o;
+            if (lane == 0) refs[warp] = make_float2(m, l);
+            __syncthreads();
+            if (warp % group != 0) continue;
+            const float mine = m;
+            for (int w = warp + 1; w < warp + group; ++w) m = fmaxf(m, refs[w].x);
+            const float f = mine == -INFINITY ? 0.f : ex2_approx(mine - m);
+            l *= f;
+            o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+            for (int w = warp + 1; w < warp + group; ++w) {
+                const float2 r = refs[w];
+                const float4 y = sums[w][lane];
+                const float g = r.x == -INFINITY ? 0.f : ex2_approx(r.x - m);
+                l = fmaf(g, r.y, l);
+                o.x = fmaf(g, y.x, o.x);
+                o.y = fmaf(g, y.y, o.y);
+                o.z = fmaf(g, y.z, o.z);
+                o.w = fmaf(g, y.w, o.w);
+            }
         }
+        if (!there) continue;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int64_t tok = c.q0 + at / G, head = (int64_t)((c.kh << hg) + (i & ((1 << hg) - 1))) * G + at % G;
+        *reinterpret_cast<uint2*>(p.out.data + tok * p.out.row + head * p.out.head + 4 * lane) =
+            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        if (p.lse && lane == 0) p.lse[tok * p.Hq + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
     }
-    sums[warp][lane] = o;
-    if (lane == 0) refs[warp] = make_float2(m, l);
-    __syncthreads();
-    if (warp % group != 0 || !there) return;
-    float top = -INFINITY;
-    for (int w = warp; w < warp + group; ++w) top = fmaxf(top, refs[w].x);
-    l = 0.f;
-    o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int w = warp; w < warp + group; ++w) {
-        const float2 r = refs[w];
-        const float4 y = sums[w][lane];
-        const float f = r.x == -INFINITY ? 0.f : ex2_approx(r.x - top);
-        l = fmaf(f, r.y, l);
-        o.x = fmaf(f, y.x, o.x);
-        o.y = fmaf(f, y.y, o.y);
-        o.z = fmaf(f, y.z, o.z);
-        o.w = fmaf(f, y.w, o.w);
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int64_t tok = c.q0 + at / G, head = (int64_t)((c.kh << hg) + (i & ((1 << hg) - 1))) * G + at % G;
-    *reinterpret_cast<uint2*>(p.out.data + tok * p.out.row + head * p.out.head + 4 * lane) =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (p.lse && lane == 0) p.lse[tok * p.Hq + head] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
 }
 
 // The cache in boxes of 144 bytes x 1 head x `rows` rows.
@@ -738,10 +768,10 @@ cudaError_t launch(const QcacheAttnParams& p, int sms, cudaStream_t stream) {
     const int ctas = min(sms * (kN == 1 ? 2 : 1), QS_MAX_CTAS / kN);
     cudaError_t e = cudaFuncSetAttribute(attn_qcache_kernel<kN, kHg>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)QsLayout<kN>::BYTES);
     if (e == cudaSuccess) e = launch_early(attn_qcache_kernel<kN, kHg>, dim3((unsigned)ctas), QsLayout<kN>::THREADS, QsLayout<kN>::BYTES, stream, p, map);
-    // eight warps a row where a tile may lie in many shares, else one
-    const int take = ctas > 8 * (int64_t)p.nseq * (p.Hk >> kHg) ? 1 : QJ_WARPS;
+    // many parts a tile where there are few units (one token over 2,000: 13.7 -> 11.3 us), else few (32 tokens 41.0 -> 39.5)
+    const bool many = ctas > 4 * (int64_t)p.nseq * (p.Hk >> kHg);
     if (e == cudaSuccess)
-        e = launch_early(attn_qcache_join_kernel, dim3((unsigned)ctas, (unsigned)((8 * kN << kHg) / take)), 32 * QJ_WARPS, 0, stream, p, ctas, 8 * kN, kHg, take);
+        e = launch_early(many ? attn_qcache_join_kernel<16, 8> : attn_qcache_join_kernel<8, 4>, dim3((unsigned)ctas), many ? 512 : 256, 0, stream, p, ctas, 8 * kN, kHg);
     return e;
 }
 
