@@ -16,7 +16,8 @@
 //
 // Bound by the instructions (issue 74 %, 190 for each key and value) about as much as by HBM: 45,661 tokens x 8 heads with the
 // values returned (427 MB) 78 us, 5.4 TB/s.  228 us with divisions, rounding to odd for every number and a search for each
-// row; 106 with four rows a warp, 93 with packed checks.
+// row; 106 with four rows a warp, 93 with packed checks.  Without the values 49 us (56 with their arithmetic left in).  16
+// channels a lane, a quarter of a warp a row: 78 as well, but one head 23 us (8 channels 13).
 #include "kda_qcache.cuh"
 
 namespace kda {
@@ -62,8 +63,8 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
     return *reinterpret_cast<const uint32_t*>(&m);
 }
 
-// kHeads: heads of a token that a warp takes, all loaded at once
-template <int kHeads>
+// kHeads: heads of a token that a warp takes, all loaded at once; kValues: what the cache then holds is written too
+template <int kHeads, bool kValues>
 __global__ void __launch_bounds__(QA_THREADS) qcache_append_kernel(const QcacheAppendParams p) {
     await_stream();
     const int lane = threadIdx.x & 31, half = lane >> 4;
@@ -97,7 +98,7 @@ __global__ void __launch_bounds__(QA_THREADS) qcache_append_kernel(const QcacheA
     if (c0 < 0 || (n == 0 && c0 != 0) || t < c0 || t >= c1 || c1 > p.T || s > p.S || s < c1 - c0) return;
     uint8_t* row = p.cache.data + n * p.cache.seq + (s - (c1 - t)) * p.cache.row + h0 * p.cache.head;
     const RowsView& out = half ? p.v_out : p.k_out;
-    __nv_bfloat16* dst = out.data ? out.data + t * out.row + h0 * out.head + 8 * (lane & 15) : nullptr;
+    __nv_bfloat16* dst = kValues ? out.data + t * out.row + h0 * out.head + 8 * (lane & 15) : nullptr;
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
         if (i >= heads) break;
@@ -127,19 +128,19 @@ __global__ void __launch_bounds__(QA_THREADS) qcache_append_kernel(const QcacheA
             for (int j = 7; j >= 0; --j) {
                 const float d = x[j] - lo, q0 = d * r, q = fmaf(fmaf(-q0, scale, d), r, q0) + 12582912.f;
                 sum = sum * 16 + __float_as_uint(q);   // (2^23 + 2^22: the last bits are the rounded quotient)
-                c[j] = fmaf(q - 12582912.f, scale, lo);
+                if (kValues) c[j] = fmaf(q - 12582912.f, scale, lo);
             }
             word = sum - 0x4b400000u * 0x11111111u;
-            y = make_uint4(pack_bf16x2(c[0], c[1]), pack_bf16x2(c[2], c[3]), pack_bf16x2(c[4], c[5]), pack_bf16x2(c[6], c[7]));
+            if (kValues) y = make_uint4(pack_bf16x2(c[0], c[1]), pack_bf16x2(c[2], c[3]), pack_bf16x2(c[4], c[5]), pack_bf16x2(c[6], c[7]));
         } else {
             const bool wide = range == INFINITY;   // the range passes fp32's: everything halved
             sz = finite ? pack_bf16x2(wide ? (hi * 0.5f - lo * 0.5f) / 7.5f : range / 15.f, lo) : 0x7fc07fc0u;
             word = codes_of_any(raw, lo, wide, bf16_lo(sz));
-            y = values_of(word, bf16_lo(sz), bf16_hi(sz));
+            if (kValues) y = values_of(word, bf16_lo(sz), bf16_hi(sz));
         }
         *reinterpret_cast<uint32_t*>(row + i * p.cache.head + 4 * lane) = word;
         if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(row + i * p.cache.head + QC_NUMBERS + (lane >> 1)) = sz;
-        if (dst) __stcs(reinterpret_cast<uint4*>(dst + i * out.head), y);
+        if (kValues) __stcs(reinterpret_cast<uint4*>(dst + i * out.head), y);
     }
 }
 
@@ -148,7 +149,8 @@ cudaError_t launch(const QcacheAppendParams& p, cudaStream_t stream) {
     int64_t blocks = (p.T * 32 + QA_THREADS - 1) / QA_THREADS;
     if (blocks == 0) blocks = 1;   // (the lengths are checked all the same)
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    return launch_early(qcache_append_kernel<kHeads>, dim3((unsigned)blocks, (unsigned)((p.Hk + kHeads - 1) / kHeads)), QA_THREADS, 0, stream, p);
+    return launch_early(p.k_out.data ? qcache_append_kernel<kHeads, true> : qcache_append_kernel<kHeads, false>,
+                        dim3((unsigned)blocks, (unsigned)((p.Hk + kHeads - 1) / kHeads)), QA_THREADS, 0, stream, p);
 }
 
 }  // namespace
