@@ -240,6 +240,9 @@ cudaError_t launch_residual_norm(const ResidualNormParams& p, cudaStream_t strea
     if (groups <= 32) return launch_residual<1, true, 128>(p, sms, stream);
     if (groups <= 128) return launch_residual<1, false, 128>(p, sms, stream);
     if (groups <= 512) return launch_residual<2, false, 256>(p, sms, stream);
+    // two groups a thread and up to 512 threads (8,192 in fp32 with a gate 6.4 TB/s, with four 5.5; bf16 without 6.1 and 5.8),
+    // but for bf16 with a gate, where four are faster (4,104 5.4 TB/s, with two 4.2; 8,192 6.1 and 5.7)
+    if (groups <= 1024 && (p.f32 || !p.gate)) return launch_residual<2, false, 512>(p, sms, stream);
     return launch_residual<4, false, 512>(p, sms, stream);
 }
 
