@@ -45,9 +45,10 @@
 // exponential with its scaling, sum and packing takes 7.3 cycles from one warp of a scheduler and 5.5 from
 // two, so that halves gain less than exchanging their maxima costs.
 //
-// Split keys (kSplit, launch_attn_split): the keys are two bf16 terms in two tiles, whose products with the queries go onto
-// the same scores, and the values are in fp16, scaled by a power of two for each block of keys; so are the weights then.
-// Half as many MMAs again.  The outputs carry the largest power so far; a block's weights take the difference.
+// Split keys (kSplit, launch_attn_split): all operands are in fp16 and scaled by powers of two, the values and keys for each block,
+// the queries for each row.  A block's scores take the powers in their scale, so m counts in steps of base 2; the outputs
+// carry the values' largest power so far, and a block's weights take the difference.  What the keys' 11 bits do not hold comes
+// as 16 more channels, one MMA on top of eight.
 #include <cuda_fp16.h>
 #include <string.h>
 
@@ -64,21 +65,23 @@ constexpr uint32_t TILE = 128 * 256, HALF = TILE / 2;
 // tokens 128, 105, 105 and 106 us.
 constexpr int PIECE = 2;
 constexpr uint32_t OFF_RING = 2 * TILE;       // behind the two query tiles
-constexpr int MAX_RING = 5;
-enum { FULL = 0, EMPTY = MAX_RING, QF = 2 * MAX_RING, QE, SF, PF = SF + 2, OF = PF + 4, SX = OF + 2, PX, PV = PX + 2, VZ, DRAIN, NBAR };
-// k and v of a block take two tiles of a ring of four; where the keys come as two terms (kSplit), three of five, which
-// leaves no room for staged results.
+constexpr int RING = 4;                        // tiles: k and v of two blocks
+enum { FULL = 0, EMPTY = RING, QF = 2 * RING, QE, SF, PF = SF + 2, OF = PF + 4, SX = OF + 2, PX, PV = PX + 2, VZ, DRAIN, NBAR };
+// Split keys: the rest of the queries' and keys' channels (16 more, without swizzle) has tiles of its own, which leaves no room
+// for staged results.
+constexpr uint32_t REST = 128 * 2 * SPLIT_REST;
 template <bool kSplit>
 struct Layout {
-    static constexpr int RING = kSplit ? 5 : 4, PER = kSplit ? 3 : 2;
     static constexpr uint32_t OFF_STAGE = OFF_RING + RING * TILE;           // 4 KB for each softmax warp: 32 rows of 128 bytes
+    static constexpr uint32_t OFF_K_REST = OFF_RING + RING * TILE;          // one for each tile of the ring
+    static constexpr uint32_t OFF_Q_REST = OFF_K_REST + RING * REST;
     // The search for the shares works here: its ordinary stores must not meet a tile's bulk loads, which
     // nothing but a proxy fence would order behind them.
-    static constexpr uint32_t OFF_SCRATCH = OFF_STAGE;
-    static constexpr uint32_t OFF_BAR = OFF_STAGE + (kSplit ? 512 : 8 * 4096);
+    static constexpr uint32_t OFF_SCRATCH = kSplit ? OFF_Q_REST + 2 * REST : OFF_STAGE;
+    static constexpr uint32_t OFF_BAR = kSplit ? OFF_SCRATCH + 512 : OFF_STAGE + 8 * 4096;
     static constexpr uint32_t OFF_TMEM = OFF_BAR + NBAR * 8;
     static constexpr uint32_t SMEM = OFF_TMEM + 8;
-    static_assert(OFF_SCRATCH >= OFF_RING + RING * TILE && OFF_SCRATCH + 48 * 8 <= OFF_BAR, "outside what bulk loads fill");
+    static_assert(OFF_SCRATCH >= (kSplit ? OFF_Q_REST + 2 * REST : OFF_RING + RING * TILE) && OFF_SCRATCH + 48 * 8 <= OFF_BAR, "outside what bulk loads fill");
     static_assert(SMEM <= 232448, "one CTA's shared memory");
 };
 // Tensor Memory (all 512 columns, so that its address is 0): two tiles of 128 columns each; P over
@@ -87,7 +90,7 @@ constexpr uint32_t TM_S = 0, TM_O = 256;
 
 struct AttnMaps {
     CUtensorMap q, k, v;
-    CUtensorMap k_low; // split keys: the second terms
+    CUtensorMap q_rest; // split keys: boxes of eight channels
     CUtensorMap out;   // boxes of a warp's 32 rows (used when G divides 32)
 };
 
@@ -287,8 +290,8 @@ __device__ Share find_share(const AttnParams& p, int tq, int G, uint64_t recip, 
     const int from = open ? 0 : (int)(at - start[e]);   // the pair's own weight is at its front
     u.j = max(from - PIECE, 0);
     // A cut near the end of a pair moves there: a pair that is cut costs its rows' partial results,
-    // written and read again (about six steps' time for 256 rows; with the steps and the join of split keys two: a prompt of
-    // 1,000 behind 15,000, 8 heads on one, 87 -> 78 us).  Both neighbours find the same.
+    // written and read again (about six steps' time for 256 rows; with the steps and the join of split keys two: 100 tokens
+    // behind 900, 32 heads on 8, 27 us instead of 33).  Both neighbours find the same.
     int64_t x = (e ? x1 : x0) - (u.j > 0 ? 0 : from);
     const int nb = blocks_seen(u.s, (u.pair + 1) * tp), near = (kSplit ? 2 : 6) * min(min(u.s.lq - u.pair * tp, tp) * G, 256) >> 8;
     bool over = false;
@@ -367,23 +370,28 @@ __device__ __forceinline__ void next_pair(const AttnParams& p, const Ctx& x, Cur
 }
 
 // ---------------------------------------------------------------- warp 8: loads
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
 template <bool kSplit>
 __device__ bool load_warp(const AttnParams& p, const AttnMaps& maps, const Ctx& x, Cursor u) {
     bool ok = true;
     if ((threadIdx.x & 31) == 0) {
         int slot = 0;
         uint32_t lap = 0, pieces = 0;
-        auto tile = [&](const CUtensorMap* m, int kh, int row, int n) {
+        auto tile = [&](const CUtensorMap* m, int kh, int row, int n, const __half* rest) {
             if (lap > 0 && !mx_wait_lane(x.bar(EMPTY + slot), (lap - 1) & 1u)) return false;
             const uint32_t dst = x.base + OFF_RING + slot * TILE, full = x.bar(FULL + slot);
             if (p.Tk == 0) {   // no row to read: every key is masked and the values are set to zero
                 mbar_arrive(full);
             } else {
-                mbar_arrive_expect_tx(full, TILE);
+                mbar_arrive_expect_tx(full, rest ? TILE + REST : TILE);
+                if (rest) bulk_load(x.base + Layout<kSplit>::OFF_K_REST + slot * REST, rest, REST, full);
                 tma_load_4d(dst, m, 0, kh, row, n, full);
                 tma_load_4d(dst + HALF, m, 64, kh, row, n, full);
             }
-            if (++slot == Layout<kSplit>::RING) slot = 0, ++lap;
+            if (++slot == RING) slot = 0, ++lap;
             return true;
         };
         for (int64_t left = x.weight; left > 0 && ok; next_pair(p, x, u), ++pieces) {
@@ -391,17 +399,22 @@ __device__ bool load_warp(const AttnParams& p, const AttnMaps& maps, const Ctx& 
             left -= r.weight;
             const int n = p.cache ? u.n : 0;
             for (int j = r.j0; j < r.j1 && ok; ++j) {
-                ok = tile(&maps.k, u.kh, u.s.k0 + j * KB, n) && (!kSplit || tile(&maps.k_low, u.kh, u.s.k0 + j * KB, n)) && tile(&maps.v, u.kh, u.s.k0 + j * KB, n);
+                const __half* rest = kSplit ? p.k_rest + (((int64_t)u.n * p.Hk + u.kh) * p.top_blocks + j) * (REST / 2) : nullptr;
+                ok = tile(&maps.k, u.kh, u.s.k0 + j * KB, n, rest) && tile(&maps.v, u.kh, u.s.k0 + j * KB, n, nullptr);
                 if (j > r.j0 || !ok) continue;
                 // the queries, once the last scores of the piece before are done
                 if (pieces > 0) ok = mx_wait_lane(x.bar(QE), (pieces - 1) & 1u);
                 if (!ok) break;
                 const int t0 = u.s.q0 + u.pair * x.tp;
-                const uint32_t bytes = (uint32_t)(x.tq * x.G) * 256u;
+                const uint32_t bytes = (uint32_t)(x.tq * x.G) * (256u + (kSplit ? 2 * SPLIT_REST : 0));
                 mbar_arrive_expect_tx(x.bar(QF), r.two ? 2 * bytes : bytes);
                 for (int t = 0; t < (r.two ? 2 : 1); ++t) {
                     tma_load_4d(x.base + t * TILE, &maps.q, 0, u.kh * x.G, t0 + t * x.tq, 0, x.bar(QF));
                     tma_load_4d(x.base + t * TILE + HALF, &maps.q, 64, u.kh * x.G, t0 + t * x.tq, 0, x.bar(QF));
+                    if (!kSplit) continue;
+                    const uint32_t rest_q = x.base + Layout<kSplit>::OFF_Q_REST + t * REST;   // eight channels: 128 rows of 16 bytes
+                    tma_load_4d(rest_q, &maps.q_rest, 0, u.kh * x.G, t0 + t * x.tq, 0, x.bar(QF));
+                    tma_load_4d(rest_q + REST / 2, &maps.q_rest, 8, u.kh * x.G, t0 + t * x.tq, 0, x.bar(QF));
                 }
             }
         }
@@ -412,7 +425,7 @@ __device__ bool load_warp(const AttnParams& p, const AttnMaps& maps, const Ctx& 
 // ---------------------------------------------------------------- warp 9: MMAs
 constexpr uint64_t K_STEP = 32 >> 4, K_HALF = HALF >> 4, MN_STEP = 2048 >> 4, D_TILE = TILE >> 4;
 constexpr uint32_t ID_KK = make_idesc_bf16_f32(128, 128), ID_MN = make_idesc_bf16_f32(128, 128, true);
-constexpr uint32_t ID_MN_F16 = ID_MN & ~(1u << 7 | 1u << 10);   // weights and values in fp16
+constexpr uint32_t F16 = ~(1u << 7 | 1u << 10);   // both operands in fp16
 
 // One warp for both tiles, strictly in turn: for each block P V of tile 0, the next scores of tile
 // 0 (over P: the MMAs of a thread go in order), P V of tile 1, the next scores of tile 1.  (Two
@@ -426,32 +439,30 @@ __device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
     const uint32_t lead = mx_leader();
     const uint64_t dQ = make_sdesc_kmajor_sw128(x.base), dK = make_sdesc_kmajor_sw128(x.base + OFF_RING);
     const uint64_t dV = make_sdesc_mnmajor_sw128(x.base + OFF_RING, HALF, 1024);
-    constexpr uint32_t RING = Layout<kSplit>::RING, PER = Layout<kSplit>::PER;
-    uint32_t it = 0;              // tiles of the ring before this piece: k (its two terms) and v alternate
+    const uint64_t dQR = make_sdesc_kmajor_noswizzle(x.base + Layout<kSplit>::OFF_Q_REST, REST / 2, 128);
+    const uint64_t dKR = make_sdesc_kmajor_noswizzle(x.base + Layout<kSplit>::OFF_K_REST, REST / 2, 128);
+    uint32_t it = 0;              // tiles of the ring before this piece: k and v alternate
     uint32_t pieces = 0, n0 = 0, n1 = 0, nX = 0, nZ = 0;
     // A wait's verdict is the lane's own (a vote each time would cost 3.5 % of a long prompt), so within a piece
     // nothing that the whole warp has to reach follows; the warp agrees at the piece's end.
     bool ok = true;
     // tile i of the piece has landed; its slot
     auto landed = [&](uint32_t i) { return mx_wait_lane(x.bar(FULL + (it + i) % RING), (it + i) / RING & 1u); };
-    auto keys_landed = [&](uint32_t j) { return landed(PER * j) && (!kSplit || landed(PER * j + 1)); };   // of block j
     auto slot = [&](uint32_t i) { return (int)((it + i) % RING); };
     auto scores = [&](int q, int t, int j, int done) {   // of query tile q with the keys of block j, into place t
-        const uint64_t a = dQ + q * D_TILE;
+        const uint64_t a = dQ + q * D_TILE, k = dK + slot(2 * j) * D_TILE;
+        constexpr uint32_t id = kSplit ? ID_KK & F16 : ID_KK;
 #pragma unroll
-        for (int term = 0; term < (kSplit ? 2 : 1); ++term) {
-            const uint64_t k = dK + slot(PER * j + term) * D_TILE;
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-                mx_mma_ss(lead, TM_S + 128 * t, a + (kk >> 2) * K_HALF + (kk & 3) * K_STEP, k + (kk >> 2) * K_HALF + (kk & 3) * K_STEP, ID_KK, kk > 0 || term > 0);
-        }
+        for (int kk = 0; kk < 8; ++kk)
+            mx_mma_ss(lead, TM_S + 128 * t, a + (kk >> 2) * K_HALF + (kk & 3) * K_STEP, k + (kk >> 2) * K_HALF + (kk & 3) * K_STEP, id, kk > 0);
+        if (kSplit) mx_mma_ss(lead, TM_S + 128 * t, dQR + q * (REST >> 4), dKR + slot(2 * j) * (REST >> 4), id, 1);
         mx_commit(lead, x.bar(done));
     };
     auto values = [&](int o, int t, int s, int half, bool first) {   // weights in place t, onto output o
         const uint64_t v = dV + s * D_TILE;
 #pragma unroll
         for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-            mx_mma_ts(lead, TM_O + 128 * o, TM_S + 128 * t + kk * 8, v + kk * MN_STEP, kSplit ? ID_MN_F16 : ID_MN, kk > 0 || !first);
+            mx_mma_ts(lead, TM_O + 128 * o, TM_S + 128 * t + kk * 8, v + kk * MN_STEP, kSplit ? ID_MN & F16 : ID_MN, kk > 0 || !first);
     };
     // (half of) the weights are in place, for the n-th time
     auto weights = [&](int done, uint32_t n) {
@@ -469,10 +480,10 @@ __device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
         // the values of block j have landed; those past the sequence's keys count for nothing,
         // whatever they hold
         auto next_values = [&](int j) {
-            if (!landed(PER * j + PER - 1)) return false;
+            if (!landed(2 * j + 1)) return false;
             const int valid = u.s.lk - (r.j0 + j) * KB;
             if (!kSplit && valid < KB) {   // (split keys and values: their rows are zeros there)
-                const uint32_t at = x.base + OFF_RING + slot(PER * j + PER - 1) * TILE;
+                const uint32_t at = x.base + OFF_RING + slot(2 * j + 1) * TILE;
 #pragma unroll 1
                 for (int row = max(valid, 0); row < KB; ++row) sts_u64(at + (lane >> 4) * HALF + row * 128 + (lane & 15) * 8, 0u, 0u);
                 fence_proxy_async_smem();
@@ -483,11 +494,10 @@ __device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
         };
         // the keys of block j are used; after the last ones the queries are too
         auto scored = [&](int j) {
-            mx_commit(lead, x.bar(EMPTY + slot(PER * j)));
-            if (kSplit) mx_commit(lead, x.bar(EMPTY + slot(PER * j + 1)));
+            mx_commit(lead, x.bar(EMPTY + slot(2 * j)));
             if (j + 1 == count) mx_commit(lead, x.bar(QE));
         };
-        ok = x.wait(QF, pieces) && __all_sync(0xffffffffu, keys_landed(0));
+        ok = x.wait(QF, pieces) && __all_sync(0xffffffffu, landed(0));
         if (!ok) break;
         if (!r.two) {
             // one tile: its scores alternate between the two places, so that the next block's are there
@@ -495,7 +505,7 @@ __device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
             scores(0, 0, 0, SF);
             scored(0);
             if (count > 1) {
-                ok = keys_landed(1);
+                ok = landed(2);
                 if (!ok) break;
                 scores(0, 1, 1, SX);
                 scored(1);
@@ -507,14 +517,14 @@ __device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
                 const int done = t ? PX : PF;
                 ok = next_values(j) && weights(done, n);
                 if (!ok) break;
-                values(0, t, slot(PER * j + PER - 1), 0, j == 0);
+                values(0, t, slot(2 * j + 1), 0, j == 0);
                 ok = weights(done + 1, n);
                 if (!ok) break;
-                values(0, t, slot(PER * j + PER - 1), 1, j == 0);
+                values(0, t, slot(2 * j + 1), 1, j == 0);
                 mx_commit(lead, x.bar(j + 1 == count ? OF : PV));
-                mx_commit(lead, x.bar(EMPTY + slot(PER * j + PER - 1)));
+                mx_commit(lead, x.bar(EMPTY + slot(2 * j + 1)));
                 if (j + 2 < count) {
-                    ok = keys_landed(j + 2);
+                    ok = landed(2 * j + 4);
                     if (!ok) break;
                     scores(0, t, j + 2, t ? SX : SF);
                     scored(j + 2);
@@ -528,7 +538,7 @@ __device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
 #pragma unroll 1
             for (int j = 0; ok; ++j) {
                 const bool more = j + 1 < count;
-                const int vs = slot(PER * j + PER - 1);
+                const int vs = slot(2 * j + 1);
                 if (j < c0) {
                     ok = weights(PF, n0);
                     if (!ok) break;
@@ -539,7 +549,7 @@ __device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
                     if (j + 1 == c0) mx_commit(lead, x.bar(OF));
                 }
                 if (more) {
-                    ok = keys_landed(j + 1);
+                    ok = landed(2 * j + 2);
                     if (!ok) break;
                     if (j + 1 < c0) scores(0, 0, j + 1, SF);
                 }
@@ -562,7 +572,7 @@ __device__ bool mma_warp(const AttnParams& p, const Ctx& x, Cursor u) {
         }
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        it += PER * count;
+        it += 2 * count;
     }
     __syncwarp();
     mx_commit(lead, x.bar(DRAIN));
@@ -574,6 +584,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
+}
+
+// x 2^e, e within 2 x (-126 .. 127)
+__device__ __forceinline__ float times_power(float x, int e) {
+    const int half = e >> 1;
+    return x * __uint_as_float((uint32_t)(127 + half) << 23) * __uint_as_float((uint32_t)(127 + e - half) << 23);
 }
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
@@ -606,8 +622,12 @@ __device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const C
         // split: a block's values are scaled by a power of two of its own (top[j]); the output by the largest so far
         const int* tops = kSplit ? p.top + ((int64_t)u.n * p.Hk + u.kh) * p.top_blocks : nullptr;
         int top_v = 0;
+        // ... and its keys and this query too: the exponents' scale is the block's, and m counts in steps of base 2
+        const int power_q = kSplit && mine ? __ldg(p.q_power + (u.s.q0 + i) * (int64_t)p.Hq + u.kh * x.G + head) - 127 - SPLIT_KEY : 0;
+        const float unit = kSplit ? 1.f : c;
         for (int j = r.j0; j < end; ++j) {
-            const int top_j = kSplit ? __ldg(tops + j) : 0;
+            const int tops_j = kSplit ? __ldg(tops + j) : 0, top_j = tops_j & 0xffff;
+            const float cj = kSplit ? fminf(fmaxf(times_power(c, power_q + (tops_j >> 16)), 1e-30f), 3e38f) : c;
             if (!x.wait(other ? SX : SF + t, other ? nX++ : nS++)) return false;
             tc_fence_after();
             const uint32_t tS = lanes + TM_S + 128 * (t + other);
@@ -627,18 +647,18 @@ __device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const C
             for (int k = 0; k < 128; k += 8)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], mx_u2f(s[k + 2 * e]), mx_u2f(s[k + 2 * e + 1]));
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            const float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), top = kSplit ? most * cj : most;
             // the output has to hold all earlier products before it is scaled: with two tiles these scores
             // came after them; with one they did not, and the product before has a barrier of its own
             if (!r.two && j > r.j0 && !x.wait(PV, nV++)) return false;
-            const bool grown = mine && (top - m) * c > 8.f;   // (m = -inf: whenever a key is seen)
+            const bool grown = mine && (top - m) * unit > 8.f;   // (m = -inf: whenever a key is seen)
             float lower = 1.f;
             if (kSplit) {
                 if (j > r.j0 && top_j > top_v) lower = __uint_as_float((uint32_t)max(127 + top_v - top_j, 1) << 23);
                 top_v = max(top_v, top_j);
             }
             if (__any_sync(0xffffffffu, grown || (kSplit && lower != 1.f))) {
-                float f = grown ? exp2f((m - top) * c) : 1.f;
+                float f = grown ? exp2f((m - top) * unit) : 1.f;
                 if (grown) m = top;
                 l *= f;
                 if (kSplit) f *= lower;
@@ -659,10 +679,10 @@ __device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const C
                     }
                 }
             }
-            float mc = m == -INFINITY ? 0.f : -m * c;
+            float mc = m == -INFINITY ? 0.f : -m * unit;
             const int less = kSplit ? max(top_j - top_v, -60) : 0;   // the weights take the difference of the powers
             if (kSplit) mc += (float)less;
-            const float2 c2 = make_float2(c, c), mc2 = make_float2(mc, mc);
+            const float2 c2 = make_float2(cj, cj), mc2 = make_float2(mc, mc);
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
@@ -771,8 +791,8 @@ __device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const C
             tc_fence_before();
         }
         if (mine) {
-            if (!r.whole) part.ml[part_slot * 256 + part_row] = make_float2(m * c, l);
-            else if (p.lse) p.lse[q * p.lse_row + h] = l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.6931471805599453f;
+            if (!r.whole) part.ml[part_slot * 256 + part_row] = make_float2(m * unit, l);
+            else if (p.lse) p.lse[q * p.lse_row + h] = l == 0.f ? -INFINITY : (m * unit + log2f(l)) * 0.6931471805599453f;
         }
     }
     if (lane == 0) bulk_wait_all();
@@ -958,8 +978,8 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParam
 }
 
 // The same for pairs of many rows: a thread takes a row, block (b, y) its channels 8 y .. 8 y + 7, so that a
-// warp reads 512 bytes together, as they were written; four parts are asked for at once.  (Continued prompts 740 -> 703 us; the join
-// above took some 40.)
+// warp reads 512 bytes together, as they were written; four parts are asked for at once.  (Continued prompts 740 -> 703 us at the
+// time; the join above took some 40.)
 __global__ void __launch_bounds__(JOIN_THREADS, 4) attn_join_rows_kernel(const AttnParams p, int ctas) {
     const int first = blockIdx.x + 1, row = threadIdx.x, G = p.Hq / p.Hk, tq = 128 / G;
     const Partials part = partials(p.workspace);
@@ -1033,7 +1053,7 @@ static cudaError_t launch(const AttnParams& p, cudaStream_t stream) {
     const int seqs = p.cache ? p.nseq : 1;
     if (!mx_encode(&maps.q, p.q.data, p.Hq, p.Tq, 1, p.q.head, p.q.row, 0, G, tq) ||
         !mx_encode(&maps.k, p.k, p.Hk, p.Tk, seqs, p.k_head, p.k_row, p.k_seq, 1, KB) ||
-        (kSplit && !mx_encode(&maps.k_low, p.k_low, p.Hk, p.Tk, seqs, p.k_head, p.k_row, p.k_seq, 1, KB)) ||
+        (kSplit && !mx_encode(&maps.q_rest, p.q_rest, p.Hq, p.Tq, 1, SPLIT_REST, (int64_t)SPLIT_REST * p.Hq, 0, G, tq, SPLIT_REST, 8)) ||
         !mx_encode(&maps.v, p.v, p.Hk, p.Tk, seqs, p.v_head, p.v_row, p.v_seq, 1, KB) ||
         !mx_encode_3d(&maps.out, p.out.data, p.Hq, p.Tq, p.out.head, p.out.row, G <= 32 ? G : 1, G <= 32 ? 32 / G : 1))
         return cudaErrorInvalidValue;

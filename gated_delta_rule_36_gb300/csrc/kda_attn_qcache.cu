@@ -28,10 +28,10 @@
 // 6, 10, 14, 20: 56, 47, 42, 42 us; drafts with 14, 20, 32, 44 on tiles of 16 rows: 67, 55, 48, 50).
 //
 // Bound by HBM between a start of about 2 us (the lengths, the search), some 3 us a tile (queries, the warps' results)
-// and the join (4 us): 32 single tokens over caches of 67 to 8,189, 32 heads on 8: 40 us (3.8 TB/s; 6.4 in the slices);
-// 16 over 5,002 to 32,767, 64 heads on 8, heads inside the rows: 88 us, where the 144 bytes of a head bring 21 %
-// of others with them (heads outside: 72 us, 4.8 TB/s); one token over 32,767: 18 us (20 through the Python call); 24 x 4 drafts:
-// 43 us, bound by latency with eight warps an SM.
+// and the join (3 us): 32 single tokens over caches of 67 to 8,189, 32 heads on 8: 40 us (3.8 TB/s; 6.4 in the slices);
+// 16 over 5,002 to 32,767, 64 heads on 8, heads inside the rows: 84 to 88 us, where the 144 bytes of a head bring 21 %
+// of others with them (heads outside: 72 us, 4.8 TB/s); one token over 32,767: 19 us (20 through the Python call), over 2,000 11 us;
+// 24 x 4 drafts: 43 us, bound by latency with eight warps an SM.
 
 #include <cuda_fp16.h>
 #include <string.h>
@@ -778,30 +778,100 @@ cudaError_t launch(const QcacheAttnParams& p, int sms, cudaStream_t stream) {
 // ---------------------------------------------------------------- many rows: expanded once, then the tensor cores
 // Many rows read a block of keys many times (a pair of query tiles each), so the codes are expanded once, for some key
 // heads at a time, into the workspace, and the kernel of kda_attn.cu runs on that.
-//   keys     scale code + zero in fp32, as two bf16 terms that both meet the queries: a single rounding of the keys would
-//            move the scores by up to 2^-9 of sum |q k| (measured: results off by 0.0042 of their norm, now 0.0017)
-//   values   in fp16, as are the weights that meet them (11 bits instead of 8: both roundings vanish beside the output's),
-//            a block of 128 scaled by the power of two that brings its largest below 2^(SPLIT_TOP + 1)
-// A CTA takes a block of keys of a head: half a warp a row, a lane eight channels of the key and of the value.  Bound by HBM
-// (144 bytes read and 768 written for each key and head).
+//   keys     y = scale (code - 8) in fp16, which is exact (8 bits times 4 with a sign, of which 8 is a power of two), and
+//            zero + 8 scale, constant over 64 channels: what it adds to a score is (zero + 8 scale) sum q, the sum in three terms
+//            of fp16, so 12 more channels hold zero and 8 scale of both halves against them.  (Keys rounded
+//            once to bf16 move the results by 0.0034 of their norm and lse by 1e-4.)
+//   values   in fp16, as are the weights that meet them (11 bits instead of 8: both roundings vanish beside the output's)
+//   queries  in fp16, which holds bf16's eight bits
+// all scaled by powers of two: a block of 128 keys and one of values each, so that its largest is below 2^(SPLIT_KEY + 1) and
+// 2^(SPLIT_TOP + 1), a query to below 2^9, so that 64 of them are below 2^15.  What is so much smaller than the largest that it loses bits
+// (2^-27 of it) is nothing beside the rounding of the sums.
+// A CTA takes a block of keys of a head: half a warp a row, a lane eight channels of the key and of the value; or 64 rows of
+// queries.  Bound by HBM (144 bytes read and 544 written for each key and head).  Prompts of 1,024, 517 and 33 behind 16,384,
+// 8,484 and 15,967, 64 heads on 8: 585 us; 700 with the keys as two terms of bf16, both multiplied with the queries (three products a
+// block instead of two and an eighth, and 768 bytes), 1,328 with codes expanded in the other kernel by four more warps.
 constexpr int EX_THREADS = 256, EX_BLOCK = 128, EX_ROWS = EX_BLOCK * 16 / EX_THREADS;   // rows of a thread
+constexpr int EX_QUERIES = 4;   // its rows of queries
+constexpr int QUERY_TOP = 8, QUERY_LEAST = 35;
 
 struct ExpandParams {
     QcacheView cache;
     const int64_t* seqlens_k;
     int64_t S;
     int head0, heads, blocks;       // blocks of a sequence
-    __nv_bfloat16 *k, *k_low;       // [nseq][heads][blocks * 128][128]
-    __half* v;
+    __half *k, *v;                  // [nseq][heads][blocks * 128][128]
+    __half* k_rest;                 // [nseq][heads][blocks][2][128][8]
     int* top;                       // [nseq][heads][blocks]
+    RowsView q;
+    int64_t query_rows, query_blocks;   // tokens times query heads of these key heads
+    int query_heads;
+    __half *q_to, *q_rest;          // [tokens][query_heads][128 and 16]
+    int* q_power;
 };
+
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
+    const __half2 y = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&y);
+}
+__device__ __forceinline__ float half_round(float x) { return __half2float(__float2half_rn(x)); }
+
+__device__ __forceinline__ void expand_queries(const ExpandParams& p, int64_t block) {
+    const int lane = threadIdx.x & 15;
+    const int64_t row0 = block * (EX_QUERIES * EX_THREADS / 16) + (threadIdx.x >> 4);
+    uint4 x[EX_QUERIES];
+#pragma unroll
+    for (int i = 0; i < EX_QUERIES; ++i) {
+        const int64_t row = row0 + i * (EX_THREADS / 16), t = row / p.query_heads;
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (row < p.query_rows) x[i] = *reinterpret_cast<const uint4*>(p.q.data + t * p.q.row + (row - t * p.query_heads) * p.q.head + 8 * lane);
+    }
+#pragma unroll
+    for (int i = 0; i < EX_QUERIES; ++i) {
+        const int64_t row = row0 + i * (EX_THREADS / 16);
+        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        uint32_t big = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) big = max(big, max(w[e] & 0x7fffu, w[e] >> 16 & 0x7fffu));   // (bf16's order is that of its bits)
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
+        const int top = max((int)(big >> 7), QUERY_LEAST);
+        const float lift = __uint_as_float((uint32_t)(127 + QUERY_TOP + 127 - top) << 23);
+        uint32_t y[4];
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float a = lift * bf16_lo(w[e]), b = lift * bf16_hi(w[e]);
+            y[e] = half2_of(a, b);
+            sum += a + b;
+        }
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float other = __shfl_xor_sync(0xffffffffu, sum, 8);   // lanes 0 .. 7 and 8 .. 15: a half each
+        if (row >= p.query_rows) continue;
+        *reinterpret_cast<uint4*>(p.q_to + row * HD + 8 * lane) = make_uint4(y[0], y[1], y[2], y[3]);
+        if (lane == 0) {
+            const float a1 = half_round(sum), a2 = half_round(sum - a1), a3 = sum - a1 - a2;
+            const float b1 = half_round(other), b2 = half_round(other - b1), b3 = other - b1 - b2;
+            uint4* rest = reinterpret_cast<uint4*>(p.q_rest + row * SPLIT_REST);
+            rest[0] = make_uint4(half2_of(a1, a2), half2_of(a3, a1), half2_of(a2, a3), half2_of(b1, b2));
+            rest[1] = make_uint4(half2_of(b3, b1), half2_of(b2, b3), 0, 0);
+            p.q_power[row] = top - 127 - QUERY_TOP;
+        }
+    }
+}
 
 __device__ __forceinline__ float code_at(uint32_t x, int bit) { return __uint_as_float((x >> bit & 15u) | 0x4b000000u) - 8388608.f; }
 
 __global__ void __launch_bounds__(EX_THREADS) qcache_expand_kernel(const ExpandParams p) {
-    __shared__ uint32_t most[EX_THREADS / 32];
+    __shared__ uint2 most[EX_THREADS / 32];
     await_stream();
     const int block = blockIdx.x, h = blockIdx.y, n = blockIdx.z;
+    if (block >= p.blocks) {
+        const int64_t b = ((int64_t)(block - p.blocks) * gridDim.z + n) * gridDim.y + h;
+        if (b < p.query_blocks) expand_queries(p, b);
+        return;
+    }
     const int64_t lk = min(max(p.seqlens_k[n], (int64_t)0), p.S);
     if (block > 0 && (int64_t)block * EX_BLOCK >= lk) return;   // (block 0 is read even if there are no keys)
     const int lane = threadIdx.x & 15, row0 = threadIdx.x >> 4;
@@ -820,47 +890,57 @@ __global__ void __launch_bounds__(EX_THREADS) qcache_expand_kernel(const ExpandP
             num[i] = *reinterpret_cast<const uint4*>(at + QC_NUMBERS);
         }
     }
-    float big = 0.f;
-#pragma unroll
-    for (int i = 0; i < EX_ROWS; ++i)
-        for (const uint32_t w : {num[i].z, num[i].w}) big = fmaxf(big, fmaxf(fabsf(bf16_hi(w)), fabsf(fmaf(15.f, bf16_lo(w), bf16_hi(w)))));
-    uint32_t all = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
-    if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = all;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < EX_THREADS / 32; ++w) all = max(all, most[w]);
-    const int top = max((int)(all >> 23), SPLIT_LEAST);
-    const int64_t unit = (int64_t)n * p.heads + h;
-    if (threadIdx.x == 0) p.top[unit * p.blocks + block] = top;
-    const float lift = __uint_as_float((uint32_t)(127 + SPLIT_TOP + 127 - top) << 23);
+    auto largest = [](float most, uint32_t w) { return fmaxf(most, fmaxf(fabsf(bf16_hi(w)), fabsf(fmaf(15.f, bf16_lo(w), bf16_hi(w))))); };
+    float big_k = 0.f, big_v = 0.f;
 #pragma unroll
     for (int i = 0; i < EX_ROWS; ++i) {
-        const int64_t at = ((unit * p.blocks + block) * EX_BLOCK + row0 + i * (EX_THREADS / 16)) * HD + 8 * lane;
+        big_k = largest(largest(big_k, num[i].x), num[i].y);
+        big_v = largest(largest(big_v, num[i].z), num[i].w);
+    }
+    uint32_t all_k = __reduce_max_sync(0xffffffffu, __float_as_uint(big_k)), all_v = __reduce_max_sync(0xffffffffu, __float_as_uint(big_v));
+    if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = make_uint2(all_k, all_v);
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < EX_THREADS / 32; ++w) all_k = max(all_k, most[w].x), all_v = max(all_v, most[w].y);
+    const int top_k = max((int)(all_k >> 23), SPLIT_KEY_LEAST), top_v = max((int)(all_v >> 23), SPLIT_LEAST);
+    const int64_t unit = ((int64_t)n * p.heads + h) * p.blocks + block;
+    if (threadIdx.x == 0) p.top[unit] = top_k << 16 | top_v;
+    const float lift_k = __uint_as_float((uint32_t)(127 + SPLIT_KEY + 127 - top_k) << 23);
+    const float lift_v = __uint_as_float((uint32_t)(127 + SPLIT_TOP + 127 - top_v) << 23);
+#pragma unroll
+    for (int i = 0; i < EX_ROWS; ++i) {
+        const int row = row0 + i * (EX_THREADS / 16);
+        const int64_t at = (unit * EX_BLOCK + row) * HD + 8 * lane;
         const bool upper = lane >= 8;
         const uint32_t kn = upper ? num[i].y : num[i].x, vn = upper ? num[i].w : num[i].z;
-        const float ks = bf16_lo(kn), kz = bf16_hi(kn), vs = lift * bf16_lo(vn), vz = lift * bf16_hi(vn);
-        uint32_t hi[4], lo[4], v[4];
+        const float ks = lift_k * bf16_lo(kn), k8 = -8.f * ks, vs = lift_v * bf16_lo(vn), vz = lift_v * bf16_hi(vn);
+        uint32_t k[4], v[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const float a = fmaf(code_at(kc[i], 8 * e), ks, kz), b = fmaf(code_at(kc[i], 8 * e + 4), ks, kz);
-            hi[e] = pack_bf16x2(a, b);
-            lo[e] = pack_bf16x2(a - bf16_lo(hi[e]), b - bf16_hi(hi[e]));
-            const __half2 y = __floats2half2_rn(fmaf(code_at(vc[i], 8 * e), vs, vz), fmaf(code_at(vc[i], 8 * e + 4), vs, vz));
-            v[e] = *reinterpret_cast<const uint32_t*>(&y);
+            k[e] = half2_of(fmaf(code_at(kc[i], 8 * e), ks, k8), fmaf(code_at(kc[i], 8 * e + 4), ks, k8));
+            v[e] = half2_of(fmaf(code_at(vc[i], 8 * e), vs, vz), fmaf(code_at(vc[i], 8 * e + 4), vs, vz));
         }
-        *reinterpret_cast<uint4*>(p.k + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(p.k_low + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        *reinterpret_cast<uint4*>(p.k + at) = make_uint4(k[0], k[1], k[2], k[3]);
         *reinterpret_cast<uint4*>(p.v + at) = make_uint4(v[0], v[1], v[2], v[3]);
+        if (lane < 2) {   // the channels against a query's sums: zero three times, 8 scale three times, for both halves
+            const float s0 = 8.f * lift_k * bf16_lo(num[i].x), z0 = lift_k * bf16_hi(num[i].x), s1 = 8.f * lift_k * bf16_lo(num[i].y), z1 = lift_k * bf16_hi(num[i].y);
+            const uint4 first = make_uint4(half2_of(z0, z0), half2_of(z0, s0), half2_of(s0, s0), half2_of(z1, z1));
+            const uint4 second = make_uint4(half2_of(z1, s1), half2_of(s1, s1), 0, 0);
+            *reinterpret_cast<uint4*>(p.k_rest + ((unit * 2 + lane) * EX_BLOCK + row) * 8) = lane ? second : first;
+        }
     }
 }
 
 }  // namespace
 
-// Few rows: this file's kernel; many: that of kda_attn.cu on expanded keys and values.
-static bool few_rows(int64_t Tq, int Hq, int Hk, int nseq) { return Tq * (Hq / Hk) <= 128 * (int64_t)nseq; }
+// Few rows: this file's kernel; many: that of kda_attn.cu on expanded keys and values.  With 64 rows for a key head and with 128,
+// few and many: 24 sequences over 71 to 8,098 131 and 205, 245 and 210 us; four over 16,000 86 and 137, 155 and 139; one over
+// 32,767 49 and 84, 85 and 86: they meet between 104 and 128 rows.
+static bool few_rows(int64_t Tq, int Hq, int Hk, int nseq) { return Tq * (Hq / Hk) <= 112 * (int64_t)nseq; }
 
 // Expanded keys and values for as many key heads at a time as fit into 1 GB, one at least.
 constexpr int64_t EX_MOST = 1LL << 30;
+constexpr int64_t EX_QUERY_BYTES = (HD + SPLIT_REST) * 2 + 4;   // of an expanded query
 struct Expanded {
     int64_t blocks, unit;   // of a sequence; bytes of one (sequence, head)
     int heads;              // at a time
@@ -868,7 +948,7 @@ struct Expanded {
 static Expanded expanded(int64_t S, int Hk, int nseq) {
     Expanded x;
     x.blocks = S > 0 ? (S + EX_BLOCK - 1) / EX_BLOCK : 1;
-    x.unit = x.blocks * (3 * EX_BLOCK * HD * 2 + 16);   // (16: a block's exponent, with what keeps the arrays aligned)
+    x.unit = x.blocks * (EX_BLOCK * (2 * HD + SPLIT_REST) * 2 + 16);   // (16: a block's powers, with what keeps the arrays aligned)
     const int64_t fit = EX_MOST / (x.unit * (nseq > 0 ? nseq : 1));
     x.heads = (int)(fit < 1 ? 1 : fit < Hk ? fit : Hk);
     return x;
@@ -877,7 +957,8 @@ static Expanded expanded(int64_t S, int Hk, int nseq) {
 size_t attn_qcache_workspace_bytes(int64_t Tq, int Hq, int Hk, int nseq, int64_t S) {
     if (few_rows(Tq, Hq, Hk, nseq)) return QS_CUT_BYTES + QS_ML_BYTES + (size_t)2 * QS_MAX_CTAS * QS_MAX_ROWS * HD * sizeof(float);   // (16 rows a tile: half as many CTAs)
     const Expanded x = expanded(S, Hk, nseq);
-    return attn_workspace_bytes(Tq, Hq, Hk) + 256 + (size_t)(x.unit * nseq * x.heads);
+    const int64_t query_rows = Tq * (Hq / Hk) * x.heads;
+    return attn_workspace_bytes(Tq, Hq, Hk) + 256 + (size_t)(x.unit * nseq * x.heads + query_rows * EX_QUERY_BYTES);
 }
 
 static cudaError_t launch_many_rows(const QcacheAttnParams& p, cudaStream_t stream) {
@@ -897,23 +978,33 @@ static cudaError_t launch_many_rows(const QcacheAttnParams& p, cudaStream_t stre
         e.head0 = h0;
         e.heads = heads;
         e.blocks = (int)x.blocks;
-        e.k = reinterpret_cast<__nv_bfloat16*>(ex);
-        e.k_low = e.k + units * rows * HD;
-        e.v = reinterpret_cast<__half*>(e.k_low + units * rows * HD);
-        e.top = reinterpret_cast<int*>(e.v + units * rows * HD);
+        e.k = reinterpret_cast<__half*>(ex);
+        e.v = e.k + units * rows * HD;
+        e.k_rest = e.v + units * rows * HD;
+        e.q = p.q;
+        e.q.data += (int64_t)h0 * G * p.q.head;
+        e.query_heads = heads * G;
+        e.query_rows = p.Tq * e.query_heads;
+        e.query_blocks = (e.query_rows + EX_QUERIES * EX_THREADS / 16 - 1) / (EX_QUERIES * EX_THREADS / 16);
+        e.q_to = e.k_rest + units * rows * SPLIT_REST;
+        e.q_rest = e.q_to + e.query_rows * HD;
+        e.q_power = reinterpret_cast<int*>(e.q_rest + e.query_rows * SPLIT_REST);
+        e.top = e.q_power + e.query_rows;
         if (p.nseq > 0) {
-            const cudaError_t err = launch_early(qcache_expand_kernel, dim3((unsigned)x.blocks, (unsigned)heads, (unsigned)p.nseq), EX_THREADS, 0, stream, e);
+            const int64_t more = (e.query_blocks + (int64_t)heads * p.nseq - 1) / ((int64_t)heads * p.nseq);
+            const cudaError_t err = launch_early(qcache_expand_kernel, dim3((unsigned)(x.blocks + more), (unsigned)heads, (unsigned)p.nseq), EX_THREADS, 0, stream, e);
             if (err != cudaSuccess) return err;
         }
         AttnParams a;
         memset(&a, 0, sizeof(a));
-        a.q = p.q;
-        a.q.data += (int64_t)h0 * G * p.q.head;
+        a.q = RowsView{reinterpret_cast<__nv_bfloat16*>(e.q_to), (int64_t)HD * e.query_heads, HD};
         a.out = p.out;
         a.out.data += (int64_t)h0 * G * p.out.head;
-        a.k = e.k;
-        a.k_low = e.k_low;
+        a.k = reinterpret_cast<__nv_bfloat16*>(e.k);
         a.v = reinterpret_cast<__nv_bfloat16*>(e.v);
+        a.q_rest = e.q_rest;
+        a.k_rest = e.k_rest;
+        a.q_power = e.q_power;
         a.top = e.top;
         a.top_blocks = x.blocks;
         a.k_row = a.v_row = HD;

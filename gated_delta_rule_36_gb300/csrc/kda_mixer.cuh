@@ -174,19 +174,19 @@ inline MxEncodeFn mx_encode_fn() {
     return fn;
 }
 
-// A bf16 tensor (128 channels, heads, rows, sequences) with strides in elements, read or
-// written in boxes of 64 channels x box_heads x box_rows in the 128-byte swizzle.
+// A tensor of 16-bit numbers (128 channels, heads, rows, sequences) with strides in elements, read or
+// written in boxes of 64 channels x box_heads x box_rows in the 128-byte swizzle (or other channels and boxes: without).
 inline bool mx_encode(CUtensorMap* m, const void* ptr, int64_t heads, int64_t rows, int64_t seqs, int64_t head_stride,
-                      int64_t row_stride, int64_t seq_stride, int box_heads, int box_rows) {
+                      int64_t row_stride, int64_t seq_stride, int box_heads, int box_rows, int channels = HD, int box_channels = 64) {
     MxEncodeFn fn = mx_encode_fn();
     if (!fn) return false;
-    const cuuint64_t dims[4] = {(cuuint64_t)HD, (cuuint64_t)heads, (cuuint64_t)(rows > 0 ? rows : 1), (cuuint64_t)(seqs > 0 ? seqs : 1)};
+    const cuuint64_t dims[4] = {(cuuint64_t)channels, (cuuint64_t)heads, (cuuint64_t)(rows > 0 ? rows : 1), (cuuint64_t)(seqs > 0 ? seqs : 1)};
     const cuuint64_t strides[3] = {(cuuint64_t)head_stride * 2, (cuuint64_t)row_stride * 2,
                                    (cuuint64_t)(seq_stride > 0 ? seq_stride : row_stride) * 2};
-    const cuuint32_t box[4] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows, 1};
+    const cuuint32_t box[4] = {(cuuint32_t)box_channels, (cuuint32_t)box_heads, (cuuint32_t)box_rows, 1};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, box_channels == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -35,11 +35,12 @@ struct NormRopeParams {
 struct AttnParams {
     RowsView q, out;
     __nv_bfloat16 *k, *v;
-    // launch_attn_split: the keys are k + k_low, both bf16 with the strides of k, and a block of 128 values is v in fp16 times
-    // 2^(top - 127 - SPLIT_TOP), with its own top[sequence * Hk + head][block], at least SPLIT_LEAST; rows of the last
-    // block past the sequence's keys hold zeros
-    __nv_bfloat16* k_low;
-    const int* top;
+    // launch_attn_split: queries, keys and values in fp16.  A block of 128 values is v times 2^(top_v - 127 - SPLIT_TOP), one of
+    // keys k times 2^(top_k - 127 - SPLIT_KEY), a query q times 2^q_power[token][head]; top[sequence * Hk + head][block] is
+    // top_k << 16 | top_v, at least SPLIT_KEY_LEAST and SPLIT_LEAST.  16 more channels of both (q_rest[token][head][16] and
+    // k_rest[sequence * Hk + head][block][2][128][8]) count in the scores.  Rows of the last block past the sequence's keys hold zeros.
+    __half *q_rest, *k_rest;
+    const int *q_power, *top;
     int64_t top_blocks;
     int64_t k_seq, k_row, k_head;   // strides in elements; k_seq = 0 for packed keys
     int64_t v_seq, v_row, v_head;
@@ -60,7 +61,7 @@ struct AttnParams {
     int test_skip;                  // the test-only build: the share b that withholds an arrival, -2 - b: that finds itself unsound; -1 for none
 };
 
-constexpr int SPLIT_TOP = 13, SPLIT_LEAST = 27;
+constexpr int SPLIT_TOP = 13, SPLIT_LEAST = 27, SPLIT_KEY = 13, SPLIT_KEY_LEAST = 40, SPLIT_REST = 16;
 
 struct LinParams {
     RowsView q, k, v, out;
