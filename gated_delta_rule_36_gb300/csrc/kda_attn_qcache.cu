@@ -863,7 +863,7 @@ __device__ __forceinline__ void expand_queries(const ExpandParams& p, int64_t bl
 
 __device__ __forceinline__ float code_at(uint32_t x, int bit) { return __uint_as_float((x >> bit & 15u) | 0x4b000000u) - 8388608.f; }
 
-__global__ void __launch_bounds__(EX_THREADS) qcache_expand_kernel(const ExpandParams p) {
+__global__ void __launch_bounds__(EX_THREADS, 4) qcache_expand_kernel(const ExpandParams p) {
     __shared__ uint2 most[EX_THREADS / 32];
     await_stream();
     const int block = blockIdx.x, h = blockIdx.y, n = blockIdx.z;
@@ -876,26 +876,25 @@ __global__ void __launch_bounds__(EX_THREADS) qcache_expand_kernel(const ExpandP
     if (block > 0 && (int64_t)block * EX_BLOCK >= lk) return;   // (block 0 is read even if there are no keys)
     const int lane = threadIdx.x & 15, row0 = threadIdx.x >> 4;
     const uint8_t* src = p.cache.data + n * p.cache.seq + (int64_t)(p.head0 + h) * p.cache.head;
-    uint32_t kc[EX_ROWS], vc[EX_ROWS];
-    uint4 num[EX_ROWS];
+    uint32_t kc[EX_ROWS], vc[EX_ROWS], kn[EX_ROWS], vn[EX_ROWS];   // codes; scale and zero of this lane's half
 #pragma unroll
     for (int i = 0; i < EX_ROWS; ++i) {
         const int64_t key = (int64_t)block * EX_BLOCK + row0 + i * (EX_THREADS / 16);
-        kc[i] = vc[i] = 0;
-        num[i] = make_uint4(0, 0, 0, 0);
+        kc[i] = vc[i] = kn[i] = vn[i] = 0;
         if (key < lk) {
             const uint8_t* at = src + key * p.cache.row;
             kc[i] = __ldcs(reinterpret_cast<const uint32_t*>(at) + lane);
             vc[i] = __ldcs(reinterpret_cast<const uint32_t*>(at + 64) + lane);
-            num[i] = *reinterpret_cast<const uint4*>(at + QC_NUMBERS);
+            kn[i] = *reinterpret_cast<const uint32_t*>(at + QC_NUMBERS + (lane >> 3) * 4);
+            vn[i] = *reinterpret_cast<const uint32_t*>(at + QC_NUMBERS + (lane >> 3) * 4 + 8);
         }
     }
     auto largest = [](float most, uint32_t w) { return fmaxf(most, fmaxf(fabsf(bf16_hi(w)), fabsf(fmaf(15.f, bf16_lo(w), bf16_hi(w))))); };
     float big_k = 0.f, big_v = 0.f;
 #pragma unroll
     for (int i = 0; i < EX_ROWS; ++i) {
-        big_k = largest(largest(big_k, num[i].x), num[i].y);
-        big_v = largest(largest(big_v, num[i].z), num[i].w);
+        big_k = largest(big_k, kn[i]);
+        big_v = largest(big_v, vn[i]);
     }
     uint32_t all_k = __reduce_max_sync(0xffffffffu, __float_as_uint(big_k)), all_v = __reduce_max_sync(0xffffffffu, __float_as_uint(big_v));
     if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = make_uint2(all_k, all_v);
@@ -911,9 +910,7 @@ __global__ void __launch_bounds__(EX_THREADS) qcache_expand_kernel(const ExpandP
     for (int i = 0; i < EX_ROWS; ++i) {
         const int row = row0 + i * (EX_THREADS / 16);
         const int64_t at = (unit * EX_BLOCK + row) * HD + 8 * lane;
-        const bool upper = lane >= 8;
-        const uint32_t kn = upper ? num[i].y : num[i].x, vn = upper ? num[i].w : num[i].z;
-        const float ks = lift_k * bf16_lo(kn), k8 = -8.f * ks, vs = lift_v * bf16_lo(vn), vz = lift_v * bf16_hi(vn);
+        const float ks = lift_k * bf16_lo(kn[i]), k8 = -8.f * ks, vs = lift_v * bf16_lo(vn[i]), vz = lift_v * bf16_hi(vn[i]);
         uint32_t k[4], v[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -922,8 +919,9 @@ __global__ void __launch_bounds__(EX_THREADS) qcache_expand_kernel(const ExpandP
         }
         *reinterpret_cast<uint4*>(p.k + at) = make_uint4(k[0], k[1], k[2], k[3]);
         *reinterpret_cast<uint4*>(p.v + at) = make_uint4(v[0], v[1], v[2], v[3]);
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, kn[i], 8);
         if (lane < 2) {   // the channels against a query's sums: zero three times, 8 scale three times, for both halves
-            const float s0 = 8.f * lift_k * bf16_lo(num[i].x), z0 = lift_k * bf16_hi(num[i].x), s1 = 8.f * lift_k * bf16_lo(num[i].y), z1 = lift_k * bf16_hi(num[i].y);
+            const float s0 = -k8, z0 = lift_k * bf16_hi(kn[i]), s1 = 8.f * lift_k * bf16_lo(other), z1 = lift_k * bf16_hi(other);
             const uint4 first = make_uint4(half2_of(z0, z0), half2_of(z0, s0), half2_of(s0, s0), half2_of(z1, z1));
             const uint4 second = make_uint4(half2_of(z1, s1), half2_of(s1, s1), 0, 0);
             *reinterpret_cast<uint4*>(p.k_rest + ((unit * 2 + lane) * EX_BLOCK + row) * 8) = lane ? second : first;
