@@ -254,8 +254,8 @@ template <int kN>
 struct QsLayout {
     static constexpr uint32_t ROWS = 8 * kN, WARPS = QS_WARPS[kN], THREADS = 32 * WARPS;
     static constexpr uint32_t OFF_SUMS = WARPS * QS_STAGES * SLICE_BYTES;          // [warps][rows][128] fp32
-    static constexpr uint32_t OFF_ML = OFF_SUMS + WARPS * ROWS * 512;              // [warps][rows] float2
-    static constexpr uint32_t OFF_BAR = OFF_ML + WARPS * ROWS * 8;
+    static constexpr uint32_t OFF_ML = OFF_SUMS + WARPS * ROWS * 512;              // [piece & 1][warps][rows] float2
+    static constexpr uint32_t OFF_BAR = OFF_ML + 2 * WARPS * ROWS * 8;
     static constexpr uint32_t OFF_SCRATCH = OFF_BAR + WARPS * QS_STAGES * 8;
     static constexpr uint32_t BYTES = OFF_SCRATCH + 32 * 8;
 };
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(QsLayout<kN>::THREADS, kN == 1 ? 2 : 1) attn_q
     // this lane's keys and its values' codes in a slice
     const unsigned char* krow = smem_raw + warp * QS_STAGES * SLICE_BYTES + key_row(g) * QC_ROW;
     const unsigned char* vrow = smem_raw + warp * QS_STAGES * SLICE_BYTES + key_row(2 * t) * QC_ROW + 64 + 4 * g;
-    bool ok = true, first_piece = true;
+    bool ok = true, first_piece = true, odd = false;
 #pragma unroll 1
     while (left > 0) {
         const int kh = (u.kh << kHg) + mine;
@@ -549,7 +549,10 @@ __global__ void __launch_bounds__(QsLayout<kN>::THREADS, kN == 1 ? 2 : 1) attn_q
             load_first(u, r);
         }
         // ---- the warps' results: reference and sum of every row, then the rows themselves
-        float2* ml = reinterpret_cast<float2*>(smem_raw + L::OFF_ML);
+        // (two places for the references: a warp without a slice of the next piece writes its own there while others still read these;
+        // the rows are written behind a barrier that those reach after)
+        float2* ml = reinterpret_cast<float2*>(smem_raw + L::OFF_ML) + (odd ? WARPS * rows : 0);
+        odd = !odd;
         float* sums = reinterpret_cast<float*>(smem_raw + L::OFF_SUMS);
 #pragma unroll
         for (int b = 0; b < kN; ++b)

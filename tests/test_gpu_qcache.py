@@ -330,6 +330,24 @@ def test_attention_over_constant_groups_and_long_means():
     check(out, lse, ref_attn(q, cache, 0.05, [1, 1], lens_k), False, 2)
 
 
+@pytest.mark.parametrize("tokens,hq,order", [(1, 16, "heads"), (1, 32, "rows"), (2, 64, "heads")])
+def test_attention_of_many_short_sequences(tokens, hq, order):
+    """Pieces of fewer slices than a CTA has warps, one after another: some warps have none and run ahead."""
+    g = gen_of(41)
+    hk, lens_k = 8, [2 + (37 * i) % 90 if i % 5 else 300 + i for i in range(600)]
+    lens_q = [tokens] * len(lens_k)
+    cache = filled(g, lens_k, hk, order)
+    q = rand(g, sum(lens_q), hq, D)
+    ref, first = ref_attn(q, cache, 0.08, lens_q, lens_k), None
+    for _ in range(8):
+        out, lse = torch.full_like(q, NAN), torch.full(q.shape[:2], NAN, device="cuda")
+        kda.kda_attn_qcache_fwd(q, cache, 0.08, out, i64(lens_k), lse=lse)
+        if first is None:
+            check(out, lse, ref, False, q.shape[0])
+            first = out, lse
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+
+
 @pytest.mark.parametrize("lens_q,lens_k", [([3, 1, 2], [700, 300, 90]), ([70, 129, 65], [700, 300, 90])])
 def test_attention_of_any_powers(lens_q, lens_k):
     """Queries and keys whose powers of two cancel, sequence by sequence; some rows and some blocks of keys far below the others."""
