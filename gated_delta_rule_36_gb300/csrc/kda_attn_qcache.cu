@@ -107,10 +107,65 @@ __device__ __forceinline__ int64_t qs_share_start(int64_t total, int b, int shar
     return total / shares * b + total % shares * b / shares;
 }
 
-// The whole block: checks the lengths, counts the steps and finds where share b starts and ends among them.
+// Sequence n's lengths contradict the tensors.
+__device__ __forceinline__ bool qs_bad(const QcacheAttnParams& p, int n) {
+    bool b = p.seqlens_k[n] < 0 || p.seqlens_k[n] > p.S;
+    if (p.cu_q) b |= p.cu_q[n + 1] < p.cu_q[n] || (n == 0 && p.cu_q[0] != 0) || (n + 1 == p.nseq && p.cu_q[n + 1] > p.Tq);
+    return b;
+}
+template <int kN, int kHg>
+__device__ __forceinline__ int64_t qs_weight(const QcacheAttnParams& p, const QsSeq& s, int G) {
+    constexpr int own = PIECE[kN] >> kHg;
+    return (int64_t)qs_tiles(s, G, 8 * kN) * (p.Hk >> kHg) * (qs_slices(s) + own);
+}
+// Step `at` of sequence n.  A cut inside a tile's own weight, which is at its front, moves to the tile's start: by `back` steps.
+template <int kN, int kHg>
+__device__ __forceinline__ QsCursor qs_cursor(const QsSeq& s, int n, int64_t at, int G, int& back) {
+    constexpr int own = PIECE[kN] >> kHg;
+    const int w = qs_slices(s) + own, tiles = qs_tiles(s, G, 8 * kN);
+    const bool small = (at >> 31) == 0;   // (64-bit divisions take long)
+    const int64_t unit = small ? (int64_t)((uint32_t)at / (uint32_t)w) : at / w;
+    const int head = tiles == 1 ? (int)unit : small ? (int)((uint32_t)unit / (uint32_t)tiles) : (int)(unit / tiles);
+    const int from = (int)(at - unit * w), j = max(from - own, 0);
+    back = j > 0 ? 0 : from;
+    return QsCursor{n, head, (int)(unit - (int64_t)head * tiles), j, s};
+}
+
+// Checks the lengths, counts the steps and finds where share b starts and ends among them.  At most 32 sequences: every warp by itself.
+template <int kN, int kHg>
+__device__ QsShare qs_find_share_by_warp(const QcacheAttnParams& p, int G) {
+    const int lane = threadIdx.x & 31;
+    const bool mine = lane < p.nseq;
+    QsSeq s{};
+    QsShare r{};
+    if (mine) s = qs_seq(p, lane);
+    r.bad = __any_sync(0xffffffffu, mine && qs_bad(p, lane));
+    if (r.bad) return r;
+    const int64_t weight = mine ? qs_weight<kN, kHg>(p, s, G) : 0;
+    int64_t end = weight;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, end, o);
+        if (lane >= o) end += y;
+    }
+    const int64_t total = __shfl_sync(0xffffffffu, end, 31);
+    const int shares = (int)min((int64_t)gridDim.x, max(total / (QS_WARPS[kN] >> kHg), (int64_t)1));
+    const int64_t x0 = qs_share_start(total, blockIdx.x, shares), x1 = qs_share_start(total, blockIdx.x + 1, shares);
+    if (x0 >= total) return r;
+    const uint32_t first = __ffs(__ballot_sync(0xffffffffu, x0 < end)) - 1, last = __ffs(__ballot_sync(0xffffffffu, x1 < end)) - 1;   // (-1: none)
+    int back0 = 0, back1 = 0;
+    QsCursor u{};
+    if (lane == first) u = qs_cursor<kN, kHg>(s, lane, x0 - (end - weight), G, back0);
+    if (lane == last) qs_cursor<kN, kHg>(s, lane, x1 - (end - weight), G, back1);
+    auto of = [](int x, uint32_t l) { return __shfl_sync(0xffffffffu, x, l); };
+    r.at = QsCursor{(int)first, of(u.kh, first), of(u.tile, first), of(u.j, first), QsSeq{of(s.q0, first), of(s.lq, first), of(s.lk, first)}};
+    r.weight = x1 - (last == ~0u ? 0 : of(back1, last)) - (x0 - of(back0, first));
+    return r;
+}
+// ... the whole block.
 template <int kN, int kHg>
 __device__ QsShare qs_find_share(const QcacheAttnParams& p, int G, int64_t* scratch /* 32 */) {
-    constexpr int own = PIECE[kN] >> kHg, rows = 8 * kN, warps = QS_WARPS[kN], threads = 32 * warps;
+    constexpr int warps = QS_WARPS[kN], threads = 32 * warps;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (p.nseq + threads - 1) / threads;
     const int n0 = min(tid * per, p.nseq), n1 = min(n0 + per, p.nseq);
@@ -119,12 +174,10 @@ __device__ QsShare qs_find_share(const QcacheAttnParams& p, int G, int64_t* scra
     bool bad = false;
 #pragma unroll 1
     for (int n = n0; n < n1; ++n) {   // nothing is computed from bad lengths
-        bool b = false;
-        if (p.cu_q) b |= p.cu_q[n + 1] < p.cu_q[n] || (n == 0 && p.cu_q[0] != 0) || (n + 1 == p.nseq && p.cu_q[n + 1] > p.Tq);
-        b |= p.seqlens_k[n] < 0 || p.seqlens_k[n] > p.S;
+        const bool b = qs_bad(p, n);
         bad |= b;
         s = qs_seq(p, n);
-        each = b ? 0 : (int64_t)qs_tiles(s, G, rows) * (p.Hk >> kHg) * (qs_slices(s) + own);
+        each = b ? 0 : qs_weight<kN, kHg>(p, s, G);
         mine += each;
     }
     int64_t sum = mine;
@@ -158,18 +211,14 @@ __device__ QsShare qs_find_share(const QcacheAttnParams& p, int G, int64_t* scra
         if (n > n0)
             for (n = n0;; ++n) {
                 s = qs_seq(p, n);
-                each = (int64_t)qs_tiles(s, G, rows) * (p.Hk >> kHg) * (qs_slices(s) + own);
+                each = qs_weight<kN, kHg>(p, s, G);
                 if (x < base + each) break;
                 base += each;
             }
-        const int64_t at = x - base;
-        const int w = qs_slices(s) + own, tiles = qs_tiles(s, G, rows);
-        const bool small = (at >> 31) == 0;   // (64-bit divisions take long)
-        const int64_t unit = small ? (int64_t)((uint32_t)at / (uint32_t)w) : at / w;
-        const int head = tiles == 1 ? (int)unit : small ? (int)((uint32_t)unit / (uint32_t)tiles) : (int)(unit / tiles);
-        const int from = (int)(at - unit * w), j = max(from - own, 0);   // the tile's own weight is at its front
-        scratch[16 + e] = x - (j > 0 ? 0 : from);                          // (a cut inside it moves to the tile's start)
-        if (e == 0) *place = QsCursor{n, head, (int)(unit - (int64_t)head * tiles), j, s};
+        int back;
+        const QsCursor c = qs_cursor<kN, kHg>(s, n, x - base, G, back);
+        scratch[16 + e] = x - back;
+        if (e == 0) *place = c;
     }
     __syncthreads();
     if (x0 < total) {
@@ -280,7 +329,8 @@ __global__ void __launch_bounds__(QsLayout<kN>::THREADS, kN == 1 ? 2 : 1) attn_q
     }
     __syncwarp();
     await_stream();
-    const QsShare share = qs_find_share<kN, kHg>(p, G, reinterpret_cast<int64_t*>(smem_raw + L::OFF_SCRATCH));
+    const QsShare share = p.nseq <= 32 ? qs_find_share_by_warp<kN, kHg>(p, G)
+                                       : qs_find_share<kN, kHg>(p, G, reinterpret_cast<int64_t*>(smem_raw + L::OFF_SCRATCH));
     QsPartials part = qs_partials(p.workspace);
     QsCursor u = share.at;
     if (tid == 0) {
