@@ -30,7 +30,7 @@
 // Bound by HBM between a start of about 2 us (the lengths, the search), some 3 us a tile (queries, the warps' results)
 // and the join (3 us): 32 single tokens over caches of 67 to 8,189, 32 heads on 8: 40 us (3.8 TB/s; 6.4 in the slices);
 // 16 over 5,002 to 32,767, 64 heads on 8, heads inside the rows: 84 to 88 us, where the 144 bytes of a head bring 21 %
-// of others with them (heads outside: 72 us, 4.8 TB/s); one token over 32,767: 19 us (20 through the Python call), over 2,000 11 us;
+// of others with them (heads outside: 72 us, 4.8 TB/s); one token over 32,767: 19 us, over 2,000 9.7;
 // 24 x 4 drafts: 43 us, bound by latency with eight warps an SM.
 
 #include <cuda_fp16.h>
@@ -682,13 +682,12 @@ __global__ void __launch_bounds__(QsLayout<kN>::THREADS, kN == 1 ? 2 : 1) attn_q
 
 // Joins the partial rows of the tiles that several shares hold (and, the last block, the shares' status bits: one
 // store, so that none is lost).  Block b takes the tile that share b + 1 starts in, if that is the tile's first cut; a warp
-// takes a row of a head (two warps where there are more), lane l its channels 4 l .. 4 l + 3.  Bound by latency: what it
-// needs of the shares is asked for at once, then kParts parts at once, and blocks are few (one for each row: 2 to 7 us more;
-// reading part after part: one token over 32,767 6 us more).
-template <int kWarps, int kParts>
-__global__ void __launch_bounds__(32 * kWarps, 2) attn_qcache_join_kernel(const QcacheAttnParams p, int ctas, int rows, int hg) {
-    __shared__ float4 sums[kWarps][32];
-    __shared__ float2 refs[kWarps];
+// takes a row of a head, lane l its channels 4 l .. 4 l + 3.  Bound by latency: what it needs of the shares is asked for at once,
+// then kParts parts at once, and blocks are few and small (one for each row: 2 to 7 us more; 16 warps, two for a row,
+// with eight parts each: 1.3 us more; 32: 4 us).
+constexpr int QJ_WARPS = 8;
+template <int kParts>
+__global__ void __launch_bounds__(32 * QJ_WARPS, 2) attn_qcache_join_kernel(const QcacheAttnParams p, int ctas, int rows, int hg) {
     const int first = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = p.Hq / p.Hk;
     const QsPartials part = qs_partials(p.workspace);
     await_stream();
@@ -731,24 +730,24 @@ __global__ void __launch_bounds__(32 * kWarps, 2) attn_qcache_join_kernel(const 
         if (past) break;
         e = part.cut[min(base + 32 + lane, ctas - 1)];
     }
-    const int count = 1 + end - first, group = rows << hg < kWarps ? kWarps / (rows << hg) : 1;
+    const int count = 1 + end - first;
 #pragma unroll 1
-    for (int i0 = 0; i0 < rows << hg; i0 += kWarps / group) {   // (one turn with 8 rows and 8 warps)
-        const int i = i0 + warp / group, row = i >> hg;
+    for (int i = warp; i < rows << hg; i += QJ_WARPS) {
+        const int row = i >> hg;
         const int64_t at = (int64_t)c.tile * rows + row;
-        const bool there = at < (int64_t)c.lq * G;
+        if (at >= (int64_t)c.lq * G) break;
         auto slot = [&](int k) {
             return (size_t)(k == 0 ? 2 * b + (same ? 0 : 1) : 2 * (first + k - 1)) * (rows / 8) * QS_MAX_ROWS + i;
         };
         float m = -INFINITY, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-        for (int k0 = warp % group; k0 < count && there; k0 += kParts * group) {
+        for (int k0 = 0; k0 < count; k0 += kParts) {
             float2 ml[kParts];
             float4 y[kParts];
 #pragma unroll
             for (int d = 0; d < kParts; ++d) {
-                const int k = k0 + d * group;
+                const int k = k0 + d;
                 ml[d] = make_float2(-INFINITY, 0.f);
                 if (k < count) {
                     ml[d] = __ldcg(part.ml + slot(k));
@@ -773,28 +772,6 @@ __global__ void __launch_bounds__(32 * kWarps, 2) attn_qcache_join_kernel(const 
                 o.w = fmaf(w, y[d].w, o.w);
             }
         }
-        if (group > 1) {   // the row's warps, in order
-            sums[warp][lane] = o;
-            if (lane == 0) refs[warp] = make_float2(m, l);
-            __syncthreads();
-            if (warp % group != 0) continue;
-            const float mine = m;
-            for (int w = warp + 1; w < warp + group; ++w) m = fmaxf(m, refs[w].x);
-            const float f = mine == -INFINITY ? 0.f : ex2_approx(mine - m);
-            l *= f;
-            o.x *= f, o.y *= f, o.z *= f, o.w *= f;
-            for (int w = warp + 1; w < warp + group; ++w) {
-                const float2 r = refs[w];
-                const float4 y = sums[w][lane];
-                const float g = r.x == -INFINITY ? 0.f : ex2_approx(r.x - m);
-                l = fmaf(g, r.y, l);
-                o.x = fmaf(g, y.x, o.x);
-                o.y = fmaf(g, y.y, o.y);
-                o.z = fmaf(g, y.z, o.z);
-                o.w = fmaf(g, y.w, o.w);
-            }
-        }
-        if (!there) continue;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const int64_t tok = c.q0 + at / G, head = (int64_t)((c.kh << hg) + (i & ((1 << hg) - 1))) * G + at % G;
         *reinterpret_cast<uint2*>(p.out.data + tok * p.out.row + head * p.out.head + 4 * lane) =
@@ -821,10 +798,11 @@ cudaError_t launch(const QcacheAttnParams& p, int sms, cudaStream_t stream) {
     const int ctas = min(sms * (kN == 1 ? 2 : 1), QS_MAX_CTAS / kN);
     cudaError_t e = cudaFuncSetAttribute(attn_qcache_kernel<kN, kHg>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)QsLayout<kN>::BYTES);
     if (e == cudaSuccess) e = launch_early(attn_qcache_kernel<kN, kHg>, dim3((unsigned)ctas), QsLayout<kN>::THREADS, QsLayout<kN>::BYTES, stream, p, map);
-    // many parts a tile where there are few units (one token over 2,000: 13.7 -> 11.3 us), else few (32 tokens 41.0 -> 39.5)
+    // parts asked for at once: 16 where there are few units (one token over 32,767: 19.1 us; four 21, 20 20.7), else four
+    // (16 tokens over 5,002 to 32,767, rows order, 82.7 us; eight 83.6)
     const bool many = ctas > 4 * (int64_t)p.nseq * (p.Hk >> kHg);
     if (e == cudaSuccess)
-        e = launch_early(many ? attn_qcache_join_kernel<16, 8> : attn_qcache_join_kernel<8, 4>, dim3((unsigned)ctas), many ? 512 : 256, 0, stream, p, ctas, 8 * kN, kHg);
+        e = launch_early(many ? attn_qcache_join_kernel<16> : attn_qcache_join_kernel<4>, dim3((unsigned)ctas), 32 * QJ_WARPS, 0, stream, p, ctas, 8 * kN, kHg);
     return e;
 }
 
