@@ -603,7 +603,7 @@ __device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const C
     const uint32_t lanes = (uint32_t)(row & ~31) << 16, tO = lanes + TM_O + 128 * t;
     const int lane = threadIdx.x & 31;
     const uint32_t stage = x.base + Layout<kSplit>::OFF_STAGE + (threadIdx.x >> 5) * 4096;
-    const float c = fmaxf(p.scale * LOG2E, 1e-30f);   // (a scale of 0 must not turn a masked -inf into NaN)
+    const float c = kSplit ? p.scale * LOG2E : fmaxf(p.scale * LOG2E, 1e-30f);   // (a scale of 0 must not turn a masked -inf into NaN)
     const Partials part = partials(p.workspace);
     const int tok = row / x.G, head = row - tok * x.G;
     uint32_t nS = 0, nX = 0, nO = 0, nV = 0;   // uses so far of SF, SX, OF and PV
@@ -627,7 +627,7 @@ __device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const C
         const float unit = kSplit ? 1.f : c;
         for (int j = r.j0; j < end; ++j) {
             const int tops_j = kSplit ? __ldg(tops + j) : 0, top_j = tops_j & 0xffff;
-            const float cj = kSplit ? fminf(fmaxf(times_power(c, power_q + (tops_j >> 16)), 1e-30f), 3e38f) : c;
+            float cj = kSplit ? fminf(fmaxf(times_power(c, power_q + (tops_j >> 16)), 1e-30f), 3e38f) : c;
             if (!x.wait(other ? SX : SF + t, other ? nX++ : nS++)) return false;
             tc_fence_after();
             const uint32_t tS = lanes + TM_S + 128 * (t + other);
@@ -680,6 +680,12 @@ __device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const C
                 }
             }
             float mc = m == -INFINITY ? 0.f : -m * unit;
+            if (kSplit && __any_sync(0xffffffffu, fabsf(mc) > 0x1p20f)) {   // so large that the scores have to be rounded as the maximum was
+#pragma unroll
+                for (int k = 0; k < 128; ++k) s[k] = __float_as_uint(__fadd_rn(__fmul_rn(mx_u2f(s[k]), cj), mc));
+                cj = 1.f;
+                mc = 0.f;
+            }
             const int less = kSplit ? max(top_j - top_v, -60) : 0;   // the weights take the difference of the powers
             if (kSplit) mc += (float)less;
             const float2 c2 = make_float2(cj, cj), mc2 = make_float2(mc, mc);

@@ -365,8 +365,8 @@ __global__ void __launch_bounds__(QsLayout<kN>::THREADS, kN == 1 ? 2 : 1) attn_q
         load_first(u, r);
     }
 
-    // what turns s into an exponent of base 2 (a scale of 0 must not turn a masked -inf into NaN)
-    const float cq = fmaxf(p.scale * LOG2E, 1e-30f) / KEY_CODE;
+    // what turns s into an exponent of base 2 (a scale of 0 must not turn a masked -inf into NaN, nor one past fp32 a score of 0)
+    const float cq = fminf(fmaxf(p.scale * LOG2E / KEY_CODE, 1.2e-38f), 3e38f);
     // this lane's keys and its values' codes in a slice
     const unsigned char* krow = smem_raw + warp * QS_STAGES * SLICE_BYTES + key_row(g) * QC_ROW;
     const unsigned char* vrow = smem_raw + warp * QS_STAGES * SLICE_BYTES + key_row(2 * t) * QC_ROW + 64 + 4 * g;
@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(QsLayout<kN>::THREADS, kN == 1 ? 2 : 1) attn_q
                         float w[2];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            w[e] = ex2_approx(fmaf(cq, s[b][a][2 * i + e], -low[b][e]));
+                            w[e] = ex2_approx(__fsub_rn(__fmul_rn(cq, s[b][a][2 * i + e]), low[b][e]));   // (rounded as the maximum was: scores may be large)
                             l[b][e] += w[e];
                             z[b][0][e] = fmaf(w[e], m0, z[b][0][e]);
                             z[b][1][e] = fmaf(w[e], m1, z[b][1][e]);
@@ -996,7 +996,6 @@ static cudaError_t launch_many_rows(const QcacheAttnParams& p, cudaStream_t stre
     char* ex = static_cast<char*>(p.workspace) + attn_workspace_bytes(p.Tq, p.Hq, p.Hk);
     ex += -(uintptr_t)ex & 255;
     const int64_t rows = x.blocks * EX_BLOCK, units = (int64_t)p.nseq * x.heads;
-    if (p.nseq > 65535) return cudaErrorInvalidValue;
     for (int h0 = 0; h0 < p.Hk; h0 += x.heads) {
         const int heads = min(x.heads, p.Hk - h0);
         ExpandParams e;

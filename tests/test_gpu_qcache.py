@@ -305,6 +305,38 @@ def test_attention_of_scores_that_matter(lens_q, lens_k, hq, hk):
             assert ((out.double() - ref).abs() <= U * (ref.abs() + size + spread) + 1.01 * (err.exp() - (-err).exp()) * largest(cache, lens_q, lens_k, hq) + 1e-30).all()
 
 
+@pytest.mark.parametrize("lens_q,lens_k", [([2, 1], [300, 40]), ([90, 100], [500, 300])])
+def test_attention_with_the_smallest_and_largest_scales(lens_q, lens_k):
+    """A scale of 0 makes all keys alike, however large the products; one of 1e30 leaves a single key."""
+    g = gen_of(78)
+    hq, hk, T = 8, 2, sum(lens_q)
+    cache = empty_cache(2, 501, hk)
+    for power, scale in ((45, 0.0), (0, 1e30)):
+        for n, lk in enumerate(lens_k):
+            far = 2.0 ** -(torch.arange(lk, device="cuda") // 128 * 7 % 12).float()[:, None, None]   # (blocks of values, powers apart)
+            cache[n, :lk] = rows_of(rand(g, lk, hk, D) * 2.0 ** power, (rand(g, lk, hk, D).float() * far).bfloat16())
+        q = rand(g, T, hq, D) * 2.0 ** (power + 10 if power else 0)
+        out, lse = torch.full((T, hq, D), NAN, dtype=torch.bfloat16, device="cuda"), torch.full((T, hq), NAN, device="cuda")
+        kda.kda_attn_qcache_fwd(q, cache, scale, out, i64(lens_k), lse=lse, cu_seqlens_q=cu_of(lens_q))
+        if scale == 0.0:
+            check(out, lse, ref_attn(q, cache, scale, lens_q, lens_k), many_rows(lens_q, hq, hk), T)
+            continue
+        # a scale of 1e6 leaves the same single key where the first two scores are 1e-3 apart (weights of e^-1000)
+        a = 0
+        for n, (lq, lk) in enumerate(zip(lens_q, lens_k)):
+            for h in range(hq):
+                k, v = values_of(cache[n, :lk, h * hk // hq])
+                w = q[a:a + lq, h].double() @ k.T
+                w = w.masked_fill(torch.arange(lk, device="cuda") > torch.arange(lq, device="cuda")[:, None] + lk - lq, -math.inf)
+                top = w.topk(2, -1)
+                clear = top.values[:, 0] - top.values[:, 1] > 1e-3
+                assert clear.float().mean() > 0.9
+                got, want = out[a:a + lq, h].double(), v[top.indices[:, 0]]
+                # the output's rounding, and a weight's (of less than the spread of its group, twice the row's largest)
+                assert ((got - want).abs() <= 2.01 * U * (want.abs() + want.abs().amax(-1, keepdim=True)))[clear].all()
+            a += lq
+
+
 def largest(cache, lens_q, lens_k, hq):
     """The largest |v| that each query's channel can meet, [T, hq, 128]."""
     out = []
