@@ -31,7 +31,7 @@
 // and the join (3 us): 32 single tokens over caches of 67 to 8,189, 32 heads on 8: 40 us (3.8 TB/s; 6.4 in the slices);
 // 16 over 5,002 to 32,767, 64 heads on 8, heads inside the rows: 84 to 88 us, where the 144 bytes of a head bring 21 %
 // of others with them (heads outside: 72 us, 4.8 TB/s); one token over 32,767: 19 us, over 2,000 9.7;
-// 24 x 4 drafts: 43 us, bound by latency with eight warps an SM.
+// 24 x 4 drafts: 42 us, bound by latency with eight warps an SM.
 
 #include <cuda_fp16.h>
 #include <string.h>
@@ -681,10 +681,10 @@ __global__ void __launch_bounds__(QsLayout<kN>::THREADS, kN == 1 ? 2 : 1) attn_q
 }
 
 // Joins the partial rows of the tiles that several shares hold (and, the last block, the shares' status bits: one
-// store, so that none is lost).  Block b takes the tile that share b + 1 starts in, if that is the tile's first cut; a warp
-// takes a row of a head, lane l its channels 4 l .. 4 l + 3.  Bound by latency: what it needs of the shares is asked for at once,
-// then kParts parts at once, and blocks are few and small (one for each row: 2 to 7 us more; 16 warps, two for a row,
-// with eight parts each: 1.3 us more; 32: 4 us).
+// store, so that none is lost).  Block (b, y) takes eight rows of the tile that share b + 1 starts in, if that is the tile's first
+// cut; a warp takes a row of a head, lane l its channels 4 l .. 4 l + 3.  Bound by latency: what it needs of the shares is asked for
+// at once, then kParts parts at once, and blocks are few and small (one for each row: 2 to 7 us more; one for a tile's 32 rows:
+// 24 x 4 drafts 2.3 us more; 16 warps, two for a row, with eight parts each: 1.3 us more for one token; 32: 4 us).
 constexpr int QJ_WARPS = 8;
 template <int kParts>
 __global__ void __launch_bounds__(32 * QJ_WARPS, 2) attn_qcache_join_kernel(const QcacheAttnParams p, int ctas, int rows, int hg) {
@@ -692,7 +692,7 @@ __global__ void __launch_bounds__(32 * QJ_WARPS, 2) attn_qcache_join_kernel(cons
     const QsPartials part = qs_partials(p.workspace);
     await_stream();
     if (first == ctas) {
-        if (warp != 0) return;
+        if (warp != 0 || blockIdx.y != 0) return;
         uint32_t status = 0;
         for (int s = lane; s < ctas; s += 32) status |= part.cut[s].status;
         status = __reduce_or_sync(0xffffffffu, status);
@@ -731,53 +731,50 @@ __global__ void __launch_bounds__(32 * QJ_WARPS, 2) attn_qcache_join_kernel(cons
         e = part.cut[min(base + 32 + lane, ctas - 1)];
     }
     const int count = 1 + end - first;
+    const int i = QJ_WARPS * blockIdx.y + warp, row = i >> hg;
+    const int64_t at = (int64_t)c.tile * rows + row;
+    if (at >= (int64_t)c.lq * G) return;
+    auto slot = [&](int k) {
+        return (size_t)(k == 0 ? 2 * b + (same ? 0 : 1) : 2 * (first + k - 1)) * (rows / 8) * QS_MAX_ROWS + i;
+    };
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-    for (int i = warp; i < rows << hg; i += QJ_WARPS) {
-        const int row = i >> hg;
-        const int64_t at = (int64_t)c.tile * rows + row;
-        if (at >= (int64_t)c.lq * G) break;
-        auto slot = [&](int k) {
-            return (size_t)(k == 0 ? 2 * b + (same ? 0 : 1) : 2 * (first + k - 1)) * (rows / 8) * QS_MAX_ROWS + i;
-        };
-        float m = -INFINITY, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-        for (int k0 = 0; k0 < count; k0 += kParts) {
-            float2 ml[kParts];
-            float4 y[kParts];
+    for (int k0 = 0; k0 < count; k0 += kParts) {
+        float2 ml[kParts];
+        float4 y[kParts];
 #pragma unroll
-            for (int d = 0; d < kParts; ++d) {
-                const int k = k0 + d;
-                ml[d] = make_float2(-INFINITY, 0.f);
-                if (k < count) {
-                    ml[d] = __ldcg(part.ml + slot(k));
-                    y[d] = __ldcg(reinterpret_cast<const float4*>(part.o + slot(k) * 128 + 4 * lane));
-                }
-            }
-            float top = m;
-#pragma unroll
-            for (int d = 0; d < kParts; ++d) top = fmaxf(top, ml[d].x);
-            const float old = m == -INFINITY ? 0.f : ex2_approx(m - top);
-            m = top;
-            l *= old;
-            o.x *= old, o.y *= old, o.z *= old, o.w *= old;
-#pragma unroll
-            for (int d = 0; d < kParts; ++d) {
-                if (ml[d].x == -INFINITY) continue;   // a part that saw no key, or an empty share
-                const float w = ex2_approx(ml[d].x - m);
-                l = fmaf(w, ml[d].y, l);
-                o.x = fmaf(w, y[d].x, o.x);
-                o.y = fmaf(w, y[d].y, o.y);
-                o.z = fmaf(w, y[d].z, o.z);
-                o.w = fmaf(w, y[d].w, o.w);
+        for (int d = 0; d < kParts; ++d) {
+            const int k = k0 + d;
+            ml[d] = make_float2(-INFINITY, 0.f);
+            if (k < count) {
+                ml[d] = __ldcg(part.ml + slot(k));
+                y[d] = __ldcg(reinterpret_cast<const float4*>(part.o + slot(k) * 128 + 4 * lane));
             }
         }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int64_t tok = c.q0 + at / G, head = (int64_t)((c.kh << hg) + (i & ((1 << hg) - 1))) * G + at % G;
-        *reinterpret_cast<uint2*>(p.out.data + tok * p.out.row + head * p.out.head + 4 * lane) =
-            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-        if (p.lse && lane == 0) p.lse[tok * p.Hq + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+        float top = m;
+#pragma unroll
+        for (int d = 0; d < kParts; ++d) top = fmaxf(top, ml[d].x);
+        const float old = m == -INFINITY ? 0.f : ex2_approx(m - top);
+        m = top;
+        l *= old;
+        o.x *= old, o.y *= old, o.z *= old, o.w *= old;
+#pragma unroll
+        for (int d = 0; d < kParts; ++d) {
+            if (ml[d].x == -INFINITY) continue;   // a part that saw no key, or an empty share
+            const float w = ex2_approx(ml[d].x - m);
+            l = fmaf(w, ml[d].y, l);
+            o.x = fmaf(w, y[d].x, o.x);
+            o.y = fmaf(w, y[d].y, o.y);
+            o.z = fmaf(w, y[d].z, o.z);
+            o.w = fmaf(w, y[d].w, o.w);
+        }
     }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int64_t tok = c.q0 + at / G, head = (int64_t)((c.kh << hg) + (i & ((1 << hg) - 1))) * G + at % G;
+    *reinterpret_cast<uint2*>(p.out.data + tok * p.out.row + head * p.out.head + 4 * lane) =
+        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (p.lse && lane == 0) p.lse[tok * p.Hq + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 // The cache in boxes of 144 bytes x 1 head x `rows` rows.
@@ -802,7 +799,7 @@ cudaError_t launch(const QcacheAttnParams& p, int sms, cudaStream_t stream) {
     // (16 tokens over 5,002 to 32,767, rows order, 82.7 us; eight 83.6)
     const bool many = ctas > 4 * (int64_t)p.nseq * (p.Hk >> kHg);
     if (e == cudaSuccess)
-        e = launch_early(many ? attn_qcache_join_kernel<16> : attn_qcache_join_kernel<4>, dim3((unsigned)ctas), 32 * QJ_WARPS, 0, stream, p, ctas, 8 * kN, kHg);
+        e = launch_early(many ? attn_qcache_join_kernel<16> : attn_qcache_join_kernel<4>, dim3((unsigned)ctas, (8 * kN << kHg) / QJ_WARPS), 32 * QJ_WARPS, 0, stream, p, ctas, 8 * kN, kHg);
     return e;
 }
 
