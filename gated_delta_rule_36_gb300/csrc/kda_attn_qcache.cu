@@ -961,8 +961,12 @@ __global__ void __launch_bounds__(EX_THREADS, 4) qcache_expand_kernel(const Expa
 
 // Few rows: this file's kernel; many: that of kda_attn.cu on expanded keys and values.  With 64 rows for a key head and with 128,
 // few and many: 24 sequences over 71 to 8,098 131 and 205, 245 and 210 us; four over 16,000 86 and 137, 155 and 139; one over
-// 32,767 49 and 84, 85 and 86: they meet between 104 and 128 rows.
-static bool few_rows(int64_t Tq, int Hq, int Hk, int nseq) { return Tq * (Hq / Hk) <= 112 * (int64_t)nseq; }
+// 32,767 49 and 84, 85 and 86: they meet between 104 and 128 rows.  Where there is room for few keys only, three launches and the
+// expansion cost more than they bring (100 queries over up to 1,000 keys, 8 heads on one, 13 and 32 us; 128 over up to 512, 32 heads
+// on 8, 18 and 23; but 300 over up to 300 30 and 23, and four times 100 over up to 400 40 and 29).
+static bool few_rows(int64_t Tq, int Hq, int Hk, int nseq, int64_t S) {
+    return Tq * (Hq / Hk) <= 112 * (int64_t)nseq || (double)Tq * Hq * S <= 1 << 21;
+}
 
 // Expanded keys and values for as many key heads at a time as fit into 1 GB, one at least.
 constexpr int64_t EX_MOST = 1LL << 30;
@@ -981,7 +985,7 @@ static Expanded expanded(int64_t S, int Hk, int nseq) {
 }
 
 size_t attn_qcache_workspace_bytes(int64_t Tq, int Hq, int Hk, int nseq, int64_t S) {
-    if (few_rows(Tq, Hq, Hk, nseq)) return QS_CUT_BYTES + QS_ML_BYTES + (size_t)2 * QS_MAX_CTAS * QS_MAX_ROWS * HD * sizeof(float);   // (16 rows a tile: half as many CTAs)
+    if (few_rows(Tq, Hq, Hk, nseq, S)) return QS_CUT_BYTES + QS_ML_BYTES + (size_t)2 * QS_MAX_CTAS * QS_MAX_ROWS * HD * sizeof(float);   // (16 rows a tile: half as many CTAs)
     const Expanded x = expanded(S, Hk, nseq);
     const int64_t query_rows = Tq * (Hq / Hk) * x.heads;
     return attn_workspace_bytes(Tq, Hq, Hk) + 256 + (size_t)(x.unit * nseq * x.heads + query_rows * EX_QUERY_BYTES);
@@ -1059,7 +1063,7 @@ static cudaError_t launch_many_rows(const QcacheAttnParams& p, cudaStream_t stre
 }
 
 cudaError_t launch_attn_qcache(const QcacheAttnParams& p, cudaStream_t stream) {
-    if (!few_rows(p.Tq, p.Hq, p.Hk, p.nseq)) return launch_many_rows(p, stream);
+    if (!few_rows(p.Tq, p.Hq, p.Hk, p.nseq, p.S)) return launch_many_rows(p, stream);
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);

@@ -258,22 +258,29 @@ CASES = [
 ]
 
 
-def many_rows(lens_q, hq, hk):
-    return sum(lens_q) * (hq // hk) > 112 * len(lens_q)
+def many_rows(T, n, cache, hq):
+    """Whether a call's keys and values are expanded: by its tokens, sequences and the cache's room."""
+    return T * (hq // cache.shape[2]) > 112 * n and T * hq * cache.shape[1] > 1 << 21
 
 
-@pytest.mark.parametrize("lens_q,lens_k,hq,hk,order", CASES)
-def test_attention(lens_q, lens_k, hq, hk, order):
+def wide(lens_q, hq):
+    """Room for so many keys that many rows are taken as such."""
+    return (1 << 21) // (sum(lens_q) * hq) + 1
+
+
+# (those of many rows also with little room, where they are few)
+@pytest.mark.parametrize("lens_q,lens_k,hq,hk,order,more", [(*c, False) for c in CASES] +
+                         [(*c, True) for c in CASES if sum(c[0]) * (c[2] // c[3]) > 112 * len(c[0])])
+def test_attention(lens_q, lens_k, hq, hk, order, more):
     g = gen_of(sum(lens_k) + hq)
     T = sum(lens_q)
-    cache = filled(g, lens_k, hk, order)
+    cache = filled(g, lens_k, hk, order, room=max(wide(lens_q, hq), max(lens_k)) if more else None)
     q = rand(g, T + 3, (hq + 1) * D, mul=1.5)[:, D:].unflatten(1, (hq, D))
     out = torch.full((T + 3, hq, D), NAN, dtype=torch.bfloat16, device="cuda")
     lse = torch.full((T + 3, hq), NAN, device="cuda")
     ws = kda.kda_attn_qcache_fwd(q, cache, 0.1, out, i64(lens_k), lse=lse, cu_seqlens_q=cu_of(lens_q))
     assert kda.kda_read_device_status(ws) == 0
-    many = (T + 3) * (hq // hk) > 112 * len(lens_q)       # (by the rows of q, those behind the last sequence among them)
-    check(out, lse, ref_attn(q, cache, 0.1, lens_q, lens_k), many, T)
+    check(out, lse, ref_attn(q, cache, 0.1, lens_q, lens_k), many_rows(T + 3, len(lens_q), cache, hq), T)   # (the rows of q, those behind the last sequence among them)
     assert torch.isnan(out[T:]).all() and torch.isnan(lse[T:]).all()     # rows behind the last sequence
     again, lse2 = torch.full_like(out, NAN), torch.full_like(lse, NAN)
     kda.kda_attn_qcache_fwd(q, cache, 0.1, again, i64(lens_k), lse=lse2, cu_seqlens_q=cu_of(lens_q), workspace=ws.fill_(255))
@@ -281,7 +288,7 @@ def test_attention(lens_q, lens_k, hq, hk, order):
     if len(set(lens_q)) == 1:
         again = torch.full_like(out, NAN)
         kda.kda_attn_qcache_fwd(q[:T], cache, 0.1, again[:T], i64(lens_k))               # without cu_seqlens_q and lse
-        check(again, None, ref_attn(q, cache, 0.1, lens_q, lens_k), many_rows(lens_q, hq, hk), T)
+        check(again, None, ref_attn(q, cache, 0.1, lens_q, lens_k), many_rows(T, len(lens_q), cache, hq), T)
         assert torch.isnan(again[T:]).all()
 
 
@@ -289,15 +296,16 @@ def test_attention(lens_q, lens_k, hq, hk, order):
 def test_attention_of_scores_that_matter(lens_q, lens_k, hq, hk):
     """Large scores, so that single keys win, scores far below them, and a scale of zero."""
     g = gen_of(77)
-    cache = filled(g, lens_k, hk, "heads")
+    cache = filled(g, lens_k, hk, "heads", room=1200)
     T = sum(lens_q)
+    assert many_rows(T, len(lens_q), cache, hq) == (T > 100)
     q = rand(g, T, hq, D, mul=4.0)
     for scale in (0.0, 1e-6, 1.5):
         out = torch.full((T, hq, D), NAN, dtype=torch.bfloat16, device="cuda")
         lse = torch.full((T, hq), NAN, device="cuda")
         kda.kda_attn_qcache_fwd(q, cache, scale, out, i64(lens_k), lse=lse, cu_seqlens_q=cu_of(lens_q))
         if scale <= 1e-6:
-            check(out, lse, ref_attn(q, cache, scale, lens_q, lens_k), many_rows(lens_q, hq, hk), T)
+            check(out, lse, ref_attn(q, cache, scale, lens_q, lens_k), many_rows(T, len(lens_q), cache, hq), T)
         else:       # scores in the hundreds: the weights' relative error is the scores' absolute one
             ref, size, spread, moved, rlse, most = ref_attn(q, cache, scale, lens_q, lens_k)
             unit = 2.0 ** -14
@@ -310,7 +318,8 @@ def test_attention_with_the_smallest_and_largest_scales(lens_q, lens_k):
     """A scale of 0 makes all keys alike, however large the products; one of 1e30 leaves a single key."""
     g = gen_of(78)
     hq, hk, T = 8, 2, sum(lens_q)
-    cache = empty_cache(2, 501, hk)
+    cache = empty_cache(2, 1501, hk)
+    assert many_rows(T, 2, cache, hq) == (T > 100)
     for power, scale in ((45, 0.0), (0, 1e30)):
         for n, lk in enumerate(lens_k):
             far = 2.0 ** -(torch.arange(lk, device="cuda") // 128 * 7 % 12).float()[:, None, None]   # (blocks of values, powers apart)
@@ -319,7 +328,7 @@ def test_attention_with_the_smallest_and_largest_scales(lens_q, lens_k):
         out, lse = torch.full((T, hq, D), NAN, dtype=torch.bfloat16, device="cuda"), torch.full((T, hq), NAN, device="cuda")
         kda.kda_attn_qcache_fwd(q, cache, scale, out, i64(lens_k), lse=lse, cu_seqlens_q=cu_of(lens_q))
         if scale == 0.0:
-            check(out, lse, ref_attn(q, cache, scale, lens_q, lens_k), many_rows(lens_q, hq, hk), T)
+            check(out, lse, ref_attn(q, cache, scale, lens_q, lens_k), many_rows(T, len(lens_q), cache, hq), T)
             continue
         # a scale of 1e6 leaves the same single key where the first two scores are 1e-3 apart (weights of e^-1000)
         a = 0
@@ -385,7 +394,9 @@ def test_attention_of_any_powers(lens_q, lens_k):
     """Queries and keys whose powers of two cancel, sequence by sequence; some rows and some blocks of keys far below the others."""
     g = gen_of(31)
     hq, hk, T = 8, 2, sum(lens_q)
-    cache, q = empty_cache(len(lens_k), 701, hk), rand(g, T, hq, D)
+    cache, q = empty_cache(len(lens_k), 1101, hk), rand(g, T, hq, D)
+    many = many_rows(T, 3, cache, hq)
+    assert many == (T > 100)
     a = 0
     for n, (lq, lk, power) in enumerate(zip(lens_q, lens_k, (40, -45, 0))):
         small = torch.ones(lk, 1, 1, device="cuda")
@@ -402,7 +413,7 @@ def test_attention_of_any_powers(lens_q, lens_k):
     ref = ref_attn(q, cache, 0.09, lens_q, lens_k)
     for r in zip(lens_q, [sum(lens_q[:n]) for n in range(3)]):   # (a sequence by itself: their values differ by powers of two)
         rows = slice(r[1], sum(r))
-        check(out[rows], lse[rows], [x[rows] for x in ref], many_rows(lens_q, hq, hk), r[0])
+        check(out[rows], lse[rows], [x[rows] for x in ref], many, r[0])
 
 
 @pytest.mark.parametrize("lens_q,lens_k", [
@@ -470,7 +481,7 @@ def test_captured_and_replayed(T, lens_k, hq):
         both(out)
         assert torch.equal(got, out) and torch.equal(rows, cache)
         lens_k = [a + b for a, b in zip(lens_k, per)]
-        check(got, None, ref_attn(q, cache, 0.1, per, lens_k), many_rows(per, hq, hk), T)
+        check(got, None, ref_attn(q, cache, 0.1, per, lens_k), many_rows(T, n, cache, hq), T)
 
 
 @pytest.mark.parametrize("lens_q,lens_k,hq", [([1] * 6, [900, 33, 5000, 1, 0, 64], 32), ([200, 40], [900, 40], 8)])
@@ -480,7 +491,8 @@ def test_two_at_once(lens_q, lens_k, hq):
     T, hk = sum(lens_q), 4
     sides = []
     for _ in range(2):
-        cache, q = filled(g, lens_k, hk, "heads"), rand(g, T, hq, D)
+        cache, q = filled(g, lens_k, hk, "heads", room=5003), rand(g, T, hq, D)
+        assert many_rows(T, len(lens_q), cache, hq) == (T > 100)
         want = torch.empty_like(q)
         kda.kda_attn_qcache_fwd(q, cache, 0.1, want, i64(lens_k), cu_seqlens_q=cu_of(lens_q))
         sides.append((torch.cuda.Stream(), cache, q, want, torch.empty_like(q), i64(lens_k), cu_of(lens_q)))
