@@ -983,9 +983,11 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const AttnParam
     }
 }
 
-// The same for pairs of many rows: a thread takes a row, block (b, y) its channels 8 y .. 8 y + 7, so that a
-// warp reads 512 bytes together, as they were written; four parts are asked for at once.  (Continued prompts 740 -> 703 us at the
-// time; the join above took some 40.)
+// The same for pairs of many rows: a thread takes a row, block (b, y) its channels 16 y .. 16 y + 15, so that a
+// warp reads 512 bytes together, as they were written; two parts are asked for at once.  (Continued prompts 740 -> 703 us at the
+// time; the join above took some 40.  Eight channels and four parts: 1,000 over 5,000, 32 heads on 8, 83.5 us, now 81.7; two parts
+// 83.7; 32 channels 104.)
+constexpr int JOIN_PARTS = 2, JOIN_GROUPS = 4;
 __global__ void __launch_bounds__(JOIN_THREADS, 4) attn_join_rows_kernel(const AttnParams p, int ctas) {
     const int first = blockIdx.x + 1, row = threadIdx.x, G = p.Hq / p.Hk, tq = 128 / G;
     const Partials part = partials(p.workspace);
@@ -999,36 +1001,36 @@ __global__ void __launch_bounds__(JOIN_THREADS, 4) attn_join_rows_kernel(const A
     const int t = row >> 7, tok = (row & 127) / G, head = (row & 127) - tok * G, i = (2 * r.c.pair + t) * tq + tok;
     if (tok >= tq || i >= r.c.lq) return;
     float m = -INFINITY, l = 0.f;
-    float4 o[2] = {};
+    float4 o[JOIN_GROUPS] = {};
 #pragma unroll 1
-    for (int s0 = r.b; s0 < r.end; s0 += 4) {
-        float2 ml[4];
-        float4 y[4][2];
+    for (int s0 = r.b; s0 < r.end; s0 += JOIN_PARTS) {
+        float2 ml[JOIN_PARTS];
+        float4 y[JOIN_PARTS][JOIN_GROUPS];
 #pragma unroll
-        for (int d = 0; d < 4; ++d) {
+        for (int d = 0; d < JOIN_PARTS; ++d) {
             const int s = s0 + d;
             ml[d] = make_float2(-INFINITY, 0.f);
             if (s < r.end && (s == r.b || part.cut[s].nb != 0)) {
                 ml[d] = __ldcg(part.ml + r.slot(s) * 256 + row);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) y[d][k] = __ldcg(part.o + (r.slot(s) * 32 + 2 * blockIdx.y + k) * 256 + row);
+                for (int k = 0; k < JOIN_GROUPS; ++k) y[d][k] = __ldcg(part.o + (r.slot(s) * 32 + JOIN_GROUPS * blockIdx.y + k) * 256 + row);
             }
         }
         float top = m;
 #pragma unroll
-        for (int d = 0; d < 4; ++d) top = ml[d].y != 0.f ? fmaxf(top, ml[d].x) : top;   // a part that saw no key has a sum of 0 (a NaN goes on into the results)
+        for (int d = 0; d < JOIN_PARTS; ++d) top = ml[d].y != 0.f ? fmaxf(top, ml[d].x) : top;   // a part that saw no key has a sum of 0 (a NaN goes on into the results)
         const float old = m == -INFINITY ? 0.f : exp2f(m - top);
         m = top;
         l *= old;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) o[k].x *= old, o[k].y *= old, o[k].z *= old, o[k].w *= old;
+        for (int k = 0; k < JOIN_GROUPS; ++k) o[k].x *= old, o[k].y *= old, o[k].z *= old, o[k].w *= old;
 #pragma unroll
-        for (int d = 0; d < 4; ++d) {
+        for (int d = 0; d < JOIN_PARTS; ++d) {
             if (ml[d].y == 0.f) continue;   // (its rows may not even be written)
             const float w = exp2f(ml[d].x - m);
             l = fmaf(w, ml[d].y, l);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
+            for (int k = 0; k < JOIN_GROUPS; ++k) {
                 o[k].x = fmaf(w, y[d][k].x, o[k].x);
                 o[k].y = fmaf(w, y[d][k].y, o[k].y);
                 o[k].z = fmaf(w, y[d][k].z, o[k].z);
@@ -1039,9 +1041,11 @@ __global__ void __launch_bounds__(JOIN_THREADS, 4) attn_join_rows_kernel(const A
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const int64_t q = r.c.q0 + i;
     const int h = r.c.kh * G + head;
-    *reinterpret_cast<uint4*>(p.out.data + q * p.out.row + h * p.out.head + 8 * blockIdx.y) =
-        make_uint4(pack_bf16x2(o[0].x * inv, o[0].y * inv), pack_bf16x2(o[0].z * inv, o[0].w * inv), pack_bf16x2(o[1].x * inv, o[1].y * inv),
-                   pack_bf16x2(o[1].z * inv, o[1].w * inv));
+#pragma unroll
+    for (int k = 0; k < JOIN_GROUPS; k += 2)
+        *reinterpret_cast<uint4*>(p.out.data + q * p.out.row + h * p.out.head + 4 * (JOIN_GROUPS * blockIdx.y + k)) =
+            make_uint4(pack_bf16x2(o[k].x * inv, o[k].y * inv), pack_bf16x2(o[k].z * inv, o[k].w * inv), pack_bf16x2(o[k + 1].x * inv, o[k + 1].y * inv),
+                       pack_bf16x2(o[k + 1].z * inv, o[k + 1].w * inv));
     if (p.lse && blockIdx.y == 0) p.lse[q * p.lse_row + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
@@ -1072,7 +1076,8 @@ static cudaError_t launch(const AttnParams& p, cudaStream_t stream) {
     e = launch_early(attn_kernel<kSplit>, dim3((unsigned)ctas), AT_THREADS, Layout<kSplit>::SMEM, stream, p, maps,
                      ctas > 1 ? ~0ull / (uint64_t)ctas + 1 : (uint64_t)0);
     if (e != cudaSuccess) return e;
-    return launch_early(kSplit ? attn_join_rows_kernel : attn_join_kernel, dim3((unsigned)ctas, kSplit ? HD / 8 : 256 / JOIN_ROWS), JOIN_THREADS, 0, stream, p, ctas);
+    if constexpr (kSplit) return launch_early(attn_join_rows_kernel, dim3((unsigned)ctas, HD / (4 * JOIN_GROUPS)), JOIN_THREADS, 0, stream, p, ctas);
+    return launch_early(attn_join_kernel, dim3((unsigned)ctas, 256 / JOIN_ROWS), JOIN_THREADS, 0, stream, p, ctas);
 }
 
 cudaError_t launch_attn(const AttnParams& p, cudaStream_t stream) { return launch<false>(p, stream); }
