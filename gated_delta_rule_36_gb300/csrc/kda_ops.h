@@ -4,6 +4,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -138,7 +139,7 @@ cudaError_t launch_gated_norm(const GatedNormParams& p, cudaStream_t stream);
 cudaError_t launch_residual_norm(const ResidualNormParams& p, cudaStream_t stream);
 cudaError_t launch_norm_rope(const NormRopeParams& p, cudaStream_t stream);
 cudaError_t launch_attn(const AttnParams& p, cudaStream_t stream);
-// The same over expanded keys and values (k, k_low and v of AttnParams).
+// The same over expanded queries, keys and values (AttnParams: "launch_attn_split").
 cudaError_t launch_attn_split(const AttnParams& p, cudaStream_t stream);
 size_t attn_workspace_bytes(int64_t Tq, int Hq, int Hk);
 cudaError_t launch_lin_fwd(const LinParams& p, cudaStream_t stream);

@@ -130,7 +130,7 @@ def test_residual_norm(dim, dtype, post, gate, T):
         assert torch.equal(alone, again)
 
 
-@pytest.mark.parametrize("dim,T", [(4096, 3000), (512, 20000), (2304, 1500)])
+@pytest.mark.parametrize("dim,T", [(4096, 3000), (512, 20000), (2304, 1500), (5120, 900), (8192, 1100)])
 def test_residual_norm_of_many_tokens(dim, T):
     g = gen_of(dim)
     y, res, gt = rand(g, T, dim), rand(g, T, dim, dtype=torch.float32), rand(g, T, dim)
