@@ -374,7 +374,8 @@ def fwd(q, k, v, g, beta, scale, out, A_log, dt_bias, lower_bound, initial_state
 # a kda_tensor) instead of filling ctypes structures field by field.
 # ---------------------------------------------------------------------------
 _PACK_VIEW = struct.Struct("=Qii4q4q").pack
-_PACK_DENSE = struct.Struct("=Qii4q").pack
+_PACK_VIEW2, _PACK_VIEW3 = struct.Struct("=Qii2q16x2q16x").pack, struct.Struct("=Qii3q8x3q8x").pack   # (0.2 us less than the former)
+_PACK_DENSE, _PACK_DENSE1 = struct.Struct("=Qii4q").pack, struct.Struct("=Qiiq24x").pack
 _PAD = ((0, 0, 0, 0), (0, 0, 0), (0, 0), (0,), ())
 
 
@@ -395,11 +396,22 @@ def _view(t, name, device):
     if t is None:
         return None
     dtype = _DTYPE.get(t.dtype) if isinstance(t, torch.Tensor) else None
-    if dtype is None or t.get_device() != device or device < 0 or t.dim() > 4:
+    if dtype is None or t.get_device() != device or device < 0:
         _bad_tensor(t, name)
     shape = t.shape
-    pad = _PAD[len(shape)]
-    return _PACK_VIEW(t.data_ptr() or 16, dtype, len(shape), *shape, *pad, *t.stride(), *pad)
+    n = len(shape)
+    if n == 3:
+        a, b, c = shape
+        x, y, z = t.stride()
+        return _PACK_VIEW3(t.data_ptr() or 16, dtype, 3, a, b, c, x, y, z)
+    if n == 2:
+        a, b = shape
+        x, y = t.stride()
+        return _PACK_VIEW2(t.data_ptr() or 16, dtype, 2, a, b, x, y)
+    if n > 4:
+        _bad_tensor(t, name)
+    pad = _PAD[n]
+    return _PACK_VIEW(t.data_ptr() or 16, dtype, n, *shape, *pad, *t.stride(), *pad)
 
 
 def _bytes_view(t, name, device):
@@ -408,7 +420,9 @@ def _bytes_view(t, name, device):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if t.dtype != torch.uint8 or t.get_device() != device or device < 0 or t.dim() != 4:
         raise ValueError(f"{name}: must be a uint8 CUDA tensor [N, S, Hk, {KDA_QCACHE_ROW}] on the other tensors' device")
-    return _PACK_VIEW(t.data_ptr() or 16, KDA_U8, 4, *t.shape, *t.stride())
+    n, s, h, b = t.shape
+    sn, ss, sh, sb = t.stride()
+    return _PACK_VIEW(t.data_ptr() or 16, KDA_U8, 4, n, s, h, b, sn, ss, sh, sb)
 
 
 def _status_word(status, device):
@@ -424,12 +438,17 @@ def _dense(t, name, device):
     if t is None:
         return None
     dtype = _DTYPE.get(t.dtype) if isinstance(t, torch.Tensor) else None
-    if dtype is None or t.get_device() != device or device < 0 or t.dim() > 4:
+    if dtype is None or t.get_device() != device or device < 0:
+        _bad_tensor(t, name)
+    shape = t.shape
+    n = len(shape)
+    if n > 4:
         _bad_tensor(t, name)
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
-    shape = t.shape
-    return _PACK_DENSE(t.data_ptr() or 16, dtype, len(shape), *shape, *_PAD[len(shape)])
+    if n == 1:
+        return _PACK_DENSE1(t.data_ptr() or 16, dtype, 1, shape[0])
+    return _PACK_DENSE(t.data_ptr() or 16, dtype, n, *shape, *_PAD[n])
 
 
 def _device(t, name):
