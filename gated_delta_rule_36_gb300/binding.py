@@ -487,25 +487,28 @@ def _workspace(workspace, nbytes, device, stream):
 # rest of the call, so the last one of every stream is kept (if it is small) and taken again once nobody else holds it.
 _KEPT, _KEPT_MOST = {}, 32 << 20
 _storage_uses = getattr(torch._C, "_storage_Use_Count", None)
+_refs = sys.getrefcount
 
 
-def _kept_workspace(nbytes, device, stream):
-    """A workspace from torch for a call on ``stream``.  On the current stream it is that of the stream's call before, if
-    neither the caller nor a view keeps it: what it held is used by earlier work of that stream only.  Calls that are
-    captured into a graph get their own, as memory of the graph."""
+def _kept_workspace(nbytes, device, stream, raw):
+    """A workspace from torch for a call on ``stream`` (``raw``: its handle), and where it is.  On the current stream it is
+    that of the stream's call before, if neither the caller nor a view keeps it: what it held is used by earlier work of that
+    stream only.  Calls that are captured into a graph get their own, as memory of the graph."""
     if stream is not None or nbytes > _KEPT_MOST or _storage_uses is None or torch._C._cuda_isCurrentStreamCapturing():
-        return _workspace(None, nbytes, device, stream)
-    key = (device, torch._C._cuda_getCurrentRawStream(device))
-    kept = _KEPT.get(key)
+        ws = _workspace(None, nbytes, device, stream)
+        return ws, ws.data_ptr(), ws.numel()
+    kept = _KEPT.get((device, raw))
     if kept is not None:
-        ws, uses = kept
-        # (the pair's reference, this one and the count's own; views hold the storage)
-        if ws.shape[0] >= nbytes and sys.getrefcount(ws) <= 3 and _storage_uses(ws.untyped_storage()._cdata) <= uses:
-            return ws
+        ws, storage, at, room, handle, uses = kept
+        # (the entry's reference, this one and the count's own; views hold the storage)
+        if room >= nbytes and _refs(ws) <= 3 and _refs(storage) <= 3 and _storage_uses(handle) <= uses:
+            return ws, at, room
     ws = _workspace(None, nbytes, device, None)
-    _storage_uses(ws.untyped_storage()._cdata)   # (asking once may make an object that stays)
-    _KEPT[key] = ws, _storage_uses(ws.untyped_storage()._cdata)
-    return ws
+    storage = ws.untyped_storage()
+    handle = storage._cdata
+    _storage_uses(handle)   # (asking once may make an object that stays)
+    _KEPT[device, raw] = ws, storage, ws.data_ptr(), nbytes, handle, _storage_uses(handle)
+    return ws, ws.data_ptr(), nbytes
 
 
 def kda_qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, q_out, k_out, eps=1e-6, status=None, flags=0,
@@ -626,22 +629,22 @@ def kda_attn_qcache_fwd(q, cache, scale, out, seqlens_k, lse=None, cu_seqlens_q=
     serves the stream's next such call once it is dropped."""
     lib = _lib or load()
     dev = _device(q, "q")
-    dq, dc = _view(q, "q", dev), _bytes_view(cache, "cache", dev)
+    dq, dc, raw = _view(q, "q", dev), _bytes_view(cache, "cache", dev), _stream(stream, dev)
     if workspace is None and q.dim() == 3:
         nseq, S, Hk, _ = cache.shape
-        n = nseq if cu_seqlens_q is None else max(cu_seqlens_q.numel() - 1, 0)
-        sizes = (q.shape[0], q.shape[1], Hk, n, S)
+        Tq, Hq, _ = q.shape
+        sizes = (Tq, Hq, Hk, nseq if cu_seqlens_q is None else max(cu_seqlens_q.numel() - 1, 0), S)
         nbytes = _QCACHE_SIZES.get(sizes)
         if nbytes is None:
             if len(_QCACHE_SIZES) > 4096:
                 _QCACHE_SIZES.clear()
             nbytes = _QCACHE_SIZES[sizes] = lib.kda_attn_qcache_workspace_size(*sizes) or 256   # 0: refused below
-        workspace = _kept_workspace(nbytes, dev, stream)
+        workspace, at, room = _kept_workspace(nbytes, dev, stream, raw)
     else:
         workspace = _workspace(workspace, 256, dev, stream)
+        at, room = workspace.data_ptr(), workspace.numel()
     st = lib.kda_attn_qcache_fwd(dq, dc, scale, _view(out, "out", dev), _dense(seqlens_k, "seqlens_k", dev), _dense(lse, "lse", dev),
-                                 _dense(cu_seqlens_q, "cu_seqlens_q", dev), workspace.data_ptr(), workspace.numel(),
-                                 _stream(stream, dev))
+                                 _dense(cu_seqlens_q, "cu_seqlens_q", dev), at, room, raw)
     if st:
         _check(lib, st)
     return workspace

@@ -553,6 +553,10 @@ def test_workspaces_are_kept_only_when_nobody_holds_them():
     view, ptr = second[:4], second.data_ptr()
     del second
     assert call().data_ptr() != ptr                                  # a view keeps it too
+    third = call()
+    storage, ptr = third.untyped_storage(), third.data_ptr()
+    del third
+    assert call().data_ptr() != ptr and storage.data_ptr() == ptr    # ... and its storage
     bad = i64([1 << 40, 1, 1])
     first = kda.kda_attn_qcache_fwd(q, cache, 0.1, out, bad)
     call()
