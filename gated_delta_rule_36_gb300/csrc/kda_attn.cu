@@ -46,9 +46,11 @@
 // two, so that halves gain less than exchanging their maxima costs.
 //
 // Split keys (kSplit, launch_attn_split): all operands are in fp16 and scaled by powers of two, the values and keys for each block,
-// the queries for each row.  A block's scores take the powers in their scale, so m counts in steps of base 2; the outputs
-// carry the values' largest power so far, and a block's weights take the difference.  What the keys' 11 bits do not hold comes
-// as 16 more channels, one MMA on top of eight.
+// the queries for each row.  A block's scores take the powers in their scale, so m counts in steps of base 2.  What the keys' 11 bits
+// do not hold comes as 16 more channels, one MMA on top of eight.  The weights take their values' powers with them, and what
+// a row of outputs refers to follows the largest product of a weight and its values' power, not the largest power: fp16 ends
+// at 2^-24, and a large value without weight (or one that the mask hides) must not push the others' weights below that.  A block whose
+// keys' powers lie further apart than 2^SPLIT_SPREAD has them key by key, and its sums of weights are made by themselves.
 #include <cuda_fp16.h>
 #include <string.h>
 
@@ -619,14 +621,16 @@ __device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const C
         // the last key it sees; a row that is no query's is left as it is, nothing reads its results
         const int last = mine ? i + u.s.lk - u.s.lq : 0x7fffffff;
         float m = -INFINITY, l = 0.f;
-        // split: a block's values are scaled by a power of two of its own (top[j]); the output by the largest so far
-        const int* tops = kSplit ? p.top + ((int64_t)u.n * p.Hk + u.kh) * p.top_blocks : nullptr;
-        int top_v = 0;
+        // split: a block's values are scaled by a power of two of their own (top[j], or one for each key); the output refers to
+        // 2^(m + ref), where powers count from -127 as in a float.  m and ref are whole numbers, so that they move without rounding
+        const int64_t unit_0 = kSplit ? ((int64_t)u.n * p.Hk + u.kh) * p.top_blocks : 0;
+        // (at least 18 once a key is seen, since powers are SPLIT_LEAST and more)
+        float ref = 20.f, neg = 0.f;   // neg: -m
         // ... and its keys and this query too: the exponents' scale is the block's, and m counts in steps of base 2
         const int power_q = kSplit && mine ? __ldg(p.q_power + (u.s.q0 + i) * (int64_t)p.Hq + u.kh * x.G + head) - 127 - SPLIT_KEY : 0;
         const float unit = kSplit ? 1.f : c;
         for (int j = r.j0; j < end; ++j) {
-            const int tops_j = kSplit ? __ldg(tops + j) : 0, top_j = tops_j & 0xffff;
+            const int tops_j = kSplit ? __ldg(p.top + unit_0 + j) : 0;
             float cj = kSplit ? fminf(fmaxf(times_power(c, power_q + (tops_j >> 16)), 1e-30f), 3e38f) : c;
             if (!x.wait(other ? SX : SF + t, other ? nX++ : nS++)) return false;
             tc_fence_after();
@@ -651,43 +655,86 @@ __device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const C
             // the output has to hold all earlier products before it is scaled: with two tiles these scores
             // came after them; with one they did not, and the product before has a barrier of its own
             if (!r.two && j > r.j0 && !x.wait(PV, nV++)) return false;
-            const bool grown = mine && (top - m) * unit > 8.f;   // (m = -inf: whenever a key is seen)
-            float lower = 1.f;
-            if (kSplit) {
-                if (j > r.j0 && top_j > top_v) lower = __uint_as_float((uint32_t)max(127 + top_v - top_j, 1) << 23);
-                top_v = max(top_v, top_j);
-            }
-            if (__any_sync(0xffffffffu, grown || (kSplit && lower != 1.f))) {
-                float f = grown ? exp2f((m - top) * unit) : 1.f;
-                if (grown) m = top;
-                l *= f;
-                if (kSplit) f *= lower;
-                if (j > r.j0) {
-                    const float2 f2 = make_float2(f, f);
+            auto scale_output = [&](float f) {
+                const float2 f2 = make_float2(f, f);
 #pragma unroll 1
-                    for (int b = 0; b < 8; ++b) {
-                        uint32_t o[16];
-                        tmem_ld16(tO + 16 * b, o);
-                        tmem_wait_ld_regs(o);
+                for (int b = 0; b < 8; ++b) {
+                    uint32_t o[16];
+                    tmem_ld16(tO + 16 * b, o);
+                    tmem_wait_ld_regs(o);
 #pragma unroll
-                        for (int k = 0; k < 16; k += 2) {
-                            const float2 y = __fmul2_rn(make_float2(mx_u2f(o[k]), mx_u2f(o[k + 1])), f2);
-                            o[k] = __float_as_uint(y.x);
-                            o[k + 1] = __float_as_uint(y.y);
-                        }
-                        tmem_st16(tO + 16 * b, o);
+                    for (int k = 0; k < 16; k += 2) {
+                        const float2 y = __fmul2_rn(make_float2(mx_u2f(o[k]), mx_u2f(o[k + 1])), f2);
+                        o[k] = __float_as_uint(y.x);
+                        o[k + 1] = __float_as_uint(y.y);
                     }
+                    tmem_st16(tO + 16 * b, o);
                 }
-            }
-            float mc = m == -INFINITY ? 0.f : -m * unit;
-            if (kSplit && __any_sync(0xffffffffu, fabsf(mc) > 0x1p20f)) {   // so large that the scores have to be rounded as the maximum was
+            };
+            float mc, power = 0.f;   // what the exponents take; of it, what is not m's
+            if constexpr (kSplit) {
+                // (a comparison with m = -inf holds whenever a key is seen)
+                float power_v = (float)(tops_j & 0xff);
+                const bool each = tops_j & SPLIT_EACH, grown = mine && top - m > 8.f;
+                mc = neg;
+                if (each || __any_sync(0xffffffffu, grown || (mine && top - m + power_v > ref + 8.f) || fabsf(neg) > 0x1p20f)) {
+                    if (grown) {
+                        const float to = ceilf(top);
+                        l *= exp2f(m - to);
+                        if (m != -INFINITY) ref -= to - m;
+                        m = to;
+                        neg = -to;
+                    }
+                    float high = top + neg + power_v;   // the largest product of a weight and its value's power, as ref counts
+                    mc = neg;
+                    if (each) {
+                        const uint4* powers = reinterpret_cast<const uint4*>(p.value_power + (unit_0 + j) * KB);
+                        float sum[2] = {0.f, 0.f}, far[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                for (int k = 0; k < 128; ++k) s[k] = __float_as_uint(__fadd_rn(__fmul_rn(mx_u2f(s[k]), cj), mc));
-                cj = 1.f;
-                mc = 0.f;
+                        for (int b = 0; b < 8; ++b) {
+                            const uint4 w = __ldg(powers + b);
+                            const uint32_t of[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                const float z = __fadd_rn(__fmul_rn(mx_u2f(s[16 * b + k]), cj), mc);
+                                sum[k & 1] += ex2_approx(z);
+                                const float y = z + (float)(of[k >> 2] >> 8 * (k & 3) & 255u);
+                                far[k & 1] = fmaxf(far[k & 1], y);
+                                s[16 * b + k] = __float_as_uint(y);
+                            }
+                        }
+                        l += sum[0] + sum[1];
+                        high = fmaxf(far[0], far[1]);
+                        power_v = mc = 0.f;
+                        cj = 1.f;
+                    } else if (__any_sync(0xffffffffu, fabsf(mc) > 0x1p20f)) {   // so large that the scores have to be rounded as the maximum was
+#pragma unroll
+                        for (int k = 0; k < 128; ++k) s[k] = __float_as_uint(__fadd_rn(__fmul_rn(mx_u2f(s[k]), cj), mc));
+                        cj = 1.f;
+                        mc = 0.f;
+                    }
+                    const bool moved = mine && high > ref + 8.f;
+                    float f = 1.f;
+                    if (moved) {
+                        const float to = ceilf(high);
+                        f = exp2f(ref - to);
+                        ref = to;
+                    }
+                    if (__any_sync(0xffffffffu, moved) && j > r.j0) scale_output(f);
+                }
+                power = power_v + (SPLIT_LIFT - ref);
+                if (!each) power = fmaxf(power, -60.f);   // (weights far below that are nothing, and l is made from them)
+                mc += power;
+            } else {
+                const bool grown = mine && (top - m) * unit > 8.f;   // (m = -inf: whenever a key is seen)
+                if (__any_sync(0xffffffffu, grown)) {
+                    const float f = grown ? exp2f((m - top) * unit) : 1.f;
+                    if (grown) m = top;
+                    l *= f;
+                    if (j > r.j0) scale_output(f);
+                }
+                mc = m == -INFINITY ? 0.f : -m * unit;
             }
-            const int less = kSplit ? max(top_j - top_v, -60) : 0;   // the weights take the difference of the powers
-            if (kSplit) mc += (float)less;
             const float2 c2 = make_float2(cj, cj), mc2 = make_float2(mc, mc);
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -711,7 +758,8 @@ __device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const C
                 }
             }
             const float all = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-            l += kSplit ? all * __uint_as_float((uint32_t)(127 - less) << 23) : all;
+            if (!kSplit) l += all;
+            else if (!(tops_j & SPLIT_EACH)) l += times_power(all, -(int)power);
             other = !r.two && !other;
         }
         const int64_t q = u.s.q0 + i;
@@ -723,7 +771,7 @@ __device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const C
             if (!x.wait(OF + t, nO)) return false;
             ++nO;
             tc_fence_after();
-            const float back = kSplit ? __uint_as_float((uint32_t)(top_v - SPLIT_TOP) << 23) : 1.f;   // of the values' scaling
+            const float back = kSplit ? times_power(1.f, (int)ref - 127 - SPLIT_TOP - SPLIT_LIFT) : 1.f;   // to 2^m
             if (!r.whole) {
                 float4* o = part.o + part_slot * 32 * 256 + part_row;
 #pragma unroll 1

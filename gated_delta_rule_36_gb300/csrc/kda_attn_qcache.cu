@@ -813,10 +813,12 @@ cudaError_t launch(const QcacheAttnParams& p, int sms, cudaStream_t stream) {
 //   values   in fp16, as are the weights that meet them (11 bits instead of 8: both roundings vanish beside the output's)
 //   queries  in fp16, which holds bf16's eight bits
 // all scaled by powers of two: a block of 128 keys and one of values each, so that its largest is below 2^(SPLIT_KEY + 1) and
-// 2^(SPLIT_TOP + 1), a query to below 2^9, so that 64 of them are below 2^15.  What is so much smaller than the largest that it loses bits
-// (2^-27 of it) is nothing beside the rounding of the sums.
+// 2^(SPLIT_TOP + 1), a query to below 2^9, so that 64 of them are below 2^15.  Where the keys of a block have values of very
+// different size, each has its own power.  fp16 holds all bits down to 2^-27 of the largest (queries: 2^-22) and is off by 2^-38 (2^-33)
+// of it below: keys and queries lose by that what only products of 2^20 and more would show, a key's values what is that
+// small beside its own largest channel (or 2^-SPLIT_SPREAD of that).
 // A CTA takes a block of keys of a head: half a warp a row, a lane eight channels of the key and of the value; or 64 rows of
-// queries.  Bound by HBM (144 bytes read and 544 written for each key and head).  Prompts of 1,024, 517 and 33 behind 16,384,
+// queries.  Bound by HBM (144 bytes read and 544 written, 545 at most, for each key and head).  Prompts of 1,024, 517 and 33 behind 16,384,
 // 8,484 and 15,967, 64 heads on 8: 585 us; 700 with the keys as two terms of bf16, both multiplied with the queries (three products a
 // block instead of two and an eighth, and 768 bytes), 1,328 with codes expanded in the other kernel by four more warps.
 constexpr int EX_THREADS = 256, EX_BLOCK = 128, EX_ROWS = EX_BLOCK * 16 / EX_THREADS;   // rows of a thread
@@ -831,6 +833,7 @@ struct ExpandParams {
     __half *k, *v;                  // [nseq][heads][blocks * 128][128]
     __half* k_rest;                 // [nseq][heads][blocks][2][128][8]
     int* top;                       // [nseq][heads][blocks]
+    uint8_t* value_power;           // [nseq][heads][blocks][128], of the blocks that have them
     RowsView q;
     int64_t query_rows, query_blocks;   // tokens times query heads of these key heads
     int query_heads;
@@ -892,7 +895,7 @@ __device__ __forceinline__ void expand_queries(const ExpandParams& p, int64_t bl
 __device__ __forceinline__ float code_at(uint32_t x, int bit) { return __uint_as_float((x >> bit & 15u) | 0x4b000000u) - 8388608.f; }
 
 __global__ void __launch_bounds__(EX_THREADS, 4) qcache_expand_kernel(const ExpandParams p) {
-    __shared__ uint2 most[EX_THREADS / 32];
+    __shared__ uint3 most[EX_THREADS / 32];
     await_stream();
     const int block = blockIdx.x, h = blockIdx.y, n = blockIdx.z;
     if (block >= p.blocks) {
@@ -918,26 +921,41 @@ __global__ void __launch_bounds__(EX_THREADS, 4) qcache_expand_kernel(const Expa
         }
     }
     auto largest = [](float most, uint32_t w) { return fmaxf(most, fmaxf(fabsf(bf16_hi(w)), fabsf(fmaf(15.f, bf16_lo(w), bf16_hi(w))))); };
-    float big_k = 0.f, big_v = 0.f;
+    // the largest of a row's values, which lie in both halves of its lanes
+    auto row_value = [&](uint32_t w) {
+        const float x = largest(0.f, w);
+        return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+    };
+    float big_k = 0.f, big_v = 0.f, least_v = INFINITY;   // (a row of zeros has no size)
 #pragma unroll
     for (int i = 0; i < EX_ROWS; ++i) {
         big_k = largest(big_k, kn[i]);
-        big_v = largest(big_v, vn[i]);
+        const float v = row_value(vn[i]);
+        big_v = fmaxf(big_v, v);
+        if (v > 0.f) least_v = fminf(least_v, v);
     }
     uint32_t all_k = __reduce_max_sync(0xffffffffu, __float_as_uint(big_k)), all_v = __reduce_max_sync(0xffffffffu, __float_as_uint(big_v));
-    if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = make_uint2(all_k, all_v);
+    uint32_t all_least = __reduce_min_sync(0xffffffffu, __float_as_uint(least_v));
+    if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = make_uint3(all_k, all_v, all_least);
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < EX_THREADS / 32; ++w) all_k = max(all_k, most[w].x), all_v = max(all_v, most[w].y);
+    for (int w = 0; w < EX_THREADS / 32; ++w) all_k = max(all_k, most[w].x), all_v = max(all_v, most[w].y), all_least = min(all_least, most[w].z);
     const int top_k = max((int)(all_k >> 23), SPLIT_KEY_LEAST), top_v = max((int)(all_v >> 23), SPLIT_LEAST);
+    const bool each = top_v - max((int)(all_least >> 23), SPLIT_LEAST) > SPLIT_SPREAD;
     const int64_t unit = ((int64_t)n * p.heads + h) * p.blocks + block;
-    if (threadIdx.x == 0) p.top[unit] = top_k << 16 | top_v;
+    if (threadIdx.x == 0) p.top[unit] = top_k << 16 | (each ? SPLIT_EACH : 0) | top_v;
     const float lift_k = __uint_as_float((uint32_t)(127 + SPLIT_KEY + 127 - top_k) << 23);
-    const float lift_v = __uint_as_float((uint32_t)(127 + SPLIT_TOP + 127 - top_v) << 23);
+    const float lift_block = __uint_as_float((uint32_t)(127 + SPLIT_TOP + 127 - top_v) << 23);
 #pragma unroll
     for (int i = 0; i < EX_ROWS; ++i) {
         const int row = row0 + i * (EX_THREADS / 16);
         const int64_t at = (unit * EX_BLOCK + row) * HD + 8 * lane;
+        float lift_v = lift_block;
+        if (each) {
+            const int top = max((int)(__float_as_uint(row_value(vn[i])) >> 23), SPLIT_LEAST);
+            lift_v = __uint_as_float((uint32_t)(127 + SPLIT_TOP + 127 - top) << 23);
+            if (lane == 0) p.value_power[unit * EX_BLOCK + row] = (uint8_t)top;
+        }
         const float ks = lift_k * bf16_lo(kn[i]), k8 = -8.f * ks, vs = lift_v * bf16_lo(vn[i]), vz = lift_v * bf16_hi(vn[i]);
         uint32_t k[4], v[4];
 #pragma unroll
@@ -978,7 +996,7 @@ struct Expanded {
 static Expanded expanded(int64_t S, int Hk, int nseq) {
     Expanded x;
     x.blocks = S > 0 ? (S + EX_BLOCK - 1) / EX_BLOCK : 1;
-    x.unit = x.blocks * (EX_BLOCK * (2 * HD + SPLIT_REST) * 2 + 16);   // (16: a block's powers, with what keeps the arrays aligned)
+    x.unit = x.blocks * (EX_BLOCK * (2 * HD + SPLIT_REST) * 2 + EX_BLOCK + 16);   // (keys' powers, a byte each; 16: a block's, with what keeps the arrays aligned)
     const int64_t fit = EX_MOST / (x.unit * (nseq > 0 ? nseq : 1));
     x.heads = (int)(fit < 1 ? 1 : fit < Hk ? fit : Hk);
     return x;
@@ -1015,7 +1033,8 @@ static cudaError_t launch_many_rows(const QcacheAttnParams& p, cudaStream_t stre
         e.query_heads = heads * G;
         e.query_rows = p.Tq * e.query_heads;
         e.query_blocks = (e.query_rows + EX_QUERIES * EX_THREADS / 16 - 1) / (EX_QUERIES * EX_THREADS / 16);
-        e.q_to = e.k_rest + units * rows * SPLIT_REST;
+        e.value_power = reinterpret_cast<uint8_t*>(e.k_rest + units * rows * SPLIT_REST);
+        e.q_to = reinterpret_cast<__half*>(e.value_power + units * rows);
         e.q_rest = e.q_to + e.query_rows * HD;
         e.q_power = reinterpret_cast<int*>(e.q_rest + e.query_rows * SPLIT_REST);
         e.top = e.q_power + e.query_rows;
@@ -1035,6 +1054,7 @@ static cudaError_t launch_many_rows(const QcacheAttnParams& p, cudaStream_t stre
         a.k_rest = e.k_rest;
         a.q_power = e.q_power;
         a.top = e.top;
+        a.value_power = e.value_power;
         a.top_blocks = x.blocks;
         a.k_row = a.v_row = HD;
         a.k_head = a.v_head = rows * HD;

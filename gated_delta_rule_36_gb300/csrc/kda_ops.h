@@ -38,10 +38,12 @@ struct AttnParams {
     __nv_bfloat16 *k, *v;
     // launch_attn_split: queries, keys and values in fp16.  A block of 128 values is v times 2^(top_v - 127 - SPLIT_TOP), one of
     // keys k times 2^(top_k - 127 - SPLIT_KEY), a query q times 2^q_power[token][head]; top[sequence * Hk + head][block] is
-    // top_k << 16 | top_v, at least SPLIT_KEY_LEAST and SPLIT_LEAST.  16 more channels of both (q_rest[token][head][16] and
+    // top_k << 16 | top_v, at least SPLIT_KEY_LEAST and SPLIT_LEAST.  With SPLIT_EACH in it, which says that the block's keys have values
+    // of very different size, top_v is each key's own, value_power[sequence * Hk + head][block][128].  16 more channels of both (q_rest[token][head][16] and
     // k_rest[sequence * Hk + head][block][2][128][8]) count in the scores.  Rows of the last block past the sequence's keys hold zeros.
     __half *q_rest, *k_rest;
     const int *q_power, *top;
+    const uint8_t* value_power;
     int64_t top_blocks;
     int64_t k_seq, k_row, k_head;   // strides in elements; k_seq = 0 for packed keys
     int64_t v_seq, v_row, v_head;
@@ -63,6 +65,11 @@ struct AttnParams {
 };
 
 constexpr int SPLIT_TOP = 13, SPLIT_LEAST = 27, SPLIT_KEY = 13, SPLIT_KEY_LEAST = 40, SPLIT_REST = 16;
+// Weights are carried as 2^SPLIT_LIFT times what their row's outputs refer to, which they pass by 2^8 at most: the upper
+// end of fp16, whose lower end (2^-14 with all bits) is then as far away as it can be.
+constexpr int SPLIT_LIFT = 7, SPLIT_EACH = 0x100;
+// The values of a block's keys share a power of two if each key's largest is within 2^SPLIT_SPREAD of the block's.
+constexpr int SPLIT_SPREAD = 8;
 
 struct LinParams {
     RowsView q, k, v, out;

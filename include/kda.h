@@ -504,7 +504,7 @@ kda_status kda_qcache_append(const kda_view* k, const kda_view* v, const kda_vie
  * Bytes of workspace kda_attn_qcache_fwd needs for Tq query tokens, Hq query heads, Hk key/value heads
  * and N sequences with room for S keys each.  Its contents need no initialisation.  At present 5.4 MB where the
  * sequences have at most 112 (token, head) rows for a key head on average, Tq Hq / Hk <= 112 N, or Tq Hq S <= 2^21.
- * Beyond that the keys and values are expanded there, 544 bytes for each row of the cache: for as many key heads at a
+ * Beyond that the keys and values are expanded there, 545 bytes for each row of the cache: for as many key heads at a
  * time as fit into 1 GB (one at least); their queries too, 292 bytes for each head; and 43 MB.  Returns 0 for invalid
  * arguments.
  */
@@ -522,7 +522,10 @@ size_t kda_attn_qcache_workspace_size(int64_t Tq, int Hq, int Hk, int N, int64_t
  * Cache rows past a sequence's keys are never used, whatever they hold; the scales and zeros inside a
  * sequence are taken to be finite.  Queries are taken to be below 2^60 in size, scales and zeros below 2^50; values' scales
  * below 2^-40 lose accuracy.  Weights are rounded to bf16 (few rows, see the workspace) or fp16 for the product with the
- * values' codes or values; scores, softmax sums and the output's accumulation are fp32.  The same inputs give the same bits.
+ * values' codes or values; scores, softmax sums and the output's accumulation are fp32.  With many rows a value keeps its bits down
+ * to 2^-19 of its key's largest channel, keys and queries down to 2^-27 and 2^-22 of the largest of their block of 128 keys and of their
+ * row, and a key whose weight times largest value is below 2^-11 of the row's largest such product R moves an output by up to 2^-21 R
+ * beside the weight's rounding.  The same inputs give the same bits.
  */
 kda_status kda_attn_qcache_fwd(const kda_view* q, const kda_view* cache, float scale, const kda_view* out,
                                const kda_tensor* seqlens_k, const kda_tensor* lse, const kda_tensor* cu_seqlens_q,
