@@ -213,6 +213,7 @@ __device__ Share find_share(const AttnParams& p, int tq, int G, uint64_t recip, 
     Seq s{};
     int64_t mine = 0, each = 0;
     Share r{};
+    auto weight = [&](int n) { return kSplit && (n < p.seq0 || n >= p.seq0 + p.seqs) ? (int64_t)0 : weight_of(s, tp); };   // of sequence n, which s holds
     bool bad = false;
 #pragma unroll 1
     for (int n = n0; n < n1; ++n) {   // nothing is computed from bad lengths
@@ -222,7 +223,7 @@ __device__ Share find_share(const AttnParams& p, int tq, int G, uint64_t recip, 
         if (p.seqlens_k) b |= p.seqlens_k[n] < 0 || p.seqlens_k[n] > p.keys;
         bad |= b;
         s = seq_of(p, n);
-        each = b ? 0 : weight_of(s, tp);
+        each = b ? 0 : weight(n);
         mine += each * p.Hk;
     }
     int64_t sum = mine;
@@ -255,7 +256,7 @@ __device__ Share find_share(const AttnParams& p, int tq, int G, uint64_t recip, 
         if (n > n0)
             for (n = n0;; ++n) {
                 s = seq_of(p, n);
-                each = weight_of(s, tp);
+                each = weight(n);
                 if (x < base + each * p.Hk) break;
                 base += each * p.Hk;
             }
@@ -399,9 +400,9 @@ __device__ bool load_warp(const AttnParams& p, const AttnMaps& maps, const Ctx& 
         for (int64_t left = x.weight; left > 0 && ok; next_pair(p, x, u), ++pieces) {
             const Piece r = piece_at(x, u, left);
             left -= r.weight;
-            const int n = p.cache ? u.n : 0;
+            const int n = kSplit ? u.n - p.seq0 : p.cache ? u.n : 0;
             for (int j = r.j0; j < r.j1 && ok; ++j) {
-                const __half* rest = kSplit ? p.k_rest + (((int64_t)u.n * p.Hk + u.kh) * p.top_blocks + j) * (REST / 2) : nullptr;
+                const __half* rest = kSplit ? p.k_rest + (((int64_t)n * p.Hk + u.kh) * p.top_blocks + j) * (REST / 2) : nullptr;
                 ok = tile(&maps.k, u.kh, u.s.k0 + j * KB, n, rest) && tile(&maps.v, u.kh, u.s.k0 + j * KB, n, nullptr);
                 if (j > r.j0 || !ok) continue;
                 // the queries, once the last scores of the piece before are done
@@ -623,7 +624,7 @@ __device__ bool softmax_warps(const AttnParams& p, const AttnMaps& maps, const C
         float m = -INFINITY, l = 0.f;
         // split: a block's values are scaled by a power of two of their own (top[j], or one for each key); the output refers to
         // 2^(m + ref), where powers count from -127 as in a float.  m and ref are whole numbers, so that they move without rounding
-        const int64_t unit_0 = kSplit ? ((int64_t)u.n * p.Hk + u.kh) * p.top_blocks : 0;
+        const int64_t unit_0 = kSplit ? ((int64_t)(u.n - p.seq0) * p.Hk + u.kh) * p.top_blocks : 0;
         // (at least 18 once a key is seen, since powers are SPLIT_LEAST and more)
         float ref = 20.f, neg = 0.f;   // neg: -m
         // ... and its keys and this query too: the exponents' scale is the block's, and m counts in steps of base 2
@@ -1108,7 +1109,7 @@ static cudaError_t launch(const AttnParams& p, cudaStream_t stream) {
     const int G = p.Hq / p.Hk, tq = 128 / G;
     AttnMaps maps;
     memset(&maps, 0, sizeof(maps));
-    const int seqs = p.cache ? p.nseq : 1;
+    const int seqs = kSplit ? p.seqs : p.cache ? p.nseq : 1;
     if (!mx_encode(&maps.q, p.q.data, p.Hq, p.Tq, 1, p.q.head, p.q.row, 0, G, tq) ||
         !mx_encode(&maps.k, p.k, p.Hk, p.Tk, seqs, p.k_head, p.k_row, p.k_seq, 1, KB) ||
         (kSplit && !mx_encode(&maps.q_rest, p.q_rest, p.Hq, p.Tq, 1, SPLIT_REST, (int64_t)SPLIT_REST * p.Hq, 0, G, tq, SPLIT_REST, 8)) ||

@@ -829,11 +829,11 @@ struct ExpandParams {
     QcacheView cache;
     const int64_t* seqlens_k;
     int64_t S;
-    int head0, heads, blocks;       // blocks of a sequence
-    __half *k, *v;                  // [nseq][heads][blocks * 128][128]
-    __half* k_rest;                 // [nseq][heads][blocks][2][128][8]
-    int* top;                       // [nseq][heads][blocks]
-    uint8_t* value_power;           // [nseq][heads][blocks][128], of the blocks that have them
+    int seq0, head0, heads, blocks; // blocks of a sequence
+    __half *k, *v;                  // [sequences][heads][blocks * 128][128]
+    __half* k_rest;                 // [sequences][heads][blocks][2][128][8]
+    int* top;                       // [sequences][heads][blocks]
+    uint8_t* value_power;           // [sequences][heads][blocks][128], of the blocks that have them
     RowsView q;
     int64_t query_rows, query_blocks;   // tokens times query heads of these key heads
     int query_heads;
@@ -903,10 +903,10 @@ __global__ void __launch_bounds__(EX_THREADS, 4) qcache_expand_kernel(const Expa
         if (b < p.query_blocks) expand_queries(p, b);
         return;
     }
-    const int64_t lk = min(max(p.seqlens_k[n], (int64_t)0), p.S);
+    const int64_t lk = min(max(p.seqlens_k[p.seq0 + n], (int64_t)0), p.S);
     if (block > 0 && (int64_t)block * EX_BLOCK >= lk) return;   // (block 0 is read even if there are no keys)
     const int lane = threadIdx.x & 15, row0 = threadIdx.x >> 4;
-    const uint8_t* src = p.cache.data + n * p.cache.seq + (int64_t)(p.head0 + h) * p.cache.head;
+    const uint8_t* src = p.cache.data + (int64_t)(p.seq0 + n) * p.cache.seq + (int64_t)(p.head0 + h) * p.cache.head;
     uint32_t kc[EX_ROWS], vc[EX_ROWS], kn[EX_ROWS], vn[EX_ROWS];   // codes; scale and zero of this lane's half
 #pragma unroll
     for (int i = 0; i < EX_ROWS; ++i) {
@@ -986,19 +986,24 @@ static bool few_rows(int64_t Tq, int Hq, int Hk, int nseq, int64_t S) {
     return Tq * (Hq / Hk) <= 112 * (int64_t)nseq || (double)Tq * Hq * S <= 1 << 21;
 }
 
-// Expanded keys and values for as many key heads at a time as fit into 1 GB, one at least.
-constexpr int64_t EX_MOST = 1LL << 30;
+// Expanded keys and values: of all sequences, for as many key heads at a time as fit into 1 GB, one at least.  Where one
+// head of all sequences would pass 4 GB (the room counts, whether used or not), some sequences at a time, with as many heads
+// as fit into 4 GB: a turn costs three launches, however little there is in it, so turns are not made smaller before that.
+constexpr int64_t EX_MOST = 1LL << 30, EX_HEAD_MOST = 1LL << 32;
 constexpr int64_t EX_QUERY_BYTES = (HD + SPLIT_REST) * 2 + 4;   // of an expanded query
 struct Expanded {
     int64_t blocks, unit;   // of a sequence; bytes of one (sequence, head)
-    int heads;              // at a time
+    int heads, seqs;        // at a time
 };
 static Expanded expanded(int64_t S, int Hk, int nseq) {
     Expanded x;
     x.blocks = S > 0 ? (S + EX_BLOCK - 1) / EX_BLOCK : 1;
     x.unit = x.blocks * (EX_BLOCK * (2 * HD + SPLIT_REST) * 2 + EX_BLOCK + 16);   // (keys' powers, a byte each; 16: a block's, with what keeps the arrays aligned)
-    const int64_t fit = EX_MOST / (x.unit * (nseq > 0 ? nseq : 1));
-    x.heads = (int)(fit < 1 ? 1 : fit < Hk ? fit : Hk);
+    auto within = [](int64_t n, int64_t most) { return (int)(n < 1 ? 1 : n < most ? n : most); };
+    const int all = nseq > 0 ? nseq : 1;
+    const int64_t units = EX_HEAD_MOST / x.unit;
+    x.heads = within(units >= all ? EX_MOST / x.unit / all : units, Hk);
+    x.seqs = within(units / x.heads, all);
     return x;
 }
 
@@ -1006,7 +1011,7 @@ size_t attn_qcache_workspace_bytes(int64_t Tq, int Hq, int Hk, int nseq, int64_t
     if (few_rows(Tq, Hq, Hk, nseq, S)) return QS_CUT_BYTES + QS_ML_BYTES + (size_t)2 * QS_MAX_CTAS * QS_MAX_ROWS * HD * sizeof(float);   // (16 rows a tile: half as many CTAs)
     const Expanded x = expanded(S, Hk, nseq);
     const int64_t query_rows = Tq * (Hq / Hk) * x.heads;
-    return attn_workspace_bytes(Tq, Hq, Hk) + 256 + (size_t)(x.unit * nseq * x.heads + query_rows * EX_QUERY_BYTES);
+    return attn_workspace_bytes(Tq, Hq, Hk) + 256 + (size_t)(x.unit * x.seqs * x.heads + query_rows * EX_QUERY_BYTES);
 }
 
 static cudaError_t launch_many_rows(const QcacheAttnParams& p, cudaStream_t stream) {
@@ -1014,14 +1019,15 @@ static cudaError_t launch_many_rows(const QcacheAttnParams& p, cudaStream_t stre
     const int G = p.Hq / p.Hk;
     char* ex = static_cast<char*>(p.workspace) + attn_workspace_bytes(p.Tq, p.Hq, p.Hk);
     ex += -(uintptr_t)ex & 255;
-    const int64_t rows = x.blocks * EX_BLOCK, units = (int64_t)p.nseq * x.heads;
-    for (int h0 = 0; h0 < p.Hk; h0 += x.heads) {
-        const int heads = min(x.heads, p.Hk - h0);
+    const int64_t rows = x.blocks * EX_BLOCK, units = (int64_t)x.seqs * x.heads;
+    for (int h0 = 0, n0 = 0; h0 < p.Hk;) {
+        const int heads = min(x.heads, p.Hk - h0), seqs = min(x.seqs, p.nseq - n0);
         ExpandParams e;
         memset(&e, 0, sizeof(e));
         e.cache = p.cache;
         e.seqlens_k = p.seqlens_k;
         e.S = p.S;
+        e.seq0 = n0;
         e.head0 = h0;
         e.heads = heads;
         e.blocks = (int)x.blocks;
@@ -1032,15 +1038,15 @@ static cudaError_t launch_many_rows(const QcacheAttnParams& p, cudaStream_t stre
         e.q.data += (int64_t)h0 * G * p.q.head;
         e.query_heads = heads * G;
         e.query_rows = p.Tq * e.query_heads;
-        e.query_blocks = (e.query_rows + EX_QUERIES * EX_THREADS / 16 - 1) / (EX_QUERIES * EX_THREADS / 16);
+        if (n0 == 0) e.query_blocks = (e.query_rows + EX_QUERIES * EX_THREADS / 16 - 1) / (EX_QUERIES * EX_THREADS / 16);
         e.value_power = reinterpret_cast<uint8_t*>(e.k_rest + units * rows * SPLIT_REST);
         e.q_to = reinterpret_cast<__half*>(e.value_power + units * rows);
         e.q_rest = e.q_to + e.query_rows * HD;
         e.q_power = reinterpret_cast<int*>(e.q_rest + e.query_rows * SPLIT_REST);
         e.top = e.q_power + e.query_rows;
-        if (p.nseq > 0) {
-            const int64_t more = (e.query_blocks + (int64_t)heads * p.nseq - 1) / ((int64_t)heads * p.nseq);
-            const cudaError_t err = launch_early(qcache_expand_kernel, dim3((unsigned)(x.blocks + more), (unsigned)heads, (unsigned)p.nseq), EX_THREADS, 0, stream, e);
+        if (seqs > 0) {
+            const int64_t more = (e.query_blocks + (int64_t)heads * seqs - 1) / ((int64_t)heads * seqs);
+            const cudaError_t err = launch_early(qcache_expand_kernel, dim3((unsigned)(x.blocks + more), (unsigned)heads, (unsigned)seqs), EX_THREADS, 0, stream, e);
             if (err != cudaSuccess) return err;
         }
         AttnParams a;
@@ -1056,6 +1062,8 @@ static cudaError_t launch_many_rows(const QcacheAttnParams& p, cudaStream_t stre
         a.top = e.top;
         a.value_power = e.value_power;
         a.top_blocks = x.blocks;
+        a.seq0 = n0;
+        a.seqs = seqs;
         a.k_row = a.v_row = HD;
         a.k_head = a.v_head = rows * HD;
         a.k_seq = a.v_seq = rows * HD * heads;
@@ -1067,7 +1075,7 @@ static cudaError_t launch_many_rows(const QcacheAttnParams& p, cudaStream_t stre
         a.Tq = p.Tq;
         a.Tk = rows;
         a.keys = p.S;
-        a.keep_status = h0 > 0;
+        a.keep_status = h0 > 0 || n0 > 0;
         a.nseq = p.nseq;
         a.Hq = heads * G;
         a.Hk = heads;
@@ -1078,6 +1086,8 @@ static cudaError_t launch_many_rows(const QcacheAttnParams& p, cudaStream_t stre
         a.test_skip = -1;
         const cudaError_t err = launch_attn_split(a, stream);
         if (err != cudaSuccess) return err;
+        n0 += x.seqs;
+        if (n0 >= p.nseq) n0 = 0, h0 += x.heads;
     }
     return cudaSuccess;
 }

@@ -45,6 +45,7 @@ struct AttnParams {
     const int *q_power, *top;
     const uint8_t* value_power;
     int64_t top_blocks;
+    int seq0, seqs;                 // the sequences that this launch answers; all of what is expanded counts from seq0
     int64_t k_seq, k_row, k_head;   // strides in elements; k_seq = 0 for packed keys
     int64_t v_seq, v_row, v_head;
     float* lse;                     // [Tq, Hq] in rows of lse_row, or nullptr

@@ -504,8 +504,11 @@ kda_status kda_qcache_append(const kda_view* k, const kda_view* v, const kda_vie
  * Bytes of workspace kda_attn_qcache_fwd needs for Tq query tokens, Hq query heads, Hk key/value heads
  * and N sequences with room for S keys each.  Its contents need no initialisation.  At present 5.4 MB where the
  * sequences have at most 112 (token, head) rows for a key head on average, Tq Hq / Hk <= 112 N, or Tq Hq S <= 2^21.
- * Beyond that the keys and values are expanded there, 545 bytes for each row of the cache: for as many key heads at a
- * time as fit into 1 GB (one at least); their queries too, 292 bytes for each head; and 43 MB.  Returns 0 for invalid
+ * Beyond that the keys and values are expanded there, 545 bytes for each row of the cache that there is
+ * room for: for as many key heads at a time as fit into 1 GB (one at least), and where one head of all sequences would pass
+ * 4 GB, for as many sequences and heads at a time as fit into that (one of each at least); their queries too, 292 bytes for each
+ * head; and 43 MB.  The average is over all N: a call in which one sequence has most of the queries, and the others one or
+ * none, is taken as few rows, which reads a sequence's keys once for every 16 rows.  Returns 0 for invalid
  * arguments.
  */
 size_t kda_attn_qcache_workspace_size(int64_t Tq, int Hq, int Hk, int N, int64_t S);

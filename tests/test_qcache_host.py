@@ -205,3 +205,20 @@ def test_binding_constants():
     consts = _header_constants()
     for name in ("KDA_U8", "KDA_QCACHE_ROW", "KDA_FLAG_GATE_SILU", "KDA_RESIDUAL_MAX_DIM"):
         assert getattr(kb, name) == consts[name]
+
+
+@pytest.mark.parametrize("tokens,hq,hk,n,room", [(4096, 64, 8, 256, 131072), (20000, 64, 8, 32767, 4096), (300, 16, 8, 2, 1 << 27), (1 << 20, 8, 1, 32767, 1 << 30)])
+def test_attention_workspace_is_bounded(lib, tokens, hq, hk, n, room):  # noqa: F811
+    """4 GB of expanded keys and values, or one sequence's one head where that is more, besides the queries."""
+    one = (-(-room // 128)) * (128 * (2 * 128 + 16) * 2 + 128 + 16)
+    need = kb.kda_attn_qcache_workspace_size(tokens, hq, hk, n, room)
+    assert 0 < need <= max(1 << 32, one) + tokens * hq * 292 + (64 << 20)
+
+
+def test_attention_workspace_of_ordinary_caches(lib):  # noqa: F811
+    """As many key heads of all sequences as fit into 1 GB; one of all of them up to 4 GB."""
+    for n, room, hk, heads in ((4, 16384, 8, 8), (64, 4096, 8, 7), (64, 32768, 8, 1), (64, 100000, 8, 1)):
+        unit = (room + 127) // 128 * (128 * (2 * 128 + 16) * 2 + 128 + 16)
+        need = kb.kda_attn_qcache_workspace_size(1024 * n, 4 * hk, hk, n, room)
+        keys = need - 1024 * n * 4 * heads * 292
+        assert unit * n * heads <= keys <= unit * n * heads + (64 << 20)
