@@ -490,6 +490,20 @@ _storage_uses = getattr(torch._C, "_storage_Use_Count", None)
 _refs = sys.getrefcount
 
 
+def _kept_and_uses(kept):
+    """A kept workspace, which the caller holds from here on, and the references that there are to it and its storage (views
+    hold the storage).  How many of them are the interpreter's and torch's own differs between versions."""
+    ws, storage, handle = kept[0], kept[1], kept[4]
+    return ws, (_refs(ws), _refs(storage), _storage_uses(handle))
+
+
+def _to_keep(nbytes, device):
+    ws = _workspace(None, nbytes, device, None)
+    storage = ws.untyped_storage()
+    _storage_uses(storage._cdata)   # (asking once may make an object that stays)
+    return [ws, storage, ws.data_ptr(), nbytes, storage._cdata, None]
+
+
 def _kept_workspace(nbytes, device, stream, raw):
     """A workspace from torch for a call on ``stream`` (``raw``: its handle), and where it is.  On the current stream it is
     that of the stream's call before, if neither the caller nor a view keeps it: what it held is used by earlier work of that
@@ -498,17 +512,15 @@ def _kept_workspace(nbytes, device, stream, raw):
         ws = _workspace(None, nbytes, device, stream)
         return ws, ws.data_ptr(), ws.numel()
     kept = _KEPT.get((device, raw))
-    if kept is not None:
-        ws, storage, at, room, handle, uses = kept
-        # (the entry's reference, this one and the count's own; views hold the storage)
-        if room >= nbytes and _refs(ws) <= 3 and _refs(storage) <= 3 and _storage_uses(handle) <= uses:
-            return ws, at, room
-    ws = _workspace(None, nbytes, device, None)
-    storage = ws.untyped_storage()
-    handle = storage._cdata
-    _storage_uses(handle)   # (asking once may make an object that stays)
-    _KEPT[device, raw] = ws, storage, ws.data_ptr(), nbytes, handle, _storage_uses(handle)
-    return ws, ws.data_ptr(), nbytes
+    if kept is not None and kept[3] >= nbytes:
+        ws, uses = _kept_and_uses(kept)
+        if uses == kept[5]:
+            return ws, kept[2], kept[3]
+        del ws
+    kept = _to_keep(nbytes, device)
+    ws, kept[5] = _kept_and_uses(kept)   # (nobody else holds it yet)
+    _KEPT[device, raw] = kept
+    return ws, kept[2], nbytes
 
 
 def kda_qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, q_out, k_out, eps=1e-6, status=None, flags=0,
