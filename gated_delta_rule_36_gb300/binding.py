@@ -485,7 +485,8 @@ def _workspace(workspace, nbytes, device, stream):
 
 # Workspaces of attention over a 4-bit cache: an allocation between two launches costs 8 us of host time, more than the
 # rest of the call, so the last one of every stream is kept (if it is small) and taken again once nobody else holds it.
-_KEPT, _KEPT_MOST = {}, 32 << 20
+# Of so many streams at most: those of streams that are no more go with the others then.
+_KEPT, _KEPT_MOST, _KEPT_STREAMS = {}, 32 << 20, 32
 _storage_uses = getattr(torch._C, "_storage_Use_Count", None)
 _refs = sys.getrefcount
 
@@ -519,6 +520,8 @@ def _kept_workspace(nbytes, device, stream, raw):
         del ws
     kept = _to_keep(nbytes, device)
     ws, kept[5] = _kept_and_uses(kept)   # (nobody else holds it yet)
+    if len(_KEPT) >= _KEPT_STREAMS and (device, raw) not in _KEPT:
+        _KEPT.clear()
     _KEPT[device, raw] = kept
     return ws, kept[2], nbytes
 

@@ -73,3 +73,14 @@ def test_large_ones_are_not_kept(allocations):
     for _ in range(2):
         take(kb._KEPT_MOST + 1)
     assert not kb._KEPT and len(allocations) == 2
+
+
+def test_no_more_than_some_streams_keep_one(allocations):
+    """A program that makes a stream for each request does not keep a workspace for each."""
+    held = take(raw=1000)[0]
+    for raw in range(10 * kb._KEPT_STREAMS):
+        take(raw=raw)
+        assert len(kb._KEPT) <= kb._KEPT_STREAMS
+    assert take(raw=1000)[1] != held.data_ptr()          # (one that is held is the caller's, whatever was kept)
+    n = len(allocations)
+    assert take(raw=5)[1] and take(raw=5)[1] and len(allocations) <= n + 1
