@@ -346,8 +346,9 @@ __global__ void __launch_bounds__(QsLayout<kN>::THREADS, kN == 1 ? 2 : 1) attn_q
     // the warp's slices: loads run QS_STAGES ahead within a piece, and the next piece's first ones are under way while
     // the warps put this one's results together
     uint32_t used = 0;
+    bool ok = true;   // no wait has run out: a warp that gave up starts no more copies, whose arrivals could meet a phase that is still open
     auto load = [&](int kh, int n, int j, uint32_t count) {   // slice j, the count-th of this warp
-        if (lane == 0) {
+        if (lane == 0 && ok) {
             const uint32_t stage = count % QS_STAGES;
             mbar_arrive_expect_tx(bars + 8 * stage, SLICE_BYTES);
             tma_load_4d(ring + stage * SLICE_BYTES, &map, 0, kh, j * SLICE, n, bars + 8 * stage);
@@ -370,7 +371,7 @@ __global__ void __launch_bounds__(QsLayout<kN>::THREADS, kN == 1 ? 2 : 1) attn_q
     // this lane's keys and its values' codes in a slice
     const unsigned char* krow = smem_raw + warp * QS_STAGES * SLICE_BYTES + key_row(g) * QC_ROW;
     const unsigned char* vrow = smem_raw + warp * QS_STAGES * SLICE_BYTES + key_row(2 * t) * QC_ROW + 64 + 4 * g;
-    bool ok = true, first_piece = true, odd = false;
+    bool first_piece = true, odd = false;
 #pragma unroll 1
     while (left > 0) {
         const int kh = (u.kh << kHg) + mine;
