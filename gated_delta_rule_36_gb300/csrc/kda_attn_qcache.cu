@@ -348,6 +348,9 @@ __global__ void __launch_bounds__(QsLayout<kN>::THREADS, kN == 1 ? 2 : 1) attn_q
     uint32_t used = 0;
     bool ok = true;   // no wait has run out: a warp that gave up starts no more copies, whose arrivals could meet a phase that is still open
     auto load = [&](int kh, int n, int j, uint32_t count) {   // slice j, the count-th of this warp
+#ifdef KDA_WAIT_TEST
+        if (warp == 0 && count == 0 && (int)blockIdx.x == p.test_skip) return;
+#endif
         if (lane == 0 && ok) {
             const uint32_t stage = count % QS_STAGES;
             mbar_arrive_expect_tx(bars + 8 * stage, SLICE_BYTES);
@@ -1084,7 +1087,7 @@ static cudaError_t launch_many_rows(const QcacheAttnParams& p, cudaStream_t stre
         a.scale = p.scale;
         a.status = p.status;
         a.workspace = p.workspace;
-        a.test_skip = -1;
+        a.test_skip = h0 == 0 && n0 == 0 ? p.test_skip : -1;
         const cudaError_t err = launch_attn_split(a, stream);
         if (err != cudaSuccess) return err;
         n0 += x.seqs;

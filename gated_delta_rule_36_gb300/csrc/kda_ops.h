@@ -116,6 +116,7 @@ struct QcacheAttnParams {
     float scale;
     uint32_t* status;
     void* workspace;                // behind the status word
+    int test_skip;                  // the test-only build: few rows, the share b whose first copy never starts; many, as in AttnParams, in the first of its launches
 };
 
 struct GatedNormParams {

@@ -700,6 +700,7 @@ kda_status kda_attn_qcache_fwd(const kda_view* q, const kda_view* cache, float s
     p.scale = scale;
     p.status = static_cast<uint32_t*>(workspace);
     p.workspace = static_cast<char*>(workspace) + kHeaderBytes;
+    p.test_skip = test_skip();
     const cudaError_t e = kda::launch_attn_qcache(p, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(KDA_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
     return KDA_OK;
