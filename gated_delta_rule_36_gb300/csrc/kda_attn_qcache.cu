@@ -48,7 +48,10 @@ constexpr int SLICE = 32;                          // keys
 constexpr uint32_t SLICE_BYTES = SLICE * QC_ROW;
 constexpr int QS_MAX_ROWS = 16;                    // of a tile of 8 rows for the heads that go together (16 rows: 32)
 constexpr int PIECE[3] = {0, 18, 34};              // a tile's own weight, in slices, by kN
-constexpr float LIFT = 60.f;                       // weights are carried as p 2^60
+// Weights are carried as p 2^60, and pass that by 2^8 at most: with scales and zeros below 2^40 a lane's sums of their
+// products (2^68 2^43.1 each) stay in fp32's range for 2^15 keys, 4 million of a share; with scales from 2^-40 on the
+// products with codes (2^-73) are normal numbers.
+constexpr float LIFT = 60.f;
 constexpr float NO_KEY = -3e38f;                   // (finite, so that a masked -inf less this is -inf)
 constexpr float UNLIFT = 0x1p-60f, CODE = 0x1p73f; // a product of a value's code and a weight, brought back
 constexpr float KEY_CODE = 0x1p-69f;               // a product of a key's code and a query, of 1 and 1

@@ -523,8 +523,8 @@ size_t kda_attn_qcache_workspace_size(int64_t Tq, int Hq, int Hk, int N, int64_t
  *   cu_seqlens_q   int64 [N + 1]; NULL/absent: Tq / N queries each
  *   workspace      >= kda_attn_qcache_workspace_size(Tq, Hq, Hk, N, S) bytes, 256-byte aligned
  * Cache rows past a sequence's keys are never used, whatever they hold; the scales and zeros inside a
- * sequence are taken to be finite.  Queries are taken to be below 2^60 in size, scales and zeros below 2^50; values' scales
- * below 2^-40 lose accuracy.  Weights are rounded to bf16 (few rows, see the workspace) or fp16 for the product with the
+ * sequence are taken to be finite.  Queries are taken to be below 2^60 in size, keys' scales and zeros below 2^50, values'
+ * below 2^40; values' scales below 2^-40 lose accuracy.  Weights are rounded to bf16 (few rows, see the workspace) or fp16 for the product with the
  * values' codes or values; scores, softmax sums and the output's accumulation are fp32.  With many rows a value keeps its bits down
  * to 2^-19 of its key's largest channel, keys and queries down to 2^-27 and 2^-22 of the largest of their block of 128 keys and of their
  * row, and a key whose weight times largest value is below 2^-11 of the row's largest such product R moves an output by up to 2^-21 R
