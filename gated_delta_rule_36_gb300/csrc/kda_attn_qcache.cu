@@ -349,12 +349,11 @@ __global__ void __launch_bounds__(QsLayout<kN>::THREADS, kN == 1 ? 2 : 1) attn_q
     // the warp's slices: loads run QS_STAGES ahead within a piece, and the next piece's first ones are under way while
     // the warps put this one's results together
     uint32_t used = 0;
-    bool ok = true;   // no wait has run out: a warp that gave up starts no more copies, whose arrivals could meet a phase that is still open
     auto load = [&](int kh, int n, int j, uint32_t count) {   // slice j, the count-th of this warp
 #ifdef KDA_WAIT_TEST
         if (warp == 0 && count == 0 && (int)blockIdx.x == p.test_skip) return;
 #endif
-        if (lane == 0 && ok) {
+        if (lane == 0) {
             const uint32_t stage = count % QS_STAGES;
             mbar_arrive_expect_tx(bars + 8 * stage, SLICE_BYTES);
             tma_load_4d(ring + stage * SLICE_BYTES, &map, 0, kh, j * SLICE, n, bars + 8 * stage);
@@ -377,7 +376,7 @@ __global__ void __launch_bounds__(QsLayout<kN>::THREADS, kN == 1 ? 2 : 1) attn_q
     // this lane's keys and its values' codes in a slice
     const unsigned char* krow = smem_raw + warp * QS_STAGES * SLICE_BYTES + key_row(g) * QC_ROW;
     const unsigned char* vrow = smem_raw + warp * QS_STAGES * SLICE_BYTES + key_row(2 * t) * QC_ROW + 64 + 4 * g;
-    bool first_piece = true, odd = false;
+    bool ok = true, first_piece = true, odd = false;
 #pragma unroll 1
     while (left > 0) {
         const int kh = (u.kh << kHg) + mine;
@@ -443,9 +442,13 @@ __global__ void __launch_bounds__(QsLayout<kN>::THREADS, kN == 1 ? 2 : 1) attn_q
                 }
             }
 #pragma unroll 1
-        for (int j = r.j0 + from; j < r.j1; j += step) {
+        for (int j = ok ? r.j0 + from : r.j1; j < r.j1; j += step) {
             const uint32_t stage = used % QS_STAGES;
-            if (ok) ok = mx_wait(bars + 8 * stage, (used / QS_STAGES) & 1);
+            // (a warp whose wait ran out starts no more copies: their arrivals could meet a phase that is still open)
+            if (!mx_wait(bars + 8 * stage, (used / QS_STAGES) & 1)) {
+                ok = false;
+                break;
+            }
             const unsigned char* kat = krow + stage * SLICE_BYTES;
             const unsigned char* vat = vrow + stage * SLICE_BYTES;
             float s[kN][2][4];
@@ -603,7 +606,7 @@ __global__ void __launch_bounds__(QsLayout<kN>::THREADS, kN == 1 ? 2 : 1) attn_q
         if (left > 0) {
             qs_next_tile<kHg>(p, G, rows, u);
             r = qs_piece<kN, kHg>(u, left);
-            load_first(u, r);
+            if (ok) load_first(u, r);
         }
         // ---- the warps' results: reference and sum of every row, then the rows themselves
         // (two places for the references: a warp without a slice of the next piece writes its own there while others still read these;
