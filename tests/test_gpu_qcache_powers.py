@@ -118,3 +118,25 @@ def test_an_early_token_does_not_depend_on_later_values(r):
     bound = 1.01 * (U * ref.abs() + 2.0 ** -10 * size + U * U * moved) + 2.0 ** -14 * (size + moved) + below
     for out in outs:
         assert ((out - ref).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("r", [9, 16, 24, 40])
+@pytest.mark.parametrize("kind", ["blocks", "rows", "later", "sink", "mixed", "steps", "zeros"])
+@pytest.mark.parametrize("lens_q,lens_k", [([1, 1], [5000, 333]), ([4, 1, 2], [2500, 90, 700])])
+def test_few_rows_over_values_of_different_powers(lens_q, lens_k, kind, r):
+    """The same without expansion, where weights carry their values' scales in bf16 and so have powers enough."""
+    g = gen_of(200 + r)
+    hq, hk, T, scale = 32, 8, sum(lens_q), 0.1
+    cache = empty_cache(len(lens_k), 5001, hk)
+    assert not many_rows(T, len(lens_q), cache, hq)
+    for n, lk in enumerate(lens_k):
+        cache[n, :lk] = rows_of(*keys_and_values(g, kind, r, lk, hk))
+    q = (rand(g, T, hq, D).float() + 1.0).bfloat16()
+    out, lse = torch.full((T, hq, D), NAN, dtype=torch.bfloat16, device="cuda"), torch.full((T, hq), NAN, device="cuda")
+    ws = kda.kda_attn_qcache_fwd(q, cache, scale, out, i64(lens_k), lse=lse, cu_seqlens_q=cu_of(lens_q))
+    assert kda.kda_read_device_status(ws) == 0
+    ref, size, spread, moved, rlse, most = ref_attn(q, cache, scale, lens_q, lens_k)
+    bound = 1.01 * (U * ref.abs() + U * spread) + 2.0 ** -14 * (size + spread + moved) + 1e-30
+    err = (out.double() - ref).abs()
+    assert (err <= bound).all(), f"{(err / bound).max().item():.3g} of its bound, {(err > bound).sum().item()} of {err.numel()}"
+    assert ((lse.double() - rlse).abs() <= 2.0 ** -14 * (1 + most)).all()
