@@ -28,8 +28,8 @@
 // 6, 10, 14, 20: 56, 47, 42, 42 us; drafts with 14, 20, 32, 44 on tiles of 16 rows: 67, 55, 48, 50).
 //
 // Bound by HBM between a start of about 2 us (the lengths, the search), some 3 us a tile (queries, the warps' results)
-// and the join (3 us): 32 single tokens over caches of 67 to 8,189, 32 heads on 8: 40 us (3.8 TB/s; 6.4 in the slices);
-// 16 over 5,002 to 32,767, 64 heads on 8, heads inside the rows: 84 to 88 us, where the 144 bytes of a head bring 21 %
+// and the join (3 us): 32 single tokens over caches of 67 to 8,189, 32 heads on 8: 39 us (3.9 TB/s; 6.4 in the slices);
+// 16 over 5,002 to 32,767, 64 heads on 8, heads inside the rows: 83 to 87 us, where the 144 bytes of a head bring 21 %
 // of others with them (heads outside: 72 us, 4.8 TB/s); one token over 32,767: 19 us, over 2,000 9.7;
 // 24 x 4 drafts: 42 us, bound by latency with eight warps an SM.
 
@@ -829,7 +829,7 @@ cudaError_t launch(const QcacheAttnParams& p, int sms, cudaStream_t stream) {
 // small beside its own largest channel (or 2^-SPLIT_SPREAD of that).
 // A CTA takes a block of keys of a head: half a warp a row, a lane eight channels of the key and of the value; or 64 rows of
 // queries.  Bound by HBM (144 bytes read and 544 written, 545 at most, for each key and head).  Prompts of 1,024, 517 and 33 behind 16,384,
-// 8,484 and 15,967, 64 heads on 8: 585 us; 700 with the keys as two terms of bf16, both multiplied with the queries (three products a
+// 8,484 and 15,967, 64 heads on 8: 580 us; 700 with the keys as two terms of bf16, both multiplied with the queries (three products a
 // block instead of two and an eighth, and 768 bytes), 1,328 with codes expanded in the other kernel by four more warps.
 constexpr int EX_THREADS = 256, EX_BLOCK = 128, EX_ROWS = EX_BLOCK * 16 / EX_THREADS;   // rows of a thread
 constexpr int EX_QUERIES = 4;   // its rows of queries
