@@ -11,7 +11,9 @@
 //   out_h = (O_h - 7.5 u_h + z_h) / l
 // so that codes count from their middle (7.5): a weight's rounding to bf16, at most 2^-8 of it, then moves the output by that
 // share of what the value deviates from its group's middle, and the middle itself is summed in fp32.  Against 64 bits the
-// output is off by 0.0021 to 0.0024 of its norm, 0.0017 of which is its own rounding to bf16.
+// output is off by 0.0021 to 0.0024 of its norm, 0.0017 of which is its own rounding to bf16.  One term for a weight, as
+// attention over a bf16 cache has: with a second one (its rest) the output's own rounding is all that remains, but one token over 32,767
+// takes 20.5 instead of 18.9 us, 32 tokens 44.4 instead of 38.7, 24 x 4 drafts 51.6 instead of 42 (16 long ones 85 both).
 //
 // A code becomes a bf16 operand by a mask alone: in the lowest eight bits (seven of the fraction and one of the
 // exponent, whose first step continues the subnormal numbers) bf16 counts linearly, so four bits there are
@@ -29,7 +31,7 @@
 //
 // Bound by HBM between a start of about 2 us (the lengths, the search), some 3 us a tile (queries, the warps' results)
 // and the join (3 us): 32 single tokens over caches of 67 to 8,189, 32 heads on 8: 39 us (3.9 TB/s; 6.4 in the slices);
-// 16 over 5,002 to 32,767, 64 heads on 8, heads inside the rows: 83 to 87 us, where the 144 bytes of a head bring 21 %
+// 16 over 5,002 to 32,767, 64 heads on 8, heads inside the rows: 83 to 88 us, where the 144 bytes of a head bring 21 %
 // of others with them (heads outside: 72 us, 4.8 TB/s); one token over 32,767: 19 us, over 2,000 9.7;
 // 24 x 4 drafts: 42 us, bound by latency with eight warps an SM.
 
